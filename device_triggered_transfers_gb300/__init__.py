@@ -33,6 +33,7 @@ ERROR_NAMES = {OK: "OK", EINVAL: "EINVAL", EOUTOFROWS: "EOUTOFROWS", EOVERLAP: "
 PREPARED, RUNNING, DONE, FAILED, CLOSING, CLOSED = range(6)
 RC_CLOSING = 1      # dtt_plan_close left the plan CLOSING (not an error)
 BF16, F32, U8 = 0, 1, 2
+E4M3 = 3                # an output type of the norm (include/dtt_ops.h)
 DTYPE_CODES = {"bf16": BF16, "f32": F32, "u8": U8}
 ELEM_BYTES = {"bf16": 2, "f32": 4, "u8": 1}
 COPY_VEC16, COPY_TMA, COPY_ENGINE = 0, 1, 2
@@ -111,6 +112,20 @@ class dtt_allreduce_desc(C.Structure):
                 ("reduce_threads", C.c_uint32), ("scatter_only", C.c_uint32)]
 
 
+class dtt_rmsnorm_desc(C.Structure):
+    _fields_ = [("x_dtype", C.c_uint32), ("residual_dtype", C.c_uint32), ("weight_dtype", C.c_uint32),
+                ("y_dtype", C.c_uint32), ("group", C.c_uint32), ("eps", C.c_float), ("cols", C.c_uint64)]
+
+
+ORTHO_MAX_STEPS = 32
+
+
+class dtt_ortho_desc(C.Structure):
+    _fields_ = [("x_dtype", C.c_uint32), ("batch", C.c_uint32), ("rows", C.c_uint64), ("cols", C.c_uint64),
+                ("steps", C.c_uint32), ("momentum", C.c_uint32), ("nesterov", C.c_uint32), ("mu", C.c_float),
+                ("eps", C.c_float), ("scale", C.c_float), ("coeffs", (C.c_float * 3) * ORTHO_MAX_STEPS)]
+
+
 ORDER_FN = C.CFUNCTYPE(C.c_int, C.c_uint64, C.c_void_p, C.POINTER(C.c_uint32),
                        C.POINTER(C.c_uint32))
 
@@ -178,6 +193,15 @@ _SIGS = {
     "dtt_barrier_destroy": (None, [_P]),
     "dtt_barrier_reveal": (C.c_int, [_P, C.POINTER(_P), C.POINTER(_P), C.POINTER(_P), _u32, _u64,
                                      _P, _P]),
+    "dtt_rmsnorm_forward": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), _u64, _P, _u64, _P, _u64, _P, _P, _u64,
+                                      _P, _u64, _P, _P, _P]),
+    "dtt_rmsnorm_backward": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), _u64, _P, _u64, _P, _u64, _P, _P, _P, _u64,
+                                       _P, _u64, _P, _P, _u64, _P]),
+    "dtt_rmsnorm_workspace": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), C.POINTER(_u64)]),
+    "dtt_ortho_workspace": (C.c_int, [C.POINTER(dtt_ortho_desc), C.POINTER(_u64)]),
+    "dtt_ortho_create": (C.c_int, [C.POINTER(dtt_ortho_desc), _P, _u64, C.POINTER(_P)]),
+    "dtt_ortho_run": (C.c_int, [_P, _P, _u64, _u64, _P, _u64, _u64, _P, _u64, _u64, _P, _P]),
+    "dtt_ortho_destroy": (None, [_P]),
     "dtt_barrier_reveal_noalloc": (C.c_int, [C.POINTER(_P), C.POINTER(_P), C.POINTER(_P), _u32,
                                              _u32, _u64, _P, _P]),
 }
@@ -939,3 +963,7 @@ def dtt_gemm_producer(A, Bt, bufs, M: int, N: int, K: int, ldc: int, slice_offs,
     offs = slice_offs if isinstance(slice_offs, C.Array) else (C.c_uint64 * len(bufs))(*slice_offs)
     _check(lib().dtt_gemm_producer(_ptr(A), _ptr(Bt), _ptr_array(bufs), len(bufs), M, N, K, ldc, offs,
                                    num_programs, handles, _ptr(err), _stream(stream)))
+
+
+# ---- operators on a rank's own block (include/dtt_ops.h) --------------------------------------
+from .ops import Orthogonalizer, RMSNorm  # noqa: E402,F401

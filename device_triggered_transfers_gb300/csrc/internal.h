@@ -265,6 +265,8 @@ int launch_gemm_consumer(const ConsumerLaunch& cl, cudaStream_t stream);
 cudaError_t preload_fill_kernels();
 cudaError_t preload_barrier_kernels();
 cudaError_t preload_gemm_kernels();
+cudaError_t preload_norm_kernels();
+cudaError_t preload_ortho_kernels();
 // dtt_preload() for library-internal callers: once per device, then a no-op.
 int preload_once();
 

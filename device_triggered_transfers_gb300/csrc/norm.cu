@@ -1,0 +1,585 @@
+// Residual addition with a root-mean-square norm, and its backward pass (dtt_ops.h).
+//
+// A row is spread over TPR threads in chunks of 8 columns: thread t holds columns 8 (i TPR + t) ..
+// + 7 of chunk i, so a warp's loads and stores are contiguous, a thread moves 16 bytes of bf16 or
+// 32 of f32 at a time, and a group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes of
+// one warp.  Everything between the loads and the stores is f32.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "dtt_ops.h"
+#include "internal.h"
+
+namespace dtt {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its reciprocal stays finite
+constexpr uint32_t kMaxPartials = 608;     // partial rows of the weight's gradient: four a SM
+constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512;   // a row's most threads
+constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
+
+struct FwdParams {
+    const char* x;
+    const char* res;            // or null
+    const char* w;              // or null
+    char* res_out;              // or null
+    char* y;
+    float* scales;
+    float* rstd;                // or null
+    uint64_t x_pitch, res_pitch, res_out_pitch, y_pitch;
+    uint64_t rows;
+    uint32_t cols, groups;
+    uint32_t x_dt, res_dt, w_dt, y_dt;
+    uint32_t group_lanes;       // lanes that share a scale: 4, 8, 16; 0: one scale per row
+    float eps, inv_cols;
+};
+
+struct BwdParams {
+    const char* dy;
+    const char* h;
+    const char* w;              // or null
+    const float* rstd;
+    const char* dres;           // or null
+    char* dx;
+    float* partial;             // [partials][cols], or null: no weight gradient
+    uint64_t dy_pitch, h_pitch, dres_pitch, dx_pitch;
+    uint64_t rows;
+    uint32_t cols, partials;
+    uint32_t dy_dt, h_dt, w_dt;
+    float inv_cols;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {      // 16 bits
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The larger of two, NaN if either is: a NaN in a row must reach its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// Columns c .. c + 7 of a row, zeros from `cols` on.  VEC: the row is 16-byte aligned, so a whole
+// chunk is one or two 16-byte loads.
+template <bool VEC>
+__device__ __forceinline__ void load8(const char* row, uint32_t dt, uint32_t c, uint32_t cols, float (&v)[8]) {
+    if (VEC && c + 8 <= cols) {
+        if (dt == DTT_BF16) {
+            const uint4 q = *reinterpret_cast<const uint4*>(row + (uint64_t)c * 2);
+            v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+            v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(row + (uint64_t)c * 4);
+            const float4 b = *reinterpret_cast<const float4*>(row + (uint64_t)c * 4 + 16);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        v[k] = 0.0f;
+        if (c + k < cols) {
+            if (dt == DTT_BF16)
+                v[k] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[c + k] << 16);
+            else
+                v[k] = reinterpret_cast<const float*>(row)[c + k];
+        }
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(char* row, uint32_t dt, uint32_t c, uint32_t cols, const float (&v)[8]) {
+    if (VEC && c + 8 <= cols) {
+        if (dt == DTT_BF16) {
+            *reinterpret_cast<uint4*>(row + (uint64_t)c * 2) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        } else if (dt == DTT_F32) {
+            *reinterpret_cast<float4*>(row + (uint64_t)c * 4) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(row + (uint64_t)c * 4 + 16) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint2*>(row + c) =
+                make_uint2(pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16,
+                           pack_e4m3(v[4], v[5]) | pack_e4m3(v[6], v[7]) << 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+        if (c + k < cols) {
+            if (dt == DTT_BF16)
+                reinterpret_cast<uint16_t*>(row)[c + k] = (uint16_t)pack_bf16(v[k], 0.0f);
+            else if (dt == DTT_F32)
+                reinterpret_cast<float*>(row)[c + k] = v[k];
+            else
+                reinterpret_cast<uint8_t*>(row)[c + k] = (uint8_t)pack_e4m3(v[k], 0.0f);
+        }
+}
+
+struct Sum {
+    __device__ float operator()(float a, float b) const { return a + b; }
+};
+struct MaxNan {
+    __device__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
+
+// Over the TPR threads of a row, the same bits in each.  One warp: butterfly shuffles.  More: the
+// warps' values through shared memory (`slot`: 32 floats used by this reduction alone between two
+// of the row's barriers).
+template <class Op>
+__device__ __forceinline__ float row_reduce(float v, uint32_t tpr, float* slot, Op op) {
+#pragma unroll
+    for (uint32_t o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    if (tpr == 32) return v;
+    const uint32_t warps = tpr / 32;
+    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = slot[threadIdx.x % 32 < warps ? threadIdx.x % 32 : 0];
+    if (threadIdx.x % 32 >= warps) v = 0.0f;        // neutral: sums, and maxima of magnitudes
+#pragma unroll
+    for (uint32_t o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// One row by blockDim.x threads; blockDim.y rows a CTA where a row is one warp.  NCH chunks a
+// thread stay in registers; kLong reads the row again for each pass over it.
+template <uint32_t NCH, bool VEC>
+__global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsnorm_fwd_kernel(const __grid_constant__ FwdParams p) {
+    __shared__ float slots[2][32];
+    const uint32_t tpr = blockDim.x, t = threadIdx.x;
+    const uint64_t r = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (r >= p.rows) return;                        // a whole warp: rows share no barrier
+    const char* x = p.x + r * p.x_pitch;
+    const char* res = p.res ? p.res + r * p.res_pitch : nullptr;
+    char* res_out = p.res_out ? p.res_out + r * p.res_out_pitch : nullptr;
+    char* y = p.y + r * p.y_pitch;
+
+    constexpr uint32_t HELD = NCH == kLong ? 1 : NCH;
+    const uint32_t nch = NCH == kLong ? (p.cols + 8 * tpr - 1) / (8 * tpr) : NCH;
+    float h[HELD][8];
+    auto load = [&](uint32_t i, float (&v)[8]) {
+        const uint32_t c = 8 * (i * tpr + t);
+        load8<VEC>(x, p.x_dt, c, p.cols, v);
+        if (res) {
+            float q[8];
+            load8<VEC>(res, p.res_dt, c, p.cols, q);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) v[k] += q[k];
+        }
+    };
+    float sum = 0.0f;
+    if constexpr (NCH != kLong) {
+#pragma unroll
+        for (uint32_t i = 0; i < HELD; ++i) load(i, h[i]);
+    }
+#pragma unroll HELD
+    for (uint32_t i = 0; i < nch; ++i) {
+        float (&v)[8] = h[NCH == kLong ? 0 : i];
+        if (NCH == kLong) load(i, v);
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) sum += v[k] * v[k];
+    }
+    const float s = rsqrtf(row_reduce(sum, tpr, slots[0], Sum()) * p.inv_cols + p.eps);
+    if (t == 0 && p.rstd) p.rstd[r] = s;
+
+    auto normed = [&](uint32_t i, const float (&v)[8], float (&o)[8]) {
+        const uint32_t c = 8 * (i * tpr + t);
+        if (p.w) load8<VEC>(p.w, p.w_dt, c, p.cols, o);
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) o[k] = p.w ? v[k] * s * o[k] : v[k] * s;
+    };
+    auto amax8 = [&](const float (&o)[8]) {
+        float m = 0.0f;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) m = max_nan(m, fabsf(o[k]));
+        return m;
+    };
+    float inv = 1.0f;
+    const bool e4m3 = p.y_dt == DTT_E4M3, row_scale = e4m3 && p.group_lanes == 0;
+    if (row_scale) {
+        float m = 0.0f;
+#pragma unroll HELD
+        for (uint32_t i = 0; i < nch; ++i) {
+            float (&v)[8] = h[NCH == kLong ? 0 : i];
+            float o[8];
+            if (NCH == kLong) load(i, v);
+            normed(i, v, o);
+            m = max_nan(m, amax8(o));
+        }
+        const float scale = max_nan(row_reduce(m, tpr, slots[1], MaxNan()) / kE4m3Max, kScaleMin);
+        if (t == 0) p.scales[r] = scale;
+        inv = 1.0f / scale;
+    }
+#pragma unroll HELD
+    for (uint32_t i = 0; i < nch; ++i) {
+        float (&v)[8] = h[NCH == kLong ? 0 : i];
+        float o[8];
+        const uint32_t c = 8 * (i * tpr + t);
+        if (NCH == kLong) load(i, v);
+        normed(i, v, o);
+        if (e4m3 && !row_scale) {
+            float m = amax8(o);
+            for (uint32_t d = p.group_lanes >> 1; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            const float scale = max_nan(m / kE4m3Max, kScaleMin);
+            inv = 1.0f / scale;
+            if (t % p.group_lanes == 0 && c < p.cols)
+                p.scales[r * p.groups + c / (8 * p.group_lanes)] = scale;
+        }
+        if (e4m3) {
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) o[k] *= inv;
+        }
+        if (res_out) store8<VEC>(res_out, p.res_dt, c, p.cols, v);
+        store8<VEC>(y, p.y_dt, c, p.cols, o);
+    }
+}
+
+// Rows blockIdx.x, + partials, ... by one CTA (or warp, where a row is one warp): each thread keeps
+// the same columns for all of them, so the weight's gradient adds up in its registers and is
+// written once, as one partial row (kLong: in the partial row itself).
+template <uint32_t NCH, bool VEC>
+__global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
+    __shared__ float slots[2][32];
+    const uint32_t tpr = blockDim.x, t = threadIdx.x;
+    const uint32_t me = blockIdx.x * blockDim.y + threadIdx.y;
+    if (me >= p.partials) return;                   // a whole warp: rows share no barrier
+    constexpr uint32_t HELD = NCH == kLong ? 1 : NCH;
+    const uint32_t nch = NCH == kLong ? (p.cols + 8 * tpr - 1) / (8 * tpr) : NCH;
+    float acc[HELD][8];
+#pragma unroll
+    for (uint32_t i = 0; i < HELD; ++i)
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) acc[i][k] = 0.0f;
+    float* part = p.partial ? p.partial + (uint64_t)me * p.cols : nullptr;
+
+    uint32_t turn = 0;
+    for (uint64_t r = me; r < p.rows; r += p.partials, turn ^= 1) {
+        const char* dyr = p.dy + r * p.dy_pitch;
+        const char* hr = p.h + r * p.h_pitch;
+        const char* dresr = p.dres ? p.dres + r * p.dres_pitch : nullptr;
+        char* dxr = p.dx + r * p.dx_pitch;
+        const float s = p.rstd[r];
+        float g[HELD][8], n[HELD][8];               // dy, h rstd
+        auto load = [&](uint32_t i, float (&gv)[8], float (&nv)[8]) {
+            const uint32_t c = 8 * (i * tpr + t);
+            load8<VEC>(dyr, p.dy_dt, c, p.cols, gv);
+            load8<VEC>(hr, p.h_dt, c, p.cols, nv);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) nv[k] *= s;
+        };
+        if constexpr (NCH != kLong) {
+#pragma unroll
+            for (uint32_t i = 0; i < HELD; ++i) load(i, g[i], n[i]);
+        }
+        float dot = 0.0f;
+#pragma unroll HELD
+        for (uint32_t i = 0; i < nch; ++i) {
+            const uint32_t j = NCH == kLong ? 0 : i, c = 8 * (i * tpr + t);
+            if (NCH == kLong) load(i, g[j], n[j]);
+            if (part) {
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) {
+                    if (NCH != kLong)
+                        acc[j][k] += g[j][k] * n[j][k];
+                    else if (c + k < p.cols)
+                        part[c + k] = (r == me ? 0.0f : part[c + k]) + g[j][k] * n[j][k];
+                }
+            }
+            if (p.w) {
+                float w[8];
+                load8<VEC>(p.w, p.w_dt, c, p.cols, w);
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) g[j][k] *= w[k];
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) dot += g[j][k] * n[j][k];
+        }
+        const float m = row_reduce(dot, tpr, slots[turn], Sum()) * p.inv_cols;
+#pragma unroll HELD
+        for (uint32_t i = 0; i < nch; ++i) {
+            const uint32_t j = NCH == kLong ? 0 : i, c = 8 * (i * tpr + t);
+            if (NCH == kLong) {
+                load(i, g[j], n[j]);
+                if (p.w) {
+                    float w[8];
+                    load8<VEC>(p.w, p.w_dt, c, p.cols, w);
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) g[j][k] *= w[k];
+                }
+            }
+            float o[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) o[k] = s * (g[j][k] - n[j][k] * m);
+            if (dresr) {
+                float q[8];
+                load8<VEC>(dresr, p.h_dt, c, p.cols, q);
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) o[k] += q[k];
+            }
+            store8<VEC>(dxr, p.h_dt, c, p.cols, o);
+        }
+    }
+    if (part && NCH != kLong) {
+#pragma unroll
+        for (uint32_t i = 0; i < HELD; ++i)
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                const uint32_t c = 8 * (i * tpr + t) + k;
+                if (c < p.cols) part[c] = acc[i][k];
+            }
+    }
+}
+
+// dweight[c] = the partial rows' sum.  32 columns a CTA; its 8 warps take every eighth partial row,
+// and their sums are added in warp order.
+__global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* partial, uint32_t partials,
+                                                              uint32_t cols, float* dweight) {
+    __shared__ float part[8][32];
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
+    float v = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+        for (uint32_t i = warp; i < partials; i += 8) v += partial[(uint64_t)i * cols + c];
+    }
+    part[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+#pragma unroll
+        for (uint32_t w = 1; w < 8; ++w) v += part[w][lane];
+        dweight[c] = v;
+    }
+}
+
+struct Shape {
+    uint32_t nch, tpr, rows_per_cta;
+};
+
+// Up to four chunks a thread in registers; `threads` threads a row at most.
+Shape shape_of(uint32_t cols, uint32_t threads) {
+    const uint32_t chunks = (cols + 7) / 8;
+    for (uint32_t nch : {1u, 2u, 4u}) {
+        const uint32_t tpr = ((chunks + nch - 1) / nch + 31) / 32 * 32;
+        if (tpr <= (nch == 4 ? threads : 256u)) return {nch, tpr, tpr == 32 ? 8u : 1u};
+    }
+    return {kLong, threads, 1};
+}
+
+template <bool VEC>
+void launch_fwd(const FwdParams& p, const Shape& s, cudaStream_t stream) {
+    const dim3 block(s.tpr, s.rows_per_cta);
+    const uint32_t grid = (uint32_t)((p.rows + s.rows_per_cta - 1) / s.rows_per_cta);
+    if (s.nch == 1) rmsnorm_fwd_kernel<1, VEC><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 2) rmsnorm_fwd_kernel<2, VEC><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 4) rmsnorm_fwd_kernel<4, VEC><<<grid, block, 0, stream>>>(p);
+    else rmsnorm_fwd_kernel<kLong, VEC><<<grid, block, 0, stream>>>(p);
+}
+
+template <bool VEC>
+void launch_bwd(const BwdParams& p, const Shape& s, cudaStream_t stream) {
+    const dim3 block(s.tpr, s.rows_per_cta);
+    const uint32_t grid = (p.partials + s.rows_per_cta - 1) / s.rows_per_cta;
+    if (s.nch == 1) rmsnorm_bwd_kernel<1, VEC><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 2) rmsnorm_bwd_kernel<2, VEC><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 4) rmsnorm_bwd_kernel<4, VEC><<<grid, block, 0, stream>>>(p);
+    else rmsnorm_bwd_kernel<kLong, VEC><<<grid, block, 0, stream>>>(p);
+}
+
+uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
+
+int check_desc(const char* who, const dtt_rmsnorm_desc* d) {
+    if (!d) return fail(DTT_EINVAL, "%s: null desc", who);
+    for (uint32_t t : {d->x_dtype, d->residual_dtype, d->weight_dtype})
+        if (t != DTT_BF16 && t != DTT_F32) return fail(DTT_EINVAL, "%s: x, residual and weight are bf16 or f32", who);
+    if (d->y_dtype != DTT_BF16 && d->y_dtype != DTT_F32 && d->y_dtype != DTT_E4M3)
+        return fail(DTT_EINVAL, "%s: y is bf16, f32 or e4m3", who);
+    if (d->y_dtype == DTT_E4M3 ? (d->group != 0 && d->group != 32 && d->group != 64 && d->group != 128) : d->group != 0)
+        return fail(DTT_EINVAL, "%s: group is 0, 32, 64 or 128 with an e4m3 y, else 0", who);
+    if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) return fail(DTT_EINVAL, "%s: eps must be finite and not negative", who);
+    if (d->cols == 0 || d->cols > (1u << 24)) return fail(DTT_EINVAL, "%s: cols must be 1 .. 2^24", who);
+    return DTT_OK;
+}
+
+// A tensor argument: present unless optional, aligned to its element, rows that do not overlap.
+int check_rows(const char* who, const char* name, const void* ptr, uint64_t pitch, uint64_t rows, uint64_t cols,
+               uint32_t dt, bool optional) {
+    if (!ptr) return optional ? DTT_OK : fail(DTT_EINVAL, "%s: %s is missing", who, name);
+    const uint32_t e = elem_bytes(dt);
+    if (reinterpret_cast<uintptr_t>(ptr) % e || pitch % e)
+        return fail(DTT_EINVAL, "%s: %s must be aligned to its %u-byte elements", who, name, e);
+    if (rows > 1 && pitch < cols * e) return fail(DTT_EINVAL, "%s: %s: the pitch is less than a row", who, name);
+    return DTT_OK;
+}
+
+bool aligned(const void* ptr, uint64_t pitch, uint32_t to) {
+    return reinterpret_cast<uintptr_t>(ptr) % to == 0 && pitch % to == 0;      // null: aligned
+}
+
+cudaError_t prepare(const void* kernel) {
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t preload_norm_kernels() {
+    const void* kernels[] = {
+        (const void*)rmsnorm_fwd_kernel<1, true>, (const void*)rmsnorm_fwd_kernel<2, true>,
+        (const void*)rmsnorm_fwd_kernel<4, true>, (const void*)rmsnorm_fwd_kernel<kLong, true>,
+        (const void*)rmsnorm_fwd_kernel<1, false>, (const void*)rmsnorm_fwd_kernel<2, false>,
+        (const void*)rmsnorm_fwd_kernel<4, false>, (const void*)rmsnorm_fwd_kernel<kLong, false>,
+        (const void*)rmsnorm_bwd_kernel<1, true>, (const void*)rmsnorm_bwd_kernel<2, true>,
+        (const void*)rmsnorm_bwd_kernel<4, true>, (const void*)rmsnorm_bwd_kernel<kLong, true>,
+        (const void*)rmsnorm_bwd_kernel<1, false>, (const void*)rmsnorm_bwd_kernel<2, false>,
+        (const void*)rmsnorm_bwd_kernel<4, false>, (const void*)rmsnorm_bwd_kernel<kLong, false>,
+        (const void*)rmsnorm_dweight_kernel};
+    for (const void* k : kernels) {
+        const cudaError_t e = prepare(k);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace dtt
+
+using namespace dtt;
+
+extern "C" int dtt_rmsnorm_workspace(const dtt_rmsnorm_desc* d, uint64_t* bytes) {
+    const int rc = check_desc("dtt_rmsnorm_workspace", d);
+    if (rc) return rc;
+    if (!bytes) return fail(DTT_EINVAL, "dtt_rmsnorm_workspace: null bytes");
+    *bytes = (uint64_t)kMaxPartials * d->cols * 4;
+    return DTT_OK;
+}
+
+extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, const void* x, uint64_t x_pitch,
+                                   const void* residual, uint64_t residual_pitch, const void* weight,
+                                   void* residual_out, uint64_t residual_out_pitch, void* y, uint64_t y_pitch,
+                                   float* scales, float* rstd, cudaStream_t stream) {
+    const char* who = "dtt_rmsnorm_forward";
+    int rc = check_desc(who, d);
+    if (rc) return rc;
+    if (rows >= (1ull << 31)) return fail(DTT_EINVAL, "%s: 2^31 rows or more", who);
+    if (rows == 0) return DTT_OK;
+    const bool e4m3 = d->y_dtype == DTT_E4M3;
+    if ((rc = check_rows(who, "x", x, x_pitch, rows, d->cols, d->x_dtype, false)) ||
+        (rc = check_rows(who, "residual", residual, residual_pitch, rows, d->cols, d->residual_dtype, true)) ||
+        (rc = check_rows(who, "weight", weight, 0, 1, d->cols, d->weight_dtype, true)) ||
+        (rc = check_rows(who, "residual_out", residual_out, residual_out_pitch, rows, d->cols, d->residual_dtype, true)) ||
+        (rc = check_rows(who, "y", y, y_pitch, rows, d->cols, d->y_dtype, false)) ||
+        (rc = check_rows(who, "scales", scales, 0, 1, 0, DTT_F32, !e4m3)) ||
+        (rc = check_rows(who, "rstd", rstd, 0, 1, 0, DTT_F32, true)))
+        return rc;
+    if (scales && !e4m3) return fail(DTT_EINVAL, "%s: scales go with an e4m3 y alone", who);
+    if (residual && residual == residual_out && residual_pitch != residual_out_pitch)
+        return fail(DTT_EINVAL, "%s: in place, residual and residual_out have one pitch", who);
+    if ((rc = preload_once())) return rc;
+    FwdParams p{};
+    p.x = static_cast<const char*>(x);
+    p.res = static_cast<const char*>(residual);
+    p.w = static_cast<const char*>(weight);
+    p.res_out = static_cast<char*>(residual_out);
+    p.y = static_cast<char*>(y);
+    p.scales = scales;
+    p.rstd = rstd;
+    p.x_pitch = x_pitch;
+    p.res_pitch = residual_pitch;
+    p.res_out_pitch = residual_out_pitch;
+    p.y_pitch = y_pitch;
+    p.rows = rows;
+    p.cols = (uint32_t)d->cols;
+    p.groups = d->group ? (uint32_t)((d->cols + d->group - 1) / d->group) : 1;
+    p.x_dt = d->x_dtype;
+    p.res_dt = d->residual_dtype;
+    p.w_dt = d->weight_dtype;
+    p.y_dt = d->y_dtype;
+    p.group_lanes = d->group / 8;
+    p.eps = d->eps;
+    p.inv_cols = 1.0f / (float)d->cols;
+    const bool vec = aligned(x, x_pitch, 16) && aligned(residual, residual ? residual_pitch : 0, 16) &&
+                     aligned(weight, 0, 16) && aligned(residual_out, residual_out ? residual_out_pitch : 0, 16) &&
+                     aligned(y, y_pitch, e4m3 ? 8 : 16);
+    const Shape s = shape_of(p.cols, kFwdThreads);
+    if (vec) launch_fwd<true>(p, s, stream);
+    else launch_fwd<false>(p, s, stream);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    return DTT_OK;
+}
+
+extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, const void* dy, uint64_t dy_pitch,
+                                    const void* h, uint64_t h_pitch, const void* weight, const float* rstd,
+                                    const void* dres, uint64_t dres_pitch, void* dx, uint64_t dx_pitch,
+                                    float* dweight, void* workspace, uint64_t workspace_bytes, cudaStream_t stream) {
+    const char* who = "dtt_rmsnorm_backward";
+    int rc = check_desc(who, d);
+    if (rc) return rc;
+    if (rows >= (1ull << 31)) return fail(DTT_EINVAL, "%s: 2^31 rows or more", who);
+    if (dweight && !weight) return fail(DTT_EINVAL, "%s: a weight's gradient without a weight", who);
+    if ((rc = check_rows(who, "weight", weight, 0, 1, d->cols, d->weight_dtype, true)) ||
+        (rc = check_rows(who, "dweight", dweight, 0, 1, 0, DTT_F32, true)))
+        return rc;
+    if (dweight && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 ||
+                    workspace_bytes < (uint64_t)kMaxPartials * d->cols * 4))
+        return fail(DTT_EINVAL, "%s: the workspace is missing, misaligned or short", who);
+    if (rows == 0) {
+        if (dweight) DTT_CUDA_TRY(cudaMemsetAsync(dweight, 0, d->cols * 4, stream));
+        return DTT_OK;
+    }
+    if ((rc = check_rows(who, "dy", dy, dy_pitch, rows, d->cols, d->x_dtype, false)) ||
+        (rc = check_rows(who, "h", h, h_pitch, rows, d->cols, d->residual_dtype, false)) ||
+        (rc = check_rows(who, "rstd", rstd, 0, 1, 0, DTT_F32, false)) ||
+        (rc = check_rows(who, "dres", dres, dres_pitch, rows, d->cols, d->residual_dtype, true)) ||
+        (rc = check_rows(who, "dx", dx, dx_pitch, rows, d->cols, d->residual_dtype, false)))
+        return rc;
+    if (dres && dres == dx && dres_pitch != dx_pitch)
+        return fail(DTT_EINVAL, "%s: in place, dres and dx have one pitch", who);
+    if ((rc = preload_once())) return rc;
+    BwdParams p{};
+    p.dy = static_cast<const char*>(dy);
+    p.h = static_cast<const char*>(h);
+    p.w = static_cast<const char*>(weight);
+    p.rstd = rstd;
+    p.dres = static_cast<const char*>(dres);
+    p.dx = static_cast<char*>(dx);
+    p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+    p.dy_pitch = dy_pitch;
+    p.h_pitch = h_pitch;
+    p.dres_pitch = dres_pitch;
+    p.dx_pitch = dx_pitch;
+    p.rows = rows;
+    p.cols = (uint32_t)d->cols;
+    p.partials = (uint32_t)std::min<uint64_t>(rows, kMaxPartials);
+    p.dy_dt = d->x_dtype;
+    p.h_dt = d->residual_dtype;
+    p.w_dt = d->weight_dtype;
+    p.inv_cols = 1.0f / (float)d->cols;
+    const bool vec = aligned(dy, dy_pitch, 16) && aligned(h, h_pitch, 16) && aligned(weight, 0, 16) &&
+                     aligned(dres, dres ? dres_pitch : 0, 16) && aligned(dx, dx_pitch, 16);
+    const Shape s = shape_of(p.cols, kBwdThreads);
+    if (vec) launch_bwd<true>(p, s, stream);
+    else launch_bwd<false>(p, s, stream);
+    if (dweight)
+        rmsnorm_dweight_kernel<<<(p.cols + 31) / 32, 256, 0, stream>>>(p.partial, p.partials, p.cols, dweight);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    return DTT_OK;
+}

@@ -1081,6 +1081,8 @@ int preload_once() {
     if (e == cudaSuccess) e = preload_barrier_kernels();
     if (e == cudaSuccess) e = preload_gemm_kernels();
     if (e == cudaSuccess) e = preload_allreduce_kernels();
+    if (e == cudaSuccess) e = preload_norm_kernels();
+    if (e == cudaSuccess) e = preload_ortho_kernels();
     if (e != cudaSuccess) return fail(DTT_ECUDA, "dtt_preload: %s", cudaGetErrorString(e));
     g_preloaded |= bit;
     return DTT_OK;
