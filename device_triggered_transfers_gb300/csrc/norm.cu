@@ -1,9 +1,14 @@
 // Residual addition with a root-mean-square norm, and its backward pass (dtt_ops.h).
 //
-// A row is spread over TPR threads in chunks of 8 columns: thread t holds columns 8 (i TPR + t) ..
-// + 7 of chunk i, so a warp's loads and stores are contiguous, a thread moves 16 bytes of bf16 or
-// 32 of f32 at a time, and a group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes of
-// one warp.  Everything between the loads and the stores is f32.
+// Three forms of each pass, all f32 between the loads and the stores:
+//  - chunks (few rows, or rows too long for the others; 16-byte aligned, whole chunks): a row is spread over TPR
+//    threads in chunks of 8 columns: thread t holds columns 8 (i TPR + t) .. + 7 of chunk i, so a
+//    warp's accesses are contiguous, a thread moves 16 bytes of bf16 or 32 of f32 at a time, and a
+//    group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes of one warp;
+//  - ring (many aligned rows): the same layout by persistent CTAs whose rows come through a ring of
+//    shared-memory stages, bulk copies running ahead of the arithmetic;
+//  - elements (rows that are not 16-byte aligned, or no whole number of chunks): thread t holds columns t, t + TPR, ..., so that
+//    accesses of single elements are contiguous over a warp.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -19,7 +24,10 @@ namespace {
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its reciprocal stays finite
 constexpr uint32_t kMaxPartials = 608;     // partial rows of the weight's gradient: four a SM
-constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512;   // a row's most threads
+constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   // a row's most threads
+constexpr uint32_t kRingStages = 8;        // of a CTA, at most
+constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
+constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
 
 struct FwdParams {
@@ -346,6 +354,366 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsn
     }
 }
 
+// ---- elements ----------------------------------------------------------------------------------
+__device__ __forceinline__ float load1(const char* row, uint32_t dt, uint32_t c) {
+    return dt == DTT_BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[c] << 16)
+                          : reinterpret_cast<const float*>(row)[c];
+}
+
+__device__ __forceinline__ void store1(char* row, uint32_t dt, uint32_t c, float v) {
+    if (dt == DTT_BF16)
+        reinterpret_cast<uint16_t*>(row)[c] = (uint16_t)pack_bf16(v, 0.0f);
+    else if (dt == DTT_F32)
+        reinterpret_cast<float*>(row)[c] = v;
+    else
+        reinterpret_cast<uint8_t*>(row)[c] = (uint8_t)pack_e4m3(v, 0.0f);
+}
+
+// Columns t, t + T, ... (E of them, those below `cols`) of a row.
+template <uint32_t E>
+__device__ __forceinline__ void load_elements(const char* row, uint32_t dt, uint32_t cols, float (&v)[E]) {
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) {
+        const uint32_t c = k * blockDim.x + threadIdx.x;
+        v[k] = c < cols ? load1(row, dt, c) : 0.0f;
+    }
+}
+
+// One row a CTA.  A group of columns is one, two or four neighbours of the row's segments of 32
+// columns (segment k T / 32 + warp), whose maxima meet in shared memory.
+template <uint32_t E>
+__global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const __grid_constant__ FwdParams p) {
+    __shared__ float slots[2][32];
+    __shared__ float segment[E * kFwdThreads / 32];
+    const uint32_t T = blockDim.x, t = threadIdx.x, warps = T / 32;
+    const uint64_t r = blockIdx.x;
+    const char* x = p.x + r * p.x_pitch;
+    char* y = p.y + r * p.y_pitch;
+    float h[E], o[E];
+    load_elements(x, p.x_dt, p.cols, h);
+    if (p.res) {
+        load_elements(p.res + r * p.res_pitch, p.res_dt, p.cols, o);
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) h[k] += o[k];
+    }
+    if (p.w) load_elements(p.w, p.w_dt, p.cols, o);
+    float sum = 0.0f;
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
+    const float s = rsqrtf(row_reduce(sum, T, slots[0], Sum()) * p.inv_cols + p.eps);
+    if (t == 0 && p.rstd) p.rstd[r] = s;
+    if (p.res_out) {
+        char* res_out = p.res_out + r * p.res_out_pitch;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (k * T + t < p.cols) store1(res_out, p.res_dt, k * T + t, h[k]);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) h[k] = p.w ? h[k] * s * o[k] : h[k] * s;
+    if (p.y_dt == DTT_E4M3 && p.group_lanes == 0) {
+        float m = 0.0f;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) m = max_nan(m, fabsf(h[k]));
+        const float scale = max_nan(row_reduce(m, T, slots[1], MaxNan()) / kE4m3Max, kScaleMin);
+        if (t == 0) p.scales[r] = scale;
+        const float inv = 1.0f / scale;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) h[k] *= inv;
+    } else if (p.y_dt == DTT_E4M3) {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) {
+            float m = fabsf(h[k]);
+#pragma unroll
+            for (uint32_t d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            if (t % 32 == 0) segment[k * warps + t / 32] = m;
+        }
+        __syncthreads();
+        const uint32_t per = p.group_lanes / 4;               // segments a group
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) {
+            const uint32_t q = k * warps + t / 32, q0 = q / per * per;
+            float m = 0.0f;
+            for (uint32_t i = q0; i < q0 + per && i < E * warps; ++i) m = max_nan(m, segment[i]);
+            const float scale = max_nan(m / kE4m3Max, kScaleMin);
+            if (t % 32 == 0 && q == q0 && q * 32 < p.cols) p.scales[r * p.groups + q / per] = scale;
+            h[k] *= 1.0f / scale;
+        }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k)
+        if (k * T + t < p.cols) store1(y, p.y_dt, k * T + t, h[k]);
+}
+
+// As the chunk form: rows blockIdx.x, + partials, ..., the weight's gradient in registers.
+template <uint32_t E>
+__global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
+    __shared__ float slots[2][32];
+    const uint32_t T = blockDim.x, t = threadIdx.x;
+    float acc[E], w[E];
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) {
+        acc[k] = 0.0f;
+        w[k] = 1.0f;
+    }
+    if (p.w) load_elements(p.w, p.w_dt, p.cols, w);
+    uint32_t turn = 0;
+    for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
+        const float s = p.rstd[r];
+        float g[E], n[E], q[E];
+        load_elements(p.dy + r * p.dy_pitch, p.dy_dt, p.cols, g);
+        load_elements(p.h + r * p.h_pitch, p.h_dt, p.cols, n);
+        if (p.dres) load_elements(p.dres + r * p.dres_pitch, p.h_dt, p.cols, q);
+        float dot = 0.0f;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) {
+            n[k] *= s;
+            acc[k] += g[k] * n[k];
+            g[k] *= w[k];
+            dot += g[k] * n[k];
+        }
+        const float m = row_reduce(dot, T, slots[turn], Sum()) * p.inv_cols;
+        char* dx = p.dx + r * p.dx_pitch;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (k * T + t < p.cols) {
+                const float v = s * (g[k] - n[k] * m);
+                store1(dx, p.h_dt, k * T + t, p.dres ? v + q[k] : v);
+            }
+    }
+    if (p.partial) {
+        float* part = p.partial + (uint64_t)blockIdx.x * p.cols;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (k * T + t < p.cols) part[k * T + t] = acc[k];
+    }
+}
+
+// ---- ring --------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t saddr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Bounded; false when it ran out.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const char* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Rows blockIdx.x, + gridDim.x, ... by one CTA.  Stage i % S holds the row of turn i: x, then the
+// residual.  Thread 0 starts the copies of turn i + S - 1 once turn i's reduction has passed its
+// barrier: every thread is then done with that stage's last row (turn i - 1).  A copy that does not
+// arrive makes the row NaN.
+template <uint32_t NCH>
+__global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+    extern __shared__ __align__(128) uint8_t stages[];
+    __shared__ float slots[2][2][32];
+    __shared__ uint64_t full[kRingStages];
+    const uint32_t T = blockDim.x, t = threadIdx.x;
+    const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
+    const uint32_t stage_bytes = xb + rb;
+    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    auto start = [&](uint64_t i) {
+        const uint64_t r = blockIdx.x + i * gridDim.x;
+        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+        bar_expect_tx(bar, stage_bytes);
+        bulk_load(dst, p.x + r * p.x_pitch, xb, bar);
+        if (rb) bulk_load(dst + xb, p.res + r * p.res_pitch, rb, bar);
+    };
+    if (t == 0) {
+        for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+    }
+    float w[NCH][8];
+#pragma unroll
+    for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) w[i][k] = 1.0f;
+    if (p.w) {
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) load8<true>(p.w, p.w_dt, 8 * (i * T + t), p.cols, w[i]);
+    }
+    __syncthreads();
+
+    uint32_t st = 0, phase = 0;
+    for (uint64_t turn = 0; turn < turns; ++turn) {
+        const uint64_t r = blockIdx.x + turn * gridDim.x;
+        const bool here = bar_wait(saddr(full + st), phase);
+        const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
+        float h[NCH][8], sum = 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) load8<true>(row, p.x_dt, 8 * (i * T + t), p.cols, h[i]);
+        if (rb) {
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i) {
+                float q[8];
+                load8<true>(row + xb, p.res_dt, 8 * (i * T + t), p.cols, q);
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) h[i][k] += q[k];
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) sum += h[i][k] * h[i][k];
+        if (!here) sum = __int_as_float(0x7FC00000);
+        const float s = rsqrtf(row_reduce(sum, T, slots[turn & 1][0], Sum()) * p.inv_cols + p.eps);
+        if (t == 0) {
+            if (turn + S - 1 < turns) start(turn + S - 1);
+            if (p.rstd) p.rstd[r] = s;
+        }
+        if (p.res_out) {
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i)
+                store8<true>(p.res_out + r * p.res_out_pitch, p.res_dt, 8 * (i * T + t), p.cols, h[i]);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) h[i][k] *= s * w[i][k];
+        if (p.y_dt == DTT_E4M3) {
+            float m[NCH];
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i) {
+                m[i] = 0.0f;
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) m[i] = max_nan(m[i], fabsf(h[i][k]));
+            }
+            if (p.group_lanes == 0) {
+                float all = m[0];
+#pragma unroll
+                for (uint32_t i = 1; i < NCH; ++i) all = max_nan(all, m[i]);
+                const float scale = max_nan(row_reduce(all, T, slots[turn & 1][1], MaxNan()) / kE4m3Max, kScaleMin);
+                if (t == 0) p.scales[r] = scale;
+                const float inv = 1.0f / scale;
+#pragma unroll
+                for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) h[i][k] *= inv;
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < NCH; ++i) {
+                    for (uint32_t d = p.group_lanes >> 1; d > 0; d >>= 1)
+                        m[i] = max_nan(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], d));
+                    const float scale = max_nan(m[i] / kE4m3Max, kScaleMin), inv = 1.0f / scale;
+                    const uint32_t c = 8 * (i * T + t);
+                    if (t % p.group_lanes == 0 && c < p.cols) p.scales[r * p.groups + c / (8 * p.group_lanes)] = scale;
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) h[i][k] *= inv;
+                }
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) store8<true>(p.y + r * p.y_pitch, p.y_dt, 8 * (i * T + t), p.cols, h[i]);
+        if (++st == S) { st = 0; phase ^= 1; }
+    }
+}
+
+// The backward pass the same way: a stage holds dy, h, then dres.
+template <uint32_t NCH>
+__global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+    extern __shared__ __align__(128) uint8_t stages[];
+    __shared__ float slots[2][32];
+    __shared__ uint64_t full[kRingStages];
+    const uint32_t T = blockDim.x, t = threadIdx.x;
+    const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
+    const uint32_t stage_bytes = gb + hb + (p.dres ? hb : 0);
+    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    auto start = [&](uint64_t i) {
+        const uint64_t r = blockIdx.x + i * gridDim.x;
+        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+        bar_expect_tx(bar, stage_bytes);
+        bulk_load(dst, p.dy + r * p.dy_pitch, gb, bar);
+        bulk_load(dst + gb, p.h + r * p.h_pitch, hb, bar);
+        if (p.dres) bulk_load(dst + gb + hb, p.dres + r * p.dres_pitch, hb, bar);
+    };
+    if (t == 0) {
+        for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+    }
+    float w[NCH][8], acc[NCH][8];
+#pragma unroll
+    for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            w[i][k] = 1.0f;
+            acc[i][k] = 0.0f;
+        }
+    if (p.w) {
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) load8<true>(p.w, p.w_dt, 8 * (i * T + t), p.cols, w[i]);
+    }
+    __syncthreads();
+
+    uint32_t st = 0, phase = 0;
+    for (uint64_t turn = 0; turn < turns; ++turn) {
+        const uint64_t r = blockIdx.x + turn * gridDim.x;
+        const float s = p.rstd[r];
+        const bool here = bar_wait(saddr(full + st), phase);
+        const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
+        float g[NCH][8], n[NCH][8], dot = 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) {
+            load8<true>(row, p.dy_dt, 8 * (i * T + t), p.cols, g[i]);
+            load8<true>(row + gb, p.h_dt, 8 * (i * T + t), p.cols, n[i]);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                n[i][k] *= s;
+                acc[i][k] += g[i][k] * n[i][k];
+                g[i][k] *= w[i][k];
+                dot += g[i][k] * n[i][k];
+            }
+        }
+        if (!here) dot = __int_as_float(0x7FC00000);
+        const float m = row_reduce(dot, T, slots[turn & 1], Sum()) * p.inv_cols;
+        if (t == 0 && turn + S - 1 < turns) start(turn + S - 1);
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) {
+            const uint32_t c = 8 * (i * T + t);
+            float o[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) o[k] = s * (g[i][k] - n[i][k] * m);
+            if (p.dres) {
+                float q[8];
+                load8<true>(row + gb + hb, p.h_dt, c, p.cols, q);
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) o[k] += q[k];
+            }
+            store8<true>(p.dx + r * p.dx_pitch, p.h_dt, c, p.cols, o);
+        }
+        if (++st == S) { st = 0; phase ^= 1; }
+    }
+    if (p.partial) {
+        float* part = p.partial + (uint64_t)blockIdx.x * p.cols;
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) store8<true>(reinterpret_cast<char*>(part), DTT_F32, 8 * (i * T + t), p.cols, acc[i]);
+    }
+}
+
 // dweight[c] = the partial rows' sum.  32 columns a CTA; its 8 warps take every eighth partial row,
 // and their sums are added in warp order.
 __global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* partial, uint32_t partials,
@@ -371,7 +739,7 @@ struct Shape {
     uint32_t nch, tpr, rows_per_cta;
 };
 
-// Up to four chunks a thread in registers; `threads` threads a row at most.
+// Chunks: up to four a thread in registers; `threads` threads a row at most.
 Shape shape_of(uint32_t cols, uint32_t threads) {
     const uint32_t chunks = (cols + 7) / 8;
     for (uint32_t nch : {1u, 2u, 4u}) {
@@ -381,24 +749,104 @@ Shape shape_of(uint32_t cols, uint32_t threads) {
     return {kLong, threads, 1};
 }
 
-template <bool VEC>
-void launch_fwd(const FwdParams& p, const Shape& s, cudaStream_t stream) {
-    const dim3 block(s.tpr, s.rows_per_cta);
-    const uint32_t grid = (uint32_t)((p.rows + s.rows_per_cta - 1) / s.rows_per_cta);
-    if (s.nch == 1) rmsnorm_fwd_kernel<1, VEC><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 2) rmsnorm_fwd_kernel<2, VEC><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 4) rmsnorm_fwd_kernel<4, VEC><<<grid, block, 0, stream>>>(p);
-    else rmsnorm_fwd_kernel<kLong, VEC><<<grid, block, 0, stream>>>(p);
+struct Ring {
+    uint32_t nch, threads, ctas, stages, smem;       // ctas: of an SM; 0: no ring for these rows
+};
+
+// Two chunks a thread up to 512 threads, then four (twice the registers).  As many CTAs as make
+// `threads_per_sm` threads an SM (half as many with four chunks), fewer where three stages each would
+// not fit; then as many stages as fit.
+Ring ring_of(uint32_t cols, uint32_t stage_bytes, uint32_t threads_per_sm) {
+    const uint32_t chunks = cols / 8;
+    Ring g{};
+    for (uint32_t nch : {2u, 4u}) {
+        g.nch = nch;
+        g.threads = ((chunks + nch - 1) / nch + 31) / 32 * 32;
+        if (g.threads <= kRingThreads) break;
+    }
+    if (g.threads < 64 || g.threads > kRingThreads || 3 * stage_bytes > kRingSmem) return {};
+    g.ctas = std::min(std::max(threads_per_sm * 2 / g.nch / g.threads, 1u), kRingSmem / (3 * stage_bytes));
+    g.stages = std::min(kRingStages, kRingSmem / (g.ctas * stage_bytes));
+    g.smem = g.stages * stage_bytes;
+    return g;
 }
 
-template <bool VEC>
-void launch_bwd(const BwdParams& p, const Shape& s, cudaStream_t stream) {
+uint32_t sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 1;
+    return (uint32_t)std::max(sms, 1);
+}
+
+// Threads of the element form: E elements each, `threads` at most; 0: the row is longer.
+uint32_t element_threads(uint32_t cols, uint32_t E, uint32_t threads) {
+    const uint32_t t = ((cols + E - 1) / E + 31) / 32 * 32;
+    return t <= threads ? t : 0;
+}
+
+void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
+    const uint32_t xe = p.x_dt == DTT_BF16 ? 2 : 4, re = p.res ? (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
+    const uint32_t sms = sm_count();
+    const Ring g = vec ? ring_of(p.cols, (uint32_t)std::min<uint64_t>((uint64_t)p.cols * (xe + re), kRingSmem), 1024) : Ring{};
+    if (g.ctas && p.rows >= 2 * sms) {
+        const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
+        if (g.nch == 2) rmsnorm_fwd_ring_kernel<2><<<grid, g.threads, g.smem, stream>>>(p, g.stages);
+        else rmsnorm_fwd_ring_kernel<4><<<grid, g.threads, g.smem, stream>>>(p, g.stages);
+        return;
+    }
+    if (!vec) {
+        if (const uint32_t t = element_threads(p.cols, 8, kFwdThreads)) {
+            rmsnorm_fwd_elements_kernel<8><<<(uint32_t)p.rows, t, 0, stream>>>(p);
+            return;
+        }
+        if (const uint32_t t = element_threads(p.cols, 16, kFwdThreads)) {
+            rmsnorm_fwd_elements_kernel<16><<<(uint32_t)p.rows, t, 0, stream>>>(p);
+            return;
+        }
+        rmsnorm_fwd_kernel<kLong, false><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
+        return;
+    }
+    const Shape s = shape_of(p.cols, kFwdThreads);
+    const dim3 block(s.tpr, s.rows_per_cta);
+    const uint32_t grid = (uint32_t)((p.rows + s.rows_per_cta - 1) / s.rows_per_cta);
+    if (s.nch == 1) rmsnorm_fwd_kernel<1, true><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 2) rmsnorm_fwd_kernel<2, true><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 4) rmsnorm_fwd_kernel<4, true><<<grid, block, 0, stream>>>(p);
+    else rmsnorm_fwd_kernel<kLong, true><<<grid, block, 0, stream>>>(p);
+}
+
+// Sets p.partials, the partial rows of the weight's gradient that the launch writes.
+void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
+    const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
+    const uint32_t sms = sm_count();
+    const Ring g = vec ? ring_of(p.cols, (uint32_t)std::min<uint64_t>((uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he), kRingSmem), 512)
+                       : Ring{};
+    if (g.ctas && p.rows >= 2 * sms) {
+        p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)kMaxPartials});
+        if (g.nch == 2) rmsnorm_bwd_ring_kernel<2><<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
+        else rmsnorm_bwd_ring_kernel<4><<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
+        return;
+    }
+    p.partials = (uint32_t)std::min<uint64_t>(p.rows, kMaxPartials);
+    if (!vec) {
+        if (const uint32_t t = element_threads(p.cols, 8, kBwdThreads)) {
+            rmsnorm_bwd_elements_kernel<8><<<p.partials, t, 0, stream>>>(p);
+            return;
+        }
+        if (const uint32_t t = element_threads(p.cols, 16, kBwdThreads)) {
+            rmsnorm_bwd_elements_kernel<16><<<p.partials, t, 0, stream>>>(p);
+            return;
+        }
+        rmsnorm_bwd_kernel<kLong, false><<<p.partials, kBwdThreads, 0, stream>>>(p);
+        return;
+    }
+    const Shape s = shape_of(p.cols, kBwdThreads);
     const dim3 block(s.tpr, s.rows_per_cta);
     const uint32_t grid = (p.partials + s.rows_per_cta - 1) / s.rows_per_cta;
-    if (s.nch == 1) rmsnorm_bwd_kernel<1, VEC><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 2) rmsnorm_bwd_kernel<2, VEC><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 4) rmsnorm_bwd_kernel<4, VEC><<<grid, block, 0, stream>>>(p);
-    else rmsnorm_bwd_kernel<kLong, VEC><<<grid, block, 0, stream>>>(p);
+    if (s.nch == 1) rmsnorm_bwd_kernel<1, true><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 2) rmsnorm_bwd_kernel<2, true><<<grid, block, 0, stream>>>(p);
+    else if (s.nch == 4) rmsnorm_bwd_kernel<4, true><<<grid, block, 0, stream>>>(p);
+    else rmsnorm_bwd_kernel<kLong, true><<<grid, block, 0, stream>>>(p);
 }
 
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
@@ -444,15 +892,21 @@ cudaError_t preload_norm_kernels() {
     const void* kernels[] = {
         (const void*)rmsnorm_fwd_kernel<1, true>, (const void*)rmsnorm_fwd_kernel<2, true>,
         (const void*)rmsnorm_fwd_kernel<4, true>, (const void*)rmsnorm_fwd_kernel<kLong, true>,
-        (const void*)rmsnorm_fwd_kernel<1, false>, (const void*)rmsnorm_fwd_kernel<2, false>,
-        (const void*)rmsnorm_fwd_kernel<4, false>, (const void*)rmsnorm_fwd_kernel<kLong, false>,
+        (const void*)rmsnorm_fwd_kernel<kLong, false>, (const void*)rmsnorm_fwd_elements_kernel<8>,
+        (const void*)rmsnorm_fwd_elements_kernel<16>,
         (const void*)rmsnorm_bwd_kernel<1, true>, (const void*)rmsnorm_bwd_kernel<2, true>,
         (const void*)rmsnorm_bwd_kernel<4, true>, (const void*)rmsnorm_bwd_kernel<kLong, true>,
-        (const void*)rmsnorm_bwd_kernel<1, false>, (const void*)rmsnorm_bwd_kernel<2, false>,
-        (const void*)rmsnorm_bwd_kernel<4, false>, (const void*)rmsnorm_bwd_kernel<kLong, false>,
-        (const void*)rmsnorm_dweight_kernel};
+        (const void*)rmsnorm_bwd_kernel<kLong, false>, (const void*)rmsnorm_bwd_elements_kernel<8>,
+        (const void*)rmsnorm_bwd_elements_kernel<16>, (const void*)rmsnorm_dweight_kernel};
     for (const void* k : kernels) {
         const cudaError_t e = prepare(k);
+        if (e != cudaSuccess) return e;
+    }
+    const void* rings[] = {(const void*)rmsnorm_fwd_ring_kernel<2>, (const void*)rmsnorm_fwd_ring_kernel<4>,
+                           (const void*)rmsnorm_bwd_ring_kernel<2>, (const void*)rmsnorm_bwd_ring_kernel<4>};
+    for (const void* k : rings) {
+        cudaError_t e = prepare(k);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmem);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -514,12 +968,10 @@ extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, con
     p.group_lanes = d->group / 8;
     p.eps = d->eps;
     p.inv_cols = 1.0f / (float)d->cols;
-    const bool vec = aligned(x, x_pitch, 16) && aligned(residual, residual ? residual_pitch : 0, 16) &&
+    const bool vec = d->cols % 8 == 0 && aligned(x, x_pitch, 16) && aligned(residual, residual ? residual_pitch : 0, 16) &&
                      aligned(weight, 0, 16) && aligned(residual_out, residual_out ? residual_out_pitch : 0, 16) &&
                      aligned(y, y_pitch, e4m3 ? 8 : 16);
-    const Shape s = shape_of(p.cols, kFwdThreads);
-    if (vec) launch_fwd<true>(p, s, stream);
-    else launch_fwd<false>(p, s, stream);
+    launch_fwd(p, vec, stream);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
@@ -567,16 +1019,13 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
     p.dx_pitch = dx_pitch;
     p.rows = rows;
     p.cols = (uint32_t)d->cols;
-    p.partials = (uint32_t)std::min<uint64_t>(rows, kMaxPartials);
     p.dy_dt = d->x_dtype;
     p.h_dt = d->residual_dtype;
     p.w_dt = d->weight_dtype;
     p.inv_cols = 1.0f / (float)d->cols;
-    const bool vec = aligned(dy, dy_pitch, 16) && aligned(h, h_pitch, 16) && aligned(weight, 0, 16) &&
+    const bool vec = d->cols % 8 == 0 && aligned(dy, dy_pitch, 16) && aligned(h, h_pitch, 16) && aligned(weight, 0, 16) &&
                      aligned(dres, dres ? dres_pitch : 0, 16) && aligned(dx, dx_pitch, 16);
-    const Shape s = shape_of(p.cols, kBwdThreads);
-    if (vec) launch_bwd<true>(p, s, stream);
-    else launch_bwd<false>(p, s, stream);
+    launch_bwd(p, vec, stream);
     if (dweight)
         rmsnorm_dweight_kernel<<<(p.cols + 31) / 32, 256, 0, stream>>>(p.partial, p.partials, p.cols, dweight);
     const cudaError_t e = cudaGetLastError();

@@ -65,7 +65,7 @@ int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* desc, uint64_t rows, const void*
  *     dweight_c = sum over rows of dy_c n_c             (f32)
  * dres is the gradient that reaches residual_out from its other readers (NULL: none).  An 8-bit
  * y passes its gradient straight through.  Sums are f32 in an order that depends on the sizes
- * alone, so the same inputs give the same bits.  rows 0: dweight is zeroed, nothing else.
+ * and alignments alone, so the same call gives the same bits.  rows 0: dweight is zeroed, nothing else.
  *  - dweight may be NULL (not computed; workspace is then unused and may be NULL); a NULL weight
  *    (1 everywhere) needs dweight NULL.  dx may be dres itself; no other overlap.
  *  - workspace: dtt_rmsnorm_workspace's bytes, 16-byte aligned.
