@@ -13,10 +13,9 @@
 #include <cmath>
 #include <cstdint>
 
-#include <cuda_bf16.h>
-
 #include "dtt_ops.h"
 #include "internal.h"
+#include "rowio.cuh"
 
 namespace dtt {
 namespace {
@@ -60,85 +59,6 @@ struct BwdParams {
     uint32_t dy_dt, h_dt, w_dt;
     float inv_cols;
 };
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {      // 16 bits
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// The larger of two, NaN if either is: a NaN in a row must reach its scale.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
-// Columns c .. c + 7 of a row, zeros from `cols` on.  VEC: the row is 16-byte aligned, so a whole
-// chunk is one or two 16-byte loads.
-template <bool VEC>
-__device__ __forceinline__ void load8(const char* row, uint32_t dt, uint32_t c, uint32_t cols, float (&v)[8]) {
-    if (VEC && c + 8 <= cols) {
-        if (dt == DTT_BF16) {
-            const uint4 q = *reinterpret_cast<const uint4*>(row + (uint64_t)c * 2);
-            v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
-            v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
-        } else {
-            const float4 a = *reinterpret_cast<const float4*>(row + (uint64_t)c * 4);
-            const float4 b = *reinterpret_cast<const float4*>(row + (uint64_t)c * 4 + 16);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        }
-        return;
-    }
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) {
-        v[k] = 0.0f;
-        if (c + k < cols) {
-            if (dt == DTT_BF16)
-                v[k] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[c + k] << 16);
-            else
-                v[k] = reinterpret_cast<const float*>(row)[c + k];
-        }
-    }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store8(char* row, uint32_t dt, uint32_t c, uint32_t cols, const float (&v)[8]) {
-    if (VEC && c + 8 <= cols) {
-        if (dt == DTT_BF16) {
-            *reinterpret_cast<uint4*>(row + (uint64_t)c * 2) =
-                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-        } else if (dt == DTT_F32) {
-            *reinterpret_cast<float4*>(row + (uint64_t)c * 4) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(row + (uint64_t)c * 4 + 16) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<uint2*>(row + c) =
-                make_uint2(pack_e4m3(v[0], v[1]) | pack_e4m3(v[2], v[3]) << 16,
-                           pack_e4m3(v[4], v[5]) | pack_e4m3(v[6], v[7]) << 16);
-        }
-        return;
-    }
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-        if (c + k < cols) {
-            if (dt == DTT_BF16)
-                reinterpret_cast<uint16_t*>(row)[c + k] = (uint16_t)pack_bf16(v[k], 0.0f);
-            else if (dt == DTT_F32)
-                reinterpret_cast<float*>(row)[c + k] = v[k];
-            else
-                reinterpret_cast<uint8_t*>(row)[c + k] = (uint8_t)pack_e4m3(v[k], 0.0f);
-        }
-}
 
 struct Sum {
     __device__ float operator()(float a, float b) const { return a + b; }
@@ -355,20 +275,6 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsn
 }
 
 // ---- elements ----------------------------------------------------------------------------------
-__device__ __forceinline__ float load1(const char* row, uint32_t dt, uint32_t c) {
-    return dt == DTT_BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[c] << 16)
-                          : reinterpret_cast<const float*>(row)[c];
-}
-
-__device__ __forceinline__ void store1(char* row, uint32_t dt, uint32_t c, float v) {
-    if (dt == DTT_BF16)
-        reinterpret_cast<uint16_t*>(row)[c] = (uint16_t)pack_bf16(v, 0.0f);
-    else if (dt == DTT_F32)
-        reinterpret_cast<float*>(row)[c] = v;
-    else
-        reinterpret_cast<uint8_t*>(row)[c] = (uint8_t)pack_e4m3(v, 0.0f);
-}
-
 // Columns t, t + T, ... (E of them, those below `cols`) of a row.
 template <uint32_t E>
 __device__ __forceinline__ void load_elements(const char* row, uint32_t dt, uint32_t cols, float (&v)[E]) {
@@ -489,18 +395,6 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const
 }
 
 // ---- ring --------------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t saddr(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
 // Bounded; false when it ran out.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {

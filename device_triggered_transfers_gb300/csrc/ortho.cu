@@ -19,6 +19,7 @@
 
 #include "dtt_ops.h"
 #include "internal.h"
+#include "rowio.cuh"
 
 namespace dtt {
 namespace {
@@ -37,8 +38,8 @@ constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * TILE_S
 constexpr uint32_t IDESC = (1u << 4) | ((TN >> 3) << 17) | ((TM >> 4) << 24);
 constexpr uint32_t IDESC_B_MN = 1u << 16;            // B stored with N contiguous
 
-constexpr uint32_t kLoadTile = 32;                   // ortho_load_kernel: elements a side
-constexpr uint32_t kMaxParts = 304;                  // its CTAs a matrix at most: two a SM
+constexpr uint32_t kStartTile = 64;                  // ortho_start_tiles_kernel: elements a side
+constexpr uint32_t kMaxParts = 1216;                 // ortho_update_kernel: CTAs a matrix at most, eight a SM
 
 enum Product { GRAM, POLY, APPLY };
 
@@ -59,20 +60,8 @@ struct GemmParams {
     uint32_t* err;
 };
 
-__device__ __forceinline__ uint32_t saddr(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // Bounded wait for the phase of the given parity; false when the limit ran out or another role
@@ -162,12 +151,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
@@ -402,96 +385,161 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_gemm_kernel(const __grid_con
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
 }
 
-struct LoadParams {
+struct UpdateParams {
     const char* x;
     uint64_t x_pitch, x_stride;
     char* mom;                   // f32, or null
     uint64_t mom_pitch, mom_stride;
-    float mu;
+    float mu, eps;
     uint32_t nesterov, x_dt;
-    uint32_t rows, cols, transposed, parts;
+    uint32_t rows, cols, parts;
+    float* sums;                 // [batch][parts]
     float* x32;
+    __half* x16;
     uint64_t l_pitch;
     uint32_t S;
-    float* sums;                 // [batch][parts]
 };
 
-// u from the gradient (and the momentum, which it updates), into x32 with the smaller side first, and
-// the parts of |u|^2: CTA q of a matrix takes tiles q, q + parts, ... and adds in a fixed order.
-__global__ void __launch_bounds__(256) ortho_load_kernel(const __grid_constant__ LoadParams p) {
-    __shared__ float tile[kLoadTile][kLoadTile + 1];
-    __shared__ float warp_sum[8];
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, m = blockIdx.y;
-    const uint32_t tc = (p.cols + kLoadTile - 1) / kLoadTile, tr = (p.rows + kLoadTile - 1) / kLoadTile;
+// Sum over a CTA's 256 threads, in one fixed order, the same bits in each.
+__device__ __forceinline__ float cta_sum(float v, float (&slot)[8]) {
+#pragma unroll
+    for (uint32_t o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = slot[0];
+#pragma unroll
+    for (uint32_t w = 1; w < 8; ++w) v += slot[w];
+    return v;
+}
+
+// The momentum's update, and a part of |u|^2 from each of `parts` CTAs a matrix, which stride over its
+// rows in chunks of 8 columns (VEC) or single elements.
+template <bool VEC>
+__global__ void __launch_bounds__(256) ortho_update_kernel(const __grid_constant__ UpdateParams p) {
+    __shared__ float slot[8];
+    constexpr uint32_t W = VEC ? 8 : 1;
+    const uint32_t m = blockIdx.y, per_row = (p.cols + W - 1) / W;
     const char* x = p.x + (uint64_t)m * p.x_stride;
     char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
-    float* x32 = p.x32 + (uint64_t)m * p.S * p.l_pitch;
+    const uint64_t total = (uint64_t)p.rows * per_row;
     float sum = 0.0f;
-    for (uint64_t t = blockIdx.x; t < (uint64_t)tc * tr; t += p.parts) {
-        const uint32_t r0 = (uint32_t)(t / tc) * kLoadTile, c0 = (uint32_t)(t % tc) * kLoadTile;
-        const uint32_t c = c0 + lane;
+#pragma unroll 4
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (uint64_t)p.parts * 256) {
+        const uint32_t r = (uint32_t)(i / per_row), c = (uint32_t)(i - (uint64_t)r * per_row) * W;
+        float u[8], v[8];
+        if (VEC) load8<true>(x + r * p.x_pitch, p.x_dt, c, p.cols, u);
+        else u[0] = load1(x + r * p.x_pitch, p.x_dt, c);
+        if (mom) {
+            char* row = mom + r * p.mom_pitch;
+            if (VEC) load8<true>(row, DTT_F32, c, p.cols, v);
+            else v[0] = load1(row, DTT_F32, c);
 #pragma unroll
-        for (uint32_t k = 0; k < kLoadTile / 8; ++k) {
-            const uint32_t r = r0 + warp + 8 * k;
-            float u = 0.0f;
-            if (r < p.rows && c < p.cols) {
-                const char* at = x + (uint64_t)r * p.x_pitch;
-                u = p.x_dt == DTT_BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(at)[c] << 16)
-                                       : reinterpret_cast<const float*>(at)[c];
-                if (mom) {
-                    float* mp = reinterpret_cast<float*>(mom + (uint64_t)r * p.mom_pitch) + c;
-                    const float v = p.mu * *mp + u;
-                    *mp = v;
-                    u = p.nesterov ? u + p.mu * v : v;
-                }
-                sum += u * u;
-                if (!p.transposed) x32[(uint64_t)r * p.l_pitch + c] = u;
+            for (uint32_t k = 0; k < W; ++k) {
+                v[k] = p.mu * v[k] + u[k];
+                u[k] = p.nesterov ? u[k] + p.mu * v[k] : v[k];
             }
-            tile[warp + 8 * k][lane] = u;
+            if (VEC) store8<true>(row, DTT_F32, c, p.cols, v);
+            else store1(row, DTT_F32, c, v[0]);
         }
-        if (p.transposed) {
-            __syncthreads();
 #pragma unroll
-            for (uint32_t k = 0; k < kLoadTile / 8; ++k) {
-                const uint32_t cc = c0 + warp + 8 * k, rr = r0 + lane;
-                if (cc < p.cols && rr < p.rows) x32[(uint64_t)cc * p.l_pitch + rr] = tile[lane][warp + 8 * k];
-            }
-            __syncthreads();
-        }
+        for (uint32_t k = 0; k < W; ++k) sum += u[k] * u[k];
     }
+    sum = cta_sum(sum, slot);
+    if (threadIdx.x == 0) p.sums[(uint64_t)m * p.parts + blockIdx.x] = sum;
+}
+
+// 1 / (|u| + eps) of matrix m, from its parts; 0 where that overflows (u is then 0 in f16 as well).
+__device__ __forceinline__ float inverse_norm(const UpdateParams& p, uint32_t m, float (&slot)[8]) {
+    float sum = 0.0f;
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < p.parts; i += 256) sum += p.sums[(uint64_t)m * p.parts + i];
+    const float inv = 1.0f / (sqrtf(cta_sum(sum, slot)) + p.eps);
+    return isinf(inv) ? 0.0f : inv;
+}
+
+// u again (the momentum is updated by now) and X = u / (|u| + eps), in f32 and as the f16 operand: rows
+// <= cols, 16-byte aligned.  A thread has two chunks of 8 columns under way.
+__global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant__ UpdateParams p) {
+    __shared__ float slot[8];
+    const uint32_t m = blockIdx.y, per_row = p.cols / 8, total = p.rows * per_row, step = gridDim.x * 256;
+    const char* x = p.x + (uint64_t)m * p.x_stride;
+    const char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
+    float* x32 = p.x32 + (uint64_t)m * p.S * p.l_pitch;
+    __half* x16 = p.x16 + (uint64_t)m * p.S * p.l_pitch;
+    const float inv = inverse_norm(p, m, slot);
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += 2 * step) {
+        float u[2][8], v[2][8];
 #pragma unroll
-    for (uint32_t o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) warp_sum[warp] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (uint32_t w = 1; w < 8; ++w) sum += warp_sum[w];
-        p.sums[(uint64_t)m * p.parts + blockIdx.x] = sum;
+        for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t j = min(i + h * step, total - 1), r = j / per_row, c = 8 * (j - r * per_row);
+            load8<true>(x + r * p.x_pitch, p.x_dt, c, p.cols, u[h]);
+            if (mom) load8<true>(mom + r * p.mom_pitch, DTT_F32, c, p.cols, v[h]);
+        }
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t j = i + h * step, r = j / per_row, c = 8 * (j - r * per_row);
+            if (j >= total) break;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                if (mom) u[h][k] = p.nesterov ? u[h][k] + p.mu * v[h][k] : v[h][k];
+                u[h][k] *= inv;
+            }
+            store8<true>(reinterpret_cast<char*>(x32 + r * p.l_pitch), DTT_F32, c, p.cols, u[h]);
+            *reinterpret_cast<uint4*>(x16 + r * p.l_pitch + c) =
+                make_uint4(pack_f16(u[h][0], u[h][1]), pack_f16(u[h][2], u[h][3]), pack_f16(u[h][4], u[h][5]),
+                           pack_f16(u[h][6], u[h][7]));
+        }
     }
 }
 
-// X = u / (|u| + eps): x32 in place and its f16 operand copy.
-__global__ void __launch_bounds__(256) ortho_scale_kernel(float* x32, __half* x16, uint64_t matrix /* elements */,
-                                                          const float* sums, uint32_t parts, float eps) {
-    __shared__ float warp_sum[8];
-    const uint32_t m = blockIdx.y;
-    float sum = 0.0f;
-    for (uint32_t i = threadIdx.x; i < parts; i += 256) sum += sums[(uint64_t)m * parts + i];
+// The same for any alignment, and for rows > cols (TALL: turned over in shared memory): a tile of 64 x
+// 64 elements a CTA.
+template <bool TALL>
+__global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_constant__ UpdateParams p) {
+    __shared__ float slot[8];
+    __shared__ float tile[TALL ? kStartTile : 1][kStartTile + 1];
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, m = blockIdx.z;
+    const uint32_t r0 = blockIdx.y * kStartTile, c0 = blockIdx.x * kStartTile;
+    const char* x = p.x + (uint64_t)m * p.x_stride;
+    const char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
+    float u[kStartTile / 8][2];
 #pragma unroll
-    for (uint32_t o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = sum;
-    __syncthreads();
-    sum = 0.0f;
+    for (uint32_t k = 0; k < kStartTile / 8; ++k)
 #pragma unroll
-    for (uint32_t w = 0; w < 8; ++w) sum += warp_sum[w];
-    const float norm = sqrtf(sum) + eps;
-    float4* x = reinterpret_cast<float4*>(x32 + (uint64_t)m * matrix);
-    uint2* h = reinterpret_cast<uint2*>(x16 + (uint64_t)m * matrix);
-    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < matrix / 4; i += (uint64_t)gridDim.x * 256) {
-        float4 v = x[i];
-        v = make_float4(v.x / norm, v.y / norm, v.z / norm, v.w / norm);
-        x[i] = v;
-        h[i] = make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+        for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t r = r0 + warp + 8 * k, c = c0 + lane + 32 * h;
+            u[k][h] = 0.0f;
+            if (r < p.rows && c < p.cols) {
+                if (!mom || p.nesterov) u[k][h] = load1(x + r * p.x_pitch, p.x_dt, c);
+                if (mom) {
+                    const float v = load1(mom + r * p.mom_pitch, DTT_F32, c);
+                    u[k][h] = p.nesterov ? u[k][h] + p.mu * v : v;
+                }
+            }
+        }
+    const float inv = inverse_norm(p, m, slot);
+    float* x32 = p.x32 + (uint64_t)m * p.S * p.l_pitch;
+    __half* x16 = p.x16 + (uint64_t)m * p.S * p.l_pitch;
+    if (TALL) {
+#pragma unroll
+        for (uint32_t k = 0; k < kStartTile / 8; ++k)
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) tile[warp + 8 * k][lane + 32 * h] = u[k][h];
+        __syncthreads();
     }
+#pragma unroll
+    for (uint32_t k = 0; k < kStartTile / 8; ++k)
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t a = warp + 8 * k, b = lane + 32 * h;      // TALL: column a, row b of the tile
+            const uint32_t r = r0 + (TALL ? b : a), c = c0 + (TALL ? a : b);
+            if (r < p.rows && c < p.cols) {
+                const float v = (TALL ? tile[b][a] : u[k][h]) * inv;
+                const uint64_t at = TALL ? c * p.l_pitch + r : r * p.l_pitch + c;
+                x32[at] = v;
+                x16[at] = __float2half_rn(v);
+            }
+        }
 }
 
 // A batch of matrices rows x cols f16, `pitch` elements a row, in boxes of 64 columns (128 bytes,
@@ -583,8 +631,11 @@ cudaError_t preload_ortho_kernels() {
     cudaError_t e = prepare_gemm<GRAM>();
     if (e == cudaSuccess) e = prepare_gemm<POLY>();
     if (e == cudaSuccess) e = prepare_gemm<APPLY>();
-    if (e == cudaSuccess) e = prepare_kernel(ortho_load_kernel);
-    if (e == cudaSuccess) e = prepare_kernel(ortho_scale_kernel);
+    if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<true>);
+    if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<false>);
+    if (e == cudaSuccess) e = prepare_kernel(ortho_start_kernel);
+    if (e == cudaSuccess) e = prepare_kernel(ortho_start_tiles_kernel<true>);
+    if (e == cudaSuccess) e = prepare_kernel(ortho_start_tiles_kernel<false>);
     return e;
 }
 
@@ -669,30 +720,40 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     if (reinterpret_cast<uintptr_t>(err) % 4) return fail(DTT_EINVAL, "%s: err is misaligned", who);
 
     float* x32 = reinterpret_cast<float*>(o->ws + l.x32);
-    float* sums = reinterpret_cast<float*>(o->ws + l.sums);
-    LoadParams lp{};
-    lp.x = static_cast<const char*>(x);
-    lp.x_pitch = x_pitch;
-    lp.x_stride = x_stride;
-    lp.mom = reinterpret_cast<char*>(momentum);
-    lp.mom_pitch = momentum_pitch;
-    lp.mom_stride = momentum_stride;
-    lp.mu = d.mu;
-    lp.nesterov = d.nesterov;
-    lp.x_dt = d.x_dtype;
-    lp.rows = (uint32_t)d.rows;
-    lp.cols = (uint32_t)d.cols;
-    lp.transposed = d.rows > d.cols;
-    const uint64_t load_tiles = ((d.rows + kLoadTile - 1) / kLoadTile) * ((d.cols + kLoadTile - 1) / kLoadTile);
-    lp.parts = (uint32_t)std::min<uint64_t>(load_tiles, kMaxParts);
-    lp.x32 = x32;
-    lp.l_pitch = l.l_pitch;
-    lp.S = (uint32_t)l.S;
-    lp.sums = sums;
-    ortho_load_kernel<<<dim3(lp.parts, d.batch), 256, 0, stream>>>(lp);
-    const uint64_t matrix = l.S * l.l_pitch;
-    ortho_scale_kernel<<<dim3((uint32_t)std::min<uint64_t>((matrix / 4 + 255) / 256, 4 * o->sms), d.batch), 256, 0, stream>>>(
-        x32, reinterpret_cast<__half*>(o->ws + l.x16[0]), matrix, sums, lp.parts, d.eps);
+    UpdateParams up{};
+    up.x = static_cast<const char*>(x);
+    up.x_pitch = x_pitch;
+    up.x_stride = x_stride;
+    up.mom = reinterpret_cast<char*>(momentum);
+    up.mom_pitch = momentum_pitch;
+    up.mom_stride = momentum_stride;
+    up.mu = d.mu;
+    up.eps = d.eps;
+    up.nesterov = d.nesterov;
+    up.x_dt = d.x_dtype;
+    up.rows = (uint32_t)d.rows;
+    up.cols = (uint32_t)d.cols;
+    up.sums = reinterpret_cast<float*>(o->ws + l.sums);
+    up.x32 = x32;
+    up.x16 = reinterpret_cast<__half*>(o->ws + l.x16[0]);
+    up.l_pitch = l.l_pitch;
+    up.S = (uint32_t)l.S;
+    const bool tall = d.rows > d.cols;
+    bool vec = d.cols % 8 == 0;
+    for (const auto& a : args)
+        if (a.p != out && a.p) vec = vec && reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.pitch % 16 == 0 && a.stride % 16 == 0;
+    const uint64_t items = d.rows * (vec ? d.cols / 8 : d.cols);
+    up.parts = (uint32_t)std::min<uint64_t>((items + 1023) / 1024, std::max(kMaxParts / d.batch, 1u));
+    if (vec) ortho_update_kernel<true><<<dim3(up.parts, d.batch), 256, 0, stream>>>(up);
+    else ortho_update_kernel<false><<<dim3(up.parts, d.batch), 256, 0, stream>>>(up);
+    if (vec && !tall) {
+        const uint32_t ctas = (uint32_t)std::min<uint64_t>((items + 511) / 512, std::max(8 * o->sms / d.batch, 1u));
+        ortho_start_kernel<<<dim3(ctas, d.batch), 256, 0, stream>>>(up);
+    } else {
+        const dim3 tiles((up.cols + kStartTile - 1) / kStartTile, (up.rows + kStartTile - 1) / kStartTile, d.batch);
+        if (tall) ortho_start_tiles_kernel<true><<<tiles, 256, 0, stream>>>(up);
+        else ortho_start_tiles_kernel<false><<<tiles, 256, 0, stream>>>(up);
+    }
 
     GemmParams g{};
     g.S = (uint32_t)l.S;
@@ -702,7 +763,7 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     g.x32 = x32;
     g.err = err;
     g.scale = d.scale;
-    g.transposed = lp.transposed;
+    g.transposed = tall;
     g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_pitch % 16 == 0 && (d.batch == 1 || out_stride % 16 == 0);
     g.out_pitch = out_pitch;
     g.out_stride = out_stride;
