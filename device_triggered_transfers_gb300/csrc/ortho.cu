@@ -12,7 +12,10 @@
 // stored twice, once transposed.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
+#include <cstdio>
 #include <cstdint>
+#include <mutex>
 #include <new>
 
 #include <cuda_fp16.h>
@@ -24,19 +27,23 @@
 namespace dtt {
 namespace {
 
-constexpr uint32_t TM = 128, TN = 128, BK = 64, UMMA_K = 16;
-constexpr uint32_t TILE_STAGE = TM * BK * 2;         // 16 KiB an operand and stage
+constexpr uint32_t BK = 64, UMMA_K = 16;
+constexpr uint32_t HALF_STAGE = 128 * BK * 2;        // 16 KiB: 128 rows or columns of an operand
 constexpr uint32_t STAGES = 6;
-constexpr uint32_t ACC_BUFS = 2;
-constexpr uint32_t TMEM_COLS = ACC_BUFS * TN;
+constexpr uint32_t ACC_BUFS = 2;                     // TMEM accumulators of the pair form
 constexpr uint32_t EPI_THREADS = 128;
 constexpr uint32_t THREADS = EPI_THREADS + 64;       // + TMA warp + MMA warp
 constexpr uint32_t TMA_WARP = 4, MMA_WARP = 5;
 constexpr uint32_t WAIT_LIMIT = 1u << 22;
-constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * TILE_STAGE + 256;
-// instruction descriptor (kind::f16): f32 accumulator, f16 operands, N = TN, M = TM
-constexpr uint32_t IDESC = (1u << 4) | ((TN >> 3) << 17) | ((TM >> 4) << 24);
+constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + 256;
+// instruction descriptor (kind::f16): f32 accumulator, f16 operands, M = m, N = n
+__host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 constexpr uint32_t IDESC_B_MN = 1u << 16;            // B stored with N contiguous
+// split form: the tile's f32 sums, and its f16 or bf16 rows, in the shared memory of the stages
+constexpr uint32_t T_PITCH = 132;                    // floats: rows 16 bytes apart in the banks
+constexpr uint32_t T16_PITCH = 130;                  // 16-bit elements: columns fall on different banks
+constexpr uint32_t T16_OFFSET = 128 * T_PITCH * 4;
+static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= STAGES * 2 * HALF_STAGE, "the tile fits the stages");
 
 constexpr uint32_t kStartTile = 64;                  // ortho_start_tiles_kernel: elements a side
 constexpr uint32_t kMaxParts = 1216;                 // ortho_update_kernel: CTAs a matrix at most, eight a SM
@@ -46,7 +53,8 @@ enum Product { GRAM, POLY, APPLY };
 struct GemmParams {
     CUtensorMap tmA, tmB;
     uint32_t S, L, K;            // output rows S and columns (GRAM, POLY: S; APPLY: L)
-    uint32_t batch, tiles_m, tiles_n, tiles;   // tiles: of one matrix
+    uint32_t batch, tiles_m, tiles;   // tiles: of one matrix
+    uint32_t tn;                 // pair form: columns of a tile
     uint64_t s_pitch, l_pitch;   // elements between rows of the S-wide and L-wide arrays
     float a, b, c;
     const __half* gram;          // POLY: A
@@ -114,6 +122,10 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t addr, uint32_t leading, uin
 }
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return desc_of(addr, 16, 1024); }
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) { return desc_of(addr, 64 * BK * 2, 1024); }
+// 16 k further, in the descriptor's units: 32 bytes along a K-contiguous row, 16 rows of 128 bytes else
+constexpr uint32_t STEP_K = UMMA_K * 2 / 16, STEP_MN = UMMA_K * 128 / 16;
+template <Product P>
+__device__ __forceinline__ constexpr uint32_t step_b() { return P == APPLY ? STEP_MN : STEP_K; }
 
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -154,6 +166,18 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
+// Eight f32 from or to 32 aligned bytes: a whole sector a thread, where threads hold rows of their own.
+__device__ __forceinline__ void load_sector(const void* at, uint32_t (&v)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(at) : "memory");
+}
+__device__ __forceinline__ void store_sector(void* at, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Tile t of a lower triangle counted row by row: (0,0), (1,0), (1,1), (2,0), ...
 __device__ __forceinline__ void triangle(uint32_t t, uint32_t& i, uint32_t& j) {
     i = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
@@ -175,24 +199,43 @@ __device__ __forceinline__ void tile_of(const GemmParams& p, uint32_t u, uint32_
     }
 }
 
+// The launch after this one may begin (it waits for this one's results itself), and: everything the
+// launch before wrote is there, and it reads nothing any more.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The shared::cluster address of the same shared-memory offset in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// ---- pair form ---------------------------------------------------------------------------------
 // 32 columns from column c of output row r of matrix m, in the thread that holds them.
 template <Product P>
 __device__ __forceinline__ void finish(const GemmParams& p, uint32_t m, uint32_t r, uint32_t c, bool mirror, float (&v)[32]) {
+    uint32_t w[8];
     if (P == APPLY) {
         if (r >= p.S || c >= p.L) return;
-        float4* x = reinterpret_cast<float4*>(p.x32 + ((uint64_t)m * p.S + r) * p.l_pitch + c);
+        float* x = p.x32 + ((uint64_t)m * p.S + r) * p.l_pitch + c;
 #pragma unroll
-        for (uint32_t q = 0; q < 8; ++q) {
-            const float4 o = x[q];
-            v[4 * q] += p.a * o.x;
-            v[4 * q + 1] += p.a * o.y;
-            v[4 * q + 2] += p.a * o.z;
-            v[4 * q + 3] += p.a * o.w;
+        for (uint32_t q = 0; q < 4; ++q) {
+            load_sector(x + 8 * q, w);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) v[8 * q + k] += p.a * __uint_as_float(w[k]);
         }
-        if (!p.out) {
-#pragma unroll
-            for (uint32_t q = 0; q < 8; ++q) x[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        } else {
+        if (p.out) {
             char* out = p.out + (uint64_t)m * p.out_stride;
 #pragma unroll
             for (uint32_t k = 0; k < 32; ++k) v[k] *= p.scale;
@@ -217,29 +260,35 @@ __device__ __forceinline__ void finish(const GemmParams& p, uint32_t m, uint32_t
             }
             return;
         }
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * q + k]);
+            store_sector(x + 8 * q, w);
+        }
     } else {
         if (r >= p.S || c >= p.S) return;
         if (P == POLY) {
-            const uint4* g = reinterpret_cast<const uint4*>(p.gram + ((uint64_t)m * p.S + r) * p.s_pitch + c);
+            const __half* g = p.gram + ((uint64_t)m * p.S + r) * p.s_pitch + c;
 #pragma unroll
-            for (uint32_t q = 0; q < 4; ++q) {
-                const uint4 w = g[q];
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            for (uint32_t q = 0; q < 2; ++q) {
+                load_sector(g + 16 * q, w);
 #pragma unroll
-                for (uint32_t k = 0; k < 4; ++k) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
-                    v[8 * q + 2 * k] = p.c * v[8 * q + 2 * k] + p.b * f.x;
-                    v[8 * q + 2 * k + 1] = p.c * v[8 * q + 2 * k + 1] + p.b * f.y;
+                for (uint32_t k = 0; k < 8; ++k) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                    v[16 * q + 2 * k] = p.c * v[16 * q + 2 * k] + p.b * f.x;
+                    v[16 * q + 2 * k + 1] = p.c * v[16 * q + 2 * k + 1] + p.b * f.y;
                 }
             }
         }
     }
-    const uint64_t pitch = P == APPLY ? p.l_pitch : p.s_pitch;
-    uint4* o = reinterpret_cast<uint4*>(p.out16 + ((uint64_t)m * p.S + r) * pitch + c);
+    __half* o = p.out16 + ((uint64_t)m * p.S + r) * (P == APPLY ? p.l_pitch : p.s_pitch) + c;
 #pragma unroll
-    for (uint32_t q = 0; q < 4; ++q)       // rows are padded to 64 elements: the whole chunk is the array's
-        o[q] = make_uint4(pack_f16(v[8 * q], v[8 * q + 1]), pack_f16(v[8 * q + 2], v[8 * q + 3]),
-                          pack_f16(v[8 * q + 4], v[8 * q + 5]), pack_f16(v[8 * q + 6], v[8 * q + 7]));
+    for (uint32_t q = 0; q < 2; ++q) {     // rows are padded to 64 elements: the whole chunk is the array's
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) w[k] = pack_f16(v[16 * q + 2 * k], v[16 * q + 2 * k + 1]);
+        store_sector(o + 16 * q, w);
+    }
     if (P != APPLY && mirror) {
 #pragma unroll
         for (uint32_t k = 0; k < 32; ++k)  // neighbouring lanes hold neighbouring columns of the mirrored rows
@@ -249,32 +298,69 @@ __device__ __forceinline__ void finish(const GemmParams& p, uint32_t m, uint32_t
     }
 }
 
-// Persistent: CTA q takes tiles q, q + gridDim, ... of all matrices.  Warp 4 loads 128 x 64 tiles of
-// both operands into a ring of stages (TMA, out-of-range rows and columns as zeros), one thread of warp
-// 5 issues the MMAs into one of two TMEM accumulators, and warps 0-3 drain the other.
+__device__ __forceinline__ void bar_arrive_at(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// A tile load into this CTA's shared memory that completes on the leader's mbarrier.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t cluster_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(id), "r"(accumulate) : "memory");
+}
+
+// Arrive once on the mbarrier at this offset in both CTAs when the MMAs issued so far finish.
+__device__ __forceinline__ void umma_commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"((uint16_t)0x3) : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_local2(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Clusters of two CTAs on two SMs, persistent: cluster c takes tiles c, c + clusters, ... of all
+// matrices.  A tile is 256 rows by p.tn columns (a multiple of 32, at most 256) of one
+// tcgen05.mma.cta_group::2: each CTA holds 128 of the rows and half of the columns.  Warp 4 of each
+// loads its operand halves into a ring of stages (TMA, out-of-range rows and columns as zeros), one
+// thread of the leader issues the MMAs into one of two TMEM accumulators (its mbarriers count both
+// CTAs' loads and both epilogues), and warps 0-3 of each drain the CTA's 128 rows of the other.
 template <Product P>
-__global__ void __launch_bounds__(THREADS, 1) ortho_gemm_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+ortho_pair_kernel(const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
-    uint8_t* sB = smem + STAGES * TILE_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + STAGES * TILE_STAGE);   // [STAGES]  TMA -> MMA
-    uint64_t* empty = full + STAGES;              // [STAGES]  MMA -> TMA
-    uint64_t* acc_full = empty + STAGES;          // [2]       MMA -> epilogue
-    uint64_t* acc_empty = acc_full + ACC_BUFS;    // [2]       epilogue -> MMA
-    uint64_t* drain = acc_empty + ACC_BUFS;       // [1]       MMA teardown
+    uint8_t* sB = smem + STAGES * HALF_STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + STAGES * HALF_STAGE);   // [STAGES]  leader: both CTAs' loads -> MMA
+    uint64_t* empty = full + STAGES;              // [STAGES]  each CTA: MMA -> its TMA warp
+    uint64_t* acc_full = empty + STAGES;          // [2]       each CTA: MMA -> its epilogue
+    uint64_t* acc_empty = acc_full + ACC_BUFS;    // [2]       leader: both epilogues -> MMA
+    uint64_t* drain = acc_empty + ACC_BUFS;       // [1]       leader: MMA teardown
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = cluster_rank();
+    const bool leader = q == 0;
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < STAGES; ++i) {
-            bar_init(saddr(full + i), 1);
+            bar_init(saddr(full + i), 1);            // the leader's expect_tx covers both CTAs' bytes
             bar_init(saddr(empty + i), 1);
         }
         for (uint32_t i = 0; i < ACC_BUFS; ++i) {
             bar_init(saddr(acc_full + i), 1);
-            bar_init(saddr(acc_empty + i), EPI_THREADS);
+            bar_init(saddr(acc_empty + i), 2);       // one arrival per CTA's epilogue
         }
         bar_init(saddr(drain), 1);
         *abort_flag = 0;
@@ -282,18 +368,23 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_gemm_kernel(const __grid_con
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(saddr(tmem_slot)), "r"(TMEM_COLS) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(saddr(tmem_slot)), "r"(ACC_BUFS * 256) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    __syncthreads();
+    cluster_sync_all();          // both CTAs' barriers exist before either arrives remotely
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    launch_next();
+    wait_previous();
 
     const uint32_t places = p.batch * p.tiles, kblocks = (p.K + BK - 1) / BK;
+    const uint32_t c0 = blockIdx.x / 2, NC = gridDim.x / 2;
+    const uint32_t peer_abort = at_rank(saddr(tmem_slot + 1), q ^ 1);
     auto fail = [&]() {
         *abort_flag = 1;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_abort), "r"(1u) : "memory");
         atomicAdd(p.err, 1u);
     };
 
@@ -301,88 +392,294 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_gemm_kernel(const __grid_con
         if (lane == 0) {
             uint32_t stage = 0, phase = 0, issued = 0;
             bool ok = true;
-            for (uint32_t u = blockIdx.x; u < places && ok; u += gridDim.x) {
+            for (uint32_t u = c0; u < places && ok; u += NC) {
                 uint32_t m, i, j;
                 tile_of<P>(p, u, m, i, j);
+                const int32_t row = (int32_t)(i * 256 + q * 128), col = (int32_t)(j * p.tn + q * (p.tn / 2)), z = (int32_t)m;
                 for (uint32_t kb = 0; kb < kblocks; ++kb) {
                     if (!bar_wait(saddr(empty + stage), phase ^ 1, abort_flag)) { fail(); ok = false; break; }
-                    const uint32_t bar = saddr(full + stage), k = kb * BK;
-                    const uint32_t dA = saddr(sA + stage * TILE_STAGE), dB = saddr(sB + stage * TILE_STAGE);
-                    bar_expect_tx(bar, 2 * TILE_STAGE);
-                    tma_load_3d(dA, &p.tmA, (int32_t)k, (int32_t)(i * TM), (int32_t)m, bar);
+                    // The peer's loads may land before the leader's expect_tx (the barrier's
+                    // transaction count goes below zero for a while), but never a phase early: its
+                    // stage is free only once the MMA has consumed that stage.
+                    const uint32_t bar = at_rank(saddr(full + stage), 0);
+                    const int32_t k = (int32_t)(kb * BK);
+                    const uint32_t dA = saddr(sA + stage * HALF_STAGE), dB = saddr(sB + stage * HALF_STAGE);
+                    if (leader) bar_expect_tx(saddr(full + stage), 4 * HALF_STAGE);
+                    tma_load_3d_pair(dA, &p.tmA, k, row, z, bar);
                     if (P == APPLY) {             // X: rows k, 64 columns a box
-                        tma_load_3d(dB, &p.tmB, (int32_t)(j * TN), (int32_t)k, (int32_t)m, bar);
-                        tma_load_3d(dB + TILE_STAGE / 2, &p.tmB, (int32_t)(j * TN + 64), (int32_t)k, (int32_t)m, bar);
+                        tma_load_3d_pair(dB, &p.tmB, col, k, z, bar);
+                        tma_load_3d_pair(dB + HALF_STAGE / 2, &p.tmB, col + 64, k, z, bar);
                     } else {
-                        tma_load_3d(dB, &p.tmB, (int32_t)k, (int32_t)(j * TN), (int32_t)m, bar);
+                        tma_load_3d_pair(dB, &p.tmB, k, col, z, bar);
                     }
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
             }
-            // the last loads of every stage have landed before the CTA can leave
-            volatile uint32_t never = 0;
-            for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-                (void)bar_wait(saddr(full + i % STAGES), (i / STAGES) & 1, &never);
+            // the leader's full barriers count both CTAs' loads: once its last phases complete, every
+            // load of the pair has landed
+            if (leader) {
+                volatile uint32_t never = 0;
+                for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+                    (void)bar_wait(saddr(full + i % STAGES), (i / STAGES) & 1, &never);
+            }
         }
     } else if (warp == MMA_WARP) {
-        if (lane == 0) {
+        if (lane == 0 && leader) {
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            const uint32_t id = idesc(256, p.tn) | (P == APPLY ? IDESC_B_MN : 0);
             bool ok = true;
-            for (uint32_t u = blockIdx.x; u < places && ok; u += gridDim.x) {
+            for (uint32_t u = c0; u < places && ok; u += NC) {
                 if (!bar_wait(saddr(acc_empty + acc), acc_phase ^ 1, abort_flag)) { fail(); break; }
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * TN;
+                const uint32_t d_tmem = tmem_base + acc * 256;
                 for (uint32_t kb = 0; kb < kblocks; ++kb) {
                     if (!bar_wait(saddr(full + stage), phase, abort_flag)) { fail(); ok = false; break; }
                     tc_fence_after();
-                    const uint64_t da = desc_k(saddr(sA + stage * TILE_STAGE));
-                    const uint32_t b0 = saddr(sB + stage * TILE_STAGE);
+                    const uint64_t da = desc_k(saddr(sA + stage * HALF_STAGE));
+                    const uint32_t b0 = saddr(sB + stage * HALF_STAGE);
                     const uint64_t db = P == APPLY ? desc_mn(b0) : desc_k(b0);
-                    // 16 k further: 32 bytes along a K-contiguous row, 16 rows of 128 bytes otherwise
-                    constexpr uint32_t step_b = P == APPLY ? UMMA_K * 128 / 16 : UMMA_K * 2 / 16;
 #pragma unroll
-                    for (uint32_t k = 0; k < BK / UMMA_K; ++k)
-                        umma(d_tmem, da + 2 * k, db + step_b * k, P == APPLY ? IDESC | IDESC_B_MN : IDESC, (kb | k) != 0);
-                    umma_commit(saddr(empty + stage));     // the stage is free once these finish
+                    for (uint32_t k = 0; k < BK / UMMA_K; ++k) umma_pair(d_tmem, da + STEP_K * k, db + step_b<P>() * k, id, (kb | k) != 0);
+                    umma_commit_both(saddr(empty + stage));   // both CTAs' stages are free
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
-                umma_commit(saddr(acc_full + acc));        // the tile is complete in TMEM
+                umma_commit_both(saddr(acc_full + acc));      // the tile is in both TMEMs
                 if (++acc == ACC_BUFS) { acc = 0; acc_phase ^= 1; }
             }
-            // every MMA this thread issued has finished before TMEM is released
-            umma_commit(saddr(drain));
+            // every MMA has finished before either CTA releases TMEM or shared memory
+            umma_commit_local2(saddr(drain));
             volatile uint32_t never = 0;
             (void)bar_wait(saddr(drain), 0, &never);
         }
     } else {
-        // epilogue: thread t of warp w owns row 32 w + t of every tile
+        // epilogue: thread t of warp w owns row 32 w + t of this CTA's 128
         uint32_t acc = 0, acc_phase = 0;
-        for (uint32_t u = blockIdx.x; u < places; u += gridDim.x) {
+        for (uint32_t u = c0; u < places; u += NC) {
             uint32_t m, i, j;
             tile_of<P>(p, u, m, i, j);
             const bool mine = bar_wait(saddr(acc_full + acc), acc_phase, abort_flag);
             if (!mine) fail();
             if (!epi_all(mine && !*abort_flag)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + ((warp * 32u) << 16) + acc * TN;
+            const uint32_t taddr = tmem_base + ((warp * 32u) << 16) + acc * 256;
 #pragma unroll 1
-            for (uint32_t g = 0; g < TN / 32; ++g) {
+            for (uint32_t g = 0; g < p.tn / 32; ++g) {
                 float v[32];
                 tmem_ld32(taddr + g * 32, v);
-                finish<P>(p, m, i * TM + warp * 32 + lane, j * TN + g * 32, i != j, v);
+                finish<P>(p, m, i * 256 + q * 128 + warp * 32 + lane, j * p.tn + g * 32, i != j, v);
             }
             tc_fence_before();
-            bar_arrive(saddr(acc_empty + acc));            // the accumulator may be overwritten
+            // every TMEM read of this CTA's rows precedes one arrival at the leader
+            asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+            if (threadIdx.x == 0) bar_arrive_at(at_rank(saddr(acc_empty + acc), 0));
             if (++acc == ACC_BUFS) { acc = 0; acc_phase ^= 1; }
         }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();          // no CTA leaves while the pair's MMAs or loads may touch it
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(ACC_BUFS * 256) : "memory");
+}
+
+// ---- split form --------------------------------------------------------------------------------
+__device__ __forceinline__ float4 load_peer(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// One 128 x 128 tile a cluster, its k blocks shared out over the cluster's CTAs (one, two, four or
+// eight).  Each CTA leaves its f32 sums in its shared memory; CTA q then adds rows q 128 / CTAs .. of
+// all of them, in the CTAs' order, through distributed shared memory, and stores those rows.
+template <Product P>
+__global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_constant__ GemmParams p, uint32_t ctas) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + STAGES * HALF_STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + STAGES * HALF_STAGE);   // [STAGES]  TMA -> MMA
+    uint64_t* empty = full + STAGES;              // [STAGES]  MMA -> TMA
+    uint64_t* done = empty + STAGES;              // [1]       every MMA of the tile
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < STAGES; ++i) {
+            bar_init(saddr(full + i), 1);
+            bar_init(saddr(empty + i), 1);
+        }
+        bar_init(saddr(done), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(128) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    launch_next();
+    wait_previous();
+
+    uint32_t m, i, j;
+    tile_of<P>(p, blockIdx.x / ctas, m, i, j);
+    const uint32_t kblocks = (p.K + BK - 1) / BK, k0 = kblocks * q / ctas, k1 = kblocks * (q + 1) / ctas;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicAdd(p.err, 1u);
+    };
+    if (warp == TMA_WARP) {
+        if (lane == 0) {
+            uint32_t issued = 0;
+            for (uint32_t kb = k0; kb < k1; ++kb, ++issued) {
+                const uint32_t stage = issued % STAGES;
+                if (!bar_wait(saddr(empty + stage), (issued / STAGES & 1) ^ 1, abort_flag)) { fail(); break; }
+                const uint32_t bar = saddr(full + stage);
+                const int32_t k = (int32_t)(kb * BK), row = (int32_t)(i * 128), col = (int32_t)(j * 128), z = (int32_t)m;
+                const uint32_t dA = saddr(sA + stage * HALF_STAGE), dB = saddr(sB + stage * HALF_STAGE);
+                bar_expect_tx(bar, 2 * HALF_STAGE);
+                tma_load_3d(dA, &p.tmA, k, row, z, bar);
+                if (P == APPLY) {                 // X: rows k, 64 columns a box
+                    tma_load_3d(dB, &p.tmB, col, k, z, bar);
+                    tma_load_3d(dB + HALF_STAGE / 2, &p.tmB, col + 64, k, z, bar);
+                } else {
+                    tma_load_3d(dB, &p.tmB, k, col, z, bar);
+                }
+            }
+            // the last loads of every stage have landed before the stages are used for the tile
+            volatile uint32_t never = 0;
+            for (uint32_t n = issued > STAGES ? issued - STAGES : 0; n < issued; ++n)
+                (void)bar_wait(saddr(full + n % STAGES), (n / STAGES) & 1, &never);
+        }
+    } else if (warp == MMA_WARP) {
+        if (lane == 0) {
+            for (uint32_t n = 0; n < k1 - k0; ++n) {
+                const uint32_t stage = n % STAGES;
+                if (!bar_wait(saddr(full + stage), n / STAGES & 1, abort_flag)) { fail(); break; }
+                tc_fence_after();
+                const uint64_t da = desc_k(saddr(sA + stage * HALF_STAGE));
+                const uint32_t b0 = saddr(sB + stage * HALF_STAGE);
+                const uint64_t db = P == APPLY ? desc_mn(b0) : desc_k(b0);
+                constexpr uint32_t id = idesc(128, 128) | (P == APPLY ? IDESC_B_MN : 0);
+#pragma unroll
+                for (uint32_t k = 0; k < BK / UMMA_K; ++k) umma(tmem_base, da + STEP_K * k, db + step_b<P>() * k, id, (n | k) != 0);
+                umma_commit(saddr(empty + stage));     // the stage is free once these finish
+            }
+            umma_commit(saddr(done));
+            volatile uint32_t never = 0;
+            (void)bar_wait(saddr(done), 0, &never);
+        }
+    }
+    __syncwarp();
+    __syncthreads();                              // the MMAs are done and no load is under way
+    tc_fence_after();
+    float* tile = reinterpret_cast<float*>(smem);
+    if (warp < 4) {                               // thread t of warp w: row 32 w + t
+#pragma unroll 1
+        for (uint32_t g = 0; g < 4; ++g) {
+            float v[32];
+            tmem_ld32(tmem_base + ((warp * 32u) << 16) + g * 32, v);
+            float4* to = reinterpret_cast<float4*>(tile + (warp * 32 + lane) * T_PITCH + g * 32);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+    }
+    tc_fence_before();
+    cluster_sync_all();                           // every CTA's sums are there
+    tc_fence_after();
     if (warp == 0)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(128) : "memory");
+
+    // a warp a row, four columns a lane
+    const uint32_t rows = 128 / ctas, first = q * rows, cols = P == APPLY ? p.L : p.S;
+    const uint64_t pitch = P == APPLY ? p.l_pitch : p.s_pitch;
+    const uint32_t c = j * 128 + 4 * lane;
+    const bool turned = P == APPLY ? p.out && p.transposed : i != j;   // the rows are stored as columns (too)
+    uint16_t* turn = reinterpret_cast<uint16_t*>(smem + T16_OFFSET);
+    for (uint32_t n = warp; n < rows; n += THREADS / 32) {
+        const uint32_t r = i * 128 + first + n;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const uint32_t at = saddr(tile + (first + n) * T_PITCH + 4 * lane);
+        for (uint32_t o = 0; o < ctas; ++o) {
+            const float4 w = load_peer(at_rank(at, o));
+            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+        }
+        const bool in = r < p.S && c < cols;      // rows are padded to 64 elements: then all four are the array's
+        const uint64_t to = ((uint64_t)m * p.S + r) * pitch + c;
+        if (P == POLY && in) {
+            const uint2 g = *reinterpret_cast<const uint2*>(p.gram + to);
+            const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&g.x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&g.y));
+            v = make_float4(p.c * v.x + p.b * lo.x, p.c * v.y + p.b * lo.y, p.c * v.z + p.b * hi.x, p.c * v.w + p.b * hi.y);
+        }
+        if (P == APPLY && in) {
+            float4* x = reinterpret_cast<float4*>(p.x32 + to);
+            const float4 w = *x;
+            v = make_float4(v.x + p.a * w.x, v.y + p.a * w.y, v.z + p.a * w.z, v.w + p.a * w.w);
+            if (!p.out) *x = v;
+        }
+        uint32_t lo, hi;
+        if (P == APPLY && p.out) {
+            lo = pack_bf16(v.x * p.scale, v.y * p.scale);
+            hi = pack_bf16(v.z * p.scale, v.w * p.scale);
+        } else {
+            lo = pack_f16(v.x, v.y);
+            hi = pack_f16(v.z, v.w);
+        }
+        if (turned) {
+            uint32_t* row = reinterpret_cast<uint32_t*>(turn + n * T16_PITCH + 4 * lane);
+            row[0] = in ? lo : 0;
+            row[1] = in ? hi : 0;
+        }
+        if (!in || (P == APPLY && p.out && p.transposed)) continue;
+        if (P == APPLY && p.out) {
+            char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)r * p.out_pitch + (uint64_t)c * 2;
+            if (p.out_vec && c + 4 <= p.L) {
+                *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+            } else {
+                const uint32_t e[4] = {lo & 0xFFFF, lo >> 16, hi & 0xFFFF, hi >> 16};
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k)
+                    if (c + k < p.L) reinterpret_cast<uint16_t*>(out)[k] = (uint16_t)e[k];
+            }
+        } else {
+            *reinterpret_cast<uint2*>(p.out16 + to) = make_uint2(lo, hi);
+        }
+    }
+    __syncthreads();
+    // a thread a column of the tile: `rows` neighbouring elements of row j 128 + t of the result
+    const uint32_t tc = j * 128 + threadIdx.x;
+    if (turned && threadIdx.x < 128 && tc < cols) {
+        for (uint32_t n = 0; n < rows; n += 8) {
+            const uint32_t r = i * 128 + first + n;
+            if (r >= p.S) break;
+            uint32_t e[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) e[k] = turn[(n + k) * T16_PITCH + threadIdx.x];
+            const uint4 w = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+            if (P != APPLY) {
+                *reinterpret_cast<uint4*>(p.out16 + ((uint64_t)m * p.S + tc) * p.s_pitch + r) = w;
+            } else {
+                char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)tc * p.out_pitch + (uint64_t)r * 2;
+                if (p.out_vec && r + 8 <= p.S) {
+                    *reinterpret_cast<uint4*>(out) = w;
+                } else {
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k)
+                        if (r + k < p.S) reinterpret_cast<uint16_t*>(out)[k] = (uint16_t)e[k];
+                }
+            }
+        }
+    }
+    cluster_sync_all();                           // no CTA leaves while its sums may be read
 }
 
 struct UpdateParams {
@@ -423,6 +720,7 @@ __global__ void __launch_bounds__(256) ortho_update_kernel(const __grid_constant
     char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
     const uint64_t total = (uint64_t)p.rows * per_row;
     float sum = 0.0f;
+    launch_next();
 #pragma unroll 4
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (uint64_t)p.parts * 256) {
         const uint32_t r = (uint32_t)(i / per_row), c = (uint32_t)(i - (uint64_t)r * per_row) * W;
@@ -451,6 +749,8 @@ __global__ void __launch_bounds__(256) ortho_update_kernel(const __grid_constant
 // 1 / (|u| + eps) of matrix m, from its parts; 0 where that overflows (u is then 0 in f16 as well).
 __device__ __forceinline__ float inverse_norm(const UpdateParams& p, uint32_t m, float (&slot)[8]) {
     float sum = 0.0f;
+    launch_next();
+    wait_previous();
 #pragma unroll 4
     for (uint32_t i = threadIdx.x; i < p.parts; i += 256) sum += p.sums[(uint64_t)m * p.parts + i];
     const float inv = 1.0f / (sqrtf(cta_sum(sum, slot)) + p.eps);
@@ -503,6 +803,7 @@ __global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_con
     const char* x = p.x + (uint64_t)m * p.x_stride;
     const char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
     float u[kStartTile / 8][2];
+    wait_previous();
 #pragma unroll
     for (uint32_t k = 0; k < kStartTile / 8; ++k)
 #pragma unroll
@@ -590,8 +891,8 @@ int check_desc(const char* who, const dtt_ortho_desc* d) {
     if (d->rows == 0 || d->cols == 0 || d->rows > 65536 || d->cols > 65536)
         return fail(DTT_EINVAL, "%s: rows and cols must be 1 .. 65536", who);
     if (d->batch == 0 || d->batch > 65535) return fail(DTT_EINVAL, "%s: batch must be 1 .. 65535", who);
-    if (((d->rows + TM - 1) / TM) * ((d->cols + TN - 1) / TN) * d->batch >= (1ull << 31))
-        return fail(DTT_EINVAL, "%s: 2^31 tiles of 128 x 128 or more", who);
+    if (((d->rows + 127) / 128) * ((d->cols + 127) / 128) * d->batch >= (1ull << 28))
+        return fail(DTT_EINVAL, "%s: 2^28 tiles of 128 x 128 or more", who);
     if (d->steps == 0 || d->steps > DTT_ORTHO_MAX_STEPS)
         return fail(DTT_EINVAL, "%s: steps must be 1 .. %d", who, DTT_ORTHO_MAX_STEPS);
     if (d->momentum > 1 || d->nesterov > 1 || (d->nesterov && !d->momentum))
@@ -617,20 +918,136 @@ int check_desc(const char* who, const dtt_ortho_desc* d) {
     return DTT_OK;
 }
 
+// Launched so that the next kernel's set-up overlaps this one's end (every kernel waits for the one before
+// it before it touches memory).  cluster: CTAs of a cluster, 0 where the kernel itself says.
+template <class... Params, class... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, cudaStream_t stream,
+                   const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// Clusters that can be resident at once: pairs, and splits of 1, 2, 4 and 8 CTAs.
+struct Fit {
+    uint32_t pairs, splits[4];
+};
+
+template <class... Params>
+uint32_t clusters_of(void (*kernel)(Params...), uint32_t ctas) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+    }
+    return (uint32_t)std::max(n, 1);
+}
+
+// A property of the device: asked once per device.
+Fit fit_of(int device, uint32_t sms) {
+    static std::mutex mu;
+    static Fit known[64];
+    std::lock_guard<std::mutex> lock(mu);
+    Fit local{};
+    Fit& f = device < 64 ? known[device] : local;
+    if (!f.pairs) {
+        f.pairs = clusters_of(ortho_pair_kernel<APPLY>, 2);
+        f.splits[0] = sms;
+        for (uint32_t n = 1; n < 4; ++n) f.splits[n] = clusters_of(ortho_split_kernel<APPLY>, 1u << n);
+    }
+    return f;
+}
+
+// How one product runs: by CTA pairs on tiles of 256 x tn, or split over clusters on tiles of 128 x 128.
+struct Form {
+    bool pair;
+    uint32_t tn, ctas;           // pair: columns of a tile; split: CTAs of a cluster
+};
+
+uint32_t ceil_div(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); }
+
+uint32_t tiles_of(bool square, uint32_t tile_m, uint32_t tile_n, uint64_t rows, uint64_t cols) {
+    const uint32_t tm = ceil_div(rows, tile_m);
+    return square ? tm * (tm + 1) / 2 : tm * ceil_div(cols, tile_n);
+}
+
+// The form whose estimated time is least.  A k block of 64 costs a pair 0.34 us at 256 columns (0.30 +
+// 0.04 tn / 256 where loads bound it) and a split CTA 0.27 us; a round of tiles costs a pair 2 us and
+// a split CTA 4 us besides, 1 us more where a cluster adds up its sums.
+Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t batch, const Fit& fit) {
+    const uint32_t kblocks = ceil_div(K, BK);
+    Form best{};
+    double least = 1e30;
+    for (uint32_t tn = 256; tn >= 128; tn -= 32) {
+        if (square && tn != 256) break;
+        const double rounds = ceil_div((uint64_t)tiles_of(square, 256, tn, rows, cols) * batch, fit.pairs);
+        const double t = rounds * (2.0 + kblocks * (0.08 + 0.26 * tn / 256));
+        if (t < least) {
+            least = t;
+            best = {true, tn, 0};
+        }
+    }
+    for (uint32_t n = 0; n < 4 && (1u << n) <= kblocks; ++n) {
+        const uint32_t ctas = 1u << n;
+        const double rounds = ceil_div((uint64_t)tiles_of(square, 128, 128, rows, cols) * batch, fit.splits[n]);
+        const double t = rounds * (4.0 + (ctas > 1) + 0.27 * ceil_div(kblocks, ctas));
+        if (t < least) {
+            least = t;
+            best = {false, 128, ctas};
+        }
+    }
+    return best;
+}
+
 template <Product P>
-cudaError_t prepare_gemm() {
-    cudaError_t e = prepare_kernel(ortho_gemm_kernel<P>);
+cudaError_t launch_product(GemmParams& p, const Form& f, uint32_t pairs, cudaStream_t stream) {
+    const uint32_t tile_m = f.pair ? 256 : 128;
+    p.tn = f.tn;
+    p.tiles_m = ceil_div(p.S, tile_m);
+    p.tiles = tiles_of(P != APPLY, tile_m, f.tn, p.S, p.L);
+    const uint32_t places = p.tiles * p.batch;
+    if (f.pair) return launch(ortho_pair_kernel<P>, 2 * std::min(places, pairs), THREADS, SMEM_BYTES, 0, stream, p);
+    return launch(ortho_split_kernel<P>, places * f.ctas, THREADS, SMEM_BYTES, f.ctas, stream, p, f.ctas);
+}
+
+template <Product P>
+cudaError_t prepare_product() {
+    cudaError_t e = prepare_kernel(ortho_pair_kernel<P>);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(ortho_gemm_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+        e = cudaFuncSetAttribute(ortho_pair_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e == cudaSuccess) e = prepare_kernel(ortho_split_kernel<P>);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ortho_split_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     return e;
 }
 
 }  // namespace
 
 cudaError_t preload_ortho_kernels() {
-    cudaError_t e = prepare_gemm<GRAM>();
-    if (e == cudaSuccess) e = prepare_gemm<POLY>();
-    if (e == cudaSuccess) e = prepare_gemm<APPLY>();
+    cudaError_t e = prepare_product<GRAM>();
+    if (e == cudaSuccess) e = prepare_product<POLY>();
+    if (e == cudaSuccess) e = prepare_product<APPLY>();
     if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<true>);
     if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<false>);
     if (e == cudaSuccess) e = prepare_kernel(ortho_start_kernel);
@@ -651,6 +1068,8 @@ struct dtt_ortho {
     CUtensorMap x_rows[2];       // x16, K-major operand of A = X X^T: boxes of 64 x 128
     CUtensorMap x_cols[2];       // x16, N-contiguous operand of the last product: boxes of 64 x 64
     CUtensorMap gram, poly;      // boxes of 64 x 128
+    Fit fit;
+    Form form[3];                // of each Product
 };
 
 extern "C" int dtt_ortho_workspace(const dtt_ortho_desc* d, uint64_t* bytes) {
@@ -681,10 +1100,15 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     o->l = l;
     o->ws = static_cast<char*>(workspace);
     o->sms = (uint32_t)sms;
-    bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, TM) &&
-              make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, TM);
+    o->fit = fit_of(dev, o->sms);
+    o->form[GRAM] = form_of(true, l.S, l.S, l.L, d->batch, o->fit);
+    o->form[POLY] = form_of(true, l.S, l.S, l.S, d->batch, o->fit);
+    o->form[APPLY] = form_of(false, l.S, l.L, l.S, d->batch, o->fit);
+    if (getenv("DBG")) { printf("fit %u %u %u %u %u\n", o->fit.pairs, o->fit.splits[0], o->fit.splits[1], o->fit.splits[2], o->fit.splits[3]); for (auto& f : o->form) printf("  form pair %d tn %u ctas %u\n", f.pair, f.tn, f.ctas); }
+    bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 128) &&
+              make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128);
     for (int i = 0; i < 2 && ok; ++i)
-        ok = make_map(&o->x_rows[i], o->ws + l.x16[i], l.L, l.S, d->batch, l.l_pitch, TM) &&
+        ok = make_map(&o->x_rows[i], o->ws + l.x16[i], l.L, l.S, d->batch, l.l_pitch, 128) &&
              make_map(&o->x_cols[i], o->ws + l.x16[i], l.L, l.S, d->batch, l.l_pitch, BK);
     if (!ok) {
         delete o;
@@ -744,15 +1168,17 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         if (a.p != out && a.p) vec = vec && reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.pitch % 16 == 0 && a.stride % 16 == 0;
     const uint64_t items = d.rows * (vec ? d.cols / 8 : d.cols);
     up.parts = (uint32_t)std::min<uint64_t>((items + 1023) / 1024, std::max(kMaxParts / d.batch, 1u));
-    if (vec) ortho_update_kernel<true><<<dim3(up.parts, d.batch), 256, 0, stream>>>(up);
-    else ortho_update_kernel<false><<<dim3(up.parts, d.batch), 256, 0, stream>>>(up);
+    const dim3 parts(up.parts, d.batch);
+    // not overlapped with what ran before: it may write the update that this reads
+    if (vec) ortho_update_kernel<true><<<parts, 256, 0, stream>>>(up);
+    else ortho_update_kernel<false><<<parts, 256, 0, stream>>>(up);
+    DTT_CUDA_TRY(cudaGetLastError());
     if (vec && !tall) {
         const uint32_t ctas = (uint32_t)std::min<uint64_t>((items + 511) / 512, std::max(8 * o->sms / d.batch, 1u));
-        ortho_start_kernel<<<dim3(ctas, d.batch), 256, 0, stream>>>(up);
+        DTT_CUDA_TRY(launch(ortho_start_kernel, dim3(ctas, d.batch), 256, 0, 0, stream, up));
     } else {
-        const dim3 tiles((up.cols + kStartTile - 1) / kStartTile, (up.rows + kStartTile - 1) / kStartTile, d.batch);
-        if (tall) ortho_start_tiles_kernel<true><<<tiles, 256, 0, stream>>>(up);
-        else ortho_start_tiles_kernel<false><<<tiles, 256, 0, stream>>>(up);
+        const dim3 tiles(ceil_div(up.cols, kStartTile), ceil_div(up.rows, kStartTile), d.batch);
+        DTT_CUDA_TRY(launch(tall ? ortho_start_tiles_kernel<true> : ortho_start_tiles_kernel<false>, tiles, 256, 0, 0, stream, up));
     }
 
     GemmParams g{};
@@ -767,36 +1193,27 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_pitch % 16 == 0 && (d.batch == 1 || out_stride % 16 == 0);
     g.out_pitch = out_pitch;
     g.out_stride = out_stride;
-    g.tiles_m = (uint32_t)((l.S + TM - 1) / TM);
-    const uint32_t triangle_tiles = g.tiles_m * (g.tiles_m + 1) / 2;
-    auto grid = [&](uint64_t tiles) { return (uint32_t)std::min<uint64_t>(tiles * d.batch, o->sms); };
     for (uint32_t k = 0; k < d.steps; ++k) {
         const uint32_t now = k & 1;
         g.a = d.coeffs[k][0];
         g.b = d.coeffs[k][1];
         g.c = d.coeffs[k][2];
         g.L = g.S;
-        g.tiles_n = g.tiles_m;
-        g.tiles = triangle_tiles;
         g.tmA = g.tmB = o->x_rows[now];
         g.K = (uint32_t)l.L;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.gram);
-        ortho_gemm_kernel<GRAM><<<grid(g.tiles), THREADS, SMEM_BYTES, stream>>>(g);
+        DTT_CUDA_TRY(launch_product<GRAM>(g, o->form[GRAM], o->fit.pairs, stream));
         g.tmA = g.tmB = o->gram;
         g.K = g.S;
         g.gram = g.out16;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.poly);
-        ortho_gemm_kernel<POLY><<<grid(g.tiles), THREADS, SMEM_BYTES, stream>>>(g);
+        DTT_CUDA_TRY(launch_product<POLY>(g, o->form[POLY], o->fit.pairs, stream));
         g.tmA = o->poly;
         g.tmB = o->x_cols[now];
         g.L = (uint32_t)l.L;
-        g.tiles_n = (uint32_t)((l.L + TN - 1) / TN);
-        g.tiles = g.tiles_m * g.tiles_n;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.x16[now ^ 1]);
         g.out = k + 1 == d.steps ? static_cast<char*>(out) : nullptr;
-        ortho_gemm_kernel<APPLY><<<grid(g.tiles), THREADS, SMEM_BYTES, stream>>>(g);
+        DTT_CUDA_TRY(launch_product<APPLY>(g, o->form[APPLY], o->fit.pairs, stream));
     }
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }
