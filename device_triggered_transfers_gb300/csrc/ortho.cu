@@ -31,11 +31,12 @@ constexpr uint32_t BK = 64, UMMA_K = 16;
 constexpr uint32_t HALF_STAGE = 128 * BK * 2;        // 16 KiB: 128 rows or columns of an operand
 constexpr uint32_t STAGES = 6;
 constexpr uint32_t ACC_BUFS = 2;                     // TMEM accumulators of the pair form
-constexpr uint32_t EPI_THREADS = 128;
-constexpr uint32_t THREADS = EPI_THREADS + 64;       // + TMA warp + MMA warp
-constexpr uint32_t TMA_WARP = 4, MMA_WARP = 5;
+constexpr uint32_t EPI_WARPS = 8;                    // two for each 32 lanes of TMEM: half of the columns each
+constexpr uint32_t THREADS = EPI_WARPS * 32 + 64;    // + TMA warp + MMA warp
+constexpr uint32_t TMA_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
+constexpr uint32_t TURN_BYTES = 32 * 32 * 4;         // pair form: 32 x 32 sums of an epilogue warp
 constexpr uint32_t WAIT_LIMIT = 1u << 22;
-constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + 256;
+constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + EPI_WARPS * TURN_BYTES + 256;
 // instruction descriptor (kind::f16): f32 accumulator, f16 operands, M = m, N = n
 __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 constexpr uint32_t IDESC_B_MN = 1u << 16;            // B stored with N contiguous
@@ -88,7 +89,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return false;
 }
 
-// AND of v over the epilogue's threads (named barrier 1), the same result in each.
+// AND of v over the epilogue's warps (named barrier 1), the same result in each thread.
 __device__ __forceinline__ bool epi_all(bool v) {
     uint32_t r;
     asm volatile(
@@ -96,7 +97,7 @@ __device__ __forceinline__ bool epi_all(bool v) {
         "setp.ne.u32 p, %1, 0;\n\t"
         "bar.red.and.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)v), "n"(EPI_THREADS) : "memory");
+        : "=r"(r) : "r"((uint32_t)v), "n"(EPI_WARPS * 32) : "memory");
     return r != 0;
 }
 
@@ -222,79 +223,96 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 
 // ---- pair form ---------------------------------------------------------------------------------
-// 32 columns from column c of output row r of matrix m, in the thread that holds them.
+// GRAM, POLY: 32 columns from column c of output row r of matrix m, in the thread that holds them.
 template <Product P>
 __device__ __forceinline__ void finish(const GemmParams& p, uint32_t m, uint32_t r, uint32_t c, bool mirror, float (&v)[32]) {
+    if (r >= p.S || c >= p.S) return;
     uint32_t w[8];
-    if (P == APPLY) {
-        if (r >= p.S || c >= p.L) return;
-        float* x = p.x32 + ((uint64_t)m * p.S + r) * p.l_pitch + c;
+    if (P == POLY) {
+        const __half* g = p.gram + ((uint64_t)m * p.S + r) * p.s_pitch + c;
 #pragma unroll
-        for (uint32_t q = 0; q < 4; ++q) {
-            load_sector(x + 8 * q, w);
+        for (uint32_t q = 0; q < 2; ++q) {
+            load_sector(g + 16 * q, w);
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) v[8 * q + k] += p.a * __uint_as_float(w[k]);
-        }
-        if (p.out) {
-            char* out = p.out + (uint64_t)m * p.out_stride;
-#pragma unroll
-            for (uint32_t k = 0; k < 32; ++k) v[k] *= p.scale;
-            if (p.transposed) {
-#pragma unroll
-                for (uint32_t k = 0; k < 32; ++k)       // neighbouring lanes hold neighbouring columns of `out`
-                    if (c + k < p.L)
-                        *reinterpret_cast<uint16_t*>(out + (uint64_t)(c + k) * p.out_pitch + (uint64_t)r * 2) =
-                            (uint16_t)pack_bf16(v[k], 0.0f);
-            } else if (p.out_vec && c + 32 <= p.L) {
-                uint4* o = reinterpret_cast<uint4*>(out + (uint64_t)r * p.out_pitch + (uint64_t)c * 2);
-#pragma unroll
-                for (uint32_t q = 0; q < 4; ++q)
-                    o[q] = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                                      pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
-            } else {
-#pragma unroll
-                for (uint32_t k = 0; k < 32; ++k)
-                    if (c + k < p.L)
-                        *reinterpret_cast<uint16_t*>(out + (uint64_t)r * p.out_pitch + (uint64_t)(c + k) * 2) =
-                            (uint16_t)pack_bf16(v[k], 0.0f);
-            }
-            return;
-        }
-#pragma unroll
-        for (uint32_t q = 0; q < 4; ++q) {
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * q + k]);
-            store_sector(x + 8 * q, w);
-        }
-    } else {
-        if (r >= p.S || c >= p.S) return;
-        if (P == POLY) {
-            const __half* g = p.gram + ((uint64_t)m * p.S + r) * p.s_pitch + c;
-#pragma unroll
-            for (uint32_t q = 0; q < 2; ++q) {
-                load_sector(g + 16 * q, w);
-#pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                    v[16 * q + 2 * k] = p.c * v[16 * q + 2 * k] + p.b * f.x;
-                    v[16 * q + 2 * k + 1] = p.c * v[16 * q + 2 * k + 1] + p.b * f.y;
-                }
+            for (uint32_t k = 0; k < 8; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                v[16 * q + 2 * k] = p.c * v[16 * q + 2 * k] + p.b * f.x;
+                v[16 * q + 2 * k + 1] = p.c * v[16 * q + 2 * k + 1] + p.b * f.y;
             }
         }
     }
-    __half* o = p.out16 + ((uint64_t)m * p.S + r) * (P == APPLY ? p.l_pitch : p.s_pitch) + c;
+    __half* o = p.out16 + ((uint64_t)m * p.S + r) * p.s_pitch + c;
 #pragma unroll
     for (uint32_t q = 0; q < 2; ++q) {     // rows are padded to 64 elements: the whole chunk is the array's
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) w[k] = pack_f16(v[16 * q + 2 * k], v[16 * q + 2 * k + 1]);
         store_sector(o + 16 * q, w);
     }
-    if (P != APPLY && mirror) {
+    if (mirror) {
 #pragma unroll
         for (uint32_t k = 0; k < 32; ++k)  // neighbouring lanes hold neighbouring columns of the mirrored rows
             if (c + k < p.S)
                 *reinterpret_cast<uint16_t*>(p.out16 + ((uint64_t)m * p.S + c + k) * p.s_pitch + r) =
                     (uint16_t)pack_f16(v[k], 0.0f);
+    }
+}
+
+// APPLY: the 32 x 32 sums at TMEM address taddr are output rows r0 .., columns c0 .. of matrix m.  A
+// lane holds a row of them; through the warp's part of shared memory (`turn`, 16-byte words swizzled
+// by the row) they become four columns of a row in each of eight lanes, so that the iterate is read
+// and written in whole lines.  A row a lane would take 3.6 times the shared-memory cycles, which the
+// MMAs' operand reads need.
+__device__ __forceinline__ void apply_block(const GemmParams& p, uint32_t m, uint32_t r0, uint32_t c0, uint32_t taddr, float4* turn) {
+    const uint32_t lane = threadIdx.x % 32, sub = lane / 8, c = c0 + 4 * (lane % 8);
+    const uint64_t base = ((uint64_t)m * p.S + r0 + sub) * p.l_pitch + c;
+    const bool in = c < p.L;               // rows are padded to 64 elements: then all four are the array's
+    float4 x[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+        if (in && r0 + 4 * k + sub < p.S) x[k] = *reinterpret_cast<const float4*>(p.x32 + base + 4 * k * p.l_pitch);
+    float v[32];
+    tmem_ld32(taddr, v);
+    __syncwarp();                          // the last block's words have been read
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+        turn[lane * 8 + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    __syncwarp();
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        const uint32_t n = 4 * k + sub, r = r0 + n;
+        float4& word = turn[n * 8 + ((lane % 8) ^ (n & 7))];
+        float4 w = word;
+        w = make_float4(w.x + p.a * x[k].x, w.y + p.a * x[k].y, w.z + p.a * x[k].z, w.w + p.a * x[k].w);
+        if (p.out && p.transposed) word = w;
+        if (!in || r >= p.S) continue;
+        if (!p.out) {
+            *reinterpret_cast<float4*>(p.x32 + base + 4 * k * p.l_pitch) = w;
+            *reinterpret_cast<uint2*>(p.out16 + base + 4 * k * p.l_pitch) = make_uint2(pack_f16(w.x, w.y), pack_f16(w.z, w.w));
+        } else if (!p.transposed) {
+            const uint32_t lo = pack_bf16(w.x * p.scale, w.y * p.scale), hi = pack_bf16(w.z * p.scale, w.w * p.scale);
+            char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)r * p.out_pitch + (uint64_t)c * 2;
+            if (p.out_vec && c + 4 <= p.L) {
+                *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+            } else {
+                const uint32_t e[4] = {lo & 0xFFFF, lo >> 16, hi & 0xFFFF, hi >> 16};
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i)
+                    if (c + i < p.L) reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)e[i];
+            }
+        }
+    }
+    if (p.out && p.transposed) {
+        __syncwarp();
+        char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)(r0 + lane) * 2;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            const float4 w = turn[lane * 8 + (k ^ (lane & 7))];
+            const float e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)       // neighbouring lanes hold neighbouring columns of `out`
+                if (r0 + lane < p.S && c0 + 4 * k + i < p.L)
+                    *reinterpret_cast<uint16_t*>(out + (uint64_t)(c0 + 4 * k + i) * p.out_pitch) = (uint16_t)pack_bf16(e[i] * p.scale, 0.0f);
+        }
     }
 }
 
@@ -332,10 +350,10 @@ __device__ __forceinline__ void umma_commit_local2(uint32_t bar) {
 
 // Clusters of two CTAs on two SMs, persistent: cluster c takes tiles c, c + clusters, ... of all
 // matrices.  A tile is 256 rows by p.tn columns (a multiple of 32, at most 256) of one
-// tcgen05.mma.cta_group::2: each CTA holds 128 of the rows and half of the columns.  Warp 4 of each
+// tcgen05.mma.cta_group::2: each CTA holds 128 of the rows and half of the columns.  Warp 8 of each
 // loads its operand halves into a ring of stages (TMA, out-of-range rows and columns as zeros), one
 // thread of the leader issues the MMAs into one of two TMEM accumulators (its mbarriers count both
-// CTAs' loads and both epilogues), and warps 0-3 of each drain the CTA's 128 rows of the other.
+// CTAs' loads and both epilogues), and warps 0-7 of each drain the CTA's 128 rows of the other.
 template <Product P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 ortho_pair_kernel(const __grid_constant__ GemmParams p) {
@@ -343,7 +361,8 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + STAGES * HALF_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + STAGES * HALF_STAGE);   // [STAGES]  leader: both CTAs' loads -> MMA
+    float4* turns = reinterpret_cast<float4*>(sB + STAGES * HALF_STAGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + STAGES * HALF_STAGE + EPI_WARPS * TURN_BYTES);   // [STAGES]  leader: both CTAs' loads -> MMA
     uint64_t* empty = full + STAGES;              // [STAGES]  each CTA: MMA -> its TMA warp
     uint64_t* acc_full = empty + STAGES;          // [2]       each CTA: MMA -> its epilogue
     uint64_t* acc_empty = acc_full + ACC_BUFS;    // [2]       leader: both epilogues -> MMA
@@ -454,8 +473,9 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
             (void)bar_wait(saddr(drain), 0, &never);
         }
     } else {
-        // epilogue: thread t of warp w owns row 32 w + t of this CTA's 128
+        // epilogue: warps w and w + 4 own rows 32 w .. of this CTA's 128 and every other block of 32 columns
         uint32_t acc = 0, acc_phase = 0;
+        const uint32_t rows = 32 * (warp % 4);
         for (uint32_t u = c0; u < places; u += NC) {
             uint32_t m, i, j;
             tile_of<P>(p, u, m, i, j);
@@ -463,16 +483,20 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
             if (!mine) fail();
             if (!epi_all(mine && !*abort_flag)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + ((warp * 32u) << 16) + acc * 256;
+            const uint32_t taddr = tmem_base + (rows << 16) + acc * 256, r0 = i * 256 + q * 128 + rows;
 #pragma unroll 1
-            for (uint32_t g = 0; g < p.tn / 32; ++g) {
-                float v[32];
-                tmem_ld32(taddr + g * 32, v);
-                finish<P>(p, m, i * 256 + q * 128 + warp * 32 + lane, j * p.tn + g * 32, i != j, v);
+            for (uint32_t g = warp / 4; g < p.tn / 32; g += EPI_WARPS / 4) {
+                if (P == APPLY) {
+                    apply_block(p, m, r0, j * p.tn + g * 32, taddr + g * 32, turns + warp * (TURN_BYTES / 16));
+                } else {
+                    float v[32];
+                    tmem_ld32(taddr + g * 32, v);
+                    finish<P>(p, m, r0 + lane, j * p.tn + g * 32, i != j, v);
+                }
             }
             tc_fence_before();
             // every TMEM read of this CTA's rows precedes one arrival at the leader
-            asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
             if (threadIdx.x == 0) bar_arrive_at(at_rank(saddr(acc_empty + acc), 0));
             if (++acc == ACC_BUFS) { acc = 0; acc_phase ^= 1; }
         }
@@ -583,12 +607,13 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
     __syncthreads();                              // the MMAs are done and no load is under way
     tc_fence_after();
     float* tile = reinterpret_cast<float*>(smem);
-    if (warp < 4) {                               // thread t of warp w: row 32 w + t
+    if (warp < EPI_WARPS) {                       // a lane a row, 64 columns a warp
+        const uint32_t row = 32 * (warp % 4);
 #pragma unroll 1
-        for (uint32_t g = 0; g < 4; ++g) {
+        for (uint32_t g = warp / 4 * 2; g < warp / 4 * 2 + 2; ++g) {
             float v[32];
-            tmem_ld32(tmem_base + ((warp * 32u) << 16) + g * 32, v);
-            float4* to = reinterpret_cast<float4*>(tile + (warp * 32 + lane) * T_PITCH + g * 32);
+            tmem_ld32(tmem_base + (row << 16) + g * 32, v);
+            float4* to = reinterpret_cast<float4*>(tile + (row + lane) * T_PITCH + g * 32);
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         }
