@@ -1,12 +1,13 @@
 // Orthogonalising an update by Newton-Schulz products (dtt_ops.h): X <- a X + (b A + c A A) X with
 // A = X X^T, a few times over, for a batch of S x L matrices (S <= L: the smaller side first).
 //
-// Precision.  The tensor cores take f16 operands and add in f32.  X is held in f32 (x32) and only
-// its operand copy (x16) is rounded: f16 has 11 significant bits where bf16 has 8, at the same
-// rate, and every value here is below 3 in magnitude.  Rounding X itself would put noise of 2^-12 |X|
-// into the singular directions that the update lacks, where a step multiplies it by a = 3.44: for a
-// rank-1 update five steps in f16 end 10 % off, in bf16 75 %, with X in f32 0.2 % (the bf16 output).
-// Rounded operands meet their noise only through b A + c A A, whose range holds nothing of it.
+// Precision.  The tensor cores take f16 operands and add in f32: f16 has 11 significant bits where
+// bf16 has 8, at the same rate, and every value here is below 3 in magnitude.  X is held in 32 bits,
+// as its f16 operand (hi) and the rest of it times 2^11 in f16 (lo): 22 significant bits, and nothing
+// below 2^-35 is lost.  An X of one f16 would carry noise of 2^-12 |X| in the singular directions that
+// the update lacks, where a step multiplies it by a = 3.44: for a rank-1 update five steps in f16 end
+// 10 % off, in bf16 75 %, with 32 bits 0.2 % (the bf16 output).  The noise of rounded operands meets X
+// only through b A + c A A, whose range holds nothing of those directions.
 //
 // A and b A + c A A are symmetric: only tiles on and below the diagonal are computed, and each is
 // stored twice, once transposed.
@@ -29,14 +30,16 @@ namespace {
 
 constexpr uint32_t BK = 64, UMMA_K = 16;
 constexpr uint32_t HALF_STAGE = 128 * BK * 2;        // 16 KiB: 128 rows or columns of an operand
-constexpr uint32_t STAGES = 6;
+constexpr uint32_t STAGES = 5;
 constexpr uint32_t ACC_BUFS = 2;                     // TMEM accumulators of the pair form
 constexpr uint32_t EPI_WARPS = 8;                    // two for each 32 lanes of TMEM: half of the columns each
-constexpr uint32_t THREADS = EPI_WARPS * 32 + 64;    // + TMA warp + MMA warp
-constexpr uint32_t TMA_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
-constexpr uint32_t TURN_BYTES = 32 * 32 * 4;         // pair form: 32 x 32 sums of an epilogue warp
+constexpr uint32_t THREADS = EPI_WARPS * 32 + 96;    // + TMA warp, MMA warp, slab warp
+constexpr uint32_t TMA_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1, SLAB_WARP = EPI_WARPS + 2;
+constexpr uint32_t SLAB = 64;                        // pair form: columns that its epilogue takes at a time
+constexpr uint32_t SLAB_BYTES = 128 * SLAB * 2;      // of one f16 array: 16 KiB
+constexpr uint32_t SLAB_BUFS = 2;
 constexpr uint32_t WAIT_LIMIT = 1u << 22;
-constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + EPI_WARPS * TURN_BYTES + 256;
+constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + SLAB_BUFS * 2 * SLAB_BYTES + 256;
 // instruction descriptor (kind::f16): f32 accumulator, f16 operands, M = m, N = n
 __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 constexpr uint32_t IDESC_B_MN = 1u << 16;            // B stored with N contiguous
@@ -52,15 +55,18 @@ constexpr uint32_t kMaxParts = 1216;                 // ortho_update_kernel: CTA
 enum Product { GRAM, POLY, APPLY };
 
 struct GemmParams {
-    CUtensorMap tmA, tmB;
+    CUtensorMap tmA, tmB;        // operands
+    CUtensorMap in0, in1;        // pair form, what the epilogue reads: POLY: A; APPLY: hi and lo
+    CUtensorMap out0, out1;      // and writes: the matrix and, in boxes of 64 x 64, its mirrored part; APPLY: the next hi, and lo
     uint32_t S, L, K;            // output rows S and columns (GRAM, POLY: S; APPLY: L)
     uint32_t batch, tiles_m, tiles;   // tiles: of one matrix
-    uint32_t tn;                 // pair form: columns of a tile
+    uint32_t tn;                 // pair form: columns of a tile, 256 or 128
     uint64_t s_pitch, l_pitch;   // elements between rows of the S-wide and L-wide arrays
     float a, b, c;
     const __half* gram;          // POLY: A
-    __half* out16;               // GRAM: A; POLY: b A + c A A; APPLY: the next x16
-    float* x32;                  // APPLY
+    __half* out16;               // GRAM: A; POLY: b A + c A A; APPLY: the next hi
+    const __half* hi;            // APPLY
+    __half* lo;                  // APPLY, in place
     // APPLY, last step: the result
     char* out;                   // or null: not the last step
     uint64_t out_pitch, out_stride;
@@ -87,18 +93,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
         if ((i & 255) == 255 && *abort) return false;
     }
     return false;
-}
-
-// AND of v over the epilogue's warps (named barrier 1), the same result in each thread.
-__device__ __forceinline__ bool epi_all(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, 1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)v), "n"(EPI_WARPS * 32) : "memory");
-    return r != 0;
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
@@ -167,16 +161,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
-// Eight f32 from or to 32 aligned bytes: a whole sector a thread, where threads hold rows of their own.
-__device__ __forceinline__ void load_sector(const void* at, uint32_t (&v)[8]) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(at) : "memory");
+// The iterate's two halves: x = hi + 2^-11 lo.
+constexpr float LO_SCALE = 2048.0f;
+__device__ __forceinline__ float2 join(uint32_t hi, uint32_t lo) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi)), l = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    return make_float2(h.x + l.x * (1.0f / LO_SCALE), h.y + l.y * (1.0f / LO_SCALE));
 }
-__device__ __forceinline__ void store_sector(void* at, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+__device__ __forceinline__ void part(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack_f16(x, y);
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = pack_f16((x - h.x) * LO_SCALE, (y - h.y) * LO_SCALE);
 }
 
 // Tile t of a lower triangle counted row by row: (0,0), (1,0), (1,1), (2,0), ...
@@ -223,97 +217,99 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 
 // ---- pair form ---------------------------------------------------------------------------------
-// GRAM, POLY: 32 columns from column c of output row r of matrix m, in the thread that holds them.
+// A slab is 128 rows by 64 columns of f16 in shared memory, rows of 128 bytes with their 16-byte words
+// swizzled by the row, as the tensor maps move it.  The epilogue's thread with lane `lane` of warp w
+// holds row 32 (w % 4) + lane and columns 32 (w / 4) .. of it: words 4 (w / 4) .. + 3.
+__device__ __forceinline__ uint4& slab_word(uint8_t* slab, uint32_t row, uint32_t word) {
+    return *reinterpret_cast<uint4*>(slab + row * 128 + ((word ^ (row & 7)) << 4));
+}
+
+// GRAM, POLY: the thread's 32 columns into the slab (which holds A's for POLY) and, for the mirrored
+// part, into the two blocks of 64 columns by 64 rows behind it, as rows.
 template <Product P>
-__device__ __forceinline__ void finish(const GemmParams& p, uint32_t m, uint32_t r, uint32_t c, bool mirror, float (&v)[32]) {
-    if (r >= p.S || c >= p.S) return;
-    uint32_t w[8];
-    if (P == POLY) {
-        const __half* g = p.gram + ((uint64_t)m * p.S + r) * p.s_pitch + c;
+__device__ __forceinline__ void finish(const GemmParams& p, uint8_t* slab, uint32_t row, uint32_t half, bool mirror, float (&v)[32]) {
+    uint8_t* turned = slab + SLAB_BYTES + row / 64 * (SLAB_BYTES / 2);
 #pragma unroll
-        for (uint32_t q = 0; q < 2; ++q) {
-            load_sector(g + 16 * q, w);
+    for (uint32_t k = 0; k < 4; ++k) {
+        uint4& word = slab_word(slab, row, 4 * half + k);
+        if (P == POLY) {
+            const uint32_t g[4] = {word.x, word.y, word.z, word.w};
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                v[16 * q + 2 * k] = p.c * v[16 * q + 2 * k] + p.b * f.x;
-                v[16 * q + 2 * k + 1] = p.c * v[16 * q + 2 * k + 1] + p.b * f.y;
+            for (uint32_t e = 0; e < 4; ++e) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&g[e]));
+                v[8 * k + 2 * e] = p.c * v[8 * k + 2 * e] + p.b * f.x;
+                v[8 * k + 2 * e + 1] = p.c * v[8 * k + 2 * e + 1] + p.b * f.y;
             }
         }
-    }
-    __half* o = p.out16 + ((uint64_t)m * p.S + r) * p.s_pitch + c;
-#pragma unroll
-    for (uint32_t q = 0; q < 2; ++q) {     // rows are padded to 64 elements: the whole chunk is the array's
-#pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) w[k] = pack_f16(v[16 * q + 2 * k], v[16 * q + 2 * k + 1]);
-        store_sector(o + 16 * q, w);
+        word = make_uint4(pack_f16(v[8 * k], v[8 * k + 1]), pack_f16(v[8 * k + 2], v[8 * k + 3]),
+                          pack_f16(v[8 * k + 4], v[8 * k + 5]), pack_f16(v[8 * k + 6], v[8 * k + 7]));
     }
     if (mirror) {
 #pragma unroll
-        for (uint32_t k = 0; k < 32; ++k)  // neighbouring lanes hold neighbouring columns of the mirrored rows
-            if (c + k < p.S)
-                *reinterpret_cast<uint16_t*>(p.out16 + ((uint64_t)m * p.S + c + k) * p.s_pitch + r) =
-                    (uint16_t)pack_f16(v[k], 0.0f);
+        for (uint32_t k = 0; k < 32; ++k) {        // neighbouring lanes: neighbouring elements of row 32 half + k
+            uint8_t* to = turned + (32 * half + k) * 128 + ((((row % 64) / 8) ^ (k & 7)) << 4) + (row & 7) * 2;
+            *reinterpret_cast<uint16_t*>(to) = (uint16_t)pack_f16(v[k], 0.0f);
+        }
     }
 }
 
-// APPLY: the 32 x 32 sums at TMEM address taddr are output rows r0 .., columns c0 .. of matrix m.  A
-// lane holds a row of them; through the warp's part of shared memory (`turn`, 16-byte words swizzled
-// by the row) they become four columns of a row in each of eight lanes, so that the iterate is read
-// and written in whole lines.  A row a lane would take 3.6 times the shared-memory cycles, which the
-// MMAs' operand reads need.
-__device__ __forceinline__ void apply_block(const GemmParams& p, uint32_t m, uint32_t r0, uint32_t c0, uint32_t taddr, float4* turn) {
-    const uint32_t lane = threadIdx.x % 32, sub = lane / 8, c = c0 + 4 * (lane % 8);
-    const uint64_t base = ((uint64_t)m * p.S + r0 + sub) * p.l_pitch + c;
-    const bool in = c < p.L;               // rows are padded to 64 elements: then all four are the array's
-    float4 x[8];
+// APPLY: a X of the two slabs (hi, lo) added to the thread's 32 columns, and the next iterate left in
+// the slabs (not in the last step).
+__device__ __forceinline__ void finish_apply(const GemmParams& p, uint8_t* slab, uint32_t row, uint32_t half, float (&v)[32]) {
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-        if (in && r0 + 4 * k + sub < p.S) x[k] = *reinterpret_cast<const float4*>(p.x32 + base + 4 * k * p.l_pitch);
-    float v[32];
-    tmem_ld32(taddr, v);
-    __syncwarp();                          // the last block's words have been read
+    for (uint32_t k = 0; k < 4; ++k) {
+        uint4& wh = slab_word(slab, row, 4 * half + k);
+        uint4& wl = slab_word(slab + SLAB_BYTES, row, 4 * half + k);
+        uint32_t h[4] = {wh.x, wh.y, wh.z, wh.w}, l[4] = {wl.x, wl.y, wl.z, wl.w};
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-        turn[lane * 8 + (k ^ (lane & 7))] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    __syncwarp();
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) {
-        const uint32_t n = 4 * k + sub, r = r0 + n;
-        float4& word = turn[n * 8 + ((lane % 8) ^ (n & 7))];
-        float4 w = word;
-        w = make_float4(w.x + p.a * x[k].x, w.y + p.a * x[k].y, w.z + p.a * x[k].z, w.w + p.a * x[k].w);
-        if (p.out && p.transposed) word = w;
-        if (!in || r >= p.S) continue;
+        for (uint32_t e = 0; e < 4; ++e) {
+            const float2 x = join(h[e], l[e]);
+            v[8 * k + 2 * e] += p.a * x.x;
+            v[8 * k + 2 * e + 1] += p.a * x.y;
+            part(v[8 * k + 2 * e], v[8 * k + 2 * e + 1], h[e], l[e]);
+        }
         if (!p.out) {
-            *reinterpret_cast<float4*>(p.x32 + base + 4 * k * p.l_pitch) = w;
-            *reinterpret_cast<uint2*>(p.out16 + base + 4 * k * p.l_pitch) = make_uint2(pack_f16(w.x, w.y), pack_f16(w.z, w.w));
-        } else if (!p.transposed) {
-            const uint32_t lo = pack_bf16(w.x * p.scale, w.y * p.scale), hi = pack_bf16(w.z * p.scale, w.w * p.scale);
-            char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)r * p.out_pitch + (uint64_t)c * 2;
-            if (p.out_vec && c + 4 <= p.L) {
-                *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
-            } else {
-                const uint32_t e[4] = {lo & 0xFFFF, lo >> 16, hi & 0xFFFF, hi >> 16};
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i)
-                    if (c + i < p.L) reinterpret_cast<uint16_t*>(out)[i] = (uint16_t)e[i];
-            }
+            wh = make_uint4(h[0], h[1], h[2], h[3]);
+            wl = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
-    if (p.out && p.transposed) {
-        __syncwarp();
-        char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)(r0 + lane) * 2;
+}
+
+// The last step's 32 columns from column c of row r of matrix m, to the caller's tensor.
+__device__ __forceinline__ void store_result(const GemmParams& p, uint32_t m, uint32_t r, uint32_t c, float (&v)[32]) {
+    if (r >= p.S || c >= p.L) return;
+    char* out = p.out + (uint64_t)m * p.out_stride;
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-            const float4 w = turn[lane * 8 + (k ^ (lane & 7))];
-            const float e[4] = {w.x, w.y, w.z, w.w};
+    for (uint32_t k = 0; k < 32; ++k) v[k] *= p.scale;
+    if (p.transposed) {
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)       // neighbouring lanes hold neighbouring columns of `out`
-                if (r0 + lane < p.S && c0 + 4 * k + i < p.L)
-                    *reinterpret_cast<uint16_t*>(out + (uint64_t)(c0 + 4 * k + i) * p.out_pitch) = (uint16_t)pack_bf16(e[i] * p.scale, 0.0f);
-        }
+        for (uint32_t k = 0; k < 32; ++k)          // neighbouring lanes hold neighbouring columns of `out`
+            if (c + k < p.L)
+                *reinterpret_cast<uint16_t*>(out + (uint64_t)(c + k) * p.out_pitch + (uint64_t)r * 2) =
+                    (uint16_t)pack_bf16(v[k], 0.0f);
+    } else if (p.out_vec && c + 32 <= p.L) {
+        uint4* o = reinterpret_cast<uint4*>(out + (uint64_t)r * p.out_pitch + (uint64_t)c * 2);
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q)
+            o[q] = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                              pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 32; ++k)
+            if (c + k < p.L)
+                *reinterpret_cast<uint16_t*>(out + (uint64_t)r * p.out_pitch + (uint64_t)(c + k) * 2) =
+                    (uint16_t)pack_bf16(v[k], 0.0f);
     }
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 __device__ __forceinline__ void bar_arrive_at(uint32_t cluster_bar) {
@@ -349,11 +345,18 @@ __device__ __forceinline__ void umma_commit_local2(uint32_t bar) {
 }
 
 // Clusters of two CTAs on two SMs, persistent: cluster c takes tiles c, c + clusters, ... of all
-// matrices.  A tile is 256 rows by p.tn columns (a multiple of 32, at most 256) of one
-// tcgen05.mma.cta_group::2: each CTA holds 128 of the rows and half of the columns.  Warp 8 of each
-// loads its operand halves into a ring of stages (TMA, out-of-range rows and columns as zeros), one
-// thread of the leader issues the MMAs into one of two TMEM accumulators (its mbarriers count both
-// CTAs' loads and both epilogues), and warps 0-7 of each drain the CTA's 128 rows of the other.
+// matrices.  A tile is 256 rows by p.tn columns of one tcgen05.mma.cta_group::2: each CTA holds 128 of
+// the rows and half of the columns.  At 256 columns an SM takes in 32 KiB for 512 cycles of MMA, about
+// the 64 bytes a cycle that it can, so everything else is kept off that path as far as it goes.
+//   warp 8      loads the CTA's operand halves into a ring of stages (TMA, out-of-range rows and
+//               columns as zeros);
+//   warp 9      one thread of the leader issues the MMAs into one of two TMEM accumulators (its
+//               mbarriers count both CTAs' loads and both epilogues);
+//   warps 0-7   drain the CTA's 128 rows of the other accumulator, a slab of 64 columns at a time,
+//               into one of two slab buffers;
+//   warp 10     fills the slab buffers with what a slab needs (two slabs ahead) and stores them:
+//               whole 128-byte lines, where stores from the threads that hold the rows took 14 us
+//               cycles (thousands) a tile against 5.
 template <Product P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 ortho_pair_kernel(const __grid_constant__ GemmParams p) {
@@ -361,12 +364,14 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + STAGES * HALF_STAGE;
-    float4* turns = reinterpret_cast<float4*>(sB + STAGES * HALF_STAGE);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + STAGES * HALF_STAGE + EPI_WARPS * TURN_BYTES);   // [STAGES]  leader: both CTAs' loads -> MMA
+    uint8_t* slabs = sB + STAGES * HALF_STAGE;    // [2] x 32 KiB
+    uint64_t* full = reinterpret_cast<uint64_t*>(slabs + SLAB_BUFS * 2 * SLAB_BYTES);   // [STAGES]  leader: both CTAs' loads -> MMA
     uint64_t* empty = full + STAGES;              // [STAGES]  each CTA: MMA -> its TMA warp
     uint64_t* acc_full = empty + STAGES;          // [2]       each CTA: MMA -> its epilogue
     uint64_t* acc_empty = acc_full + ACC_BUFS;    // [2]       leader: both epilogues -> MMA
-    uint64_t* drain = acc_empty + ACC_BUFS;       // [1]       leader: MMA teardown
+    uint64_t* slab_in = acc_empty + ACC_BUFS;     // [2]       slab warp: free, and what it needs is there -> epilogue
+    uint64_t* slab_out = slab_in + SLAB_BUFS;     // [2]       epilogue: to be stored -> slab warp
+    uint64_t* drain = slab_out + SLAB_BUFS;       // [1]       leader: MMA teardown
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
@@ -379,7 +384,11 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
         }
         for (uint32_t i = 0; i < ACC_BUFS; ++i) {
             bar_init(saddr(acc_full + i), 1);
-            bar_init(saddr(acc_empty + i), 2);       // one arrival per CTA's epilogue
+            bar_init(saddr(acc_empty + i), 2 * EPI_WARPS);
+        }
+        for (uint32_t i = 0; i < SLAB_BUFS; ++i) {
+            bar_init(saddr(slab_in + i), 1);
+            bar_init(saddr(slab_out + i), EPI_WARPS);
         }
         bar_init(saddr(drain), 1);
         *abort_flag = 0;
@@ -390,6 +399,10 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(saddr(tmem_slot)), "r"(ACC_BUFS * 256) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (warp == TMA_WARP && lane == 0) {
+        prefetch_map(&p.tmA);
+        prefetch_map(&p.tmB);
     }
     tc_fence_before();
     cluster_sync_all();          // both CTAs' barriers exist before either arrives remotely
@@ -411,6 +424,7 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
         if (lane == 0) {
             uint32_t stage = 0, phase = 0, issued = 0;
             bool ok = true;
+            const bool wide = p.tn > 128;
             for (uint32_t u = c0; u < places && ok; u += NC) {
                 uint32_t m, i, j;
                 tile_of<P>(p, u, m, i, j);
@@ -423,11 +437,11 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
                     const uint32_t bar = at_rank(saddr(full + stage), 0);
                     const int32_t k = (int32_t)(kb * BK);
                     const uint32_t dA = saddr(sA + stage * HALF_STAGE), dB = saddr(sB + stage * HALF_STAGE);
-                    if (leader) bar_expect_tx(saddr(full + stage), 4 * HALF_STAGE);
+                    if (leader) bar_expect_tx(saddr(full + stage), P == APPLY && !wide ? 3 * HALF_STAGE : 4 * HALF_STAGE);
                     tma_load_3d_pair(dA, &p.tmA, k, row, z, bar);
                     if (P == APPLY) {             // X: rows k, 64 columns a box
                         tma_load_3d_pair(dB, &p.tmB, col, k, z, bar);
-                        tma_load_3d_pair(dB + HALF_STAGE / 2, &p.tmB, col + 64, k, z, bar);
+                        if (wide) tma_load_3d_pair(dB + HALF_STAGE / 2, &p.tmB, col + 64, k, z, bar);
                     } else {
                         tma_load_3d_pair(dB, &p.tmB, k, col, z, bar);
                     }
@@ -472,32 +486,92 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
             volatile uint32_t never = 0;
             (void)bar_wait(saddr(drain), 0, &never);
         }
-    } else {
-        // epilogue: warps w and w + 4 own rows 32 w .. of this CTA's 128 and every other block of 32 columns
-        uint32_t acc = 0, acc_phase = 0;
-        const uint32_t rows = 32 * (warp % 4);
-        for (uint32_t u = c0; u < places; u += NC) {
-            uint32_t m, i, j;
-            tile_of<P>(p, u, m, i, j);
-            const bool mine = bar_wait(saddr(acc_full + acc), acc_phase, abort_flag);
-            if (!mine) fail();
-            if (!epi_all(mine && !*abort_flag)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + (rows << 16) + acc * 256, r0 = i * 256 + q * 128 + rows;
-#pragma unroll 1
-            for (uint32_t g = warp / 4; g < p.tn / 32; g += EPI_WARPS / 4) {
-                if (P == APPLY) {
-                    apply_block(p, m, r0, j * p.tn + g * 32, taddr + g * 32, turns + warp * (TURN_BYTES / 16));
+    } else if (warp == SLAB_WARP) {
+        if (lane == 0 && c0 < places) {
+            const uint32_t per_tile = p.tn / SLAB, total = (places - c0 + NC - 1) / NC * per_tile;
+            const uint32_t cols = P == APPLY ? p.L : p.S;
+            uint32_t loaded = 0;
+            auto place = [&](uint32_t s, uint32_t& m, uint32_t& i, uint32_t& j, uint32_t& x, uint32_t& y) {
+                tile_of<P>(p, c0 + s / per_tile * NC, m, i, j);
+                x = j * p.tn + s % per_tile * SLAB;
+                y = i * 256 + q * 128;
+                return x < cols && y < p.S;       // else the slab lies outside
+            };
+            auto load = [&](uint32_t s) {
+                uint32_t m, i, j, x, y;
+                const bool inside = place(s, m, i, j, x, y);
+                const uint32_t bar = saddr(slab_in + s % SLAB_BUFS), to = saddr(slabs) + s % SLAB_BUFS * 2 * SLAB_BYTES;
+                if (P == GRAM || !inside) {
+                    bar_arrive(bar);
                 } else {
-                    float v[32];
-                    tmem_ld32(taddr + g * 32, v);
-                    finish<P>(p, m, r0 + lane, j * p.tn + g * 32, i != j, v);
+                    bar_expect_tx(bar, P == APPLY ? 2 * SLAB_BYTES : SLAB_BYTES);
+                    tma_load_3d(to, &p.in0, (int32_t)x, (int32_t)y, (int32_t)m, bar);
+                    if (P == APPLY) tma_load_3d(to + SLAB_BYTES, &p.in1, (int32_t)x, (int32_t)y, (int32_t)m, bar);
+                }
+                ++loaded;
+            };
+            for (uint32_t s = 0; s < SLAB_BUFS && s < total; ++s) load(s);
+            for (uint32_t s = 0; s < total; ++s) {
+                if (!bar_wait(saddr(slab_out + s % SLAB_BUFS), s / SLAB_BUFS & 1, abort_flag)) { fail(); break; }
+                uint32_t m, i, j, x, y;
+                const bool inside = place(s, m, i, j, x, y);
+                const uint32_t from = saddr(slabs) + s % SLAB_BUFS * 2 * SLAB_BYTES;
+                if (P != APPLY) {
+                    if (inside) tma_store_3d(&p.out0, (int32_t)x, (int32_t)y, (int32_t)m, from);
+                    if (i != j && x < p.S)        // as rows x .., columns y ..
+                        for (uint32_t h = 0; h < 2; ++h)
+                            if (y + 64 * h < p.S)
+                                tma_store_3d(&p.out1, (int32_t)(y + 64 * h), (int32_t)x, (int32_t)m, from + SLAB_BYTES + h * (SLAB_BYTES / 2));
+                } else if (!p.out && inside) {
+                    tma_store_3d(&p.out0, (int32_t)x, (int32_t)y, (int32_t)m, from);
+                    tma_store_3d(&p.out1, (int32_t)x, (int32_t)y, (int32_t)m, from + SLAB_BYTES);
+                }
+                bulk_commit();
+                if (s + SLAB_BUFS < total) {
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    load(s + SLAB_BUFS);
                 }
             }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            volatile uint32_t never = 0;          // every load has landed before the CTA can leave
+            for (uint32_t s = loaded > SLAB_BUFS ? loaded - SLAB_BUFS : 0; s < loaded; ++s)
+                (void)bar_wait(saddr(slab_in + s % SLAB_BUFS), s / SLAB_BUFS & 1, &never);
+        }
+    } else {
+        // epilogue
+        uint32_t acc = 0, acc_phase = 0, s = 0;
+        const uint32_t row = 32 * (warp % 4) + lane, half = warp / 4;
+        bool ok = true;
+        for (uint32_t u = c0; u < places && ok; u += NC) {
+            uint32_t m, i, j;
+            tile_of<P>(p, u, m, i, j);
+            ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(acc_full + acc), acc_phase, abort_flag));
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((32u * (warp % 4)) << 16) + acc * 256 + 32 * half;
+            for (uint32_t g = 0; g < p.tn / SLAB && ok; ++g, ++s) {
+                uint8_t* slab = slabs + s % SLAB_BUFS * 2 * SLAB_BYTES;
+                float v[32];
+                tmem_ld32(taddr + g * SLAB, v);
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(slab_in + s % SLAB_BUFS), s / SLAB_BUFS & 1, abort_flag));
+                if (!ok) break;
+                if (P == APPLY) {
+                    finish_apply(p, slab, row, half, v);
+                    if (p.out) store_result(p, m, i * 256 + q * 128 + row, j * p.tn + g * SLAB + 32 * half, v);
+                } else {
+                    finish<P>(p, slab, row, half, i != j, v);
+                }
+                // the slab warp's stores read what every lane wrote
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive(saddr(slab_out + s % SLAB_BUFS));
+            }
+            if (!ok) {
+                if (lane == 0) fail();
+                break;
+            }
             tc_fence_before();
-            // every TMEM read of this CTA's rows precedes one arrival at the leader
-            asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
-            if (threadIdx.x == 0) bar_arrive_at(at_rank(saddr(acc_empty + acc), 0));
+            __syncwarp();
+            if (lane == 0) bar_arrive_at(at_rank(saddr(acc_empty + acc), 0));   // this warp's TMEM reads are done
             if (++acc == ACC_BUFS) { acc = 0; acc_phase ^= 1; }
         }
     }
@@ -546,6 +620,10 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(128) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == TMA_WARP && lane == 0) {
+        prefetch_map(&p.tmA);
+        prefetch_map(&p.tmB);
     }
     tc_fence_before();
     __syncthreads();
@@ -646,37 +724,44 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
             v = make_float4(p.c * v.x + p.b * lo.x, p.c * v.y + p.b * lo.y, p.c * v.z + p.b * hi.x, p.c * v.w + p.b * hi.y);
         }
         if (P == APPLY && in) {
-            float4* x = reinterpret_cast<float4*>(p.x32 + to);
-            const float4 w = *x;
-            v = make_float4(v.x + p.a * w.x, v.y + p.a * w.y, v.z + p.a * w.z, v.w + p.a * w.w);
-            if (!p.out) *x = v;
+            const uint2 h = *reinterpret_cast<const uint2*>(p.hi + to);
+            uint2* rest = reinterpret_cast<uint2*>(p.lo + to);
+            uint2 l = *rest;
+            const float2 x0 = join(h.x, l.x), x1 = join(h.y, l.y);
+            v = make_float4(v.x + p.a * x0.x, v.y + p.a * x0.y, v.z + p.a * x1.x, v.w + p.a * x1.y);
+            if (!p.out) {
+                uint32_t unused;
+                part(v.x, v.y, unused, l.x);
+                part(v.z, v.w, unused, l.y);
+                *rest = l;
+            }
         }
-        uint32_t lo, hi;
+        uint32_t e01, e23;                        // the four as stored
         if (P == APPLY && p.out) {
-            lo = pack_bf16(v.x * p.scale, v.y * p.scale);
-            hi = pack_bf16(v.z * p.scale, v.w * p.scale);
+            e01 = pack_bf16(v.x * p.scale, v.y * p.scale);
+            e23 = pack_bf16(v.z * p.scale, v.w * p.scale);
         } else {
-            lo = pack_f16(v.x, v.y);
-            hi = pack_f16(v.z, v.w);
+            e01 = pack_f16(v.x, v.y);
+            e23 = pack_f16(v.z, v.w);
         }
         if (turned) {
             uint32_t* row = reinterpret_cast<uint32_t*>(turn + n * T16_PITCH + 4 * lane);
-            row[0] = in ? lo : 0;
-            row[1] = in ? hi : 0;
+            row[0] = in ? e01 : 0;
+            row[1] = in ? e23 : 0;
         }
         if (!in || (P == APPLY && p.out && p.transposed)) continue;
         if (P == APPLY && p.out) {
             char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)r * p.out_pitch + (uint64_t)c * 2;
             if (p.out_vec && c + 4 <= p.L) {
-                *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+                *reinterpret_cast<uint2*>(out) = make_uint2(e01, e23);
             } else {
-                const uint32_t e[4] = {lo & 0xFFFF, lo >> 16, hi & 0xFFFF, hi >> 16};
+                const uint32_t e[4] = {e01 & 0xFFFF, e01 >> 16, e23 & 0xFFFF, e23 >> 16};
 #pragma unroll
                 for (uint32_t k = 0; k < 4; ++k)
                     if (c + k < p.L) reinterpret_cast<uint16_t*>(out)[k] = (uint16_t)e[k];
             }
         } else {
-            *reinterpret_cast<uint2*>(p.out16 + to) = make_uint2(lo, hi);
+            *reinterpret_cast<uint2*>(p.out16 + to) = make_uint2(e01, e23);
         }
     }
     __syncthreads();
@@ -716,8 +801,8 @@ struct UpdateParams {
     uint32_t nesterov, x_dt;
     uint32_t rows, cols, parts;
     float* sums;                 // [batch][parts]
-    float* x32;
-    __half* x16;
+    __half* hi;
+    __half* lo;
     uint64_t l_pitch;
     uint32_t S;
 };
@@ -782,15 +867,15 @@ __device__ __forceinline__ float inverse_norm(const UpdateParams& p, uint32_t m,
     return isinf(inv) ? 0.0f : inv;
 }
 
-// u again (the momentum is updated by now) and X = u / (|u| + eps), in f32 and as the f16 operand: rows
+// u again (the momentum is updated by now) and X = u / (|u| + eps), in its two halves: rows
 // <= cols, 16-byte aligned.  A thread has two chunks of 8 columns under way.
 __global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
     const uint32_t m = blockIdx.y, per_row = p.cols / 8, total = p.rows * per_row, step = gridDim.x * 256;
     const char* x = p.x + (uint64_t)m * p.x_stride;
     const char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
-    float* x32 = p.x32 + (uint64_t)m * p.S * p.l_pitch;
-    __half* x16 = p.x16 + (uint64_t)m * p.S * p.l_pitch;
+    __half* hi = p.hi + (uint64_t)m * p.S * p.l_pitch;
+    __half* lo = p.lo + (uint64_t)m * p.S * p.l_pitch;
     const float inv = inverse_norm(p, m, slot);
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += 2 * step) {
         float u[2][8], v[2][8];
@@ -809,10 +894,13 @@ __global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant_
                 if (mom) u[h][k] = p.nesterov ? u[h][k] + p.mu * v[h][k] : v[h][k];
                 u[h][k] *= inv;
             }
-            store8<true>(reinterpret_cast<char*>(x32 + r * p.l_pitch), DTT_F32, c, p.cols, u[h]);
-            *reinterpret_cast<uint4*>(x16 + r * p.l_pitch + c) =
-                make_uint4(pack_f16(u[h][0], u[h][1]), pack_f16(u[h][2], u[h][3]), pack_f16(u[h][4], u[h][5]),
-                           pack_f16(u[h][6], u[h][7]));
+            uint4 a, b;
+            part(u[h][0], u[h][1], a.x, b.x);
+            part(u[h][2], u[h][3], a.y, b.y);
+            part(u[h][4], u[h][5], a.z, b.z);
+            part(u[h][6], u[h][7], a.w, b.w);
+            *reinterpret_cast<uint4*>(hi + r * p.l_pitch + c) = a;
+            *reinterpret_cast<uint4*>(lo + r * p.l_pitch + c) = b;
         }
     }
 }
@@ -844,8 +932,8 @@ __global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_con
             }
         }
     const float inv = inverse_norm(p, m, slot);
-    float* x32 = p.x32 + (uint64_t)m * p.S * p.l_pitch;
-    __half* x16 = p.x16 + (uint64_t)m * p.S * p.l_pitch;
+    __half* hi = p.hi + (uint64_t)m * p.S * p.l_pitch;
+    __half* lo = p.lo + (uint64_t)m * p.S * p.l_pitch;
     if (TALL) {
 #pragma unroll
         for (uint32_t k = 0; k < kStartTile / 8; ++k)
@@ -862,8 +950,10 @@ __global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_con
             if (r < p.rows && c < p.cols) {
                 const float v = (TALL ? tile[b][a] : u[k][h]) * inv;
                 const uint64_t at = TALL ? c * p.l_pitch + r : r * p.l_pitch + c;
-                x32[at] = v;
-                x16[at] = __float2half_rn(v);
+                uint32_t a, b;
+                part(v, 0.0f, a, b);
+                reinterpret_cast<uint16_t*>(hi)[at] = (uint16_t)a;
+                reinterpret_cast<uint16_t*>(lo)[at] = (uint16_t)b;
             }
         }
 }
@@ -885,7 +975,7 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, ui
 
 struct Layout {
     uint64_t S, L, s_pitch, l_pitch;                 // elements
-    uint64_t x32, x16[2], gram, poly, sums, bytes;   // byte offsets in the workspace
+    uint64_t hi[2], lo, gram, poly, sums, bytes;     // byte offsets in the workspace
 };
 
 Layout layout_of(const dtt_ortho_desc& d) {
@@ -900,9 +990,9 @@ Layout layout_of(const dtt_ortho_desc& d) {
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    l.x32 = take(d.batch * l.S * l.l_pitch * 4);
-    l.x16[0] = take(d.batch * l.S * l.l_pitch * 2);
-    l.x16[1] = take(d.batch * l.S * l.l_pitch * 2);
+    l.hi[0] = take(d.batch * l.S * l.l_pitch * 2);
+    l.hi[1] = take(d.batch * l.S * l.l_pitch * 2);
+    l.lo = take(d.batch * l.S * l.l_pitch * 2);
     l.gram = take(d.batch * l.S * l.s_pitch * 2);
     l.poly = take(d.batch * l.S * l.s_pitch * 2);
     l.sums = take((uint64_t)d.batch * kMaxParts * 4);
@@ -1017,17 +1107,16 @@ uint32_t tiles_of(bool square, uint32_t tile_m, uint32_t tile_n, uint64_t rows, 
     return square ? tm * (tm + 1) / 2 : tm * ceil_div(cols, tile_n);
 }
 
-// The form whose estimated time is least.  A k block of 64 costs a pair 0.34 us at 256 columns (0.30 +
-// 0.04 tn / 256 where loads bound it) and a split CTA 0.27 us; a round of tiles costs a pair 2 us and
-// a split CTA 4 us besides, 1 us more where a cluster adds up its sums.
+// The form whose estimated time is least.  A k block of 64 costs a pair 0.27 us at 256 columns, 0.21 us
+// at 128 (loads bound it), and a split CTA 0.27 us; a round of tiles costs a pair 0.5 us, its set-up and
+// last epilogue 5 us, and a split CTA 4 us a round, 1 us more where a cluster adds up its sums.
 Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t batch, const Fit& fit) {
     const uint32_t kblocks = ceil_div(K, BK);
     Form best{};
     double least = 1e30;
-    for (uint32_t tn = 256; tn >= 128; tn -= 32) {
-        if (square && tn != 256) break;
+    for (uint32_t tn = 256; tn >= (square ? 256u : 128u); tn /= 2) {
         const double rounds = ceil_div((uint64_t)tiles_of(square, 256, tn, rows, cols) * batch, fit.pairs);
-        const double t = rounds * (2.0 + kblocks * (0.08 + 0.26 * tn / 256));
+        const double t = 5.0 + rounds * (0.5 + kblocks * (tn == 256 ? 0.27 : 0.21));
         if (t < least) {
             least = t;
             best = {true, tn, 0};
@@ -1090,9 +1179,10 @@ struct dtt_ortho {
     Layout l;
     char* ws;
     uint32_t sms;
-    CUtensorMap x_rows[2];       // x16, K-major operand of A = X X^T: boxes of 64 x 128
-    CUtensorMap x_cols[2];       // x16, N-contiguous operand of the last product: boxes of 64 x 64
-    CUtensorMap gram, poly;      // boxes of 64 x 128
+    // boxes of 64 x 128 (columns x rows): K-contiguous operands, and slabs
+    CUtensorMap hi_rows[2], lo_rows, gram, poly;
+    // boxes of 64 x 64: the N-contiguous operand of the last product, and mirrored blocks
+    CUtensorMap hi_cols[2], gram_blocks, poly_blocks;
     Fit fit;
     Form form[3];                // of each Product
 };
@@ -1131,10 +1221,13 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     o->form[APPLY] = form_of(false, l.S, l.L, l.S, d->batch, o->fit);
     if (getenv("DBG")) { printf("fit %u %u %u %u %u\n", o->fit.pairs, o->fit.splits[0], o->fit.splits[1], o->fit.splits[2], o->fit.splits[3]); for (auto& f : o->form) printf("  form pair %d tn %u ctas %u\n", f.pair, f.tn, f.ctas); }
     bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 128) &&
-              make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128);
+              make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128) &&
+              make_map(&o->gram_blocks, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 64) &&
+              make_map(&o->poly_blocks, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 64) &&
+              make_map(&o->lo_rows, o->ws + l.lo, l.L, l.S, d->batch, l.l_pitch, 128);
     for (int i = 0; i < 2 && ok; ++i)
-        ok = make_map(&o->x_rows[i], o->ws + l.x16[i], l.L, l.S, d->batch, l.l_pitch, 128) &&
-             make_map(&o->x_cols[i], o->ws + l.x16[i], l.L, l.S, d->batch, l.l_pitch, BK);
+        ok = make_map(&o->hi_rows[i], o->ws + l.hi[i], l.L, l.S, d->batch, l.l_pitch, 128) &&
+             make_map(&o->hi_cols[i], o->ws + l.hi[i], l.L, l.S, d->batch, l.l_pitch, 64);
     if (!ok) {
         delete o;
         return fail(DTT_ECUDA, "%s: cannot encode the tensor maps", who);
@@ -1168,7 +1261,6 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     }
     if (reinterpret_cast<uintptr_t>(err) % 4) return fail(DTT_EINVAL, "%s: err is misaligned", who);
 
-    float* x32 = reinterpret_cast<float*>(o->ws + l.x32);
     UpdateParams up{};
     up.x = static_cast<const char*>(x);
     up.x_pitch = x_pitch;
@@ -1183,8 +1275,8 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     up.rows = (uint32_t)d.rows;
     up.cols = (uint32_t)d.cols;
     up.sums = reinterpret_cast<float*>(o->ws + l.sums);
-    up.x32 = x32;
-    up.x16 = reinterpret_cast<__half*>(o->ws + l.x16[0]);
+    up.hi = reinterpret_cast<__half*>(o->ws + l.hi[0]);
+    up.lo = reinterpret_cast<__half*>(o->ws + l.lo);
     up.l_pitch = l.l_pitch;
     up.S = (uint32_t)l.S;
     const bool tall = d.rows > d.cols;
@@ -1211,7 +1303,7 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     g.batch = d.batch;
     g.s_pitch = l.s_pitch;
     g.l_pitch = l.l_pitch;
-    g.x32 = x32;
+    g.lo = up.lo;
     g.err = err;
     g.scale = d.scale;
     g.transposed = tall;
@@ -1224,19 +1316,27 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         g.b = d.coeffs[k][1];
         g.c = d.coeffs[k][2];
         g.L = g.S;
-        g.tmA = g.tmB = o->x_rows[now];
+        g.tmA = g.tmB = o->hi_rows[now];
+        g.out0 = o->gram;
+        g.out1 = o->gram_blocks;
         g.K = (uint32_t)l.L;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.gram);
         DTT_CUDA_TRY(launch_product<GRAM>(g, o->form[GRAM], o->fit.pairs, stream));
-        g.tmA = g.tmB = o->gram;
+        g.tmA = g.tmB = g.in0 = o->gram;
+        g.out0 = o->poly;
+        g.out1 = o->poly_blocks;
         g.K = g.S;
         g.gram = g.out16;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.poly);
         DTT_CUDA_TRY(launch_product<POLY>(g, o->form[POLY], o->fit.pairs, stream));
         g.tmA = o->poly;
-        g.tmB = o->x_cols[now];
+        g.tmB = o->hi_cols[now];
+        g.in0 = o->hi_rows[now];
+        g.in1 = g.out1 = o->lo_rows;
+        g.out0 = o->hi_rows[now ^ 1];
         g.L = (uint32_t)l.L;
-        g.out16 = reinterpret_cast<__half*>(o->ws + l.x16[now ^ 1]);
+        g.hi = reinterpret_cast<const __half*>(o->ws + l.hi[now]);
+        g.out16 = reinterpret_cast<__half*>(o->ws + l.hi[now ^ 1]);
         g.out = k + 1 == d.steps ? static_cast<char*>(out) : nullptr;
         DTT_CUDA_TRY(launch_product<APPLY>(g, o->form[APPLY], o->fit.pairs, stream));
     }
