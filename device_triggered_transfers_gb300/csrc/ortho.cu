@@ -13,8 +13,6 @@
 // stored twice, once transposed.
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
-#include <cstdio>
 #include <cstdint>
 #include <mutex>
 #include <new>
@@ -354,9 +352,9 @@ __device__ __forceinline__ void umma_commit_local2(uint32_t bar) {
 //               mbarriers count both CTAs' loads and both epilogues);
 //   warps 0-7   drain the CTA's 128 rows of the other accumulator, a slab of 64 columns at a time,
 //               into one of two slab buffers;
-//   warp 10     fills the slab buffers with what a slab needs (two slabs ahead) and stores them:
-//               whole 128-byte lines, where stores from the threads that hold the rows took 14 us
-//               cycles (thousands) a tile against 5.
+//   warp 10     fills the slab buffers with what a slab needs (two slabs ahead) and stores them, in
+//               whole 128-byte lines: stored by the threads that hold the rows, a tile took 14,000
+//               cycles instead of 6,000.
 template <Product P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 ortho_pair_kernel(const __grid_constant__ GemmParams p) {
@@ -591,11 +589,11 @@ __device__ __forceinline__ float4 load_peer(uint32_t cluster_addr) {
     return v;
 }
 
-// One 128 x 128 tile a cluster, its k blocks shared out over the cluster's CTAs (one, two, four or
-// eight).  Each CTA leaves its f32 sums in its shared memory; CTA q then adds rows q 128 / CTAs .. of
+// One 128 x 128 tile a cluster, its k blocks shared out over the cluster's CTAs (CTAS: one, two, four
+// or eight).  Each CTA leaves its f32 sums in its shared memory; CTA q then adds rows q 128 / CTAs .. of
 // all of them, in the CTAs' order, through distributed shared memory, and stores those rows.
-template <Product P>
-__global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_constant__ GemmParams p, uint32_t ctas) {
+template <Product P, uint32_t CTAS>
+__global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
@@ -633,8 +631,25 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
     wait_previous();
 
     uint32_t m, i, j;
-    tile_of<P>(p, blockIdx.x / ctas, m, i, j);
-    const uint32_t kblocks = (p.K + BK - 1) / BK, k0 = kblocks * q / ctas, k1 = kblocks * (q + 1) / ctas;
+    tile_of<P>(p, blockIdx.x / CTAS, m, i, j);
+    const uint32_t kblocks = (p.K + BK - 1) / BK, k0 = kblocks * q / CTAS, k1 = kblocks * (q + 1) / CTAS;
+    // the rows that this CTA stores: a warp a row, four columns a lane, and what they need besides the sums
+    constexpr uint32_t rows = 128 / CTAS, MAX_ROWS = rows / EPI_WARPS;
+    const uint32_t first = q * rows, cols = P == APPLY ? p.L : p.S;
+    const uint64_t pitch = P == APPLY ? p.l_pitch : p.s_pitch;
+    const uint32_t c = j * 128 + 4 * lane;
+    uint2 held[P == GRAM ? 1 : MAX_ROWS], rest[P == APPLY ? MAX_ROWS : 1];
+    if (P != GRAM && warp < EPI_WARPS && c < cols) {
+#pragma unroll
+        for (uint32_t k = 0; k < MAX_ROWS; ++k) {
+            const uint32_t n = warp + EPI_WARPS * k, r = i * 128 + first + n;
+            if (r < p.S) {
+                const uint64_t at = ((uint64_t)m * p.S + r) * pitch + c;
+                held[k] = *reinterpret_cast<const uint2*>((P == POLY ? p.gram : p.hi) + at);
+                if (P == APPLY) rest[k] = *reinterpret_cast<const uint2*>(p.lo + at);
+            }
+        }
+    }
     auto fail = [&]() {
         *abort_flag = 1;
         atomicAdd(p.err, 1u);
@@ -697,43 +712,46 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
         }
     }
     tc_fence_before();
-    cluster_sync_all();                           // every CTA's sums are there
+    if (CTAS > 1) cluster_sync_all();             // every CTA's sums are there
+    else __syncthreads();
     tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(128) : "memory");
 
-    // a warp a row, four columns a lane
-    const uint32_t rows = 128 / ctas, first = q * rows, cols = P == APPLY ? p.L : p.S;
-    const uint64_t pitch = P == APPLY ? p.l_pitch : p.s_pitch;
-    const uint32_t c = j * 128 + 4 * lane;
     const bool turned = P == APPLY ? p.out && p.transposed : i != j;   // the rows are stored as columns (too)
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + T16_OFFSET);
-    for (uint32_t n = warp; n < rows; n += THREADS / 32) {
-        const uint32_t r = i * 128 + first + n;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const uint32_t at = saddr(tile + (first + n) * T_PITCH + 4 * lane);
-        for (uint32_t o = 0; o < ctas; ++o) {
-            const float4 w = load_peer(at_rank(at, o));
-            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    // all the sums that the thread adds are under way before it adds the first
+    float4 sums[MAX_ROWS][CTAS];
+#pragma unroll
+    for (uint32_t k = 0; k < MAX_ROWS; ++k)
+#pragma unroll
+        for (uint32_t o = 0; o < CTAS; ++o) {
+            const float* at = tile + (first + warp % EPI_WARPS + EPI_WARPS * k) * T_PITCH + 4 * lane;
+            sums[k][o] = CTAS == 1 ? *reinterpret_cast<const float4*>(at) : load_peer(at_rank(saddr(at), o));
         }
+#pragma unroll
+    for (uint32_t k = 0; k < MAX_ROWS; ++k) {
+        const uint32_t n = warp + EPI_WARPS * k, r = i * 128 + first + n;
+        if (warp >= EPI_WARPS) break;
+        float4 v = sums[k][0];
+#pragma unroll
+        for (uint32_t o = 1; o < CTAS; ++o)
+            v = make_float4(v.x + sums[k][o].x, v.y + sums[k][o].y, v.z + sums[k][o].z, v.w + sums[k][o].w);
         const bool in = r < p.S && c < cols;      // rows are padded to 64 elements: then all four are the array's
         const uint64_t to = ((uint64_t)m * p.S + r) * pitch + c;
         if (P == POLY && in) {
-            const uint2 g = *reinterpret_cast<const uint2*>(p.gram + to);
-            const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&g.x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&g.y));
-            v = make_float4(p.c * v.x + p.b * lo.x, p.c * v.y + p.b * lo.y, p.c * v.z + p.b * hi.x, p.c * v.w + p.b * hi.y);
+            const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&held[k].x)), g1 = __half22float2(*reinterpret_cast<const __half2*>(&held[k].y));
+            v = make_float4(p.c * v.x + p.b * g0.x, p.c * v.y + p.b * g0.y, p.c * v.z + p.b * g1.x, p.c * v.w + p.b * g1.y);
         }
         if (P == APPLY && in) {
-            const uint2 h = *reinterpret_cast<const uint2*>(p.hi + to);
-            uint2* rest = reinterpret_cast<uint2*>(p.lo + to);
-            uint2 l = *rest;
-            const float2 x0 = join(h.x, l.x), x1 = join(h.y, l.y);
+            const float2 x0 = join(held[k].x, rest[k].x), x1 = join(held[k].y, rest[k].y);
             v = make_float4(v.x + p.a * x0.x, v.y + p.a * x0.y, v.z + p.a * x1.x, v.w + p.a * x1.y);
             if (!p.out) {
                 uint32_t unused;
+                uint2 l;
                 part(v.x, v.y, unused, l.x);
                 part(v.z, v.w, unused, l.y);
-                *rest = l;
+                *reinterpret_cast<uint2*>(p.lo + to) = l;
             }
         }
         uint32_t e01, e23;                        // the four as stored
@@ -757,8 +775,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
             } else {
                 const uint32_t e[4] = {e01 & 0xFFFF, e01 >> 16, e23 & 0xFFFF, e23 >> 16};
 #pragma unroll
-                for (uint32_t k = 0; k < 4; ++k)
-                    if (c + k < p.L) reinterpret_cast<uint16_t*>(out)[k] = (uint16_t)e[k];
+                for (uint32_t x = 0; x < 4; ++x)
+                    if (c + x < p.L) reinterpret_cast<uint16_t*>(out)[x] = (uint16_t)e[x];
             }
         } else {
             *reinterpret_cast<uint2*>(p.out16 + to) = make_uint2(e01, e23);
@@ -789,7 +807,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
             }
         }
     }
-    cluster_sync_all();                           // no CTA leaves while its sums may be read
+    if (CTAS > 1) cluster_sync_all();             // no CTA leaves while its sums may be read
 }
 
 struct UpdateParams {
@@ -1089,7 +1107,9 @@ Fit fit_of(int device, uint32_t sms) {
     if (!f.pairs) {
         f.pairs = clusters_of(ortho_pair_kernel<APPLY>, 2);
         f.splits[0] = sms;
-        for (uint32_t n = 1; n < 4; ++n) f.splits[n] = clusters_of(ortho_split_kernel<APPLY>, 1u << n);
+        f.splits[1] = clusters_of(ortho_split_kernel<APPLY, 2>, 2);
+        f.splits[2] = clusters_of(ortho_split_kernel<APPLY, 4>, 4);
+        f.splits[3] = clusters_of(ortho_split_kernel<APPLY, 8>, 8);
     }
     return f;
 }
@@ -1107,16 +1127,17 @@ uint32_t tiles_of(bool square, uint32_t tile_m, uint32_t tile_n, uint64_t rows, 
     return square ? tm * (tm + 1) / 2 : tm * ceil_div(cols, tile_n);
 }
 
-// The form whose estimated time is least.  A k block of 64 costs a pair 0.27 us at 256 columns, 0.21 us
-// at 128 (loads bound it), and a split CTA 0.27 us; a round of tiles costs a pair 0.5 us, its set-up and
-// last epilogue 5 us, and a split CTA 4 us a round, 1 us more where a cluster adds up its sums.
+// The form whose estimated time is least.  Measured: a k block of 64 costs a pair 0.275 us at 256 columns,
+// 0.21 us at 128, and its set-up and last epilogue 8 us; a split CTA takes 0.36 us a k block (what one SM
+// can load) and 4.6 us besides in every round of tiles, 0.6 us more where a cluster adds up its sums, 0.5
+// more in one of eight.
 Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t batch, const Fit& fit) {
     const uint32_t kblocks = ceil_div(K, BK);
     Form best{};
     double least = 1e30;
     for (uint32_t tn = 256; tn >= (square ? 256u : 128u); tn /= 2) {
         const double rounds = ceil_div((uint64_t)tiles_of(square, 256, tn, rows, cols) * batch, fit.pairs);
-        const double t = 5.0 + rounds * (0.5 + kblocks * (tn == 256 ? 0.27 : 0.21));
+        const double t = 8.0 + rounds * (0.3 + kblocks * (tn == 256 ? 0.275 : 0.21));
         if (t < least) {
             least = t;
             best = {true, tn, 0};
@@ -1125,7 +1146,7 @@ Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t bat
     for (uint32_t n = 0; n < 4 && (1u << n) <= kblocks; ++n) {
         const uint32_t ctas = 1u << n;
         const double rounds = ceil_div((uint64_t)tiles_of(square, 128, 128, rows, cols) * batch, fit.splits[n]);
-        const double t = rounds * (4.0 + (ctas > 1) + 0.27 * ceil_div(kblocks, ctas));
+        const double t = 0.8 + rounds * (4.6 + 0.6 * (ctas > 1) + 0.5 * (ctas > 4) + 0.36 * ceil_div(kblocks, ctas));
         if (t < least) {
             least = t;
             best = {false, 128, ctas};
@@ -1142,7 +1163,9 @@ cudaError_t launch_product(GemmParams& p, const Form& f, uint32_t pairs, cudaStr
     p.tiles = tiles_of(P != APPLY, tile_m, f.tn, p.S, p.L);
     const uint32_t places = p.tiles * p.batch;
     if (f.pair) return launch(ortho_pair_kernel<P>, 2 * std::min(places, pairs), THREADS, SMEM_BYTES, 0, stream, p);
-    return launch(ortho_split_kernel<P>, places * f.ctas, THREADS, SMEM_BYTES, f.ctas, stream, p, f.ctas);
+    auto kernel = f.ctas == 1 ? ortho_split_kernel<P, 1> : f.ctas == 2 ? ortho_split_kernel<P, 2>
+                : f.ctas == 4 ? ortho_split_kernel<P, 4> : ortho_split_kernel<P, 8>;
+    return launch(kernel, places * f.ctas, THREADS, SMEM_BYTES, f.ctas, stream, p);
 }
 
 template <Product P>
@@ -1150,9 +1173,10 @@ cudaError_t prepare_product() {
     cudaError_t e = prepare_kernel(ortho_pair_kernel<P>);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(ortho_pair_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-    if (e == cudaSuccess) e = prepare_kernel(ortho_split_kernel<P>);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(ortho_split_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    for (auto kernel : {ortho_split_kernel<P, 1>, ortho_split_kernel<P, 2>, ortho_split_kernel<P, 4>, ortho_split_kernel<P, 8>}) {
+        if (e == cudaSuccess) e = prepare_kernel(kernel);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    }
     return e;
 }
 
@@ -1219,7 +1243,6 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     o->form[GRAM] = form_of(true, l.S, l.S, l.L, d->batch, o->fit);
     o->form[POLY] = form_of(true, l.S, l.S, l.S, d->batch, o->fit);
     o->form[APPLY] = form_of(false, l.S, l.L, l.S, d->batch, o->fit);
-    if (getenv("DBG")) { printf("fit %u %u %u %u %u\n", o->fit.pairs, o->fit.splits[0], o->fit.splits[1], o->fit.splits[2], o->fit.splits[3]); for (auto& f : o->form) printf("  form pair %d tn %u ctas %u\n", f.pair, f.tn, f.ctas); }
     bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->gram_blocks, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 64) &&
