@@ -10,7 +10,11 @@
 // only through b A + c A A, whose range holds nothing of those directions.
 //
 // A and b A + c A A are symmetric: only tiles on and below the diagonal are computed, and each is
-// stored twice, once transposed.
+// stored twice, once transposed (not in the resident form).
+//
+// Three forms: resident (S <= 128, L <= 4096: one launch, X in the shared memory of a cluster); a launch
+// a product by CTA pairs on tiles of 256 rows (large); or on tiles of 128 x 128 split over clusters along
+// k (between).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -65,12 +69,20 @@ struct GemmParams {
     __half* out16;               // GRAM: A; POLY: b A + c A A; APPLY: the next hi
     const __half* hi;            // APPLY
     __half* lo;                  // APPLY, in place
-    // APPLY, last step: the result
-    char* out;                   // or null: not the last step
+    char* out;                   // APPLY, last step: the result (see Result); null: not the last step
     uint64_t out_pitch, out_stride;
     float scale;
     uint32_t transposed, out_vec;
     uint32_t* err;
+};
+
+// Where the result goes: scale X, rounded to bf16, by rows or (transposed) by columns of X.
+struct Result {
+    char* out;                   // of one matrix
+    uint64_t pitch;
+    uint32_t S, L;
+    float scale;
+    uint32_t transposed, vec;    // vec: rows of 16-byte words
 };
 
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
@@ -251,52 +263,49 @@ __device__ __forceinline__ void finish(const GemmParams& p, uint8_t* slab, uint3
     }
 }
 
-// APPLY: a X of the two slabs (hi, lo) added to the thread's 32 columns, and the next iterate left in
-// the slabs (not in the last step).
-__device__ __forceinline__ void finish_apply(const GemmParams& p, uint8_t* slab, uint32_t row, uint32_t half, float (&v)[32]) {
+// APPLY: a X of the two slabs added to the thread's 32 columns, and the next iterate left in the slabs
+// (keep).
+__device__ __forceinline__ void finish_apply(float a, uint8_t* hi, uint8_t* lo, uint32_t row, uint32_t half, float (&v)[32], bool keep) {
 #pragma unroll
     for (uint32_t k = 0; k < 4; ++k) {
-        uint4& wh = slab_word(slab, row, 4 * half + k);
-        uint4& wl = slab_word(slab + SLAB_BYTES, row, 4 * half + k);
+        uint4& wh = slab_word(hi, row, 4 * half + k);
+        uint4& wl = slab_word(lo, row, 4 * half + k);
         uint32_t h[4] = {wh.x, wh.y, wh.z, wh.w}, l[4] = {wl.x, wl.y, wl.z, wl.w};
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
             const float2 x = join(h[e], l[e]);
-            v[8 * k + 2 * e] += p.a * x.x;
-            v[8 * k + 2 * e + 1] += p.a * x.y;
+            v[8 * k + 2 * e] += a * x.x;
+            v[8 * k + 2 * e + 1] += a * x.y;
             part(v[8 * k + 2 * e], v[8 * k + 2 * e + 1], h[e], l[e]);
         }
-        if (!p.out) {
+        if (keep) {
             wh = make_uint4(h[0], h[1], h[2], h[3]);
             wl = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
 }
 
-// The last step's 32 columns from column c of row r of matrix m, to the caller's tensor.
-__device__ __forceinline__ void store_result(const GemmParams& p, uint32_t m, uint32_t r, uint32_t c, float (&v)[32]) {
-    if (r >= p.S || c >= p.L) return;
-    char* out = p.out + (uint64_t)m * p.out_stride;
+// 32 columns from column c of row r of the result.
+__device__ __forceinline__ void store_result(const Result& o, uint32_t r, uint32_t c, float (&v)[32]) {
+    if (r >= o.S || c >= o.L) return;
 #pragma unroll
-    for (uint32_t k = 0; k < 32; ++k) v[k] *= p.scale;
-    if (p.transposed) {
+    for (uint32_t k = 0; k < 32; ++k) v[k] *= o.scale;
+    if (o.transposed) {
 #pragma unroll
         for (uint32_t k = 0; k < 32; ++k)          // neighbouring lanes hold neighbouring columns of `out`
-            if (c + k < p.L)
-                *reinterpret_cast<uint16_t*>(out + (uint64_t)(c + k) * p.out_pitch + (uint64_t)r * 2) =
-                    (uint16_t)pack_bf16(v[k], 0.0f);
-    } else if (p.out_vec && c + 32 <= p.L) {
-        uint4* o = reinterpret_cast<uint4*>(out + (uint64_t)r * p.out_pitch + (uint64_t)c * 2);
+            if (c + k < o.L)
+                *reinterpret_cast<uint16_t*>(o.out + (uint64_t)(c + k) * o.pitch + (uint64_t)r * 2) = (uint16_t)pack_bf16(v[k], 0.0f);
+    } else if (o.vec && c + 32 <= o.L) {
+        uint4* to = reinterpret_cast<uint4*>(o.out + (uint64_t)r * o.pitch + (uint64_t)c * 2);
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q)
-            o[q] = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                              pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+            to[q] = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                               pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
     } else {
 #pragma unroll
         for (uint32_t k = 0; k < 32; ++k)
-            if (c + k < p.L)
-                *reinterpret_cast<uint16_t*>(out + (uint64_t)r * p.out_pitch + (uint64_t)(c + k) * 2) =
-                    (uint16_t)pack_bf16(v[k], 0.0f);
+            if (c + k < o.L)
+                *reinterpret_cast<uint16_t*>(o.out + (uint64_t)r * o.pitch + (uint64_t)(c + k) * 2) = (uint16_t)pack_bf16(v[k], 0.0f);
     }
 }
 
@@ -553,8 +562,10 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(slab_in + s % SLAB_BUFS), s / SLAB_BUFS & 1, abort_flag));
                 if (!ok) break;
                 if (P == APPLY) {
-                    finish_apply(p, slab, row, half, v);
-                    if (p.out) store_result(p, m, i * 256 + q * 128 + row, j * p.tn + g * SLAB + 32 * half, v);
+                    finish_apply(p.a, slab, slab + SLAB_BYTES, row, half, v, !p.out);
+                    if (p.out)
+                        store_result({p.out + (uint64_t)m * p.out_stride, p.out_pitch, p.S, p.L, p.scale, p.transposed, p.out_vec},
+                                     i * 256 + q * 128 + row, j * p.tn + g * SLAB + 32 * half, v);
                 } else {
                     finish<P>(p, slab, row, half, i != j, v);
                 }
@@ -976,6 +987,344 @@ __global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_con
         }
 }
 
+// ---- resident form -----------------------------------------------------------------------------
+constexpr uint32_t RES_THREADS = 256;
+constexpr uint32_t RES_BLOCKS = 4;                   // blocks of 64 columns a CTA, at most
+constexpr uint32_t RES_CTAS = 16;                    // of a cluster, at most
+constexpr uint32_t BLOCK_BYTES = 128 * 64 * 2;       // 128 rows by 64 columns of f16
+// hi; two blocks of A (later b A + c A A); the CTA's own f32 sums; and the sums of its rows from all CTAs
+constexpr uint32_t RES_SUMS = 128 * 128 * 4;
+constexpr uint32_t RES_SMEM = 1024 /* alignment slack */ + (RES_BLOCKS + 2) * BLOCK_BYTES + 2 * RES_SUMS + 128;
+struct ResidentParams {
+    UpdateParams u;
+    Result out;                  // of matrix 0
+    uint64_t out_stride;
+    uint32_t blocks;             // of a CTA
+    uint32_t vec;                // the update and the momentum: rows of 16-byte words, whole chunks of 8 columns
+    uint32_t steps;
+    uint32_t* err;
+    float coeffs[DTT_ORTHO_MAX_STEPS][3];
+};
+
+// A copy to a CTA of the cluster that counts, in bytes, on an mbarrier of that CTA.
+__device__ __forceinline__ void push(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(to), "r"(from), "r"(bytes), "r"(bar) : "memory");
+}
+// 16 words of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float load_peer1(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// S <= 128: one cluster of CTAS a matrix, from the update to the result: hi stays in shared memory, lo in
+// TMEM.  CTA q holds columns 64 blocks q .. of X; a block of 64 columns by 128 rows serves as it lies
+// as the K-contiguous operand of A = X X^T and as the N-contiguous one of (b A + c A A) X.  Only A
+// crosses CTAs: each sends its f32 sums of rows 128 / CTAS o .. to CTA o, which adds them in the CTAs'
+// order and sends the rows of A, in f16, to all; every CTA then works out b A + c A A for itself, in A's
+// place.  The two exchanges (bulk copies; stores by the threads took twice as long) are their own
+// hand-shake: a CTA's sums of the next step leave after it has used b A + c A A, its rows of A after
+// it has read the sums, and nobody goes on without all of either.  One launch, and nothing but the
+// update and the result in memory: a product's 5 us as a launch of its own are mostly set-up here.
+template <uint32_t CTAS>
+__global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __grid_constant__ ResidentParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* hi = smem;
+    uint8_t* gram = hi + RES_BLOCKS * BLOCK_BYTES;
+    // rows of 32 words of four columns, words swizzled by the row: the CTA's own [128], and
+    // [CTAS sources][128 / CTAS]
+    float4* own = reinterpret_cast<float4*>(gram + 2 * BLOCK_BYTES);
+    float4* sums = own + RES_SUMS / 16;
+    uint64_t* done = reinterpret_cast<uint64_t*>(sums + RES_SUMS / 16);
+    uint64_t* sums_full = done + 1;
+    uint64_t* gram_full = done + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 3);
+    float* norm_part = reinterpret_cast<float*>(tmem_slot + 1);
+    __shared__ float slot[8];
+
+    const uint32_t t = threadIdx.x, warp = t / 32, lane = t % 32, q = CTAS > 1 ? cluster_rank() : 0, m = blockIdx.x / CTAS;
+    const uint32_t S = p.u.S, L = p.out.L, width = p.blocks * 64, l0 = q * width;
+    const bool tall = p.out.transposed;
+    if (t == 0) {
+        bar_init(saddr(done), 1);
+        bar_init(saddr(sums_full), 1);
+        bar_init(saddr(gram_full), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+
+    // the update (and the momentum) in f32 over the two arrays of sums, 16-byte words swizzled by the
+    // row; zeros beyond S and L.  Loads go out together before any is stored.
+    const char* x = p.u.x + (uint64_t)m * p.u.x_stride;
+    char* mom = p.u.mom ? p.u.mom + (uint64_t)m * p.u.mom_stride : nullptr;
+    auto staged = [&](uint32_t s, uint32_t l) -> float4& {
+        return own[l / 64 * (128 * 16) + s * 16 + ((l % 64 / 4) ^ ((s ^ s / 8) & 15))];
+    };
+    float sum = 0.0f;
+    if (p.vec) {                                      // 16-byte aligned: 8 columns of the update a thread
+        constexpr uint32_t N = 4;
+        const uint32_t per_row = (tall ? 128 : width) / 8;
+        for (uint32_t e0 = t; e0 < 16 * width; e0 += N * RES_THREADS) {     // 16 width: a multiple of N RES_THREADS
+            float u[N][8], v[N][8];
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n) {
+                const uint32_t e = e0 + n * RES_THREADS, r = e / per_row, c = 8 * (e - r * per_row);
+                const uint32_t gr = tall ? l0 + r : r, gc = tall ? c : l0 + c;
+                const bool in = gr < p.u.rows && gc < p.u.cols;
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) u[n][k] = v[n][k] = 0.0f;
+                if (in) load8<true>(x + gr * p.u.x_pitch, p.u.x_dt, gc, p.u.cols, u[n]);
+                if (in && mom) load8<true>(mom + gr * p.u.mom_pitch, DTT_F32, gc, p.u.cols, v[n]);
+            }
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n) {
+                const uint32_t e = e0 + n * RES_THREADS, r = e / per_row, c = 8 * (e - r * per_row);
+                const uint32_t gr = tall ? l0 + r : r, gc = tall ? c : l0 + c;
+                if (mom) {
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) {
+                        v[n][k] = p.u.mu * v[n][k] + u[n][k];
+                        u[n][k] = p.u.nesterov ? u[n][k] + p.u.mu * v[n][k] : v[n][k];
+                    }
+                    if (gr < p.u.rows && gc < p.u.cols) store8<true>(mom + gr * p.u.mom_pitch, DTT_F32, gc, p.u.cols, v[n]);
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) sum += u[n][k] * u[n][k];
+                if (tall) {
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k) reinterpret_cast<float*>(&staged(c + k, r))[r % 4] = u[n][k];
+                } else {
+                    staged(r, c) = make_float4(u[n][0], u[n][1], u[n][2], u[n][3]);
+                    staged(r, c + 4) = make_float4(u[n][4], u[n][5], u[n][6], u[n][7]);
+                }
+            }
+        }
+    } else {                                          // an element a lane: 32 columns of a row of the update a warp
+        constexpr uint32_t N = 16;
+        const uint32_t per_row = (tall ? 128 : width) / 32, total = 4 * width;     // a multiple of 8 N / 4
+        for (uint32_t e0 = warp; e0 < total; e0 += N * (RES_THREADS / 32)) {
+            float u[N], v[N];
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n) {
+                const uint32_t e = e0 + n * (RES_THREADS / 32), r = e / per_row, c = 32 * (e - r * per_row) + lane;
+                const uint32_t gr = tall ? l0 + r : r, gc = tall ? c : l0 + c;
+                const bool in = e < total && gr < p.u.rows && gc < p.u.cols;
+                u[n] = in ? load1(x + gr * p.u.x_pitch, p.u.x_dt, gc) : 0.0f;
+                v[n] = in && mom ? load1(mom + gr * p.u.mom_pitch, DTT_F32, gc) : 0.0f;
+            }
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n) {
+                const uint32_t e = e0 + n * (RES_THREADS / 32), r = e / per_row, c = 32 * (e - r * per_row) + lane;
+                const uint32_t gr = tall ? l0 + r : r, gc = tall ? c : l0 + c, s = tall ? c : r, l = tall ? r : c;
+                if (e >= total) break;
+                if (mom) {
+                    v[n] = p.u.mu * v[n] + u[n];
+                    u[n] = p.u.nesterov ? u[n] + p.u.mu * v[n] : v[n];
+                    if (gr < p.u.rows && gc < p.u.cols) store1(mom + gr * p.u.mom_pitch, DTT_F32, gc, v[n]);
+                }
+                sum += u[n] * u[n];
+                reinterpret_cast<float*>(&staged(s, l))[l % 4] = u[n];
+            }
+        }
+    }
+    sum = cta_sum(sum, slot);
+    if (CTAS > 1) {
+        if (t == 0) *norm_part = sum;
+        cluster_sync_all();
+        sum = 0.0f;
+#pragma unroll
+        for (uint32_t o = 0; o < CTAS; ++o) sum += load_peer1(at_rank(saddr(norm_part), o));
+    }
+    float inv = 1.0f / (sqrtf(sum) + p.u.eps);
+    if (isinf(inv)) inv = 0.0f;                       // u is then 0 in f16 as well
+    const uint32_t row = 32 * (warp % 4) + lane, half = warp / 4;
+    uint32_t phase = 0;
+    volatile uint32_t never = 0;
+    auto await = [&](uint64_t* bar, uint32_t parity) {
+        if (!bar_wait(saddr(bar), parity, &never) && lane == 0) atomicAdd(p.err, 1u);
+        __syncwarp();
+    };
+    // what the threads wrote is there for the MMAs that `issue` starts; all threads wait for these
+    auto product = [&](auto issue) {
+        fence_async();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (t == 0) {
+            issue();
+            umma_commit(saddr(done));
+        }
+        __syncwarp();
+        await(done, phase);
+        phase ^= 1;
+        tc_fence_after();
+    };
+    tc_fence_before();
+    __syncthreads();                                  // the update is staged, the allocation's address there
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot, d_square = tmem, d_apply = tmem + 128;
+    const uint32_t lanes = (32u * (warp % 4)) << 16, lo = tmem + 384 + lanes + 16 * half;   // 32 words a block
+    for (uint32_t n = 0; n < p.blocks; ++n) {         // X = inv u: 32 columns of a row a thread, as ever after
+        uint32_t rest[16];
+#pragma unroll
+        for (uint32_t w = 0; w < 4; ++w) {
+            const float4 u = staged(row, 64 * n + 32 * half + 8 * w), v = staged(row, 64 * n + 32 * half + 8 * w + 4);
+            uint4 h;
+            part(u.x * inv, u.y * inv, h.x, rest[4 * w]);
+            part(u.z * inv, u.w * inv, h.y, rest[4 * w + 1]);
+            part(v.x * inv, v.y * inv, h.z, rest[4 * w + 2]);
+            part(v.z * inv, v.w * inv, h.w, rest[4 * w + 3]);
+            slab_word(hi + n * BLOCK_BYTES, row, 4 * half + w) = h;
+        }
+        tmem_st16(lo + 32 * n, rest);
+    }
+    if (CTAS > 1) cluster_sync_all();                 // the update has been read: sums may come in its place
+
+    for (uint32_t k = 0; k < p.steps; ++k) {
+        const float a = p.coeffs[k][0], b = p.coeffs[k][1], c = p.coeffs[k][2];
+        product([&] {
+            for (uint32_t n = 0; n < 4 * p.blocks; ++n) {
+                const uint64_t d = desc_k(saddr(hi + n / 4 * BLOCK_BYTES)) + STEP_K * (n % 4);
+                umma(d_square, d, d, idesc(128, 128), n != 0);
+            }
+        });
+        if (CTAS == 1) {
+#pragma unroll
+            for (uint32_t g = 0; g < 2; ++g) {        // columns 64 half + 32 g ..
+                float v[32];
+                tmem_ld32(d_square + lanes + 64 * half + 32 * g, v);
+#pragma unroll
+                for (uint32_t w = 0; w < 4; ++w)
+                    slab_word(gram + half * BLOCK_BYTES, row, 4 * g + w) =
+                        make_uint4(pack_f16(v[8 * w], v[8 * w + 1]), pack_f16(v[8 * w + 2], v[8 * w + 3]),
+                                   pack_f16(v[8 * w + 4], v[8 * w + 5]), pack_f16(v[8 * w + 6], v[8 * w + 7]));
+            }
+        } else {
+            constexpr uint32_t ROWS = 128 / CTAS, SLICE = ROWS * 512, A_SLICE = ROWS * 128;
+#pragma unroll
+            for (uint32_t g = 0; g < 2; ++g) {
+                float v[32];
+                tmem_ld32(d_square + lanes + 64 * half + 32 * g, v);
+#pragma unroll
+                for (uint32_t w = 0; w < 8; ++w)
+                    own[row * 32 + ((16 * half + 8 * g + w) ^ (row & 7))] = make_float4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+            }
+            fence_async();
+            __syncthreads();
+            if (t == 0) {
+                bar_expect_tx(saddr(sums_full), (CTAS - 1) * SLICE);
+                bar_expect_tx(saddr(gram_full), (CTAS - 1) * 2 * A_SLICE);
+            }
+            if (t < CTAS && t != q)
+                push(at_rank(saddr(sums) + q * SLICE, t), saddr(own) + t * SLICE, SLICE, at_rank(saddr(sums_full), t));
+            await(sums_full, k & 1);
+            // the CTA's rows of A, a word of four columns at a time; to be sent from the place of its own
+            // slice, which nobody sends it
+            constexpr uint32_t EACH = ROWS * 32 / RES_THREADS;
+            uint8_t* made = reinterpret_cast<uint8_t*>(sums) + q * SLICE;
+#pragma unroll
+            for (uint32_t n = 0; n < EACH; ++n) {
+                const uint32_t word = n * RES_THREADS + t, r = q * ROWS + word / 32, w = word % 32, at = w ^ (r & 7);
+                float4 from[CTAS];
+#pragma unroll
+                for (uint32_t o = 0; o < CTAS; ++o) from[o] = o == q ? own[r * 32 + at] : sums[(o * ROWS + word / 32) * 32 + at];
+                float4 v = from[0];
+#pragma unroll
+                for (uint32_t o = 1; o < CTAS; ++o) v = make_float4(v.x + from[o].x, v.y + from[o].y, v.z + from[o].z, v.w + from[o].w);
+                const uint2 a16 = make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+                const uint32_t in_block = r * 128 + ((w % 16 / 2 ^ (r & 7)) << 4) + w % 2 * 8;
+                *reinterpret_cast<uint2*>(gram + w / 16 * BLOCK_BYTES + in_block) = a16;
+                *reinterpret_cast<uint2*>(made + w / 16 * A_SLICE + in_block - q * A_SLICE) = a16;
+            }
+            fence_async();
+            __syncthreads();
+            if (t < 2 * CTAS && t / 2 != q)
+                push(at_rank(saddr(gram) + t % 2 * BLOCK_BYTES + q * A_SLICE, t / 2), saddr(made) + t % 2 * A_SLICE, A_SLICE,
+                     at_rank(saddr(gram_full), t / 2));
+            await(gram_full, k & 1);
+        }
+        product([&] {
+            for (uint32_t n = 0; n < 8; ++n) {
+                const uint64_t d = desc_k(saddr(gram + n / 4 * BLOCK_BYTES)) + STEP_K * (n % 4);
+                umma(d_square, d, d, idesc(128, 128), n != 0);
+            }
+        });
+#pragma unroll
+        for (uint32_t g = 0; g < 2; ++g) {
+            float v[32];
+            tmem_ld32(d_square + lanes + 64 * half + 32 * g, v);
+#pragma unroll
+            for (uint32_t w = 0; w < 4; ++w) {
+                uint4& word = slab_word(gram + half * BLOCK_BYTES, row, 4 * g + w);
+                const uint32_t from[4] = {word.x, word.y, word.z, word.w};
+                uint32_t to[4];
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&from[e]));
+                    to[e] = pack_f16(c * v[8 * w + 2 * e] + b * f.x, c * v[8 * w + 2 * e + 1] + b * f.y);
+                }
+                word = make_uint4(to[0], to[1], to[2], to[3]);
+            }
+        }
+        product([&] {
+            for (uint32_t n = 0; n < 8; ++n)
+                umma(d_apply, desc_k(saddr(gram + n / 4 * BLOCK_BYTES)) + STEP_K * (n % 4),
+                     desc_of(saddr(hi), BLOCK_BYTES, 1024) + STEP_MN * n, idesc(128, width) | IDESC_B_MN, n != 0);
+        });
+        const bool last = k + 1 == p.steps;
+        for (uint32_t n = 0; n < p.blocks; ++n) {
+            float v[32];
+            uint32_t rest[16];
+            tmem_ld32(d_apply + lanes + 64 * n + 32 * half, v);
+            tmem_ld16(lo + 32 * n, rest);
+#pragma unroll
+            for (uint32_t w = 0; w < 4; ++w) {
+                uint4& word = slab_word(hi + n * BLOCK_BYTES, row, 4 * half + w);
+                uint32_t h[4] = {word.x, word.y, word.z, word.w};
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    const float2 from = join(h[e], rest[4 * w + e]);
+                    v[8 * w + 2 * e] += a * from.x;
+                    v[8 * w + 2 * e + 1] += a * from.y;
+                    part(v[8 * w + 2 * e], v[8 * w + 2 * e + 1], h[e], rest[4 * w + e]);
+                }
+                word = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            if (!last) tmem_st16(lo + 32 * n, rest);
+            if (last) {
+                Result out = p.out;
+                out.out += (uint64_t)m * p.out_stride;
+                store_result(out, row, l0 + 64 * n + 32 * half, v);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (CTAS > 1) cluster_sync_all();                 // no CTA leaves while a peer may still send to it
+}
+
 // A batch of matrices rows x cols f16, `pitch` elements a row, in boxes of 64 columns (128 bytes,
 // swizzled) by box_rows rows.
 bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t batch, uint64_t pitch,
@@ -1052,9 +1401,10 @@ int check_desc(const char* who, const dtt_ortho_desc* d) {
 }
 
 // Launched so that the next kernel's set-up overlaps this one's end (every kernel waits for the one before
-// it before it touches memory).  cluster: CTAs of a cluster, 0 where the kernel itself says.
+// it before it touches memory), unless `overlap` says otherwise.  cluster: CTAs of a cluster, 0 where the
+// kernel itself says.
 template <class... Params, class... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, cudaStream_t stream,
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, bool overlap, cudaStream_t stream,
                    const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
@@ -1063,7 +1413,7 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, uint32_t threads, uint3
     cfg.stream = stream;
     cudaLaunchAttribute attr[2]{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = overlap;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -1155,6 +1505,13 @@ Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t bat
     return best;
 }
 
+// CTAs of a cluster that hold S x L in shared memory: as few as can (A crosses them all); 0: none can.
+uint32_t resident_ctas(uint64_t S, uint64_t L) {
+    uint32_t ctas = 1;
+    while (ctas < RES_CTAS && ceil_div(L, 64) > ctas * RES_BLOCKS) ctas *= 2;
+    return S <= 128 && ceil_div(L, 64) <= ctas * RES_BLOCKS ? ctas : 0;
+}
+
 template <Product P>
 cudaError_t launch_product(GemmParams& p, const Form& f, uint32_t pairs, cudaStream_t stream) {
     const uint32_t tile_m = f.pair ? 256 : 128;
@@ -1162,10 +1519,10 @@ cudaError_t launch_product(GemmParams& p, const Form& f, uint32_t pairs, cudaStr
     p.tiles_m = ceil_div(p.S, tile_m);
     p.tiles = tiles_of(P != APPLY, tile_m, f.tn, p.S, p.L);
     const uint32_t places = p.tiles * p.batch;
-    if (f.pair) return launch(ortho_pair_kernel<P>, 2 * std::min(places, pairs), THREADS, SMEM_BYTES, 0, stream, p);
+    if (f.pair) return launch(ortho_pair_kernel<P>, 2 * std::min(places, pairs), THREADS, SMEM_BYTES, 0, true, stream, p);
     auto kernel = f.ctas == 1 ? ortho_split_kernel<P, 1> : f.ctas == 2 ? ortho_split_kernel<P, 2>
                 : f.ctas == 4 ? ortho_split_kernel<P, 4> : ortho_split_kernel<P, 8>;
-    return launch(kernel, places * f.ctas, THREADS, SMEM_BYTES, f.ctas, stream, p);
+    return launch(kernel, places * f.ctas, THREADS, SMEM_BYTES, f.ctas, true, stream, p);
 }
 
 template <Product P>
@@ -1186,6 +1543,12 @@ cudaError_t preload_ortho_kernels() {
     cudaError_t e = prepare_product<GRAM>();
     if (e == cudaSuccess) e = prepare_product<POLY>();
     if (e == cudaSuccess) e = prepare_product<APPLY>();
+    for (auto kernel : {ortho_resident_kernel<1>, ortho_resident_kernel<2>, ortho_resident_kernel<4>, ortho_resident_kernel<8>,
+                        ortho_resident_kernel<16>}) {
+        if (e == cudaSuccess) e = prepare_kernel(kernel);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RES_SMEM);
+    }
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ortho_resident_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<true>);
     if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<false>);
     if (e == cudaSuccess) e = prepare_kernel(ortho_start_kernel);
@@ -1207,6 +1570,7 @@ struct dtt_ortho {
     CUtensorMap hi_rows[2], lo_rows, gram, poly;
     // boxes of 64 x 64: the N-contiguous operand of the last product, and mirrored blocks
     CUtensorMap hi_cols[2], gram_blocks, poly_blocks;
+    uint32_t resident;           // CTAs of a cluster in the resident form; 0: a launch a product
     Fit fit;
     Form form[3];                // of each Product
 };
@@ -1239,6 +1603,7 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     o->l = l;
     o->ws = static_cast<char*>(workspace);
     o->sms = (uint32_t)sms;
+    o->resident = resident_ctas(l.S, l.L);
     o->fit = fit_of(dev, o->sms);
     o->form[GRAM] = form_of(true, l.S, l.S, l.L, d->batch, o->fit);
     o->form[POLY] = form_of(true, l.S, l.S, l.S, d->batch, o->fit);
@@ -1303,11 +1668,27 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     up.l_pitch = l.l_pitch;
     up.S = (uint32_t)l.S;
     const bool tall = d.rows > d.cols;
+    const bool out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_pitch % 16 == 0 && (d.batch == 1 || out_stride % 16 == 0);
     bool vec = d.cols % 8 == 0;
     for (const auto& a : args)
         if (a.p != out && a.p) vec = vec && reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.pitch % 16 == 0 && a.stride % 16 == 0;
     const uint64_t items = d.rows * (vec ? d.cols / 8 : d.cols);
     up.parts = (uint32_t)std::min<uint64_t>((items + 1023) / 1024, std::max(kMaxParts / d.batch, 1u));
+    if (o->resident) {
+        ResidentParams r{};
+        r.u = up;
+        r.out = {static_cast<char*>(out), out_pitch, (uint32_t)l.S, (uint32_t)l.L, d.scale, tall, out_vec};
+        r.out_stride = out_stride;
+        r.blocks = ceil_div(ceil_div(l.L, 64), o->resident);
+        r.vec = vec;
+        r.steps = d.steps;
+        r.err = err;
+        std::copy(&d.coeffs[0][0], &d.coeffs[0][0] + 3 * d.steps, &r.coeffs[0][0]);
+        auto kernel = o->resident == 1 ? ortho_resident_kernel<1> : o->resident == 2 ? ortho_resident_kernel<2>
+                    : o->resident == 4 ? ortho_resident_kernel<4> : o->resident == 8 ? ortho_resident_kernel<8> : ortho_resident_kernel<16>;
+        DTT_CUDA_TRY(launch(kernel, d.batch * o->resident, RES_THREADS, RES_SMEM, o->resident, false, stream, r));
+        return DTT_OK;
+    }
     const dim3 parts(up.parts, d.batch);
     // not overlapped with what ran before: it may write the update that this reads
     if (vec) ortho_update_kernel<true><<<parts, 256, 0, stream>>>(up);
@@ -1315,10 +1696,10 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     DTT_CUDA_TRY(cudaGetLastError());
     if (vec && !tall) {
         const uint32_t ctas = (uint32_t)std::min<uint64_t>((items + 511) / 512, std::max(8 * o->sms / d.batch, 1u));
-        DTT_CUDA_TRY(launch(ortho_start_kernel, dim3(ctas, d.batch), 256, 0, 0, stream, up));
+        DTT_CUDA_TRY(launch(ortho_start_kernel, dim3(ctas, d.batch), 256, 0, 0, true, stream, up));
     } else {
         const dim3 tiles(ceil_div(up.cols, kStartTile), ceil_div(up.rows, kStartTile), d.batch);
-        DTT_CUDA_TRY(launch(tall ? ortho_start_tiles_kernel<true> : ortho_start_tiles_kernel<false>, tiles, 256, 0, 0, stream, up));
+        DTT_CUDA_TRY(launch(tall ? ortho_start_tiles_kernel<true> : ortho_start_tiles_kernel<false>, tiles, 256, 0, 0, true, stream, up));
     }
 
     GemmParams g{};
@@ -1330,7 +1711,7 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     g.err = err;
     g.scale = d.scale;
     g.transposed = tall;
-    g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_pitch % 16 == 0 && (d.batch == 1 || out_stride % 16 == 0);
+    g.out_vec = out_vec;
     g.out_pitch = out_pitch;
     g.out_stride = out_stride;
     for (uint32_t k = 0; k < d.steps; ++k) {
