@@ -275,14 +275,20 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsn
 }
 
 // ---- elements ----------------------------------------------------------------------------------
-// Columns t, t + T, ... (E of them, those below `cols`) of a row.
+// Columns t, t + T, ... (E of them; zeros from `cols` on) of a row.
 template <uint32_t E>
 __device__ __forceinline__ void load_elements(const char* row, uint32_t dt, uint32_t cols, float (&v)[E]) {
+    const char* rows[E];
+    uint32_t c[E];
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) {
-        const uint32_t c = k * blockDim.x + threadIdx.x;
-        v[k] = c < cols ? load1(row, dt, c) : 0.0f;
+        rows[k] = row;
+        c[k] = min(k * blockDim.x + threadIdx.x, cols - 1);
     }
+    gather(rows, dt, c, v);
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k)
+        if (k * blockDim.x + threadIdx.x >= cols) v[k] = 0.0f;
 }
 
 // One row a CTA.  A group of columns is one, two or four neighbours of the row's segments of 32

@@ -858,28 +858,55 @@ __global__ void __launch_bounds__(256) ortho_update_kernel(const __grid_constant
     const char* x = p.x + (uint64_t)m * p.x_stride;
     char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
     const uint64_t total = (uint64_t)p.rows * per_row;
+    const uint64_t step = (uint64_t)p.parts * 256;
     float sum = 0.0f;
     launch_next();
-#pragma unroll 4
-    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (uint64_t)p.parts * 256) {
-        const uint32_t r = (uint32_t)(i / per_row), c = (uint32_t)(i - (uint64_t)r * per_row) * W;
-        float u[8], v[8];
-        if (VEC) load8<true>(x + r * p.x_pitch, p.x_dt, c, p.cols, u);
-        else u[0] = load1(x + r * p.x_pitch, p.x_dt, c);
-        if (mom) {
-            char* row = mom + r * p.mom_pitch;
-            if (VEC) load8<true>(row, DTT_F32, c, p.cols, v);
-            else v[0] = load1(row, DTT_F32, c);
+    constexpr uint32_t N = VEC ? 4 : 8;                // under way at a time
+    for (uint64_t i0 = (uint64_t)blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += N * step) {
+        float u[N][W], v[N][W];
+        const char *xs[N], *moms[N];
+        uint32_t cs[N];
 #pragma unroll
-            for (uint32_t k = 0; k < W; ++k) {
-                v[k] = p.mu * v[k] + u[k];
-                u[k] = p.nesterov ? u[k] + p.mu * v[k] : v[k];
+        for (uint32_t n = 0; n < N; ++n) {
+            const uint64_t i = min(i0 + n * step, total - 1);
+            const uint32_t r = (uint32_t)(i / per_row);
+            cs[n] = (uint32_t)(i - (uint64_t)r * per_row) * W;
+            xs[n] = x + r * p.x_pitch;
+            moms[n] = mom + r * p.mom_pitch;
+        }
+        if constexpr (VEC) {
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n) load8<true>(xs[n], p.x_dt, cs[n], p.cols, u[n]);
+            if (mom) {
+#pragma unroll
+                for (uint32_t n = 0; n < N; ++n) load8<true>(moms[n], DTT_F32, cs[n], p.cols, v[n]);
             }
-            if (VEC) store8<true>(row, DTT_F32, c, p.cols, v);
-            else store1(row, DTT_F32, c, v[0]);
+        } else {
+            float a[N], b[N];
+            gather(xs, p.x_dt, cs, a);
+            if (mom) gather(moms, DTT_F32, cs, b);
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n) {
+                u[n][0] = a[n];
+                v[n][0] = b[n];
+            }
         }
 #pragma unroll
-        for (uint32_t k = 0; k < W; ++k) sum += u[k] * u[k];
+        for (uint32_t n = 0; n < N; ++n) {
+            if (i0 + n * step >= total) break;
+            if (mom) {
+                char* row = const_cast<char*>(moms[n]);
+#pragma unroll
+                for (uint32_t k = 0; k < W; ++k) {
+                    v[n][k] = p.mu * v[n][k] + u[n][k];
+                    u[n][k] = p.nesterov ? u[n][k] + p.mu * v[n][k] : v[n][k];
+                }
+                if constexpr (VEC) store8<true>(row, DTT_F32, cs[n], p.cols, v[n]);
+                else store1(row, DTT_F32, cs[n], v[n][0]);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < W; ++k) sum += u[n][k] * u[n][k];
+        }
     }
     sum = cta_sum(sum, slot);
     if (threadIdx.x == 0) p.sums[(uint64_t)m * p.parts + blockIdx.x] = sum;
@@ -944,22 +971,24 @@ __global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_con
     const uint32_t r0 = blockIdx.y * kStartTile, c0 = blockIdx.x * kStartTile;
     const char* x = p.x + (uint64_t)m * p.x_stride;
     const char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
-    float u[kStartTile / 8][2];
+    constexpr uint32_t N = kStartTile / 4;             // elements a thread: rows warp + 8 (n / 2), columns lane + 32 (n % 2)
+    float u[N], v[N];
+    const char *xs[N], *moms[N];
+    uint32_t cs[N];
     wait_previous();
 #pragma unroll
-    for (uint32_t k = 0; k < kStartTile / 8; ++k)
+    for (uint32_t n = 0; n < N; ++n) {
+        const uint32_t r = min(r0 + warp + 8 * (n / 2), p.rows - 1);
+        cs[n] = min(c0 + lane + 32 * (n % 2), p.cols - 1);
+        xs[n] = x + r * p.x_pitch;
+        moms[n] = mom + r * p.mom_pitch;
+    }
+    if (!mom || p.nesterov) gather(xs, p.x_dt, cs, u);
+    if (mom) {
+        gather(moms, DTT_F32, cs, v);
 #pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-            const uint32_t r = r0 + warp + 8 * k, c = c0 + lane + 32 * h;
-            u[k][h] = 0.0f;
-            if (r < p.rows && c < p.cols) {
-                if (!mom || p.nesterov) u[k][h] = load1(x + r * p.x_pitch, p.x_dt, c);
-                if (mom) {
-                    const float v = load1(mom + r * p.mom_pitch, DTT_F32, c);
-                    u[k][h] = p.nesterov ? u[k][h] + p.mu * v : v;
-                }
-            }
-        }
+        for (uint32_t n = 0; n < N; ++n) u[n] = p.nesterov ? u[n] + p.mu * v[n] : v[n];
+    }
     const float inv = inverse_norm(p, m, slot);
     __half* hi = p.hi + (uint64_t)m * p.S * p.l_pitch;
     __half* lo = p.lo + (uint64_t)m * p.S * p.l_pitch;
@@ -967,7 +996,7 @@ __global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_con
 #pragma unroll
         for (uint32_t k = 0; k < kStartTile / 8; ++k)
 #pragma unroll
-            for (uint32_t h = 0; h < 2; ++h) tile[warp + 8 * k][lane + 32 * h] = u[k][h];
+            for (uint32_t h = 0; h < 2; ++h) tile[warp + 8 * k][lane + 32 * h] = u[2 * k + h];
         __syncthreads();
     }
 #pragma unroll
@@ -977,7 +1006,7 @@ __global__ void __launch_bounds__(256) ortho_start_tiles_kernel(const __grid_con
             const uint32_t a = warp + 8 * k, b = lane + 32 * h;      // TALL: column a, row b of the tile
             const uint32_t r = r0 + (TALL ? b : a), c = c0 + (TALL ? a : b);
             if (r < p.rows && c < p.cols) {
-                const float v = (TALL ? tile[b][a] : u[k][h]) * inv;
+                const float v = (TALL ? tile[b][a] : u[2 * k + h]) * inv;
                 const uint64_t at = TALL ? c * p.l_pitch + r : r * p.l_pitch + c;
                 uint32_t a, b;
                 part(v, 0.0f, a, b);
@@ -1032,7 +1061,7 @@ __device__ __forceinline__ float load_peer1(uint32_t cluster_addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // S <= 128: one cluster of CTAS a matrix, from the update to the result: hi stays in shared memory, lo in
 // TMEM.  CTA q holds columns 64 blocks q .. of X; a block of 64 columns by 128 rows serves as it lies
@@ -1125,14 +1154,24 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
         const uint32_t per_row = (tall ? 128 : width) / 32, total = 4 * width;     // a multiple of 8 N / 4
         for (uint32_t e0 = warp; e0 < total; e0 += N * (RES_THREADS / 32)) {
             float u[N], v[N];
+            const char *xs[N], *moms[N];
+            uint32_t cs[N], inside = 0;
 #pragma unroll
             for (uint32_t n = 0; n < N; ++n) {
                 const uint32_t e = e0 + n * (RES_THREADS / 32), r = e / per_row, c = 32 * (e - r * per_row) + lane;
                 const uint32_t gr = tall ? l0 + r : r, gc = tall ? c : l0 + c;
                 const bool in = e < total && gr < p.u.rows && gc < p.u.cols;
-                u[n] = in ? load1(x + gr * p.u.x_pitch, p.u.x_dt, gc) : 0.0f;
-                v[n] = in && mom ? load1(mom + gr * p.u.mom_pitch, DTT_F32, gc) : 0.0f;
+                inside |= (uint32_t)in << n;
+                cs[n] = in ? gc : 0;
+                xs[n] = x + (in ? gr : 0) * p.u.x_pitch;
+                moms[n] = mom + (in ? gr : 0) * p.u.mom_pitch;
+                v[n] = 0.0f;
             }
+            gather(xs, p.u.x_dt, cs, u);
+            if (mom) gather(moms, DTT_F32, cs, v);
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n)
+                if (!(inside >> n & 1)) u[n] = v[n] = 0.0f;
 #pragma unroll
             for (uint32_t n = 0; n < N; ++n) {
                 const uint32_t e = e0 + n * (RES_THREADS / 32), r = e / per_row, c = 32 * (e - r * per_row) + lane;

@@ -113,4 +113,20 @@ __device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// N elements at rows[n], column c[n], as f32.  The loads go out together: they are unconditional and the
+// type is decided once, since a load behind a branch of its own waits for the one before it.
+template <uint32_t N>
+__device__ __forceinline__ void gather(const char* const (&rows)[N], uint32_t dt, const uint32_t (&c)[N], float (&v)[N]) {
+    if (dt == DTT_BF16) {
+        uint16_t raw[N];
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) raw[n] = reinterpret_cast<const uint16_t*>(rows[n])[c[n]];
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) v[n] = __uint_as_float((uint32_t)raw[n] << 16);
+    } else {
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) v[n] = reinterpret_cast<const float*>(rows[n])[c[n]];
+    }
+}
+
 }  // namespace dtt
