@@ -5,10 +5,10 @@
 //    threads in chunks of 8 columns: thread t holds columns 8 (i TPR + t) .. + 7 of chunk i, so a
 //    warp's accesses are contiguous, a thread moves 16 bytes of bf16 or 32 of f32 at a time, and a
 //    group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes of one warp;
-//  - ring (many aligned rows): the same layout by persistent CTAs whose rows come through a ring of
-//    shared-memory stages, bulk copies running ahead of the arithmetic;
-//  - elements (rows that are not 16-byte aligned, or no whole number of chunks): thread t holds columns t, t + TPR, ..., so that
-//    accesses of single elements are contiguous over a warp.
+//  - elements (few rows that are not 16-byte aligned, or no whole number of chunks): thread t holds
+//    columns t, t + TPR, ..., so that accesses of single elements are contiguous over a warp;
+//  - ring (many rows, either layout): persistent CTAs whose rows come through a ring of shared-memory
+//    stages, bulk copies running ahead of the arithmetic.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -291,13 +291,56 @@ __device__ __forceinline__ void load_elements(const char* row, uint32_t dt, uint
         if (k * blockDim.x + threadIdx.x >= cols) v[k] = 0.0f;
 }
 
-// One row a CTA.  A group of columns is one, two or four neighbours of the row's segments of 32
-// columns (segment k T / 32 + warp), whose maxima meet in shared memory.
+template <uint32_t E>
+__device__ __forceinline__ void store_elements(char* row, uint32_t dt, uint32_t cols, const float (&v)[E]) {
+    const uint32_t T = blockDim.x, t = threadIdx.x;
+    if (dt == DTT_BF16) {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (k * T + t < cols) reinterpret_cast<uint16_t*>(row)[k * T + t] = (uint16_t)pack_bf16(v[k], 0.0f);
+    } else if (dt == DTT_F32) {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (k * T + t < cols) reinterpret_cast<float*>(row)[k * T + t] = v[k];
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (k * T + t < cols) reinterpret_cast<uint8_t*>(row)[k * T + t] = (uint8_t)pack_e4m3(v[k], 0.0f);
+    }
+}
+
+// The scales of row r's groups, and h divided by them.  A group is one, two or four neighbours of the row's
+// segments of 32 columns (segment k T / 32 + warp), whose maxima meet in shared memory.
+template <uint32_t E>
+__device__ __forceinline__ void scale_groups(const FwdParams& p, uint64_t r, float* segment, float (&h)[E]) {
+    const uint32_t T = blockDim.x, t = threadIdx.x, warps = T / 32;
+    __syncthreads();                                          // the last row's have been read
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) {
+        float m = fabsf(h[k]);
+#pragma unroll
+        for (uint32_t d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        if (t % 32 == 0) segment[k * warps + t / 32] = m;
+    }
+    __syncthreads();
+    const uint32_t per = p.group_lanes / 4;                   // segments a group
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) {
+        const uint32_t q = k * warps + t / 32, q0 = q / per * per;
+        float m = 0.0f;
+        for (uint32_t i = q0; i < q0 + per && i < E * warps; ++i) m = max_nan(m, segment[i]);
+        const float scale = max_nan(m / kE4m3Max, kScaleMin);
+        if (t % 32 == 0 && q == q0 && q * 32 < p.cols) p.scales[r * p.groups + q / per] = scale;
+        h[k] *= 1.0f / scale;
+    }
+}
+
+// One row a CTA.
 template <uint32_t E>
 __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const __grid_constant__ FwdParams p) {
     __shared__ float slots[2][32];
     __shared__ float segment[E * kFwdThreads / 32];
-    const uint32_t T = blockDim.x, t = threadIdx.x, warps = T / 32;
+    const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint64_t r = blockIdx.x;
     const char* x = p.x + r * p.x_pitch;
     char* y = p.y + r * p.y_pitch;
@@ -314,12 +357,7 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const
     for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
     const float s = rsqrtf(row_reduce(sum, T, slots[0], Sum()) * p.inv_cols + p.eps);
     if (t == 0 && p.rstd) p.rstd[r] = s;
-    if (p.res_out) {
-        char* res_out = p.res_out + r * p.res_out_pitch;
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k)
-            if (k * T + t < p.cols) store1(res_out, p.res_dt, k * T + t, h[k]);
-    }
+    if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) h[k] = p.w ? h[k] * s * o[k] : h[k] * s;
     if (p.y_dt == DTT_E4M3 && p.group_lanes == 0) {
@@ -332,28 +370,9 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) h[k] *= inv;
     } else if (p.y_dt == DTT_E4M3) {
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k) {
-            float m = fabsf(h[k]);
-#pragma unroll
-            for (uint32_t d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            if (t % 32 == 0) segment[k * warps + t / 32] = m;
-        }
-        __syncthreads();
-        const uint32_t per = p.group_lanes / 4;               // segments a group
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k) {
-            const uint32_t q = k * warps + t / 32, q0 = q / per * per;
-            float m = 0.0f;
-            for (uint32_t i = q0; i < q0 + per && i < E * warps; ++i) m = max_nan(m, segment[i]);
-            const float scale = max_nan(m / kE4m3Max, kScaleMin);
-            if (t % 32 == 0 && q == q0 && q * 32 < p.cols) p.scales[r * p.groups + q / per] = scale;
-            h[k] *= 1.0f / scale;
-        }
+        scale_groups(p, r, segment, h);
     }
-#pragma unroll
-    for (uint32_t k = 0; k < E; ++k)
-        if (k * T + t < p.cols) store1(y, p.y_dt, k * T + t, h[k]);
+    store_elements(y, p.y_dt, p.cols, h);
 }
 
 // As the chunk form: rows blockIdx.x, + partials, ..., the weight's gradient in registers.
@@ -384,20 +403,14 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const
             dot += g[k] * n[k];
         }
         const float m = row_reduce(dot, T, slots[turn], Sum()) * p.inv_cols;
-        char* dx = p.dx + r * p.dx_pitch;
 #pragma unroll
-        for (uint32_t k = 0; k < E; ++k)
-            if (k * T + t < p.cols) {
-                const float v = s * (g[k] - n[k] * m);
-                store1(dx, p.h_dt, k * T + t, p.dres ? v + q[k] : v);
-            }
+        for (uint32_t k = 0; k < E; ++k) {
+            g[k] = s * (g[k] - n[k] * m);
+            if (p.dres) g[k] += q[k];
+        }
+        store_elements(p.dx + r * p.dx_pitch, p.h_dt, p.cols, g);
     }
-    if (p.partial) {
-        float* part = p.partial + (uint64_t)blockIdx.x * p.cols;
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k)
-            if (k * T + t < p.cols) part[k * T + t] = acc[k];
-    }
+    if (p.partial) store_elements(reinterpret_cast<char*>(p.partial + (uint64_t)blockIdx.x * p.cols), DTT_F32, p.cols, acc);
 }
 
 // ---- ring --------------------------------------------------------------------------------------
@@ -614,6 +627,166 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __
     }
 }
 
+// ---- ring of unaligned rows --------------------------------------------------------------------
+// The ring for rows at any alignment, a thread's columns t, t + T, ...  A bulk copy moves whole 16-byte
+// words: from the one that holds the row's first byte to the one that holds its last.  The few bytes
+// beside the row in these two are copied with it and not looked at (an allocation never ends within
+// such a word).
+struct Words {
+    uint64_t from;              // address of the first word
+    uint32_t skip, bytes;       // the row's first byte in it; bytes of all words
+};
+
+__device__ __forceinline__ Words words_of(const char* row, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(row), first = a & ~15ull;
+    const uint32_t skip = (uint32_t)(a - first);
+    return {first, skip, (skip + bytes + 15) & ~15u};
+}
+
+__host__ __device__ __forceinline__ uint32_t words_room(uint32_t bytes) { return (bytes + 30) & ~15u; }
+
+template <uint32_t E>
+__global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+    extern __shared__ __align__(128) uint8_t stages[];
+    __shared__ float slots[2][2][32];
+    __shared__ float segment[E * kRingThreads / 32];
+    __shared__ uint64_t full[kRingStages];
+    const uint32_t T = blockDim.x, t = threadIdx.x, warps = T / 32;
+    const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
+    const uint32_t x_room = words_room(xb), stage_bytes = x_room + (rb ? words_room(rb) : 0);
+    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    auto start = [&](uint64_t i) {
+        const uint64_t r = blockIdx.x + i * gridDim.x;
+        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+        const Words x = words_of(p.x + r * p.x_pitch, xb);
+        Words res{0, 0, 0};
+        if (rb) res = words_of(p.res + r * p.res_pitch, rb);
+        bar_expect_tx(bar, x.bytes + res.bytes);
+        bulk_load(dst, reinterpret_cast<const char*>(x.from), x.bytes, bar);
+        if (rb) bulk_load(dst + x_room, reinterpret_cast<const char*>(res.from), res.bytes, bar);
+    };
+    if (t == 0) {
+        for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+    }
+    float w[E];
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) w[k] = 1.0f;
+    if (p.w) load_elements(p.w, p.w_dt, p.cols, w);
+    __syncthreads();
+
+    uint32_t st = 0, phase = 0;
+    for (uint64_t turn = 0; turn < turns; ++turn) {
+        const uint64_t r = blockIdx.x + turn * gridDim.x;
+        const bool here = bar_wait(saddr(full + st), phase);
+        const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
+        float h[E], sum = 0.0f;
+        load_elements(row + words_of(p.x + r * p.x_pitch, xb).skip, p.x_dt, p.cols, h);
+        if (rb) {
+            float q[E];
+            load_elements(row + x_room + words_of(p.res + r * p.res_pitch, rb).skip, p.res_dt, p.cols, q);
+#pragma unroll
+            for (uint32_t k = 0; k < E; ++k) h[k] += q[k];
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
+        if (!here) sum = __int_as_float(0x7FC00000);
+        const float s = rsqrtf(row_reduce(sum, T, slots[turn & 1][0], Sum()) * p.inv_cols + p.eps);
+        if (T == 32) __syncwarp();
+        if (t == 0) {
+            if (turn + S - 1 < turns) start(turn + S - 1);
+            if (p.rstd) p.rstd[r] = s;
+        }
+        if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) h[k] *= s * w[k];
+        if (p.y_dt == DTT_E4M3 && p.group_lanes == 0) {
+            float m = 0.0f;
+#pragma unroll
+            for (uint32_t k = 0; k < E; ++k) m = max_nan(m, fabsf(h[k]));
+            const float scale = max_nan(row_reduce(m, T, slots[turn & 1][1], MaxNan()) / kE4m3Max, kScaleMin);
+            if (t == 0) p.scales[r] = scale;
+            const float inv = 1.0f / scale;
+#pragma unroll
+            for (uint32_t k = 0; k < E; ++k) h[k] *= inv;
+        } else if (p.y_dt == DTT_E4M3) {
+            scale_groups(p, r, segment, h);
+        }
+        store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
+        if (++st == S) { st = 0; phase ^= 1; }
+    }
+}
+
+template <uint32_t E>
+__global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+    extern __shared__ __align__(128) uint8_t stages[];
+    __shared__ float slots[2][32];
+    __shared__ uint64_t full[kRingStages];
+    const uint32_t T = blockDim.x, t = threadIdx.x;
+    const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
+    const uint32_t g_room = words_room(gb), h_room = words_room(hb), stage_bytes = g_room + (p.dres ? 2 : 1) * h_room;
+    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    auto start = [&](uint64_t i) {
+        const uint64_t r = blockIdx.x + i * gridDim.x;
+        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+        const Words g = words_of(p.dy + r * p.dy_pitch, gb), h = words_of(p.h + r * p.h_pitch, hb);
+        Words d{0, 0, 0};
+        if (p.dres) d = words_of(p.dres + r * p.dres_pitch, hb);
+        bar_expect_tx(bar, g.bytes + h.bytes + d.bytes);
+        bulk_load(dst, reinterpret_cast<const char*>(g.from), g.bytes, bar);
+        bulk_load(dst + g_room, reinterpret_cast<const char*>(h.from), h.bytes, bar);
+        if (p.dres) bulk_load(dst + g_room + h_room, reinterpret_cast<const char*>(d.from), d.bytes, bar);
+    };
+    if (t == 0) {
+        for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+    }
+    float w[E], acc[E];
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) {
+        w[k] = 1.0f;
+        acc[k] = 0.0f;
+    }
+    if (p.w) load_elements(p.w, p.w_dt, p.cols, w);
+    __syncthreads();
+
+    uint32_t st = 0, phase = 0;
+    for (uint64_t turn = 0; turn < turns; ++turn) {
+        const uint64_t r = blockIdx.x + turn * gridDim.x;
+        const float s = p.rstd[r];
+        const bool here = bar_wait(saddr(full + st), phase);
+        const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
+        float g[E], n[E], dot = 0.0f;
+        load_elements(row + words_of(p.dy + r * p.dy_pitch, gb).skip, p.dy_dt, p.cols, g);
+        load_elements(row + g_room + words_of(p.h + r * p.h_pitch, hb).skip, p.h_dt, p.cols, n);
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) {
+            n[k] *= s;
+            acc[k] += g[k] * n[k];
+            g[k] *= w[k];
+            dot += g[k] * n[k];
+        }
+        if (!here) dot = __int_as_float(0x7FC00000);
+        const float m = row_reduce(dot, T, slots[turn & 1], Sum()) * p.inv_cols;
+        if (T == 32) __syncwarp();
+        if (t == 0 && turn + S - 1 < turns) start(turn + S - 1);
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) g[k] = s * (g[k] - n[k] * m);
+        if (p.dres) {
+            load_elements(row + g_room + h_room + words_of(p.dres + r * p.dres_pitch, hb).skip, p.h_dt, p.cols, n);
+#pragma unroll
+            for (uint32_t k = 0; k < E; ++k) g[k] += n[k];
+        }
+        store_elements(p.dx + r * p.dx_pitch, p.h_dt, p.cols, g);
+        if (++st == S) { st = 0; phase ^= 1; }
+    }
+    if (p.partial) store_elements(reinterpret_cast<char*>(p.partial + (uint64_t)blockIdx.x * p.cols), DTT_F32, p.cols, acc);
+}
+
 // dweight[c] = the partial rows' sum.  32 columns a CTA; its 8 warps take every eighth partial row,
 // and their sums are added in warp order.
 __global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* partial, uint32_t partials,
@@ -653,19 +826,21 @@ struct Ring {
     uint32_t nch, threads, ctas, stages, smem;       // ctas: of an SM; 0: no ring for these rows
 };
 
-// Two chunks a thread up to 512 threads, then four (twice the registers).  As many CTAs as make
-// `threads_per_sm` threads an SM (half as many with four chunks), fewer where three stages each would
-// not fit; then as many stages as fit.
-Ring ring_of(uint32_t cols, uint32_t stage_bytes, uint32_t threads_per_sm) {
-    const uint32_t chunks = cols / 8;
+// Chunks (vec): two a thread up to 512 threads, then four (twice the registers); one warp a row is left to
+// the chunk form.  Elements: 8 a thread up to 256 threads, then 16.  As many CTAs as make `threads_per_sm`
+// threads an SM (half as many with four chunks), fewer where three stages each would not fit; then as
+// many stages as fit.
+Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t threads_per_sm) {
     Ring g{};
-    for (uint32_t nch : {2u, 4u}) {
+    if (3 * stage > kRingSmem) return g;
+    const uint32_t stage_bytes = (uint32_t)stage;
+    for (uint32_t nch : {vec ? 2u : 1u, vec ? 4u : 2u}) {
         g.nch = nch;
-        g.threads = ((chunks + nch - 1) / nch + 31) / 32 * 32;
-        if (g.threads <= kRingThreads) break;
+        g.threads = ((cols + 8 * nch - 1) / (8 * nch) + 31) / 32 * 32;
+        if (g.threads <= (nch == 1 ? 256 : kRingThreads)) break;
     }
-    if (g.threads < 64 || g.threads > kRingThreads || 3 * stage_bytes > kRingSmem) return {};
-    g.ctas = std::min(std::max(threads_per_sm * 2 / g.nch / g.threads, 1u), kRingSmem / (3 * stage_bytes));
+    if ((vec && g.threads < 64) || g.threads > kRingThreads) return {};
+    g.ctas = std::min(std::min(std::max(threads_per_sm * 2 / std::max(g.nch, 2u) / g.threads, 1u), kRingSmem / (3 * stage_bytes)), 16u);
     g.stages = std::min(kRingStages, kRingSmem / (g.ctas * stage_bytes));
     g.smem = g.stages * stage_bytes;
     return g;
@@ -687,11 +862,13 @@ uint32_t element_threads(uint32_t cols, uint32_t E, uint32_t threads) {
 void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t xe = p.x_dt == DTT_BF16 ? 2 : 4, re = p.res ? (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t sms = sm_count();
-    const Ring g = vec ? ring_of(p.cols, (uint32_t)std::min<uint64_t>((uint64_t)p.cols * (xe + re), kRingSmem), 1024) : Ring{};
+    const uint64_t xb = (uint64_t)p.cols * xe, rb = (uint64_t)p.cols * re;
+    const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, 1024);
     if (g.ctas && p.rows >= 2 * sms) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
-        if (g.nch == 2) rmsnorm_fwd_ring_kernel<2><<<grid, g.threads, g.smem, stream>>>(p, g.stages);
-        else rmsnorm_fwd_ring_kernel<4><<<grid, g.threads, g.smem, stream>>>(p, g.stages);
+        auto kernel = vec ? (g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
+                          : (g.nch == 1 ? rmsnorm_fwd_ring_elements_kernel<8> : rmsnorm_fwd_ring_elements_kernel<16>);
+        kernel<<<grid, g.threads, g.smem, stream>>>(p, g.stages);
         return;
     }
     if (!vec) {
@@ -719,12 +896,13 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
 void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
     const uint32_t sms = sm_count();
-    const Ring g = vec ? ring_of(p.cols, (uint32_t)std::min<uint64_t>((uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he), kRingSmem), 512)
-                       : Ring{};
+    const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
+    const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 512);
     if (g.ctas && p.rows >= 2 * sms) {
         p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)kMaxPartials});
-        if (g.nch == 2) rmsnorm_bwd_ring_kernel<2><<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
-        else rmsnorm_bwd_ring_kernel<4><<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
+        auto kernel = vec ? (g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
+                          : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
+        kernel<<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
         return;
     }
     p.partials = (uint32_t)std::min<uint64_t>(p.rows, kMaxPartials);
@@ -803,7 +981,9 @@ cudaError_t preload_norm_kernels() {
         if (e != cudaSuccess) return e;
     }
     const void* rings[] = {(const void*)rmsnorm_fwd_ring_kernel<2>, (const void*)rmsnorm_fwd_ring_kernel<4>,
-                           (const void*)rmsnorm_bwd_ring_kernel<2>, (const void*)rmsnorm_bwd_ring_kernel<4>};
+                           (const void*)rmsnorm_bwd_ring_kernel<2>, (const void*)rmsnorm_bwd_ring_kernel<4>,
+                           (const void*)rmsnorm_fwd_ring_elements_kernel<8>, (const void*)rmsnorm_fwd_ring_elements_kernel<16>,
+                           (const void*)rmsnorm_bwd_ring_elements_kernel<8>, (const void*)rmsnorm_bwd_ring_elements_kernel<16>};
     for (const void* k : rings) {
         cudaError_t e = prepare(k);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmem);

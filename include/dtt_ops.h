@@ -9,7 +9,8 @@
  * it to one stream at a time, or orders the streams).  Every call is asynchronous on `stream`, makes
  * no device-wide synchronisation and can be captured into a CUDA graph once dtt_preload has run.
  * A tensor is rows of contiguous elements, `pitch` bytes apart, at any alignment its element type
- * allows; rows that are 16-byte aligned throughout take the faster paths.
+ * allows; rows that are 16-byte aligned throughout take the faster paths.  Inputs may be read in whole
+ * aligned 16-byte words (no allocation ends within one); outputs are written exactly.
  */
 #ifndef DTT_OPS_H
 #define DTT_OPS_H
