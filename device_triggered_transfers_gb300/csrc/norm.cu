@@ -27,6 +27,8 @@ constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   
 constexpr uint32_t kRingStages = 8;        // of a CTA, at most
 constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
 constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kFwdWarpCols = 1024, kBwdWarpCols = 512;   // columns of rows that one warp takes, at most
+constexpr uint32_t kWarpRows = 8;          // rows of a CTA whose rows are one warp each
 constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
 
 struct FwdParams {
@@ -55,34 +57,39 @@ struct BwdParams {
     float* partial;             // [partials][cols], or null: no weight gradient
     uint64_t dy_pitch, h_pitch, dres_pitch, dx_pitch;
     uint64_t rows;
-    uint32_t cols, partials;
+    uint32_t cols, partials, walkers;   // walker i takes rows i, i + walkers, ...
     uint32_t dy_dt, h_dt, w_dt;
     float inv_cols;
 };
 
-struct Sum {
-    __device__ float operator()(float a, float b) const { return a + b; }
-};
-struct MaxNan {
-    __device__ float operator()(float a, float b) const { return max_nan(a, b); }
-};
-
-// Over the TPR threads of a row, the same bits in each.  One warp: butterfly shuffles.  More: the
-// warps' values through shared memory (`slot`: 32 floats used by this reduction alone between two
-// of the row's barriers).
-template <class Op>
-__device__ __forceinline__ float row_reduce(float v, uint32_t tpr, float* slot, Op op) {
+// Over the TPR threads of a row, the same bits in each.  One warp: butterfly shuffles.  More: the warps'
+// values through shared memory (`slot`: 32 words used by this reduction alone between two of the row's
+// barriers).
+__device__ __forceinline__ float row_sum(float v, uint32_t tpr, float* slot) {
 #pragma unroll
-    for (uint32_t o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (uint32_t o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (tpr == 32) return v;
-    const uint32_t warps = tpr / 32;
-    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
+    const uint32_t lane = threadIdx.x % 32;
+    if (lane == 0) slot[threadIdx.x / 32] = v;
     __syncthreads();
-    v = slot[threadIdx.x % 32 < warps ? threadIdx.x % 32 : 0];
-    if (threadIdx.x % 32 >= warps) v = 0.0f;        // neutral: sums, and maxima of magnitudes
+    v = lane < tpr / 32 ? slot[lane] : 0.0f;
 #pragma unroll
-    for (uint32_t o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (uint32_t o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
+}
+
+// The largest of magnitudes, NaN if one is: as bits, magnitudes order like integers, with NaN on top.
+__device__ __forceinline__ float warp_max(float v) {
+    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
+}
+
+__device__ __forceinline__ float row_max(float v, uint32_t tpr, float* slot) {
+    v = warp_max(v);
+    if (tpr == 32) return v;
+    const uint32_t lane = threadIdx.x % 32;
+    if (lane == 0) slot[threadIdx.x / 32] = v;
+    __syncthreads();
+    return warp_max(lane < tpr / 32 ? slot[lane] : 0.0f);
 }
 
 // One row by blockDim.x threads; blockDim.y rows a CTA where a row is one warp.  NCH chunks a
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsn
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) sum += v[k] * v[k];
     }
-    const float s = rsqrtf(row_reduce(sum, tpr, slots[0], Sum()) * p.inv_cols + p.eps);
+    const float s = rsqrtf(row_sum(sum, tpr, slots[0]) * p.inv_cols + p.eps);
     if (t == 0 && p.rstd) p.rstd[r] = s;
 
     auto normed = [&](uint32_t i, const float (&v)[8], float (&o)[8]) {
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsn
             normed(i, v, o);
             m = max_nan(m, amax8(o));
         }
-        const float scale = max_nan(row_reduce(m, tpr, slots[1], MaxNan()) / kE4m3Max, kScaleMin);
+        const float scale = max_nan(row_max(m, tpr, slots[1]) / kE4m3Max, kScaleMin);
         if (t == 0) p.scales[r] = scale;
         inv = 1.0f / scale;
     }
@@ -178,15 +185,28 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsn
     }
 }
 
-// Rows blockIdx.x, + partials, ... by one CTA (or warp, where a row is one warp): each thread keeps
-// the same columns for all of them, so the weight's gradient adds up in its registers and is
-// written once, as one partial row (kLong: in the partial row itself).
+// Partial row of a CTA whose warps took rows of their own: their sums, in the warps' order.
+template <uint32_t N>
+__device__ __forceinline__ void add_warps(const float (&sums)[kWarpRows][N], float* part, uint32_t cols) {
+    __syncthreads();
+    for (uint32_t c = threadIdx.y * 32 + threadIdx.x; c < cols; c += kWarpRows * 32) {
+        float v = sums[0][c];
+#pragma unroll
+        for (uint32_t i = 1; i < kWarpRows; ++i) v += sums[i][c];
+        part[c] = v;
+    }
+}
+
+// A CTA (or a warp, where a row is one warp) walks over rows: each thread keeps the same columns for
+// all of them, so the weight's gradient adds up in its registers and is written once, as the CTA's
+// partial row (kLong: in the partial row itself).
 template <uint32_t NCH, bool VEC>
 __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
     __shared__ float slots[2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
+    constexpr bool WARPS = NCH != kLong && 32 * 8 * NCH <= kBwdWarpCols;     // rows of one warp come here
+    __shared__ float sums[kWarpRows][WARPS ? 32 * 8 * NCH : 1];
     const uint32_t me = blockIdx.x * blockDim.y + threadIdx.y;
-    if (me >= p.partials) return;                   // a whole warp: rows share no barrier
     constexpr uint32_t HELD = NCH == kLong ? 1 : NCH;
     const uint32_t nch = NCH == kLong ? (p.cols + 8 * tpr - 1) / (8 * tpr) : NCH;
     float acc[HELD][8];
@@ -194,10 +214,10 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsn
     for (uint32_t i = 0; i < HELD; ++i)
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) acc[i][k] = 0.0f;
-    float* part = p.partial ? p.partial + (uint64_t)me * p.cols : nullptr;
+    float* part = p.partial ? p.partial + (uint64_t)blockIdx.x * p.cols : nullptr;
 
     uint32_t turn = 0;
-    for (uint64_t r = me; r < p.rows; r += p.partials, turn ^= 1) {
+    for (uint64_t r = me; r < p.rows; r += p.walkers, turn ^= 1) {
         const char* dyr = p.dy + r * p.dy_pitch;
         const char* hr = p.h + r * p.h_pitch;
         const char* dresr = p.dres ? p.dres + r * p.dres_pitch : nullptr;
@@ -238,7 +258,7 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsn
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) dot += g[j][k] * n[j][k];
         }
-        const float m = row_reduce(dot, tpr, slots[turn], Sum()) * p.inv_cols;
+        const float m = row_sum(dot, tpr, slots[turn]) * p.inv_cols;
 #pragma unroll HELD
         for (uint32_t i = 0; i < nch; ++i) {
             const uint32_t j = NCH == kLong ? 0 : i, c = 8 * (i * tpr + t);
@@ -269,13 +289,22 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsn
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
                 const uint32_t c = 8 * (i * tpr + t) + k;
-                if (c < p.cols) part[c] = acc[i][k];
+                if (WARPS && blockDim.y > 1) sums[threadIdx.y][WARPS ? c : 0] = acc[i][k];
+                else if (c < p.cols) part[c] = acc[i][k];
             }
+        if (WARPS && blockDim.y > 1) add_warps(sums, part, p.cols);
     }
 }
 
 // ---- elements ----------------------------------------------------------------------------------
-// Columns t, t + T, ... (E of them; zeros from `cols` on) of a row.
+// A warp holds 32 E neighbouring columns, a thread every 32nd of them: an access is contiguous over the
+// warp, and a group of 32, 64 or 128 columns is one, two or four of each of its threads'.
+template <uint32_t E>
+__device__ __forceinline__ uint32_t column_of(uint32_t k) {
+    return threadIdx.x / 32 * (32 * E) + 32 * k + threadIdx.x % 32;
+}
+
+// The thread's columns of a row (zeros from `cols` on).
 template <uint32_t E>
 __device__ __forceinline__ void load_elements(const char* row, uint32_t dt, uint32_t cols, float (&v)[E]) {
     const char* rows[E];
@@ -283,69 +312,79 @@ __device__ __forceinline__ void load_elements(const char* row, uint32_t dt, uint
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) {
         rows[k] = row;
-        c[k] = min(k * blockDim.x + threadIdx.x, cols - 1);
+        c[k] = min(column_of<E>(k), cols - 1);
     }
     gather(rows, dt, c, v);
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k)
-        if (k * blockDim.x + threadIdx.x >= cols) v[k] = 0.0f;
+        if (column_of<E>(k) >= cols) v[k] = 0.0f;
 }
 
 template <uint32_t E>
 __device__ __forceinline__ void store_elements(char* row, uint32_t dt, uint32_t cols, const float (&v)[E]) {
-    const uint32_t T = blockDim.x, t = threadIdx.x;
+    const uint32_t c = column_of<E>(0);
     if (dt == DTT_BF16) {
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k)
-            if (k * T + t < cols) reinterpret_cast<uint16_t*>(row)[k * T + t] = (uint16_t)pack_bf16(v[k], 0.0f);
+            if (c + 32 * k < cols) reinterpret_cast<uint16_t*>(row)[c + 32 * k] = (uint16_t)pack_bf16(v[k], 0.0f);
     } else if (dt == DTT_F32) {
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k)
-            if (k * T + t < cols) reinterpret_cast<float*>(row)[k * T + t] = v[k];
+            if (c + 32 * k < cols) reinterpret_cast<float*>(row)[c + 32 * k] = v[k];
     } else {
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k)
-            if (k * T + t < cols) reinterpret_cast<uint8_t*>(row)[k * T + t] = (uint8_t)pack_e4m3(v[k], 0.0f);
+            if (c + 32 * k < cols) reinterpret_cast<uint8_t*>(row)[c + 32 * k] = (uint8_t)pack_e4m3(v[k], 0.0f);
     }
 }
 
-// The scales of row r's groups, and h divided by them.  A group is one, two or four neighbours of the row's
-// segments of 32 columns (segment k T / 32 + warp), whose maxima meet in shared memory.
+// The scales of row r, and its values divided by them.
 template <uint32_t E>
-__device__ __forceinline__ void scale_groups(const FwdParams& p, uint64_t r, float* segment, float (&h)[E]) {
-    const uint32_t T = blockDim.x, t = threadIdx.x, warps = T / 32;
-    __syncthreads();                                          // the last row's have been read
-#pragma unroll
-    for (uint32_t k = 0; k < E; ++k) {
-        float m = fabsf(h[k]);
-#pragma unroll
-        for (uint32_t d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        if (t % 32 == 0) segment[k * warps + t / 32] = m;
-    }
-    __syncthreads();
-    const uint32_t per = p.group_lanes / 4;                   // segments a group
-#pragma unroll
-    for (uint32_t k = 0; k < E; ++k) {
-        const uint32_t q = k * warps + t / 32, q0 = q / per * per;
+__device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, float* slot, float (&v)[E]) {
+    const uint32_t c = column_of<E>(0);
+    if (p.group_lanes == 0) {
         float m = 0.0f;
-        for (uint32_t i = q0; i < q0 + per && i < E * warps; ++i) m = max_nan(m, segment[i]);
-        const float scale = max_nan(m / kE4m3Max, kScaleMin);
-        if (t % 32 == 0 && q == q0 && q * 32 < p.cols) p.scales[r * p.groups + q / per] = scale;
-        h[k] *= 1.0f / scale;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) m = max_nan(m, fabsf(v[k]));
+        const float scale = max_nan(row_max(m, blockDim.x, slot) / kE4m3Max, kScaleMin);
+        if (threadIdx.x == 0) p.scales[r] = scale;
+        const float inv = 1.0f / scale;
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) v[k] *= inv;
+        return;
+    }
+    const uint32_t per = p.group_lanes / 4;                   // of a thread's columns: 1, 2 or 4
+#pragma unroll
+    for (uint32_t k = 0; k < E; k += 4) {
+        float m[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) m[i] = fabsf(v[k + i]);
+        if (per >= 2) {
+            m[0] = m[1] = max_nan(m[0], m[1]);
+            m[2] = m[3] = max_nan(m[2], m[3]);
+        }
+        if (per == 4) m[0] = m[1] = m[2] = m[3] = max_nan(m[0], m[2]);
+        float scale = 0.0f, inv = 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            if (i % per == 0) {
+                scale = max_nan(warp_max(m[i]) / kE4m3Max, kScaleMin);
+                inv = 1.0f / scale;
+                if (threadIdx.x % 32 == 0 && c + 32 * (k + i) < p.cols) p.scales[r * p.groups + (c + 32 * (k + i)) / (32 * per)] = scale;
+            }
+            v[k + i] *= inv;
+        }
     }
 }
 
-// One row a CTA.
+// A row a CTA, or a warp (blockDim.y of them).
 template <uint32_t E>
 __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const __grid_constant__ FwdParams p) {
     __shared__ float slots[2][32];
-    __shared__ float segment[E * kFwdThreads / 32];
-    const uint32_t T = blockDim.x, t = threadIdx.x;
-    const uint64_t r = blockIdx.x;
-    const char* x = p.x + r * p.x_pitch;
-    char* y = p.y + r * p.y_pitch;
+    const uint64_t r = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (r >= p.rows) return;                        // a whole warp: rows share no barrier
     float h[E], o[E];
-    load_elements(x, p.x_dt, p.cols, h);
+    load_elements(p.x + r * p.x_pitch, p.x_dt, p.cols, h);
     if (p.res) {
         load_elements(p.res + r * p.res_pitch, p.res_dt, p.cols, o);
 #pragma unroll
@@ -355,31 +394,21 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const
     float sum = 0.0f;
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
-    const float s = rsqrtf(row_reduce(sum, T, slots[0], Sum()) * p.inv_cols + p.eps);
-    if (t == 0 && p.rstd) p.rstd[r] = s;
+    const float s = rsqrtf(row_sum(sum, blockDim.x, slots[0]) * p.inv_cols + p.eps);
+    if (threadIdx.x == 0 && p.rstd) p.rstd[r] = s;
     if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) h[k] = p.w ? h[k] * s * o[k] : h[k] * s;
-    if (p.y_dt == DTT_E4M3 && p.group_lanes == 0) {
-        float m = 0.0f;
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k) m = max_nan(m, fabsf(h[k]));
-        const float scale = max_nan(row_reduce(m, T, slots[1], MaxNan()) / kE4m3Max, kScaleMin);
-        if (t == 0) p.scales[r] = scale;
-        const float inv = 1.0f / scale;
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k) h[k] *= inv;
-    } else if (p.y_dt == DTT_E4M3) {
-        scale_groups(p, r, segment, h);
-    }
-    store_elements(y, p.y_dt, p.cols, h);
+    if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[1], h);
+    store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
 }
 
-// As the chunk form: rows blockIdx.x, + partials, ..., the weight's gradient in registers.
+// As the chunk form: a CTA or a warp walks over rows, the weight's gradient in its registers.
 template <uint32_t E>
 __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
     __shared__ float slots[2][32];
-    const uint32_t T = blockDim.x, t = threadIdx.x;
+    __shared__ float sums[kWarpRows][32 * E];
+    const uint32_t T = blockDim.x;
     float acc[E], w[E];
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) {
@@ -388,7 +417,7 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const
     }
     if (p.w) load_elements(p.w, p.w_dt, p.cols, w);
     uint32_t turn = 0;
-    for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
+    for (uint64_t r = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y; r < p.rows; r += p.walkers, turn ^= 1) {
         const float s = p.rstd[r];
         float g[E], n[E], q[E];
         load_elements(p.dy + r * p.dy_pitch, p.dy_dt, p.cols, g);
@@ -402,7 +431,7 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const
             g[k] *= w[k];
             dot += g[k] * n[k];
         }
-        const float m = row_reduce(dot, T, slots[turn], Sum()) * p.inv_cols;
+        const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) {
             g[k] = s * (g[k] - n[k] * m);
@@ -410,7 +439,15 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const
         }
         store_elements(p.dx + r * p.dx_pitch, p.h_dt, p.cols, g);
     }
-    if (p.partial) store_elements(reinterpret_cast<char*>(p.partial + (uint64_t)blockIdx.x * p.cols), DTT_F32, p.cols, acc);
+    if (!p.partial) return;
+    float* part = p.partial + (uint64_t)blockIdx.x * p.cols;
+    if (blockDim.y == 1) {
+        store_elements(reinterpret_cast<char*>(part), DTT_F32, p.cols, acc);
+        return;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) sums[threadIdx.y][32 * k + threadIdx.x] = acc[k];
+    add_warps(sums, part, p.cols);
 }
 
 // ---- ring --------------------------------------------------------------------------------------
@@ -492,7 +529,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) sum += h[i][k] * h[i][k];
         if (!here) sum = __int_as_float(0x7FC00000);
-        const float s = rsqrtf(row_reduce(sum, T, slots[turn & 1][0], Sum()) * p.inv_cols + p.eps);
+        const float s = rsqrtf(row_sum(sum, T, slots[turn & 1][0]) * p.inv_cols + p.eps);
         if (t == 0) {
             if (turn + S - 1 < turns) start(turn + S - 1);
             if (p.rstd) p.rstd[r] = s;
@@ -518,7 +555,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
                 float all = m[0];
 #pragma unroll
                 for (uint32_t i = 1; i < NCH; ++i) all = max_nan(all, m[i]);
-                const float scale = max_nan(row_reduce(all, T, slots[turn & 1][1], MaxNan()) / kE4m3Max, kScaleMin);
+                const float scale = max_nan(row_max(all, T, slots[turn & 1][1]) / kE4m3Max, kScaleMin);
                 if (t == 0) p.scales[r] = scale;
                 const float inv = 1.0f / scale;
 #pragma unroll
@@ -602,7 +639,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __
             }
         }
         if (!here) dot = __int_as_float(0x7FC00000);
-        const float m = row_reduce(dot, T, slots[turn & 1], Sum()) * p.inv_cols;
+        const float m = row_sum(dot, T, slots[turn & 1]) * p.inv_cols;
         if (t == 0 && turn + S - 1 < turns) start(turn + S - 1);
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) {
@@ -628,7 +665,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __
 }
 
 // ---- ring of unaligned rows --------------------------------------------------------------------
-// The ring for rows at any alignment, a thread's columns t, t + T, ...  A bulk copy moves whole 16-byte
+// The ring for rows at any alignment, an element a thread.  A bulk copy moves whole 16-byte
 // words: from the one that holds the row's first byte to the one that holds its last.  The few bytes
 // beside the row in these two are copied with it and not looked at (an allocation never ends within
 // such a word).
@@ -649,9 +686,8 @@ template <uint32_t E>
 __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][2][32];
-    __shared__ float segment[E * kRingThreads / 32];
     __shared__ uint64_t full[kRingStages];
-    const uint32_t T = blockDim.x, t = threadIdx.x, warps = T / 32;
+    const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t x_room = words_room(xb), stage_bytes = x_room + (rb ? words_room(rb) : 0);
     const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
@@ -693,8 +729,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
         if (!here) sum = __int_as_float(0x7FC00000);
-        const float s = rsqrtf(row_reduce(sum, T, slots[turn & 1][0], Sum()) * p.inv_cols + p.eps);
-        if (T == 32) __syncwarp();
+        const float s = rsqrtf(row_sum(sum, T, slots[turn & 1][0]) * p.inv_cols + p.eps);
         if (t == 0) {
             if (turn + S - 1 < turns) start(turn + S - 1);
             if (p.rstd) p.rstd[r] = s;
@@ -702,18 +737,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
         if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) h[k] *= s * w[k];
-        if (p.y_dt == DTT_E4M3 && p.group_lanes == 0) {
-            float m = 0.0f;
-#pragma unroll
-            for (uint32_t k = 0; k < E; ++k) m = max_nan(m, fabsf(h[k]));
-            const float scale = max_nan(row_reduce(m, T, slots[turn & 1][1], MaxNan()) / kE4m3Max, kScaleMin);
-            if (t == 0) p.scales[r] = scale;
-            const float inv = 1.0f / scale;
-#pragma unroll
-            for (uint32_t k = 0; k < E; ++k) h[k] *= inv;
-        } else if (p.y_dt == DTT_E4M3) {
-            scale_groups(p, r, segment, h);
-        }
+        if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[turn & 1][1], h);
         store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
         if (++st == S) { st = 0; phase ^= 1; }
     }
@@ -771,8 +795,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
             dot += g[k] * n[k];
         }
         if (!here) dot = __int_as_float(0x7FC00000);
-        const float m = row_reduce(dot, T, slots[turn & 1], Sum()) * p.inv_cols;
-        if (T == 32) __syncwarp();
+        const float m = row_sum(dot, T, slots[turn & 1]) * p.inv_cols;
         if (t == 0 && turn + S - 1 < turns) start(turn + S - 1);
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) g[k] = s * (g[k] - n[k] * m);
@@ -787,37 +810,37 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
     if (p.partial) store_elements(reinterpret_cast<char*>(p.partial + (uint64_t)blockIdx.x * p.cols), DTT_F32, p.cols, acc);
 }
 
-// dweight[c] = the partial rows' sum.  32 columns a CTA; its 8 warps take every eighth partial row,
-// and their sums are added in warp order.
-__global__ void __launch_bounds__(256) rmsnorm_dweight_kernel(const float* partial, uint32_t partials,
-                                                              uint32_t cols, float* dweight) {
-    __shared__ float part[8][32];
+// dweight[c] = the partial rows' sum.  32 columns a CTA; its 32 warps take every 32nd partial row, and
+// their sums are added in warp order.
+__global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* partial, uint32_t partials, uint32_t cols, float* dweight) {
+    __shared__ float part[32][33];
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (c < cols) {
-#pragma unroll 8
-        for (uint32_t i = warp; i < partials; i += 8) v += partial[(uint64_t)i * cols + c];
+#pragma unroll 10
+        for (uint32_t i = warp; i < partials; i += 32) v += partial[(uint64_t)i * cols + c];
     }
     part[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && c < cols) {
+    v = part[lane][warp];                            // warp w adds column w
 #pragma unroll
-        for (uint32_t w = 1; w < 8; ++w) v += part[w][lane];
-        dweight[c] = v;
-    }
+    for (uint32_t o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane == 0 && (uint64_t)blockIdx.x * 32 + warp < cols) dweight[(uint64_t)blockIdx.x * 32 + warp] = v;
 }
 
 struct Shape {
     uint32_t nch, tpr, rows_per_cta;
 };
 
-// Chunks: up to four a thread in registers; `threads` threads a row at most.
-Shape shape_of(uint32_t cols, uint32_t threads) {
+// Chunks: a warp a row up to `warp_cols` columns; else up to four a thread in registers, `threads` threads a
+// row at most.
+Shape shape_of(uint32_t cols, uint32_t threads, uint32_t warp_cols) {
     const uint32_t chunks = (cols + 7) / 8;
     for (uint32_t nch : {1u, 2u, 4u}) {
+        if (cols <= warp_cols && chunks <= 32 * nch) return {nch, 32, kWarpRows};
         const uint32_t tpr = ((chunks + nch - 1) / nch + 31) / 32 * 32;
-        if (tpr <= (nch == 4 ? threads : 256u)) return {nch, tpr, tpr == 32 ? 8u : 1u};
+        if (cols > warp_cols && tpr <= (nch == 4 ? threads : 256u)) return {nch, tpr, 1};
     }
     return {kLong, threads, 1};
 }
@@ -826,8 +849,8 @@ struct Ring {
     uint32_t nch, threads, ctas, stages, smem;       // ctas: of an SM; 0: no ring for these rows
 };
 
-// Chunks (vec): two a thread up to 512 threads, then four (twice the registers); one warp a row is left to
-// the chunk form.  Elements: 8 a thread up to 256 threads, then 16.  As many CTAs as make `threads_per_sm`
+// Chunks (vec): two a thread up to 512 threads, then four (twice the registers).  Elements: 8 a thread up to
+// 256 threads, then 16.  Rows of one warp are left to the other forms.  As many CTAs as make `threads_per_sm`
 // threads an SM (half as many with four chunks), fewer where three stages each would not fit; then as
 // many stages as fit.
 Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t threads_per_sm) {
@@ -839,7 +862,7 @@ Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t threads_per_sm) {
         g.threads = ((cols + 8 * nch - 1) / (8 * nch) + 31) / 32 * 32;
         if (g.threads <= (nch == 1 ? 256 : kRingThreads)) break;
     }
-    if ((vec && g.threads < 64) || g.threads > kRingThreads) return {};
+    if (g.threads < 64 || g.threads > kRingThreads) return {};
     g.ctas = std::min(std::min(std::max(threads_per_sm * 2 / std::max(g.nch, 2u) / g.threads, 1u), kRingSmem / (3 * stage_bytes)), 16u);
     g.stages = std::min(kRingStages, kRingSmem / (g.ctas * stage_bytes));
     g.smem = g.stages * stage_bytes;
@@ -864,7 +887,7 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t sms = sm_count();
     const uint64_t xb = (uint64_t)p.cols * xe, rb = (uint64_t)p.cols * re;
     const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, 1024);
-    if (g.ctas && p.rows >= 2 * sms) {
+    if (g.ctas && p.rows >= 2 * sms && !(vec && p.cols <= kFwdWarpCols)) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
         auto kernel = vec ? (g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_fwd_ring_elements_kernel<8> : rmsnorm_fwd_ring_elements_kernel<16>);
@@ -873,7 +896,8 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     }
     if (!vec) {
         if (const uint32_t t = element_threads(p.cols, 8, kFwdThreads)) {
-            rmsnorm_fwd_elements_kernel<8><<<(uint32_t)p.rows, t, 0, stream>>>(p);
+            const uint32_t each = t == 32 ? kWarpRows : 1;
+            rmsnorm_fwd_elements_kernel<8><<<(uint32_t)((p.rows + each - 1) / each), dim3(t, each), 0, stream>>>(p);
             return;
         }
         if (const uint32_t t = element_threads(p.cols, 16, kFwdThreads)) {
@@ -883,7 +907,7 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
         rmsnorm_fwd_kernel<kLong, false><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
         return;
     }
-    const Shape s = shape_of(p.cols, kFwdThreads);
+    const Shape s = shape_of(p.cols, kFwdThreads, kFwdWarpCols);
     const dim3 block(s.tpr, s.rows_per_cta);
     const uint32_t grid = (uint32_t)((p.rows + s.rows_per_cta - 1) / s.rows_per_cta);
     if (s.nch == 1) rmsnorm_fwd_kernel<1, true><<<grid, block, 0, stream>>>(p);
@@ -898,17 +922,23 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t sms = sm_count();
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
     const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 512);
-    if (g.ctas && p.rows >= 2 * sms) {
+    if (g.ctas && p.rows >= 2 * sms && !(vec && p.cols <= kBwdWarpCols)) {
         p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)kMaxPartials});
         auto kernel = vec ? (g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
         kernel<<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
         return;
     }
-    p.partials = (uint32_t)std::min<uint64_t>(p.rows, kMaxPartials);
+    auto walk = [&](uint32_t each) {       // walkers a CTA
+        p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, kMaxPartials);
+        p.walkers = p.partials * each;
+    };
+    walk(1);
     if (!vec) {
         if (const uint32_t t = element_threads(p.cols, 8, kBwdThreads)) {
-            rmsnorm_bwd_elements_kernel<8><<<p.partials, t, 0, stream>>>(p);
+            const uint32_t each = t == 32 ? kWarpRows : 1;
+            walk(each);
+            rmsnorm_bwd_elements_kernel<8><<<p.partials, dim3(t, each), 0, stream>>>(p);
             return;
         }
         if (const uint32_t t = element_threads(p.cols, 16, kBwdThreads)) {
@@ -918,9 +948,10 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         rmsnorm_bwd_kernel<kLong, false><<<p.partials, kBwdThreads, 0, stream>>>(p);
         return;
     }
-    const Shape s = shape_of(p.cols, kBwdThreads);
+    const Shape s = shape_of(p.cols, kBwdThreads, kBwdWarpCols);
     const dim3 block(s.tpr, s.rows_per_cta);
-    const uint32_t grid = (p.partials + s.rows_per_cta - 1) / s.rows_per_cta;
+    walk(s.rows_per_cta);
+    const uint32_t grid = p.partials;
     if (s.nch == 1) rmsnorm_bwd_kernel<1, true><<<grid, block, 0, stream>>>(p);
     else if (s.nch == 2) rmsnorm_bwd_kernel<2, true><<<grid, block, 0, stream>>>(p);
     else if (s.nch == 4) rmsnorm_bwd_kernel<4, true><<<grid, block, 0, stream>>>(p);
@@ -1107,7 +1138,7 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
                      aligned(dres, dres ? dres_pitch : 0, 16) && aligned(dx, dx_pitch, 16);
     launch_bwd(p, vec, stream);
     if (dweight)
-        rmsnorm_dweight_kernel<<<(p.cols + 31) / 32, 256, 0, stream>>>(p.partial, p.partials, p.cols, dweight);
+        rmsnorm_dweight_kernel<<<(p.cols + 31) / 32, 1024, 0, stream>>>(p.partial, p.partials, p.cols, dweight);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
