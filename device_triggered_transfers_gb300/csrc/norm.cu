@@ -27,7 +27,7 @@ constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   
 constexpr uint32_t kRingStages = 8;        // of a CTA, at most
 constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr uint32_t kFwdWarpCols = 1024, kBwdWarpCols = 512;   // columns of rows that one warp takes, at most
+constexpr uint32_t kFwdWarpCols = 256, kBwdWarpCols = 512;   // columns of rows that one warp takes, at most
 constexpr uint32_t kWarpRows = 8;          // rows of a CTA whose rows are one warp each
 constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
 
@@ -61,6 +61,15 @@ struct BwdParams {
     uint32_t dy_dt, h_dt, w_dt;
     float inv_cols;
 };
+
+// The scale of a group whose largest magnitude is m, and what its values are multiplied by: the reciprocal
+// to one ulp (a full division an 8-column chunk was a quarter of the instructions).
+__device__ __forceinline__ float scale_of(float m) { return max_nan(m * (1.0f / kE4m3Max), kScaleMin); }
+__device__ __forceinline__ float inverse_of(float scale) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+    return r;
+}
 
 // Over the TPR threads of a row, the same bits in each.  One warp: butterfly shuffles.  More: the warps'
 // values through shared memory (`slot`: 32 words used by this reduction alone between two of the row's
@@ -157,9 +166,9 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsn
             normed(i, v, o);
             m = max_nan(m, amax8(o));
         }
-        const float scale = max_nan(row_max(m, tpr, slots[1]) / kE4m3Max, kScaleMin);
+        const float scale = scale_of(row_max(m, tpr, slots[1]));
         if (t == 0) p.scales[r] = scale;
-        inv = 1.0f / scale;
+        inv = inverse_of(scale);
     }
 #pragma unroll HELD
     for (uint32_t i = 0; i < nch; ++i) {
@@ -171,8 +180,8 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsn
         if (e4m3 && !row_scale) {
             float m = amax8(o);
             for (uint32_t d = p.group_lanes >> 1; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            const float scale = max_nan(m / kE4m3Max, kScaleMin);
-            inv = 1.0f / scale;
+            const float scale = scale_of(m);
+            inv = inverse_of(scale);
             if (t % p.group_lanes == 0 && c < p.cols)
                 p.scales[r * p.groups + c / (8 * p.group_lanes)] = scale;
         }
@@ -304,38 +313,67 @@ __device__ __forceinline__ uint32_t column_of(uint32_t k) {
     return threadIdx.x / 32 * (32 * E) + 32 * k + threadIdx.x % 32;
 }
 
-// The thread's columns of a row (zeros from `cols` on).
+// Whether the warp's columns all lie in the row: no address and no store needs a check of its own then.
+template <uint32_t E>
+__device__ __forceinline__ bool whole_warp(uint32_t cols) {
+    return (threadIdx.x / 32 + 1) * (32 * E) <= cols;
+}
+
+// The thread's columns of a row (zeros from `cols` on).  The loads go out together (gather's reasons).
 template <uint32_t E>
 __device__ __forceinline__ void load_elements(const char* row, uint32_t dt, uint32_t cols, float (&v)[E]) {
+    const uint32_t c0 = column_of<E>(0);
+    if (whole_warp<E>(cols)) {
+        if (dt == DTT_BF16) {
+            const uint16_t* at = reinterpret_cast<const uint16_t*>(row) + c0;
+            uint16_t raw[E];
+#pragma unroll
+            for (uint32_t k = 0; k < E; ++k) raw[k] = at[32 * k];
+#pragma unroll
+            for (uint32_t k = 0; k < E; ++k) v[k] = __uint_as_float((uint32_t)raw[k] << 16);
+        } else {
+            const float* at = reinterpret_cast<const float*>(row) + c0;
+#pragma unroll
+            for (uint32_t k = 0; k < E; ++k) v[k] = at[32 * k];
+        }
+        return;
+    }
     const char* rows[E];
     uint32_t c[E];
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) {
         rows[k] = row;
-        c[k] = min(column_of<E>(k), cols - 1);
+        c[k] = min(c0 + 32 * k, cols - 1);
     }
     gather(rows, dt, c, v);
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k)
-        if (column_of<E>(k) >= cols) v[k] = 0.0f;
+        if (c0 + 32 * k >= cols) v[k] = 0.0f;
+}
+
+template <uint32_t E, bool WHOLE>
+__device__ __forceinline__ void store_elements_as(char* row, uint32_t dt, uint32_t left, const float (&v)[E]) {
+    if (dt == DTT_BF16) {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (WHOLE || 32 * k < left) reinterpret_cast<uint16_t*>(row)[32 * k] = (uint16_t)pack_bf16(v[k], 0.0f);
+    } else if (dt == DTT_F32) {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (WHOLE || 32 * k < left) reinterpret_cast<float*>(row)[32 * k] = v[k];
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k)
+            if (WHOLE || 32 * k < left) reinterpret_cast<uint8_t*>(row)[32 * k] = (uint8_t)pack_e4m3(v[k], 0.0f);
+    }
 }
 
 template <uint32_t E>
 __device__ __forceinline__ void store_elements(char* row, uint32_t dt, uint32_t cols, const float (&v)[E]) {
-    const uint32_t c = column_of<E>(0);
-    if (dt == DTT_BF16) {
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k)
-            if (c + 32 * k < cols) reinterpret_cast<uint16_t*>(row)[c + 32 * k] = (uint16_t)pack_bf16(v[k], 0.0f);
-    } else if (dt == DTT_F32) {
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k)
-            if (c + 32 * k < cols) reinterpret_cast<float*>(row)[c + 32 * k] = v[k];
-    } else {
-#pragma unroll
-        for (uint32_t k = 0; k < E; ++k)
-            if (c + 32 * k < cols) reinterpret_cast<uint8_t*>(row)[c + 32 * k] = (uint8_t)pack_e4m3(v[k], 0.0f);
-    }
+    const uint32_t c0 = column_of<E>(0);
+    char* at = row + (uint64_t)c0 * (dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1);
+    if (whole_warp<E>(cols)) store_elements_as<E, true>(at, dt, 0, v);
+    else store_elements_as<E, false>(at, dt, c0 < cols ? cols - c0 : 0, v);
 }
 
 // The scales of row r, and its values divided by them.
@@ -346,9 +384,9 @@ __device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, f
         float m = 0.0f;
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) m = max_nan(m, fabsf(v[k]));
-        const float scale = max_nan(row_max(m, blockDim.x, slot) / kE4m3Max, kScaleMin);
+        const float scale = scale_of(row_max(m, blockDim.x, slot));
         if (threadIdx.x == 0) p.scales[r] = scale;
-        const float inv = 1.0f / scale;
+        const float inv = inverse_of(scale);
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) v[k] *= inv;
         return;
@@ -368,8 +406,8 @@ __device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, f
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
             if (i % per == 0) {
-                scale = max_nan(warp_max(m[i]) / kE4m3Max, kScaleMin);
-                inv = 1.0f / scale;
+                scale = scale_of(warp_max(m[i]));
+                inv = inverse_of(scale);
                 if (threadIdx.x % 32 == 0 && c + 32 * (k + i) < p.cols) p.scales[r * p.groups + (c + 32 * (k + i)) / (32 * per)] = scale;
             }
             v[k + i] *= inv;
@@ -555,9 +593,9 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
                 float all = m[0];
 #pragma unroll
                 for (uint32_t i = 1; i < NCH; ++i) all = max_nan(all, m[i]);
-                const float scale = max_nan(row_max(all, T, slots[turn & 1][1]) / kE4m3Max, kScaleMin);
+                const float scale = scale_of(row_max(all, T, slots[turn & 1][1]));
                 if (t == 0) p.scales[r] = scale;
-                const float inv = 1.0f / scale;
+                const float inv = inverse_of(scale);
 #pragma unroll
                 for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
@@ -567,7 +605,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
                 for (uint32_t i = 0; i < NCH; ++i) {
                     for (uint32_t d = p.group_lanes >> 1; d > 0; d >>= 1)
                         m[i] = max_nan(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], d));
-                    const float scale = max_nan(m[i] / kE4m3Max, kScaleMin), inv = 1.0f / scale;
+                    const float scale = scale_of(m[i]), inv = inverse_of(scale);
                     const uint32_t c = 8 * (i * T + t);
                     if (t % p.group_lanes == 0 && c < p.cols) p.scales[r * p.groups + c / (8 * p.group_lanes)] = scale;
 #pragma unroll
