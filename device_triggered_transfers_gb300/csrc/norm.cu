@@ -22,7 +22,8 @@ namespace {
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its reciprocal stays finite
-constexpr uint32_t kMaxPartials = 608;     // partial rows of the weight's gradient: four a SM
+// Partial rows of the weight's gradient, at most: four, eight or sixteen a SM.
+__host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return cols > 1024 ? 608 : cols > 512 ? 1216 : 2432; }
 constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   // a row's most threads
 constexpr uint32_t kRingStages = 8;        // of a CTA, at most
 constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
@@ -211,6 +212,7 @@ __device__ __forceinline__ void add_warps(const float (&sums)[kWarpRows][N], flo
 // partial row (kLong: in the partial row itself).
 template <uint32_t NCH, bool VEC>
 __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
+    launch_next();
     __shared__ float slots[2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
     constexpr bool WARPS = NCH != kLong && 32 * 8 * NCH <= kBwdWarpCols;     // rows of one warp come here
@@ -444,6 +446,7 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const
 // As the chunk form: a CTA or a warp walks over rows, the weight's gradient in its registers.
 template <uint32_t E>
 __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
+    launch_next();
     __shared__ float slots[2][32];
     __shared__ float sums[kWarpRows][32 * E];
     const uint32_t T = blockDim.x;
@@ -513,17 +516,21 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const char* src, uint32_
 // barrier: every thread is then done with that stage's last row (turn i - 1).  A copy that does not
 // arrive makes the row NaN.
 template <uint32_t NCH>
-__global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][2][32];
     __shared__ uint64_t full[kRingStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t stage_bytes = xb + rb;
-    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
-    auto start = [&](uint64_t i) {
-        const uint64_t r = blockIdx.x + i * gridDim.x;
-        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+    uint64_t next = blockIdx.x;                     // thread 0: the row to be fetched next, and its stage
+    uint32_t next_st = 0;
+    auto start = [&] {
+        if (next >= p.rows) return;
+        const uint64_t r = next;
+        const uint32_t bar = saddr(full + next_st), dst = saddr(stages) + next_st * stage_bytes;
+        next += gridDim.x;
+        if (++next_st == S) next_st = 0;
         bar_expect_tx(bar, stage_bytes);
         bulk_load(dst, p.x + r * p.x_pitch, xb, bar);
         if (rb) bulk_load(dst + xb, p.res + r * p.res_pitch, rb, bar);
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
     float w[NCH][8];
 #pragma unroll
@@ -546,8 +553,8 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
     __syncthreads();
 
     uint32_t st = 0, phase = 0;
-    for (uint64_t turn = 0; turn < turns; ++turn) {
-        const uint64_t r = blockIdx.x + turn * gridDim.x;
+    uint32_t turn = 0;
+    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
         const bool here = bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float h[NCH][8], sum = 0.0f;
@@ -567,9 +574,9 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) sum += h[i][k] * h[i][k];
         if (!here) sum = __int_as_float(0x7FC00000);
-        const float s = rsqrtf(row_sum(sum, T, slots[turn & 1][0]) * p.inv_cols + p.eps);
+        const float s = rsqrtf(row_sum(sum, T, slots[turn][0]) * p.inv_cols + p.eps);
         if (t == 0) {
-            if (turn + S - 1 < turns) start(turn + S - 1);
+            start();
             if (p.rstd) p.rstd[r] = s;
         }
         if (p.res_out) {
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
                 float all = m[0];
 #pragma unroll
                 for (uint32_t i = 1; i < NCH; ++i) all = max_nan(all, m[i]);
-                const float scale = scale_of(row_max(all, T, slots[turn & 1][1]));
+                const float scale = scale_of(row_max(all, T, slots[turn][1]));
                 if (t == 0) p.scales[r] = scale;
                 const float inv = inverse_of(scale);
 #pragma unroll
@@ -621,17 +628,22 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_fwd_ring_kernel(const __
 
 // The backward pass the same way: a stage holds dy, h, then dres.
 template <uint32_t NCH>
-__global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 1) rmsnorm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+    launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][32];
     __shared__ uint64_t full[kRingStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
     const uint32_t stage_bytes = gb + hb + (p.dres ? hb : 0);
-    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
-    auto start = [&](uint64_t i) {
-        const uint64_t r = blockIdx.x + i * gridDim.x;
-        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+    uint64_t next = blockIdx.x;                     // thread 0: the row to be fetched next, and its stage
+    uint32_t next_st = 0;
+    auto start = [&] {
+        if (next >= p.rows) return;
+        const uint64_t r = next;
+        const uint32_t bar = saddr(full + next_st), dst = saddr(stages) + next_st * stage_bytes;
+        next += gridDim.x;
+        if (++next_st == S) next_st = 0;
         bar_expect_tx(bar, stage_bytes);
         bulk_load(dst, p.dy + r * p.dy_pitch, gb, bar);
         bulk_load(dst + gb, p.h + r * p.h_pitch, hb, bar);
@@ -641,7 +653,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
     float w[NCH][8], acc[NCH][8];
 #pragma unroll
@@ -658,8 +670,8 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __
     __syncthreads();
 
     uint32_t st = 0, phase = 0;
-    for (uint64_t turn = 0; turn < turns; ++turn) {
-        const uint64_t r = blockIdx.x + turn * gridDim.x;
+    uint32_t turn = 0;
+    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
         const float s = p.rstd[r];
         const bool here = bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
@@ -677,8 +689,8 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __
             }
         }
         if (!here) dot = __int_as_float(0x7FC00000);
-        const float m = row_sum(dot, T, slots[turn & 1]) * p.inv_cols;
-        if (t == 0 && turn + S - 1 < turns) start(turn + S - 1);
+        const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
+        if (t == 0) start();
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) {
             const uint32_t c = 8 * (i * T + t);
@@ -708,14 +720,18 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_kernel(const __
 // beside the row in these two are copied with it and not looked at (an allocation never ends within
 // such a word).
 struct Words {
-    uint64_t from;              // address of the first word
-    uint32_t skip, bytes;       // the row's first byte in it; bytes of all words
+    uint64_t from;              // address of the first
+    uint32_t bytes;             // of all
 };
 
 __device__ __forceinline__ Words words_of(const char* row, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(row), first = a & ~15ull;
-    const uint32_t skip = (uint32_t)(a - first);
-    return {first, skip, (skip + bytes + 15) & ~15u};
+    return {first, ((uint32_t)(a - first) + bytes + 15) & ~15u};
+}
+
+// Where a row begins in its first word.
+__device__ __forceinline__ uint32_t skip_of(const char* base, uint64_t r, uint64_t pitch) {
+    return ((uint32_t)reinterpret_cast<uint64_t>(base) + (uint32_t)r * (uint32_t)pitch) & 15u;
 }
 
 __host__ __device__ __forceinline__ uint32_t words_room(uint32_t bytes) { return (bytes + 30) & ~15u; }
@@ -728,12 +744,16 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t x_room = words_room(xb), stage_bytes = x_room + (rb ? words_room(rb) : 0);
-    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
-    auto start = [&](uint64_t i) {
-        const uint64_t r = blockIdx.x + i * gridDim.x;
-        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+    uint64_t next = blockIdx.x;                     // thread 0: the row to be fetched next, and its stage
+    uint32_t next_st = 0;
+    auto start = [&] {
+        if (next >= p.rows) return;
+        const uint64_t r = next;
+        const uint32_t bar = saddr(full + next_st), dst = saddr(stages) + next_st * stage_bytes;
+        next += gridDim.x;
+        if (++next_st == S) next_st = 0;
         const Words x = words_of(p.x + r * p.x_pitch, xb);
-        Words res{0, 0, 0};
+        Words res{0, 0};
         if (rb) res = words_of(p.res + r * p.res_pitch, rb);
         bar_expect_tx(bar, x.bytes + res.bytes);
         bulk_load(dst, reinterpret_cast<const char*>(x.from), x.bytes, bar);
@@ -743,7 +763,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
     float w[E];
 #pragma unroll
@@ -752,30 +772,30 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
     __syncthreads();
 
     uint32_t st = 0, phase = 0;
-    for (uint64_t turn = 0; turn < turns; ++turn) {
-        const uint64_t r = blockIdx.x + turn * gridDim.x;
+    uint32_t turn = 0;
+    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
         const bool here = bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float h[E], sum = 0.0f;
-        load_elements(row + words_of(p.x + r * p.x_pitch, xb).skip, p.x_dt, p.cols, h);
+        load_elements(row + skip_of(p.x, r, p.x_pitch), p.x_dt, p.cols, h);
         if (rb) {
             float q[E];
-            load_elements(row + x_room + words_of(p.res + r * p.res_pitch, rb).skip, p.res_dt, p.cols, q);
+            load_elements(row + x_room + skip_of(p.res, r, p.res_pitch), p.res_dt, p.cols, q);
 #pragma unroll
             for (uint32_t k = 0; k < E; ++k) h[k] += q[k];
         }
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
         if (!here) sum = __int_as_float(0x7FC00000);
-        const float s = rsqrtf(row_sum(sum, T, slots[turn & 1][0]) * p.inv_cols + p.eps);
+        const float s = rsqrtf(row_sum(sum, T, slots[turn][0]) * p.inv_cols + p.eps);
         if (t == 0) {
-            if (turn + S - 1 < turns) start(turn + S - 1);
+            start();
             if (p.rstd) p.rstd[r] = s;
         }
         if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) h[k] *= s * w[k];
-        if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[turn & 1][1], h);
+        if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[turn][1], h);
         store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
         if (++st == S) { st = 0; phase ^= 1; }
     }
@@ -783,18 +803,23 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
 
 template <uint32_t E>
 __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+    launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][32];
     __shared__ uint64_t full[kRingStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
     const uint32_t g_room = words_room(gb), h_room = words_room(hb), stage_bytes = g_room + (p.dres ? 2 : 1) * h_room;
-    const uint64_t turns = (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
-    auto start = [&](uint64_t i) {
-        const uint64_t r = blockIdx.x + i * gridDim.x;
-        const uint32_t st = (uint32_t)(i % S), bar = saddr(full + st), dst = saddr(stages) + st * stage_bytes;
+    uint64_t next = blockIdx.x;                     // thread 0: the row to be fetched next, and its stage
+    uint32_t next_st = 0;
+    auto start = [&] {
+        if (next >= p.rows) return;
+        const uint64_t r = next;
+        const uint32_t bar = saddr(full + next_st), dst = saddr(stages) + next_st * stage_bytes;
+        next += gridDim.x;
+        if (++next_st == S) next_st = 0;
         const Words g = words_of(p.dy + r * p.dy_pitch, gb), h = words_of(p.h + r * p.h_pitch, hb);
-        Words d{0, 0, 0};
+        Words d{0, 0};
         if (p.dres) d = words_of(p.dres + r * p.dres_pitch, hb);
         bar_expect_tx(bar, g.bytes + h.bytes + d.bytes);
         bulk_load(dst, reinterpret_cast<const char*>(g.from), g.bytes, bar);
@@ -805,7 +830,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint64_t i = 0; i + 1 < S && i < turns; ++i) start(i);
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
     float w[E], acc[E];
 #pragma unroll
@@ -817,14 +842,14 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
     __syncthreads();
 
     uint32_t st = 0, phase = 0;
-    for (uint64_t turn = 0; turn < turns; ++turn) {
-        const uint64_t r = blockIdx.x + turn * gridDim.x;
+    uint32_t turn = 0;
+    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
         const float s = p.rstd[r];
         const bool here = bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float g[E], n[E], dot = 0.0f;
-        load_elements(row + words_of(p.dy + r * p.dy_pitch, gb).skip, p.dy_dt, p.cols, g);
-        load_elements(row + g_room + words_of(p.h + r * p.h_pitch, hb).skip, p.h_dt, p.cols, n);
+        load_elements(row + skip_of(p.dy, r, p.dy_pitch), p.dy_dt, p.cols, g);
+        load_elements(row + g_room + skip_of(p.h, r, p.h_pitch), p.h_dt, p.cols, n);
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) {
             n[k] *= s;
@@ -833,12 +858,12 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
             dot += g[k] * n[k];
         }
         if (!here) dot = __int_as_float(0x7FC00000);
-        const float m = row_sum(dot, T, slots[turn & 1]) * p.inv_cols;
-        if (t == 0 && turn + S - 1 < turns) start(turn + S - 1);
+        const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
+        if (t == 0) start();
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) g[k] = s * (g[k] - n[k] * m);
         if (p.dres) {
-            load_elements(row + g_room + h_room + words_of(p.dres + r * p.dres_pitch, hb).skip, p.h_dt, p.cols, n);
+            load_elements(row + g_room + h_room + skip_of(p.dres, r, p.dres_pitch), p.h_dt, p.cols, n);
 #pragma unroll
             for (uint32_t k = 0; k < E; ++k) g[k] += n[k];
         }
@@ -855,6 +880,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* part
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
     float v = 0.0f;
+    wait_previous();
     if (c < cols) {
 #pragma unroll 10
         for (uint32_t i = warp; i < partials; i += 32) v += partial[(uint64_t)i * cols + c];
@@ -887,22 +913,23 @@ struct Ring {
     uint32_t nch, threads, ctas, stages, smem;       // ctas: of an SM; 0: no ring for these rows
 };
 
-// Chunks (vec): two a thread up to 512 threads, then four (twice the registers).  Elements: 8 a thread up to
-// 256 threads, then 16.  Rows of one warp are left to the other forms.  As many CTAs as make `threads_per_sm`
-// threads an SM (half as many with four chunks), fewer where three stages each would not fit; then as
-// many stages as fit.
-Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t threads_per_sm) {
+// Chunks (vec): one a thread up to `one` columns, two up to 512 threads, then four.  Elements: 8 a thread up to
+// `one` columns, then 16.  Rows of one warp are left to the other forms.  threads: of an SM with one, two
+// and four chunks (what the registers allow), in as many CTAs, fewer where three stages each would not
+// fit; then as many stages as fit, but no more than `stages` where an SM has four CTAs or more.
+Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t one, const uint32_t (&threads)[3], uint32_t stages) {
     Ring g{};
     if (3 * stage > kRingSmem) return g;
     const uint32_t stage_bytes = (uint32_t)stage;
-    for (uint32_t nch : {vec ? 2u : 1u, vec ? 4u : 2u}) {
-        g.nch = nch;
-        g.threads = ((cols + 8 * nch - 1) / (8 * nch) + 31) / 32 * 32;
-        if (g.threads <= (nch == 1 ? 256 : kRingThreads)) break;
+    uint32_t i = 0;
+    for (; i < (vec ? 3 : 2); ++i) {
+        g.nch = 1u << i;
+        g.threads = ((cols + 8 * g.nch - 1) / (8 * g.nch) + 31) / 32 * 32;
+        if (g.threads <= kRingThreads && (i > 0 || cols <= one)) break;
     }
     if (g.threads < 64 || g.threads > kRingThreads) return {};
-    g.ctas = std::min(std::min(std::max(threads_per_sm * 2 / std::max(g.nch, 2u) / g.threads, 1u), kRingSmem / (3 * stage_bytes)), 16u);
-    g.stages = std::min(kRingStages, kRingSmem / (g.ctas * stage_bytes));
+    g.ctas = std::min({std::max(threads[i] / g.threads, 1u), kRingSmem / (3 * stage_bytes), 16u});
+    g.stages = std::min(g.ctas >= 4 ? stages : kRingStages, kRingSmem / (g.ctas * stage_bytes));
     g.smem = g.stages * stage_bytes;
     return g;
 }
@@ -924,10 +951,13 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t xe = p.x_dt == DTT_BF16 ? 2 : 4, re = p.res ? (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t sms = sm_count();
     const uint64_t xb = (uint64_t)p.cols * xe, rb = (uint64_t)p.cols * re;
-    const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, 1024);
+    // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
+    // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
+    // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
+    const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, p.rows >= 32 * sms ? 2 : kRingStages);
     if (g.ctas && p.rows >= 2 * sms && !(vec && p.cols <= kFwdWarpCols)) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
-        auto kernel = vec ? (g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
+        auto kernel = vec ? (g.nch == 1 ? rmsnorm_fwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_fwd_ring_elements_kernel<8> : rmsnorm_fwd_ring_elements_kernel<16>);
         kernel<<<grid, g.threads, g.smem, stream>>>(p, g.stages);
         return;
@@ -959,16 +989,16 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
     const uint32_t sms = sm_count();
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
-    const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 512);
+    const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 2048, {1024, 512, 256}, kRingStages);
     if (g.ctas && p.rows >= 2 * sms && !(vec && p.cols <= kBwdWarpCols)) {
-        p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)kMaxPartials});
-        auto kernel = vec ? (g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
+        p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)most_partials(p.cols)});
+        auto kernel = vec ? (g.nch == 1 ? rmsnorm_bwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
         kernel<<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
         return;
     }
     auto walk = [&](uint32_t each) {       // walkers a CTA
-        p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, kMaxPartials);
+        p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, most_partials(p.cols));
         p.walkers = p.partials * each;
     };
     walk(1);
@@ -1049,7 +1079,8 @@ cudaError_t preload_norm_kernels() {
         const cudaError_t e = prepare(k);
         if (e != cudaSuccess) return e;
     }
-    const void* rings[] = {(const void*)rmsnorm_fwd_ring_kernel<2>, (const void*)rmsnorm_fwd_ring_kernel<4>,
+    const void* rings[] = {(const void*)rmsnorm_fwd_ring_kernel<1>, (const void*)rmsnorm_bwd_ring_kernel<1>,
+                           (const void*)rmsnorm_fwd_ring_kernel<2>, (const void*)rmsnorm_fwd_ring_kernel<4>,
                            (const void*)rmsnorm_bwd_ring_kernel<2>, (const void*)rmsnorm_bwd_ring_kernel<4>,
                            (const void*)rmsnorm_fwd_ring_elements_kernel<8>, (const void*)rmsnorm_fwd_ring_elements_kernel<16>,
                            (const void*)rmsnorm_bwd_ring_elements_kernel<8>, (const void*)rmsnorm_bwd_ring_elements_kernel<16>};
@@ -1069,7 +1100,7 @@ extern "C" int dtt_rmsnorm_workspace(const dtt_rmsnorm_desc* d, uint64_t* bytes)
     const int rc = check_desc("dtt_rmsnorm_workspace", d);
     if (rc) return rc;
     if (!bytes) return fail(DTT_EINVAL, "dtt_rmsnorm_workspace: null bytes");
-    *bytes = (uint64_t)kMaxPartials * d->cols * 4;
+    *bytes = (uint64_t)most_partials(d->cols) * d->cols * 4;
     return DTT_OK;
 }
 
@@ -1139,7 +1170,7 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
         (rc = check_rows(who, "dweight", dweight, 0, 1, 0, DTT_F32, true)))
         return rc;
     if (dweight && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 ||
-                    workspace_bytes < (uint64_t)kMaxPartials * d->cols * 4))
+                    workspace_bytes < (uint64_t)most_partials(d->cols) * d->cols * 4))
         return fail(DTT_EINVAL, "%s: the workspace is missing, misaligned or short", who);
     if (rows == 0) {
         if (dweight) DTT_CUDA_TRY(cudaMemsetAsync(dweight, 0, d->cols * 4, stream));
@@ -1175,9 +1206,9 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
     const bool vec = d->cols % 8 == 0 && aligned(dy, dy_pitch, 16) && aligned(h, h_pitch, 16) && aligned(weight, 0, 16) &&
                      aligned(dres, dres ? dres_pitch : 0, 16) && aligned(dx, dx_pitch, 16);
     launch_bwd(p, vec, stream);
-    if (dweight)
-        rmsnorm_dweight_kernel<<<(p.cols + 31) / 32, 1024, 0, stream>>>(p.partial, p.partials, p.cols, dweight);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && dweight)
+        e = launch(rmsnorm_dweight_kernel, (p.cols + 31) / 32, 1024, 0, 0, true, stream, p.partial, p.partials, p.cols, dweight);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }

@@ -204,11 +204,6 @@ __device__ __forceinline__ void tile_of(const GemmParams& p, uint32_t u, uint32_
     }
 }
 
-// The launch after this one may begin (it waits for this one's results itself), and: everything the
-// launch before wrote is there, and it reads nothing any more.
-__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -1437,28 +1432,6 @@ int check_desc(const char* who, const dtt_ortho_desc* d) {
         if (bound > 16.0) return fail(DTT_EINVAL, "%s: step %u's coefficients let the iterate grow past 16", who, k);
     }
     return DTT_OK;
-}
-
-// Launched so that the next kernel's set-up overlaps this one's end (every kernel waits for the one before
-// it before it touches memory), unless `overlap` says otherwise.  cluster: CTAs of a cluster, 0 where the
-// kernel itself says.
-template <class... Params, class... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, bool overlap, cudaStream_t stream,
-                   const Args&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = overlap;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
 // Clusters that can be resident at once: pairs, and splits of 1, 2, 4 and 8 CTAs.

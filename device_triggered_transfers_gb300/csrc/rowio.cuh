@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include <cuda_runtime.h>
+
 #include "dtt_ops.h"
 
 namespace dtt {
@@ -127,6 +129,33 @@ __device__ __forceinline__ void gather(const char* const (&rows)[N], uint32_t dt
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) v[n] = reinterpret_cast<const float*>(rows[n])[c[n]];
     }
+}
+
+// The launch after this one may begin (it waits for this one's results itself), and: everything the
+// launch before wrote is there, and it reads nothing any more.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launched so that its set-up overlaps the end of the kernel before it (for which it waits with
+// wait_previous), unless `overlap` says otherwise.  cluster: CTAs of a cluster, 0 where the kernel itself
+// says.
+template <class... Params, class... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, bool overlap, cudaStream_t stream,
+                   const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = overlap;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
 }  // namespace dtt

@@ -10,6 +10,7 @@ from typing import Optional, Sequence, Tuple, Union
 import device_triggered_transfers_gb300 as D
 
 _CODES = {"bf16": D.BF16, "f32": D.F32, "e4m3": D.E4M3}
+_SIZES = {"bf16": 2, "f32": 4, "e4m3": 1}
 
 
 def _torch_types():
@@ -62,21 +63,22 @@ class RMSNorm:
         types = _torch_types()
         self._x, self._res, self._w, self._y = types[x], types[residual], types[weight], types[y]
         self._f32 = types["f32"]
+        self._xe, self._rese, self._ye = (_SIZES[k] for k in (x, residual, y))
         self.scale_cols = -(-cols // group) if group else 1
         self._workspace = None
         self._ref = C.byref(self.desc)
         self._forward, self._backward = D.lib().dtt_rmsnorm_forward, D.lib().dtt_rmsnorm_backward
 
-    def _rows(self, name: str, t, rows: int, dtype) -> Tuple[int, int]:
-        """(address, pitch in bytes) of a [rows, cols] argument; (0, 0) for None."""
+    def _rows(self, name: str, t, shape, dtype, size: int) -> Tuple[int, int]:
+        """(address, pitch in bytes) of a [rows, cols] argument of `size`-byte elements; (0, 0) for None."""
         if t is None:
             return 0, 0
-        if t.dtype != dtype or tuple(t.shape) != (rows, self.cols):
-            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be {dtype} [{rows}, {self.cols}], not {t.dtype} {tuple(t.shape)}")
+        if t.dtype != dtype or t.shape != shape:
+            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
         row, col = t.stride()
         if not t.is_cuda or (col != 1 and self.cols > 1):
             raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be on the GPU with contiguous rows")
-        return t.data_ptr(), row * t.element_size()
+        return t.data_ptr(), row * size
 
     def _flat(self, name: str, t, n: int, dtype) -> int:
         """Address of a contiguous argument of n elements; 0 for None."""
@@ -90,10 +92,11 @@ class RMSNorm:
         """y, and where given residual_out (= h; may be residual itself), scales ([rows, scale_cols]
         f32, with an e4m3 y) and rstd ([rows] f32, which the backward pass needs)."""
         rows = x.shape[0]
-        xp, xs = self._rows("x", x, rows, self._x)
-        rp, rs = self._rows("residual", residual, rows, self._res)
-        op, os_ = self._rows("residual_out", residual_out, rows, self._res)
-        yp, ys = self._rows("y", y, rows, self._y)
+        shape = (rows, self.cols)
+        xp, xs = self._rows("x", x, shape, self._x, self._xe)
+        rp, rs = self._rows("residual", residual, shape, self._res, self._rese)
+        op, os_ = self._rows("residual_out", residual_out, shape, self._res, self._rese)
+        yp, ys = self._rows("y", y, shape, self._y, self._ye)
         rc = self._forward(self._ref, rows, xp, xs, rp, rs, self._flat("weight", weight, self.cols, self._w),
                            op, os_, yp, ys, self._flat("scales", scales, rows * self.scale_cols, self._f32),
                            self._flat("rstd", rstd, rows, self._f32), D._stream(stream))
@@ -105,10 +108,11 @@ class RMSNorm:
         itself) and, where given, dweight ([cols] f32), from the forward's h and rstd and the
         gradients dy of y and dres of residual_out (None: zero)."""
         rows = dy.shape[0]
-        gp, gs = self._rows("dy", dy, rows, self._x)
-        hp, hs = self._rows("h", h, rows, self._res)
-        sp, ss = self._rows("dres", dres, rows, self._res)
-        xp, xs = self._rows("dx", dx, rows, self._res)
+        shape = (rows, self.cols)
+        gp, gs = self._rows("dy", dy, shape, self._x, self._xe)
+        hp, hs = self._rows("h", h, shape, self._res, self._rese)
+        sp, ss = self._rows("dres", dres, shape, self._res, self._rese)
+        xp, xs = self._rows("dx", dx, shape, self._res, self._rese)
         ws, need = 0, 0
         if dweight is not None:
             if self._workspace is None or self._workspace.buffer.device != dy.device:
