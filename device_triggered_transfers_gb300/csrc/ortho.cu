@@ -1077,6 +1077,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
     // [CTAS sources][128 / CTAS]
     float4* own = reinterpret_cast<float4*>(gram + 2 * BLOCK_BYTES);
     float4* sums = own + RES_SUMS / 16;
+    uint8_t* poly_rest = reinterpret_cast<uint8_t*>(own);   // two blocks, once the sums have been sent
     uint64_t* done = reinterpret_cast<uint64_t*>(sums + RES_SUMS / 16);
     uint64_t* sums_full = done + 1;
     uint64_t* gram_full = done + 2;
@@ -1312,19 +1313,24 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
             for (uint32_t w = 0; w < 4; ++w) {
                 uint4& word = slab_word(gram + half * BLOCK_BYTES, row, 4 * g + w);
                 const uint32_t from[4] = {word.x, word.y, word.z, word.w};
-                uint32_t to[4];
+                uint32_t to[4], rest[4];
 #pragma unroll
                 for (uint32_t e = 0; e < 4; ++e) {
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&from[e]));
-                    to[e] = pack_f16(c * v[8 * w + 2 * e] + b * f.x, c * v[8 * w + 2 * e + 1] + b * f.y);
+                    const float x = c * v[8 * w + 2 * e] + b * f.x, y = c * v[8 * w + 2 * e + 1] + b * f.y;
+                    to[e] = pack_f16(x, y);
+                    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&to[e]));
+                    rest[e] = pack_f16(x - h.x, y - h.y);
                 }
                 word = make_uint4(to[0], to[1], to[2], to[3]);
+                slab_word(poly_rest + half * BLOCK_BYTES, row, 4 * g + w) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
             }
         }
+        // b A + c A A in two f16 terms: the second costs a few MMAs here and takes a third off the error
         product([&] {
-            for (uint32_t n = 0; n < 8; ++n)
-                umma(d_apply, desc_k(saddr(gram + n / 4 * BLOCK_BYTES)) + STEP_K * (n % 4),
-                     desc_of(saddr(hi), BLOCK_BYTES, 1024) + STEP_MN * n, idesc(128, width) | IDESC_B_MN, n != 0);
+            for (uint32_t n = 0; n < 16; ++n)
+                umma(d_apply, desc_k(saddr((n < 8 ? gram : poly_rest) + n % 8 / 4 * BLOCK_BYTES)) + STEP_K * (n % 4),
+                     desc_of(saddr(hi), BLOCK_BYTES, 1024) + STEP_MN * (n % 8), idesc(128, width) | IDESC_B_MN, n != 0);
         });
         const bool last = k + 1 == p.steps;
         for (uint32_t n = 0; n < p.blocks; ++n) {
