@@ -46,10 +46,10 @@ constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_S
 __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 constexpr uint32_t IDESC_B_MN = 1u << 16;            // B stored with N contiguous
 // split form: the tile's f32 sums, and its f16 or bf16 rows, in the shared memory of the stages
-constexpr uint32_t T_PITCH = 132;                    // floats: rows 16 bytes apart in the banks
 constexpr uint32_t T16_PITCH = 130;                  // 16-bit elements: columns fall on different banks
-constexpr uint32_t T16_OFFSET = 128 * T_PITCH * 4;
-static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= STAGES * 2 * HALF_STAGE, "the tile fits the stages");
+constexpr uint32_t T16_OFFSET = 128 * 128 * 4;
+static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= STAGES * 2 * HALF_STAGE && 128 * 128 * 4 <= SLAB_BUFS * 2 * SLAB_BYTES,
+              "the tile fits the stages, the sums of the cluster the slabs");
 
 constexpr uint32_t kStartTile = 64;                  // ortho_start_tiles_kernel: elements a side
 constexpr uint32_t kMaxParts = 1216;                 // ortho_update_kernel: CTAs a matrix at most, eight a SM
@@ -588,12 +588,13 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
 }
 
 // ---- split form --------------------------------------------------------------------------------
-__device__ __forceinline__ float4 load_peer(uint32_t cluster_addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr) : "memory");
-    return v;
+// A copy to a CTA of the cluster that counts, in bytes, on an mbarrier of that CTA.
+__device__ __forceinline__ void push(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(to), "r"(from), "r"(bytes), "r"(bar) : "memory");
 }
+// What the threads wrote to shared memory is there for copies and MMAs that start after a barrier.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One 128 x 128 tile a cluster, its k blocks shared out over the cluster's CTAs (CTAS: one, two, four
 // or eight).  Each CTA leaves its f32 sums in its shared memory; CTA q then adds rows q 128 / CTAs .. of
@@ -604,12 +605,18 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + STAGES * HALF_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sB + STAGES * HALF_STAGE);   // [STAGES]  TMA -> MMA
+    // f32 sums, rows of 32 words of four columns, words swizzled by the row: the CTA's own [128] in place of
+    // the stages, and [CTAS sources][128 / CTAS]
+    float4* tile = reinterpret_cast<float4*>(smem);
+    float4* from = reinterpret_cast<float4*>(sB + STAGES * HALF_STAGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(from + 128 * 32);   // [STAGES]  TMA -> MMA
     uint64_t* empty = full + STAGES;              // [STAGES]  MMA -> TMA
     uint64_t* done = empty + STAGES;              // [1]       every MMA of the tile
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* sums_full = done + 1;               // [1]       the other CTAs' sums
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums_full + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
+    constexpr uint32_t rows = 128 / CTAS, SLICE = rows * 512, MAX_ROWS = rows / EPI_WARPS;
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = cluster_rank();
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < STAGES; ++i) {
@@ -617,9 +624,11 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
             bar_init(saddr(empty + i), 1);
         }
         bar_init(saddr(done), 1);
+        bar_init(saddr(sums_full), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        bar_expect_tx(saddr(sums_full), (CTAS - 1) * SLICE);
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(128) : "memory");
@@ -630,7 +639,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
         prefetch_map(&p.tmB);
     }
     tc_fence_before();
-    __syncthreads();
+    if (CTAS > 1) cluster_sync_all();             // the barriers of all CTAs exist
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     launch_next();
@@ -640,7 +650,6 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
     tile_of<P>(p, blockIdx.x / CTAS, m, i, j);
     const uint32_t kblocks = (p.K + BK - 1) / BK, k0 = kblocks * q / CTAS, k1 = kblocks * (q + 1) / CTAS;
     // the rows that this CTA stores: a warp a row, four columns a lane, and what they need besides the sums
-    constexpr uint32_t rows = 128 / CTAS, MAX_ROWS = rows / EPI_WARPS;
     const uint32_t first = q * rows, cols = P == APPLY ? p.L : p.S;
     const uint64_t pitch = P == APPLY ? p.l_pitch : p.s_pitch;
     const uint32_t c = j * 128 + 4 * lane;
@@ -705,44 +714,46 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
     __syncwarp();
     __syncthreads();                              // the MMAs are done and no load is under way
     tc_fence_after();
-    float* tile = reinterpret_cast<float*>(smem);
     if (warp < EPI_WARPS) {                       // a lane a row, 64 columns a warp
-        const uint32_t row = 32 * (warp % 4);
-#pragma unroll 1
-        for (uint32_t g = warp / 4 * 2; g < warp / 4 * 2 + 2; ++g) {
-            float v[32];
-            tmem_ld32(tmem_base + (row << 16) + g * 32, v);
-            float4* to = reinterpret_cast<float4*>(tile + (row + lane) * T_PITCH + g * 32);
+        const uint32_t row = 32 * (warp % 4) + lane;
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        for (uint32_t g = 0; g < 2; ++g) {
+            float v[32];
+            tmem_ld32(tmem_base + ((32 * (warp % 4)) << 16) + 64 * (warp / 4) + 32 * g, v);
+#pragma unroll
+            for (uint32_t w = 0; w < 8; ++w)
+                tile[row * 32 + ((16 * (warp / 4) + 8 * g + w) ^ (row & 7))] = make_float4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
         }
     }
+    fence_async();
     tc_fence_before();
-    if (CTAS > 1) cluster_sync_all();             // every CTA's sums are there
-    else __syncthreads();
+    __syncthreads();
     tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(128) : "memory");
+    if (CTAS > 1) {
+        if (threadIdx.x < CTAS && threadIdx.x != q)
+            push(at_rank(saddr(from) + q * SLICE, threadIdx.x), saddr(tile) + threadIdx.x * SLICE, SLICE, at_rank(saddr(sums_full), threadIdx.x));
+        __syncwarp();
+        if (warp < EPI_WARPS && !bar_wait(saddr(sums_full), 0, abort_flag) && lane == 0) fail();
+        __syncwarp();
+        // here: every CTA has what was sent to it (the wait is at the end, before the CTA leaves)
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    }
 
     const bool turned = P == APPLY ? p.out && p.transposed : i != j;   // the rows are stored as columns (too)
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + T16_OFFSET);
-    // all the sums that the thread adds are under way before it adds the first
-    float4 sums[MAX_ROWS][CTAS];
-#pragma unroll
-    for (uint32_t k = 0; k < MAX_ROWS; ++k)
-#pragma unroll
-        for (uint32_t o = 0; o < CTAS; ++o) {
-            const float* at = tile + (first + warp % EPI_WARPS + EPI_WARPS * k) * T_PITCH + 4 * lane;
-            sums[k][o] = CTAS == 1 ? *reinterpret_cast<const float4*>(at) : load_peer(at_rank(saddr(at), o));
-        }
 #pragma unroll
     for (uint32_t k = 0; k < MAX_ROWS; ++k) {
         const uint32_t n = warp + EPI_WARPS * k, r = i * 128 + first + n;
         if (warp >= EPI_WARPS) break;
-        float4 v = sums[k][0];
+        const uint32_t word = lane ^ ((first + n) & 7);
+        float4 sums[CTAS];
 #pragma unroll
-        for (uint32_t o = 1; o < CTAS; ++o)
-            v = make_float4(v.x + sums[k][o].x, v.y + sums[k][o].y, v.z + sums[k][o].z, v.w + sums[k][o].w);
+        for (uint32_t o = 0; o < CTAS; ++o) sums[o] = o == q ? tile[(first + n) * 32 + word] : from[(o * rows + n) * 32 + word];
+        float4 v = sums[0];
+#pragma unroll
+        for (uint32_t o = 1; o < CTAS; ++o) v = make_float4(v.x + sums[o].x, v.y + sums[o].y, v.z + sums[o].z, v.w + sums[o].w);
         const bool in = r < p.S && c < cols;      // rows are padded to 64 elements: then all four are the array's
         const uint64_t to = ((uint64_t)m * p.S + r) * pitch + c;
         if (P == POLY && in) {
@@ -813,7 +824,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
             }
         }
     }
-    if (CTAS > 1) cluster_sync_all();             // no CTA leaves while its sums may be read
+    if (CTAS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");   // its sums have been sent and received
 }
 
 struct UpdateParams {
@@ -1030,11 +1041,6 @@ struct ResidentParams {
     float coeffs[DTT_ORTHO_MAX_STEPS][3];
 };
 
-// A copy to a CTA of the cluster that counts, in bytes, on an mbarrier of that CTA.
-__device__ __forceinline__ void push(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(to), "r"(from), "r"(bytes), "r"(bar) : "memory");
-}
 // 16 words of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile(
@@ -1056,7 +1062,6 @@ __device__ __forceinline__ float load_peer1(uint32_t cluster_addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // S <= 128: one cluster of CTAS a matrix, from the update to the result: hi stays in shared memory, lo in
 // TMEM.  CTA q holds columns 64 blocks q .. of X; a block of 64 columns by 128 rows serves as it lies
