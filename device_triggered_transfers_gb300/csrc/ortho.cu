@@ -596,6 +596,99 @@ __device__ __forceinline__ void push(uint32_t to, uint32_t from, uint32_t bytes,
 // What the threads wrote to shared memory is there for copies and MMAs that start after a barrier.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Four columns from column c of output row r of matrix m, a lane's share of a tile's row: v with what the
+// product adds to it (held, rest: A, or hi and lo, of the same place), stored, and kept in `turn` (or null)
+// for store_turned.
+template <Product P>
+__device__ __forceinline__ void store_four(const GemmParams& p, uint32_t m, uint32_t r, uint32_t c, float4 v, uint2 held, uint2 rest, uint32_t* turn) {
+    const uint32_t cols = P == APPLY ? p.L : p.S;
+    const bool in = r < p.S && c < cols;          // rows are padded to 64 elements: then all four are the array's
+    const uint64_t to = ((uint64_t)m * p.S + r) * (P == APPLY ? p.l_pitch : p.s_pitch) + c;
+    if (P == POLY && in) {
+        const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&held.x)), g1 = __half22float2(*reinterpret_cast<const __half2*>(&held.y));
+        v = make_float4(p.c * v.x + p.b * g0.x, p.c * v.y + p.b * g0.y, p.c * v.z + p.b * g1.x, p.c * v.w + p.b * g1.y);
+    }
+    if (P == APPLY && in) {
+        const float2 x0 = join(held.x, rest.x), x1 = join(held.y, rest.y);
+        v = make_float4(v.x + p.a * x0.x, v.y + p.a * x0.y, v.z + p.a * x1.x, v.w + p.a * x1.y);
+        if (!p.out) {
+            uint32_t unused;
+            uint2 l;
+            part(v.x, v.y, unused, l.x);
+            part(v.z, v.w, unused, l.y);
+            *reinterpret_cast<uint2*>(p.lo + to) = l;
+        }
+    }
+    uint32_t e01, e23;                            // the four as stored
+    if (P == APPLY && p.out) {
+        e01 = pack_bf16(v.x * p.scale, v.y * p.scale);
+        e23 = pack_bf16(v.z * p.scale, v.w * p.scale);
+    } else {
+        e01 = pack_f16(v.x, v.y);
+        e23 = pack_f16(v.z, v.w);
+    }
+    if (turn) {
+        turn[0] = in ? e01 : 0;
+        turn[1] = in ? e23 : 0;
+    }
+    if (!in || (P == APPLY && p.out && p.transposed)) return;
+    if (P == APPLY && p.out) {
+        char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)r * p.out_pitch + (uint64_t)c * 2;
+        if (p.out_vec && c + 4 <= p.L) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(e01, e23);
+        } else {
+            const uint32_t e[4] = {e01 & 0xFFFF, e01 >> 16, e23 & 0xFFFF, e23 >> 16};
+#pragma unroll
+            for (uint32_t x = 0; x < 4; ++x)
+                if (c + x < p.L) reinterpret_cast<uint16_t*>(out)[x] = (uint16_t)e[x];
+        }
+    } else {
+        *reinterpret_cast<uint2*>(p.out16 + to) = make_uint2(e01, e23);
+    }
+}
+
+// `rows` rows from row r0 (of the columns c0 .. + 127) as columns: a thread a column, whose elements
+// neighbour each other in row c0 + thread of the result.
+template <Product P>
+__device__ __forceinline__ void store_turned(const GemmParams& p, uint32_t m, uint32_t r0, uint32_t c0, uint32_t rows, const uint16_t* turn) {
+    const uint32_t c = c0 + threadIdx.x;
+    if (threadIdx.x >= 128 || c >= (P == APPLY ? p.L : p.S)) return;
+    for (uint32_t n = 0; n < rows && r0 + n < p.S; n += 8) {
+        const uint32_t r = r0 + n;
+        uint32_t e[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) e[k] = turn[(n + k) * T16_PITCH + threadIdx.x];
+        const uint4 w = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        if (P != APPLY) {
+            *reinterpret_cast<uint4*>(p.out16 + ((uint64_t)m * p.S + c) * p.s_pitch + r) = w;
+        } else {
+            char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)c * p.out_pitch + (uint64_t)r * 2;
+            if (p.out_vec && r + 8 <= p.S) {
+                *reinterpret_cast<uint4*>(out) = w;
+            } else {
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    if (r + k < p.S) reinterpret_cast<uint16_t*>(out)[k] = (uint16_t)e[k];
+            }
+        }
+    }
+}
+
+// What store_four needs for the thread's rows of a tile (rows first + warp + 8 k), fetched ahead.
+template <Product P, uint32_t N>
+__device__ __forceinline__ void fetch_fours(const GemmParams& p, uint32_t m, uint32_t r0, uint32_t c, uint2 (&held)[N], uint2 (&rest)[N]) {
+    if (P == GRAM || threadIdx.x / 32 >= EPI_WARPS || c >= (P == APPLY ? p.L : p.S)) return;
+#pragma unroll
+    for (uint32_t k = 0; k < N; ++k) {
+        const uint32_t r = r0 + threadIdx.x / 32 + EPI_WARPS * k;
+        if (r < p.S) {
+            const uint64_t at = ((uint64_t)m * p.S + r) * (P == APPLY ? p.l_pitch : p.s_pitch) + c;
+            held[k] = *reinterpret_cast<const uint2*>((P == POLY ? p.gram : p.hi) + at);
+            if (P == APPLY) rest[k] = *reinterpret_cast<const uint2*>(p.lo + at);
+        }
+    }
+}
+
 // One 128 x 128 tile a cluster, its k blocks shared out over the cluster's CTAs (CTAS: one, two, four
 // or eight).  Each CTA leaves its f32 sums in its shared memory; CTA q then adds rows q 128 / CTAs .. of
 // all of them, in the CTAs' order, through distributed shared memory, and stores those rows.
@@ -650,21 +743,9 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
     tile_of<P>(p, blockIdx.x / CTAS, m, i, j);
     const uint32_t kblocks = (p.K + BK - 1) / BK, k0 = kblocks * q / CTAS, k1 = kblocks * (q + 1) / CTAS;
     // the rows that this CTA stores: a warp a row, four columns a lane, and what they need besides the sums
-    const uint32_t first = q * rows, cols = P == APPLY ? p.L : p.S;
-    const uint64_t pitch = P == APPLY ? p.l_pitch : p.s_pitch;
-    const uint32_t c = j * 128 + 4 * lane;
-    uint2 held[P == GRAM ? 1 : MAX_ROWS], rest[P == APPLY ? MAX_ROWS : 1];
-    if (P != GRAM && warp < EPI_WARPS && c < cols) {
-#pragma unroll
-        for (uint32_t k = 0; k < MAX_ROWS; ++k) {
-            const uint32_t n = warp + EPI_WARPS * k, r = i * 128 + first + n;
-            if (r < p.S) {
-                const uint64_t at = ((uint64_t)m * p.S + r) * pitch + c;
-                held[k] = *reinterpret_cast<const uint2*>((P == POLY ? p.gram : p.hi) + at);
-                if (P == APPLY) rest[k] = *reinterpret_cast<const uint2*>(p.lo + at);
-            }
-        }
-    }
+    const uint32_t first = q * rows, c = j * 128 + 4 * lane;
+    uint2 held[MAX_ROWS], rest[MAX_ROWS];
+    fetch_fours<P>(p, m, i * 128 + first, c, held, rest);
     auto fail = [&]() {
         *abort_flag = 1;
         atomicAdd(p.err, 1u);
@@ -754,77 +835,161 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
         float4 v = sums[0];
 #pragma unroll
         for (uint32_t o = 1; o < CTAS; ++o) v = make_float4(v.x + sums[o].x, v.y + sums[o].y, v.z + sums[o].z, v.w + sums[o].w);
-        const bool in = r < p.S && c < cols;      // rows are padded to 64 elements: then all four are the array's
-        const uint64_t to = ((uint64_t)m * p.S + r) * pitch + c;
-        if (P == POLY && in) {
-            const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&held[k].x)), g1 = __half22float2(*reinterpret_cast<const __half2*>(&held[k].y));
-            v = make_float4(p.c * v.x + p.b * g0.x, p.c * v.y + p.b * g0.y, p.c * v.z + p.b * g1.x, p.c * v.w + p.b * g1.y);
+        store_four<P>(p, m, r, c, v, held[k], rest[k], turned ? reinterpret_cast<uint32_t*>(turn + n * T16_PITCH + 4 * lane) : nullptr);
+    }
+    __syncthreads();
+    if (turned) store_turned<P>(p, m, i * 128 + first, j * 128, rows, turn);
+    if (CTAS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");   // its sums have been sent and received
+}
+
+// S <= 256, APPLY with its own b A + c A A: one 128 x 128 tile a CTA.  All of A (as two row blocks) and the
+// tile's columns of X are loaded at once; b A + c A A of the tile's rows takes their place in A.  A launch
+// of POLY costs 6 us at these sizes, working its rows out again in every CTA 3 us.
+constexpr uint32_t FUSED_SMEM = 1024 /* alignment slack */ + (8 + 4) * HALF_STAGE + 256;
+static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= 8 * HALF_STAGE, "the tile fits A's place");
+
+__global__ void __launch_bounds__(THREADS, 1) ortho_fused_kernel(const __grid_constant__ GemmParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;                           // [4 blocks of 64 k][2 blocks of 128 rows]
+    uint8_t* sX = sA + 8 * HALF_STAGE;            // [4 blocks of 64 k], 128 columns
+    uint64_t* a_full = reinterpret_cast<uint64_t*>(sX + 4 * HALF_STAGE);   // [4]
+    uint64_t* x_full = a_full + 4;
+    uint64_t* done = x_full + 1;                  // [2]       the MMAs of b A + c A A; of the tile
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (uint32_t k = 0; k < 4; ++k) bar_init(saddr(a_full + k), 1);
+        bar_init(saddr(x_full), 1);
+        bar_init(saddr(done), 1);
+        bar_init(saddr(done + 1), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == TMA_WARP && lane == 0) {
+        prefetch_map(&p.tmA);
+        prefetch_map(&p.tmB);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t d_poly = *tmem_slot, d_tile = d_poly + 256;
+    launch_next();
+    wait_previous();
+
+    uint32_t m, i, j;
+    tile_of<APPLY>(p, blockIdx.x, m, i, j);
+    const uint32_t kblocks = (p.S + BK - 1) / BK, wide = p.S > 128 ? 256 : 128;    // 256: both row blocks of A
+    constexpr uint32_t ROWS = 128 / EPI_WARPS;
+    const uint32_t c = j * 128 + 4 * lane;
+    uint2 held[ROWS], rest[ROWS];
+    fetch_fours<APPLY>(p, m, i * 128, c, held, rest);
+    auto wait = [&](uint64_t* bar) {
+        if (!bar_wait(saddr(bar), 0, abort_flag) && lane == 0) {
+            *abort_flag = 1;
+            atomicAdd(p.err, 1u);
         }
-        if (P == APPLY && in) {
-            const float2 x0 = join(held[k].x, rest[k].x), x1 = join(held[k].y, rest[k].y);
-            v = make_float4(v.x + p.a * x0.x, v.y + p.a * x0.y, v.z + p.a * x1.x, v.w + p.a * x1.y);
-            if (!p.out) {
-                uint32_t unused;
-                uint2 l;
-                part(v.x, v.y, unused, l.x);
-                part(v.z, v.w, unused, l.y);
-                *reinterpret_cast<uint2*>(p.lo + to) = l;
+        __syncwarp();
+    };
+    if (warp == TMA_WARP) {
+        if (lane == 0) {
+            for (uint32_t k = 0; k < kblocks; ++k) {
+                bar_expect_tx(saddr(a_full + k), wide / 128 * HALF_STAGE);
+                for (uint32_t h = 0; h < wide / 128; ++h)
+                    tma_load_3d(saddr(sA + (2 * k + h) * HALF_STAGE), &p.tmA, (int32_t)(k * BK), (int32_t)(h * 128), (int32_t)m, saddr(a_full + k));
             }
+            bar_expect_tx(saddr(x_full), kblocks * HALF_STAGE);
+            for (uint32_t k = 0; k < kblocks; ++k)
+                for (uint32_t h = 0; h < 2; ++h)
+                    tma_load_3d(saddr(sX + k * HALF_STAGE + h * (HALF_STAGE / 2)), &p.tmB, (int32_t)(j * 128 + 64 * h), (int32_t)(k * BK), (int32_t)m, saddr(x_full));
         }
-        uint32_t e01, e23;                        // the four as stored
-        if (P == APPLY && p.out) {
-            e01 = pack_bf16(v.x * p.scale, v.y * p.scale);
-            e23 = pack_bf16(v.z * p.scale, v.w * p.scale);
-        } else {
-            e01 = pack_f16(v.x, v.y);
-            e23 = pack_f16(v.z, v.w);
+        __syncwarp();
+        for (uint32_t k = 0; k < kblocks; ++k) wait(a_full + k);   // every load has landed before the CTA can leave
+        wait(x_full);
+    } else if (warp == MMA_WARP) {
+        for (uint32_t k = 0; k < kblocks; ++k) {
+            wait(a_full + k);
+            tc_fence_after();
+            if (lane == 0)
+                for (uint32_t n = 0; n < 4; ++n)
+                    umma(d_poly, desc_k(saddr(sA + (2 * k + i) * HALF_STAGE)) + STEP_K * n, desc_k(saddr(sA + 2 * k * HALF_STAGE)) + STEP_K * n,
+                         idesc(128, wide), (k | n) != 0);
         }
-        if (turned) {
-            uint32_t* row = reinterpret_cast<uint32_t*>(turn + n * T16_PITCH + 4 * lane);
-            row[0] = in ? e01 : 0;
-            row[1] = in ? e23 : 0;
-        }
-        if (!in || (P == APPLY && p.out && p.transposed)) continue;
-        if (P == APPLY && p.out) {
-            char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)r * p.out_pitch + (uint64_t)c * 2;
-            if (p.out_vec && c + 4 <= p.L) {
-                *reinterpret_cast<uint2*>(out) = make_uint2(e01, e23);
-            } else {
-                const uint32_t e[4] = {e01 & 0xFFFF, e01 >> 16, e23 & 0xFFFF, e23 >> 16};
+        if (lane == 0) umma_commit(saddr(done));
+        __syncwarp();
+    }
+    if (warp < EPI_WARPS) {                       // a lane a row; a warp every other 32 columns
+        wait(done);
+        tc_fence_after();
+        const uint32_t row = 32 * (warp % 4) + lane;
+        for (uint32_t g = warp / 4; g < 2 * kblocks; g += 2) {
+            float v[32];
+            tmem_ld32(d_poly + ((32 * (warp % 4)) << 16) + 32 * g, v);
 #pragma unroll
-                for (uint32_t x = 0; x < 4; ++x)
-                    if (c + x < p.L) reinterpret_cast<uint16_t*>(out)[x] = (uint16_t)e[x];
+            for (uint32_t w = 0; w < 4; ++w) {
+                uint4& word = slab_word(sA + (2 * (g / 2) + i) * HALF_STAGE, row, 4 * (g % 2) + w);
+                const uint32_t old[4] = {word.x, word.y, word.z, word.w};
+                uint32_t to[4];
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&old[e]));
+                    to[e] = pack_f16(p.c * v[8 * w + 2 * e] + p.b * f.x, p.c * v[8 * w + 2 * e + 1] + p.b * f.y);
+                }
+                word = make_uint4(to[0], to[1], to[2], to[3]);
             }
-        } else {
-            *reinterpret_cast<uint2*>(p.out16 + to) = make_uint2(e01, e23);
+        }
+        fence_async();
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        wait(x_full);
+        tc_fence_after();
+        if (lane == 0) {
+            for (uint32_t k = 0; k < 4 * kblocks; ++k)
+                umma(d_tile, desc_k(saddr(sA + (2 * (k / 4) + i) * HALF_STAGE)) + STEP_K * (k % 4),
+                     desc_mn(saddr(sX + k / 4 * HALF_STAGE)) + STEP_MN * (k % 4), idesc(128, 128) | IDESC_B_MN, k != 0);
+            umma_commit(saddr(done + 1));
+        }
+        __syncwarp();
+    }
+    wait(done + 1);                               // all: the MMAs are done, A's place is free
+    tc_fence_after();
+    float4* tile = reinterpret_cast<float4*>(smem);
+    if (warp < EPI_WARPS) {
+        const uint32_t row = 32 * (warp % 4) + lane;
+#pragma unroll
+        for (uint32_t g = 0; g < 2; ++g) {
+            float v[32];
+            tmem_ld32(d_tile + ((32 * (warp % 4)) << 16) + 64 * (warp / 4) + 32 * g, v);
+#pragma unroll
+            for (uint32_t w = 0; w < 8; ++w)
+                tile[row * 32 + ((16 * (warp / 4) + 8 * g + w) ^ (row & 7))] = make_float4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(d_poly), "r"(512) : "memory");
+    const bool turned = p.out && p.transposed;
+    uint16_t* turn = reinterpret_cast<uint16_t*>(smem + T16_OFFSET);
+    if (warp < EPI_WARPS) {
+#pragma unroll
+        for (uint32_t k = 0; k < ROWS; ++k) {
+            const uint32_t n = warp + EPI_WARPS * k;
+            store_four<APPLY>(p, m, i * 128 + n, c, tile[n * 32 + (lane ^ (n & 7))], held[k], rest[k],
+                              turned ? reinterpret_cast<uint32_t*>(turn + n * T16_PITCH + 4 * lane) : nullptr);
         }
     }
     __syncthreads();
-    // a thread a column of the tile: `rows` neighbouring elements of row j 128 + t of the result
-    const uint32_t tc = j * 128 + threadIdx.x;
-    if (turned && threadIdx.x < 128 && tc < cols) {
-        for (uint32_t n = 0; n < rows; n += 8) {
-            const uint32_t r = i * 128 + first + n;
-            if (r >= p.S) break;
-            uint32_t e[8];
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) e[k] = turn[(n + k) * T16_PITCH + threadIdx.x];
-            const uint4 w = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-            if (P != APPLY) {
-                *reinterpret_cast<uint4*>(p.out16 + ((uint64_t)m * p.S + tc) * p.s_pitch + r) = w;
-            } else {
-                char* out = p.out + (uint64_t)m * p.out_stride + (uint64_t)tc * p.out_pitch + (uint64_t)r * 2;
-                if (p.out_vec && r + 8 <= p.S) {
-                    *reinterpret_cast<uint4*>(out) = w;
-                } else {
-#pragma unroll
-                    for (uint32_t k = 0; k < 8; ++k)
-                        if (r + k < p.S) reinterpret_cast<uint16_t*>(out)[k] = (uint16_t)e[k];
-                }
-            }
-        }
-    }
-    if (CTAS > 1) asm volatile("barrier.cluster.wait;" ::: "memory");   // its sums have been sent and received
+    if (turned) store_turned<APPLY>(p, m, i * 128, j * 128, 128, turn);
 }
 
 struct UpdateParams {
@@ -1491,6 +1656,7 @@ Fit fit_of(int device, uint32_t sms) {
 struct Form {
     bool pair;
     uint32_t tn, ctas;           // pair: columns of a tile; split: CTAs of a cluster
+    double us;                   // estimated
 };
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); }
@@ -1513,7 +1679,7 @@ Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t bat
         const double t = 8.0 + rounds * (0.3 + kblocks * (tn == 256 ? 0.275 : 0.21));
         if (t < least) {
             least = t;
-            best = {true, tn, 0};
+            best = {true, tn, 0, t};
         }
     }
     for (uint32_t n = 0; n < 4 && (1u << n) <= kblocks; ++n) {
@@ -1522,10 +1688,15 @@ Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t bat
         const double t = 0.8 + rounds * (4.6 + 0.6 * (ctas > 1) + 0.5 * (ctas > 4) + 0.36 * ceil_div(kblocks, ctas));
         if (t < least) {
             least = t;
-            best = {false, 128, ctas};
+            best = {false, 128, ctas, t};
         }
     }
     return best;
+}
+
+// The same for POLY and APPLY in one (S <= 256): 9 us a round of tiles, measured.
+double fused_us(uint64_t S, uint64_t L, uint32_t batch, uint32_t sms) {
+    return 0.8 + 9.0 * ceil_div((uint64_t)tiles_of(false, 128, 128, S, L) * batch, sms);
 }
 
 // CTAs of a cluster that hold S x L in shared memory: as few as can (A crosses them all); 0: none can.
@@ -1572,6 +1743,8 @@ cudaError_t preload_ortho_kernels() {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RES_SMEM);
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(ortho_resident_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = prepare_kernel(ortho_fused_kernel);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ortho_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FUSED_SMEM);
     if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<true>);
     if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<false>);
     if (e == cudaSuccess) e = prepare_kernel(ortho_start_kernel);
@@ -1593,6 +1766,7 @@ struct dtt_ortho {
     CUtensorMap hi_rows[2], lo_rows, gram, poly;
     // boxes of 64 x 64: the N-contiguous operand of the last product, and mirrored blocks
     CUtensorMap hi_cols[2], gram_blocks, poly_blocks;
+    bool fused;                  // POLY within APPLY
     uint32_t resident;           // CTAs of a cluster in the resident form; 0: a launch a product
     Fit fit;
     Form form[3];                // of each Product
@@ -1631,6 +1805,7 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     o->form[GRAM] = form_of(true, l.S, l.S, l.L, d->batch, o->fit);
     o->form[POLY] = form_of(true, l.S, l.S, l.S, d->batch, o->fit);
     o->form[APPLY] = form_of(false, l.S, l.L, l.S, d->batch, o->fit);
+    o->fused = l.S <= 256 && fused_us(l.S, l.L, d->batch, o->sms) < o->form[POLY].us + o->form[APPLY].us;
     bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->gram_blocks, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 64) &&
@@ -1755,8 +1930,8 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         g.K = g.S;
         g.gram = g.out16;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.poly);
-        DTT_CUDA_TRY(launch_product<POLY>(g, o->form[POLY], o->fit.pairs, stream));
-        g.tmA = o->poly;
+        if (!o->fused) DTT_CUDA_TRY(launch_product<POLY>(g, o->form[POLY], o->fit.pairs, stream));
+        g.tmA = o->fused ? o->gram : o->poly;
         g.tmB = o->hi_cols[now];
         g.in0 = o->hi_rows[now];
         g.in1 = g.out1 = o->lo_rows;
@@ -1765,7 +1940,13 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         g.hi = reinterpret_cast<const __half*>(o->ws + l.hi[now]);
         g.out16 = reinterpret_cast<__half*>(o->ws + l.hi[now ^ 1]);
         g.out = k + 1 == d.steps ? static_cast<char*>(out) : nullptr;
-        DTT_CUDA_TRY(launch_product<APPLY>(g, o->form[APPLY], o->fit.pairs, stream));
+        if (o->fused) {
+            g.tiles_m = ceil_div(g.S, 128);
+            g.tiles = tiles_of(false, 128, 128, g.S, g.L);
+            DTT_CUDA_TRY(launch(ortho_fused_kernel, g.tiles * g.batch, THREADS, FUSED_SMEM, 0, true, stream, g));
+        } else {
+            DTT_CUDA_TRY(launch_product<APPLY>(g, o->form[APPLY], o->fit.pairs, stream));
+        }
     }
     return DTT_OK;
 }
