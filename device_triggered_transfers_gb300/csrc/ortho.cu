@@ -20,6 +20,7 @@
 #include <cstdint>
 #include <mutex>
 #include <new>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -181,6 +182,13 @@ __device__ __forceinline__ void part(float x, float y, uint32_t& hi, uint32_t& l
     hi = pack_f16(x, y);
     const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     lo = pack_f16((x - h.x) * LO_SCALE, (y - h.y) * LO_SCALE);
+}
+
+// Two f16 terms of each value: x = hi + below, to 22 bits.
+__device__ __forceinline__ void two_terms(float x, float y, uint32_t& hi, uint32_t& below) {
+    hi = pack_f16(x, y);
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    below = pack_f16(x - h.x, y - h.y);
 }
 
 // Tile t of a lower triangle counted row by row: (0,0), (1,0), (1,1), (2,0), ...
@@ -843,7 +851,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
 }
 
 // S <= 256, APPLY with its own b A + c A A: one 128 x 128 tile a CTA.  All of A (as two row blocks) and the
-// tile's columns of X are loaded at once; b A + c A A of the tile's rows takes their place in A.  A launch
+// tile's columns of X are loaded at once; b A + c A A of the tile's rows takes their place in A, what its
+// rounding to f16 leaves the other row block's (a second term of the last product).  A launch
 // of POLY costs 6 us at these sizes, working its rows out again in every CTA 3 us.
 constexpr uint32_t FUSED_SMEM = 1024 /* alignment slack */ + (8 + 4) * HALF_STAGE + 256;
 static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= 8 * HALF_STAGE, "the tile fits A's place");
@@ -936,13 +945,14 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_fused_kernel(const __grid_co
             for (uint32_t w = 0; w < 4; ++w) {
                 uint4& word = slab_word(sA + (2 * (g / 2) + i) * HALF_STAGE, row, 4 * (g % 2) + w);
                 const uint32_t old[4] = {word.x, word.y, word.z, word.w};
-                uint32_t to[4];
+                uint32_t to[4], below[4];
 #pragma unroll
                 for (uint32_t e = 0; e < 4; ++e) {
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&old[e]));
-                    to[e] = pack_f16(p.c * v[8 * w + 2 * e] + p.b * f.x, p.c * v[8 * w + 2 * e + 1] + p.b * f.y);
+                    two_terms(p.c * v[8 * w + 2 * e] + p.b * f.x, p.c * v[8 * w + 2 * e + 1] + p.b * f.y, to[e], below[e]);
                 }
                 word = make_uint4(to[0], to[1], to[2], to[3]);
+                slab_word(sA + (2 * (g / 2) + 1 - i) * HALF_STAGE, row, 4 * (g % 2) + w) = make_uint4(below[0], below[1], below[2], below[3]);
             }
         }
         fence_async();
@@ -954,8 +964,9 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_fused_kernel(const __grid_co
         tc_fence_after();
         if (lane == 0) {
             for (uint32_t k = 0; k < 4 * kblocks; ++k)
-                umma(d_tile, desc_k(saddr(sA + (2 * (k / 4) + i) * HALF_STAGE)) + STEP_K * (k % 4),
-                     desc_mn(saddr(sX + k / 4 * HALF_STAGE)) + STEP_MN * (k % 4), idesc(128, 128) | IDESC_B_MN, k != 0);
+                for (uint32_t n = 0; n < 2; ++n)
+                    umma(d_tile, desc_k(saddr(sA + (2 * (k / 4) + (n ? 1 - i : i)) * HALF_STAGE)) + STEP_K * (k % 4),
+                         desc_mn(saddr(sX + k / 4 * HALF_STAGE)) + STEP_MN * (k % 4), idesc(128, 128) | IDESC_B_MN, (k | n) != 0);
             umma_commit(saddr(done + 1));
         }
         __syncwarp();
@@ -1028,20 +1039,21 @@ __global__ void __launch_bounds__(256) ortho_update_kernel(const __grid_constant
     const uint32_t m = blockIdx.y, per_row = (p.cols + W - 1) / W;
     const char* x = p.x + (uint64_t)m * p.x_stride;
     char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
-    const uint64_t total = (uint64_t)p.rows * per_row;
-    const uint64_t step = (uint64_t)p.parts * 256;
+    // at most 2^29 chunks, but up to 2^32 elements
+    using Index = std::conditional_t<VEC, uint32_t, uint64_t>;
+    const Index total = (Index)p.rows * per_row, step = (Index)p.parts * 256;
     float sum = 0.0f;
     launch_next();
     constexpr uint32_t N = VEC ? 4 : 8;                // under way at a time
-    for (uint64_t i0 = (uint64_t)blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += N * step) {
+    for (Index i0 = blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += N * step) {
         float u[N][W], v[N][W];
         const char *xs[N], *moms[N];
         uint32_t cs[N];
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) {
-            const uint64_t i = min(i0 + n * step, total - 1);
+            const Index i = min(i0 + n * step, total - 1);
             const uint32_t r = (uint32_t)(i / per_row);
-            cs[n] = (uint32_t)(i - (uint64_t)r * per_row) * W;
+            cs[n] = (uint32_t)(i - (Index)r * per_row) * W;
             xs[n] = x + r * p.x_pitch;
             moms[n] = mom + r * p.mom_pitch;
         }
@@ -1487,10 +1499,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
 #pragma unroll
                 for (uint32_t e = 0; e < 4; ++e) {
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&from[e]));
-                    const float x = c * v[8 * w + 2 * e] + b * f.x, y = c * v[8 * w + 2 * e + 1] + b * f.y;
-                    to[e] = pack_f16(x, y);
-                    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&to[e]));
-                    rest[e] = pack_f16(x - h.x, y - h.y);
+                    two_terms(c * v[8 * w + 2 * e] + b * f.x, c * v[8 * w + 2 * e + 1] + b * f.y, to[e], rest[e]);
                 }
                 word = make_uint4(to[0], to[1], to[2], to[3]);
                 slab_word(poly_rest + half * BLOCK_BYTES, row, 4 * g + w) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
@@ -1805,7 +1814,8 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     o->form[GRAM] = form_of(true, l.S, l.S, l.L, d->batch, o->fit);
     o->form[POLY] = form_of(true, l.S, l.S, l.S, d->batch, o->fit);
     o->form[APPLY] = form_of(false, l.S, l.L, l.S, d->batch, o->fit);
-    o->fused = l.S <= 256 && fused_us(l.S, l.L, d->batch, o->sms) < o->form[POLY].us + o->form[APPLY].us;
+    // its second term of b A + c A A is worth some time: without it a flat spectrum's error is 1.6 times bf16's own
+    o->fused = l.S <= 256 && fused_us(l.S, l.L, d->batch, o->sms) < 1.3 * (o->form[POLY].us + o->form[APPLY].us);
     bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->gram_blocks, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 64) &&
