@@ -12,9 +12,10 @@
 // A and b A + c A A are symmetric: only tiles on and below the diagonal are computed, and each is
 // stored twice, once transposed (not in the resident form).
 //
-// Three forms: resident (S <= 128, L <= 4096: one launch, X in the shared memory of a cluster); a launch
-// a product by CTA pairs on tiles of 256 rows (large); or on tiles of 128 x 128 split over clusters along
-// k (between).
+// Four forms, the smallest matrices first: resident (S <= 128, L <= 4096: one launch, X in the shared memory
+// of a cluster); a launch a product on tiles of 128 x 128 split over clusters along k (up to S = 256 with
+// the second product within the third); a launch a product by CTA pairs on tiles of 256 rows; and all
+// products of all steps in one launch of such pairs.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -57,13 +58,11 @@ constexpr uint32_t kMaxParts = 1216;                 // ortho_update_kernel: CTA
 
 enum Product { GRAM, POLY, APPLY };
 
+// A product in the split form.
 struct GemmParams {
     CUtensorMap tmA, tmB;        // operands
-    CUtensorMap in0, in1;        // pair form, what the epilogue reads: POLY: A; APPLY: hi and lo
-    CUtensorMap out0, out1;      // and writes: the matrix and, in boxes of 64 x 64, its mirrored part; APPLY: the next hi, and lo
     uint32_t S, L, K;            // output rows S and columns (GRAM, POLY: S; APPLY: L)
     uint32_t batch, tiles_m, tiles;   // tiles: of one matrix
-    uint32_t tn;                 // pair form: columns of a tile, 256 or 128
     uint64_t s_pitch, l_pitch;   // elements between rows of the S-wide and L-wide arrays
     float a, b, c;
     const __half* gram;          // POLY: A
@@ -230,6 +229,110 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 
 // ---- pair form ---------------------------------------------------------------------------------
+// The products first .. last of `steps` steps in one launch.  Alone (first == last, one step) a product
+// follows the launch before it.  With counters, all products of all steps are one sequence of tiles that
+// the clusters, all resident, take in turn, and a tile waits for what it reads: each row block of 256 rows
+// counts, per matrix and product, the CTAs that have stored into it.
+struct PairParams {
+    CUtensorMap hi_rows[2], lo_rows, gram, poly;             // boxes of 64 x 128 (columns x rows)
+    CUtensorMap hi_cols[2], gram_blocks, poly_blocks;        // boxes of 64 x 64
+    uint32_t S, L, batch;
+    uint32_t n, across, tn;      // row blocks of S; tiles of tn columns (256 or 128) across L
+    uint32_t first, last;
+    uint32_t step, steps;        // the first step of this launch (its parity names the hi that is read), and how many
+    uint32_t* counters;          // [batch][GRAM, POLY, APPLY][n], or null
+    char* out;                   // the result of the launch's last step (see Result); null: another launch follows
+    uint64_t out_pitch, out_stride;
+    float scale;
+    uint32_t transposed, out_vec;
+    uint32_t* err;
+    float coeffs[DTT_ORTHO_MAX_STEPS][3];                    // of this launch's steps
+};
+
+// Place u of the sequence: its step (of this launch), product, matrix and tile.  A by rows and b A + c A A
+// by columns, and the last product by rows again, because then the first row blocks of each are complete
+// while the last tiles of it still run.  4096 x 4096 fills 7.0 rounds of the clusters a step, where a launch
+// a product takes 2 + 2 + 4: 990 us for five steps with these, 915 in one sequence.
+struct Tile {
+    uint32_t k, product, m, i, j;
+};
+
+__device__ __forceinline__ Tile pair_tile(const PairParams& p, uint32_t u) {
+    const uint32_t square = p.n * (p.n + 1) / 2, oblong = p.n * p.across;
+    uint32_t per_step = 0;
+    for (uint32_t q = p.first; q <= p.last; ++q) per_step += p.batch * (q == APPLY ? oblong : square);
+    Tile t{};
+    t.k = u / per_step;
+    uint32_t r = u % per_step;
+    for (t.product = p.first;; ++t.product) {
+        const uint32_t all = p.batch * (t.product == APPLY ? oblong : square);
+        if (r < all) break;
+        r -= all;
+    }
+    const uint32_t each = t.product == APPLY ? oblong : square;
+    t.m = r / each;
+    r %= each;
+    if (t.product == APPLY) {
+        t.i = r / p.across;
+        t.j = r % p.across;
+    } else if (t.product == GRAM) {
+        triangle(r, t.i, t.j);
+    } else {
+        triangle(square - 1 - r, t.i, t.j);       // the columns of a triangle are the rows of it turned over
+        const uint32_t i = p.n - 1 - t.j;
+        t.j = p.n - 1 - t.i;
+        t.i = i;
+    }
+    return t;
+}
+
+__device__ __forceinline__ uint32_t pair_tiles(const PairParams& p) {
+    uint32_t per_step = 0;
+    for (uint32_t q = p.first; q <= p.last; ++q) per_step += p.batch * p.n * (q == APPLY ? 2 * p.across : p.n + 1) / 2;
+    return per_step * p.steps;
+}
+
+// Wait (bounded) until `target` CTAs have stored into row block i of product q of matrix m.
+__device__ __forceinline__ bool stored(const PairParams& p, uint32_t m, uint32_t q, uint32_t i, uint32_t target, volatile uint32_t* abort) {
+    const uint32_t* c = p.counters + (m * 3 + q) * p.n + i;
+    for (uint32_t polls = 0; polls < WAIT_LIMIT; ++polls) {
+        uint32_t v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+        if (v >= target) return true;
+        if ((polls & 63) == 63 && *abort) return false;
+        __nanosleep(64);
+    }
+    return false;
+}
+
+// Everything that tile t reads is there, for copies too.  X of step k was complete before b A + c A A of any
+// of its rows could be, so the last product waits for these alone; and whoever read what a tile
+// overwrites had stored before what the tile waits for could be stored.
+__device__ __forceinline__ bool inputs_ready(const PairParams& p, const Tile& t, volatile uint32_t* abort) {
+    if (!p.counters) return true;
+    bool ok = true;
+    if (t.product == GRAM && t.k > 0) {
+        const uint32_t target = 2 * p.across * t.k;
+        ok = stored(p, t.m, APPLY, t.i, target, abort) && stored(p, t.m, APPLY, t.j, target, abort);
+    } else if (t.product == POLY) {
+        const uint32_t target = 2 * p.n * (t.k + 1);
+        ok = stored(p, t.m, GRAM, t.i, target, abort) && stored(p, t.m, GRAM, t.j, target, abort);
+    } else if (t.product == APPLY) {
+        ok = stored(p, t.m, POLY, t.i, 2 * p.n * (t.k + 1), abort);
+    }
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    return ok;
+}
+
+// This thread's copies of tile t have been written: count the CTA.
+__device__ __forceinline__ void count_stored(const PairParams& p, const Tile& t) {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    uint32_t* c = p.counters + (t.m * 3 + t.product) * p.n;
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(c + t.i) : "memory");
+    if (t.product != APPLY && t.i != t.j) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(c + t.j) : "memory");
+}
+
 // A slab is 128 rows by 64 columns of f16 in shared memory, rows of 128 bytes with their 16-byte words
 // swizzled by the row, as the tensor maps move it.  The epilogue's thread with lane `lane` of warp w
 // holds row 32 (w % 4) + lane and columns 32 (w / 4) .. of it: words 4 (w / 4) .. + 3.
@@ -237,21 +340,21 @@ __device__ __forceinline__ uint4& slab_word(uint8_t* slab, uint32_t row, uint32_
     return *reinterpret_cast<uint4*>(slab + row * 128 + ((word ^ (row & 7)) << 4));
 }
 
-// GRAM, POLY: the thread's 32 columns into the slab (which holds A's for POLY) and, for the mirrored
-// part, into the two blocks of 64 columns by 64 rows behind it, as rows.
-template <Product P>
-__device__ __forceinline__ void finish(const GemmParams& p, uint8_t* slab, uint32_t row, uint32_t half, bool mirror, float (&v)[32]) {
+// A, or b A + c A A of the slab's A: the thread's 32 columns into the slab and, for the mirrored part, into
+// the two blocks of 64 columns by 64 rows behind it, as rows.
+template <bool POLYNOMIAL>
+__device__ __forceinline__ void finish(float b, float c, uint8_t* slab, uint32_t row, uint32_t half, bool mirror, float (&v)[32]) {
     uint8_t* turned = slab + SLAB_BYTES + row / 64 * (SLAB_BYTES / 2);
 #pragma unroll
     for (uint32_t k = 0; k < 4; ++k) {
         uint4& word = slab_word(slab, row, 4 * half + k);
-        if (P == POLY) {
+        if (POLYNOMIAL) {
             const uint32_t g[4] = {word.x, word.y, word.z, word.w};
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&g[e]));
-                v[8 * k + 2 * e] = p.c * v[8 * k + 2 * e] + p.b * f.x;
-                v[8 * k + 2 * e + 1] = p.c * v[8 * k + 2 * e + 1] + p.b * f.y;
+                v[8 * k + 2 * e] = c * v[8 * k + 2 * e] + b * f.x;
+                v[8 * k + 2 * e + 1] = c * v[8 * k + 2 * e + 1] + b * f.y;
             }
         }
         word = make_uint4(pack_f16(v[8 * k], v[8 * k + 1]), pack_f16(v[8 * k + 2], v[8 * k + 3]),
@@ -367,9 +470,8 @@ __device__ __forceinline__ void umma_commit_local2(uint32_t bar) {
 //   warp 10     fills the slab buffers with what a slab needs (two slabs ahead) and stores them, in
 //               whole 128-byte lines: stored by the threads that hold the rows, a tile took 14,000
 //               cycles instead of 6,000.
-template <Product P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-ortho_pair_kernel(const __grid_constant__ GemmParams p) {
+ortho_pair_kernel(const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
@@ -411,18 +513,20 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     if (warp == TMA_WARP && lane == 0) {
-        prefetch_map(&p.tmA);
-        prefetch_map(&p.tmB);
+        prefetch_map(p.first == GRAM ? &p.hi_rows[p.step & 1] : p.first == POLY ? &p.gram : &p.poly);
+        if (p.first == APPLY) prefetch_map(&p.hi_cols[p.step & 1]);
     }
     tc_fence_before();
     cluster_sync_all();          // both CTAs' barriers exist before either arrives remotely
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     launch_next();
+    const uint32_t places = pair_tiles(p), k_long = (p.L + BK - 1) / BK, k_short = (p.S + BK - 1) / BK;   // k blocks: GRAM; else
+    const uint32_t c0 = blockIdx.x / 2, NC = gridDim.x / 2;
+    const Tile tile0 = pair_tile(p, c0);          // worked out before the wait
+    auto tile_at = [&](uint32_t u) { return u == c0 ? tile0 : pair_tile(p, u); };
     wait_previous();
 
-    const uint32_t places = p.batch * p.tiles, kblocks = (p.K + BK - 1) / BK;
-    const uint32_t c0 = blockIdx.x / 2, NC = gridDim.x / 2;
     const uint32_t peer_abort = at_rank(saddr(tmem_slot + 1), q ^ 1);
     auto fail = [&]() {
         *abort_flag = 1;
@@ -434,11 +538,14 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
         if (lane == 0) {
             uint32_t stage = 0, phase = 0, issued = 0;
             bool ok = true;
-            const bool wide = p.tn > 128;
             for (uint32_t u = c0; u < places && ok; u += NC) {
-                uint32_t m, i, j;
-                tile_of<P>(p, u, m, i, j);
-                const int32_t row = (int32_t)(i * 256 + q * 128), col = (int32_t)(j * p.tn + q * (p.tn / 2)), z = (int32_t)m;
+                const Tile t = tile_at(u);
+                if (!inputs_ready(p, t, abort_flag)) { fail(); break; }
+                const uint32_t now = (p.step + t.k) & 1, tn = t.product == APPLY ? p.tn : 256;
+                const CUtensorMap* mA = t.product == GRAM ? &p.hi_rows[now] : t.product == POLY ? &p.gram : &p.poly;
+                const CUtensorMap* mB = t.product == APPLY ? &p.hi_cols[now] : mA;
+                const int32_t row = (int32_t)(t.i * 256 + q * 128), col = (int32_t)(t.j * tn + q * (tn / 2)), z = (int32_t)t.m;
+                const uint32_t kblocks = t.product == GRAM ? k_long : k_short;
                 for (uint32_t kb = 0; kb < kblocks; ++kb) {
                     if (!bar_wait(saddr(empty + stage), phase ^ 1, abort_flag)) { fail(); ok = false; break; }
                     // The peer's loads may land before the leader's expect_tx (the barrier's
@@ -447,13 +554,13 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
                     const uint32_t bar = at_rank(saddr(full + stage), 0);
                     const int32_t k = (int32_t)(kb * BK);
                     const uint32_t dA = saddr(sA + stage * HALF_STAGE), dB = saddr(sB + stage * HALF_STAGE);
-                    if (leader) bar_expect_tx(saddr(full + stage), P == APPLY && !wide ? 3 * HALF_STAGE : 4 * HALF_STAGE);
-                    tma_load_3d_pair(dA, &p.tmA, k, row, z, bar);
-                    if (P == APPLY) {             // X: rows k, 64 columns a box
-                        tma_load_3d_pair(dB, &p.tmB, col, k, z, bar);
-                        if (wide) tma_load_3d_pair(dB + HALF_STAGE / 2, &p.tmB, col + 64, k, z, bar);
+                    if (leader) bar_expect_tx(saddr(full + stage), tn == 128 ? 3 * HALF_STAGE : 4 * HALF_STAGE);
+                    tma_load_3d_pair(dA, mA, k, row, z, bar);
+                    if (t.product == APPLY) {     // X: rows k, 64 columns a box
+                        tma_load_3d_pair(dB, mB, col, k, z, bar);
+                        if (tn > 128) tma_load_3d_pair(dB + HALF_STAGE / 2, mB, col + 64, k, z, bar);
                     } else {
-                        tma_load_3d_pair(dB, &p.tmB, k, col, z, bar);
+                        tma_load_3d_pair(dB, mB, k, col, z, bar);
                     }
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -470,9 +577,11 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
     } else if (warp == MMA_WARP) {
         if (lane == 0 && leader) {
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
-            const uint32_t id = idesc(256, p.tn) | (P == APPLY ? IDESC_B_MN : 0);
             bool ok = true;
             for (uint32_t u = c0; u < places && ok; u += NC) {
+                const uint32_t product = tile_at(u).product;
+                const uint32_t id = product == APPLY ? idesc(256, p.tn) | IDESC_B_MN : idesc(256, 256);
+                const uint32_t step = product == APPLY ? STEP_MN : STEP_K, kblocks = product == GRAM ? k_long : k_short;
                 if (!bar_wait(saddr(acc_empty + acc), acc_phase ^ 1, abort_flag)) { fail(); break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
@@ -481,9 +590,9 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
                     tc_fence_after();
                     const uint64_t da = desc_k(saddr(sA + stage * HALF_STAGE));
                     const uint32_t b0 = saddr(sB + stage * HALF_STAGE);
-                    const uint64_t db = P == APPLY ? desc_mn(b0) : desc_k(b0);
+                    const uint64_t db = product == APPLY ? desc_mn(b0) : desc_k(b0);
 #pragma unroll
-                    for (uint32_t k = 0; k < BK / UMMA_K; ++k) umma_pair(d_tmem, da + STEP_K * k, db + step_b<P>() * k, id, (kb | k) != 0);
+                    for (uint32_t k = 0; k < BK / UMMA_K; ++k) umma_pair(d_tmem, da + STEP_K * k, db + step * k, id, (kb | k) != 0);
                     umma_commit_both(saddr(empty + stage));   // both CTAs' stages are free
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
@@ -498,54 +607,55 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
         }
     } else if (warp == SLAB_WARP) {
         if (lane == 0 && c0 < places) {
-            const uint32_t per_tile = p.tn / SLAB, total = (places - c0 + NC - 1) / NC * per_tile;
-            const uint32_t cols = P == APPLY ? p.L : p.S;
-            uint32_t loaded = 0;
-            auto place = [&](uint32_t s, uint32_t& m, uint32_t& i, uint32_t& j, uint32_t& x, uint32_t& y) {
-                tile_of<P>(p, c0 + s / per_tile * NC, m, i, j);
-                x = j * p.tn + s % per_tile * SLAB;
-                y = i * 256 + q * 128;
-                return x < cols && y < p.S;       // else the slab lies outside
-            };
-            auto load = [&](uint32_t s) {
-                uint32_t m, i, j, x, y;
-                const bool inside = place(s, m, i, j, x, y);
-                const uint32_t bar = saddr(slab_in + s % SLAB_BUFS), to = saddr(slabs) + s % SLAB_BUFS * 2 * SLAB_BYTES;
-                if (P == GRAM || !inside) {
-                    bar_arrive(bar);
-                } else {
-                    bar_expect_tx(bar, P == APPLY ? 2 * SLAB_BYTES : SLAB_BYTES);
-                    tma_load_3d(to, &p.in0, (int32_t)x, (int32_t)y, (int32_t)m, bar);
-                    if (P == APPLY) tma_load_3d(to + SLAB_BYTES, &p.in1, (int32_t)x, (int32_t)y, (int32_t)m, bar);
-                }
-                ++loaded;
-            };
-            for (uint32_t s = 0; s < SLAB_BUFS && s < total; ++s) load(s);
-            for (uint32_t s = 0; s < total; ++s) {
-                if (!bar_wait(saddr(slab_out + s % SLAB_BUFS), s / SLAB_BUFS & 1, abort_flag)) { fail(); break; }
-                uint32_t m, i, j, x, y;
-                const bool inside = place(s, m, i, j, x, y);
-                const uint32_t from = saddr(slabs) + s % SLAB_BUFS * 2 * SLAB_BYTES;
-                if (P != APPLY) {
-                    if (inside) tma_store_3d(&p.out0, (int32_t)x, (int32_t)y, (int32_t)m, from);
-                    if (i != j && x < p.S)        // as rows x .., columns y ..
-                        for (uint32_t h = 0; h < 2; ++h)
-                            if (y + 64 * h < p.S)
-                                tma_store_3d(&p.out1, (int32_t)(y + 64 * h), (int32_t)x, (int32_t)m, from + SLAB_BYTES + h * (SLAB_BYTES / 2));
-                } else if (!p.out && inside) {
-                    tma_store_3d(&p.out0, (int32_t)x, (int32_t)y, (int32_t)m, from);
-                    tma_store_3d(&p.out1, (int32_t)x, (int32_t)y, (int32_t)m, from + SLAB_BYTES);
-                }
-                bulk_commit();
-                if (s + SLAB_BUFS < total) {
+            uint32_t loaded = 0, stored_slabs = 0;
+            bool ok = true;
+            for (uint32_t u = c0; u < places && ok; u += NC) {
+                const Tile t = tile_at(u);
+                const bool apply = t.product == APPLY, result = p.out && t.k + 1 == p.steps;
+                const uint32_t count = (apply ? p.tn : 256) / SLAB;
+                const int32_t y = (int32_t)(t.i * 256 + q * 128), m = (int32_t)t.m;
+                auto column = [&](uint32_t g) { return (int32_t)(t.j * count * SLAB + g * SLAB); };
+                auto inside = [&](uint32_t g) { return (uint32_t)column(g) < (apply ? p.L : p.S) && (uint32_t)y < p.S; };
+                auto load = [&](uint32_t g) {
+                    const uint32_t bar = saddr(slab_in + loaded % SLAB_BUFS), to = saddr(slabs) + loaded % SLAB_BUFS * 2 * SLAB_BYTES;
+                    if (t.product == GRAM || !inside(g)) {
+                        bar_arrive(bar);
+                    } else {
+                        bar_expect_tx(bar, apply ? 2 * SLAB_BYTES : SLAB_BYTES);
+                        tma_load_3d(to, apply ? &p.hi_rows[(p.step + t.k) & 1] : &p.gram, column(g), y, m, bar);
+                        if (apply) tma_load_3d(to + SLAB_BYTES, &p.lo_rows, column(g), y, m, bar);
+                    }
+                    ++loaded;
+                };
+                // not before the last tile has been stored and counted: this one may wait for it
+                if (!inputs_ready(p, t, abort_flag)) { ok = false; break; }
+                for (uint32_t g = 0; g < SLAB_BUFS; ++g) load(g);
+                for (uint32_t g = 0; g < count; ++g, ++stored_slabs) {
+                    if (!bar_wait(saddr(slab_out + stored_slabs % SLAB_BUFS), stored_slabs / SLAB_BUFS & 1, abort_flag)) { ok = false; break; }
+                    const int32_t x = column(g);
+                    const uint32_t from = saddr(slabs) + stored_slabs % SLAB_BUFS * 2 * SLAB_BYTES;
+                    if (!apply) {
+                        const bool gram = t.product == GRAM;
+                        if (inside(g)) tma_store_3d(gram ? &p.gram : &p.poly, x, y, m, from);
+                        if (t.i != t.j && (uint32_t)x < p.S)                 // as rows x .., columns y ..
+                            for (int32_t h = 0; h < 2; ++h)
+                                if ((uint32_t)(y + 64 * h) < p.S)
+                                    tma_store_3d(gram ? &p.gram_blocks : &p.poly_blocks, y + 64 * h, x, m, from + SLAB_BYTES + h * (SLAB_BYTES / 2));
+                    } else if (!result && inside(g)) {
+                        tma_store_3d(&p.hi_rows[(p.step + t.k + 1) & 1], x, y, m, from);
+                        tma_store_3d(&p.lo_rows, x, y, m, from + SLAB_BYTES);
+                    }
+                    bulk_commit();
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    load(s + SLAB_BUFS);
+                    if (g + SLAB_BUFS < count) load(g + SLAB_BUFS);
                 }
+                if (ok && p.counters && !(apply && result)) count_stored(p, t);
             }
+            if (!ok) fail();
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             volatile uint32_t never = 0;          // every load has landed before the CTA can leave
-            for (uint32_t s = loaded > SLAB_BUFS ? loaded - SLAB_BUFS : 0; s < loaded; ++s)
-                (void)bar_wait(saddr(slab_in + s % SLAB_BUFS), s / SLAB_BUFS & 1, &never);
+            for (uint32_t n = loaded > SLAB_BUFS ? loaded - SLAB_BUFS : 0; n < loaded; ++n)
+                (void)bar_wait(saddr(slab_in + n % SLAB_BUFS), n / SLAB_BUFS & 1, &never);
         }
     } else {
         // epilogue
@@ -553,24 +663,28 @@ ortho_pair_kernel(const __grid_constant__ GemmParams p) {
         const uint32_t row = 32 * (warp % 4) + lane, half = warp / 4;
         bool ok = true;
         for (uint32_t u = c0; u < places && ok; u += NC) {
-            uint32_t m, i, j;
-            tile_of<P>(p, u, m, i, j);
+            const Tile t = tile_at(u);
+            const float a = p.coeffs[t.k][0], b = p.coeffs[t.k][1], c = p.coeffs[t.k][2];
+            const bool result = p.out && t.k + 1 == p.steps;
+            const uint32_t tn = t.product == APPLY ? p.tn : 256;
             ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(acc_full + acc), acc_phase, abort_flag));
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((32u * (warp % 4)) << 16) + acc * 256 + 32 * half;
-            for (uint32_t g = 0; g < p.tn / SLAB && ok; ++g, ++s) {
+            for (uint32_t g = 0; g < tn / SLAB && ok; ++g, ++s) {
                 uint8_t* slab = slabs + s % SLAB_BUFS * 2 * SLAB_BYTES;
                 float v[32];
                 tmem_ld32(taddr + g * SLAB, v);
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(slab_in + s % SLAB_BUFS), s / SLAB_BUFS & 1, abort_flag));
                 if (!ok) break;
-                if (P == APPLY) {
-                    finish_apply(p.a, slab, slab + SLAB_BYTES, row, half, v, !p.out);
-                    if (p.out)
-                        store_result({p.out + (uint64_t)m * p.out_stride, p.out_pitch, p.S, p.L, p.scale, p.transposed, p.out_vec},
-                                     i * 256 + q * 128 + row, j * p.tn + g * SLAB + 32 * half, v);
+                if (t.product == APPLY) {
+                    finish_apply(a, slab, slab + SLAB_BYTES, row, half, v, !result);
+                    if (result)
+                        store_result({p.out + (uint64_t)t.m * p.out_stride, p.out_pitch, p.S, p.L, p.scale, p.transposed, p.out_vec},
+                                     t.i * 256 + q * 128 + row, t.j * tn + g * SLAB + 32 * half, v);
+                } else if (t.product == GRAM) {
+                    finish<false>(b, c, slab, row, half, t.i != t.j, v);
                 } else {
-                    finish<P>(p, slab, row, half, i != j, v);
+                    finish<true>(b, c, slab, row, half, t.i != t.j, v);
                 }
                 // the slab warp's stores read what every lane wrote
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1012,6 +1126,8 @@ struct UpdateParams {
     uint32_t nesterov, x_dt;
     uint32_t rows, cols, parts;
     float* sums;                 // [batch][parts]
+    uint32_t* counters;          // the pair form's, zeroed here; or null
+    uint32_t n_counters;
     __half* hi;
     __half* lo;
     uint64_t l_pitch;
@@ -1044,6 +1160,8 @@ __global__ void __launch_bounds__(256) ortho_update_kernel(const __grid_constant
     const Index total = (Index)p.rows * per_row, step = (Index)p.parts * 256;
     float sum = 0.0f;
     launch_next();
+    if (p.counters && blockIdx.x == 0 && m == 0)
+        for (uint32_t i = threadIdx.x; i < p.n_counters; i += 256) p.counters[i] = 0;
     constexpr uint32_t N = VEC ? 4 : 8;                // under way at a time
     for (Index i0 = blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += N * step) {
         float u[N][W], v[N][W];
@@ -1561,7 +1679,8 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, ui
 
 struct Layout {
     uint64_t S, L, s_pitch, l_pitch;                 // elements
-    uint64_t hi[2], lo, gram, poly, sums, bytes;     // byte offsets in the workspace
+    uint64_t hi[2], lo, gram, poly, sums, counters, bytes;   // byte offsets in the workspace
+    uint64_t n_counters;
 };
 
 Layout layout_of(const dtt_ortho_desc& d) {
@@ -1582,6 +1701,8 @@ Layout layout_of(const dtt_ortho_desc& d) {
     l.gram = take(d.batch * l.S * l.s_pitch * 2);
     l.poly = take(d.batch * l.S * l.s_pitch * 2);
     l.sums = take((uint64_t)d.batch * kMaxParts * 4);
+    l.n_counters = (uint64_t)d.batch * 3 * ((l.S + 255) / 256);
+    l.counters = take(l.n_counters * 4);
     l.bytes = at;
     return l;
 }
@@ -1652,7 +1773,7 @@ Fit fit_of(int device, uint32_t sms) {
     Fit local{};
     Fit& f = device < 64 ? known[device] : local;
     if (!f.pairs) {
-        f.pairs = clusters_of(ortho_pair_kernel<APPLY>, 2);
+        f.pairs = clusters_of(ortho_pair_kernel, 2);
         f.splits[0] = sms;
         f.splits[1] = clusters_of(ortho_split_kernel<APPLY, 2>, 2);
         f.splits[2] = clusters_of(ortho_split_kernel<APPLY, 4>, 4);
@@ -1703,6 +1824,16 @@ Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t bat
     return best;
 }
 
+// The same for a whole step in the one launch of CTA pairs: the tiles' time over all pairs, or one tile of each
+// product after the other, and 6 us a product from the last tile's sums to the next one's first.  Measured,
+// five steps, this against a launch a product: 4096 x 4096 915 us and 990, 3000 x 3000 456 and 576, four of
+// 2048 x 2048 540 and 640; the rule leaves alone two of 1024 x 4096, 281 and 247, and 1500 x 3500, 410 and 400.
+double flow_us(uint64_t S, uint64_t L, uint32_t batch, const Fit& fit) {
+    const double square = (double)tiles_of(true, 256, 256, S, S) * batch, oblong = (double)tiles_of(false, 256, 256, S, L) * batch;
+    const double gram = 0.3 + 0.275 * ceil_div(L, BK), other = 0.3 + 0.275 * ceil_div(S, BK);
+    return 18.0 + std::max(1.15 * (square * (gram + other) + oblong * other) / fit.pairs, gram + 2 * other);
+}
+
 // The same for POLY and APPLY in one (S <= 256): 9 us a round of tiles, measured.
 double fused_us(uint64_t S, uint64_t L, uint32_t batch, uint32_t sms) {
     return 0.8 + 9.0 * ceil_div((uint64_t)tiles_of(false, 128, 128, S, L) * batch, sms);
@@ -1716,23 +1847,42 @@ uint32_t resident_ctas(uint64_t S, uint64_t L) {
 }
 
 template <Product P>
-cudaError_t launch_product(GemmParams& p, const Form& f, uint32_t pairs, cudaStream_t stream) {
-    const uint32_t tile_m = f.pair ? 256 : 128;
-    p.tn = f.tn;
-    p.tiles_m = ceil_div(p.S, tile_m);
-    p.tiles = tiles_of(P != APPLY, tile_m, f.tn, p.S, p.L);
-    const uint32_t places = p.tiles * p.batch;
-    if (f.pair) return launch(ortho_pair_kernel<P>, 2 * std::min(places, pairs), THREADS, SMEM_BYTES, 0, true, stream, p);
+cudaError_t launch_split(GemmParams& p, const Form& f, cudaStream_t stream) {
+    p.tiles_m = ceil_div(p.S, 128);
+    p.tiles = tiles_of(P != APPLY, 128, 128, p.S, p.L);
     auto kernel = f.ctas == 1 ? ortho_split_kernel<P, 1> : f.ctas == 2 ? ortho_split_kernel<P, 2>
                 : f.ctas == 4 ? ortho_split_kernel<P, 4> : ortho_split_kernel<P, 8>;
-    return launch(kernel, places * f.ctas, THREADS, SMEM_BYTES, f.ctas, true, stream, p);
+    return launch(kernel, p.tiles * p.batch * f.ctas, THREADS, SMEM_BYTES, f.ctas, true, stream, p);
+}
+
+// Tiles of a step's products first .. last, of all matrices.
+uint32_t pair_tiles_of(const PairParams& p) {
+    uint32_t tiles = 0;
+    for (uint32_t q = p.first; q <= p.last; ++q) tiles += p.batch * p.n * (q == APPLY ? 2 * p.across : p.n + 1) / 2;
+    return tiles;
+}
+
+// One product after the launch before it; or, with counters, everything: a cooperative launch then, since
+// its clusters wait for one another.
+cudaError_t launch_pair(const PairParams& p, uint32_t pairs, cudaStream_t stream) {
+    const uint32_t grid = 2 * (uint32_t)std::min<uint64_t>((uint64_t)pair_tiles_of(p) * p.steps, pairs);
+    if (!p.counters) return launch(ortho_pair_kernel, grid, THREADS, SMEM_BYTES, 0, true, stream, p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ortho_pair_kernel, p);
 }
 
 template <Product P>
-cudaError_t prepare_product() {
-    cudaError_t e = prepare_kernel(ortho_pair_kernel<P>);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(ortho_pair_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+cudaError_t prepare_splits() {
+    cudaError_t e = cudaSuccess;
     for (auto kernel : {ortho_split_kernel<P, 1>, ortho_split_kernel<P, 2>, ortho_split_kernel<P, 4>, ortho_split_kernel<P, 8>}) {
         if (e == cudaSuccess) e = prepare_kernel(kernel);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
@@ -1743,9 +1893,12 @@ cudaError_t prepare_product() {
 }  // namespace
 
 cudaError_t preload_ortho_kernels() {
-    cudaError_t e = prepare_product<GRAM>();
-    if (e == cudaSuccess) e = prepare_product<POLY>();
-    if (e == cudaSuccess) e = prepare_product<APPLY>();
+    cudaError_t e = prepare_kernel(ortho_pair_kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ortho_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e == cudaSuccess) e = prepare_splits<GRAM>();
+    if (e == cudaSuccess) e = prepare_splits<POLY>();
+    if (e == cudaSuccess) e = prepare_splits<APPLY>();
     for (auto kernel : {ortho_resident_kernel<1>, ortho_resident_kernel<2>, ortho_resident_kernel<4>, ortho_resident_kernel<8>,
                         ortho_resident_kernel<16>}) {
         if (e == cudaSuccess) e = prepare_kernel(kernel);
@@ -1776,6 +1929,7 @@ struct dtt_ortho {
     // boxes of 64 x 64: the N-contiguous operand of the last product, and mirrored blocks
     CUtensorMap hi_cols[2], gram_blocks, poly_blocks;
     bool fused;                  // POLY within APPLY
+    bool flow;                   // all products of all steps in one launch of CTA pairs
     uint32_t resident;           // CTAs of a cluster in the resident form; 0: a launch a product
     Fit fit;
     Form form[3];                // of each Product
@@ -1816,6 +1970,8 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     o->form[APPLY] = form_of(false, l.S, l.L, l.S, d->batch, o->fit);
     // its second term of b A + c A A is worth some time: without it a flat spectrum's error is 1.6 times bf16's own
     o->fused = l.S <= 256 && fused_us(l.S, l.L, d->batch, o->sms) < 1.3 * (o->form[POLY].us + o->form[APPLY].us);
+    o->flow = !o->resident && !o->fused &&
+              flow_us(l.S, l.L, d->batch, o->fit) < o->form[GRAM].us + o->form[POLY].us + o->form[APPLY].us;
     bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->gram_blocks, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 64) &&
@@ -1871,6 +2027,8 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     up.rows = (uint32_t)d.rows;
     up.cols = (uint32_t)d.cols;
     up.sums = reinterpret_cast<float*>(o->ws + l.sums);
+    up.counters = o->flow ? reinterpret_cast<uint32_t*>(o->ws + l.counters) : nullptr;
+    up.n_counters = (uint32_t)l.n_counters;
     up.hi = reinterpret_cast<__half*>(o->ws + l.hi[0]);
     up.lo = reinterpret_cast<__half*>(o->ws + l.lo);
     up.l_pitch = l.l_pitch;
@@ -1910,6 +2068,47 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         DTT_CUDA_TRY(launch(tall ? ortho_start_tiles_kernel<true> : ortho_start_tiles_kernel<false>, tiles, 256, 0, 0, true, stream, up));
     }
 
+    PairParams pp{};
+    for (int i = 0; i < 2; ++i) {
+        pp.hi_rows[i] = o->hi_rows[i];
+        pp.hi_cols[i] = o->hi_cols[i];
+    }
+    pp.lo_rows = o->lo_rows;
+    pp.gram = o->gram;
+    pp.poly = o->poly;
+    pp.gram_blocks = o->gram_blocks;
+    pp.poly_blocks = o->poly_blocks;
+    pp.S = (uint32_t)l.S;
+    pp.L = (uint32_t)l.L;
+    pp.batch = d.batch;
+    pp.n = ceil_div(l.S, 256);
+    pp.tn = !o->flow && o->form[APPLY].pair ? o->form[APPLY].tn : 256;
+    pp.across = ceil_div(l.L, pp.tn);
+    pp.out_pitch = out_pitch;
+    pp.out_stride = out_stride;
+    pp.scale = d.scale;
+    pp.transposed = tall;
+    pp.out_vec = out_vec;
+    pp.err = err;
+    if (o->flow) {
+        pp.first = GRAM;
+        pp.last = APPLY;
+        pp.steps = d.steps;
+        pp.counters = up.counters;
+        pp.out = static_cast<char*>(out);
+        std::copy(&d.coeffs[0][0], &d.coeffs[0][0] + 3 * d.steps, &pp.coeffs[0][0]);
+        DTT_CUDA_TRY(launch_pair(pp, o->fit.pairs, stream));
+        return DTT_OK;
+    }
+    auto pair = [&](Product product, uint32_t k) {
+        pp.first = pp.last = product;
+        pp.step = k;
+        pp.steps = 1;
+        pp.out = product == APPLY && k + 1 == d.steps ? static_cast<char*>(out) : nullptr;
+        std::copy(&d.coeffs[k][0], &d.coeffs[k][0] + 3, &pp.coeffs[0][0]);
+        return launch_pair(pp, o->fit.pairs, stream);
+    };
+
     GemmParams g{};
     g.S = (uint32_t)l.S;
     g.batch = d.batch;
@@ -1929,23 +2128,16 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         g.c = d.coeffs[k][2];
         g.L = g.S;
         g.tmA = g.tmB = o->hi_rows[now];
-        g.out0 = o->gram;
-        g.out1 = o->gram_blocks;
         g.K = (uint32_t)l.L;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.gram);
-        DTT_CUDA_TRY(launch_product<GRAM>(g, o->form[GRAM], o->fit.pairs, stream));
-        g.tmA = g.tmB = g.in0 = o->gram;
-        g.out0 = o->poly;
-        g.out1 = o->poly_blocks;
+        DTT_CUDA_TRY(o->form[GRAM].pair ? pair(GRAM, k) : launch_split<GRAM>(g, o->form[GRAM], stream));
+        g.tmA = g.tmB = o->gram;
         g.K = g.S;
         g.gram = g.out16;
         g.out16 = reinterpret_cast<__half*>(o->ws + l.poly);
-        if (!o->fused) DTT_CUDA_TRY(launch_product<POLY>(g, o->form[POLY], o->fit.pairs, stream));
+        if (!o->fused) DTT_CUDA_TRY(o->form[POLY].pair ? pair(POLY, k) : launch_split<POLY>(g, o->form[POLY], stream));
         g.tmA = o->fused ? o->gram : o->poly;
         g.tmB = o->hi_cols[now];
-        g.in0 = o->hi_rows[now];
-        g.in1 = g.out1 = o->lo_rows;
-        g.out0 = o->hi_rows[now ^ 1];
         g.L = (uint32_t)l.L;
         g.hi = reinterpret_cast<const __half*>(o->ws + l.hi[now]);
         g.out16 = reinterpret_cast<__half*>(o->ws + l.hi[now ^ 1]);
@@ -1955,7 +2147,7 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
             g.tiles = tiles_of(false, 128, 128, g.S, g.L);
             DTT_CUDA_TRY(launch(ortho_fused_kernel, g.tiles * g.batch, THREADS, FUSED_SMEM, 0, true, stream, g));
         } else {
-            DTT_CUDA_TRY(launch_product<APPLY>(g, o->form[APPLY], o->fit.pairs, stream));
+            DTT_CUDA_TRY(o->form[APPLY].pair ? pair(APPLY, k) : launch_split<APPLY>(g, o->form[APPLY], stream));
         }
     }
     return DTT_OK;

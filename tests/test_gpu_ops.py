@@ -270,6 +270,87 @@ def test_orthogonalize(batch, rows, cols, dtype):
         assert rel(f64(out[i]), OO.orthogonalize(f64(x[i]), 5, [COEFFS] * 5, 1e-7, 0.5)) < ORTHO_TOL
 
 
+def orthogonalized(x, steps=5):
+    """The formula in 64 bits on the device, for matrices that take the host too long."""
+    x = x.double()
+    if x.shape[0] > x.shape[1]:
+        return orthogonalized(x.T, steps).T
+    x = x / (x.norm() + 1e-7)
+    a, b, c = COEFFS
+    for _ in range(steps):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x
+
+
+# one cluster a matrix, up to its longest row and one past it; the second product within the third; its limit
+# and one past it; a product by CTA pairs; everything in one launch, with a last row block of 1, 2 or 64 rows
+LARGE = [(2, 128, 4096), (1, 128, 4097), (1, 4096, 100), (5, 129, 1000), (9, 256, 700), (1, 2000, 250), (1, 257, 3000),
+         (3, 1024, 1500), (1, 2048, 2048), (3, 2050, 2049), (1, 2300, 1900), (1, 1600, 5000), (5, 1025, 1100), (40, 257, 600)]
+
+
+@pytest.mark.parametrize("batch,rows,cols", LARGE)
+def test_orthogonalize_large(batch, rows, cols):
+    x = torch.randn(batch, rows, cols, generator=gen(rows + cols), device="cuda").to(torch.bfloat16)
+    if batch > 2:
+        x[1, 5, 7] = float("nan")               # spoils its own matrix alone
+    out, again = (torch.zeros(batch, rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    with D.Orthogonalizer(rows, cols, batch=batch) as op:
+        op.run(x, out)
+        op.run(x, again)
+        assert op.errors == 0
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    for i in range(batch):
+        if batch > 2 and i == 1:
+            assert torch.isnan(out[i]).all()
+            continue
+        want = orthogonalized(x[i])
+        assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
+
+
+def test_orthogonalize_large_in_a_graph_beside_strided_arguments():
+    """Everything in one launch: captured, replayed on new values, the result by columns and by rows into slices."""
+    s = torch.cuda.Stream()
+    for rows, cols in ((2100, 2501), (2501, 2100)):
+        g = gen(rows)
+        x = torch.randn(rows, cols, generator=g, device="cuda")
+        res = torch.full((rows + 2, cols + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+        m = torch.zeros(rows, cols, device="cuda")
+        out = res[1:rows + 1, 2:cols + 2]
+        with D.Orthogonalizer(rows, cols, dtype="f32", mu=0.5, steps=3, coeffs=[COEFFS] * 3) as op:
+            s.wait_stream(torch.cuda.current_stream())
+            op.run(x, out, momentum=m, stream=s)
+            s.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                op.run(x, out, momentum=m, stream=s)
+            x.normal_(generator=g)
+            before = m.clone()
+            out.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert op.errors == 0
+        want_m = 0.5 * before.double() + x.double()
+        assert float((m.double() - want_m).abs().max()) < 1e-5
+        want = orthogonalized(want_m, 3)
+        assert float((out.double() - want).norm() / want.norm()) < ORTHO_TOL
+        out.fill_(7)
+        assert (res == 7).all()
+
+
+@pytest.mark.parametrize("rank", [1, 4])
+def test_orthogonalize_large_of_low_rank(rank):
+    g = gen(rank)
+    x = torch.randn(2048, rank, generator=g, device="cuda") @ torch.randn(rank, 2304, generator=g, device="cuda")
+    out = torch.empty(2048, 2304, dtype=torch.bfloat16, device="cuda")
+    with D.Orthogonalizer(2048, 2304, dtype="f32") as op:
+        op.run(x, out)
+        assert op.errors == 0
+    want = orthogonalized(x)
+    assert float((out.double() - want).norm() / want.norm()) < RANK1_TOL
+
+
 @pytest.mark.parametrize("nesterov", [False, True])
 def test_orthogonalize_with_momentum_over_steps(nesterov):
     rows, cols, mu = 96, 160, 0.95
