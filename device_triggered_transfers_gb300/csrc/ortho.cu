@@ -54,7 +54,8 @@ static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= STAGES * 2 * HALF_STAGE && 128
               "the tile fits the stages, the sums of the cluster the slabs");
 
 constexpr uint32_t kStartTile = 64;                  // ortho_start_tiles_kernel: elements a side
-constexpr uint32_t kMaxParts = 1216;                 // ortho_update_kernel: CTAs a matrix at most, eight a SM
+constexpr uint32_t START_CTAS = 4;                   // of the update and start kernels on a SM
+constexpr uint32_t kMaxParts = 152 * START_CTAS;     // CTAs of the update's launch at most: all run at once
 
 enum Product { GRAM, POLY, APPLY };
 
@@ -1146,67 +1147,129 @@ __device__ __forceinline__ float cta_sum(float v, float (&slot)[8]) {
     return v;
 }
 
+// The N chunks of 8 columns that a thread has under way, from chunk i of a matrix in steps of `step`: rows r,
+// columns c .., of the momentum (MOM) and of x (bf16 where B16, else f32), where it is wanted.  No load here
+// is behind a condition of its own, so that all go out together: the whole call on two bf16 updates of
+// 1024 x 4096 with momentum takes 255 us so, 262 with one after the other.
+template <bool B16, bool MOM, uint32_t N>
+__device__ __forceinline__ void chunks(const UpdateParams& p, const char* x, const char* mom, bool want_x, uint32_t i, uint32_t step,
+                                       uint32_t total, uint32_t (&r)[N], uint32_t (&c)[N], float (&u)[N][8], float (&v)[N][8]) {
+    const uint32_t per_row = p.cols / 8;
+#pragma unroll
+    for (uint32_t n = 0; n < N; ++n) {
+        const uint32_t j = min(i + n * step, total - 1);
+        r[n] = j / per_row;
+        c[n] = 8 * (j - r[n] * per_row);
+    }
+    uint4 raw[N][2], old[N][2];
+    if (want_x) {
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) {
+            const uint4* at = reinterpret_cast<const uint4*>(x + r[n] * p.x_pitch + (uint64_t)c[n] * (B16 ? 2 : 4));
+            raw[n][0] = at[0];
+            if (!B16) raw[n][1] = at[1];
+        }
+    }
+    if (MOM) {
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) {
+            const uint4* at = reinterpret_cast<const uint4*>(mom + r[n] * p.mom_pitch + (uint64_t)c[n] * 4);
+            old[n][0] = at[0];
+            old[n][1] = at[1];
+        }
+    }
+#pragma unroll
+    for (uint32_t n = 0; n < N; ++n)
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            auto word = [](const uint4& q, uint32_t e) { return e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w; };
+            if (want_x) {
+                const uint32_t w = B16 ? word(raw[n][0], k / 2) : word(raw[n][k / 4], k % 4);
+                u[n][k] = !B16 ? __uint_as_float(w) : k % 2 ? bf16_hi(w) : bf16_lo(w);
+            }
+            if (MOM) v[n][k] = __uint_as_float(word(old[n][k / 4], k % 4));
+        }
+}
+// Bytes under way are what counts: a thread has 64 to 128 of them.
+template <bool B16, bool MOM>
+constexpr uint32_t kChunks = B16 && !MOM ? 4 : 2;
+
+__device__ __forceinline__ void zero_counters(const UpdateParams& p) {
+    if (p.counters && blockIdx.x == 0 && blockIdx.y == 0)
+        for (uint32_t i = threadIdx.x; i < p.n_counters; i += 256) p.counters[i] = 0;
+}
+
 // The momentum's update, and a part of |u|^2 from each of `parts` CTAs a matrix, which stride over its
-// rows in chunks of 8 columns (VEC) or single elements.
-template <bool VEC>
-__global__ void __launch_bounds__(256) ortho_update_kernel(const __grid_constant__ UpdateParams p) {
+// chunks: 16-byte aligned.
+template <bool B16, bool MOM>
+__global__ void __launch_bounds__(256, START_CTAS) ortho_update_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
-    constexpr uint32_t W = VEC ? 8 : 1;
-    const uint32_t m = blockIdx.y, per_row = (p.cols + W - 1) / W;
+    constexpr uint32_t N = kChunks<B16, MOM>;
+    const uint32_t m = blockIdx.y, total = p.rows * (p.cols / 8), step = p.parts * 256;
     const char* x = p.x + (uint64_t)m * p.x_stride;
-    char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
-    // at most 2^29 chunks, but up to 2^32 elements
-    using Index = std::conditional_t<VEC, uint32_t, uint64_t>;
-    const Index total = (Index)p.rows * per_row, step = (Index)p.parts * 256;
+    char* mom = MOM ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
     float sum = 0.0f;
     launch_next();
-    if (p.counters && blockIdx.x == 0 && m == 0)
-        for (uint32_t i = threadIdx.x; i < p.n_counters; i += 256) p.counters[i] = 0;
-    constexpr uint32_t N = VEC ? 4 : 8;                // under way at a time
-    for (Index i0 = blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += N * step) {
-        float u[N][W], v[N][W];
+    zero_counters(p);
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += N * step) {
+        float u[N][8], v[N][8];
+        uint32_t r[N], c[N];
+        chunks<B16, MOM, N>(p, x, mom, true, i, step, total, r, c, u, v);
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) {
+            if (i + n * step >= total) break;
+            if (MOM) {
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) {
+                    v[n][k] = p.mu * v[n][k] + u[n][k];
+                    u[n][k] = p.nesterov ? u[n][k] + p.mu * v[n][k] : v[n][k];
+                }
+                float4* to = reinterpret_cast<float4*>(mom + r[n] * p.mom_pitch + (uint64_t)c[n] * 4);
+                to[0] = make_float4(v[n][0], v[n][1], v[n][2], v[n][3]);
+                to[1] = make_float4(v[n][4], v[n][5], v[n][6], v[n][7]);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) sum += u[n][k] * u[n][k];
+        }
+    }
+    sum = cta_sum(sum, slot);
+    if (threadIdx.x == 0) p.sums[(uint64_t)m * p.parts + blockIdx.x] = sum;
+}
+
+// The same for any alignment, by single elements.
+__global__ void __launch_bounds__(256) ortho_update_elements_kernel(const __grid_constant__ UpdateParams p) {
+    __shared__ float slot[8];
+    const uint32_t m = blockIdx.y;
+    const char* x = p.x + (uint64_t)m * p.x_stride;
+    char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
+    const uint64_t total = (uint64_t)p.rows * p.cols, step = (uint64_t)p.parts * 256;   // up to 2^32 elements
+    float sum = 0.0f;
+    launch_next();
+    zero_counters(p);
+    constexpr uint32_t N = 8;                          // under way at a time
+    for (uint64_t i0 = blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += N * step) {
+        float u[N], v[N];
         const char *xs[N], *moms[N];
         uint32_t cs[N];
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) {
-            const Index i = min(i0 + n * step, total - 1);
-            const uint32_t r = (uint32_t)(i / per_row);
-            cs[n] = (uint32_t)(i - (Index)r * per_row) * W;
+            const uint64_t i = min(i0 + n * step, total - 1);
+            const uint32_t r = (uint32_t)(i / p.cols);
+            cs[n] = (uint32_t)(i - (uint64_t)r * p.cols);
             xs[n] = x + r * p.x_pitch;
             moms[n] = mom + r * p.mom_pitch;
         }
-        if constexpr (VEC) {
-#pragma unroll
-            for (uint32_t n = 0; n < N; ++n) load8<true>(xs[n], p.x_dt, cs[n], p.cols, u[n]);
-            if (mom) {
-#pragma unroll
-                for (uint32_t n = 0; n < N; ++n) load8<true>(moms[n], DTT_F32, cs[n], p.cols, v[n]);
-            }
-        } else {
-            float a[N], b[N];
-            gather(xs, p.x_dt, cs, a);
-            if (mom) gather(moms, DTT_F32, cs, b);
-#pragma unroll
-            for (uint32_t n = 0; n < N; ++n) {
-                u[n][0] = a[n];
-                v[n][0] = b[n];
-            }
-        }
+        gather(xs, p.x_dt, cs, u);
+        if (mom) gather(moms, DTT_F32, cs, v);
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) {
             if (i0 + n * step >= total) break;
             if (mom) {
-                char* row = const_cast<char*>(moms[n]);
-#pragma unroll
-                for (uint32_t k = 0; k < W; ++k) {
-                    v[n][k] = p.mu * v[n][k] + u[n][k];
-                    u[n][k] = p.nesterov ? u[n][k] + p.mu * v[n][k] : v[n][k];
-                }
-                if constexpr (VEC) store8<true>(row, DTT_F32, cs[n], p.cols, v[n]);
-                else store1(row, DTT_F32, cs[n], v[n][0]);
+                v[n] = p.mu * v[n] + u[n];
+                u[n] = p.nesterov ? u[n] + p.mu * v[n] : v[n];
+                store1(const_cast<char*>(moms[n]), DTT_F32, cs[n], v[n]);
             }
-#pragma unroll
-            for (uint32_t k = 0; k < W; ++k) sum += u[n][k] * u[n][k];
+            sum += u[n] * u[n];
         }
     }
     sum = cta_sum(sum, slot);
@@ -1225,39 +1288,36 @@ __device__ __forceinline__ float inverse_norm(const UpdateParams& p, uint32_t m,
 }
 
 // u again (the momentum is updated by now) and X = u / (|u| + eps), in its two halves: rows
-// <= cols, 16-byte aligned.  A thread has two chunks of 8 columns under way.
-__global__ void __launch_bounds__(256) ortho_start_kernel(const __grid_constant__ UpdateParams p) {
+// <= cols, 16-byte aligned.
+template <bool B16, bool MOM>
+__global__ void __launch_bounds__(256, START_CTAS) ortho_start_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
-    const uint32_t m = blockIdx.y, per_row = p.cols / 8, total = p.rows * per_row, step = gridDim.x * 256;
+    constexpr uint32_t N = 2;
+    const uint32_t m = blockIdx.y, total = p.rows * (p.cols / 8), step = gridDim.x * 256;
     const char* x = p.x + (uint64_t)m * p.x_stride;
-    const char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
+    const char* mom = MOM ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
     __half* hi = p.hi + (uint64_t)m * p.S * p.l_pitch;
     __half* lo = p.lo + (uint64_t)m * p.S * p.l_pitch;
     const float inv = inverse_norm(p, m, slot);
-    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += 2 * step) {
-        float u[2][8], v[2][8];
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += N * step) {
+        float u[N][8], v[N][8];
+        uint32_t r[N], c[N];
+        chunks<B16, MOM, N>(p, x, mom, !MOM || p.nesterov, i, step, total, r, c, u, v);
 #pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-            const uint32_t j = min(i + h * step, total - 1), r = j / per_row, c = 8 * (j - r * per_row);
-            load8<true>(x + r * p.x_pitch, p.x_dt, c, p.cols, u[h]);
-            if (mom) load8<true>(mom + r * p.mom_pitch, DTT_F32, c, p.cols, v[h]);
-        }
-#pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-            const uint32_t j = i + h * step, r = j / per_row, c = 8 * (j - r * per_row);
-            if (j >= total) break;
+        for (uint32_t n = 0; n < N; ++n) {
+            if (i + n * step >= total) break;
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
-                if (mom) u[h][k] = p.nesterov ? u[h][k] + p.mu * v[h][k] : v[h][k];
-                u[h][k] *= inv;
+                if (MOM) u[n][k] = p.nesterov ? u[n][k] + p.mu * v[n][k] : v[n][k];
+                u[n][k] *= inv;
             }
             uint4 a, b;
-            part(u[h][0], u[h][1], a.x, b.x);
-            part(u[h][2], u[h][3], a.y, b.y);
-            part(u[h][4], u[h][5], a.z, b.z);
-            part(u[h][6], u[h][7], a.w, b.w);
-            *reinterpret_cast<uint4*>(hi + r * p.l_pitch + c) = a;
-            *reinterpret_cast<uint4*>(lo + r * p.l_pitch + c) = b;
+            part(u[n][0], u[n][1], a.x, b.x);
+            part(u[n][2], u[n][3], a.y, b.y);
+            part(u[n][4], u[n][5], a.z, b.z);
+            part(u[n][6], u[n][7], a.w, b.w);
+            *reinterpret_cast<uint4*>(hi + r[n] * p.l_pitch + c[n]) = a;
+            *reinterpret_cast<uint4*>(lo + r[n] * p.l_pitch + c[n]) = b;
         }
     }
 }
@@ -1890,6 +1950,16 @@ cudaError_t prepare_splits() {
     return e;
 }
 
+using UpdateKernel = void (*)(UpdateParams);
+UpdateKernel update_kernel(bool b16, bool mom) {
+    return b16 ? mom ? ortho_update_kernel<true, true> : ortho_update_kernel<true, false>
+               : mom ? ortho_update_kernel<false, true> : ortho_update_kernel<false, false>;
+}
+UpdateKernel start_kernel(bool b16, bool mom) {
+    return b16 ? mom ? ortho_start_kernel<true, true> : ortho_start_kernel<true, false>
+               : mom ? ortho_start_kernel<false, true> : ortho_start_kernel<false, false>;
+}
+
 }  // namespace
 
 cudaError_t preload_ortho_kernels() {
@@ -1907,9 +1977,11 @@ cudaError_t preload_ortho_kernels() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(ortho_resident_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = prepare_kernel(ortho_fused_kernel);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(ortho_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FUSED_SMEM);
-    if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<true>);
-    if (e == cudaSuccess) e = prepare_kernel(ortho_update_kernel<false>);
-    if (e == cudaSuccess) e = prepare_kernel(ortho_start_kernel);
+    for (uint32_t k = 0; k < 4; ++k) {
+        if (e == cudaSuccess) e = prepare_kernel(update_kernel(k & 1, k & 2));
+        if (e == cudaSuccess) e = prepare_kernel(start_kernel(k & 1, k & 2));
+    }
+    if (e == cudaSuccess) e = prepare_kernel(ortho_update_elements_kernel);
     if (e == cudaSuccess) e = prepare_kernel(ortho_start_tiles_kernel<true>);
     if (e == cudaSuccess) e = prepare_kernel(ortho_start_tiles_kernel<false>);
     return e;
@@ -2039,7 +2111,9 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     for (const auto& a : args)
         if (a.p != out && a.p) vec = vec && reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.pitch % 16 == 0 && a.stride % 16 == 0;
     const uint64_t items = d.rows * (vec ? d.cols / 8 : d.cols);
-    up.parts = (uint32_t)std::min<uint64_t>((items + 1023) / 1024, std::max(kMaxParts / d.batch, 1u));
+    const bool b16 = d.x_dtype == DTT_BF16;
+    const uint64_t each = 256 * (vec ? b16 && !momentum ? 4 : 2 : 4);
+    up.parts = (uint32_t)std::min<uint64_t>((items + each - 1) / each, std::max(kMaxParts / d.batch, 1u));
     if (o->resident) {
         ResidentParams r{};
         r.u = up;
@@ -2057,12 +2131,10 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     }
     const dim3 parts(up.parts, d.batch);
     // not overlapped with what ran before: it may write the update that this reads
-    if (vec) ortho_update_kernel<true><<<parts, 256, 0, stream>>>(up);
-    else ortho_update_kernel<false><<<parts, 256, 0, stream>>>(up);
-    DTT_CUDA_TRY(cudaGetLastError());
+    DTT_CUDA_TRY(launch(vec ? update_kernel(b16, momentum) : ortho_update_elements_kernel, parts, 256, 0, 0, false, stream, up));
     if (vec && !tall) {
-        const uint32_t ctas = (uint32_t)std::min<uint64_t>((items + 511) / 512, std::max(8 * o->sms / d.batch, 1u));
-        DTT_CUDA_TRY(launch(ortho_start_kernel, dim3(ctas, d.batch), 256, 0, 0, true, stream, up));
+        const uint32_t ctas = (uint32_t)std::min<uint64_t>((items + 511) / 512, std::max(START_CTAS * o->sms / d.batch, 1u));
+        DTT_CUDA_TRY(launch(start_kernel(b16, momentum), dim3(ctas, d.batch), 256, 0, 0, true, stream, up));
     } else {
         const dim3 tiles(ceil_div(up.cols, kStartTile), ceil_div(up.rows, kStartTile), d.batch);
         DTT_CUDA_TRY(launch(tall ? ortho_start_tiles_kernel<true> : ortho_start_tiles_kernel<false>, tiles, 256, 0, 0, true, stream, up));
