@@ -22,13 +22,14 @@ namespace {
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its reciprocal stays finite
-// Partial rows of the weight's gradient, at most: four, eight or sixteen a SM.
-__host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return cols > 1024 ? 608 : cols > 512 ? 1216 : 2432; }
+// Partial rows of the weight's gradient, at most: four, eight or sixteen a SM.  Rows of one warp (256
+// columns and less) have several in a CTA: 20000 x 256 25 us with sixteen CTAs a SM, 20 with four.
+__host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return cols > 1024 || cols <= 256 ? 608 : cols > 512 ? 1216 : 2432; }
 constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   // a row's most threads
 constexpr uint32_t kRingStages = 8;        // of a CTA, at most
 constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr uint32_t kFwdWarpCols = 256, kBwdWarpCols = 512;   // columns of rows that one warp takes, at most
+constexpr uint32_t kFwdWarpCols = 256, kBwdWarpCols = 256;   // columns of rows that one warp takes, at most
 constexpr uint32_t kWarpRows = 8;          // rows of a CTA whose rows are one warp each
 constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
 
@@ -916,10 +917,12 @@ struct Ring {
 // Chunks (vec): one a thread up to `one` columns, two up to 512 threads, then four.  Elements: 8 a thread up to
 // `one` columns, then 16.  Rows of one warp are left to the other forms.  threads: of an SM with one, two
 // and four chunks (what the registers allow), in as many CTAs, fewer where three stages each would not
-// fit; then as many stages as fit, but no more than `stages` where an SM has four CTAs or more.
-Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t one, const uint32_t (&threads)[3], uint32_t stages) {
+// fit, but `least` all the same where two would; then as many stages as fit, but no more than `stages`
+// where an SM has four CTAs or more.  Measured: the forward pass of 20000 x 5001 (f32) takes 279 us with
+// one CTA of five stages, 211 with two of two; the backward pass of 4000 x 4096 (f32) 49 us with one, 53 with two.
+Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t one, const uint32_t (&threads)[3], uint32_t least, uint32_t stages) {
     Ring g{};
-    if (3 * stage > kRingSmem) return g;
+    if (2 * stage > kRingSmem) return g;
     const uint32_t stage_bytes = (uint32_t)stage;
     uint32_t i = 0;
     for (; i < (vec ? 3 : 2); ++i) {
@@ -928,7 +931,7 @@ Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t one, const uint32
         if (g.threads <= kRingThreads && (i > 0 || cols <= one)) break;
     }
     if (g.threads < 64 || g.threads > kRingThreads) return {};
-    g.ctas = std::min({std::max(threads[i] / g.threads, 1u), kRingSmem / (3 * stage_bytes), 16u});
+    g.ctas = std::min({std::max(threads[i] / g.threads, 1u), std::max(kRingSmem / (3 * stage_bytes), std::min(kRingSmem / (2 * stage_bytes), least)), 16u});
     g.stages = std::min(g.ctas >= 4 ? stages : kRingStages, kRingSmem / (g.ctas * stage_bytes));
     g.smem = g.stages * stage_bytes;
     return g;
@@ -954,8 +957,11 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
     // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
     // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
-    const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, p.rows >= 32 * sms ? 2 : kRingStages);
-    if (g.ctas && p.rows >= 2 * sms && !(vec && p.cols <= kFwdWarpCols)) {
+    const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : kRingStages);
+    // The chunk form's loads wait for one another, the ring's do not: 152 x 8064 (bf16) 6.7 us by chunks, 3.7 by
+    // the ring.  The element form's go out together, and it is the faster one while there are few rows:
+    // 600 x 3001 5.7 us and 6.6, 2400 x 3001 22.2 and 18.4.
+    if (g.ctas && (vec ? p.cols > kFwdWarpCols : p.rows >= 8 * sms)) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
         auto kernel = vec ? (g.nch == 1 ? rmsnorm_fwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_fwd_ring_elements_kernel<8> : rmsnorm_fwd_ring_elements_kernel<16>);
@@ -989,8 +995,10 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
     const uint32_t sms = sm_count();
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
-    const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 2048, {1024, 512, 256}, kRingStages);
-    if (g.ctas && p.rows >= 2 * sms && !(vec && p.cols <= kBwdWarpCols)) {
+    const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 2048, {1024, 512, 256}, 1, kRingStages);
+    // by chunks and by the ring: 16 x 4096 (bf16) 6.6 us and 4.7, 16384 x 4096 255 and 92; by elements and by
+    // the ring: 152 x 1021 (f32) 5.5 and 5.6, 460 x 5001 (f32) 15.3 and 10.8
+    if (g.ctas && (vec ? p.cols > kBwdWarpCols : p.rows > sms)) {
         p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)most_partials(p.cols)});
         auto kernel = vec ? (g.nch == 1 ? rmsnorm_bwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
