@@ -1,14 +1,14 @@
 // Residual addition with a root-mean-square norm, and its backward pass (dtt_ops.h).
 //
-// Three forms of each pass, all f32 between the loads and the stores:
-//  - chunks (few rows, or rows too long for the others; 16-byte aligned, whole chunks): a row is spread over TPR
-//    threads in chunks of 8 columns: thread t holds columns 8 (i TPR + t) .. + 7 of chunk i, so a
-//    warp's accesses are contiguous, a thread moves 16 bytes of bf16 or 32 of f32 at a time, and a
-//    group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes of one warp;
-//  - elements (few rows that are not 16-byte aligned, or no whole number of chunks): thread t holds
-//    columns t, t + TPR, ..., so that accesses of single elements are contiguous over a warp;
-//  - ring (many rows, either layout): persistent CTAs whose rows come through a ring of shared-memory
-//    stages, bulk copies running ahead of the arithmetic.
+// All f32 between the loads and the stores.  The forms of each pass:
+//  - short (256 columns and less, 16-byte aligned, whole chunks of 8 columns): a row by a part of a warp;
+//  - ring (longer rows that two stages in shared memory have room for; rows that are not aligned where there
+//    are many): persistent CTAs whose rows come through a ring of stages, bulk copies running ahead of the
+//    arithmetic.  Aligned, thread t of T holds columns 8 (i T + t) .. + 7 of chunk i, so that accesses
+//    are contiguous over a warp, and a group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes;
+//  - chunks (aligned rows too long for the ring): the same layout, from global memory;
+//  - elements (what is not aligned or no whole number of chunks, and few rows of it): a warp holds 32 E
+//    neighbouring columns, a thread every 32nd of them.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -29,8 +29,8 @@ constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   
 constexpr uint32_t kRingStages = 8;        // of a CTA, at most
 constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr uint32_t kFwdWarpCols = 256, kBwdWarpCols = 256;   // columns of rows that one warp takes, at most
-constexpr uint32_t kWarpRows = 8;          // rows of a CTA whose rows are one warp each
+constexpr uint32_t kShortCols = 256;       // columns of the short form, at most
+constexpr uint32_t kWarpRows = 8;          // element form: rows of a CTA whose rows are one warp each
 constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
 
 struct FwdParams {
@@ -103,14 +103,13 @@ __device__ __forceinline__ float row_max(float v, uint32_t tpr, float* slot) {
     return warp_max(lane < tpr / 32 ? slot[lane] : 0.0f);
 }
 
-// One row by blockDim.x threads; blockDim.y rows a CTA where a row is one warp.  NCH chunks a
-// thread stay in registers; kLong reads the row again for each pass over it.
+// One row a CTA.  NCH chunks a thread stay in registers; kLong reads the row again for each pass over it.
+// 2000 x 32768 in bf16: 141 us, 0.55 of the copy rate; loads that wait for one another bound it.
 template <uint32_t NCH, bool VEC>
-__global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsnorm_fwd_kernel(const __grid_constant__ FwdParams p) {
+__global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_constant__ FwdParams p) {
     __shared__ float slots[2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
-    const uint64_t r = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (r >= p.rows) return;                        // a whole warp: rows share no barrier
+    const uint64_t r = blockIdx.x;
     const char* x = p.x + r * p.x_pitch;
     const char* res = p.res ? p.res + r * p.res_pitch : nullptr;
     char* res_out = p.res_out ? p.res_out + r * p.res_out_pitch : nullptr;
@@ -196,29 +195,119 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kFwdThreads) rmsn
     }
 }
 
-// Partial row of a CTA whose warps took rows of their own: their sums, in the warps' order.
-template <uint32_t N>
-__device__ __forceinline__ void add_warps(const float (&sums)[kWarpRows][N], float* part, uint32_t cols) {
-    __syncthreads();
-    for (uint32_t c = threadIdx.y * 32 + threadIdx.x; c < cols; c += kWarpRows * 32) {
-        float v = sums[0][c];
+// ---- short rows --------------------------------------------------------------------------------
+// A row by `lanes` neighbouring lanes of a warp (a power of two), a chunk each; a CTA has 256 / lanes rows.  A
+// thread's loads all go out before the first value is used, and many CTAs hide them: with two or four rows a
+// thread under way the forward pass of 300000 x 128 (bf16 to 8 bits) takes 58 and 82 us, with one 57,
+// 0.69 of the copy rate.
+__global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_constant__ FwdParams p, uint32_t lanes) {
+    const uint32_t t = threadIdx.x, l = t & (lanes - 1), c = 8 * l;
+    const uint64_t r = (uint64_t)blockIdx.x * (256 / lanes) + t / lanes, row = min(r, p.rows - 1);
+    const bool in = c < p.cols, mine = in && r < p.rows;
+    const uint32_t from = in ? c : 0;               // the lanes past the row read its first chunk
+    Raw8 xs = raw8(p.x + row * p.x_pitch + from * (p.x_dt == DTT_BF16 ? 2 : 4), p.x_dt), qs{}, ws{};
+    if (p.res) qs = raw8(p.res + row * p.res_pitch + from * (p.res_dt == DTT_BF16 ? 2 : 4), p.res_dt);
+    if (p.w) ws = raw8(p.w + from * (p.w_dt == DTT_BF16 ? 2 : 4), p.w_dt);
+    float h[8], o[8], sum = 0.0f;
+    expand8(xs, p.x_dt, h);
+    if (p.res) {
+        expand8(qs, p.res_dt, o);
 #pragma unroll
-        for (uint32_t i = 1; i < kWarpRows; ++i) v += sums[i][c];
-        part[c] = v;
+        for (uint32_t k = 0; k < 8; ++k) h[k] += o[k];
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        if (!in) h[k] = 0.0f;
+        sum += h[k] * h[k];
+    }
+    for (uint32_t d = lanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    const float s = rsqrtf(sum * p.inv_cols + p.eps);
+    if (mine && l == 0 && p.rstd) p.rstd[r] = s;
+    if (p.w) expand8(ws, p.w_dt, o);
+    float m = 0.0f;
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        o[k] = p.w ? h[k] * s * o[k] : h[k] * s;
+        m = max_nan(m, fabsf(o[k]));
+    }
+    if (p.y_dt == DTT_E4M3) {
+        const uint32_t share = p.group_lanes == 0 || p.group_lanes > lanes ? lanes : p.group_lanes;   // of a scale
+        if (!in) m = 0.0f;
+        for (uint32_t d = share / 2; d > 0; d /= 2) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        const float scale = scale_of(m), inv = inverse_of(scale);
+        if (mine && (l & (share - 1)) == 0) p.scales[p.group_lanes ? r * p.groups + l / share : r] = scale;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) o[k] *= inv;
+    }
+    if (!mine) return;
+    if (p.res_out) store8<true>(p.res_out + r * p.res_out_pitch, p.res_dt, c, p.cols, h);
+    store8<true>(p.y + r * p.y_pitch, p.y_dt, c, p.cols, o);
+}
+
+// The same split; a CTA walks over rows, each thread at the same columns, whose part of the weight's gradient
+// adds up in its registers; at the end the CTA's rows' sums, in their order, become its partial row.
+// 300000 x 128 in bf16: 64 us, 0.70 of the copy rate.
+__global__ void __launch_bounds__(256, 4) rmsnorm_bwd_short_kernel(const __grid_constant__ BwdParams p, uint32_t lanes) {
+    launch_next();
+    __shared__ float sums[256 * 8];
+    const uint32_t t = threadIdx.x, l = t & (lanes - 1), c = 8 * l, at_a_time = 256 / lanes;
+    const bool in = c < p.cols;
+    const uint32_t from = in ? c : 0, ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
+    float w[8], acc[8];
+    if (p.w) expand8(raw8(p.w + from * (p.w_dt == DTT_BF16 ? 2 : 4), p.w_dt), p.w_dt, w);
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        acc[k] = 0.0f;
+        if (!p.w) w[k] = 1.0f;
+    }
+    for (uint64_t r0 = (uint64_t)blockIdx.x * at_a_time; r0 < p.rows; r0 += (uint64_t)p.partials * at_a_time) {
+        const uint64_t r = r0 + t / lanes, row = min(r, p.rows - 1);
+        const bool mine = in && r < p.rows;
+        const Raw8 gs = raw8(p.dy + row * p.dy_pitch + from * ge, p.dy_dt), hs = raw8(p.h + row * p.h_pitch + from * he, p.h_dt);
+        Raw8 ds{};
+        if (p.dres) ds = raw8(p.dres + row * p.dres_pitch + from * he, p.h_dt);
+        const float s = p.rstd[row];
+        float g[8], n[8], dot = 0.0f;
+        expand8(gs, p.dy_dt, g);
+        expand8(hs, p.h_dt, n);
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            n[k] *= s;
+            if (mine) acc[k] += g[k] * n[k];
+            g[k] *= w[k];
+            if (in) dot += g[k] * n[k];
+        }
+        for (uint32_t d = lanes / 2; d > 0; d /= 2) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+        const float m = dot * p.inv_cols;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) g[k] = s * (g[k] - n[k] * m);
+        if (p.dres) {
+            expand8(ds, p.h_dt, n);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) g[k] += n[k];
+        }
+        if (mine) store8<true>(p.dx + r * p.dx_pitch, p.h_dt, c, p.cols, g);
+    }
+    if (!p.partial) return;
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) sums[8 * t + k] = acc[k];     // 256 / lanes rows of 8 lanes columns
+    __syncthreads();
+    if (t < p.cols) {
+        float v = 0.0f;
+        for (uint32_t i = 0; i < at_a_time; ++i) v += sums[i * 8 * lanes + t];
+        p.partial[(uint64_t)blockIdx.x * p.cols + t] = v;
     }
 }
 
-// A CTA (or a warp, where a row is one warp) walks over rows: each thread keeps the same columns for
-// all of them, so the weight's gradient adds up in its registers and is written once, as the CTA's
-// partial row (kLong: in the partial row itself).
+// A CTA walks over rows: each thread keeps the same columns for all of them, so the weight's gradient adds up
+// in its registers and is written once, as the CTA's partial row (kLong: in the partial row itself).
+// 2000 x 16384 in f32: 173 us, 0.45 of the copy rate, bound as the forward pass.
 template <uint32_t NCH, bool VEC>
-__global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
     __shared__ float slots[2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
-    constexpr bool WARPS = NCH != kLong && 32 * 8 * NCH <= kBwdWarpCols;     // rows of one warp come here
-    __shared__ float sums[kWarpRows][WARPS ? 32 * 8 * NCH : 1];
-    const uint32_t me = blockIdx.x * blockDim.y + threadIdx.y;
+    const uint32_t me = blockIdx.x;
     constexpr uint32_t HELD = NCH == kLong ? 1 : NCH;
     const uint32_t nch = NCH == kLong ? (p.cols + 8 * tpr - 1) / (8 * tpr) : NCH;
     float acc[HELD][8];
@@ -301,10 +390,8 @@ __global__ void __launch_bounds__(NCH == 1 || NCH == 2 ? 256 : kBwdThreads) rmsn
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
                 const uint32_t c = 8 * (i * tpr + t) + k;
-                if (WARPS && blockDim.y > 1) sums[threadIdx.y][WARPS ? c : 0] = acc[i][k];
-                else if (c < p.cols) part[c] = acc[i][k];
+                if (c < p.cols) part[c] = acc[i][k];
             }
-        if (WARPS && blockDim.y > 1) add_warps(sums, part, p.cols);
     }
 }
 
@@ -442,6 +529,18 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const
     for (uint32_t k = 0; k < E; ++k) h[k] = p.w ? h[k] * s * o[k] : h[k] * s;
     if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[1], h);
     store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
+}
+
+// Partial row of a CTA whose warps took rows of their own: their sums, in the warps' order.
+template <uint32_t N>
+__device__ __forceinline__ void add_warps(const float (&sums)[kWarpRows][N], float* part, uint32_t cols) {
+    __syncthreads();
+    for (uint32_t c = threadIdx.y * 32 + threadIdx.x; c < cols; c += kWarpRows * 32) {
+        float v = sums[0][c];
+#pragma unroll
+        for (uint32_t i = 1; i < kWarpRows; ++i) v += sums[i][c];
+        part[c] = v;
+    }
 }
 
 // As the chunk form: a CTA or a warp walks over rows, the weight's gradient in its registers.
@@ -894,22 +993,6 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* part
     if (lane == 0 && (uint64_t)blockIdx.x * 32 + warp < cols) dweight[(uint64_t)blockIdx.x * 32 + warp] = v;
 }
 
-struct Shape {
-    uint32_t nch, tpr, rows_per_cta;
-};
-
-// Chunks: a warp a row up to `warp_cols` columns; else up to four a thread in registers, `threads` threads a
-// row at most.
-Shape shape_of(uint32_t cols, uint32_t threads, uint32_t warp_cols) {
-    const uint32_t chunks = (cols + 7) / 8;
-    for (uint32_t nch : {1u, 2u, 4u}) {
-        if (cols <= warp_cols && chunks <= 32 * nch) return {nch, 32, kWarpRows};
-        const uint32_t tpr = ((chunks + nch - 1) / nch + 31) / 32 * 32;
-        if (cols > warp_cols && tpr <= (nch == 4 ? threads : 256u)) return {nch, tpr, 1};
-    }
-    return {kLong, threads, 1};
-}
-
 struct Ring {
     uint32_t nch, threads, ctas, stages, smem;       // ctas: of an SM; 0: no ring for these rows
 };
@@ -937,6 +1020,12 @@ Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t one, const uint32
     return g;
 }
 
+uint32_t short_lanes(uint32_t cols) {
+    uint32_t n = 1;
+    while (8 * n < cols) n *= 2;
+    return n;
+}
+
 uint32_t sm_count() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -957,11 +1046,17 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
     // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
     // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
+    if (vec && p.cols <= kShortCols) {
+        const uint32_t lanes = short_lanes(p.cols);
+        const uint64_t each = 256 / lanes;
+        rmsnorm_fwd_short_kernel<<<(uint32_t)((p.rows + each - 1) / each), 256, 0, stream>>>(p, lanes);
+        return;
+    }
     const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : kRingStages);
     // The chunk form's loads wait for one another, the ring's do not: 152 x 8064 (bf16) 6.7 us by chunks, 3.7 by
     // the ring.  The element form's go out together, and it is the faster one while there are few rows:
     // 600 x 3001 5.7 us and 6.6, 2400 x 3001 22.2 and 18.4.
-    if (g.ctas && (vec ? p.cols > kFwdWarpCols : p.rows >= 8 * sms)) {
+    if (g.ctas && (vec || p.rows >= 8 * sms)) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
         auto kernel = vec ? (g.nch == 1 ? rmsnorm_fwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_fwd_ring_elements_kernel<8> : rmsnorm_fwd_ring_elements_kernel<16>);
@@ -981,24 +1076,26 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
         rmsnorm_fwd_kernel<kLong, false><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
         return;
     }
-    const Shape s = shape_of(p.cols, kFwdThreads, kFwdWarpCols);
-    const dim3 block(s.tpr, s.rows_per_cta);
-    const uint32_t grid = (uint32_t)((p.rows + s.rows_per_cta - 1) / s.rows_per_cta);
-    if (s.nch == 1) rmsnorm_fwd_kernel<1, true><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 2) rmsnorm_fwd_kernel<2, true><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 4) rmsnorm_fwd_kernel<4, true><<<grid, block, 0, stream>>>(p);
-    else rmsnorm_fwd_kernel<kLong, true><<<grid, block, 0, stream>>>(p);
+    if (p.cols <= 32 * kFwdThreads) rmsnorm_fwd_kernel<4, true><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
+    else rmsnorm_fwd_kernel<kLong, true><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
 }
 
 // Sets p.partials, the partial rows of the weight's gradient that the launch writes.
 void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
     const uint32_t sms = sm_count();
+    if (vec && p.cols <= kShortCols) {
+        const uint32_t lanes = short_lanes(p.cols);
+        const uint64_t each = 256 / lanes;
+        p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, most_partials(p.cols));
+        rmsnorm_bwd_short_kernel<<<p.partials, 256, 0, stream>>>(p, lanes);
+        return;
+    }
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
     const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 2048, {1024, 512, 256}, 1, kRingStages);
     // by chunks and by the ring: 16 x 4096 (bf16) 6.6 us and 4.7, 16384 x 4096 255 and 92; by elements and by
     // the ring: 152 x 1021 (f32) 5.5 and 5.6, 460 x 5001 (f32) 15.3 and 10.8
-    if (g.ctas && (vec ? p.cols > kBwdWarpCols : p.rows > sms)) {
+    if (g.ctas && (vec || p.rows > sms)) {
         p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)most_partials(p.cols)});
         auto kernel = vec ? (g.nch == 1 ? rmsnorm_bwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
@@ -1024,14 +1121,8 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         rmsnorm_bwd_kernel<kLong, false><<<p.partials, kBwdThreads, 0, stream>>>(p);
         return;
     }
-    const Shape s = shape_of(p.cols, kBwdThreads, kBwdWarpCols);
-    const dim3 block(s.tpr, s.rows_per_cta);
-    walk(s.rows_per_cta);
-    const uint32_t grid = p.partials;
-    if (s.nch == 1) rmsnorm_bwd_kernel<1, true><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 2) rmsnorm_bwd_kernel<2, true><<<grid, block, 0, stream>>>(p);
-    else if (s.nch == 4) rmsnorm_bwd_kernel<4, true><<<grid, block, 0, stream>>>(p);
-    else rmsnorm_bwd_kernel<kLong, true><<<grid, block, 0, stream>>>(p);
+    if (p.cols <= 32 * kBwdThreads) rmsnorm_bwd_kernel<4, true><<<p.partials, kBwdThreads, 0, stream>>>(p);
+    else rmsnorm_bwd_kernel<kLong, true><<<p.partials, kBwdThreads, 0, stream>>>(p);
 }
 
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
@@ -1075,11 +1166,10 @@ cudaError_t prepare(const void* kernel) {
 
 cudaError_t preload_norm_kernels() {
     const void* kernels[] = {
-        (const void*)rmsnorm_fwd_kernel<1, true>, (const void*)rmsnorm_fwd_kernel<2, true>,
+        (const void*)rmsnorm_fwd_short_kernel, (const void*)rmsnorm_bwd_short_kernel,
         (const void*)rmsnorm_fwd_kernel<4, true>, (const void*)rmsnorm_fwd_kernel<kLong, true>,
         (const void*)rmsnorm_fwd_kernel<kLong, false>, (const void*)rmsnorm_fwd_elements_kernel<8>,
         (const void*)rmsnorm_fwd_elements_kernel<16>,
-        (const void*)rmsnorm_bwd_kernel<1, true>, (const void*)rmsnorm_bwd_kernel<2, true>,
         (const void*)rmsnorm_bwd_kernel<4, true>, (const void*)rmsnorm_bwd_kernel<kLong, true>,
         (const void*)rmsnorm_bwd_kernel<kLong, false>, (const void*)rmsnorm_bwd_elements_kernel<8>,
         (const void*)rmsnorm_bwd_elements_kernel<16>, (const void*)rmsnorm_dweight_kernel};

@@ -115,6 +115,27 @@ __device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// 8 columns of bf16 or f32, as loaded and as f32.  Apart, because a load behind a branch of its own waits
+// for the one before it only where that one's values are looked at in between.
+struct Raw8 {
+    uint4 a, b;                 // b: f32 alone
+};
+__device__ __forceinline__ Raw8 raw8(const char* at, uint32_t dt) {
+    Raw8 q{};
+    q.a = *reinterpret_cast<const uint4*>(at);
+    if (dt != DTT_BF16) q.b = *reinterpret_cast<const uint4*>(at + 16);
+    return q;
+}
+__device__ __forceinline__ void expand8(const Raw8& q, uint32_t dt, float (&v)[8]) {
+    if (dt == DTT_BF16) {
+        v[0] = bf16_lo(q.a.x); v[1] = bf16_hi(q.a.x); v[2] = bf16_lo(q.a.y); v[3] = bf16_hi(q.a.y);
+        v[4] = bf16_lo(q.a.z); v[5] = bf16_hi(q.a.z); v[6] = bf16_lo(q.a.w); v[7] = bf16_hi(q.a.w);
+    } else {
+        v[0] = __uint_as_float(q.a.x); v[1] = __uint_as_float(q.a.y); v[2] = __uint_as_float(q.a.z); v[3] = __uint_as_float(q.a.w);
+        v[4] = __uint_as_float(q.b.x); v[5] = __uint_as_float(q.b.y); v[6] = __uint_as_float(q.b.z); v[7] = __uint_as_float(q.b.w);
+    }
+}
+
 // N elements at rows[n], column c[n], as f32.  The loads go out together: they are unconditional and the
 // type is decided once, since a load behind a branch of its own waits for the one before it.
 template <uint32_t N>

@@ -237,6 +237,56 @@ def test_backward_is_the_forward_s_difference_quotient():
             assert abs((up - down) / (2 * step) - float(grad[i])) < 1e-3
 
 
+# rows of a part of a warp; and the ring where a CTA has no row, or one row, and room for two stages alone
+SHORT = [(1, 8, dict(y="e4m3")), (33, 16, dict(y="e4m3", group=128)), (1000, 24, dict(y="e4m3", group=32)),
+         (70, 40, dict(y="e4m3", group=32)), (257, 64, dict(y="e4m3", group=64)), (10001, 128, dict(y="e4m3")),
+         (5003, 128, dict(residual="f32", y="e4m3", group=64)), (77, 200, dict(x="f32", residual="f32", y="e4m3", group=128)),
+         (513, 256, dict(weight=None)), (40, 136, dict(residual=None, weight="f32", y="f32")), (65, 128, dict(pad=8)),
+         (2, 264, dict(y="e4m3", group=64)), (151, 12288, dict(x="f32", residual="f32", y="e4m3", group=128)),
+         (1217, 1001, dict(y="e4m3", group=64)), (1215, 1001, dict(y="e4m3", group=64))]
+
+
+@pytest.mark.parametrize("rows,cols,over", SHORT)
+def test_short_rows_and_small_rings(rows, cols, over):
+    op, a, out = norm_case(rows, cols, **over)
+    op.forward(**a, **out)
+    torch.cuda.synchronize()
+    check_forward(a, out, over.get("y", "bf16"), over.get("group", 0))
+    kinds = {k: over[k] for k in ("x", "pad") if k in over}
+    kinds["residual"] = over.get("residual") or "bf16"
+    for dres in (True, False):
+        op, a, dres, dx = grad_case(rows, cols, dres=dres, **kinds)
+        dw, again = torch.full((cols,), 7.0, device="cuda"), torch.zeros(cols, device="cuda")
+        op.backward(**a, dx=dx, dweight=dw, dres=dres)
+        op.backward(**a, dx=torch.empty_like(dx), dweight=again, dres=dres)
+        torch.cuda.synchronize()
+        check_backward(a, dres, dx, dw, kinds["residual"])
+        assert torch.equal(dw, again)
+
+
+def test_short_rows_keep_nan_to_themselves_and_their_slices():
+    """NaN in a row that shares its warp with others; nothing beside the rows is written."""
+    rows, cols, pad = 37, 104, 16
+    op, a, out = norm_case(rows, cols, y="e4m3", group=32)
+    a["x"][3, 50] = float("nan")
+    a["x"][4], a["residual"][4] = 0, 0
+    wide = torch.full((rows, cols + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+    out["residual_out"] = wide[:, 8:8 + cols]
+    op.forward(**a, **out)
+    torch.cuda.synchronize()
+    assert torch.isnan(out["rstd"][3]) and torch.isnan(out["y"][3].float()).all() and torch.isnan(out["scales"][3]).all()
+    assert (out["y"][4].float() == 0).all() and (out["scales"][4] == ON.SCALE_MIN).all()
+    keep = [i for i in range(rows) if i not in (3, 4)]
+    check_forward({k: v if k == "weight" else v[keep] for k, v in a.items()}, {k: v[keep] for k, v in out.items()}, "e4m3", 32)
+    assert (wide[:, :8] == 7).all() and (wide[:, 8 + cols:] == 7).all()
+    op, a, dres, dx = grad_case(rows, cols)
+    a["dy"][3, 50] = float("nan")
+    op.backward(**a, dx=dx, dres=dres)
+    torch.cuda.synchronize()
+    assert torch.isnan(dx[3]).all()
+    check_backward({k: v if k == "weight" else v[keep] for k, v in a.items()}, dres[keep], dx[keep], None, "bf16")
+
+
 # ---- orthogonalisation ----------------------------------------------------------------------------
 # The result's bf16 rounding is 1.7e-3 of its norm (half a spacing at most, uniform).  Operands rounded to f16
 # (2^-12 of the value, uniform: 1.4e-4) enter a step through b A + c A A, at most 2.9 in norm, three of
