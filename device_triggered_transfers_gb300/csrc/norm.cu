@@ -505,7 +505,7 @@ __device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, f
     }
 }
 
-// A row a CTA, or a warp (blockDim.y of them).
+// A row a CTA, or a warp (blockDim.y of them).  600 x 3001 in bf16: 5.7 us back to back, the loads' latency.
 template <uint32_t E>
 __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const __grid_constant__ FwdParams p) {
     __shared__ float slots[2][32];
@@ -543,7 +543,8 @@ __device__ __forceinline__ void add_warps(const float (&sums)[kWarpRows][N], flo
     }
 }
 
-// As the chunk form: a CTA or a warp walks over rows, the weight's gradient in its registers.
+// As the chunk form: a CTA or a warp walks over rows, the weight's gradient in its registers.  100 x 1021 in bf16:
+// 5 us back to back with the sum of the partial rows; 300000 x 101 167 us, 0.21 of the copy rate, a 2-byte element a lane.
 template <uint32_t E>
 __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
@@ -614,7 +615,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const char* src, uint32_
 // Rows blockIdx.x, + gridDim.x, ... by one CTA.  Stage i % S holds the row of turn i: x, then the
 // residual.  Thread 0 starts the copies of turn i + S - 1 once turn i's reduction has passed its
 // barrier: every thread is then done with that stage's last row (turn i - 1).  A copy that does not
-// arrive makes the row NaN.
+// arrive makes the row NaN.  16384 x 4096 (bf16 to 8 bits, groups of 128): 80 us, 0.86 of the copy rate, the issue
+// slots 73 % full.
 template <uint32_t NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
     extern __shared__ __align__(128) uint8_t stages[];
@@ -726,7 +728,9 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
     }
 }
 
-// The backward pass the same way: a stage holds dy, h, then dres.
+// The backward pass the same way: a stage holds dy, h, then dres.  16384 x 4096 in bf16: 92 us with the weight's
+// gradient, 0.86 of the copy rate; 2048 x 4096 22 us, 0.44: a row's reduction and barrier with two CTAs a SM
+// (registers), and the sum of the partial rows.
 template <uint32_t NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 1) rmsnorm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
@@ -818,7 +822,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
 // The ring for rows at any alignment, an element a thread.  A bulk copy moves whole 16-byte
 // words: from the one that holds the row's first byte to the one that holds its last.  The few bytes
 // beside the row in these two are copied with it and not looked at (an allocation never ends within
-// such a word).
+// such a word).  4093 x 5001 (bf16 with an f32 residual): 43 us, 0.83 of the copy rate.
 struct Words {
     uint64_t from;              // address of the first
     uint32_t bytes;             // of all
@@ -901,6 +905,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
     }
 }
 
+// 16384 x 4001 in f32: 179 us, 0.86 of the copy rate; 1021 x 5001 in f32 22 us, 0.53: one CTA a SM (60 KiB a
+// stage), seven rows each.
 template <uint32_t E>
 __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
@@ -974,7 +980,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
 }
 
 // dweight[c] = the partial rows' sum.  32 columns a CTA; its 32 warps take every 32nd partial row, and
-// their sums are added in warp order.
+// their sums are added in warp order.  304 partial rows of 4096: about 4 us, from L2.
 __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* partial, uint32_t partials, uint32_t cols, float* dweight) {
     __shared__ float part[32][33];
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;

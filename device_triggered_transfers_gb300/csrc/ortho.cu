@@ -471,6 +471,9 @@ __device__ __forceinline__ void umma_commit_local2(uint32_t bar) {
 //   warp 10     fills the slab buffers with what a slab needs (two slabs ahead) and stores them, in
 //               whole 128-byte lines: stored by the threads that hold the rows, a tile took 14,000
 //               cycles instead of 6,000.
+// 4096 x 4096, five steps in one launch: ~870 us for 1.37 TFLOP of products (half of each symmetric
+// one), the tensor pipe active 75 % of the time.  Back to back the power limit takes the SM clock from 2.07
+// to 1.67 GHz, and a call from 910 us to 1010.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 ortho_pair_kernel(const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -814,7 +817,9 @@ __device__ __forceinline__ void fetch_fours(const GemmParams& p, uint32_t m, uin
 
 // One 128 x 128 tile a cluster, its k blocks shared out over the cluster's CTAs (CTAS: one, two, four
 // or eight).  Each CTA leaves its f32 sums in its shared memory; CTA q then adds rows q 128 / CTAs .. of
-// all of them, in the CTAs' order, through distributed shared memory, and stores those rows.
+// all of them, in the CTAs' order, through distributed shared memory, and stores those rows.  A of two 1024 x
+// 4096: 18 us, the tensor pipe active 30 %: what an SM can load bounds it (0.36 us a k block of 32 KiB), and
+// 3 us between the launch and the first MMA.
 template <Product P, uint32_t CTAS>
 __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -968,7 +973,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
 // S <= 256, APPLY with its own b A + c A A: one 128 x 128 tile a CTA.  All of A (as two row blocks) and the
 // tile's columns of X are loaded at once; b A + c A A of the tile's rows takes their place in A, what its
 // rounding to f16 leaves the other row block's (a second term of the last product).  A launch
-// of POLY costs 6 us at these sizes, working its rows out again in every CTA 3 us.
+// of POLY costs 6 us at these sizes, working its rows out again in every CTA 3 us.  256 x 1000: 8 us, 14 us with
+// cold caches; one chain of load, MMA, rounding, MMA and store, on 16 SMs.
 constexpr uint32_t FUSED_SMEM = 1024 /* alignment slack */ + (8 + 4) * HALF_STAGE + 256;
 static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= 8 * HALF_STAGE, "the tile fits A's place");
 
@@ -1161,34 +1167,21 @@ __device__ __forceinline__ void chunks(const UpdateParams& p, const char* x, con
         r[n] = j / per_row;
         c[n] = 8 * (j - r[n] * per_row);
     }
-    uint4 raw[N][2], old[N][2];
+    Raw8 xs[N], moms[N];
     if (want_x) {
 #pragma unroll
-        for (uint32_t n = 0; n < N; ++n) {
-            const uint4* at = reinterpret_cast<const uint4*>(x + r[n] * p.x_pitch + (uint64_t)c[n] * (B16 ? 2 : 4));
-            raw[n][0] = at[0];
-            if (!B16) raw[n][1] = at[1];
-        }
+        for (uint32_t n = 0; n < N; ++n)
+            xs[n] = raw8(x + r[n] * p.x_pitch + (uint64_t)c[n] * (B16 ? 2 : 4), B16 ? DTT_BF16 : DTT_F32);
     }
     if (MOM) {
 #pragma unroll
-        for (uint32_t n = 0; n < N; ++n) {
-            const uint4* at = reinterpret_cast<const uint4*>(mom + r[n] * p.mom_pitch + (uint64_t)c[n] * 4);
-            old[n][0] = at[0];
-            old[n][1] = at[1];
-        }
+        for (uint32_t n = 0; n < N; ++n) moms[n] = raw8(mom + r[n] * p.mom_pitch + (uint64_t)c[n] * 4, DTT_F32);
     }
 #pragma unroll
-    for (uint32_t n = 0; n < N; ++n)
-#pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-            auto word = [](const uint4& q, uint32_t e) { return e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w; };
-            if (want_x) {
-                const uint32_t w = B16 ? word(raw[n][0], k / 2) : word(raw[n][k / 4], k % 4);
-                u[n][k] = !B16 ? __uint_as_float(w) : k % 2 ? bf16_hi(w) : bf16_lo(w);
-            }
-            if (MOM) v[n][k] = __uint_as_float(word(old[n][k / 4], k % 4));
-        }
+    for (uint32_t n = 0; n < N; ++n) {
+        if (want_x) expand8(xs[n], B16 ? DTT_BF16 : DTT_F32, u[n]);
+        if (MOM) expand8(moms[n], DTT_F32, v[n]);
+    }
 }
 // Bytes under way are what counts: a thread has 64 to 128 of them.
 template <bool B16, bool MOM>
@@ -1288,7 +1281,8 @@ __device__ __forceinline__ float inverse_norm(const UpdateParams& p, uint32_t m,
 }
 
 // u again (the momentum is updated by now) and X = u / (|u| + eps), in its two halves: rows
-// <= cols, 16-byte aligned.
+// <= cols, 16-byte aligned.  4096 x 4096 in bf16: 16 us behind the update (10 us), 33 MB read from L2 and 67
+// written.
 template <bool B16, bool MOM>
 __global__ void __launch_bounds__(256, START_CTAS) ortho_start_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
@@ -1426,7 +1420,9 @@ __device__ __forceinline__ float load_peer1(uint32_t cluster_addr) {
 // place.  The two exchanges (bulk copies; stores by the threads took twice as long) are their own
 // hand-shake: a CTA's sums of the next step leave after it has used b A + c A A, its rows of A after
 // it has read the sums, and nobody goes on without all of either.  One launch, and nothing but the
-// update and the result in memory: a product's 5 us as a launch of its own are mostly set-up here.
+// update and the result in memory: a product's 5 us as a launch of its own are mostly set-up here.  128 x 4096
+// takes 58 us for five steps, 128 x 128 25: the exchanges' and MMAs' latencies one after the other (tensor pipe
+// 12 % of an SM's time).
 template <uint32_t CTAS>
 __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __grid_constant__ ResidentParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -1472,15 +1468,25 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
         const uint32_t per_row = (tall ? 128 : width) / 8;
         for (uint32_t e0 = t; e0 < 16 * width; e0 += N * RES_THREADS) {     // 16 width: a multiple of N RES_THREADS
             float u[N][8], v[N][8];
+            Raw8 xs[N], moms[N];
+            uint32_t inside = 0;
 #pragma unroll
             for (uint32_t n = 0; n < N; ++n) {
                 const uint32_t e = e0 + n * RES_THREADS, r = e / per_row, c = 8 * (e - r * per_row);
                 const uint32_t gr = tall ? l0 + r : r, gc = tall ? c : l0 + c;
                 const bool in = gr < p.u.rows && gc < p.u.cols;
+                const uint64_t fr = in ? gr : 0, fc = in ? gc : 0;
+                inside |= (uint32_t)in << n;
+                xs[n] = raw8(x + fr * p.u.x_pitch + fc * (p.u.x_dt == DTT_BF16 ? 2 : 4), p.u.x_dt);
+                if (mom) moms[n] = raw8(mom + fr * p.u.mom_pitch + fc * 4, DTT_F32);
+            }
 #pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) u[n][k] = v[n][k] = 0.0f;
-                if (in) load8<true>(x + gr * p.u.x_pitch, p.u.x_dt, gc, p.u.cols, u[n]);
-                if (in && mom) load8<true>(mom + gr * p.u.mom_pitch, DTT_F32, gc, p.u.cols, v[n]);
+            for (uint32_t n = 0; n < N; ++n) {
+                expand8(xs[n], p.u.x_dt, u[n]);
+                if (mom) expand8(moms[n], DTT_F32, v[n]);
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    if (!(inside >> n & 1)) u[n][k] = v[n][k] = 0.0f;
             }
 #pragma unroll
             for (uint32_t n = 0; n < N; ++n) {
@@ -1856,7 +1862,8 @@ uint32_t tiles_of(bool square, uint32_t tile_m, uint32_t tile_n, uint64_t rows, 
     return square ? tm * (tm + 1) / 2 : tm * ceil_div(cols, tile_n);
 }
 
-// The form whose estimated time is least.  Measured: a k block of 64 costs a pair 0.275 us at 256 columns,
+// The form whose estimated time is least: clusters of 1 instead of the best number take 179 us for 1024 x 1024
+// and not 127, 234 for 700 x 4000 and not 164.  Measured: a k block of 64 costs a pair 0.275 us at 256 columns,
 // 0.21 us at 128, and its set-up and last epilogue 8 us; a split CTA takes 0.36 us a k block (what one SM
 // can load) and 4.6 us besides in every round of tiles, 0.6 us more where a cluster adds up its sums, 0.5
 // more in one of eight.
@@ -1894,12 +1901,16 @@ double flow_us(uint64_t S, uint64_t L, uint32_t batch, const Fit& fit) {
     return 18.0 + std::max(1.15 * (square * (gram + other) + oblong * other) / fit.pairs, gram + 2 * other);
 }
 
-// The same for POLY and APPLY in one (S <= 256): 9 us a round of tiles, measured.
+// The same for POLY and APPLY in one (S <= 256): 9 us a round of tiles, measured.  Two launches instead: 100 us
+// for 1000 x 256 and not 86, 109 for 256 x 4096 and not 95.
 double fused_us(uint64_t S, uint64_t L, uint32_t batch, uint32_t sms) {
     return 0.8 + 9.0 * ceil_div((uint64_t)tiles_of(false, 128, 128, S, L) * batch, sms);
 }
 
-// CTAs of a cluster that hold S x L in shared memory: as few as can (A crosses them all); 0: none can.
+// CTAs of a cluster that hold S x L in shared memory: as few as can (A crosses them all); 0: none can.  Taken
+// wherever one can: 128 x 4096 58 us against 89 with a launch a product, 32 of them 285 and 364, 256
+// of 128 x 512 188 and 430.  (At 64 rows, with more clusters of 16 than run at once, it is level: 64 of 64 x 4096
+// take 546 and 532.)
 uint32_t resident_ctas(uint64_t S, uint64_t L) {
     uint32_t ctas = 1;
     while (ctas < RES_CTAS && ceil_div(L, 64) > ctas * RES_BLOCKS) ctas *= 2;

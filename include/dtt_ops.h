@@ -94,8 +94,9 @@ int dtt_rmsnorm_workspace(const dtt_rmsnorm_desc* desc, uint64_t* bytes);
  *     out = scale X (transposed back), rounded to bf16.
  * Each step maps every singular value s of X to a s + b s^3 + c s^5 and keeps the singular
  * vectors.  The products run on the tensor cores with f16 operands and f32 sums; X itself is held
- * in f32 throughout, because a rounded iterate's noise in the directions that u lacks would grow
- * by a (3.44 with the usual coefficients) in every step. */
+ * in 32 bits (two f16 halves, 22 significant bits), because a rounded iterate's noise in the
+ * directions that u lacks would grow by a (3.44 with the usual coefficients) in every step.  Large
+ * matrices run as one cooperative launch over all SMs: it begins when they are free. */
 #define DTT_ORTHO_MAX_STEPS 32
 
 typedef struct dtt_ortho_desc {
