@@ -30,6 +30,10 @@ constexpr uint32_t kRingStages = 8;        // of a CTA, at most
 constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kShortCols = 256;       // columns of the short form, at most
+// Rows whose weight gradient is added up by columns in the same launch, at most.  By partial rows and by columns, back to
+// back in a graph: 16 x 4096 (bf16) 4.6 us and 2.8, 64 x 8064 6.6 and 4.5, 152 x 4096 6.1 and 3.8, 152 x 1024 5.1 and
+// 5.5, 152 x 16384 13.6 and 14.5, 304 x 8064 9.9 and 11.6.
+constexpr uint32_t kFewRows = 96;
 constexpr uint32_t kWarpRows = 8;          // element form: rows of a CTA whose rows are one warp each
 constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
 
@@ -56,7 +60,8 @@ struct BwdParams {
     const float* rstd;
     const char* dres;           // or null
     char* dx;
-    float* partial;             // [partials][cols], or null: no weight gradient
+    float* partial;             // [partials][cols], or null: no weight gradient, or few rows
+    float* dweight;             // few rows: the CTAs after the first `partials` work it out; else null
     uint64_t dy_pitch, h_pitch, dres_pitch, dx_pitch;
     uint64_t rows;
     uint32_t cols, partials, walkers;   // walker i takes rows i, i + walkers, ...
@@ -195,6 +200,44 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
     }
 }
 
+// The weight's gradient where there are few rows: it does not wait for the rows' means, so that CTAs of the same
+// launch add it up, 32 columns at a time, a warp every `warps`-th row, the warps' sums in their order.
+__device__ __forceinline__ void weight_columns(const BwdParams& p) {
+    __shared__ float sums[kBwdThreads / 32][32];
+    constexpr uint32_t N = 4;
+    const uint32_t t = threadIdx.y * blockDim.x + threadIdx.x, lane = t % 32, warp = t / 32, warps = blockDim.x * blockDim.y / 32;
+    for (uint32_t b = blockIdx.x - p.partials; b < (p.cols + 31) / 32; b += gridDim.x - p.partials) {
+        const uint32_t c = 32 * b + lane;
+        uint32_t cs[N];
+#pragma unroll
+        for (uint32_t n = 0; n < N; ++n) cs[n] = min(c, p.cols - 1);
+        float v = 0.0f;
+        for (uint64_t r0 = warp; r0 < p.rows; r0 += N * warps) {
+            const char *gs[N], *hs[N];
+            float g[N], h[N], s[N];
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n) {
+                const uint64_t r = min(r0 + n * warps, p.rows - 1);
+                gs[n] = p.dy + r * p.dy_pitch;
+                hs[n] = p.h + r * p.h_pitch;
+                s[n] = p.rstd[r];
+            }
+            gather(gs, p.dy_dt, cs, g);
+            gather(hs, p.h_dt, cs, h);
+#pragma unroll
+            for (uint32_t n = 0; n < N; ++n)
+                if (r0 + n * warps < p.rows) v += g[n] * (h[n] * s[n]);
+        }
+        sums[warp][lane] = v;
+        __syncthreads();
+        if (warp == 0) {
+            for (uint32_t i = 1; i < warps; ++i) v += sums[i][lane];
+            if (c < p.cols) p.dweight[c] = v;
+        }
+        __syncthreads();
+    }
+}
+
 // ---- short rows --------------------------------------------------------------------------------
 // A row by `lanes` neighbouring lanes of a warp (a power of two), a chunk each; a CTA has 256 / lanes rows.  A
 // thread's loads all go out before the first value is used, and many CTAs hide them: with two or four rows a
@@ -249,6 +292,7 @@ __global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_con
 // 300000 x 128 in bf16: 64 us, 0.70 of the copy rate.
 __global__ void __launch_bounds__(256, 4) rmsnorm_bwd_short_kernel(const __grid_constant__ BwdParams p, uint32_t lanes) {
     launch_next();
+    if (blockIdx.x >= p.partials) return weight_columns(p);
     __shared__ float sums[256 * 8];
     const uint32_t t = threadIdx.x, l = t & (lanes - 1), c = 8 * l, at_a_time = 256 / lanes;
     const bool in = c < p.cols;
@@ -305,6 +349,7 @@ __global__ void __launch_bounds__(256, 4) rmsnorm_bwd_short_kernel(const __grid_
 template <uint32_t NCH, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
+    if (blockIdx.x >= p.partials) return weight_columns(p);
     __shared__ float slots[2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
     const uint32_t me = blockIdx.x;
@@ -548,6 +593,7 @@ __device__ __forceinline__ void add_warps(const float (&sums)[kWarpRows][N], flo
 template <uint32_t E>
 __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
+    if (blockIdx.x >= p.partials) return weight_columns(p);
     __shared__ float slots[2][32];
     __shared__ float sums[kWarpRows][32 * E];
     const uint32_t T = blockDim.x;
@@ -734,6 +780,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
 template <uint32_t NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 1) rmsnorm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
+    if (blockIdx.x >= p.partials) return weight_columns(p);
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][32];
     __shared__ uint64_t full[kRingStages];
@@ -746,7 +793,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
         if (next >= p.rows) return;
         const uint64_t r = next;
         const uint32_t bar = saddr(full + next_st), dst = saddr(stages) + next_st * stage_bytes;
-        next += gridDim.x;
+        next += p.partials;
         if (++next_st == S) next_st = 0;
         bar_expect_tx(bar, stage_bytes);
         bulk_load(dst, p.dy + r * p.dy_pitch, gb, bar);
@@ -775,7 +822,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
-    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
+    for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
         const float s = p.rstd[r];
         const bool here = bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
@@ -910,6 +957,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
 template <uint32_t E>
 __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
+    if (blockIdx.x >= p.partials) return weight_columns(p);
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][32];
     __shared__ uint64_t full[kRingStages];
@@ -922,7 +970,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
         if (next >= p.rows) return;
         const uint64_t r = next;
         const uint32_t bar = saddr(full + next_st), dst = saddr(stages) + next_st * stage_bytes;
-        next += gridDim.x;
+        next += p.partials;
         if (++next_st == S) next_st = 0;
         const Words g = words_of(p.dy + r * p.dy_pitch, gb), h = words_of(p.h + r * p.h_pitch, hb);
         Words d{0, 0};
@@ -949,7 +997,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
-    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
+    for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
         const float s = p.rstd[r];
         const bool here = bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
@@ -1086,26 +1134,27 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     else rmsnorm_fwd_kernel<kLong, true><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
 }
 
-// Sets p.partials, the partial rows of the weight's gradient that the launch writes.
+// Sets p.partials, the CTAs that take rows, and as many partial rows of the weight's gradient.
 void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
+    const uint32_t columns = p.dweight ? (uint32_t)std::min<uint64_t>((p.cols + 31) / 32, 4 * sm_count()) : 0;
     const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
     const uint32_t sms = sm_count();
     if (vec && p.cols <= kShortCols) {
         const uint32_t lanes = short_lanes(p.cols);
         const uint64_t each = 256 / lanes;
         p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, most_partials(p.cols));
-        rmsnorm_bwd_short_kernel<<<p.partials, 256, 0, stream>>>(p, lanes);
+        rmsnorm_bwd_short_kernel<<<p.partials + columns, 256, 0, stream>>>(p, lanes);
         return;
     }
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
     const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 2048, {1024, 512, 256}, 1, kRingStages);
-    // by chunks and by the ring: 16 x 4096 (bf16) 6.6 us and 4.7, 16384 x 4096 255 and 92; by elements and by
+    // by chunks and by the ring: 200 x 4096 (bf16) 11.2 us and 7.6, 16384 x 4096 255 and 92; by elements and by
     // the ring: 152 x 1021 (f32) 5.5 and 5.6, 460 x 5001 (f32) 15.3 and 10.8
     if (g.ctas && (vec || p.rows > sms)) {
         p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)most_partials(p.cols)});
         auto kernel = vec ? (g.nch == 1 ? rmsnorm_bwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
-        kernel<<<p.partials, g.threads, g.smem, stream>>>(p, g.stages);
+        kernel<<<p.partials + columns, g.threads, g.smem, stream>>>(p, g.stages);
         return;
     }
     auto walk = [&](uint32_t each) {       // walkers a CTA
@@ -1117,18 +1166,18 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         if (const uint32_t t = element_threads(p.cols, 8, kBwdThreads)) {
             const uint32_t each = t == 32 ? kWarpRows : 1;
             walk(each);
-            rmsnorm_bwd_elements_kernel<8><<<p.partials, dim3(t, each), 0, stream>>>(p);
+            rmsnorm_bwd_elements_kernel<8><<<p.partials + columns, dim3(t, each), 0, stream>>>(p);
             return;
         }
         if (const uint32_t t = element_threads(p.cols, 16, kBwdThreads)) {
-            rmsnorm_bwd_elements_kernel<16><<<p.partials, t, 0, stream>>>(p);
+            rmsnorm_bwd_elements_kernel<16><<<p.partials + columns, t, 0, stream>>>(p);
             return;
         }
-        rmsnorm_bwd_kernel<kLong, false><<<p.partials, kBwdThreads, 0, stream>>>(p);
+        rmsnorm_bwd_kernel<kLong, false><<<p.partials + columns, kBwdThreads, 0, stream>>>(p);
         return;
     }
-    if (p.cols <= 32 * kBwdThreads) rmsnorm_bwd_kernel<4, true><<<p.partials, kBwdThreads, 0, stream>>>(p);
-    else rmsnorm_bwd_kernel<kLong, true><<<p.partials, kBwdThreads, 0, stream>>>(p);
+    if (p.cols <= 32 * kBwdThreads) rmsnorm_bwd_kernel<4, true><<<p.partials + columns, kBwdThreads, 0, stream>>>(p);
+    else rmsnorm_bwd_kernel<kLong, true><<<p.partials + columns, kBwdThreads, 0, stream>>>(p);
 }
 
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
@@ -1296,7 +1345,9 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
     p.rstd = rstd;
     p.dres = static_cast<const char*>(dres);
     p.dx = static_cast<char*>(dx);
-    p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+    const bool few = rows <= kFewRows;
+    p.partial = dweight && !few ? static_cast<float*>(workspace) : nullptr;
+    p.dweight = few ? dweight : nullptr;
     p.dy_pitch = dy_pitch;
     p.h_pitch = h_pitch;
     p.dres_pitch = dres_pitch;
@@ -1311,7 +1362,7 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
                      aligned(dres, dres ? dres_pitch : 0, 16) && aligned(dx, dx_pitch, 16);
     launch_bwd(p, vec, stream);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && dweight)
+    if (e == cudaSuccess && p.partial)
         e = launch(rmsnorm_dweight_kernel, (p.cols + 31) / 32, 1024, 0, 0, true, stream, p.partial, p.partials, p.cols, dweight);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;

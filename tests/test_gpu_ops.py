@@ -264,6 +264,19 @@ def test_short_rows_and_small_rings(rows, cols, over):
         assert torch.equal(dw, again)
 
 
+@pytest.mark.parametrize("rows,cols,over", [
+    (96, 1000, {}), (97, 1000, {}), (96, 4096, dict(residual="f32")), (5, 40000, {}), (63, 5001, dict(x="f32", residual="f32", pad=3)),
+    (95, 30000, dict(pad=1)), (96, 128, {}), (97, 128, {}), (1, 64, {}), (33, 31, dict(pad=1)), (2, 19500, {})])
+def test_weight_gradient_of_few_rows(rows, cols, over):
+    op, a, dres, dx = grad_case(rows, cols, **over)
+    dw, again = torch.full((cols + 9,), 7.0, device="cuda"), torch.zeros(cols, device="cuda")
+    op.backward(**a, dx=dx, dweight=dw[4:4 + cols], dres=dres)
+    op.backward(**a, dx=torch.empty_like(dx), dweight=again, dres=dres)
+    torch.cuda.synchronize()
+    check_backward(a, dres, dx, dw[4:4 + cols], over.get("residual", "bf16"))
+    assert torch.equal(dw[4:4 + cols], again) and (dw[:4] == 7).all() and (dw[4 + cols:] == 7).all()
+
+
 def test_short_rows_keep_nan_to_themselves_and_their_slices():
     """NaN in a row that shares its warp with others; nothing beside the rows is written."""
     rows, cols, pad = 37, 104, 16
