@@ -392,28 +392,44 @@ __device__ __forceinline__ void finish_apply(float a, uint8_t* hi, uint8_t* lo, 
     }
 }
 
-// 32 columns from column c of row r of the result.
-__device__ __forceinline__ void store_result(const Result& o, uint32_t r, uint32_t c, float (&v)[32]) {
-    if (r >= o.S || c >= o.L) return;
+// The thread's 32 columns, from column c of row r, of the result; all lanes of a warp, at neighbouring rows and
+// the same columns.  Rows that are no whole 16-byte words go through the thread's words of the slab, and
+// a row at a time to memory: an element of 32 rows at a time cost 1500 x 3500 65 us of 404.
+__device__ __forceinline__ void store_result(const Result& o, uint32_t r, uint32_t c, uint8_t* slab, uint32_t row, uint32_t half, float (&v)[32]) {
 #pragma unroll
     for (uint32_t k = 0; k < 32; ++k) v[k] *= o.scale;
     if (o.transposed) {
+        if (r >= o.S) return;
 #pragma unroll
         for (uint32_t k = 0; k < 32; ++k)          // neighbouring lanes hold neighbouring columns of `out`
             if (c + k < o.L)
                 *reinterpret_cast<uint16_t*>(o.out + (uint64_t)(c + k) * o.pitch + (uint64_t)r * 2) = (uint16_t)pack_bf16(v[k], 0.0f);
-    } else if (o.vec && c + 32 <= o.L) {
+        return;
+    }
+    uint4 word[4];
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q)
+        word[q] = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                             pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+    if (o.vec && c + 32 <= o.L) {
+        if (r >= o.S) return;
         uint4* to = reinterpret_cast<uint4*>(o.out + (uint64_t)r * o.pitch + (uint64_t)c * 2);
 #pragma unroll
-        for (uint32_t q = 0; q < 4; ++q)
-            to[q] = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                               pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
-    } else {
-#pragma unroll
-        for (uint32_t k = 0; k < 32; ++k)
-            if (c + k < o.L)
-                *reinterpret_cast<uint16_t*>(o.out + (uint64_t)r * o.pitch + (uint64_t)(c + k) * 2) = (uint16_t)pack_bf16(v[k], 0.0f);
+        for (uint32_t q = 0; q < 4; ++q) to[q] = word[q];
+        return;
     }
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) slab_word(slab, row, 4 * half + q) = word[q];
+    __syncwarp();
+    const uint32_t lane = threadIdx.x % 32, r0 = r - lane, row0 = row - lane;
+    if (c + lane < o.L) {
+#pragma unroll 8
+        for (uint32_t k = 0; k < 32; ++k)
+            if (r0 + k < o.S)
+                *reinterpret_cast<uint16_t*>(o.out + (uint64_t)(r0 + k) * o.pitch + (uint64_t)(c + lane) * 2) =
+                    reinterpret_cast<const uint16_t*>(&slab_word(slab, row0 + k, 4 * half + lane / 8))[lane % 8];
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t src) {
@@ -684,7 +700,7 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
                     finish_apply(a, slab, slab + SLAB_BYTES, row, half, v, !result);
                     if (result)
                         store_result({p.out + (uint64_t)t.m * p.out_stride, p.out_pitch, p.S, p.L, p.scale, p.transposed, p.out_vec},
-                                     t.i * 256 + q * 128 + row, t.j * tn + g * SLAB + 32 * half, v);
+                                     t.i * 256 + q * 128 + row, t.j * tn + g * SLAB + 32 * half, slab, row, half, v);
                 } else if (t.product == GRAM) {
                     finish<false>(b, c, slab, row, half, t.i != t.j, v);
                 } else {
@@ -1229,26 +1245,24 @@ __global__ void __launch_bounds__(256, START_CTAS) ortho_update_kernel(const __g
     if (threadIdx.x == 0) p.sums[(uint64_t)m * p.parts + blockIdx.x] = sum;
 }
 
-// The same for any alignment, by single elements.
-__global__ void __launch_bounds__(256) ortho_update_elements_kernel(const __grid_constant__ UpdateParams p) {
+// The same for any alignment, an element a lane: a warp has 256 columns of a row under way.
+__global__ void __launch_bounds__(256, START_CTAS) ortho_update_elements_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
-    const uint32_t m = blockIdx.y;
+    constexpr uint32_t N = 8;
+    const uint32_t m = blockIdx.y, lane = threadIdx.x % 32, pieces = (p.cols + 32 * N - 1) / (32 * N), total = p.rows * pieces;   // 2^24 at most
     const char* x = p.x + (uint64_t)m * p.x_stride;
     char* mom = p.mom ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
-    const uint64_t total = (uint64_t)p.rows * p.cols, step = (uint64_t)p.parts * 256;   // up to 2^32 elements
     float sum = 0.0f;
     launch_next();
     zero_counters(p);
-    constexpr uint32_t N = 8;                          // under way at a time
-    for (uint64_t i0 = blockIdx.x * 256 + threadIdx.x; i0 < total; i0 += N * step) {
+    for (uint32_t i = blockIdx.x * 8 + threadIdx.x / 32; i < total; i += p.parts * 8) {
+        const uint32_t r = i / pieces, c = 32 * N * (i - r * pieces) + lane;
         float u[N], v[N];
         const char *xs[N], *moms[N];
         uint32_t cs[N];
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) {
-            const uint64_t i = min(i0 + n * step, total - 1);
-            const uint32_t r = (uint32_t)(i / p.cols);
-            cs[n] = (uint32_t)(i - (uint64_t)r * p.cols);
+            cs[n] = min(c + 32 * n, p.cols - 1);
             xs[n] = x + r * p.x_pitch;
             moms[n] = mom + r * p.mom_pitch;
         }
@@ -1256,11 +1270,11 @@ __global__ void __launch_bounds__(256) ortho_update_elements_kernel(const __grid
         if (mom) gather(moms, DTT_F32, cs, v);
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) {
-            if (i0 + n * step >= total) break;
+            if (c + 32 * n >= p.cols) break;
             if (mom) {
                 v[n] = p.mu * v[n] + u[n];
                 u[n] = p.nesterov ? u[n] + p.mu * v[n] : v[n];
-                store1(const_cast<char*>(moms[n]), DTT_F32, cs[n], v[n]);
+                store1(mom + r * p.mom_pitch, DTT_F32, cs[n], v[n]);
             }
             sum += u[n] * u[n];
         }
@@ -1718,7 +1732,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
             if (last) {
                 Result out = p.out;
                 out.out += (uint64_t)m * p.out_stride;
-                store_result(out, row, l0 + 64 * n + 32 * half, v);
+                store_result(out, row, l0 + 64 * n + 32 * half, hi + n * BLOCK_BYTES, row, half, v);
             }
         }
     }
@@ -2121,9 +2135,9 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     bool vec = d.cols % 8 == 0;
     for (const auto& a : args)
         if (a.p != out && a.p) vec = vec && reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.pitch % 16 == 0 && a.stride % 16 == 0;
-    const uint64_t items = d.rows * (vec ? d.cols / 8 : d.cols);
+    const uint64_t items = d.rows * (vec ? d.cols / 8 : (d.cols + 255) / 256);
     const bool b16 = d.x_dtype == DTT_BF16;
-    const uint64_t each = 256 * (vec ? b16 && !momentum ? 4 : 2 : 4);
+    const uint64_t each = !vec ? 8 : b16 && !momentum ? 1024 : 512;
     up.parts = (uint32_t)std::min<uint64_t>((items + each - 1) / each, std::max(kMaxParts / d.batch, 1u));
     if (o->resident) {
         ResidentParams r{};
