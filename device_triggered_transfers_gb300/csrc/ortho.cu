@@ -42,8 +42,9 @@ constexpr uint32_t TMA_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1, SLAB_WARP = E
 constexpr uint32_t SLAB = 64;                        // pair form: columns that its epilogue takes at a time
 constexpr uint32_t SLAB_BYTES = 128 * SLAB * 2;      // of one f16 array: 16 KiB
 constexpr uint32_t SLAB_BUFS = 2;
+constexpr uint32_t TILES = 160;                      // of a cluster of the pair form, worked out beforehand
 constexpr uint32_t WAIT_LIMIT = 1u << 22;
-constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + SLAB_BUFS * 2 * SLAB_BYTES + 256;
+constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + SLAB_BUFS * 2 * SLAB_BYTES + 256 + TILES * 8;
 // instruction descriptor (kind::f16): f32 accumulator, f16 operands, M = m, N = n
 __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 constexpr uint32_t IDESC_B_MN = 1u << 16;            // B stored with N contiguous
@@ -241,7 +242,9 @@ struct PairParams {
     uint32_t n, across, tn;      // row blocks of S; tiles of tn columns (256 or 128) across L
     uint32_t first, last;
     uint32_t step, steps;        // the first step of this launch (its parity names the hi that is read), and how many
-    uint32_t* counters;          // [batch][GRAM, POLY, APPLY][n], or null
+    uint32_t* counters;          // [batch][GRAM, POLY, APPLY][n], then [batch][tiles of A] for the parts; or null
+    uint32_t splits;             // of A's k blocks, over as many places; 1 without counters
+    float* parts;                // the f32 sums of all but the last of them: [batch][tiles of A][splits - 1][256 x 256]
     char* out;                   // the result of the launch's last step (see Result); null: another launch follows
     uint64_t out_pitch, out_stride;
     float scale;
@@ -256,28 +259,32 @@ struct PairParams {
 // a product takes 2 + 2 + 4: 990 us for five steps with these, 915 in one sequence.
 struct Tile {
     uint32_t k, product, m, i, j;
+    uint32_t split, place;       // A: which part of its k blocks, and its place in the triangle
 };
 
 __device__ __forceinline__ Tile pair_tile(const PairParams& p, uint32_t u) {
     const uint32_t square = p.n * (p.n + 1) / 2, oblong = p.n * p.across;
     uint32_t per_step = 0;
-    for (uint32_t q = p.first; q <= p.last; ++q) per_step += p.batch * (q == APPLY ? oblong : square);
+    auto places = [&](uint32_t q) { return q == APPLY ? oblong : q == GRAM ? square * p.splits : square; };   // of a matrix
+    for (uint32_t q = p.first; q <= p.last; ++q) per_step += p.batch * places(q);
     Tile t{};
     t.k = u / per_step;
     uint32_t r = u % per_step;
     for (t.product = p.first;; ++t.product) {
-        const uint32_t all = p.batch * (t.product == APPLY ? oblong : square);
+        const uint32_t all = p.batch * places(t.product);
         if (r < all) break;
         r -= all;
     }
-    const uint32_t each = t.product == APPLY ? oblong : square;
+    const uint32_t each = places(t.product);
     t.m = r / each;
     r %= each;
     if (t.product == APPLY) {
         t.i = r / p.across;
         t.j = r % p.across;
     } else if (t.product == GRAM) {
-        triangle(r, t.i, t.j);
+        t.split = r % p.splits;
+        t.place = r / p.splits;
+        triangle(t.place, t.i, t.j);
     } else {
         triangle(square - 1 - r, t.i, t.j);       // the columns of a triangle are the rows of it turned over
         const uint32_t i = p.n - 1 - t.j;
@@ -287,15 +294,26 @@ __device__ __forceinline__ Tile pair_tile(const PairParams& p, uint32_t u) {
     return t;
 }
 
+// A tile in 8 bytes: steps 5 bits, matrices 16, tiles a side 9 each.  (Worked out by each warp at its turn:
+// eight of 1024 x 1024 262 us and not 229.)
+__device__ __forceinline__ uint2 packed(const Tile& t) {
+    return make_uint2(t.k | t.product << 5 | t.split << 7 | t.m << 16, t.i | t.j << 16);
+}
+__device__ __forceinline__ Tile unpacked(uint2 v) {
+    Tile t{v.x & 31, v.x >> 5 & 3, v.x >> 16, v.y & 0xFFFF, v.y >> 16, v.x >> 7 & 7, 0};
+    t.place = t.i * (t.i + 1) / 2 + t.j;
+    return t;
+}
+
 __device__ __forceinline__ uint32_t pair_tiles(const PairParams& p) {
     uint32_t per_step = 0;
-    for (uint32_t q = p.first; q <= p.last; ++q) per_step += p.batch * p.n * (q == APPLY ? 2 * p.across : p.n + 1) / 2;
+    for (uint32_t q = p.first; q <= p.last; ++q)
+        per_step += p.batch * (q == APPLY ? p.n * p.across : p.n * (p.n + 1) / 2 * (q == GRAM ? p.splits : 1));
     return per_step * p.steps;
 }
 
-// Wait (bounded) until `target` CTAs have stored into row block i of product q of matrix m.
-__device__ __forceinline__ bool stored(const PairParams& p, uint32_t m, uint32_t q, uint32_t i, uint32_t target, volatile uint32_t* abort) {
-    const uint32_t* c = p.counters + (m * 3 + q) * p.n + i;
+// Wait (bounded) until a counter has reached `target`.
+__device__ __forceinline__ bool reached(const uint32_t* c, uint32_t target, volatile uint32_t* abort) {
     for (uint32_t polls = 0; polls < WAIT_LIMIT; ++polls) {
         uint32_t v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
@@ -304,6 +322,11 @@ __device__ __forceinline__ bool stored(const PairParams& p, uint32_t m, uint32_t
         __nanosleep(64);
     }
     return false;
+}
+
+// The same for `target` CTAs that have stored into row block i of product q of matrix m.
+__device__ __forceinline__ bool stored(const PairParams& p, uint32_t m, uint32_t q, uint32_t i, uint32_t target, volatile uint32_t* abort) {
+    return reached(p.counters + (m * 3 + q) * p.n + i, target, abort);
 }
 
 // Everything that tile t reads is there, for copies too.  X of step k was complete before b A + c A A of any
@@ -332,6 +355,23 @@ __device__ __forceinline__ void count_stored(const PairParams& p, const Tile& t)
     uint32_t* c = p.counters + (t.m * 3 + t.product) * p.n;
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(c + t.i) : "memory");
     if (t.product != APPLY && t.i != t.j) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(c + t.j) : "memory");
+}
+
+// The k blocks of tile t, `all` of them in its product: first and one past the last.
+__device__ __forceinline__ uint2 k_blocks(const PairParams& p, const Tile& t, uint32_t all) {
+    if (t.product != GRAM) return make_uint2(0, all);
+    const uint32_t each = (all + p.splits - 1) / p.splits;
+    return make_uint2(t.split * each, min((t.split + 1) * each, all));
+}
+
+// Sums of a part of A's k blocks: what warp `warp` of CTA q holds of columns 64 g .., as its lanes hold it.  The
+// tile's last part adds the others in their order.
+__device__ __forceinline__ float4* part_of(const PairParams& p, const Tile& t, uint32_t split, uint32_t q, uint32_t warp, uint32_t g) {
+    const uint64_t tile = (uint64_t)t.m * (p.n * (p.n + 1) / 2) + t.place;
+    return reinterpret_cast<float4*>(p.parts + (tile * (p.splits - 1) + split) * 65536) + ((q * EPI_WARPS + warp) * 4 + g) * 256;
+}
+__device__ __forceinline__ uint32_t* parts_counter(const PairParams& p, const Tile& t) {
+    return p.counters + p.batch * 3 * p.n + t.m * (p.n * (p.n + 1) / 2) + t.place;
 }
 
 // A slab is 128 rows by 64 columns of f16 in shared memory, rows of 128 bytes with their 16-byte words
@@ -506,9 +546,12 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
     uint64_t* drain = slab_out + SLAB_BUFS;       // [1]       leader: MMA teardown
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    uint2* tiles = reinterpret_cast<uint2*>(tmem_slot + 2);   // [TILES] the cluster's first: worked out by a thread each
 
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, q = cluster_rank();
+    const uint32_t c0 = blockIdx.x / 2, NC = gridDim.x / 2;
     const bool leader = q == 0;
+    if (threadIdx.x < TILES) tiles[threadIdx.x] = packed(pair_tile(p, c0 + threadIdx.x * NC));
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < STAGES; ++i) {
             bar_init(saddr(full + i), 1);            // the leader's expect_tx covers both CTAs' bytes
@@ -542,9 +585,7 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
     const uint32_t tmem_base = *tmem_slot;
     launch_next();
     const uint32_t places = pair_tiles(p), k_long = (p.L + BK - 1) / BK, k_short = (p.S + BK - 1) / BK;   // k blocks: GRAM; else
-    const uint32_t c0 = blockIdx.x / 2, NC = gridDim.x / 2;
-    const Tile tile0 = pair_tile(p, c0);          // worked out before the wait
-    auto tile_at = [&](uint32_t u) { return u == c0 ? tile0 : pair_tile(p, u); };
+    auto tile_at = [&](uint32_t u) { return u < c0 + TILES * NC ? unpacked(tiles[(u - c0) / NC]) : pair_tile(p, u); };
     wait_previous();
 
     const uint32_t peer_abort = at_rank(saddr(tmem_slot + 1), q ^ 1);
@@ -565,8 +606,8 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
                 const CUtensorMap* mA = t.product == GRAM ? &p.hi_rows[now] : t.product == POLY ? &p.gram : &p.poly;
                 const CUtensorMap* mB = t.product == APPLY ? &p.hi_cols[now] : mA;
                 const int32_t row = (int32_t)(t.i * 256 + q * 128), col = (int32_t)(t.j * tn + q * (tn / 2)), z = (int32_t)t.m;
-                const uint32_t kblocks = t.product == GRAM ? k_long : k_short;
-                for (uint32_t kb = 0; kb < kblocks; ++kb) {
+                const uint2 ks = k_blocks(p, t, t.product == GRAM ? k_long : k_short);
+                for (uint32_t kb = ks.x; kb < ks.y; ++kb) {
                     if (!bar_wait(saddr(empty + stage), phase ^ 1, abort_flag)) { fail(); ok = false; break; }
                     // The peer's loads may land before the leader's expect_tx (the barrier's
                     // transaction count goes below zero for a while), but never a phase early: its
@@ -599,20 +640,22 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
             bool ok = true;
             for (uint32_t u = c0; u < places && ok; u += NC) {
-                const uint32_t product = tile_at(u).product;
+                const Tile t = tile_at(u);
+                const uint32_t product = t.product;
                 const uint32_t id = product == APPLY ? idesc(256, p.tn) | IDESC_B_MN : idesc(256, 256);
-                const uint32_t step = product == APPLY ? STEP_MN : STEP_K, kblocks = product == GRAM ? k_long : k_short;
+                const uint32_t step = product == APPLY ? STEP_MN : STEP_K;
+                const uint2 ks = k_blocks(p, t, product == GRAM ? k_long : k_short);
                 if (!bar_wait(saddr(acc_empty + acc), acc_phase ^ 1, abort_flag)) { fail(); break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * 256;
-                for (uint32_t kb = 0; kb < kblocks; ++kb) {
+                for (uint32_t kb = ks.x; kb < ks.y; ++kb) {
                     if (!bar_wait(saddr(full + stage), phase, abort_flag)) { fail(); ok = false; break; }
                     tc_fence_after();
                     const uint64_t da = desc_k(saddr(sA + stage * HALF_STAGE));
                     const uint32_t b0 = saddr(sB + stage * HALF_STAGE);
                     const uint64_t db = product == APPLY ? desc_mn(b0) : desc_k(b0);
 #pragma unroll
-                    for (uint32_t k = 0; k < BK / UMMA_K; ++k) umma_pair(d_tmem, da + STEP_K * k, db + step * k, id, (kb | k) != 0);
+                    for (uint32_t k = 0; k < BK / UMMA_K; ++k) umma_pair(d_tmem, da + STEP_K * k, db + step * k, id, kb != ks.x || k != 0);
                     umma_commit_both(saddr(empty + stage));   // both CTAs' stages are free
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
@@ -631,6 +674,7 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
             bool ok = true;
             for (uint32_t u = c0; u < places && ok; u += NC) {
                 const Tile t = tile_at(u);
+                if (t.product == GRAM && t.split + 1 < p.splits) continue;    // its sums leave as they are
                 const bool apply = t.product == APPLY, result = p.out && t.k + 1 == p.steps;
                 const uint32_t count = (apply ? p.tn : 256) / SLAB;
                 const int32_t y = (int32_t)(t.i * 256 + q * 128), m = (int32_t)t.m;
@@ -690,10 +734,44 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
             ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(acc_full + acc), acc_phase, abort_flag));
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((32u * (warp % 4)) << 16) + acc * 256 + 32 * half;
+            const bool parted = t.product == GRAM && p.splits > 1;
+            if (ok && parted) {
+                if (t.split + 1 < p.splits) {
+                    for (uint32_t g = 0; g < tn / SLAB; ++g) {
+                        float v[32];
+                        tmem_ld32(taddr + g * SLAB, v);
+                        float4* to = part_of(p, t, t.split, q, warp, g);
+#pragma unroll
+                        for (uint32_t k = 0; k < 8; ++k) to[k * 32 + lane] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(parts_counter(p, t)) : "memory");
+                        bar_arrive_at(at_rank(saddr(acc_empty + acc), 0));
+                    }
+                    if (++acc == ACC_BUFS) { acc = 0; acc_phase ^= 1; }
+                    continue;
+                }
+                ok = __all_sync(0xFFFFFFFFu, lane != 0 || reached(parts_counter(p, t), (t.k + 1) * (p.splits - 1) * 2 * EPI_WARPS, abort_flag));
+            }
             for (uint32_t g = 0; g < tn / SLAB && ok; ++g, ++s) {
                 uint8_t* slab = slabs + s % SLAB_BUFS * 2 * SLAB_BYTES;
                 float v[32];
                 tmem_ld32(taddr + g * SLAB, v);
+                if (parted) {
+                    for (uint32_t n = 0; n + 1 < p.splits; ++n) {
+                        const float4* from = part_of(p, t, n, q, warp, g);
+#pragma unroll
+                        for (uint32_t k = 0; k < 8; ++k) {
+                            const float4 f = __ldcg(from + k * 32 + lane);
+                            v[4 * k] += f.x;
+                            v[4 * k + 1] += f.y;
+                            v[4 * k + 2] += f.z;
+                            v[4 * k + 3] += f.w;
+                        }
+                    }
+                }
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(slab_in + s % SLAB_BUFS), s / SLAB_BUFS & 1, abort_flag));
                 if (!ok) break;
                 if (t.product == APPLY) {
@@ -1760,8 +1838,28 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, ui
 struct Layout {
     uint64_t S, L, s_pitch, l_pitch;                 // elements
     uint64_t hi[2], lo, gram, poly, sums, counters, bytes;   // byte offsets in the workspace
-    uint64_t n_counters;
+    uint64_t n_counters, parts;
+    uint32_t splits;             // of A, where all products run in one launch
 };
+
+// Time of one of A's tiles as `splits` parts, where all products run in one launch: 0.275 us a k block, and each
+// part's sums through L2, ~1 us apart and 3 us in all besides.
+double gram_us(uint64_t L, uint32_t splits) {
+    const uint64_t kblocks = (L + BK - 1) / BK;
+    return 0.3 + 0.275 * (double)((kblocks + splits - 1) / splits) + (splits > 1 ? 3.0 + splits : 0.0);
+}
+
+// How many parts: few tiles of long rows then occupy more of the 76 pairs.  Measured, by one part and by these: 512 x
+// 8192, four of them 428 us and 335, 2048 x 8192 606 and 544, 700 x 4000, four, 291 and 271; 1024 x 1024
+// would lose by two, 181 and 190.
+uint32_t splits_of(uint64_t S, uint64_t L, uint32_t batch) {
+    const uint64_t n = (S + 255) / 256, tiles = n * (n + 1) / 2 * batch, kblocks = (L + BK - 1) / BK;
+    uint32_t best = 1;
+    for (uint32_t splits = 2; splits <= 4 && tiles * splits <= 76 && kblocks >= 8 * splits; ++splits)
+        if (gram_us(L, splits) < gram_us(L, best)) best = splits;
+    const uint64_t each = (kblocks + best - 1) / best;
+    return (uint32_t)((kblocks + each - 1) / each);
+}
 
 Layout layout_of(const dtt_ortho_desc& d) {
     Layout l{};
@@ -1781,8 +1879,11 @@ Layout layout_of(const dtt_ortho_desc& d) {
     l.gram = take(d.batch * l.S * l.s_pitch * 2);
     l.poly = take(d.batch * l.S * l.s_pitch * 2);
     l.sums = take((uint64_t)d.batch * kMaxParts * 4);
-    l.n_counters = (uint64_t)d.batch * 3 * ((l.S + 255) / 256);
+    const uint64_t n = (l.S + 255) / 256, tiles = d.batch * n * (n + 1) / 2;
+    l.n_counters = d.batch * 3 * n + tiles;
     l.counters = take(l.n_counters * 4);
+    l.splits = l.S > 256 ? splits_of(l.S, l.L, d.batch) : 1;
+    l.parts = take(tiles * (l.splits - 1) * 65536 * 4);
     l.bytes = at;
     return l;
 }
@@ -1905,14 +2006,17 @@ Form form_of(bool square, uint64_t rows, uint64_t cols, uint64_t K, uint32_t bat
     return best;
 }
 
-// The same for a whole step in the one launch of CTA pairs: the tiles' time over all pairs, or one tile of each
-// product after the other, and 6 us a product from the last tile's sums to the next one's first.  Measured,
-// five steps, this against a launch a product: 4096 x 4096 915 us and 990, 3000 x 3000 456 and 576, four of
-// 2048 x 2048 540 and 640; the rule leaves alone two of 1024 x 4096, 281 and 247, and 1500 x 3500, 410 and 400.
-double flow_us(uint64_t S, uint64_t L, uint32_t batch, const Fit& fit) {
+// The same for a whole step in the one launch of CTA pairs: a tile of each product after the other, or all tiles
+// over all pairs, a tile of the last product no less than its epilogue's 3 us, and 5 us a product from the last
+// tile's sums to the next one's first.  Measured, five steps, this against a launch a product: 4096 x 4096
+// 915 us and 990, 3000 x 3000 456 and 576, four of 2048 x 2048 540 and 640, 2048 x 8192 544 and 610; the rule
+// leaves alone 1024 x 4096, 228 and 178, and four of 300 x 8192, 287 and 267.
+double flow_us(uint64_t S, uint64_t L, uint32_t batch, uint32_t splits, const Fit& fit) {
     const double square = (double)tiles_of(true, 256, 256, S, S) * batch, oblong = (double)tiles_of(false, 256, 256, S, L) * batch;
-    const double gram = 0.3 + 0.275 * ceil_div(L, BK), other = 0.3 + 0.275 * ceil_div(S, BK);
-    return 18.0 + std::max(1.15 * (square * (gram + other) + oblong * other) / fit.pairs, gram + 2 * other);
+    const double poly = 0.3 + 0.275 * ceil_div(S, BK), apply = std::max(poly, 3.0);
+    const double all = (square * (gram_us(L, 1) + poly) + oblong * apply) / fit.pairs;
+    const double chain = gram_us(L, splits) + poly + apply * std::max(1.0, oblong / fit.pairs);
+    return 16.0 + std::max(1.1 * all, 1.3 * chain);
 }
 
 // The same for POLY and APPLY in one (S <= 256): 9 us a round of tiles, measured.  Two launches instead: 100 us
@@ -1943,7 +2047,8 @@ cudaError_t launch_split(GemmParams& p, const Form& f, cudaStream_t stream) {
 // Tiles of a step's products first .. last, of all matrices.
 uint32_t pair_tiles_of(const PairParams& p) {
     uint32_t tiles = 0;
-    for (uint32_t q = p.first; q <= p.last; ++q) tiles += p.batch * p.n * (q == APPLY ? 2 * p.across : p.n + 1) / 2;
+    for (uint32_t q = p.first; q <= p.last; ++q)
+        tiles += p.batch * (q == APPLY ? p.n * p.across : p.n * (p.n + 1) / 2 * (q == GRAM ? p.splits : 1));
     return tiles;
 }
 
@@ -2068,7 +2173,7 @@ extern "C" int dtt_ortho_create(const dtt_ortho_desc* d, void* workspace, uint64
     // its second term of b A + c A A is worth some time: without it a flat spectrum's error is 1.6 times bf16's own
     o->fused = l.S <= 256 && fused_us(l.S, l.L, d->batch, o->sms) < 1.3 * (o->form[POLY].us + o->form[APPLY].us);
     o->flow = !o->resident && !o->fused &&
-              flow_us(l.S, l.L, d->batch, o->fit) < o->form[GRAM].us + o->form[POLY].us + o->form[APPLY].us;
+              flow_us(l.S, l.L, d->batch, l.splits, o->fit) < o->form[GRAM].us + o->form[POLY].us + o->form[APPLY].us;
     bool ok = make_map(&o->gram, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->poly, o->ws + l.poly, l.S, l.S, d->batch, l.s_pitch, 128) &&
               make_map(&o->gram_blocks, o->ws + l.gram, l.S, l.S, d->batch, l.s_pitch, 64) &&
@@ -2166,6 +2271,7 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     }
 
     PairParams pp{};
+    pp.splits = 1;
     for (int i = 0; i < 2; ++i) {
         pp.hi_rows[i] = o->hi_rows[i];
         pp.hi_cols[i] = o->hi_cols[i];
@@ -2192,6 +2298,8 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         pp.last = APPLY;
         pp.steps = d.steps;
         pp.counters = up.counters;
+        pp.splits = l.splits;
+        pp.parts = reinterpret_cast<float*>(o->ws + l.parts);
         pp.out = static_cast<char*>(out);
         std::copy(&d.coeffs[0][0], &d.coeffs[0][0] + 3 * d.steps, &pp.coeffs[0][0]);
         DTT_CUDA_TRY(launch_pair(pp, o->fit.pairs, stream));

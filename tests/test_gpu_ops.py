@@ -349,7 +349,8 @@ def orthogonalized(x, steps=5):
 # one cluster a matrix, up to its longest row and one past it; the second product within the third; its limit
 # and one past it; a product by CTA pairs; everything in one launch, with a last row block of 1, 2 or 64 rows
 LARGE = [(2, 128, 4096), (1, 128, 4097), (1, 4096, 100), (5, 129, 1000), (9, 256, 700), (1, 2000, 250), (1, 257, 3000),
-         (3, 1024, 1500), (1, 2048, 2048), (3, 2050, 2049), (1, 2300, 1900), (1, 1600, 5000), (5, 1025, 1100), (40, 257, 600)]
+         (3, 1024, 1500), (4, 700, 4000), (1, 1500, 3500),
+         (1, 8192, 2048), (1, 2048, 2048), (3, 2050, 2049), (1, 2300, 1900), (1, 1600, 5000), (5, 1025, 1100), (40, 257, 600)]
 
 
 @pytest.mark.parametrize("batch,rows,cols", LARGE)
