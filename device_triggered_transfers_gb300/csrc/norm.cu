@@ -9,6 +9,8 @@
 //  - chunks (aligned rows too long for the ring): the same layout, from global memory;
 //  - elements (what is not aligned or no whole number of chunks, and few rows of it): a warp holds 32 E
 //    neighbouring columns, a thread every 32nd of them.
+// Every kernel lets the next launch begin and waits for the one before it before it touches memory, so that a
+// launch's set-up overlaps the end of the kernel before: 2048 x 4096 14.6 us without and 12.5 with it.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -112,6 +114,8 @@ __device__ __forceinline__ float row_max(float v, uint32_t tpr, float* slot) {
 // 2000 x 32768 in bf16: 141 us, 0.55 of the copy rate; loads that wait for one another bound it.
 template <uint32_t NCH, bool VEC>
 __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_constant__ FwdParams p) {
+    launch_next();
+    wait_previous();
     __shared__ float slots[2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
     const uint64_t r = blockIdx.x;
@@ -205,6 +209,7 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
 __device__ __forceinline__ void weight_columns(const BwdParams& p) {
     __shared__ float sums[kBwdThreads / 32][32];
     constexpr uint32_t N = 4;
+    wait_previous();
     const uint32_t t = threadIdx.y * blockDim.x + threadIdx.x, lane = t % 32, warp = t / 32, warps = blockDim.x * blockDim.y / 32;
     for (uint32_t b = blockIdx.x - p.partials; b < (p.cols + 31) / 32; b += gridDim.x - p.partials) {
         const uint32_t c = 32 * b + lane;
@@ -241,9 +246,11 @@ __device__ __forceinline__ void weight_columns(const BwdParams& p) {
 // ---- short rows --------------------------------------------------------------------------------
 // A row by `lanes` neighbouring lanes of a warp (a power of two), a chunk each; a CTA has 256 / lanes rows.  A
 // thread's loads all go out before the first value is used, and many CTAs hide them: with two or four rows a
-// thread under way the forward pass of 300000 x 128 (bf16 to 8 bits) takes 58 and 82 us, with one 57,
-// 0.69 of the copy rate.
+// thread under way the forward pass of 300000 x 128 (bf16 to 8 bits) takes 58 and 82 us, with one 57
+// (55 behind another call), 0.72 of the copy rate.
 __global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_constant__ FwdParams p, uint32_t lanes) {
+    launch_next();
+    wait_previous();
     const uint32_t t = threadIdx.x, l = t & (lanes - 1), c = 8 * l;
     const uint64_t r = (uint64_t)blockIdx.x * (256 / lanes) + t / lanes, row = min(r, p.rows - 1);
     const bool in = c < p.cols, mine = in && r < p.rows;
@@ -289,10 +296,11 @@ __global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_con
 
 // The same split; a CTA walks over rows, each thread at the same columns, whose part of the weight's gradient
 // adds up in its registers; at the end the CTA's rows' sums, in their order, become its partial row.
-// 300000 x 128 in bf16: 64 us, 0.70 of the copy rate.
+// 300000 x 128 in bf16: 62 us, 0.73 of the copy rate.
 __global__ void __launch_bounds__(256, 4) rmsnorm_bwd_short_kernel(const __grid_constant__ BwdParams p, uint32_t lanes) {
     launch_next();
     if (blockIdx.x >= p.partials) return weight_columns(p);
+    wait_previous();
     __shared__ float sums[256 * 8];
     const uint32_t t = threadIdx.x, l = t & (lanes - 1), c = 8 * l, at_a_time = 256 / lanes;
     const bool in = c < p.cols;
@@ -350,6 +358,7 @@ template <uint32_t NCH, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
     if (blockIdx.x >= p.partials) return weight_columns(p);
+    wait_previous();
     __shared__ float slots[2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
     const uint32_t me = blockIdx.x;
@@ -553,6 +562,8 @@ __device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, f
 // A row a CTA, or a warp (blockDim.y of them).  600 x 3001 in bf16: 5.7 us back to back, the loads' latency.
 template <uint32_t E>
 __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const __grid_constant__ FwdParams p) {
+    launch_next();
+    wait_previous();
     __shared__ float slots[2][32];
     const uint64_t r = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (r >= p.rows) return;                        // a whole warp: rows share no barrier
@@ -594,6 +605,7 @@ template <uint32_t E>
 __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
     if (blockIdx.x >= p.partials) return weight_columns(p);
+    wait_previous();
     __shared__ float slots[2][32];
     __shared__ float sums[kWarpRows][32 * E];
     const uint32_t T = blockDim.x;
@@ -661,10 +673,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const char* src, uint32_
 // Rows blockIdx.x, + gridDim.x, ... by one CTA.  Stage i % S holds the row of turn i: x, then the
 // residual.  Thread 0 starts the copies of turn i + S - 1 once turn i's reduction has passed its
 // barrier: every thread is then done with that stage's last row (turn i - 1).  A copy that does not
-// arrive makes the row NaN.  16384 x 4096 (bf16 to 8 bits, groups of 128): 80 us, 0.86 of the copy rate, the issue
+// arrive makes the row NaN.  16384 x 4096 (bf16 to 8 bits, groups of 128): 77 us, 0.90 of the copy rate, the issue
 // slots 73 % full.
 template <uint32_t NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+    launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][2][32];
     __shared__ uint64_t full[kRingStages];
@@ -687,16 +700,24 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
+    wait_previous();
+    if (t == 0)
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     float w[NCH][8];
 #pragma unroll
     for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) w[i][k] = 1.0f;
     if (p.w) {
+        Raw8 ws[NCH];
 #pragma unroll
-        for (uint32_t i = 0; i < NCH; ++i) load8<true>(p.w, p.w_dt, 8 * (i * T + t), p.cols, w[i]);
+        for (uint32_t i = 0; i < NCH; ++i) {
+            const uint32_t c = 8 * (i * T + t);
+            ws[i] = raw8(p.w + (c < p.cols ? c : 0) * (p.w_dt == DTT_BF16 ? 2 : 4), p.w_dt);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) expand8(ws[i], p.w_dt, w[i]);
     }
     __syncthreads();
 
@@ -774,9 +795,10 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
     }
 }
 
-// The backward pass the same way: a stage holds dy, h, then dres.  16384 x 4096 in bf16: 92 us with the weight's
-// gradient, 0.86 of the copy rate; 2048 x 4096 22 us, 0.44: a row's reduction and barrier with two CTAs a SM
-// (registers), and the sum of the partial rows.
+// The backward pass the same way: a stage holds dy, h, then dres.  A row's latency is what the few CTAs of an SM have
+// to hide, so rstd is read a turn ahead and a thread's loads from the stage go out together: 16384 x 8064 in
+// bf16 153 us and not 201.  16384 x 4096 83 us with the weight's gradient, 0.95 of the copy rate; 2048 x 4096
+// 18.6 us, 0.53: seven rows a CTA, then the sum of the partial rows.
 template <uint32_t NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 1) rmsnorm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
@@ -804,8 +826,10 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
+    wait_previous();
+    if (t == 0)
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     float w[NCH][8], acc[NCH][8];
 #pragma unroll
     for (uint32_t i = 0; i < NCH; ++i)
@@ -815,28 +839,50 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
             acc[i][k] = 0.0f;
         }
     if (p.w) {
+        Raw8 ws[NCH];
 #pragma unroll
-        for (uint32_t i = 0; i < NCH; ++i) load8<true>(p.w, p.w_dt, 8 * (i * T + t), p.cols, w[i]);
+        for (uint32_t i = 0; i < NCH; ++i) {
+            const uint32_t c = 8 * (i * T + t);
+            ws[i] = raw8(p.w + (c < p.cols ? c : 0) * (p.w_dt == DTT_BF16 ? 2 : 4), p.w_dt);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) expand8(ws[i], p.w_dt, w[i]);
     }
     __syncthreads();
 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
+    float s_next = p.rstd[blockIdx.x];              // a turn ahead of its use
     for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
-        const float s = p.rstd[r];
+        const float s = s_next;
+        if (r + p.partials < p.rows) s_next = p.rstd[r + p.partials];
         const bool here = bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float g[NCH][8], n[NCH][8], dot = 0.0f;
+        constexpr uint32_t G = NCH > 2 ? 1 : NCH;   // chunks whose loads go out together: what the registers allow
 #pragma unroll
-        for (uint32_t i = 0; i < NCH; ++i) {
-            load8<true>(row, p.dy_dt, 8 * (i * T + t), p.cols, g[i]);
-            load8<true>(row + gb, p.h_dt, 8 * (i * T + t), p.cols, n[i]);
+        for (uint32_t i0 = 0; i0 < NCH; i0 += G) {
+            Raw8 gs[G], hs[G];
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
-                n[i][k] *= s;
-                acc[i][k] += g[i][k] * n[i][k];
-                g[i][k] *= w[i][k];
-                dot += g[i][k] * n[i][k];
+            for (uint32_t i = 0; i < G; ++i) {
+                const uint32_t c = 8 * ((i0 + i) * T + t), from = c < p.cols ? c : 0;
+                gs[i] = raw8(row + from * (p.dy_dt == DTT_BF16 ? 2 : 4), p.dy_dt);
+                hs[i] = raw8(row + gb + from * (p.h_dt == DTT_BF16 ? 2 : 4), p.h_dt);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < G; ++i) {
+                float (&gi)[8] = g[i0 + i], (&ni)[8] = n[i0 + i];
+                const bool in = 8 * ((i0 + i) * T + t) < p.cols;
+                expand8(gs[i], p.dy_dt, gi);
+                expand8(hs[i], p.h_dt, ni);
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) {
+                    gi[k] = in ? gi[k] : 0.0f;
+                    ni[k] = in ? ni[k] * s : 0.0f;
+                    acc[i0 + i][k] += gi[k] * ni[k];
+                    gi[k] *= w[i0 + i][k];
+                    dot += gi[k] * ni[k];
+                }
             }
         }
         if (!here) dot = __int_as_float(0x7FC00000);
@@ -869,7 +915,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
 // The ring for rows at any alignment, an element a thread.  A bulk copy moves whole 16-byte
 // words: from the one that holds the row's first byte to the one that holds its last.  The few bytes
 // beside the row in these two are copied with it and not looked at (an allocation never ends within
-// such a word).  4093 x 5001 (bf16 with an f32 residual): 43 us, 0.83 of the copy rate.
+// such a word).  4093 x 5001 (bf16 with an f32 residual): 41.6 us, 0.87 of the copy rate.
 struct Words {
     uint64_t from;              // address of the first
     uint32_t bytes;             // of all
@@ -889,6 +935,7 @@ __host__ __device__ __forceinline__ uint32_t words_room(uint32_t bytes) { return
 
 template <uint32_t E>
 __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+    launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][2][32];
     __shared__ uint64_t full[kRingStages];
@@ -914,8 +961,10 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
+    wait_previous();
+    if (t == 0)
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     float w[E];
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) w[k] = 1.0f;
@@ -952,7 +1001,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
     }
 }
 
-// 16384 x 4001 in f32: 179 us, 0.86 of the copy rate; 1021 x 5001 in f32 22 us, 0.53: one CTA a SM (60 KiB a
+// 16384 x 4001 in f32: 179 us, 0.86 of the copy rate; 1021 x 5001 in f32 19 us, 0.63: one CTA a SM (60 KiB a
 // stage), seven rows each.
 template <uint32_t E>
 __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
@@ -984,8 +1033,10 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
         for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (uint32_t i = 0; i + 1 < S; ++i) start();
     }
+    wait_previous();
+    if (t == 0)
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
     float w[E], acc[E];
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) {
@@ -1093,19 +1144,18 @@ uint32_t element_threads(uint32_t cols, uint32_t E, uint32_t threads) {
     return t <= threads ? t : 0;
 }
 
-void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
+cudaError_t launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t xe = p.x_dt == DTT_BF16 ? 2 : 4, re = p.res ? (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t sms = sm_count();
     const uint64_t xb = (uint64_t)p.cols * xe, rb = (uint64_t)p.cols * re;
-    // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
-    // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
-    // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
     if (vec && p.cols <= kShortCols) {
         const uint32_t lanes = short_lanes(p.cols);
         const uint64_t each = 256 / lanes;
-        rmsnorm_fwd_short_kernel<<<(uint32_t)((p.rows + each - 1) / each), 256, 0, stream>>>(p, lanes);
-        return;
+        return launch(rmsnorm_fwd_short_kernel, (uint32_t)((p.rows + each - 1) / each), 256, 0, 0, true, stream, p, lanes);
     }
+    // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
+    // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
+    // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
     const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : kRingStages);
     // The chunk form's loads wait for one another, the ring's do not: 152 x 8064 (bf16) 6.7 us by chunks, 3.7 by
     // the ring.  The element form's go out together, and it is the faster one while there are few rows:
@@ -1114,28 +1164,23 @@ void launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
         auto kernel = vec ? (g.nch == 1 ? rmsnorm_fwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_fwd_ring_elements_kernel<8> : rmsnorm_fwd_ring_elements_kernel<16>);
-        kernel<<<grid, g.threads, g.smem, stream>>>(p, g.stages);
-        return;
+        return launch(kernel, grid, g.threads, g.smem, 0, true, stream, p, g.stages);
     }
     if (!vec) {
         if (const uint32_t t = element_threads(p.cols, 8, kFwdThreads)) {
             const uint32_t each = t == 32 ? kWarpRows : 1;
-            rmsnorm_fwd_elements_kernel<8><<<(uint32_t)((p.rows + each - 1) / each), dim3(t, each), 0, stream>>>(p);
-            return;
+            return launch(rmsnorm_fwd_elements_kernel<8>, (uint32_t)((p.rows + each - 1) / each), dim3(t, each), 0, 0, true, stream, p);
         }
-        if (const uint32_t t = element_threads(p.cols, 16, kFwdThreads)) {
-            rmsnorm_fwd_elements_kernel<16><<<(uint32_t)p.rows, t, 0, stream>>>(p);
-            return;
-        }
-        rmsnorm_fwd_kernel<kLong, false><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
-        return;
+        if (const uint32_t t = element_threads(p.cols, 16, kFwdThreads))
+            return launch(rmsnorm_fwd_elements_kernel<16>, (uint32_t)p.rows, t, 0, 0, true, stream, p);
+        return launch(rmsnorm_fwd_kernel<kLong, false>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
     }
-    if (p.cols <= 32 * kFwdThreads) rmsnorm_fwd_kernel<4, true><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
-    else rmsnorm_fwd_kernel<kLong, true><<<(uint32_t)p.rows, kFwdThreads, 0, stream>>>(p);
+    if (p.cols <= 32 * kFwdThreads) return launch(rmsnorm_fwd_kernel<4, true>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
+    return launch(rmsnorm_fwd_kernel<kLong, true>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
 }
 
 // Sets p.partials, the CTAs that take rows, and as many partial rows of the weight's gradient.
-void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
+cudaError_t launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t columns = p.dweight ? (uint32_t)std::min<uint64_t>((p.cols + 31) / 32, 4 * sm_count()) : 0;
     const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
     const uint32_t sms = sm_count();
@@ -1143,8 +1188,7 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         const uint32_t lanes = short_lanes(p.cols);
         const uint64_t each = 256 / lanes;
         p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, most_partials(p.cols));
-        rmsnorm_bwd_short_kernel<<<p.partials + columns, 256, 0, stream>>>(p, lanes);
-        return;
+        return launch(rmsnorm_bwd_short_kernel, p.partials + columns, 256, 0, 0, true, stream, p, lanes);
     }
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
     const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 2048, {1024, 512, 256}, 1, kRingStages);
@@ -1154,8 +1198,7 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)most_partials(p.cols)});
         auto kernel = vec ? (g.nch == 1 ? rmsnorm_bwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
                           : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
-        kernel<<<p.partials + columns, g.threads, g.smem, stream>>>(p, g.stages);
-        return;
+        return launch(kernel, p.partials + columns, g.threads, g.smem, 0, true, stream, p, g.stages);
     }
     auto walk = [&](uint32_t each) {       // walkers a CTA
         p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, most_partials(p.cols));
@@ -1166,18 +1209,14 @@ void launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         if (const uint32_t t = element_threads(p.cols, 8, kBwdThreads)) {
             const uint32_t each = t == 32 ? kWarpRows : 1;
             walk(each);
-            rmsnorm_bwd_elements_kernel<8><<<p.partials + columns, dim3(t, each), 0, stream>>>(p);
-            return;
+            return launch(rmsnorm_bwd_elements_kernel<8>, p.partials + columns, dim3(t, each), 0, 0, true, stream, p);
         }
-        if (const uint32_t t = element_threads(p.cols, 16, kBwdThreads)) {
-            rmsnorm_bwd_elements_kernel<16><<<p.partials + columns, t, 0, stream>>>(p);
-            return;
-        }
-        rmsnorm_bwd_kernel<kLong, false><<<p.partials + columns, kBwdThreads, 0, stream>>>(p);
-        return;
+        if (const uint32_t t = element_threads(p.cols, 16, kBwdThreads))
+            return launch(rmsnorm_bwd_elements_kernel<16>, p.partials + columns, t, 0, 0, true, stream, p);
+        return launch(rmsnorm_bwd_kernel<kLong, false>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
     }
-    if (p.cols <= 32 * kBwdThreads) rmsnorm_bwd_kernel<4, true><<<p.partials + columns, kBwdThreads, 0, stream>>>(p);
-    else rmsnorm_bwd_kernel<kLong, true><<<p.partials + columns, kBwdThreads, 0, stream>>>(p);
+    if (p.cols <= 32 * kBwdThreads) return launch(rmsnorm_bwd_kernel<4, true>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
+    return launch(rmsnorm_bwd_kernel<kLong, true>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
 }
 
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
@@ -1304,8 +1343,7 @@ extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, con
     const bool vec = d->cols % 8 == 0 && aligned(x, x_pitch, 16) && aligned(residual, residual ? residual_pitch : 0, 16) &&
                      aligned(weight, 0, 16) && aligned(residual_out, residual_out ? residual_out_pitch : 0, 16) &&
                      aligned(y, y_pitch, e4m3 ? 8 : 16);
-    launch_fwd(p, vec, stream);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_fwd(p, vec, stream);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }
@@ -1360,8 +1398,7 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
     p.inv_cols = 1.0f / (float)d->cols;
     const bool vec = d->cols % 8 == 0 && aligned(dy, dy_pitch, 16) && aligned(h, h_pitch, 16) && aligned(weight, 0, 16) &&
                      aligned(dres, dres ? dres_pitch : 0, 16) && aligned(dx, dx_pitch, 16);
-    launch_bwd(p, vec, stream);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_bwd(p, vec, stream);
     if (e == cudaSuccess && p.partial)
         e = launch(rmsnorm_dweight_kernel, (p.cols + 31) / 32, 1024, 0, 0, true, stream, p.partial, p.partials, p.cols, dweight);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));

@@ -161,11 +161,11 @@ __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.w
 // wait_previous), unless `overlap` says otherwise.  cluster: CTAs of a cluster, 0 where the kernel itself
 // says.
 template <class... Params, class... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, bool overlap, cudaStream_t stream,
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, dim3 threads, uint32_t smem, uint32_t cluster, bool overlap, cudaStream_t stream,
                    const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2]{};
