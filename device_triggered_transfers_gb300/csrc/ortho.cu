@@ -55,7 +55,7 @@ static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= STAGES * 2 * HALF_STAGE && 128
               "the tile fits the stages, the sums of the cluster the slabs");
 
 constexpr uint32_t kStartTile = 64;                  // ortho_start_tiles_kernel: elements a side
-constexpr uint32_t START_CTAS = 4;                   // of the update and start kernels on a SM
+constexpr uint32_t START_CTAS = 8;                   // of the update and start kernels on a SM
 constexpr uint32_t kMaxParts = 152 * START_CTAS;     // CTAs of the update's launch at most: all run at once
 
 enum Product { GRAM, POLY, APPLY };
@@ -1247,39 +1247,21 @@ __device__ __forceinline__ float cta_sum(float v, float (&slot)[8]) {
     return v;
 }
 
-// The N chunks of 8 columns that a thread has under way, from chunk i of a matrix in steps of `step`: rows r,
-// columns c .., of the momentum (MOM) and of x (bf16 where B16, else f32), where it is wanted.  No load here
-// is behind a condition of its own, so that all go out together: the whole call on two bf16 updates of
-// 1024 x 4096 with momentum takes 255 us so, 262 with one after the other.
-template <bool B16, bool MOM, uint32_t N>
-__device__ __forceinline__ void chunks(const UpdateParams& p, const char* x, const char* mom, bool want_x, uint32_t i, uint32_t step,
-                                       uint32_t total, uint32_t (&r)[N], uint32_t (&c)[N], float (&u)[N][8], float (&v)[N][8]) {
-    const uint32_t per_row = p.cols / 8;
-#pragma unroll
-    for (uint32_t n = 0; n < N; ++n) {
-        const uint32_t j = min(i + n * step, total - 1);
-        r[n] = j / per_row;
-        c[n] = 8 * (j - r[n] * per_row);
-    }
-    Raw8 xs[N], moms[N];
-    if (want_x) {
-#pragma unroll
-        for (uint32_t n = 0; n < N; ++n)
-            xs[n] = raw8(x + r[n] * p.x_pitch + (uint64_t)c[n] * (B16 ? 2 : 4), B16 ? DTT_BF16 : DTT_F32);
-    }
-    if (MOM) {
-#pragma unroll
-        for (uint32_t n = 0; n < N; ++n) moms[n] = raw8(mom + r[n] * p.mom_pitch + (uint64_t)c[n] * 4, DTT_F32);
-    }
-#pragma unroll
-    for (uint32_t n = 0; n < N; ++n) {
-        if (want_x) expand8(xs[n], B16 ? DTT_BF16 : DTT_F32, u[n]);
-        if (MOM) expand8(moms[n], DTT_F32, v[n]);
-    }
-}
-// Bytes under way are what counts: a thread has 64 to 128 of them.
+// Chunk i of 8 columns of a matrix: row r, columns c .., of the momentum (MOM) and of x (bf16 where B16, else f32),
+// where it is wanted.  One of a thread's at a time, and many CTAs: 4096 x 4096 in bf16, one step, takes 204 us so,
+// 209 with four under way in half as many CTAs.
 template <bool B16, bool MOM>
-constexpr uint32_t kChunks = B16 && !MOM ? 4 : 2;
+__device__ __forceinline__ void chunk(const UpdateParams& p, const char* x, const char* mom, bool want_x, uint32_t i, uint32_t& r,
+                                      uint32_t& c, float (&u)[8], float (&v)[8]) {
+    const uint32_t per_row = p.cols / 8;
+    r = i / per_row;
+    c = 8 * (i - r * per_row);
+    Raw8 xs{}, moms{};
+    if (want_x) xs = raw8(x + r * p.x_pitch + (uint64_t)c * (B16 ? 2 : 4), B16 ? DTT_BF16 : DTT_F32);
+    if (MOM) moms = raw8(mom + r * p.mom_pitch + (uint64_t)c * 4, DTT_F32);
+    expand8(xs, B16 ? DTT_BF16 : DTT_F32, u);
+    if (MOM) expand8(moms, DTT_F32, v);
+}
 
 __device__ __forceinline__ void zero_counters(const UpdateParams& p) {
     if (p.counters && blockIdx.x == 0 && blockIdx.y == 0)
@@ -1291,40 +1273,35 @@ __device__ __forceinline__ void zero_counters(const UpdateParams& p) {
 template <bool B16, bool MOM>
 __global__ void __launch_bounds__(256, START_CTAS) ortho_update_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
-    constexpr uint32_t N = kChunks<B16, MOM>;
     const uint32_t m = blockIdx.y, total = p.rows * (p.cols / 8), step = p.parts * 256;
     const char* x = p.x + (uint64_t)m * p.x_stride;
     char* mom = MOM ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
     float sum = 0.0f;
     launch_next();
     zero_counters(p);
-    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += N * step) {
-        float u[N][8], v[N][8];
-        uint32_t r[N], c[N];
-        chunks<B16, MOM, N>(p, x, mom, true, i, step, total, r, c, u, v);
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
+        float u[8], v[8];
+        uint32_t r, c;
+        chunk<B16, MOM>(p, x, mom, true, i, r, c, u, v);
+        if (MOM) {
 #pragma unroll
-        for (uint32_t n = 0; n < N; ++n) {
-            if (i + n * step >= total) break;
-            if (MOM) {
-#pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) {
-                    v[n][k] = p.mu * v[n][k] + u[n][k];
-                    u[n][k] = p.nesterov ? u[n][k] + p.mu * v[n][k] : v[n][k];
-                }
-                float4* to = reinterpret_cast<float4*>(mom + r[n] * p.mom_pitch + (uint64_t)c[n] * 4);
-                to[0] = make_float4(v[n][0], v[n][1], v[n][2], v[n][3]);
-                to[1] = make_float4(v[n][4], v[n][5], v[n][6], v[n][7]);
+            for (uint32_t k = 0; k < 8; ++k) {
+                v[k] = p.mu * v[k] + u[k];
+                u[k] = p.nesterov ? u[k] + p.mu * v[k] : v[k];
             }
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) sum += u[n][k] * u[n][k];
+            float4* to = reinterpret_cast<float4*>(mom + r * p.mom_pitch + (uint64_t)c * 4);
+            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) sum += u[k] * u[k];
     }
     sum = cta_sum(sum, slot);
     if (threadIdx.x == 0) p.sums[(uint64_t)m * p.parts + blockIdx.x] = sum;
 }
 
 // The same for any alignment, an element a lane: a warp has 256 columns of a row under way.
-__global__ void __launch_bounds__(256, START_CTAS) ortho_update_elements_kernel(const __grid_constant__ UpdateParams p) {
+__global__ void __launch_bounds__(256, START_CTAS / 2) ortho_update_elements_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
     constexpr uint32_t N = 8;
     const uint32_t m = blockIdx.y, lane = threadIdx.x % 32, pieces = (p.cols + 32 * N - 1) / (32 * N), total = p.rows * pieces;   // 2^24 at most
@@ -1378,33 +1355,28 @@ __device__ __forceinline__ float inverse_norm(const UpdateParams& p, uint32_t m,
 template <bool B16, bool MOM>
 __global__ void __launch_bounds__(256, START_CTAS) ortho_start_kernel(const __grid_constant__ UpdateParams p) {
     __shared__ float slot[8];
-    constexpr uint32_t N = 2;
     const uint32_t m = blockIdx.y, total = p.rows * (p.cols / 8), step = gridDim.x * 256;
     const char* x = p.x + (uint64_t)m * p.x_stride;
     const char* mom = MOM ? p.mom + (uint64_t)m * p.mom_stride : nullptr;
     __half* hi = p.hi + (uint64_t)m * p.S * p.l_pitch;
     __half* lo = p.lo + (uint64_t)m * p.S * p.l_pitch;
     const float inv = inverse_norm(p, m, slot);
-    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += N * step) {
-        float u[N][8], v[N][8];
-        uint32_t r[N], c[N];
-        chunks<B16, MOM, N>(p, x, mom, !MOM || p.nesterov, i, step, total, r, c, u, v);
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
+        float u[8], v[8];
+        uint32_t r, c;
+        chunk<B16, MOM>(p, x, mom, !MOM || p.nesterov, i, r, c, u, v);
 #pragma unroll
-        for (uint32_t n = 0; n < N; ++n) {
-            if (i + n * step >= total) break;
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
-                if (MOM) u[n][k] = p.nesterov ? u[n][k] + p.mu * v[n][k] : v[n][k];
-                u[n][k] *= inv;
-            }
-            uint4 a, b;
-            part(u[n][0], u[n][1], a.x, b.x);
-            part(u[n][2], u[n][3], a.y, b.y);
-            part(u[n][4], u[n][5], a.z, b.z);
-            part(u[n][6], u[n][7], a.w, b.w);
-            *reinterpret_cast<uint4*>(hi + r[n] * p.l_pitch + c[n]) = a;
-            *reinterpret_cast<uint4*>(lo + r[n] * p.l_pitch + c[n]) = b;
+        for (uint32_t k = 0; k < 8; ++k) {
+            if (MOM) u[k] = p.nesterov ? u[k] + p.mu * v[k] : v[k];
+            u[k] *= inv;
         }
+        uint4 a, b;
+        part(u[0], u[1], a.x, b.x);
+        part(u[2], u[3], a.y, b.y);
+        part(u[4], u[5], a.z, b.z);
+        part(u[6], u[7], a.w, b.w);
+        *reinterpret_cast<uint4*>(hi + r * p.l_pitch + c) = a;
+        *reinterpret_cast<uint4*>(lo + r * p.l_pitch + c) = b;
     }
 }
 
@@ -2244,8 +2216,8 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         if (a.p != out && a.p) vec = vec && reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.pitch % 16 == 0 && a.stride % 16 == 0;
     const uint64_t items = d.rows * (vec ? d.cols / 8 : (d.cols + 255) / 256);
     const bool b16 = d.x_dtype == DTT_BF16;
-    const uint64_t each = !vec ? 8 : b16 && !momentum ? 1024 : 512;
-    up.parts = (uint32_t)std::min<uint64_t>((items + each - 1) / each, std::max(kMaxParts / d.batch, 1u));
+    const uint64_t each = vec ? 256 : 8;
+    up.parts = (uint32_t)std::min<uint64_t>((items + each - 1) / each, std::max((vec ? kMaxParts : kMaxParts / 2) / d.batch, 1u));
     if (o->resident) {
         ResidentParams r{};
         r.u = up;
@@ -2265,7 +2237,7 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
     // not overlapped with what ran before (512 x 512: 105 us, overlapped 108)
     DTT_CUDA_TRY(launch(vec ? update_kernel(b16, momentum) : ortho_update_elements_kernel, parts, 256, 0, 0, false, stream, up));
     if (vec && !tall) {
-        const uint32_t ctas = (uint32_t)std::min<uint64_t>((items + 511) / 512, std::max(START_CTAS * o->sms / d.batch, 1u));
+        const uint32_t ctas = (uint32_t)std::min<uint64_t>((items + 255) / 256, std::max(START_CTAS * o->sms / d.batch, 1u));
         DTT_CUDA_TRY(launch(start_kernel(b16, momentum), dim3(ctas, d.batch), 256, 0, 0, true, stream, up));
     } else {
         const dim3 tiles(ceil_div(up.cols, kStartTile), ceil_div(up.rows, kStartTile), d.batch);
