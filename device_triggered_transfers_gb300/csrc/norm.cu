@@ -71,13 +71,27 @@ struct BwdParams {
     float inv_cols;
 };
 
-// The scale of a group whose largest magnitude is m, and what its values are multiplied by: the reciprocal
-// to one ulp (a full division an 8-column chunk was a quarter of the instructions).
+// The scale of a group whose largest magnitude is m.
 __device__ __forceinline__ float scale_of(float m) { return max_nan(m * (1.0f / kE4m3Max), kScaleMin); }
-__device__ __forceinline__ float inverse_of(float scale) {
+
+// Division by a group's scale: the reciprocal once a group, and a quotient y * inv whose remainder, exact in
+// a fused multiply-add, corrects it to the f32 quotient rounded to nearest (P. Markstein, IBM J. Res. Dev. 34
+// (1), 1990).  y * inv alone turns values midway between two codes to the wrong one.  An infinite scale: d
+// and inv are 0, which gives 0 for finite values and NaN for infinities.
+struct Divisor {
+    float d, inv;
+};
+__device__ __forceinline__ Divisor divisor_of(float scale) {
+    Divisor v;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
-    return r;
+    v.d = isinf(scale) ? 0.0f : scale;
+    v.inv = fmaf(r, fmaf(-v.d, r, 1.0f), r);
+    return v;
+}
+__device__ __forceinline__ float quotient(float y, const Divisor& v) {
+    const float q = y * v.inv;
+    return fmaf(fmaf(-v.d, q, y), v.inv, q);
 }
 
 // Over the TPR threads of a row, the same bits in each.  One warp: butterfly shuffles.  More: the warps'
@@ -164,7 +178,7 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
         for (uint32_t k = 0; k < 8; ++k) m = max_nan(m, fabsf(o[k]));
         return m;
     };
-    float inv = 1.0f;
+    Divisor by{};
     const bool e4m3 = p.y_dt == DTT_E4M3, row_scale = e4m3 && p.group_lanes == 0;
     if (row_scale) {
         float m = 0.0f;
@@ -178,7 +192,7 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
         }
         const float scale = scale_of(row_max(m, tpr, slots[1]));
         if (t == 0) p.scales[r] = scale;
-        inv = inverse_of(scale);
+        by = divisor_of(scale);
     }
 #pragma unroll HELD
     for (uint32_t i = 0; i < nch; ++i) {
@@ -191,13 +205,13 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
             float m = amax8(o);
             for (uint32_t d = p.group_lanes >> 1; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
             const float scale = scale_of(m);
-            inv = inverse_of(scale);
+            by = divisor_of(scale);
             if (t % p.group_lanes == 0 && c < p.cols)
                 p.scales[r * p.groups + c / (8 * p.group_lanes)] = scale;
         }
         if (e4m3) {
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) o[k] *= inv;
+            for (uint32_t k = 0; k < 8; ++k) o[k] = quotient(o[k], by);
         }
         if (res_out) store8<VEC>(res_out, p.res_dt, c, p.cols, v);
         store8<VEC>(y, p.y_dt, c, p.cols, o);
@@ -284,10 +298,11 @@ __global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_con
         const uint32_t share = p.group_lanes == 0 || p.group_lanes > lanes ? lanes : p.group_lanes;   // of a scale
         if (!in) m = 0.0f;
         for (uint32_t d = share / 2; d > 0; d /= 2) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        const float scale = scale_of(m), inv = inverse_of(scale);
+        const float scale = scale_of(m);
+        const Divisor by = divisor_of(scale);
         if (mine && (l & (share - 1)) == 0) p.scales[p.group_lanes ? r * p.groups + l / share : r] = scale;
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) o[k] *= inv;
+        for (uint32_t k = 0; k < 8; ++k) o[k] = quotient(o[k], by);
     }
     if (!mine) return;
     if (p.res_out) store8<true>(p.res_out + r * p.res_out_pitch, p.res_dt, c, p.cols, h);
@@ -530,9 +545,9 @@ __device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, f
         for (uint32_t k = 0; k < E; ++k) m = max_nan(m, fabsf(v[k]));
         const float scale = scale_of(row_max(m, blockDim.x, slot));
         if (threadIdx.x == 0) p.scales[r] = scale;
-        const float inv = inverse_of(scale);
+        const Divisor by = divisor_of(scale);
 #pragma unroll
-        for (uint32_t k = 0; k < E; ++k) v[k] *= inv;
+        for (uint32_t k = 0; k < E; ++k) v[k] = quotient(v[k], by);
         return;
     }
     const uint32_t per = p.group_lanes / 4;                   // of a thread's columns: 1, 2 or 4
@@ -546,15 +561,15 @@ __device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, f
             m[2] = m[3] = max_nan(m[2], m[3]);
         }
         if (per == 4) m[0] = m[1] = m[2] = m[3] = max_nan(m[0], m[2]);
-        float scale = 0.0f, inv = 0.0f;
+        Divisor by{};
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
             if (i % per == 0) {
-                scale = scale_of(warp_max(m[i]));
-                inv = inverse_of(scale);
+                const float scale = scale_of(warp_max(m[i]));
+                by = divisor_of(scale);
                 if (threadIdx.x % 32 == 0 && c + 32 * (k + i) < p.cols) p.scales[r * p.groups + (c + 32 * (k + i)) / (32 * per)] = scale;
             }
-            v[k + i] *= inv;
+            v[k + i] = quotient(v[k + i], by);
         }
     }
 }
@@ -673,7 +688,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const char* src, uint32_
 // Rows blockIdx.x, + gridDim.x, ... by one CTA.  Stage i % S holds the row of turn i: x, then the
 // residual.  Thread 0 starts the copies of turn i + S - 1 once turn i's reduction has passed its
 // barrier: every thread is then done with that stage's last row (turn i - 1).  A copy that does not
-// arrive makes the row NaN.  16384 x 4096 (bf16 to 8 bits, groups of 128): 77 us, 0.90 of the copy rate, the issue
+// arrive makes the row NaN.  16384 x 4096 (bf16 to 8 bits, groups of 128): 79 us, 0.88 of the copy rate, the issue
 // slots 73 % full.
 template <uint32_t NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
@@ -771,21 +786,22 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
                 for (uint32_t i = 1; i < NCH; ++i) all = max_nan(all, m[i]);
                 const float scale = scale_of(row_max(all, T, slots[turn][1]));
                 if (t == 0) p.scales[r] = scale;
-                const float inv = inverse_of(scale);
+                const Divisor by = divisor_of(scale);
 #pragma unroll
                 for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; ++k) h[i][k] *= inv;
+                    for (uint32_t k = 0; k < 8; ++k) h[i][k] = quotient(h[i][k], by);
             } else {
 #pragma unroll
                 for (uint32_t i = 0; i < NCH; ++i) {
                     for (uint32_t d = p.group_lanes >> 1; d > 0; d >>= 1)
                         m[i] = max_nan(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], d));
-                    const float scale = scale_of(m[i]), inv = inverse_of(scale);
+                    const float scale = scale_of(m[i]);
+                    const Divisor by = divisor_of(scale);
                     const uint32_t c = 8 * (i * T + t);
                     if (t % p.group_lanes == 0 && c < p.cols) p.scales[r * p.groups + c / (8 * p.group_lanes)] = scale;
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; ++k) h[i][k] *= inv;
+                    for (uint32_t k = 0; k < 8; ++k) h[i][k] = quotient(h[i][k], by);
                 }
             }
         }

@@ -35,7 +35,8 @@ enum { DTT_E4M3 = 3 };
  *     y_c = h_c s weight_c               (weight NULL: 1)
  * residual_out = h, rounded once to its type; rstd = s.  With y_dtype DTT_E4M3 the row is cut into
  * groups of `group` columns (0: the whole row; the last group holds what is left) and
- *     scale = max(max_c |y_c| / 448, 2^-100),  y stored = e4m3(y_c / scale), nearest even,
+ *     scale = max(max_c |y_c| / 448, 2^-100) (to an ulp),
+ *     y stored = e4m3(y_c / scale), the f32 quotient to the nearest code, ties to even,
  * so y_c ~ stored * scale, and a group of zeros gives zeros.  NaN anywhere in a row makes the
  * row's rstd, scales and outputs NaN; a row whose sum of squares overflows f32 has rstd 0. */
 typedef struct dtt_rmsnorm_desc {

@@ -1,0 +1,69 @@
+"""GPU: where the operators can go wrong though ordinary values do not show it."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from conftest import ensure_built
+    ensure_built()
+    import device_triggered_transfers_gb300 as D
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "e4m3": torch.float8_e4m3fn}
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def slab(rows, cols, pad, make, kind="f32"):
+    """rows x cols of a buffer `pad` columns wider, filled by make(rows, cols + pad)."""
+    return make(rows, cols + pad).to(TYPES[kind])[:, :cols]
+
+
+# a case of each form of the forward pass: short rows, the ring's three, chunks, rows read again, and the same of
+# single elements (few and many rows)
+FORWARD = [(40, 128, 32, 0), (40, 256, 0, 0), (1300, 1024, 64, 0), (40, 4096, 128, 0), (40, 8192, 0, 0), (3, 16384, 0, 0), (3, 32768, 128, 0),
+           (2, 65536, 128, 0), (40, 128, 32, 1), (40, 4096, 0, 1), (3, 16384, 64, 1), (2, 32768, 0, 1), (1300, 1024, 128, 1), (1300, 4096, 0, 1)]
+
+
+@pytest.mark.parametrize("rows,cols,group,pad", FORWARD)
+def test_codes_are_the_quotients_nearest_even(rows, cols, group, pad):
+    """y is the weight (the rows are +-1), most of it midway between two codes times a scale of few bits: the
+    f32 quotient is exactly midway and the code the even one."""
+    g = gen(rows + cols)
+    x = slab(rows, cols, pad, lambda *s: torch.where(torch.rand(*s, generator=g, device="cuda") < 0.5, -1.0, 1.0))
+    width = group or cols
+    mid = (2.0 * torch.randint(8, 16, (cols,), generator=g, device="cuda") + 1) / 16 * 2.0 ** torch.randint(-6, 9, (cols,), generator=g, device="cuda")
+    mid = torch.where(mid > 448, 17.0, mid)
+    mid[::width] = 448.0
+    t = 1 + torch.randint(0, 1300, (cols // width,), generator=g, device="cuda") / 4096.0
+    weight = mid * t.repeat_interleave(width)
+    kinds = dict(x="f32", residual="f32", weight="f32", eps=0.0)
+    op = D.RMSNorm(cols, y="e4m3", group=group, **kinds)
+    codes = slab(rows, cols, pad, lambda *s: torch.zeros(*s, device="cuda"), "e4m3")
+    y = slab(rows, cols, pad, lambda *s: torch.zeros(*s, device="cuda"))
+    scales = torch.zeros(rows, op.scale_cols, device="cuda")
+    op.forward(x, weight, codes, scales=scales)
+    D.RMSNorm(cols, y="f32", **kinds).forward(x, weight, y)
+    quotient = y / scales.repeat_interleave(width, 1)
+    want = quotient.to(TYPES["e4m3"])
+    # 4 significant bits of e4m3, so a value midway has its fifth bit set and none after it
+    assert ((quotient.view(torch.int32) & 0xFFFFF) == 0x80000).float().mean() > 0.2
+    assert torch.equal(codes.contiguous().view(torch.uint8), want.view(torch.uint8))
+
+
+def test_codes_of_many_values_are_the_quotients():
+    for rows, cols, group, pad in ((16384, 4096, 128, 0), (100000, 128, 32, 0), (4000, 1001, 64, 1), (64, 40000, 0, 0)):
+        g = gen(cols)
+        x = slab(rows, cols, pad, lambda *s: torch.randn(*s, generator=g, device="cuda"))
+        weight = 1 + 0.2 * torch.randn(cols, generator=g, device="cuda")
+        op = D.RMSNorm(cols, x="f32", residual="f32", weight="f32", y="e4m3", group=group)
+        codes = torch.zeros(rows, cols + pad, device="cuda").to(TYPES["e4m3"])[:, :cols]
+        y = torch.zeros(rows, cols + pad, device="cuda")[:, :cols]
+        scales = torch.zeros(rows, op.scale_cols, device="cuda")
+        op.forward(x, weight, codes, scales=scales)
+        D.RMSNorm(cols, x="f32", residual="f32", weight="f32", y="f32").forward(x, weight, y)
+        want = (y / scales.repeat_interleave(group or cols, 1)[:, :cols]).to(TYPES["e4m3"])
+        assert torch.equal(codes.contiguous().view(torch.uint8), want.contiguous().view(torch.uint8)), (rows, cols)
