@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) h[i][k] *= s * w[i][k];
+            for (uint32_t k = 0; k < 8; ++k) h[i][k] = h[i][k] * s * w[i][k];      // s w alone may overflow
         if (p.y_dt == DTT_E4M3) {
             float m[NCH];
 #pragma unroll
@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
         }
         if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
 #pragma unroll
-        for (uint32_t k = 0; k < E; ++k) h[k] *= s * w[k];
+        for (uint32_t k = 0; k < E; ++k) h[k] = h[k] * s * w[k];
         if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[turn][1], h);
         store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
         if (++st == S) { st = 0; phase ^= 1; }

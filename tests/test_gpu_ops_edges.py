@@ -67,3 +67,17 @@ def test_codes_of_many_values_are_the_quotients():
         D.RMSNorm(cols, x="f32", residual="f32", weight="f32", y="f32").forward(x, weight, y)
         want = (y / scales.repeat_interleave(group or cols, 1)[:, :cols]).to(TYPES["e4m3"])
         assert torch.equal(codes.contiguous().view(torch.uint8), want.contiguous().view(torch.uint8)), (rows, cols)
+
+
+@pytest.mark.parametrize("rows,cols,group,pad", FORWARD)
+def test_rows_of_small_values_under_a_large_weight(rows, cols, group, pad):
+    """rstd weight is beyond f32, h rstd weight is not (and in reverse, where it would be 0)."""
+    for size, weight, dtype in ((1e-18, 1e21, "f32"), (1e15, 1e-32, "f32")):
+        x = slab(rows, cols, pad, lambda *s: size * (1 + torch.rand(*s, generator=gen(cols), device="cuda")))
+        y = slab(rows, cols, pad, lambda *s: torch.zeros(*s, device="cuda"), dtype)
+        w = torch.full((cols,), weight, device="cuda")
+        D.RMSNorm(cols, x="f32", residual="f32", weight="f32", y=dtype, eps=0.0).forward(x, w, y)
+        h = x.double()
+        want = h * (h.square().mean(-1, keepdim=True)).rsqrt() * w.double()
+        # the row's error as in test_gpu_ops.py; a sum of squares around 1e-36 has all of f32's bits
+        assert ((y.double() - want).abs() <= 2e-6 * want.abs()).all()
