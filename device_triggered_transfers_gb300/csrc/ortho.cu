@@ -754,6 +754,7 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
                     continue;
                 }
                 ok = __all_sync(0xFFFFFFFFu, lane != 0 || reached(parts_counter(p, t), (t.k + 1) * (p.splits - 1) * 2 * EPI_WARPS, abort_flag));
+                __syncwarp();          // what lane 0 acquired is there for all lanes: a vote orders no memory
             }
             for (uint32_t g = 0; g < tn / SLAB && ok; ++g, ++s) {
                 uint8_t* slab = slabs + s % SLAB_BUFS * 2 * SLAB_BYTES;

@@ -81,3 +81,38 @@ def test_rows_of_small_values_under_a_large_weight(rows, cols, group, pad):
         want = h * (h.square().mean(-1, keepdim=True)).rsqrt() * w.double()
         # the row's error as in test_gpu_ops.py; a sum of squares around 1e-36 has all of f32's bits
         assert ((y.double() - want).abs() <= 2e-6 * want.abs()).all()
+
+
+# ---- orthogonalisation ----------------------------------------------------------------------------
+COEFFS = (3.4445, -4.7750, 2.0315)
+ORTHO_TOL = 9e-3                             # as test_gpu_ops.py derives it
+
+
+def orthogonalized(u, steps=5, eps=1e-7):
+    """The formula in 64 bits on the device; one matrix."""
+    u = u.double()
+    if u.shape[0] > u.shape[1]:
+        return orthogonalized(u.T, steps, eps).T
+    u = u / (u.norm() + eps)
+    a, b, c = COEFFS
+    for _ in range(steps):
+        g = u @ u.T
+        u = a * u + (b * g + c * (g @ g)) @ u
+    return u
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 512, 8192), (4, 700, 4000), (1, 2048, 8192)])
+def test_parts_of_the_first_product_are_all_there(batch, rows, cols):
+    """Large matrices whose first product is worked out in parts that other CTAs add: the same bits every time."""
+    x = torch.randn(batch, rows, cols, generator=gen(rows), device="cuda").to(torch.bfloat16)
+    out, again = (torch.zeros(batch, rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    with D.Orthogonalizer(rows, cols, batch=batch) as op:
+        op.run(x, out)
+        for _ in range(20):
+            again.zero_()
+            op.run(x, again)
+            assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+        assert op.errors == 0
+    for i in range(batch):
+        want = orthogonalized(x[i])
+        assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
