@@ -34,12 +34,18 @@ class _Workspace:
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
         torch.cuda.current_stream(self.buffer.device).synchronize()
         self.address, self.nbytes = self.buffer.data_ptr(), nbytes
-        self._last = None
+        self._last = self            # no stream yet (None is the default stream)
 
     def use(self, stream) -> None:
-        if stream is None or stream is self._last:
+        """A call on `stream` is about to be launched: the allocator must not give the buffer away before
+        it has finished, whatever stream the buffer was allocated on."""
+        if stream is self._last:
             return
-        s = self._torch.cuda.ExternalStream(stream, self.buffer.device) if isinstance(stream, int) else stream
+        cuda = self._torch.cuda
+        if stream is None:
+            s = cuda.default_stream(self.buffer.device)
+        else:
+            s = cuda.ExternalStream(stream, self.buffer.device) if isinstance(stream, int) else stream
         self.buffer.record_stream(s)
         self._last = stream
 

@@ -116,3 +116,28 @@ def test_parts_of_the_first_product_are_all_there(batch, rows, cols):
     for i in range(batch):
         want = orthogonalized(x[i])
         assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
+
+
+# ---- streams ---------------------------------------------------------------------------------------
+def test_a_workspace_is_not_given_away_while_a_call_on_the_default_stream_may_use_it():
+    """Built under a side stream, used on the default one and dropped while that call waits: the side stream's
+    next allocation of the size is another block."""
+    s = torch.cuda.Stream()
+    x = torch.randn(300, 500, generator=gen(1), device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        op = D.Orthogonalizer(300, 500)
+        address, size = op._workspace.address, op._workspace.buffer.numel()
+    op.run(x, out)                              # the default stream; kernels loaded
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)              # some 0.2 s
+    op.run(x, out)
+    op.close()
+    del op
+    with torch.cuda.stream(s):
+        other = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert other.data_ptr() != address
+    torch.cuda.synchronize()
+    want = orthogonalized(x)
+    assert float((out.double() - want).norm() / want.norm()) < ORTHO_TOL
