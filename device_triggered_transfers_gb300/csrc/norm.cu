@@ -31,6 +31,10 @@ constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   
 constexpr uint32_t kRingStages = 8;        // of a CTA, at most
 constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
 constexpr uint32_t kWaitLimit = 1u << 22;
+// Whether row r of a ring does not arrive for thread t in time: a build of its own shows what becomes of such rows.
+#ifndef DTT_NORM_ROW_LATE
+#define DTT_NORM_ROW_LATE false
+#endif
 constexpr uint32_t kShortCols = 256;       // columns of the short form, at most
 // Rows whose weight gradient is added up by columns in the same launch, at most.  By partial rows and by columns, back to
 // back in a graph: 16 x 4096 (bf16) 4.6 us and 2.8, 64 x 8064 6.6 and 4.5, 152 x 4096 6.1 and 3.8, 152 x 1024 5.1 and
@@ -685,11 +689,27 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const char* src, uint32_
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
+// Rows that do not arrive.  To a thread whose wait for a row runs out (`lost`) that row and all later ones are
+// NaN, and through the rows' sums to the others.  Thread 0 starts copies only into stages whose last row it has
+// seen arrive: where it gives up it starts no more, and waits in the end for those under way, of the CTA's
+// rows before `next`.
+__device__ __noinline__ void await_copies(uint64_t* full, uint32_t S, uint64_t next, uint32_t step) {
+    const uint64_t started = (next - blockIdx.x) / step;
+    for (uint64_t n = started > S ? started - S : 0; n < started; ++n) (void)bar_wait(saddr(full + n % S), n / S & 1);
+}
+
+constexpr float kNan = __builtin_nanf("");
+
+template <uint32_t N>
+__device__ __forceinline__ void make_nan(float (&v)[N]) {
+#pragma unroll
+    for (uint32_t k = 0; k < N; ++k) v[k] = kNan;
+}
+
 // Rows blockIdx.x, + gridDim.x, ... by one CTA.  Stage i % S holds the row of turn i: x, then the
 // residual.  Thread 0 starts the copies of turn i + S - 1 once turn i's reduction has passed its
-// barrier: every thread is then done with that stage's last row (turn i - 1).  A copy that does not
-// arrive makes the row NaN.  16384 x 4096 (bf16 to 8 bits, groups of 128): 79 us, 0.88 of the copy rate, the issue
-// slots 73 % full.
+// barrier: every thread is then done with that stage's last row (turn i - 1).  16384 x 4096 (bf16 to 8 bits,
+// groups of 128): 79 us, 0.88 of the copy rate, the issue slots 73 % full.
 template <uint32_t NCH>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
     launch_next();
@@ -738,8 +758,9 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
+    bool lost = false;
     for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
-        const bool here = bar_wait(saddr(full + st), phase);
+        lost = lost || DTT_NORM_ROW_LATE || !bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float h[NCH][8], sum = 0.0f;
 #pragma unroll
@@ -757,16 +778,18 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
         for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) sum += h[i][k] * h[i][k];
-        if (!here) sum = __int_as_float(0x7FC00000);
+        if (lost) sum = kNan;
         const float s = rsqrtf(row_sum(sum, T, slots[turn][0]) * p.inv_cols + p.eps);
         if (t == 0) {
-            start();
+            if (!lost) start();
             if (p.rstd) p.rstd[r] = s;
         }
         if (p.res_out) {
 #pragma unroll
-            for (uint32_t i = 0; i < NCH; ++i)
+            for (uint32_t i = 0; i < NCH; ++i) {
+                if (lost) make_nan(h[i]);
                 store8<true>(p.res_out + r * p.res_out_pitch, p.res_dt, 8 * (i * T + t), p.cols, h[i]);
+            }
         }
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i)
@@ -809,6 +832,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
         for (uint32_t i = 0; i < NCH; ++i) store8<true>(p.y + r * p.y_pitch, p.y_dt, 8 * (i * T + t), p.cols, h[i]);
         if (++st == S) { st = 0; phase ^= 1; }
     }
+    if (lost && t == 0) await_copies(full, S, next, gridDim.x);
 }
 
 // The backward pass the same way: a stage holds dy, h, then dres.  A row's latency is what the few CTAs of an SM have
@@ -868,11 +892,12 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
+    bool lost = false;
     float s_next = p.rstd[blockIdx.x];              // a turn ahead of its use
     for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
         const float s = s_next;
         if (r + p.partials < p.rows) s_next = p.rstd[r + p.partials];
-        const bool here = bar_wait(saddr(full + st), phase);
+        lost = lost || DTT_NORM_ROW_LATE || !bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float g[NCH][8], n[NCH][8], dot = 0.0f;
         constexpr uint32_t G = NCH > 2 ? 1 : NCH;   // chunks whose loads go out together: what the registers allow
@@ -901,9 +926,9 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
                 }
             }
         }
-        if (!here) dot = __int_as_float(0x7FC00000);
+        if (lost) dot = kNan;
         const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
-        if (t == 0) start();
+        if (t == 0 && !lost) start();
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) {
             const uint32_t c = 8 * (i * T + t);
@@ -919,6 +944,11 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
             store8<true>(p.dx + r * p.dx_pitch, p.h_dt, c, p.cols, o);
         }
         if (++st == S) { st = 0; phase ^= 1; }
+    }
+    if (lost) {                                     // acc has taken rows that had not arrived
+        if (t == 0) await_copies(full, S, next, p.partials);
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) make_nan(acc[i]);
     }
     if (p.partial) {
         float* part = p.partial + (uint64_t)blockIdx.x * p.cols;
@@ -989,8 +1019,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
+    bool lost = false;
     for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
-        const bool here = bar_wait(saddr(full + st), phase);
+        lost = lost || DTT_NORM_ROW_LATE || !bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float h[E], sum = 0.0f;
         load_elements(row + skip_of(p.x, r, p.x_pitch), p.x_dt, p.cols, h);
@@ -1002,19 +1033,23 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
         }
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
-        if (!here) sum = __int_as_float(0x7FC00000);
+        if (lost) sum = kNan;
         const float s = rsqrtf(row_sum(sum, T, slots[turn][0]) * p.inv_cols + p.eps);
         if (t == 0) {
-            start();
+            if (!lost) start();
             if (p.rstd) p.rstd[r] = s;
         }
-        if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
+        if (p.res_out) {
+            if (lost) make_nan(h);
+            store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
+        }
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) h[k] = h[k] * s * w[k];
         if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[turn][1], h);
         store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
         if (++st == S) { st = 0; phase ^= 1; }
     }
+    if (lost && t == 0) await_copies(full, S, next, gridDim.x);
 }
 
 // 16384 x 4001 in f32: 179 us, 0.86 of the copy rate; 1021 x 5001 in f32 19 us, 0.63: one CTA a SM (60 KiB a
@@ -1064,9 +1099,10 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
+    bool lost = false;
     for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
         const float s = p.rstd[r];
-        const bool here = bar_wait(saddr(full + st), phase);
+        lost = lost || DTT_NORM_ROW_LATE || !bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
         float g[E], n[E], dot = 0.0f;
         load_elements(row + skip_of(p.dy, r, p.dy_pitch), p.dy_dt, p.cols, g);
@@ -1078,9 +1114,9 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
             g[k] *= w[k];
             dot += g[k] * n[k];
         }
-        if (!here) dot = __int_as_float(0x7FC00000);
+        if (lost) dot = kNan;
         const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
-        if (t == 0) start();
+        if (t == 0 && !lost) start();
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) g[k] = s * (g[k] - n[k] * m);
         if (p.dres) {
@@ -1090,6 +1126,10 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
         }
         store_elements(p.dx + r * p.dx_pitch, p.h_dt, p.cols, g);
         if (++st == S) { st = 0; phase ^= 1; }
+    }
+    if (lost) {                                     // acc has taken rows that had not arrived
+        if (t == 0) await_copies(full, S, next, p.partials);
+        make_nan(acc);
     }
     if (p.partial) store_elements(reinterpret_cast<char*>(p.partial + (uint64_t)blockIdx.x * p.cols), DTT_F32, p.cols, acc);
 }

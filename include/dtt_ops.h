@@ -38,7 +38,9 @@ enum { DTT_E4M3 = 3 };
  *     scale = max(max_c |y_c| / 448, 2^-100) (to an ulp),
  *     y stored = e4m3(y_c / scale), the f32 quotient to the nearest code, ties to even,
  * so y_c ~ stored * scale, and a group of zeros gives zeros.  NaN anywhere in a row makes the
- * row's rstd, scales and outputs NaN; a row whose sum of squares overflows f32 has rstd 0. */
+ * row's rstd, scales and outputs NaN; a row whose sum of squares overflows f32 has rstd 0.  Should one
+ * of the kernels' bounded waits for a row ever run out, that row and the rows its CTA takes after it are NaN, in
+ * residual_out, dx and dweight too. */
 typedef struct dtt_rmsnorm_desc {
     uint32_t x_dtype;        /* x and, in the backward pass, dy: DTT_BF16 or DTT_F32 */
     uint32_t residual_dtype; /* residual, residual_out; backward: h, dres and dx: DTT_BF16 or DTT_F32 */

@@ -141,3 +141,52 @@ def test_a_workspace_is_not_given_away_while_a_call_on_the_default_stream_may_us
     torch.cuda.synchronize()
     want = orthogonalized(x)
     assert float((out.double() - want).norm() / want.norm()) < ORTHO_TOL
+
+
+# ---- rows that do not arrive -------------------------------------------------------------------------
+def library_with_late_rows(late, tmp):
+    """The library, beside the one under test, with thread t of the norm's rings giving up row r where `late` says so
+    (the waits before a CTA leaves stay)."""
+    import ctypes as C
+    import os
+    import subprocess
+    from device_triggered_transfers_gb300 import build as B
+    obj, lib = os.path.join(tmp, "norm.o"), os.path.join(tmp, "libdtt_late.so")
+    subprocess.run([B.nvcc(), *B.ARCH, *B.COMMON, f"-DDTT_NORM_ROW_LATE=({late})", "-c", os.path.join(B.CSRC, "norm.cu"), "-o", obj], check=True)
+    others = [os.path.join(B.OBJ, f + ".o") for f in B.sources() if f != "norm.cu"]
+    subprocess.run([B.nvcc(), *B.ARCH, "-shared", "-Xcompiler", "-fPIC", obj, *others, "-o", lib], check=True)
+    L = C.CDLL(lib)
+    for name in ("dtt_rmsnorm_forward", "dtt_rmsnorm_backward"):
+        getattr(L, name).restype, getattr(L, name).argtypes = D._SIGS[name]
+    return L
+
+
+@pytest.mark.parametrize("late", ["true", "r % 5 == 3", "r % 5 == 3 && t == 37"])
+def test_rows_that_do_not_arrive_in_time_are_nan_and_so_is_the_weight_s_gradient(late, tmp_path):
+    """Every value is right or NaN, never something else, whether all threads give up, at once or in the middle, or one
+    of them does; the CTAs wait for their copies before they leave."""
+    L = library_with_late_rows(late, str(tmp_path))
+    for rows, cols, pad, kind in ((2000, 1024, 0, "bf16"), (1000, 4096, 0, "bf16"), (400, 12288, 0, "bf16"), (1300, 1001, 0, "f32"), (1300, 3001, 3, "f32")):
+        g = gen(rows)
+        x, res, dres = (slab(rows, cols, pad, lambda *s: torch.randn(*s, generator=g, device="cuda"), kind) for _ in range(3))
+        w = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).to(TYPES[kind])
+        got = []
+        for other in (False, True):
+            op = D.RMSNorm(cols, x=kind, residual=kind, weight=kind, y=kind)
+            back = D.RMSNorm(cols, x=kind, residual=kind, weight=kind)
+            if other:
+                op._forward, back._backward = L.dtt_rmsnorm_forward, L.dtt_rmsnorm_backward
+            y, h, dx = (slab(rows, cols, pad, lambda *s: torch.full(s, 7.0, device="cuda"), kind) for _ in range(3))
+            rstd, dw = torch.full((rows,), 7.0, device="cuda"), torch.full((cols,), 7.0, device="cuda")
+            op.forward(x, w, y, residual=res, residual_out=h, rstd=rstd)
+            back.backward(x, res, w, (x.float() + res.float()).square().mean(-1).rsqrt(), dx, dw, dres=dres)
+            torch.cuda.synchronize()
+            got.append((y, h, rstd, dx, dw))
+        for right, seen in zip(*got):
+            assert not torch.isnan(right).any()
+            gone = torch.isnan(seen)
+            assert gone.all() if late == "true" else (gone | (seen == right)).all()
+        y, h, rstd, dx, dw = got[1]
+        assert torch.isnan(rstd[3::5]).all() and torch.isnan(h[3::5]).any(-1).all() and torch.isnan(dx[3::5]).all()
+        assert torch.equal(torch.isnan(rstd), torch.isnan(y).all(-1)) and torch.equal(torch.isnan(rstd), torch.isnan(y).any(-1))
+        assert torch.equal(torch.isnan(dx).any(-1), torch.isnan(dx).all(-1)) and torch.isnan(dw).any()
