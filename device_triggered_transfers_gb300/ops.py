@@ -24,13 +24,20 @@ def _code(who: str, name: str, dtype: str) -> int:
     return _CODES[dtype]
 
 
+def _torch_stream(stream, device):
+    """torch's object for a `stream` argument (None: the default stream; an address; or a torch stream)."""
+    import torch
+    if stream is None:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+
+
 class _Workspace:
     """A device buffer from torch's allocator, handed to calls on any stream: the allocating
     stream is done with it before its first use, and it is not reused while a call may run."""
 
     def __init__(self, nbytes: int, device):
         import torch
-        self._torch = torch
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
         torch.cuda.current_stream(self.buffer.device).synchronize()
         self.address, self.nbytes = self.buffer.data_ptr(), nbytes
@@ -41,13 +48,19 @@ class _Workspace:
         it has finished, whatever stream the buffer was allocated on."""
         if stream is self._last:
             return
-        cuda = self._torch.cuda
-        if stream is None:
-            s = cuda.default_stream(self.buffer.device)
-        else:
-            s = cuda.ExternalStream(stream, self.buffer.device) if isinstance(stream, int) else stream
-        self.buffer.record_stream(s)
+        self.buffer.record_stream(_torch_stream(stream, self.buffer.device))
         self._last = stream
+
+    @classmethod
+    def on(cls, stream, nbytes: int, device) -> "_Workspace":
+        """One whose first call is on `stream`: allocated in that stream's order, so that nothing waits and the
+        stream may be capturing (the graph's own pool then has the buffer)."""
+        import torch
+        w = cls.__new__(cls)
+        with torch.cuda.stream(_torch_stream(stream, device)):
+            w.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        w.address, w.nbytes, w._last = w.buffer.data_ptr(), nbytes, stream
+        return w
 
 
 class RMSNorm:
@@ -55,8 +68,9 @@ class RMSNorm:
     (dtt_rmsnorm_forward / dtt_rmsnorm_backward: see there for the definitions).
 
     x, residual, weight, y: element types, "bf16" or "f32" (y also "e4m3", with `group` columns per
-    scale: 0 for one scale per row, 32, 64 or 128).  Keeps the backward pass's workspace, so one
-    object serves one stream at a time (or the caller orders the streams)."""
+    scale: 0 for one scale per row, 32, 64 or 128).  Keeps the backward pass's workspace (allocated by
+    the first call with a dweight, in the order of that call's stream), so one object serves one stream at a time (or
+    the caller orders the streams)."""
 
     def __init__(self, cols: int, x: str = "bf16", residual: str = "bf16", weight: str = "bf16",
                  y: str = "bf16", group: int = 0, eps: float = 1e-6):
@@ -122,7 +136,7 @@ class RMSNorm:
         ws, need = 0, 0
         if dweight is not None:
             if self._workspace is None or self._workspace.buffer.device != dy.device:
-                self._workspace = _Workspace(self.workspace_bytes, dy.device)
+                self._workspace = _Workspace.on(stream, self.workspace_bytes, dy.device)
             self._workspace.use(stream)
             ws, need = self._workspace.address, self.workspace_bytes
         rc = self._backward(self._ref, rows, gp, gs, hp, hs, self._flat("weight", weight, self.cols, self._w),

@@ -190,3 +190,54 @@ def test_rows_that_do_not_arrive_in_time_are_nan_and_so_is_the_weight_s_gradient
         assert torch.isnan(rstd[3::5]).all() and torch.isnan(h[3::5]).any(-1).all() and torch.isnan(dx[3::5]).all()
         assert torch.equal(torch.isnan(rstd), torch.isnan(y).all(-1)) and torch.equal(torch.isnan(rstd), torch.isnan(y).any(-1))
         assert torch.equal(torch.isnan(dx).any(-1), torch.isnan(dx).all(-1)) and torch.isnan(dw).any()
+
+
+# ---- the backward pass's first call ------------------------------------------------------------------
+def gradients(rows, cols, seed=3):
+    g = gen(seed)
+    x, h, dx = (torch.randn(rows, cols, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    w = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).to(torch.bfloat16)
+    return dict(dy=x, h=h, weight=w, rstd=h.float().square().mean(-1).rsqrt(), dx=dx), torch.full((cols,), 7.0, device="cuda")
+
+
+@pytest.mark.parametrize("rows", [40, 500])
+def test_an_object_s_first_backward_pass_may_be_captured(rows):
+    cols = 1000
+    a, dw = gradients(rows, cols)
+    D.RMSNorm(cols).backward(**a, dweight=dw)
+    want, want_dx = dw.clone(), a["dx"].clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    op, graph = D.RMSNorm(cols), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        op.backward(**a, dweight=dw, stream=s)
+    dw.zero_()
+    a["dx"].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dw, want) and torch.equal(a["dx"], want_dx)
+    # later calls outside the graph, on other streams
+    other = torch.cuda.Stream()
+    for stream in (None, other, other.cuda_stream):
+        dw.zero_()
+        torch.cuda.synchronize()
+        op.backward(**a, dweight=dw, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(dw, want)
+
+
+def test_an_object_s_first_backward_pass_does_not_wait_for_its_stream():
+    rows, cols = 500, 1000
+    a, dw = gradients(rows, cols)
+    op, s, done = D.RMSNorm(cols), torch.cuda.Stream(), torch.cuda.Event()
+    D.RMSNorm(cols).backward(**a, dweight=dw)
+    want = dw.clone()
+    with torch.cuda.stream(s):
+        torch.empty(op.workspace_bytes, dtype=torch.uint8, device="cuda")     # the stream's pool has the room now
+        torch.cuda.synchronize()
+        torch.cuda._sleep(400_000_000)
+        done.record()
+        op.backward(**a, dweight=dw, stream=s)
+        assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(dw, want)
