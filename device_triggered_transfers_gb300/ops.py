@@ -36,12 +36,14 @@ class _Workspace:
     """A device buffer from torch's allocator, handed to calls on any stream: the allocating
     stream is done with it before its first use, and it is not reused while a call may run."""
 
+    _UNUSED = object()               # None is the default stream
+
     def __init__(self, nbytes: int, device):
         import torch
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
         torch.cuda.current_stream(self.buffer.device).synchronize()
         self.address, self.nbytes = self.buffer.data_ptr(), nbytes
-        self._last = self            # no stream yet (None is the default stream)
+        self._last = self._UNUSED
 
     def use(self, stream) -> None:
         """A call on `stream` is about to be launched: the allocator must not give the buffer away before
@@ -50,6 +52,11 @@ class _Workspace:
             return
         self.buffer.record_stream(_torch_stream(stream, self.buffer.device))
         self._last = stream
+
+    def wait(self) -> None:
+        """Until the last call's stream has run out of work."""
+        if self._last is not self._UNUSED:
+            _torch_stream(self._last, self.buffer.device).synchronize()
 
     @classmethod
     def on(cls, stream, nbytes: int, device) -> "_Workspace":
@@ -214,7 +221,9 @@ class Orthogonalizer:
 
     @property
     def errors(self) -> int:
-        """Internal waits that gave up so far (0; synchronises with the GPU)."""
+        """Internal waits that gave up so far (0).  Waits for the last call's stream, and so for all of this
+        object's calls, but not for replays of a graph that holds some."""
+        self._workspace.wait()
         return int(self._err.item())
 
     def close(self) -> None:

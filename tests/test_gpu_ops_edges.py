@@ -241,3 +241,20 @@ def test_an_object_s_first_backward_pass_does_not_wait_for_its_stream():
         assert not done.query()
     torch.cuda.synchronize()
     assert torch.equal(dw, want)
+
+
+# ---- the error word ----------------------------------------------------------------------------------
+def test_errors_waits_for_the_last_call_whatever_its_stream():
+    x = torch.randn(64, 64, generator=gen(1), device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        with D.Orthogonalizer(64, 64) as op:
+            assert op.errors == 0
+            op.run(x, out, stream=stream)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(torch.cuda.default_stream() if stream is None else side):
+                torch.cuda._sleep(200_000_000)
+                op._err.fill_(3)                # as if the call had counted, late
+            with torch.cuda.stream(torch.cuda.Stream()):
+                assert op.errors == 3
