@@ -17,6 +17,7 @@
 
 #include "dtt_ops.h"
 #include "internal.h"
+#include "ring.h"
 #include "rowio.cuh"
 
 namespace dtt {
@@ -27,9 +28,8 @@ constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its rec
 // Partial rows of the weight's gradient, at most: four, eight or sixteen a SM.  Rows of one warp (256
 // columns and less) have several in a CTA: 20000 x 256 25 us with sixteen CTAs a SM, 20 with four.
 __host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return cols > 1024 || cols <= 256 ? 608 : cols > 512 ? 1216 : 2432; }
-constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = 512;   // a row's most threads
-constexpr uint32_t kRingStages = 8;        // of a CTA, at most
-constexpr uint32_t kRingSmem = 200 * 1024; // of all CTAs of an SM
+constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = ring::kThreads;   // a row's most threads
+constexpr uint32_t kFwdOwn = 640, kBwdOwn = 2432;    // shared memory of a ring's CTA beside its stages, at most
 constexpr uint32_t kWaitLimit = 1u << 22;
 // Whether row r of a ring does not arrive for thread t in time: a build of its own shows what becomes of such rows.
 #ifndef DTT_NORM_ROW_LATE
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
     launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][2][32];
-    __shared__ uint64_t full[kRingStages];
+    __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t stage_bytes = xb + rb;
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
     if (blockIdx.x >= p.partials) return weight_columns(p);
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][32];
-    __shared__ uint64_t full[kRingStages];
+    __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
     const uint32_t stage_bytes = gb + hb + (p.dres ? hb : 0);
@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
     launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][2][32];
-    __shared__ uint64_t full[kRingStages];
+    __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t x_room = words_room(xb), stage_bytes = x_room + (rb ? words_room(rb) : 0);
@@ -1060,7 +1060,7 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
     if (blockIdx.x >= p.partials) return weight_columns(p);
     extern __shared__ __align__(128) uint8_t stages[];
     __shared__ float slots[2][32];
-    __shared__ uint64_t full[kRingStages];
+    __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
     const uint32_t g_room = words_room(gb), h_room = words_room(hb), stage_bytes = g_room + (p.dres ? 2 : 1) * h_room;
@@ -1154,33 +1154,6 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* part
     if (lane == 0 && (uint64_t)blockIdx.x * 32 + warp < cols) dweight[(uint64_t)blockIdx.x * 32 + warp] = v;
 }
 
-struct Ring {
-    uint32_t nch, threads, ctas, stages, smem;       // ctas: of an SM; 0: no ring for these rows
-};
-
-// Chunks (vec): one a thread up to `one` columns, two up to 512 threads, then four.  Elements: 8 a thread up to
-// `one` columns, then 16.  Rows of one warp are left to the other forms.  threads: of an SM with one, two
-// and four chunks (what the registers allow), in as many CTAs, fewer where three stages each would not
-// fit, but `least` all the same where two would; then as many stages as fit, but no more than `stages`
-// where an SM has four CTAs or more.  Measured: the forward pass of 20000 x 5001 (f32) takes 279 us with
-// one CTA of five stages, 211 with two of two; the backward pass of 4000 x 4096 (f32) 49 us with one, 53 with two.
-Ring ring_of(uint32_t cols, bool vec, uint64_t stage, uint32_t one, const uint32_t (&threads)[3], uint32_t least, uint32_t stages) {
-    Ring g{};
-    if (2 * stage > kRingSmem) return g;
-    const uint32_t stage_bytes = (uint32_t)stage;
-    uint32_t i = 0;
-    for (; i < (vec ? 3 : 2); ++i) {
-        g.nch = 1u << i;
-        g.threads = ((cols + 8 * g.nch - 1) / (8 * g.nch) + 31) / 32 * 32;
-        if (g.threads <= kRingThreads && (i > 0 || cols <= one)) break;
-    }
-    if (g.threads < 64 || g.threads > kRingThreads) return {};
-    g.ctas = std::min({std::max(threads[i] / g.threads, 1u), std::max(kRingSmem / (3 * stage_bytes), std::min(kRingSmem / (2 * stage_bytes), least)), 16u});
-    g.stages = std::min(g.ctas >= 4 ? stages : kRingStages, kRingSmem / (g.ctas * stage_bytes));
-    g.smem = g.stages * stage_bytes;
-    return g;
-}
-
 uint32_t short_lanes(uint32_t cols) {
     uint32_t n = 1;
     while (8 * n < cols) n *= 2;
@@ -1212,7 +1185,7 @@ cudaError_t launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
     // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
     // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
-    const Ring g = ring_of(p.cols, vec, vec ? xb + rb : xb + rb + 60, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : kRingStages);
+    const ring::Plan g = ring::plan(p.cols, vec, vec ? xb + rb : xb + rb + 60, kFwdOwn, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : ring::kStages);
     // The chunk form's loads wait for one another, the ring's do not: 152 x 8064 (bf16) 6.7 us by chunks, 3.7 by
     // the ring.  The element form's go out together, and it is the faster one while there are few rows:
     // 600 x 3001 5.7 us and 6.6, 2400 x 3001 22.2 and 18.4.
@@ -1247,7 +1220,7 @@ cudaError_t launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         return launch(rmsnorm_bwd_short_kernel, p.partials + columns, 256, 0, 0, true, stream, p, lanes);
     }
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
-    const Ring g = ring_of(p.cols, vec, vec ? stage : stage + 90, 2048, {1024, 512, 256}, 1, kRingStages);
+    const ring::Plan g = ring::plan(p.cols, vec, vec ? stage : stage + 90, kBwdOwn, 2048, {1024, 512, 256}, 1, ring::kStages);
     // by chunks and by the ring: 200 x 4096 (bf16) 11.2 us and 7.6, 16384 x 4096 255 and 92; by elements and by
     // the ring: 152 x 1021 (f32) 5.5 and 5.6, 460 x 5001 (f32) 15.3 and 10.8
     if (g.ctas && (vec || p.rows > sms)) {
@@ -1305,9 +1278,11 @@ bool aligned(const void* ptr, uint64_t pitch, uint32_t to) {
     return reinterpret_cast<uintptr_t>(ptr) % to == 0 && pitch % to == 0;      // null: aligned
 }
 
-cudaError_t prepare(const void* kernel) {
+// own: what the launches take a kernel's shared memory beside the stages to be, at most.
+cudaError_t prepare(const void* kernel, uint32_t own = ~0u) {
     cudaFuncAttributes a;
     cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess && a.sharedSizeBytes > own) return cudaErrorInvalidConfiguration;
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
     return e;
 }
@@ -1327,14 +1302,14 @@ cudaError_t preload_norm_kernels() {
         const cudaError_t e = prepare(k);
         if (e != cudaSuccess) return e;
     }
-    const void* rings[] = {(const void*)rmsnorm_fwd_ring_kernel<1>, (const void*)rmsnorm_bwd_ring_kernel<1>,
-                           (const void*)rmsnorm_fwd_ring_kernel<2>, (const void*)rmsnorm_fwd_ring_kernel<4>,
-                           (const void*)rmsnorm_bwd_ring_kernel<2>, (const void*)rmsnorm_bwd_ring_kernel<4>,
-                           (const void*)rmsnorm_fwd_ring_elements_kernel<8>, (const void*)rmsnorm_fwd_ring_elements_kernel<16>,
-                           (const void*)rmsnorm_bwd_ring_elements_kernel<8>, (const void*)rmsnorm_bwd_ring_elements_kernel<16>};
-    for (const void* k : rings) {
-        cudaError_t e = prepare(k);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmem);
+    const void* fwd_rings[] = {(const void*)rmsnorm_fwd_ring_kernel<1>, (const void*)rmsnorm_fwd_ring_kernel<2>, (const void*)rmsnorm_fwd_ring_kernel<4>,
+                               (const void*)rmsnorm_fwd_ring_elements_kernel<8>, (const void*)rmsnorm_fwd_ring_elements_kernel<16>};
+    const void* bwd_rings[] = {(const void*)rmsnorm_bwd_ring_kernel<1>, (const void*)rmsnorm_bwd_ring_kernel<2>, (const void*)rmsnorm_bwd_ring_kernel<4>,
+                               (const void*)rmsnorm_bwd_ring_elements_kernel<8>, (const void*)rmsnorm_bwd_ring_elements_kernel<16>};
+    for (uint32_t i = 0; i < 10; ++i) {
+        const void* k = i < 5 ? fwd_rings[i] : bwd_rings[i - 5];
+        cudaError_t e = prepare(k, i < 5 ? kFwdOwn : kBwdOwn);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring::kSmem);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
