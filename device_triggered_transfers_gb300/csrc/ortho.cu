@@ -2185,8 +2185,10 @@ extern "C" int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint
         if (reinterpret_cast<uintptr_t>(a.p) % a.e || a.pitch % a.e || a.stride % a.e)
             return fail(DTT_EINVAL, "%s: %s must be aligned to its elements", who, a.name);
         if (d.rows > 1 && a.pitch < d.cols * a.e) return fail(DTT_EINVAL, "%s: %s: the pitch is less than a row", who, a.name);
-        if (d.batch > 1 && a.stride < (d.rows - 1) * a.pitch + d.cols * a.e)
-            return fail(DTT_EINVAL, "%s: %s: the stride is less than a matrix", who, a.name);
+        // one matrix after the other, or the rows of one between those of another
+        const uint64_t row = d.cols * a.e;
+        if (d.batch > 1 && a.stride < (d.rows - 1) * a.pitch + row && (a.stride < row || a.pitch < (d.batch - 1) * a.stride + row))
+            return fail(DTT_EINVAL, "%s: %s: the matrices overlap", who, a.name);
     }
     if (reinterpret_cast<uintptr_t>(err) % 4) return fail(DTT_EINVAL, "%s: err is misaligned", who);
 

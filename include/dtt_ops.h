@@ -131,7 +131,8 @@ int dtt_ortho_workspace(const dtt_ortho_desc* desc, uint64_t* bytes);
 int dtt_ortho_create(const dtt_ortho_desc* desc, void* workspace, uint64_t workspace_bytes, dtt_ortho** out);
 
 /* Run it.  x, momentum (f32; NULL exactly where the desc has none) and out (bf16): matrix i starts
- * i * stride bytes after the first, rows `pitch` bytes apart.  No output overlaps an input.
+ * i * stride bytes after the first, rows `pitch` bytes apart; the matrices follow one another, or their rows
+ * alternate.  No output overlaps an input.
  * err: device uint32, incremented by a CTA whose bounded internal wait gave up (0 after a clean
  * run; the outputs are then unspecified).
  * Errors: DTT_EINVAL (pointers, alignment to the element, pitches, strides), DTT_ECUDA. */

@@ -118,6 +118,32 @@ def test_parts_of_the_first_product_are_all_there(batch, rows, cols):
         assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
 
 
+# a form each: one cluster, the second product within the third, a product a launch, everything in one launch
+FORMS = [(3, 96, 160), (2, 256, 512), (2, 520, 1032), (2, 2048, 2056), (3, 65, 130), (2, 700, 300), (2, 1201, 2049)]
+
+
+@pytest.mark.parametrize("batch,rows,cols", FORMS)
+def test_matrices_whose_rows_alternate(batch, rows, cols):
+    """A batch as the middle dimension: the same bits as one matrix after the other."""
+    g = gen(rows)
+    x = torch.randn(batch, rows, cols, generator=g, device="cuda")
+    m = torch.randn(batch, rows, cols, generator=g, device="cuda")
+    out = torch.zeros(batch, rows, cols, dtype=torch.bfloat16, device="cuda")
+    x2, m2 = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (x, m))
+    out2 = torch.zeros(rows, batch, cols, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    assert x2.stride(0) == cols and x2.stride(1) == batch * cols
+    with D.Orthogonalizer(rows, cols, batch=batch, dtype="f32", mu=0.9, nesterov=True) as op:
+        op.run(x, out, momentum=m)
+        op.run(x2, out2, momentum=m2)
+        assert op.errors == 0
+        for shared in (x[:1].expand(batch, rows, cols), x.as_strided((batch, rows, cols), (cols - 1, batch * cols, 1)),
+                       x.as_strided((batch, rows, cols), (cols, batch * cols - 1, 1))):
+            with pytest.raises(D.DttError) as e:
+                op.run(shared, out, momentum=m)
+            assert e.value.code == D.EINVAL
+    assert torch.equal(out2, out) and torch.equal(m2, m) and out.any()
+
+
 # ---- streams ---------------------------------------------------------------------------------------
 def test_a_workspace_is_not_given_away_while_a_call_on_the_default_stream_may_use_it():
     """Built under a side stream, used on the default one and dropped while that call waits: the side stream's
