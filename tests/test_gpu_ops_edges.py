@@ -144,6 +144,35 @@ def test_matrices_whose_rows_alternate(batch, rows, cols):
     assert torch.equal(out2, out) and torch.equal(m2, m) and out.any()
 
 
+def momentum_of(x, m, mu, nesterov):
+    """(u, the new momentum) in 64 bits on the device."""
+    m = float(np.float32(mu)) * m + x.double()
+    return (x.double() + float(np.float32(mu)) * m if nesterov else m), m
+
+
+@pytest.mark.parametrize("nesterov", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,rows,cols", [(2, 256, 512), (2, 512, 1024), (2, 512, 264), (1, 2048, 2048), (2, 1024, 4096), (2, 300, 501), (2, 501, 300)])
+def test_momentum_over_steps_in_every_form(batch, rows, cols, dtype, nesterov):
+    """Updates too large for one cluster: by chunks and by elements, wide and tall.  Each step adds two roundings of
+    values below 16 to the momentum, 2^-21 each at most."""
+    g = gen(rows + cols)
+    m = torch.zeros(batch, rows, cols, device="cuda")
+    want_m = m.double()
+    out = torch.zeros(batch, rows, cols, dtype=torch.bfloat16, device="cuda")
+    with D.Orthogonalizer(rows, cols, batch=batch, dtype=dtype, mu=0.95, nesterov=nesterov) as op:
+        for step in range(3):
+            x = torch.randn(batch, rows, cols, generator=g, device="cuda").to(TYPES[dtype])
+            op.run(x, out, momentum=m)
+            assert op.errors == 0
+            u, want_m = momentum_of(x, want_m, 0.95, nesterov)
+            assert want_m.abs().max() < 16
+            assert (m.double() - want_m).abs().max() <= 2 * (step + 1) * 2.0 ** -21
+            for i in range(batch):
+                want = orthogonalized(u[i])
+                assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
+
+
 # ---- streams ---------------------------------------------------------------------------------------
 def test_a_workspace_is_not_given_away_while_a_call_on_the_default_stream_may_use_it():
     """Built under a side stream, used on the default one and dropped while that call waits: the side stream's
