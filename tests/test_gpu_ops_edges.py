@@ -173,6 +173,46 @@ def test_momentum_over_steps_in_every_form(batch, rows, cols, dtype, nesterov):
                 assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
 
 
+def modelled(u, terms, steps=5):
+    """The arithmetic that dtt_ops.h describes, in 64 bits but for the roundings it names: X in two f16 halves, the
+    products' operands in f16, b A + c A A in one or two f16 terms, the result in bf16."""
+    def f16(x):
+        return x.to(torch.float16).double()
+
+    def halves(x):
+        x = x.float().double()
+        return f16(x), f16((x - f16(x)) * 2048) / 2048
+
+    a, b, c = COEFFS
+    hi, lo = halves(u.double() / (u.double().norm() + 1e-7))
+    for _ in range(steps):
+        gram = f16(hi @ hi.T)
+        poly = (b * gram + c * (gram @ gram)).float().double()
+        operand = f16(poly)
+        if terms == 2:
+            operand = operand + f16(poly - operand)
+        x = a * (hi + lo) + operand @ hi
+        hi, lo = halves(x)
+    return x.float().to(torch.bfloat16).double()
+
+
+@pytest.mark.parametrize("terms,rows,cols", [(2, 96, 160), (2, 128, 512), (2, 128, 2048), (2, 200, 1000), (2, 256, 512), (1, 512, 512), (1, 520, 1032),
+                                             (1, 1024, 2048), (1, 2048, 2048)])
+def test_the_error_is_that_of_the_documented_roundings(terms, rows, cols):
+    """Against 64 bits, no further off than a model with those roundings alone; one f16 term where there are two would
+    be 1.12 to 1.18 times as far off.  Beside them are the f32 sums' errors, 2^-11 of the f16 operands': 8 % is for
+    the rounding errors that fall otherwise."""
+    u = torch.randn(rows, cols, generator=gen(cols), device="cuda")
+    out = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    with D.Orthogonalizer(rows, cols, dtype="f32") as op:
+        op.run(u, out)
+        assert op.errors == 0
+    want = orthogonalized(u)
+    error, model = (float((t - want).norm() / want.norm()) for t in (out.double(), modelled(u, terms)))
+    assert 1.6e-3 < model < 2.7e-3              # bf16's own is 1.66e-3
+    assert error < 1.08 * model
+
+
 # ---- streams ---------------------------------------------------------------------------------------
 def test_a_workspace_is_not_given_away_while_a_call_on_the_default_stream_may_use_it():
     """Built under a side stream, used on the default one and dropped while that call waits: the side stream's
