@@ -353,3 +353,51 @@ def test_errors_waits_for_the_last_call_whatever_its_stream():
                 op._err.fill_(3)                # as if the call had counted, late
             with torch.cuda.stream(torch.cuda.Stream()):
                 assert op.errors == 3
+
+
+# ---- nothing beside the outputs ----------------------------------------------------------------------
+def guarded(rows, cols, kind, aligned):
+    """(a buffer full of sevens, its rows x cols in the middle: 16-byte aligned or not at all)"""
+    left, right = (16, 16) if aligned else (3, 4)
+    wide = torch.full((rows + 2, left + cols + right), 7.0, device="cuda").to(TYPES[kind])
+    return wide, wide[1:rows + 1, left:left + cols]
+
+
+def untouched(wide, view):
+    """Whether everything of the buffer but the view is still sevens (the view is overwritten with them)."""
+    view.view(torch.uint8 if view.dtype == TYPES["e4m3"] else view.dtype).copy_(
+        torch.full(view.shape, 7.0, device="cuda").to(view.dtype).view(torch.uint8 if view.dtype == TYPES["e4m3"] else view.dtype))
+    return bool((wide.float() == 7).all())
+
+
+@pytest.mark.parametrize("rows,cols,group,pad", FORWARD + [(40, 136, 64, 0), (700, 264, 128, 0), (33, 1001, 32, 1), (1300, 101, 0, 1), (1217, 4001, 64, 1), (5, 9001, 128, 1)])
+def test_outputs_are_written_exactly(rows, cols, group, pad):
+    g = gen(rows)
+    for y, residual in (("e4m3", "bf16"), ("bf16", "f32"), ("f32", "bf16")):
+        x, res = (torch.randn(rows, cols, generator=g, device="cuda").to(TYPES[k]) for k in ("bf16", residual))
+        (wy, vy), (wr, vr) = guarded(rows, cols, y, not pad), guarded(rows, cols, residual, not pad)
+        op = D.RMSNorm(cols, x="bf16", residual=residual, y=y, group=group if y == "e4m3" else 0)
+        count = rows * op.scale_cols
+        ws, wd = torch.full((count + 8,), 7.0, device="cuda"), torch.full((rows + 8,), 7.0, device="cuda")
+        op.forward(x, None, vy, residual=res, residual_out=vr, scales=ws[4:4 + count] if y == "e4m3" else None, rstd=wd[4:4 + rows])
+        torch.cuda.synchronize()
+        h = x.float() + res.float()
+        assert torch.equal(vr, h.to(TYPES[residual])) and (wd[4:4 + rows] != 7).all()
+        assert untouched(wy, vy) and untouched(wr, vr)
+        for w, n in ((ws, count if y == "e4m3" else 0), (wd, rows)):
+            assert (w[:4] == 7).all() and (w[4 + n:] == 7).all()
+        # and the gradient
+        dy, dres = (torch.randn(rows, cols, generator=g, device="cuda").to(TYPES[k]) for k in ("bf16", residual))
+        rstd = h.square().mean(-1).rsqrt()
+        wx, vx = guarded(rows, cols, residual, not pad)
+        plain = torch.zeros(rows, cols, device="cuda").to(TYPES[residual])
+        weight = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+        back = D.RMSNorm(cols, x="bf16", residual=residual)
+        dws = [torch.full((cols + 8,), 7.0, device="cuda") for _ in range(2)]
+        back.backward(dy, res, weight, rstd, vx, dws[0][4:4 + cols], dres=dres)
+        back.backward(dy, res, weight, rstd, plain, dws[1][4:4 + cols], dres=dres)
+        torch.cuda.synchronize()
+        assert (vx.float() - plain.float()).abs().max() <= 2.0 ** -6 * plain.float().abs().max()     # other forms round otherwise
+        assert untouched(wx, vx)
+        for dw in dws:
+            assert (dw[:4] == 7).all() and (dw[4 + cols:] == 7).all() and (dw[4:4 + cols] != 7).all()
