@@ -401,3 +401,59 @@ def test_outputs_are_written_exactly(rows, cols, group, pad):
         assert untouched(wx, vx)
         for dw in dws:
             assert (dw[:4] == 7).all() and (dw[4 + cols:] == 7).all() and (dw[4:4 + cols] != 7).all()
+
+
+# ---- one after the other ------------------------------------------------------------------------------
+def test_calls_that_read_what_the_call_before_wrote_need_no_wait_between_them():
+    """Launches begin before the one before them has ended.  Two norms, the gradient and an orthogonalisation of it on
+    one stream, new values every time, against the same with the GPU idle between any two."""
+    rows, cols = 1536, 1024
+    kinds = dict(x="bf16", residual="bf16")
+    first, second, back = D.RMSNorm(cols, **kinds), D.RMSNorm(cols, y="f32", **kinds), D.RMSNorm(cols, **kinds)
+    ortho = [D.Orthogonalizer(rows // n, cols // n, batch=n * n, mu=0.9, nesterov=True) for n in (1, 4, 8)]
+    s = torch.cuda.Stream()
+    n_rounds = 25
+    g = gen(5)
+    inputs = [torch.randn(rows, cols, generator=g, device="cuda").to(torch.bfloat16) for _ in range(n_rounds)]
+    weight = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).to(torch.bfloat16)
+
+    def chain(wait):
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+        x, h, y, dx = (torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+        z, dw, rstd = torch.zeros(rows, cols, device="cuda"), torch.zeros(cols, device="cuda"), torch.zeros(rows, device="cuda")
+        moms = [torch.zeros(rows * cols, device="cuda") for _ in ortho]
+        outs = [torch.zeros(rows * cols, dtype=torch.bfloat16, device="cuda") for _ in ortho]
+        kept = [[torch.zeros_like(t) for _ in range(n_rounds)] for t in (z, dx, dw, *outs)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for k in range(n_rounds):
+                x.copy_(inputs[k])
+                done()
+                first.forward(x, weight, y, residual=h, residual_out=h, stream=s)
+                done()
+                second.forward(y, weight, z, residual=h, residual_out=h, rstd=rstd, stream=s)
+                done()
+                back.backward(y, h, weight, rstd, dx, dw, stream=s)
+                done()
+                for op, m, o in zip(ortho, moms, outs):
+                    shape = (op.batch, op.rows, op.cols)
+                    op.run(dx.view(shape), o.view(shape), momentum=m.view(shape), stream=s)
+                    done()
+                first.forward(outs[0].view(rows, cols), weight, y, residual=h, residual_out=h, stream=s)
+                done()
+                back.backward(outs[1].view(rows, cols), h, weight, rstd, dx, dw, dres=dx, stream=s)
+                done()
+                for t, keep in zip((z, dx, dw, *outs), kept):
+                    keep[k].copy_(t)
+                done()
+        torch.cuda.synchronize()
+        return kept
+
+    for fast, slow in zip(chain(False), chain(True)):
+        for k in range(n_rounds):
+            assert torch.equal(fast[k], slow[k]) and slow[k].any()
+    for op in ortho:
+        assert op.errors == 0
+        op.close()
