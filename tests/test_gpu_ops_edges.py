@@ -457,3 +457,57 @@ def test_calls_that_read_what_the_call_before_wrote_need_no_wait_between_them():
     for op in ortho:
         assert op.errors == 0
         op.close()
+
+
+# ---- beyond four gigabytes -----------------------------------------------------------------------------
+# aligned rows of a ring, short rows, rows of single elements in a ring; then few rows very far apart
+@pytest.mark.parametrize("rows,cols,apart", [(600000, 4096, 0), (20_000_000, 128, 0), (600000, 4001, 0), (40, 4096, 60_000_000), (40, 1001, 60_000_001),
+                                             (200, 1001, 12_000_001), (40, 40000, 60_000_000)])
+def test_offsets_past_32_bits(rows, cols, apart):
+    """More than 4 GB from the first to the last row: the last rows' values, zeros elsewhere."""
+    def big(fill=0.0):
+        if not apart:
+            return torch.full((rows, cols), fill, dtype=torch.bfloat16, device="cuda")
+        return torch.full((rows * apart,), fill, dtype=torch.bfloat16, device="cuda").as_strided((rows, cols), (apart, 1))
+
+    g = gen(cols)
+    small = {k: torch.randn(3, cols, generator=g, device="cuda").to(torch.bfloat16) for k in ("x", "res", "dres")}
+    x, y = big(), big(7.0)
+    x[-3:] = small["x"]
+    rstd = torch.zeros(rows, device="cuda")
+    weight = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).to(torch.bfloat16)
+    op = D.RMSNorm(cols, eps=1e-5)
+    op.forward(x, weight, y, rstd=rstd)
+    torch.cuda.synchronize()
+    h = small["x"].double()
+    s = (h.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    want = h * s * weight.double()
+    assert ((y[-3:].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-30).all() and not y[:-3].any()
+    assert ((rstd[-3:, None].double() - s).abs() <= 2e-6 * s).all()
+    del y
+    dx, dw = big(7.0), torch.zeros(cols, device="cuda")
+    op.backward(x, x, weight, rstd, dx, dw, dres=x)
+    torch.cuda.synchronize()
+    s = rstd[-3:, None].double()
+    n, gr = h * s, h * weight.double()
+    want = s * (gr - n * (gr * n).mean(-1, keepdim=True)) + h
+    # bf16's half spacing and 50 f32 roundings of terms below 100
+    assert ((dx[-3:].double() - want).abs() <= 2.0 ** -8 * want.abs() + 100 * 50 * 2.0 ** -24).all() and not dx[:-3].any()
+    assert ((dw.double() - (h * n).sum(0)).abs() <= 500 * 2.0 ** -24 * (h * n).abs().sum(0) + 1e-30).all()
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(3, 96, 160), (3, 300, 512), (3, 301, 511), (3, 512, 300), (1, 1536, 1600)])
+def test_matrices_past_32_bits(batch, rows, cols):
+    """Matrices, or rows, more than 4 GB apart."""
+    strides = (1_200_000_000, cols, 1) if batch > 1 else (0, 1_000_000, 1)
+    size = (batch - 1) * strides[0] + (rows - 1) * strides[1] + cols
+    x, m = (torch.zeros(size, device="cuda").as_strided((batch, rows, cols), strides) for _ in range(2))
+    out = torch.zeros(size, dtype=torch.bfloat16, device="cuda").as_strided((batch, rows, cols), strides)
+    x.copy_(torch.randn(batch, rows, cols, generator=gen(rows), device="cuda"))
+    with D.Orthogonalizer(rows, cols, batch=batch, dtype="f32", mu=0.9, nesterov=True) as op:
+        op.run(x, out, momentum=m)
+        assert op.errors == 0
+    assert torch.equal(m, x)
+    for i in range(batch):
+        want = orthogonalized(1.9 * x[i].double())
+        assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
