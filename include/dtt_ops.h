@@ -11,6 +11,12 @@
  * A tensor is rows of contiguous elements, `pitch` bytes apart, at any alignment its element type
  * allows; rows that are 16-byte aligned throughout take the faster paths.  Inputs may be read in whole
  * aligned 16-byte words (no allocation ends within one); outputs are written exactly.
+ *
+ * Run them between rounds, not in one: their kernels take nearly all shared memory and registers
+ * of an SM, and large orthogonalisations every SM at once, while a round's copiers hold theirs from
+ * the round's start (an early copier, from the round before on) until it is done.  An operator that
+ * a round in progress waits for, as its producer or before it on its stream, may not get to run
+ * beside the copiers, and the round then ends by its time limit.  No call checks this.
  */
 #ifndef DTT_OPS_H
 #define DTT_OPS_H
@@ -51,7 +57,9 @@ typedef struct dtt_rmsnorm_desc {
     uint64_t cols;           /* 1 .. 2^24 */
 } dtt_rmsnorm_desc;
 
-/* rows x cols elements (rows 0: nothing is read or written).
+/* rows x cols elements (rows 0: nothing is read or written).  The same call gives the same bits; a row of
+ * another call may differ in the last bits where the number of rows, the alignments or the absence of
+ * an argument choose another form, whose sums run in another order.
  *  - residual, residual_out, rstd may be NULL; residual_out may be residual itself (the same
  *    pointer and pitch), otherwise no output overlaps an input or another output.
  *  - scales: device f32 [rows][ceil(cols / group)] (group 0: [rows]), needed for DTT_E4M3 and
@@ -98,8 +106,15 @@ int dtt_rmsnorm_workspace(const dtt_rmsnorm_desc* desc, uint64_t* bytes);
  * Each step maps every singular value s of X to a s + b s^3 + c s^5 and keeps the singular
  * vectors.  The products run on the tensor cores with f16 operands and f32 sums; X itself is held
  * in 32 bits (two f16 halves, 22 significant bits), because a rounded iterate's noise in the
- * directions that u lacks would grow by a (3.44 with the usual coefficients) in every step.  Large
- * matrices run as one cooperative launch over all SMs: it begins when they are free. */
+ * directions that u lacks would grow by a (3.44 with the usual coefficients) in every step.  A is
+ * rounded to f16, and b A + c A A to two f16 terms where the smaller side is 128 at most (256 for
+ * most shapes), to one beyond.  Five usual steps end 1.7e-3 to 2.6e-3 of the result's norm off 64 bits,
+ * of which the bf16 output's own rounding is 1.66e-3; a matrix with a handful of singular values, all
+ * where a step is steep, up to 1e-2.
+ * |u|^2 is summed in f32: where it overflows (|u| of 1.8e19 or more) the result is zeros, and elements below
+ * 1e-19 add nothing to it (eps has to be well above what |u| is then).  Elements of X below 2^-36 are 0, as
+ * all are where eps is 1e10 times |u|.  A NaN or an infinity makes its matrix NaN, and no other of the batch.
+ * Large matrices run as one cooperative launch over all SMs: it begins when they are free. */
 #define DTT_ORTHO_MAX_STEPS 32
 
 typedef struct dtt_ortho_desc {

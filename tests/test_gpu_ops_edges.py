@@ -213,6 +213,33 @@ def test_the_error_is_that_of_the_documented_roundings(terms, rows, cols):
     assert error < 1.08 * model
 
 
+@pytest.mark.parametrize("batch,rows,cols", [f for f in FORMS if f[0] > 1])
+def test_huge_tiny_and_infinite_updates(batch, rows, cols):
+    """A sum of squares beyond f32: zeros.  Far below eps: zeros.  An infinity: NaN.  The other matrices as ever, and
+    the same for 1e15 and 1e-5 times an update."""
+    g = gen(cols)
+    u = torch.randn(rows, cols, generator=g, device="cuda")
+    x = torch.stack([u] + [torch.randn(rows, cols, generator=g, device="cuda") for _ in range(batch - 1)])
+    want = [orthogonalized(t) for t in x]
+    out = torch.zeros(batch, rows, cols, dtype=torch.bfloat16, device="cuda")
+    with D.Orthogonalizer(rows, cols, batch=batch, dtype="f32") as op:
+        for value in ("huge", "tiny", "infinite", 2.0 ** 50, 2.0 ** -3):
+            x[0] = u * {"huge": 1e19, "tiny": 1e-22, "infinite": 1.0}.get(value, value)
+            if value == "infinite":
+                x[0, rows // 2, cols // 3] = float("inf")
+            out.fill_(7)
+            op.run(x, out)
+            assert op.errors == 0
+            if value in ("huge", "tiny"):
+                assert not out[0].any()
+            elif value == "infinite":
+                assert torch.isnan(out[0]).all()
+            else:
+                assert float((out[0].double() - want[0]).norm() / want[0].norm()) < ORTHO_TOL
+            for i in range(1, batch):
+                assert float((out[i].double() - want[i]).norm() / want[i].norm()) < ORTHO_TOL
+
+
 # ---- streams ---------------------------------------------------------------------------------------
 def test_a_workspace_is_not_given_away_while_a_call_on_the_default_stream_may_use_it():
     """Built under a side stream, used on the default one and dropped while that call waits: the side stream's
