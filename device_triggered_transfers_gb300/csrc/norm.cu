@@ -27,7 +27,7 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its reciprocal stays finite
 // Partial rows of the weight's gradient, at most: four, eight or sixteen a SM.  Rows of one warp (256
 // columns and less) have several in a CTA: 20000 x 256 25 us with sixteen CTAs a SM, 20 with four.
-__host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return cols > 1024 || cols <= 256 ? 608 : cols > 512 ? 1216 : 2432; }
+__host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return (cols > 1024 || cols <= 256 ? 4 : cols > 512 ? 8 : 16) * kSms; }
 constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = ring::kThreads;   // a row's most threads
 constexpr uint32_t kFwdOwn = 640, kBwdOwn = 2432;    // shared memory of a ring's CTA beside its stages, at most
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -264,8 +264,8 @@ __device__ __forceinline__ void weight_columns(const BwdParams& p) {
 // ---- short rows --------------------------------------------------------------------------------
 // A row by `lanes` neighbouring lanes of a warp (a power of two), a chunk each; a CTA has 256 / lanes rows.  A
 // thread's loads all go out before the first value is used, and many CTAs hide them: with two or four rows a
-// thread under way the forward pass of 300000 x 128 (bf16 to 8 bits) takes 58 and 82 us, with one 57
-// (55 behind another call), 0.72 of the copy rate.
+// thread under way the forward pass of 300000 x 128 (bf16 to 8 bits) took 58 and 82 us where one took 57.
+// Behind another call it takes 59 (bf16 52), 0.67 (0.88) of the copy rate; the exact quotients are 2 us of it.
 __global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_constant__ FwdParams p, uint32_t lanes) {
     launch_next();
     wait_previous();

@@ -6,7 +6,7 @@
 // as its f16 operand (hi) and the rest of it times 2^11 in f16 (lo): 22 significant bits, and nothing
 // below 2^-35 is lost.  An X of one f16 would carry noise of 2^-12 |X| in the singular directions that
 // the update lacks, where a step multiplies it by a = 3.44: for a rank-1 update five steps in f16 end
-// 10 % off, in bf16 75 %, with 32 bits 0.2 % (the bf16 output).  The noise of rounded operands meets X
+// 10 % off, in bf16 75 %, with 32 bits 0.17 % (the bf16 output).  The noise of rounded operands meets X
 // only through b A + c A A, whose range holds nothing of those directions.
 //
 // A and b A + c A A are symmetric: only tiles on and below the diagonal are computed, and each is
@@ -56,7 +56,7 @@ static_assert(T16_OFFSET + 128 * T16_PITCH * 2 <= STAGES * 2 * HALF_STAGE && 128
 
 constexpr uint32_t kStartTile = 64;                  // ortho_start_tiles_kernel: elements a side
 constexpr uint32_t START_CTAS = 8;                   // of the update and start kernels on a SM
-constexpr uint32_t kMaxParts = 152 * START_CTAS;     // CTAs of the update's launch at most: all run at once
+constexpr uint32_t kMaxParts = kSms * START_CTAS;     // CTAs of the update's launch at most: all run at once
 
 enum Product { GRAM, POLY, APPLY };
 
@@ -1824,13 +1824,13 @@ double gram_us(uint64_t L, uint32_t splits) {
     return 0.3 + 0.275 * (double)((kblocks + splits - 1) / splits) + (splits > 1 ? 3.0 + splits : 0.0);
 }
 
-// How many parts: few tiles of long rows then occupy more of the 76 pairs.  Measured, by one part and by these: 512 x
+// How many parts: few tiles of long rows then occupy more of the SMs' pairs.  Measured, by one part and by these: 512 x
 // 8192, four of them 428 us and 335, 2048 x 8192 606 and 544, 700 x 4000, four, 291 and 271; 1024 x 1024
 // would lose by two, 181 and 190.
 uint32_t splits_of(uint64_t S, uint64_t L, uint32_t batch) {
     const uint64_t n = (S + 255) / 256, tiles = n * (n + 1) / 2 * batch, kblocks = (L + BK - 1) / BK;
     uint32_t best = 1;
-    for (uint32_t splits = 2; splits <= 4 && tiles * splits <= 76 && kblocks >= 8 * splits; ++splits)
+    for (uint32_t splits = 2; splits <= 4 && tiles * splits <= kSms / 2 && kblocks >= 8 * splits; ++splits)
         if (gram_us(L, splits) < gram_us(L, best)) best = splits;
     const uint64_t each = (kblocks + best - 1) / best;
     return (uint32_t)((kblocks + each - 1) / each);

@@ -10,6 +10,10 @@
 
 namespace dtt {
 
+// SMs of the GPU that the workspaces' sizes and the rules on sizes are made for, both asked for without a device.
+// Launches go by the device's own count; on another count the results hold and the rules are less apt.
+constexpr uint32_t kSms = 152;
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
