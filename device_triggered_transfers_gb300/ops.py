@@ -1,7 +1,8 @@
 """Operators on the block of rows that a rank owns between a reduce-scatter and an all-gather
 (C ABI in include/dtt_ops.h): the residual's addition with a root-mean-square norm, that norm's
-backward pass, and the orthogonalisation of a momentum update.  Argument checks and marshalling
-only; tensors are torch CUDA tensors whose rows are contiguous (any row pitch)."""
+backward pass, and the orthogonalisation of a momentum update.  Argument checks, marshalling and
+the workspaces only; tensors are torch CUDA tensors whose rows are contiguous (any row pitch).
+An object lives as long as the graphs that hold its calls."""
 from __future__ import annotations
 
 import ctypes as C
