@@ -43,7 +43,15 @@ constexpr uint32_t SLAB = 64;                        // pair form: columns that 
 constexpr uint32_t SLAB_BYTES = 128 * SLAB * 2;      // of one f16 array: 16 KiB
 constexpr uint32_t SLAB_BUFS = 2;
 constexpr uint32_t TILES = 160;                      // of a cluster of the pair form, worked out beforehand
-constexpr uint32_t WAIT_LIMIT = 1u << 22;
+// Looks at an mbarrier, at most: one that fails takes 4 us, so some seconds.  A build of its own makes the waits of
+// some threads run out (DTT_ORTHO_LATE), or all of them sooner.
+#ifndef DTT_ORTHO_WAIT_LIMIT
+#define DTT_ORTHO_WAIT_LIMIT (1u << 20)
+#endif
+#ifndef DTT_ORTHO_LATE
+#define DTT_ORTHO_LATE false
+#endif
+constexpr uint32_t WAIT_LIMIT = DTT_ORTHO_WAIT_LIMIT;
 constexpr uint32_t SMEM_BYTES = 1024 /* alignment slack */ + STAGES * 2 * HALF_STAGE + SLAB_BUFS * 2 * SLAB_BYTES + 256 + TILES * 8;
 // instruction descriptor (kind::f16): f32 accumulator, f16 operands, M = m, N = n
 __host__ __device__ constexpr uint32_t idesc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
@@ -92,8 +100,10 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 }
 
 // Bounded wait for the phase of the given parity; false when the limit ran out or another role
-// already reported an error.
+// already reported an error (abort; null: a wait for what is under way, before a CTA leaves, which
+// nothing cuts short).
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+    if (abort && (DTT_ORTHO_LATE)) return false;
     for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
         uint32_t done;
         asm volatile(
@@ -102,7 +112,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done) : "r"(bar), "r"(parity) : "memory");
         if (done) return true;
-        if ((i & 255) == 255 && *abort) return false;
+        if (abort && (i & 255) == 0 && *abort) return false;
     }
     return false;
 }
@@ -314,7 +324,7 @@ __device__ __forceinline__ uint32_t pair_tiles(const PairParams& p) {
 
 // Wait (bounded) until a counter has reached `target`.
 __device__ __forceinline__ bool reached(const uint32_t* c, uint32_t target, volatile uint32_t* abort) {
-    for (uint32_t polls = 0; polls < WAIT_LIMIT; ++polls) {
+    for (uint32_t polls = 0; polls < 4 * WAIT_LIMIT; ++polls) {
         uint32_t v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
         if (v >= target) return true;
@@ -601,7 +611,7 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
             bool ok = true;
             for (uint32_t u = c0; u < places && ok; u += NC) {
                 const Tile t = tile_at(u);
-                if (!inputs_ready(p, t, abort_flag)) { fail(); break; }
+                if (!inputs_ready(p, t, abort_flag)) { fail(); ok = false; break; }
                 const uint32_t now = (p.step + t.k) & 1, tn = t.product == APPLY ? p.tn : 256;
                 const CUtensorMap* mA = t.product == GRAM ? &p.hi_rows[now] : t.product == POLY ? &p.gram : &p.poly;
                 const CUtensorMap* mB = t.product == APPLY ? &p.hi_cols[now] : mA;
@@ -630,9 +640,11 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
             // the leader's full barriers count both CTAs' loads: once its last phases complete, every
             // load of the pair has landed
             if (leader) {
-                volatile uint32_t never = 0;
                 for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-                    (void)bar_wait(saddr(full + i % STAGES), (i / STAGES) & 1, &never);
+                    (void)bar_wait(saddr(full + i % STAGES), (i / STAGES) & 1, nullptr);
+            } else if (!ok) {
+                // the leader may have given up before it counted this CTA's last loads: 0.2 ms for a few us of them
+                for (uint32_t i = 0; i < 256; ++i) __nanosleep(1000);
             }
         }
     } else if (warp == MMA_WARP) {
@@ -665,8 +677,7 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
             }
             // every MMA has finished before either CTA releases TMEM or shared memory
             umma_commit_local2(saddr(drain));
-            volatile uint32_t never = 0;
-            (void)bar_wait(saddr(drain), 0, &never);
+            (void)bar_wait(saddr(drain), 0, nullptr);
         }
     } else if (warp == SLAB_WARP) {
         if (lane == 0 && c0 < places) {
@@ -717,9 +728,9 @@ ortho_pair_kernel(const __grid_constant__ PairParams p) {
             }
             if (!ok) fail();
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-            volatile uint32_t never = 0;          // every load has landed before the CTA can leave
+            // every load has landed before the CTA can leave
             for (uint32_t n = loaded > SLAB_BUFS ? loaded - SLAB_BUFS : 0; n < loaded; ++n)
-                (void)bar_wait(saddr(slab_in + n % SLAB_BUFS), n / SLAB_BUFS & 1, &never);
+                (void)bar_wait(saddr(slab_in + n % SLAB_BUFS), n / SLAB_BUFS & 1, nullptr);
         }
     } else {
         // epilogue
@@ -992,9 +1003,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
                 }
             }
             // the last loads of every stage have landed before the stages are used for the tile
-            volatile uint32_t never = 0;
             for (uint32_t n = issued > STAGES ? issued - STAGES : 0; n < issued; ++n)
-                (void)bar_wait(saddr(full + n % STAGES), (n / STAGES) & 1, &never);
+                (void)bar_wait(saddr(full + n % STAGES), (n / STAGES) & 1, nullptr);
         }
     } else if (warp == MMA_WARP) {
         if (lane == 0) {
@@ -1011,8 +1021,7 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
                 umma_commit(saddr(empty + stage));     // the stage is free once these finish
             }
             umma_commit(saddr(done));
-            volatile uint32_t never = 0;
-            (void)bar_wait(saddr(done), 0, &never);
+            (void)bar_wait(saddr(done), 0, nullptr);
         }
     }
     __syncwarp();
@@ -1039,7 +1048,8 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_split_kernel(const __grid_co
         if (threadIdx.x < CTAS && threadIdx.x != q)
             push(at_rank(saddr(from) + q * SLICE, threadIdx.x), saddr(tile) + threadIdx.x * SLICE, SLICE, at_rank(saddr(sums_full), threadIdx.x));
         __syncwarp();
-        if (warp < EPI_WARPS && !bar_wait(saddr(sums_full), 0, abort_flag) && lane == 0) fail();
+        // nothing cuts this short: the others send their sums whatever happens, and these must have landed
+        if (warp < EPI_WARPS && !bar_wait(saddr(sums_full), 0, nullptr) && lane == 0) fail();
         __syncwarp();
         // here: every CTA has what was sent to it (the wait is at the end, before the CTA leaves)
         asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
@@ -1136,8 +1146,9 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_fused_kernel(const __grid_co
                     tma_load_3d(saddr(sX + k * HALF_STAGE + h * (HALF_STAGE / 2)), &p.tmB, (int32_t)(j * 128 + 64 * h), (int32_t)(k * BK), (int32_t)m, saddr(x_full));
         }
         __syncwarp();
-        for (uint32_t k = 0; k < kblocks; ++k) wait(a_full + k);   // every load has landed before the CTA can leave
-        wait(x_full);
+        // every load has landed before the CTA can leave, and before A's place is used again
+        for (uint32_t k = 0; k < kblocks; ++k) (void)bar_wait(saddr(a_full + k), 0, nullptr);
+        (void)bar_wait(saddr(x_full), 0, nullptr);
     } else if (warp == MMA_WARP) {
         for (uint32_t k = 0; k < kblocks; ++k) {
             wait(a_full + k);
@@ -1187,7 +1198,9 @@ __global__ void __launch_bounds__(THREADS, 1) ortho_fused_kernel(const __grid_co
         }
         __syncwarp();
     }
-    wait(done + 1);                               // all: the MMAs are done, A's place is free
+    // all: the MMAs, which were issued whatever had been given up, are done, and A's place is free
+    if (!bar_wait(saddr(done + 1), 0, nullptr) && lane == 0) atomicAdd(p.err, 1u);
+    __syncwarp();
     tc_fence_after();
     float4* tile = reinterpret_cast<float4*>(smem);
     if (warp < EPI_WARPS) {
@@ -1628,9 +1641,17 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
     if (isinf(inv)) inv = 0.0f;                       // u is then 0 in f16 as well
     const uint32_t row = 32 * (warp % 4) + lane, half = warp / 4;
     uint32_t phase = 0;
-    volatile uint32_t never = 0;
+    // A thread that has given up a wait waits no more, and starts nothing that others count on, so that they give
+    // up in their turn; thread 0, which starts the MMAs and arms the barriers of what comes in, waits in
+    // the end for what it started last.
+    bool ok = true;
+    volatile uint32_t not_cut_short = 0;
+    uint32_t started = 0, armed = 0;                  // products, of thread 0; steps whose sums and rows of A it awaits
     auto await = [&](uint64_t* bar, uint32_t parity) {
-        if (!bar_wait(saddr(bar), parity, &never) && lane == 0) atomicAdd(p.err, 1u);
+        if (ok && !bar_wait(saddr(bar), parity, &not_cut_short)) {
+            ok = false;
+            atomicAdd(p.err, 1u);
+        }
         __syncwarp();
     };
     // what the threads wrote is there for the MMAs that `issue` starts; all threads wait for these
@@ -1639,9 +1660,10 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (t == 0) {
+        if (t == 0 && ok) {
             issue();
             umma_commit(saddr(done));
+            ++started;
         }
         __syncwarp();
         await(done, phase);
@@ -1700,11 +1722,12 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
             }
             fence_async();
             __syncthreads();
-            if (t == 0) {
+            if (t == 0 && ok) {
                 bar_expect_tx(saddr(sums_full), (CTAS - 1) * SLICE);
                 bar_expect_tx(saddr(gram_full), (CTAS - 1) * 2 * A_SLICE);
+                ++armed;
             }
-            if (t < CTAS && t != q)
+            if (t < CTAS && t != q && ok)
                 push(at_rank(saddr(sums) + q * SLICE, t), saddr(own) + t * SLICE, SLICE, at_rank(saddr(sums_full), t));
             await(sums_full, k & 1);
             // the CTA's rows of A, a word of four columns at a time; to be sent from the place of its own
@@ -1727,7 +1750,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
             }
             fence_async();
             __syncthreads();
-            if (t < 2 * CTAS && t / 2 != q)
+            if (t < 2 * CTAS && t / 2 != q && ok)
                 push(at_rank(saddr(gram) + t % 2 * BLOCK_BYTES + q * A_SLICE, t / 2), saddr(made) + t % 2 * A_SLICE, A_SLICE,
                      at_rank(saddr(gram_full), t / 2));
             await(gram_full, k & 1);
@@ -1788,6 +1811,11 @@ __global__ void __launch_bounds__(RES_THREADS, 1) ortho_resident_kernel(const __
                 store_result(out, row, l0 + 64 * n + 32 * half, hi + n * BLOCK_BYTES, row, half, v);
             }
         }
+    }
+    if (t == 0 && !ok) {
+        if (started) (void)bar_wait(saddr(done), (started - 1) & 1, nullptr);
+        if (armed) (void)bar_wait(saddr(sums_full), (armed - 1) & 1, nullptr);
+        if (armed) (void)bar_wait(saddr(gram_full), (armed - 1) & 1, nullptr);
     }
     tc_fence_before();
     __syncthreads();

@@ -266,28 +266,27 @@ def test_a_workspace_is_not_given_away_while_a_call_on_the_default_stream_may_us
 
 
 # ---- rows that do not arrive -------------------------------------------------------------------------
-def library_with_late_rows(late, tmp):
-    """The library, beside the one under test, with thread t of the norm's rings giving up row r where `late` says so
-    (the waits before a CTA leaves stay)."""
+def library_with(source, defines, tmp):
+    """The library, beside the one under test, with one source built for late arrivals."""
     import ctypes as C
     import os
     import subprocess
     from device_triggered_transfers_gb300 import build as B
-    obj, lib = os.path.join(tmp, "norm.o"), os.path.join(tmp, "libdtt_late.so")
-    subprocess.run([B.nvcc(), *B.ARCH, *B.COMMON, f"-DDTT_NORM_ROW_LATE=({late})", "-c", os.path.join(B.CSRC, "norm.cu"), "-o", obj], check=True)
-    others = [os.path.join(B.OBJ, f + ".o") for f in B.sources() if f != "norm.cu"]
+    obj, lib = os.path.join(tmp, "late.o"), os.path.join(tmp, "libdtt_late.so")
+    subprocess.run([B.nvcc(), *B.ARCH, *B.COMMON, *defines, "-c", os.path.join(B.CSRC, source), "-o", obj], check=True)
+    others = [os.path.join(B.OBJ, f + ".o") for f in B.sources() if f != source]
     subprocess.run([B.nvcc(), *B.ARCH, "-shared", "-Xcompiler", "-fPIC", obj, *others, "-o", lib], check=True)
     L = C.CDLL(lib)
-    for name in ("dtt_rmsnorm_forward", "dtt_rmsnorm_backward"):
-        getattr(L, name).restype, getattr(L, name).argtypes = D._SIGS[name]
+    for name, (restype, argtypes) in D._SIGS.items():
+        getattr(L, name).restype, getattr(L, name).argtypes = restype, argtypes
     return L
 
 
 @pytest.mark.parametrize("late", ["true", "r % 5 == 3", "r % 5 == 3 && t == 37"])
 def test_rows_that_do_not_arrive_in_time_are_nan_and_so_is_the_weight_s_gradient(late, tmp_path):
     """Every value is right or NaN, never something else, whether all threads give up, at once or in the middle, or one
-    of them does; the CTAs wait for their copies before they leave."""
-    L = library_with_late_rows(late, str(tmp_path))
+    of them does (thread t gives up row r where `late` says so); the CTAs wait for their copies before they leave."""
+    L = library_with("norm.cu", [f"-DDTT_NORM_ROW_LATE=({late})"], str(tmp_path))
     for rows, cols, pad, kind in ((2000, 1024, 0, "bf16"), (1000, 4096, 0, "bf16"), (400, 12288, 0, "bf16"), (1300, 1001, 0, "f32"), (1300, 3001, 3, "f32")):
         g = gen(rows)
         x, res, dres = (slab(rows, cols, pad, lambda *s: torch.randn(*s, generator=g, device="cuda"), kind) for _ in range(3))
@@ -312,6 +311,30 @@ def test_rows_that_do_not_arrive_in_time_are_nan_and_so_is_the_weight_s_gradient
         assert torch.isnan(rstd[3::5]).all() and torch.isnan(h[3::5]).any(-1).all() and torch.isnan(dx[3::5]).all()
         assert torch.equal(torch.isnan(rstd), torch.isnan(y).all(-1)) and torch.equal(torch.isnan(rstd), torch.isnan(y).any(-1))
         assert torch.equal(torch.isnan(dx).any(-1), torch.isnan(dx).all(-1)) and torch.isnan(dw).any()
+
+
+def test_an_orthogonalisation_that_gives_up_its_waits_counts_an_error_and_ends(tmp_path, monkeypatch):
+    """CTAs that give up at once, and others that wait in vain for them for 16 ms: all end soon, the error word says
+    so, and the GPU does the next call as ever.  One cluster of 1, 4 and 16 CTAs, the second product within the
+    third, a product a launch."""
+    import time
+    L = library_with("ortho.cu", ["-DDTT_ORTHO_LATE=(blockIdx.x == 0 || blockIdx.x == 5)", "-DDTT_ORTHO_WAIT_LIMIT=4096u"], str(tmp_path))
+    for batch, rows, cols in ((3, 64, 64), (2, 100, 600), (1, 128, 4096), (1, 256, 512), (1, 1000, 200), (1, 512, 512)):
+        x = torch.randn(batch, rows, cols, generator=gen(rows), device="cuda").to(torch.bfloat16)
+        out = torch.zeros(batch, rows, cols, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        with monkeypatch.context() as m:
+            m.setattr(D, "lib", lambda: L)
+            with D.Orthogonalizer(rows, cols, batch=batch) as op:
+                began = time.time()
+                op.run(x, out)
+                assert op.errors > 0 and time.time() - began < 5
+        with D.Orthogonalizer(rows, cols, batch=batch) as op:
+            op.run(x, out)
+            assert op.errors == 0
+        for i in range(batch):
+            want = orthogonalized(x[i])
+            assert float((out[i].double() - want).norm() / want.norm()) < ORTHO_TOL
 
 
 # ---- the backward pass's first call ------------------------------------------------------------------
