@@ -30,7 +30,7 @@ constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its rec
 __host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return (cols > 1024 || cols <= 256 ? 4 : cols > 512 ? 8 : 16) * kSms; }
 constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = ring::kThreads;   // a row's most threads
 constexpr uint32_t kFwdOwn = 640, kBwdOwn = 2432;    // shared memory of a ring's CTA beside its stages, at most
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 1u << 18;      // looks at an mbarrier; one that fails takes 4 us: a second
 // Whether row r of a ring does not arrive for thread t in time: a build of its own shows what becomes of such rows.
 #ifndef DTT_NORM_ROW_LATE
 #define DTT_NORM_ROW_LATE false
