@@ -148,8 +148,8 @@ int dtt_ortho_create(const dtt_ortho_desc* desc, void* workspace, uint64_t works
 /* Run it.  x, momentum (f32; NULL exactly where the desc has none) and out (bf16): matrix i starts
  * i * stride bytes after the first, rows `pitch` bytes apart; the matrices follow one another, or their rows
  * alternate.  No output overlaps an input.
- * err: device uint32, incremented by a CTA whose bounded internal wait gave up (0 after a clean
- * run; the outputs are then unspecified).
+ * err: device uint32, incremented where a bounded internal wait gives up (0 after a clean run;
+ * otherwise the outputs are unspecified, the call has ended all the same, and the next one is as ever).
  * Errors: DTT_EINVAL (pointers, alignment to the element, pitches, strides), DTT_ECUDA. */
 int dtt_ortho_run(dtt_ortho* o, const void* x, uint64_t x_pitch, uint64_t x_stride, float* momentum,
                   uint64_t momentum_pitch, uint64_t momentum_stride, void* out, uint64_t out_pitch,
