@@ -126,6 +126,22 @@ class dtt_ortho_desc(C.Structure):
                 ("eps", C.c_float), ("scale", C.c_float), ("coeffs", (C.c_float * 3) * ORTHO_MAX_STEPS)]
 
 
+class dtt_experts_desc(C.Structure):
+    _fields_ = [("experts", C.c_uint32), ("first", C.c_uint32), ("top_k", C.c_uint32), ("align", C.c_uint32)]
+
+
+class dtt_adamw_desc(C.Structure):
+    _fields_ = [("param_dtype", C.c_uint32), ("grad_dtype", C.c_uint32), ("state_dtype", C.c_uint32),
+                ("stochastic", C.c_uint32), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_float),
+                ("seed", C.c_uint32)]
+
+
+class dtt_adamw_tensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scales", C.c_void_p), ("v_scales", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_uint64),
+                ("weight_decay", C.c_float), ("reserved", C.c_uint32)]
+
+
 ORDER_FN = C.CFUNCTYPE(C.c_int, C.c_uint64, C.c_void_p, C.POINTER(C.c_uint32),
                        C.POINTER(C.c_uint32))
 
@@ -198,6 +214,22 @@ _SIGS = {
     "dtt_rmsnorm_backward": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), _u64, _P, _u64, _P, _u64, _P, _P, _P, _u64,
                                        _P, _u64, _P, _P, _u64, _P]),
     "dtt_rmsnorm_workspace": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), C.POINTER(_u64)]),
+    "dtt_layernorm_forward": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), _u64, _P, _u64, _P, _u64, _P, _P, _P, _u64,
+                                        _P, _u64, _P, _P, _P, _P]),
+    "dtt_layernorm_backward": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), _u64, _P, _u64, _P, _u64, _P, _P, _P, _P, _u64,
+                                         _P, _u64, _P, _P, _P, _u64, _P]),
+    "dtt_layernorm_workspace": (C.c_int, [C.POINTER(dtt_rmsnorm_desc), C.POINTER(_u64)]),
+    "dtt_experts_workspace": (C.c_int, [C.POINTER(dtt_experts_desc), C.POINTER(_u64)]),
+    "dtt_experts_route": (C.c_int, [C.POINTER(dtt_experts_desc), _u64, _P, _u32, _u64, _P, _P, _P, _P, _u64, _P]),
+    "dtt_experts_dispatch": (C.c_int, [C.POINTER(dtt_experts_desc), _u64, _P, _P, _P, _P, _u64, _u64, _P, _u64, _u64,
+                                       _P, _u64, _u64, _P, _u64, _P]),
+    "dtt_experts_combine": (C.c_int, [C.POINTER(dtt_experts_desc), _u64, _u64, _P, _P, _u32, _u64, _u64, _P, _P, _u32,
+                                      _u64, _P]),
+    "dtt_experts_combine_backward": (C.c_int, [C.POINTER(dtt_experts_desc), _u64, _u64, _P, _P, _P, _P, _u32, _u64, _P,
+                                               _u32, _u64, _u64, _P, _P, _u64, _P, _P]),
+    "dtt_adamw_create": (C.c_int, [C.POINTER(dtt_adamw_desc), C.POINTER(dtt_adamw_tensor), _u32, C.POINTER(_P)]),
+    "dtt_adamw_run": (C.c_int, [_P, C.POINTER(_P), C.c_float, _u32, _P, _P, _P, _P]),
+    "dtt_adamw_destroy": (None, [_P]),
     "dtt_ortho_workspace": (C.c_int, [C.POINTER(dtt_ortho_desc), C.POINTER(_u64)]),
     "dtt_ortho_create": (C.c_int, [C.POINTER(dtt_ortho_desc), _P, _u64, C.POINTER(_P)]),
     "dtt_ortho_run": (C.c_int, [_P, _P, _u64, _u64, _P, _u64, _u64, _P, _u64, _u64, _P, _P]),
@@ -966,4 +998,4 @@ def dtt_gemm_producer(A, Bt, bufs, M: int, N: int, K: int, ldc: int, slice_offs,
 
 
 # ---- operators on a rank's own block (include/dtt_ops.h) --------------------------------------
-from .ops import Orthogonalizer, RMSNorm  # noqa: E402,F401
+from .ops import AdamW, ExpertRows, LayerNorm, Orthogonalizer, RMSNorm  # noqa: E402,F401

@@ -1,0 +1,523 @@
+// Tokens' rows sorted by the experts that a rank holds, and back with weights, and their gradients (dtt_ops.h has
+// the definitions).
+//
+// The sort is a counting sort, stable and without atomics whose order could show: each warp counts a run of its
+// own, and places it once the sums before it are known.  The row kernels go by tokens, so that a token's row is
+// read once for all of its choices (dispatch, combine_backward) or written once (combine), and gradients of a
+// token's several rows are added without atomics.
+#include <algorithm>
+#include <cstdint>
+
+#include "dtt_ops.h"
+#include "internal.h"
+#include "rowio.cuh"
+
+namespace dtt {
+namespace {
+
+constexpr uint32_t kMostExperts = 1024, kMostChoices = 32;
+constexpr uint32_t kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
+constexpr uint32_t kMostParts = 64;            // CTAs of the sort, at most
+constexpr uint32_t kPartPairs = 2048;          // pairs of a CTA, at least, while there are fewer
+constexpr uint32_t kRowThreads = 256;
+constexpr uint32_t kFillRows = 8;              // rows of one CTA where an expert's rows are filled up
+
+struct RouteParams {
+    const void* ids;
+    int32_t* position;
+    int32_t* offsets;
+    int32_t* counts;
+    uint32_t* parts;            // [gridDim.x][experts]: each CTA's pairs of each expert
+    uint64_t pairs, each;       // each: of a CTA, a multiple of kRouteThreads
+    uint32_t experts, first, align, max_rows;
+    uint32_t wide;              // ids of 64 bits
+};
+
+// The expert of pair i as the rank counts them, `experts` where it is another rank's, or none.
+__device__ __forceinline__ uint32_t expert_of(const RouteParams& p, uint64_t i) {
+    const int64_t id = p.wide ? reinterpret_cast<const int64_t*>(p.ids)[i] : reinterpret_cast<const int32_t*>(p.ids)[i];
+    const uint64_t e = (uint64_t)id - p.first;                 // below: wraps to a large number
+    return id >= 0 && e < p.experts ? (uint32_t)e : p.experts;
+}
+
+// How many of the warp's run of pairs each expert has: mine[e], zero before.  Pairs of 32 neighbours that share an
+// expert are counted by the first of them.
+__device__ __forceinline__ void count_run(const RouteParams& p, uint64_t from, uint64_t to, uint32_t* mine) {
+    const uint32_t lane = threadIdx.x % 32;
+    for (uint64_t i0 = from; i0 < to; i0 += 32) {
+        const uint64_t i = i0 + lane;
+        const uint32_t e = i < to ? expert_of(p, i) : p.experts;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        if (e < p.experts && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+}
+
+__global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const __grid_constant__ RouteParams p) {
+    launch_next();
+    wait_previous();
+    extern __shared__ uint32_t counts[];           // [kRouteWarps][experts]
+    const uint32_t t = threadIdx.x, warp = t / 32;
+    for (uint32_t i = t; i < kRouteWarps * p.experts; i += kRouteThreads) counts[i] = 0;
+    __syncthreads();
+    const uint64_t run = p.each / kRouteWarps, from = blockIdx.x * p.each + warp * run;
+    count_run(p, min(from, p.pairs), min(from + run, p.pairs), counts + warp * p.experts);
+    __syncthreads();
+    for (uint32_t e = t; e < p.experts; e += kRouteThreads) {
+        uint32_t sum = 0;
+        for (uint32_t w = 0; w < kRouteWarps; ++w) sum += counts[w * p.experts + e];
+        p.parts[(uint64_t)blockIdx.x * p.experts + e] = sum;
+    }
+}
+
+// Exclusive sums over the experts' rows: n = experts values at `v`, in place; `carry`: 32 words.
+__device__ __forceinline__ void scan_experts(uint32_t* v, uint32_t n, uint32_t* carry) {
+    const uint32_t t = threadIdx.x, lane = t % 32, warp = t / 32;
+    constexpr uint32_t per = kMostExperts / kRouteThreads;
+    uint32_t x[per], sum = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < per; ++k) {
+        x[k] = per * t + k < n ? v[per * t + k] : 0;
+        sum += x[k];
+    }
+    uint32_t upto = sum;
+#pragma unroll
+    for (uint32_t d = 1; d < 32; d *= 2) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) carry[warp] = upto;
+    __syncthreads();
+    uint32_t before = upto - sum;
+    for (uint32_t w = 0; w < warp; ++w) before += carry[w];
+#pragma unroll
+    for (uint32_t k = 0; k < per; ++k) {
+        if (per * t + k < n) v[per * t + k] = before;
+        before += x[k];
+    }
+}
+
+// parts null: the one CTA counts its pairs itself.
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid_constant__ RouteParams p) {
+    launch_next();
+    wait_previous();
+    extern __shared__ uint32_t counts[];           // [kRouteWarps][experts], then [experts] twice
+    __shared__ uint32_t carry[32];
+    uint32_t* total = counts + kRouteWarps * p.experts;
+    uint32_t* offset = total + p.experts;
+    const uint32_t t = threadIdx.x, warp = t / 32, lane = t % 32;
+    for (uint32_t i = t; i < kRouteWarps * p.experts; i += kRouteThreads) counts[i] = 0;
+    __syncthreads();
+    const uint64_t run = p.each / kRouteWarps;
+    const uint64_t from = min(blockIdx.x * p.each + warp * run, p.pairs), to = min(blockIdx.x * p.each + warp * run + run, p.pairs);
+    count_run(p, from, to, counts + warp * p.experts);
+    __syncthreads();
+    // each warp's first place among its expert's rows, and all of an expert's rows
+    for (uint32_t e = t; e < p.experts; e += kRouteThreads) {
+        uint32_t sum = 0, before = 0;
+        if (p.parts)
+            for (uint32_t b = 0; b < gridDim.x; ++b) {
+                if (b == blockIdx.x) before = sum;
+                sum += p.parts[(uint64_t)b * p.experts + e];
+            }
+        for (uint32_t w = 0; w < kRouteWarps; ++w) {
+            const uint32_t n = counts[w * p.experts + e];
+            counts[w * p.experts + e] = before;
+            before += n;
+        }
+        total[e] = p.parts ? sum : before;
+        offset[e] = (total[e] + p.align - 1) / p.align * p.align;
+    }
+    __syncthreads();
+    scan_experts(offset, p.experts, carry);
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (uint32_t e = t; e < p.experts; e += kRouteThreads) {
+            const uint32_t at = min(offset[e], p.max_rows);
+            p.offsets[e] = (int32_t)at;
+            p.counts[e] = (int32_t)min(total[e], p.max_rows - at);
+            if (e + 1 == p.experts)
+                p.offsets[e + 1] = (int32_t)min(offset[e] + (total[e] + p.align - 1) / p.align * p.align, p.max_rows);
+        }
+    uint32_t* mine = counts + warp * p.experts;
+    for (uint64_t i0 = from; i0 < to; i0 += 32) {
+        const uint64_t i = i0 + lane;
+        const uint32_t e = i < to ? expert_of(p, i) : p.experts;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        uint32_t at = p.max_rows;
+        if (e < p.experts) at = offset[e] + mine[e] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (e < p.experts && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+        if (i < to) p.position[i] = at < p.max_rows ? (int32_t)at : -1;
+    }
+}
+
+// ---- rows --------------------------------------------------------------------------------------
+struct Rows {
+    char* at;
+    uint64_t pitch;
+    uint32_t bytes;             // of a row
+};
+
+// What the row kernels know of a sort.
+struct Sorted {
+    const int32_t* position;    // [tokens][k]
+    const int32_t* offsets;
+    const int32_t* counts;
+    uint64_t tokens;
+    uint32_t k, experts, max_rows;
+    uint32_t fills, fill_ctas;  // CTAs of one expert's filled rows, and all of them: the grid's first
+};
+
+__device__ __forceinline__ uint32_t row_of(const Sorted& s, uint64_t pair) { return (uint32_t)s.position[pair]; }   // -1: no row
+
+// Rows from an expert's last to where the next one's begin, zeros: CTA `cta` of fill_ctas.
+template <class W>
+__device__ __forceinline__ void zero_words(char* row, uint32_t bytes) {
+    for (uint32_t i = threadIdx.x; i < bytes / sizeof(W); i += blockDim.x) reinterpret_cast<W*>(row)[i] = W{};
+}
+template <class W>
+__device__ __forceinline__ void fill_rows(const Sorted& s, const Rows& rows, uint32_t cta) {
+    const uint32_t e = cta / s.fills;
+    const uint32_t from = (uint32_t)s.offsets[e] + (uint32_t)s.counts[e] + cta % s.fills * kFillRows;
+    const uint32_t to = min(min((uint32_t)s.offsets[e + 1], s.max_rows), from + kFillRows);
+    for (uint32_t r = from; r < to; ++r) zero_words<W>(rows.at + r * rows.pitch, rows.bytes);
+}
+
+template <class W>
+__device__ __forceinline__ void copy_row(const Sorted& s, const char* from, const Rows& rows, uint64_t token) {
+    for (uint32_t i = threadIdx.x; i < rows.bytes / sizeof(W); i += blockDim.x) {
+        const W v = reinterpret_cast<const W*>(from)[i];
+        for (uint32_t j = 0; j < s.k; ++j) {
+            const uint32_t r = row_of(s, token * s.k + j);
+            if (r < s.max_rows) reinterpret_cast<W*>(rows.at + r * rows.pitch)[i] = v;
+        }
+    }
+}
+
+struct DispatchParams {
+    Sorted s;
+    const char* x;
+    const char* scales;         // or null
+    uint64_t x_pitch, scales_pitch;
+    Rows rows, row_scales;
+};
+
+// W: the word that rows are moved by, SW: their scales.
+template <class W, class SW>
+__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_constant__ DispatchParams p) {
+    launch_next();
+    wait_previous();
+    if (blockIdx.x < p.s.fill_ctas) {
+        fill_rows<W>(p.s, p.rows, blockIdx.x);
+        if (p.scales) fill_rows<SW>(p.s, p.row_scales, blockIdx.x);
+        return;
+    }
+    const uint64_t token = blockIdx.x - p.s.fill_ctas;
+    copy_row<W>(p.s, p.x + token * p.x_pitch, p.rows, token);
+    if (p.scales) copy_row<SW>(p.s, p.scales + token * p.scales_pitch, p.row_scales, token);
+}
+
+struct CombineParams {
+    Sorted s;
+    const char* rows;
+    const float* weights;       // or null
+    char* out;
+    uint64_t rows_pitch, out_pitch;
+    uint32_t cols, rows_dt, out_dt;
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+    launch_next();
+    wait_previous();
+    const uint64_t token = blockIdx.x;
+    for (uint32_t c = 8 * threadIdx.x; c < p.cols; c += 8 * blockDim.x) {
+        float sum[8] = {};
+        for (uint32_t j = 0; j < p.s.k; ++j) {
+            const uint32_t r = row_of(p.s, token * p.s.k + j);
+            if (r >= p.s.max_rows) continue;
+            const float w = p.weights ? p.weights[token * p.s.k + j] : 1.0f;
+            float v[8];
+            load8<VEC>(p.rows + r * p.rows_pitch, p.rows_dt, c, p.cols, v);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+        }
+        store8<VEC>(p.out + token * p.out_pitch, p.out_dt, c, p.cols, sum);
+    }
+}
+
+struct BackwardParams {
+    Sorted s;
+    const char* dout;
+    const char* rows;           // or null: no weights' gradient
+    const float* weights;
+    Rows drows;
+    float* dweights;            // or null
+    uint64_t dout_pitch, rows_pitch;
+    uint32_t cols, dout_dt, rows_dt;
+};
+
+template <bool VEC, class W>
+__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __grid_constant__ BackwardParams p) {
+    launch_next();
+    wait_previous();
+    __shared__ float sums[kRowThreads / 32];
+    if (blockIdx.x < p.s.fill_ctas) return fill_rows<W>(p.s, p.drows, blockIdx.x);
+    const uint64_t token = blockIdx.x - p.s.fill_ctas;
+    for (uint32_t j = 0; j < p.s.k; ++j) {
+        const uint64_t pair = token * p.s.k + j;
+        const uint32_t r = row_of(p.s, pair);
+        float dot = 0.0f;
+        if (r < p.s.max_rows) {
+            const float w = p.weights[pair];
+            for (uint32_t c = 8 * threadIdx.x; c < p.cols; c += 8 * blockDim.x) {
+                float g[8], v[8];
+                load8<VEC>(p.dout + token * p.dout_pitch, p.dout_dt, c, p.cols, g);
+                if (p.dweights) {
+                    load8<VEC>(p.rows + r * p.rows_pitch, p.rows_dt, c, p.cols, v);
+#pragma unroll
+                    for (uint32_t i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) g[i] *= w;
+                store8<VEC>(p.drows.at + r * p.drows.pitch, p.rows_dt, c, p.cols, g);
+            }
+        }
+        if (!p.dweights) continue;
+#pragma unroll
+        for (uint32_t o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (uint32_t i = 1; i < kRowThreads / 32; ++i) dot += sums[i];
+            p.dweights[pair] = dot;
+        }
+        __syncthreads();
+    }
+}
+
+// ---- host --------------------------------------------------------------------------------------
+int check_desc(const char* who, const dtt_experts_desc* d) {
+    if (!d) return fail(DTT_EINVAL, "%s: null desc", who);
+    if (d->experts < 1 || d->experts > kMostExperts) return fail(DTT_EINVAL, "%s: experts must be 1 .. %u", who, kMostExperts);
+    if (d->top_k < 1 || d->top_k > kMostChoices) return fail(DTT_EINVAL, "%s: top_k must be 1 .. %u", who, kMostChoices);
+    if (d->align < 1 || d->align > 65536) return fail(DTT_EINVAL, "%s: align must be 1 .. 65536", who);
+    if (d->first >= 1u << 31) return fail(DTT_EINVAL, "%s: first must be below 2^31", who);
+    return DTT_OK;
+}
+
+int check_sizes(const char* who, const dtt_experts_desc* d, uint64_t tokens, uint64_t max_rows) {
+    const int rc = check_desc(who, d);
+    if (rc) return rc;
+    if (tokens >= (1ull << 31) / d->top_k || tokens * d->top_k + (uint64_t)d->experts * d->align >= 1ull << 31 || max_rows >= 1ull << 31)
+        return fail(DTT_EINVAL, "%s: 2^31 rows or more", who);
+    return DTT_OK;
+}
+
+int check_ptr(const char* who, const char* name, const void* p, uint32_t to, bool optional = false) {
+    if (!p) return optional ? DTT_OK : fail(DTT_EINVAL, "%s: %s is missing", who, name);
+    if (reinterpret_cast<uintptr_t>(p) % to) return fail(DTT_EINVAL, "%s: %s must be aligned to its %u-byte elements", who, name, to);
+    return DTT_OK;
+}
+
+int check_rows(const char* who, const char* name, const void* p, uint64_t pitch, uint64_t rows, uint64_t bytes, uint32_t element, bool optional = false) {
+    const int rc = check_ptr(who, name, p, element, optional);
+    if (rc || !p) return rc;
+    if (pitch % element) return fail(DTT_EINVAL, "%s: %s: the pitch is no multiple of its %u-byte elements", who, name, element);
+    if (rows > 1 && pitch < bytes) return fail(DTT_EINVAL, "%s: %s: the pitch is less than a row", who, name);
+    return DTT_OK;
+}
+
+Sorted sorted_of(const dtt_experts_desc* d, uint64_t tokens, uint64_t max_rows, const int32_t* position, const int32_t* offsets, const int32_t* counts) {
+    Sorted s{position, offsets, counts, tokens, d->top_k, d->experts, (uint32_t)max_rows, 0, 0};
+    if (offsets && d->align > 1) {
+        s.fills = (d->align - 1 + kFillRows - 1) / kFillRows;
+        s.fill_ctas = s.fills * d->experts;
+    }
+    return s;
+}
+
+// The widest word, of 16, 4, 2 and 1 bytes, that every address and length is a multiple of.
+uint32_t word_of(std::initializer_list<uint64_t> all) {
+    uint64_t bits = 0;
+    for (uint64_t a : all) bits |= a;
+    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
+uint64_t bits_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+template <class SW>
+cudaError_t launch_dispatch(uint32_t word, uint32_t grid, cudaStream_t stream, const DispatchParams& p) {
+    auto kernel = word == 16 ? dispatch_kernel<uint4, SW> : word == 4 ? dispatch_kernel<uint32_t, SW> : word == 2 ? dispatch_kernel<uint16_t, SW> : dispatch_kernel<uint8_t, SW>;
+    return launch(kernel, grid, kRowThreads, 0, 0, true, stream, p);
+}
+
+uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : 4; }
+bool aligned(const void* p, uint64_t pitch) { return bits_of(p) % 16 == 0 && pitch % 16 == 0; }
+
+}  // namespace
+
+cudaError_t preload_experts_kernels() {
+    cudaError_t e = cudaSuccess;
+    auto add = [&](auto... kernels) { ((e = e == cudaSuccess ? prepare_kernel(kernels) : e), ...); };
+    add(route_count_kernel, route_place_kernel, dispatch_kernel<uint4, uint4>, dispatch_kernel<uint4, uint32_t>, dispatch_kernel<uint32_t, uint4>,
+        dispatch_kernel<uint32_t, uint32_t>, dispatch_kernel<uint16_t, uint4>, dispatch_kernel<uint16_t, uint32_t>, dispatch_kernel<uint8_t, uint4>,
+        dispatch_kernel<uint8_t, uint32_t>, combine_kernel<true>, combine_kernel<false>, combine_backward_kernel<true, uint4>,
+        combine_backward_kernel<false, uint16_t>);
+    constexpr int most = (kRouteWarps + 2) * kMostExperts * 4;
+    for (auto k : {route_count_kernel, route_place_kernel})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return e;
+}
+
+}  // namespace dtt
+
+using namespace dtt;
+
+extern "C" int dtt_experts_workspace(const dtt_experts_desc* d, uint64_t* bytes) {
+    const char* who = "dtt_experts_workspace";
+    const int rc = check_desc(who, d);
+    if (rc) return rc;
+    if (!bytes) return fail(DTT_EINVAL, "%s: null bytes", who);
+    *bytes = (uint64_t)kMostParts * d->experts * 4;
+    return DTT_OK;
+}
+
+extern "C" int dtt_experts_route(const dtt_experts_desc* d, uint64_t tokens, const void* ids, uint32_t id_bytes, uint64_t max_rows,
+                                 int32_t* position, int32_t* offsets, int32_t* counts, void* workspace, uint64_t workspace_bytes,
+                                 cudaStream_t stream) {
+    const char* who = "dtt_experts_route";
+    int rc = check_sizes(who, d, tokens, max_rows);
+    if (rc) return rc;
+    if (id_bytes != 4 && id_bytes != 8) return fail(DTT_EINVAL, "%s: ids are of 4 or 8 bytes", who);
+    if ((rc = check_ptr(who, "ids", ids, id_bytes, tokens == 0)) || (rc = check_ptr(who, "position", position, 4, tokens == 0)) ||
+        (rc = check_ptr(who, "offsets", offsets, 4)) || (rc = check_ptr(who, "counts", counts, 4)) ||
+        (rc = check_ptr(who, "the workspace", workspace, 16)))
+        return rc;
+    if (workspace_bytes < (uint64_t)kMostParts * d->experts * 4) return fail(DTT_EINVAL, "%s: the workspace is short", who);
+    if ((rc = preload_once())) return rc;
+    RouteParams p{};
+    p.ids = ids;
+    p.position = position;
+    p.offsets = offsets;
+    p.counts = counts;
+    p.pairs = tokens * d->top_k;
+    p.experts = d->experts;
+    p.first = d->first;
+    p.align = d->align;
+    p.max_rows = (uint32_t)max_rows;
+    p.wide = id_bytes == 8;
+    const uint32_t parts = (uint32_t)std::clamp<uint64_t>((p.pairs + kPartPairs - 1) / kPartPairs, 1, kMostParts);
+    p.each = ((p.pairs + parts - 1) / parts + kRouteThreads - 1) / kRouteThreads * kRouteThreads;
+    p.parts = parts > 1 ? static_cast<uint32_t*>(workspace) : nullptr;
+    const uint32_t smem = kRouteWarps * d->experts * 4;
+    cudaError_t e = cudaSuccess;
+    if (parts > 1) e = launch(route_count_kernel, parts, kRouteThreads, smem, 0, true, stream, p);
+    if (e == cudaSuccess) e = launch(route_place_kernel, parts, kRouteThreads, smem + 2 * d->experts * 4, 0, true, stream, p);
+    if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    return DTT_OK;
+}
+
+extern "C" int dtt_experts_dispatch(const dtt_experts_desc* d, uint64_t tokens, const int32_t* position, const int32_t* offsets,
+                                    const int32_t* counts, const void* x, uint64_t x_pitch, uint64_t row_bytes, void* rows,
+                                    uint64_t rows_pitch, uint64_t max_rows, const float* scales, uint64_t scales_pitch,
+                                    uint64_t scale_count, float* row_scales, uint64_t row_scales_pitch, cudaStream_t stream) {
+    const char* who = "dtt_experts_dispatch";
+    int rc = check_sizes(who, d, tokens, max_rows);
+    if (rc) return rc;
+    if (row_bytes < 1 || row_bytes > 1ull << 26 || scale_count > 1ull << 24) return fail(DTT_EINVAL, "%s: a row has 1 .. 2^26 bytes and up to 2^24 scales", who);
+    if ((scales != nullptr) != (row_scales != nullptr) || (scales && !scale_count))
+        return fail(DTT_EINVAL, "%s: scales and row_scales go together, with one scale a row at least", who);
+    if ((rc = check_ptr(who, "position", position, 4, tokens == 0)) || (rc = check_ptr(who, "offsets", offsets, 4)) || (rc = check_ptr(who, "counts", counts, 4)) ||
+        (rc = check_rows(who, "x", x, x_pitch, tokens, row_bytes, 1, tokens == 0)) || (rc = check_rows(who, "rows", rows, rows_pitch, max_rows, row_bytes, 1, max_rows == 0)) ||
+        (rc = check_rows(who, "scales", scales, scales_pitch, tokens, scale_count * 4, 4, true)) ||
+        (rc = check_rows(who, "row_scales", row_scales, row_scales_pitch, max_rows, scale_count * 4, 4, true)))
+        return rc;
+    DispatchParams p{};
+    p.s = sorted_of(d, tokens, max_rows, position, offsets, counts);
+    const uint64_t grid = tokens + p.s.fill_ctas;
+    if (grid == 0 || max_rows == 0) return DTT_OK;
+    if ((rc = preload_once())) return rc;
+    p.x = static_cast<const char*>(x);
+    p.x_pitch = x_pitch;
+    p.rows = Rows{static_cast<char*>(rows), rows_pitch, (uint32_t)row_bytes};
+    p.scales = reinterpret_cast<const char*>(scales);
+    p.scales_pitch = scales_pitch;
+    p.row_scales = Rows{reinterpret_cast<char*>(row_scales), row_scales_pitch, (uint32_t)scale_count * 4};
+    const uint32_t word = word_of({bits_of(x), x_pitch, row_bytes, bits_of(rows), rows_pitch});
+    const bool wide = !scales || word_of({bits_of(scales), scales_pitch, scale_count * 4, bits_of(row_scales), row_scales_pitch}) == 16;
+    const cudaError_t e = wide ? launch_dispatch<uint4>(word, (uint32_t)grid, stream, p) : launch_dispatch<uint32_t>(word, (uint32_t)grid, stream, p);
+    if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    return DTT_OK;
+}
+
+extern "C" int dtt_experts_combine(const dtt_experts_desc* d, uint64_t tokens, uint64_t cols, const int32_t* position, const void* rows,
+                                   uint32_t rows_dtype, uint64_t rows_pitch, uint64_t max_rows, const float* weights, void* out,
+                                   uint32_t out_dtype, uint64_t out_pitch, cudaStream_t stream) {
+    const char* who = "dtt_experts_combine";
+    int rc = check_sizes(who, d, tokens, max_rows);
+    if (rc) return rc;
+    for (uint32_t t : {rows_dtype, out_dtype})
+        if (t != DTT_BF16 && t != DTT_F32) return fail(DTT_EINVAL, "%s: rows and out are bf16 or f32", who);
+    if (cols < 1 || cols > 1ull << 24) return fail(DTT_EINVAL, "%s: cols must be 1 .. 2^24", who);
+    if (tokens == 0) return DTT_OK;
+    const uint32_t re = elem_bytes(rows_dtype), oe = elem_bytes(out_dtype);
+    if ((rc = check_ptr(who, "position", position, 4)) || (rc = check_rows(who, "rows", rows, rows_pitch, max_rows, cols * re, re, max_rows == 0)) ||
+        (rc = check_ptr(who, "weights", weights, 4, true)) || (rc = check_rows(who, "out", out, out_pitch, tokens, cols * oe, oe)))
+        return rc;
+    if ((rc = preload_once())) return rc;
+    CombineParams p{};
+    p.s = sorted_of(d, tokens, max_rows, position, nullptr, nullptr);
+    p.rows = static_cast<const char*>(rows);
+    p.weights = weights;
+    p.out = static_cast<char*>(out);
+    p.rows_pitch = rows_pitch;
+    p.out_pitch = out_pitch;
+    p.cols = (uint32_t)cols;
+    p.rows_dt = rows_dtype;
+    p.out_dt = out_dtype;
+    const bool vec = cols % 8 == 0 && aligned(rows, rows_pitch) && aligned(out, out_pitch);
+    const cudaError_t e = launch(vec ? combine_kernel<true> : combine_kernel<false>, (uint32_t)tokens, kRowThreads, 0, 0, true, stream, p);
+    if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    return DTT_OK;
+}
+
+extern "C" int dtt_experts_combine_backward(const dtt_experts_desc* d, uint64_t tokens, uint64_t cols, const int32_t* position,
+                                            const int32_t* offsets, const int32_t* counts, const void* dout, uint32_t dout_dtype,
+                                            uint64_t dout_pitch, const void* rows, uint32_t rows_dtype, uint64_t rows_pitch,
+                                            uint64_t max_rows, const float* weights, void* drows, uint64_t drows_pitch,
+                                            float* dweights, cudaStream_t stream) {
+    const char* who = "dtt_experts_combine_backward";
+    int rc = check_sizes(who, d, tokens, max_rows);
+    if (rc) return rc;
+    for (uint32_t t : {rows_dtype, dout_dtype})
+        if (t != DTT_BF16 && t != DTT_F32) return fail(DTT_EINVAL, "%s: rows and dout are bf16 or f32", who);
+    if (cols < 1 || cols > 1ull << 24) return fail(DTT_EINVAL, "%s: cols must be 1 .. 2^24", who);
+    const uint32_t re = elem_bytes(rows_dtype), ge = elem_bytes(dout_dtype);
+    if ((rc = check_ptr(who, "position", position, 4, tokens == 0)) || (rc = check_ptr(who, "offsets", offsets, 4)) || (rc = check_ptr(who, "counts", counts, 4)) ||
+        (rc = check_rows(who, "dout", dout, dout_pitch, tokens, cols * ge, ge, tokens == 0)) ||
+        (rc = check_rows(who, "rows", rows, rows_pitch, max_rows, cols * re, re, !dweights || max_rows == 0)) ||
+        (rc = check_ptr(who, "weights", weights, 4, tokens == 0)) || (rc = check_rows(who, "drows", drows, drows_pitch, max_rows, cols * re, re, max_rows == 0)) ||
+        (rc = check_ptr(who, "dweights", dweights, 4, true)))
+        return rc;
+    BackwardParams p{};
+    p.s = sorted_of(d, tokens, max_rows, position, offsets, counts);
+    const uint64_t grid = tokens + p.s.fill_ctas;
+    if (grid == 0) return DTT_OK;
+    if ((rc = preload_once())) return rc;
+    p.dout = static_cast<const char*>(dout);
+    p.rows = static_cast<const char*>(rows);
+    p.weights = weights;
+    p.drows = Rows{static_cast<char*>(drows), drows_pitch, (uint32_t)cols * re};
+    p.dweights = dweights;
+    p.dout_pitch = dout_pitch;
+    p.rows_pitch = rows_pitch;
+    p.cols = (uint32_t)cols;
+    p.dout_dt = dout_dtype;
+    p.rows_dt = rows_dtype;
+    const bool vec = cols % 8 == 0 && aligned(dout, dout_pitch) && aligned(drows, drows_pitch) && (!dweights || aligned(rows, rows_pitch));
+    const cudaError_t e = launch(vec ? combine_backward_kernel<true, uint4> : combine_backward_kernel<false, uint16_t>, (uint32_t)grid, kRowThreads, 0, 0, true, stream, p);
+    if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    return DTT_OK;
+}

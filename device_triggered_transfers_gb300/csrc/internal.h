@@ -267,6 +267,8 @@ cudaError_t preload_barrier_kernels();
 cudaError_t preload_gemm_kernels();
 cudaError_t preload_norm_kernels();
 cudaError_t preload_ortho_kernels();
+cudaError_t preload_adamw_kernels();
+cudaError_t preload_experts_kernels();
 // dtt_preload() for library-internal callers: once per device, then a no-op.
 int preload_once();
 

@@ -1,5 +1,8 @@
-// Residual addition with a root-mean-square norm, and its backward pass (dtt_ops.h).
+// Residual addition with a root-mean-square norm or a layer norm, and their backward passes (dtt_ops.h).
 //
+// Each kernel has both, the layer norm where MEAN: the row's mean comes off first, and its variance is summed over
+// what is left (a mean of squares less the squared mean would lose what the mean is larger than the rest by), so that
+// a row is reduced twice; backward, its two sums go through one reduction, and two gradients add up over the rows.
 // All f32 between the loads and the stores.  The forms of each pass:
 //  - short (256 columns and less, 16-byte aligned, whole chunks of 8 columns): a row by a part of a warp;
 //  - ring (longer rows that two stages in shared memory have room for; rows that are not aligned where there
@@ -29,7 +32,8 @@ constexpr float kScaleMin = 0x1p-100f;     // scale of a group of zeros: its rec
 // columns and less) have several in a CTA: 20000 x 256 25 us with sixteen CTAs a SM, 20 with four.
 __host__ __device__ constexpr uint32_t most_partials(uint64_t cols) { return (cols > 1024 || cols <= 256 ? 4 : cols > 512 ? 8 : 16) * kSms; }
 constexpr uint32_t kFwdThreads = 1024, kBwdThreads = 512, kRingThreads = ring::kThreads;   // a row's most threads
-constexpr uint32_t kFwdOwn = 640, kBwdOwn = 2432;    // shared memory of a ring's CTA beside its stages, at most
+template <bool MEAN> constexpr uint32_t kFwdOwn = MEAN ? 896 : 640;      // shared memory of a ring's CTA beside its stages, at most
+template <bool MEAN> constexpr uint32_t kBwdOwn = MEAN ? 4736 : 2432;
 constexpr uint32_t kWaitLimit = 1u << 18;      // looks at an mbarrier; one that fails takes 4 us: a second
 // Whether row r of a ring does not arrive for thread t in time: a build of its own shows what becomes of such rows.
 #ifndef DTT_NORM_ROW_LATE
@@ -47,9 +51,11 @@ struct FwdParams {
     const char* x;
     const char* res;            // or null
     const char* w;              // or null
+    const char* b;              // layer norm: or null
     char* res_out;              // or null
     char* y;
     float* scales;
+    float* mean;                // layer norm: or null
     float* rstd;                // or null
     uint64_t x_pitch, res_pitch, res_out_pitch, y_pitch;
     uint64_t rows;
@@ -63,11 +69,14 @@ struct BwdParams {
     const char* dy;
     const char* h;
     const char* w;              // or null
+    const float* mean;          // layer norm
     const float* rstd;
     const char* dres;           // or null
     char* dx;
     float* partial;             // [partials][cols], or null: no weight gradient, or few rows
+    float* partial_b;           // layer norm: the same of the bias's gradient, or null
     float* dweight;             // few rows: the CTAs after the first `partials` work it out; else null
+    float* dbias;               // the same
     uint64_t dy_pitch, h_pitch, dres_pitch, dx_pitch;
     uint64_t rows;
     uint32_t cols, partials, walkers;   // walker i takes rows i, i + walkers, ...
@@ -114,6 +123,38 @@ __device__ __forceinline__ float row_sum(float v, uint32_t tpr, float* slot) {
     return v;
 }
 
+// Two sums with one barrier; slot: 64 words.
+__device__ __forceinline__ float2 row_sum2(float a, float b, uint32_t tpr, float* slot) {
+#pragma unroll
+    for (uint32_t o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    if (tpr == 32) return {a, b};
+    const uint32_t lane = threadIdx.x % 32;
+    if (lane == 0) {
+        slot[threadIdx.x / 32] = a;
+        slot[32 + threadIdx.x / 32] = b;
+    }
+    __syncthreads();
+    a = lane < tpr / 32 ? slot[lane] : 0.0f;
+    b = lane < tpr / 32 ? slot[32 + lane] : 0.0f;
+#pragma unroll
+    for (uint32_t o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    return {a, b};
+}
+
+// A row's means of g n and, for the layer norm, of g.
+template <bool MEAN>
+__device__ __forceinline__ float2 row_means(float dot, float all, uint32_t tpr, float* slot, float inv_cols) {
+    if constexpr (!MEAN) return {row_sum(dot, tpr, slot) * inv_cols, 0.0f};
+    const float2 sums = row_sum2(dot, all, tpr, slot);
+    return {sums.x * inv_cols, sums.y * inv_cols};
+}
+
 // The largest of magnitudes, NaN if one is: as bits, magnitudes order like integers, with NaN on top.
 __device__ __forceinline__ float warp_max(float v) {
     return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
@@ -130,11 +171,11 @@ __device__ __forceinline__ float row_max(float v, uint32_t tpr, float* slot) {
 
 // One row a CTA.  NCH chunks a thread stay in registers; kLong reads the row again for each pass over it.
 // 2000 x 32768 in bf16: 141 us, 0.55 of the copy rate; loads that wait for one another bound it.
-template <uint32_t NCH, bool VEC>
-__global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_constant__ FwdParams p) {
+template <bool MEAN, uint32_t NCH, bool VEC>
+__global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(const __grid_constant__ FwdParams p) {
     launch_next();
     wait_previous();
-    __shared__ float slots[2][32];
+    __shared__ float slots[MEAN ? 3 : 2][32];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
     const uint64_t r = blockIdx.x;
     const char* x = p.x + r * p.x_pitch;
@@ -160,12 +201,31 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
 #pragma unroll
         for (uint32_t i = 0; i < HELD; ++i) load(i, h[i]);
     }
+    float mu = 0.0f;
+    if constexpr (MEAN) {
+#pragma unroll HELD
+        for (uint32_t i = 0; i < nch; ++i) {
+            float (&v)[8] = h[NCH == kLong ? 0 : i];
+            if (NCH == kLong) load(i, v);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) mu += v[k];
+        }
+        mu = row_sum(mu, tpr, slots[2]) * p.inv_cols;
+        if (t == 0 && p.mean) p.mean[r] = mu;
+    }
 #pragma unroll HELD
     for (uint32_t i = 0; i < nch; ++i) {
         float (&v)[8] = h[NCH == kLong ? 0 : i];
         if (NCH == kLong) load(i, v);
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) sum += v[k] * v[k];
+        for (uint32_t k = 0; k < 8; ++k) {
+            if (MEAN) {
+                const float d = 8 * (i * tpr + t) + k < p.cols ? v[k] - mu : 0.0f;
+                sum += d * d;
+            } else {
+                sum += v[k] * v[k];
+            }
+        }
     }
     const float s = rsqrtf(row_sum(sum, tpr, slots[0]) * p.inv_cols + p.eps);
     if (t == 0 && p.rstd) p.rstd[r] = s;
@@ -173,8 +233,19 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
     auto normed = [&](uint32_t i, const float (&v)[8], float (&o)[8]) {
         const uint32_t c = 8 * (i * tpr + t);
         if (p.w) load8<VEC>(p.w, p.w_dt, c, p.cols, o);
+        if constexpr (MEAN) {
+            float q[8];
+            if (p.b) load8<VEC>(p.b, p.w_dt, c, p.cols, q);
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) o[k] = p.w ? v[k] * s * o[k] : v[k] * s;
+            for (uint32_t k = 0; k < 8; ++k) {
+                const float n = c + k < p.cols ? (v[k] - mu) * s : 0.0f;
+                o[k] = p.w ? n * o[k] : n;
+                if (p.b) o[k] += q[k];
+            }
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) o[k] = p.w ? v[k] * s * o[k] : v[k] * s;
+        }
     };
     auto amax8 = [&](const float (&o)[8]) {
         float m = 0.0f;
@@ -224,8 +295,9 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_kernel(const __grid_c
 
 // The weight's gradient where there are few rows: it does not wait for the rows' means, so that CTAs of the same
 // launch add it up, 32 columns at a time, a warp every `warps`-th row, the warps' sums in their order.
+template <bool MEAN>
 __device__ __forceinline__ void weight_columns(const BwdParams& p) {
-    __shared__ float sums[kBwdThreads / 32][32];
+    __shared__ float sums[MEAN ? 2 : 1][kBwdThreads / 32][32];
     constexpr uint32_t N = 4;
     wait_previous();
     const uint32_t t = threadIdx.y * blockDim.x + threadIdx.x, lane = t % 32, warp = t / 32, warps = blockDim.x * blockDim.y / 32;
@@ -234,28 +306,37 @@ __device__ __forceinline__ void weight_columns(const BwdParams& p) {
         uint32_t cs[N];
 #pragma unroll
         for (uint32_t n = 0; n < N; ++n) cs[n] = min(c, p.cols - 1);
-        float v = 0.0f;
+        float v = 0.0f, u = 0.0f;
         for (uint64_t r0 = warp; r0 < p.rows; r0 += N * warps) {
             const char *gs[N], *hs[N];
-            float g[N], h[N], s[N];
+            float g[N], h[N], s[N], mu[N];
 #pragma unroll
             for (uint32_t n = 0; n < N; ++n) {
                 const uint64_t r = min(r0 + n * warps, p.rows - 1);
                 gs[n] = p.dy + r * p.dy_pitch;
                 hs[n] = p.h + r * p.h_pitch;
                 s[n] = p.rstd[r];
+                if (MEAN) mu[n] = p.mean[r];
             }
             gather(gs, p.dy_dt, cs, g);
             gather(hs, p.h_dt, cs, h);
 #pragma unroll
             for (uint32_t n = 0; n < N; ++n)
-                if (r0 + n * warps < p.rows) v += g[n] * (h[n] * s[n]);
+                if (r0 + n * warps < p.rows) {
+                    v += g[n] * ((MEAN ? h[n] - mu[n] : h[n]) * s[n]);
+                    if (MEAN) u += g[n];
+                }
         }
-        sums[warp][lane] = v;
+        sums[0][warp][lane] = v;
+        if (MEAN) sums[MEAN][warp][lane] = u;
         __syncthreads();
         if (warp == 0) {
-            for (uint32_t i = 1; i < warps; ++i) v += sums[i][lane];
-            if (c < p.cols) p.dweight[c] = v;
+            for (uint32_t i = 1; i < warps; ++i) {
+                v += sums[0][i][lane];
+                if (MEAN) u += sums[MEAN][i][lane];
+            }
+            if (c < p.cols && (!MEAN || p.dweight)) p.dweight[c] = v;
+            if (MEAN && c < p.cols && p.dbias) p.dbias[c] = u;
         }
         __syncthreads();
     }
@@ -266,16 +347,18 @@ __device__ __forceinline__ void weight_columns(const BwdParams& p) {
 // thread's loads all go out before the first value is used, and many CTAs hide them: with two or four rows a
 // thread under way the forward pass of 300000 x 128 (bf16 to 8 bits) took 58 and 82 us where one took 57.
 // Behind another call it takes 59 (bf16 52), 0.67 (0.88) of the copy rate; the exact quotients are 2 us of it.
-__global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_constant__ FwdParams p, uint32_t lanes) {
+template <bool MEAN>
+__global__ void __launch_bounds__(256) norm_fwd_short_kernel(const __grid_constant__ FwdParams p, uint32_t lanes) {
     launch_next();
     wait_previous();
     const uint32_t t = threadIdx.x, l = t & (lanes - 1), c = 8 * l;
     const uint64_t r = (uint64_t)blockIdx.x * (256 / lanes) + t / lanes, row = min(r, p.rows - 1);
     const bool in = c < p.cols, mine = in && r < p.rows;
     const uint32_t from = in ? c : 0;               // the lanes past the row read its first chunk
-    Raw8 xs = raw8(p.x + row * p.x_pitch + from * (p.x_dt == DTT_BF16 ? 2 : 4), p.x_dt), qs{}, ws{};
+    Raw8 xs = raw8(p.x + row * p.x_pitch + from * (p.x_dt == DTT_BF16 ? 2 : 4), p.x_dt), qs{}, ws{}, bs{};
     if (p.res) qs = raw8(p.res + row * p.res_pitch + from * (p.res_dt == DTT_BF16 ? 2 : 4), p.res_dt);
     if (p.w) ws = raw8(p.w + from * (p.w_dt == DTT_BF16 ? 2 : 4), p.w_dt);
+    if (MEAN && p.b) bs = raw8(p.b + from * (p.w_dt == DTT_BF16 ? 2 : 4), p.w_dt);
     float h[8], o[8], sum = 0.0f;
     expand8(xs, p.x_dt, h);
     if (p.res) {
@@ -283,19 +366,31 @@ __global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_con
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) h[k] += o[k];
     }
+    float mu = 0.0f;
+    if constexpr (MEAN) {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) mu += in ? h[k] : 0.0f;
+        for (uint32_t d = lanes / 2; d > 0; d /= 2) mu += __shfl_xor_sync(0xFFFFFFFFu, mu, d);
+        mu *= p.inv_cols;
+        if (mine && l == 0 && p.mean) p.mean[r] = mu;
+    }
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
-        if (!in) h[k] = 0.0f;
-        sum += h[k] * h[k];
+        if (!in) h[k] = mu;
+        if (MEAN) sum += (h[k] - mu) * (h[k] - mu);
+        else sum += h[k] * h[k];
     }
     for (uint32_t d = lanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     const float s = rsqrtf(sum * p.inv_cols + p.eps);
     if (mine && l == 0 && p.rstd) p.rstd[r] = s;
     if (p.w) expand8(ws, p.w_dt, o);
-    float m = 0.0f;
+    float m = 0.0f, q[8];
+    if (MEAN && p.b) expand8(bs, p.w_dt, q);
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
-        o[k] = p.w ? h[k] * s * o[k] : h[k] * s;
+        const float n = MEAN ? h[k] - mu : h[k];
+        o[k] = p.w ? n * s * o[k] : n * s;
+        if (MEAN && p.b) o[k] += q[k];
         m = max_nan(m, fabsf(o[k]));
     }
     if (p.y_dt == DTT_E4M3) {
@@ -316,19 +411,20 @@ __global__ void __launch_bounds__(256) rmsnorm_fwd_short_kernel(const __grid_con
 // The same split; a CTA walks over rows, each thread at the same columns, whose part of the weight's gradient
 // adds up in its registers; at the end the CTA's rows' sums, in their order, become its partial row.
 // 300000 x 128 in bf16: 62 us, 0.73 of the copy rate.
-__global__ void __launch_bounds__(256, 4) rmsnorm_bwd_short_kernel(const __grid_constant__ BwdParams p, uint32_t lanes) {
+template <bool MEAN>
+__global__ void __launch_bounds__(256, 4) norm_bwd_short_kernel(const __grid_constant__ BwdParams p, uint32_t lanes) {
     launch_next();
-    if (blockIdx.x >= p.partials) return weight_columns(p);
+    if (blockIdx.x >= p.partials) return weight_columns<MEAN>(p);
     wait_previous();
-    __shared__ float sums[256 * 8];
+    __shared__ float sums[(MEAN ? 2 : 1) * 256 * 8];
     const uint32_t t = threadIdx.x, l = t & (lanes - 1), c = 8 * l, at_a_time = 256 / lanes;
     const bool in = c < p.cols;
     const uint32_t from = in ? c : 0, ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
-    float w[8], acc[8];
+    float w[8], acc[8], acc_b[8];
     if (p.w) expand8(raw8(p.w + from * (p.w_dt == DTT_BF16 ? 2 : 4), p.w_dt), p.w_dt, w);
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
-        acc[k] = 0.0f;
+        acc[k] = acc_b[k] = 0.0f;
         if (!p.w) w[k] = 1.0f;
     }
     for (uint64_t r0 = (uint64_t)blockIdx.x * at_a_time; r0 < p.rows; r0 += (uint64_t)p.partials * at_a_time) {
@@ -337,21 +433,26 @@ __global__ void __launch_bounds__(256, 4) rmsnorm_bwd_short_kernel(const __grid_
         const Raw8 gs = raw8(p.dy + row * p.dy_pitch + from * ge, p.dy_dt), hs = raw8(p.h + row * p.h_pitch + from * he, p.h_dt);
         Raw8 ds{};
         if (p.dres) ds = raw8(p.dres + row * p.dres_pitch + from * he, p.h_dt);
-        const float s = p.rstd[row];
-        float g[8], n[8], dot = 0.0f;
+        const float s = p.rstd[row], mu = MEAN ? p.mean[row] : 0.0f;
+        float g[8], n[8], dot = 0.0f, all = 0.0f;
         expand8(gs, p.dy_dt, g);
         expand8(hs, p.h_dt, n);
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) {
-            n[k] *= s;
+            n[k] = (MEAN ? n[k] - mu : n[k]) * s;
             if (mine) acc[k] += g[k] * n[k];
+            if (MEAN && mine) acc_b[k] += g[k];
             g[k] *= w[k];
             if (in) dot += g[k] * n[k];
+            if (MEAN && in) all += g[k];
         }
-        for (uint32_t d = lanes / 2; d > 0; d /= 2) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-        const float m = dot * p.inv_cols;
+        for (uint32_t d = lanes / 2; d > 0; d /= 2) {
+            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+            if (MEAN) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+        }
+        const float m = dot * p.inv_cols, a = all * p.inv_cols;
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) g[k] = s * (g[k] - n[k] * m);
+        for (uint32_t k = 0; k < 8; ++k) g[k] = s * ((MEAN ? g[k] - a : g[k]) - n[k] * m);
         if (p.dres) {
             expand8(ds, p.h_dt, n);
 #pragma unroll
@@ -361,34 +462,42 @@ __global__ void __launch_bounds__(256, 4) rmsnorm_bwd_short_kernel(const __grid_
     }
     if (!p.partial) return;
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) sums[8 * t + k] = acc[k];     // 256 / lanes rows of 8 lanes columns
+    for (uint32_t k = 0; k < 8; ++k) {                              // 256 / lanes rows of 8 lanes columns
+        sums[8 * t + k] = acc[k];
+        if (MEAN) sums[MEAN * 256 * 8 + 8 * t + k] = acc_b[k];
+    }
     __syncthreads();
     if (t < p.cols) {
-        float v = 0.0f;
-        for (uint32_t i = 0; i < at_a_time; ++i) v += sums[i * 8 * lanes + t];
+        float v = 0.0f, u = 0.0f;
+        for (uint32_t i = 0; i < at_a_time; ++i) {
+            v += sums[i * 8 * lanes + t];
+            if (MEAN) u += sums[MEAN * 256 * 8 + i * 8 * lanes + t];
+        }
         p.partial[(uint64_t)blockIdx.x * p.cols + t] = v;
+        if (MEAN) p.partial_b[(uint64_t)blockIdx.x * p.cols + t] = u;
     }
 }
 
 // A CTA walks over rows: each thread keeps the same columns for all of them, so the weight's gradient adds up
 // in its registers and is written once, as the CTA's partial row (kLong: in the partial row itself).
 // 2000 x 16384 in f32: 173 us, 0.45 of the copy rate, bound as the forward pass.
-template <uint32_t NCH, bool VEC>
-__global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_constant__ BwdParams p) {
+template <bool MEAN, uint32_t NCH, bool VEC>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
-    if (blockIdx.x >= p.partials) return weight_columns(p);
+    if (blockIdx.x >= p.partials) return weight_columns<MEAN>(p);
     wait_previous();
-    __shared__ float slots[2][32];
+    __shared__ float slots[2][64];
     const uint32_t tpr = blockDim.x, t = threadIdx.x;
     const uint32_t me = blockIdx.x;
     constexpr uint32_t HELD = NCH == kLong ? 1 : NCH;
     const uint32_t nch = NCH == kLong ? (p.cols + 8 * tpr - 1) / (8 * tpr) : NCH;
-    float acc[HELD][8];
+    float acc[HELD][8], acc_b[HELD][8];
 #pragma unroll
     for (uint32_t i = 0; i < HELD; ++i)
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) acc[i][k] = 0.0f;
+        for (uint32_t k = 0; k < 8; ++k) acc[i][k] = acc_b[i][k] = 0.0f;
     float* part = p.partial ? p.partial + (uint64_t)blockIdx.x * p.cols : nullptr;
+    float* part_b = MEAN && p.partial ? p.partial_b + (uint64_t)blockIdx.x * p.cols : nullptr;
 
     uint32_t turn = 0;
     for (uint64_t r = me; r < p.rows; r += p.walkers, turn ^= 1) {
@@ -396,20 +505,20 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_c
         const char* hr = p.h + r * p.h_pitch;
         const char* dresr = p.dres ? p.dres + r * p.dres_pitch : nullptr;
         char* dxr = p.dx + r * p.dx_pitch;
-        const float s = p.rstd[r];
-        float g[HELD][8], n[HELD][8];               // dy, h rstd
+        const float s = p.rstd[r], mu = MEAN ? p.mean[r] : 0.0f;
+        float g[HELD][8], n[HELD][8];               // dy, the normed row
         auto load = [&](uint32_t i, float (&gv)[8], float (&nv)[8]) {
             const uint32_t c = 8 * (i * tpr + t);
             load8<VEC>(dyr, p.dy_dt, c, p.cols, gv);
             load8<VEC>(hr, p.h_dt, c, p.cols, nv);
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) nv[k] *= s;
+            for (uint32_t k = 0; k < 8; ++k) nv[k] = (MEAN ? nv[k] - mu : nv[k]) * s;
         };
         if constexpr (NCH != kLong) {
 #pragma unroll
             for (uint32_t i = 0; i < HELD; ++i) load(i, g[i], n[i]);
         }
-        float dot = 0.0f;
+        float dot = 0.0f, all = 0.0f;
 #pragma unroll HELD
         for (uint32_t i = 0; i < nch; ++i) {
             const uint32_t j = NCH == kLong ? 0 : i, c = 8 * (i * tpr + t);
@@ -417,10 +526,13 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_c
             if (part) {
 #pragma unroll
                 for (uint32_t k = 0; k < 8; ++k) {
-                    if (NCH != kLong)
+                    if (NCH != kLong) {
                         acc[j][k] += g[j][k] * n[j][k];
-                    else if (c + k < p.cols)
+                        if (MEAN) acc_b[j][k] += g[j][k];
+                    } else if (c + k < p.cols) {
                         part[c + k] = (r == me ? 0.0f : part[c + k]) + g[j][k] * n[j][k];
+                        if (MEAN) part_b[c + k] = (r == me ? 0.0f : part_b[c + k]) + g[j][k];
+                    }
                 }
             }
             if (p.w) {
@@ -430,9 +542,13 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_c
                 for (uint32_t k = 0; k < 8; ++k) g[j][k] *= w[k];
             }
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) dot += g[j][k] * n[j][k];
+            for (uint32_t k = 0; k < 8; ++k) {
+                dot += g[j][k] * n[j][k];
+                if (MEAN) all += g[j][k];
+            }
         }
-        const float m = row_sum(dot, tpr, slots[turn]) * p.inv_cols;
+        const float2 means = row_means<MEAN>(dot, all, tpr, slots[turn], p.inv_cols);
+        const float m = means.x, a = means.y;
 #pragma unroll HELD
         for (uint32_t i = 0; i < nch; ++i) {
             const uint32_t j = NCH == kLong ? 0 : i, c = 8 * (i * tpr + t);
@@ -447,7 +563,7 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_c
             }
             float o[8];
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) o[k] = s * (g[j][k] - n[j][k] * m);
+            for (uint32_t k = 0; k < 8; ++k) o[k] = s * ((MEAN ? g[j][k] - a : g[j][k]) - n[j][k] * m);
             if (dresr) {
                 float q[8];
                 load8<VEC>(dresr, p.h_dt, c, p.cols, q);
@@ -464,6 +580,7 @@ __global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_kernel(const __grid_c
             for (uint32_t k = 0; k < 8; ++k) {
                 const uint32_t c = 8 * (i * tpr + t) + k;
                 if (c < p.cols) part[c] = acc[i][k];
+                if (MEAN && c < p.cols) part_b[c] = acc_b[i][k];
             }
     }
 }
@@ -578,15 +695,24 @@ __device__ __forceinline__ void scale_elements(const FwdParams& p, uint64_t r, f
     }
 }
 
-// A row a CTA, or a warp (blockDim.y of them).  600 x 3001 in bf16: 5.7 us back to back, the loads' latency.
+// The thread's columns past the row take its mean: they are zero once it comes off.
 template <uint32_t E>
-__global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const __grid_constant__ FwdParams p) {
+__device__ __forceinline__ void centre(float (&v)[E], float mu, uint32_t cols) {
+    if (whole_warp<E>(cols)) return;
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k)
+        if (column_of<E>(k) >= cols) v[k] = mu;
+}
+
+// A row a CTA, or a warp (blockDim.y of them).  600 x 3001 in bf16: 5.7 us back to back, the loads' latency.
+template <bool MEAN, uint32_t E>
+__global__ void __launch_bounds__(kFwdThreads) norm_fwd_elements_kernel(const __grid_constant__ FwdParams p) {
     launch_next();
     wait_previous();
-    __shared__ float slots[2][32];
+    __shared__ float slots[MEAN ? 3 : 2][32];
     const uint64_t r = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (r >= p.rows) return;                        // a whole warp: rows share no barrier
-    float h[E], o[E];
+    float h[E], o[E], b[E], mu = 0.0f;
     load_elements(p.x + r * p.x_pitch, p.x_dt, p.cols, h);
     if (p.res) {
         load_elements(p.res + r * p.res_pitch, p.res_dt, p.cols, o);
@@ -594,14 +720,26 @@ __global__ void __launch_bounds__(kFwdThreads) rmsnorm_fwd_elements_kernel(const
         for (uint32_t k = 0; k < E; ++k) h[k] += o[k];
     }
     if (p.w) load_elements(p.w, p.w_dt, p.cols, o);
+    if (MEAN && p.b) load_elements(p.b, p.w_dt, p.cols, b);
+    if constexpr (MEAN) {
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) mu += h[k];
+        mu = row_sum(mu, blockDim.x, slots[2]) * p.inv_cols;
+        if (threadIdx.x == 0 && p.mean) p.mean[r] = mu;
+        centre(h, mu, p.cols);
+    }
     float sum = 0.0f;
 #pragma unroll
-    for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
+    for (uint32_t k = 0; k < E; ++k) sum += MEAN ? (h[k] - mu) * (h[k] - mu) : h[k] * h[k];
     const float s = rsqrtf(row_sum(sum, blockDim.x, slots[0]) * p.inv_cols + p.eps);
     if (threadIdx.x == 0 && p.rstd) p.rstd[r] = s;
     if (p.res_out) store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
 #pragma unroll
-    for (uint32_t k = 0; k < E; ++k) h[k] = p.w ? h[k] * s * o[k] : h[k] * s;
+    for (uint32_t k = 0; k < E; ++k) {
+        if (MEAN) h[k] -= mu;
+        h[k] = p.w ? h[k] * s * o[k] : h[k] * s;
+        if (MEAN && p.b) h[k] += b[k];
+    }
     if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[1], h);
     store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
 }
@@ -620,53 +758,63 @@ __device__ __forceinline__ void add_warps(const float (&sums)[kWarpRows][N], flo
 
 // As the chunk form: a CTA or a warp walks over rows, the weight's gradient in its registers.  100 x 1021 in bf16:
 // 5 us back to back with the sum of the partial rows; 300000 x 101 167 us, 0.21 of the copy rate, a 2-byte element a lane.
-template <uint32_t E>
-__global__ void __launch_bounds__(kBwdThreads) rmsnorm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
+template <bool MEAN, uint32_t E>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_elements_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
-    if (blockIdx.x >= p.partials) return weight_columns(p);
+    if (blockIdx.x >= p.partials) return weight_columns<MEAN>(p);
     wait_previous();
-    __shared__ float slots[2][32];
+    __shared__ float slots[2][64];
     __shared__ float sums[kWarpRows][32 * E];
     const uint32_t T = blockDim.x;
-    float acc[E], w[E];
+    float acc[E], acc_b[E], w[E];
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) {
-        acc[k] = 0.0f;
+        acc[k] = acc_b[k] = 0.0f;
         w[k] = 1.0f;
     }
     if (p.w) load_elements(p.w, p.w_dt, p.cols, w);
     uint32_t turn = 0;
     for (uint64_t r = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y; r < p.rows; r += p.walkers, turn ^= 1) {
-        const float s = p.rstd[r];
+        const float s = p.rstd[r], mu = MEAN ? p.mean[r] : 0.0f;
         float g[E], n[E], q[E];
         load_elements(p.dy + r * p.dy_pitch, p.dy_dt, p.cols, g);
         load_elements(p.h + r * p.h_pitch, p.h_dt, p.cols, n);
         if (p.dres) load_elements(p.dres + r * p.dres_pitch, p.h_dt, p.cols, q);
-        float dot = 0.0f;
+        float dot = 0.0f, all = 0.0f;
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) {
-            n[k] *= s;
+            n[k] = (MEAN ? n[k] - mu : n[k]) * s;
             acc[k] += g[k] * n[k];
+            if (MEAN) acc_b[k] += g[k];
             g[k] *= w[k];
             dot += g[k] * n[k];
+            if (MEAN) all += g[k];
         }
-        const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
+        const float2 means = row_means<MEAN>(dot, all, T, slots[turn], p.inv_cols);
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) {
-            g[k] = s * (g[k] - n[k] * m);
+            g[k] = s * ((MEAN ? g[k] - means.y : g[k]) - n[k] * means.x);
             if (p.dres) g[k] += q[k];
         }
         store_elements(p.dx + r * p.dx_pitch, p.h_dt, p.cols, g);
     }
     if (!p.partial) return;
     float* part = p.partial + (uint64_t)blockIdx.x * p.cols;
+    float* part_b = MEAN ? p.partial_b + (uint64_t)blockIdx.x * p.cols : nullptr;
     if (blockDim.y == 1) {
         store_elements(reinterpret_cast<char*>(part), DTT_F32, p.cols, acc);
+        if (MEAN) store_elements(reinterpret_cast<char*>(part_b), DTT_F32, p.cols, acc_b);
         return;
     }
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) sums[threadIdx.y][32 * k + threadIdx.x] = acc[k];
     add_warps(sums, part, p.cols);
+    if (MEAN) {
+        __syncthreads();
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) sums[threadIdx.y][32 * k + threadIdx.x] = acc_b[k];
+        add_warps(sums, part_b, p.cols);
+    }
 }
 
 // ---- ring --------------------------------------------------------------------------------------
@@ -710,11 +858,11 @@ __device__ __forceinline__ void make_nan(float (&v)[N]) {
 // residual.  Thread 0 starts the copies of turn i + S - 1 once turn i's reduction has passed its
 // barrier: every thread is then done with that stage's last row (turn i - 1).  16384 x 4096 (bf16 to 8 bits,
 // groups of 128): 79 us, 0.88 of the copy rate, the issue slots 73 % full.
-template <uint32_t NCH>
-__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+template <bool MEAN, uint32_t NCH>
+__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) norm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
     launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
-    __shared__ float slots[2][2][32];
+    __shared__ float slots[2][MEAN ? 3 : 2][32];
     __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
@@ -739,11 +887,14 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
     wait_previous();
     if (t == 0)
         for (uint32_t i = 0; i + 1 < S; ++i) start();
-    float w[NCH][8];
+    float w[NCH][8], b[MEAN ? NCH : 1][8];
 #pragma unroll
     for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) w[i][k] = 1.0f;
+        for (uint32_t k = 0; k < 8; ++k) {
+            w[i][k] = 1.0f;
+            if (MEAN) b[i][k] = 0.0f;
+        }
     if (p.w) {
         Raw8 ws[NCH];
 #pragma unroll
@@ -753,6 +904,10 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
         }
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) expand8(ws[i], p.w_dt, w[i]);
+    }
+    if (MEAN && p.b) {
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) load8<true>(p.b, p.w_dt, 8 * (i * T + t), p.cols, b[i]);
     }
     __syncthreads();
 
@@ -774,10 +929,27 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
                 for (uint32_t k = 0; k < 8; ++k) h[i][k] += q[k];
             }
         }
+        float mu = 0.0f;
+        if constexpr (MEAN) {
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k) mu += h[i][k];
+            if (lost) mu = kNan;
+            mu = row_sum(mu, T, slots[turn][2]) * p.inv_cols;
+            if (t == 0 && p.mean) p.mean[r] = mu;
+        }
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) sum += h[i][k] * h[i][k];
+            for (uint32_t k = 0; k < 8; ++k) {
+                if (MEAN) {
+                    if (8 * (i * T + t) >= p.cols) h[i][k] = mu;
+                    sum += (h[i][k] - mu) * (h[i][k] - mu);
+                } else {
+                    sum += h[i][k] * h[i][k];
+                }
+            }
         if (lost) sum = kNan;
         const float s = rsqrtf(row_sum(sum, T, slots[turn][0]) * p.inv_cols + p.eps);
         if (t == 0) {
@@ -794,7 +966,11 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) h[i][k] = h[i][k] * s * w[i][k];      // s w alone may overflow
+            for (uint32_t k = 0; k < 8; ++k) {
+                if (MEAN) h[i][k] -= mu;
+                h[i][k] = h[i][k] * s * w[i][k];                                   // s w alone may overflow
+                if (MEAN) h[i][k] += b[i][k];
+            }
         if (p.y_dt == DTT_E4M3) {
             float m[NCH];
 #pragma unroll
@@ -839,12 +1015,12 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
 // to hide, so rstd is read a turn ahead and a thread's loads from the stage go out together: 16384 x 8064 in
 // bf16 153 us and not 201.  16384 x 4096 83 us with the weight's gradient, 0.95 of the copy rate; 2048 x 4096
 // 18.6 us, 0.53: seven rows a CTA, then the sum of the partial rows.
-template <uint32_t NCH>
-__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 1) rmsnorm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+template <bool MEAN, uint32_t NCH>
+__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 1) norm_bwd_ring_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
-    if (blockIdx.x >= p.partials) return weight_columns(p);
+    if (blockIdx.x >= p.partials) return weight_columns<MEAN>(p);
     extern __shared__ __align__(128) uint8_t stages[];
-    __shared__ float slots[2][32];
+    __shared__ float slots[2][MEAN ? 64 : 32];
     __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
@@ -870,13 +1046,14 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
     wait_previous();
     if (t == 0)
         for (uint32_t i = 0; i + 1 < S; ++i) start();
-    float w[NCH][8], acc[NCH][8];
+    float w[NCH][8], acc[NCH][8], acc_b[MEAN ? NCH : 1][8];
 #pragma unroll
     for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) {
             w[i][k] = 1.0f;
             acc[i][k] = 0.0f;
+            if (MEAN) acc_b[i][k] = 0.0f;
         }
     if (p.w) {
         Raw8 ws[NCH];
@@ -893,13 +1070,16 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
     uint32_t st = 0, phase = 0;
     uint32_t turn = 0;
     bool lost = false;
-    float s_next = p.rstd[blockIdx.x];              // a turn ahead of its use
+    float s_next = p.rstd[blockIdx.x], mu_next = MEAN ? p.mean[blockIdx.x] : 0.0f;      // a turn ahead of their use
     for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
-        const float s = s_next;
-        if (r + p.partials < p.rows) s_next = p.rstd[r + p.partials];
+        const float s = s_next, mu = mu_next;
+        if (r + p.partials < p.rows) {
+            s_next = p.rstd[r + p.partials];
+            if (MEAN) mu_next = p.mean[r + p.partials];
+        }
         lost = lost || DTT_NORM_ROW_LATE || !bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
-        float g[NCH][8], n[NCH][8], dot = 0.0f;
+        float g[NCH][8], n[NCH][8], dot = 0.0f, all = 0.0f;
         constexpr uint32_t G = NCH > 2 ? 1 : NCH;   // chunks whose loads go out together: what the registers allow
 #pragma unroll
         for (uint32_t i0 = 0; i0 < NCH; i0 += G) {
@@ -919,22 +1099,25 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
 #pragma unroll
                 for (uint32_t k = 0; k < 8; ++k) {
                     gi[k] = in ? gi[k] : 0.0f;
-                    ni[k] = in ? ni[k] * s : 0.0f;
+                    ni[k] = in ? (MEAN ? ni[k] - mu : ni[k]) * s : 0.0f;
                     acc[i0 + i][k] += gi[k] * ni[k];
+                    if (MEAN) acc_b[i0 + i][k] += gi[k];
                     gi[k] *= w[i0 + i][k];
                     dot += gi[k] * ni[k];
+                    if (MEAN) all += gi[k];
                 }
             }
         }
         if (lost) dot = kNan;
-        const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
+        const float2 means = row_means<MEAN>(dot, all, T, slots[turn], p.inv_cols);
+        const float m = means.x;
         if (t == 0 && !lost) start();
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) {
             const uint32_t c = 8 * (i * T + t);
             float o[8];
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) o[k] = s * (g[i][k] - n[i][k] * m);
+            for (uint32_t k = 0; k < 8; ++k) o[k] = s * ((MEAN ? g[i][k] - means.y : g[i][k]) - n[i][k] * m);
             if (p.dres) {
                 float q[8];
                 load8<true>(row + gb + hb, p.h_dt, c, p.cols, q);
@@ -948,12 +1131,20 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
     if (lost) {                                     // acc has taken rows that had not arrived
         if (t == 0) await_copies(full, S, next, p.partials);
 #pragma unroll
-        for (uint32_t i = 0; i < NCH; ++i) make_nan(acc[i]);
+        for (uint32_t i = 0; i < NCH; ++i) {
+            make_nan(acc[i]);
+            if (MEAN) make_nan(acc_b[i]);
+        }
     }
     if (p.partial) {
         float* part = p.partial + (uint64_t)blockIdx.x * p.cols;
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) store8<true>(reinterpret_cast<char*>(part), DTT_F32, 8 * (i * T + t), p.cols, acc[i]);
+        if constexpr (MEAN) {
+            float* part_b = p.partial_b + (uint64_t)blockIdx.x * p.cols;
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i) store8<true>(reinterpret_cast<char*>(part_b), DTT_F32, 8 * (i * T + t), p.cols, acc_b[i]);
+        }
     }
 }
 
@@ -979,11 +1170,11 @@ __device__ __forceinline__ uint32_t skip_of(const char* base, uint64_t r, uint64
 
 __host__ __device__ __forceinline__ uint32_t words_room(uint32_t bytes) { return (bytes + 30) & ~15u; }
 
-template <uint32_t E>
-__global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+template <bool MEAN, uint32_t E>
+__global__ void __launch_bounds__(kRingThreads, 2) norm_fwd_ring_elements_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
     launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
-    __shared__ float slots[2][2][32];
+    __shared__ float slots[2][MEAN ? 3 : 2][32];
     __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
@@ -1011,10 +1202,15 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
     wait_previous();
     if (t == 0)
         for (uint32_t i = 0; i + 1 < S; ++i) start();
-    float w[E];
+    float w[E], b[MEAN ? E : 1];
 #pragma unroll
-    for (uint32_t k = 0; k < E; ++k) w[k] = 1.0f;
+    for (uint32_t k = 0; k < E; ++k) {
+        w[k] = 1.0f;
+        if (MEAN) b[k] = 0.0f;
+    }
     if (p.w) load_elements(p.w, p.w_dt, p.cols, w);
+    if constexpr (MEAN)
+        if (p.b) load_elements(p.b, p.w_dt, p.cols, b);
     __syncthreads();
 
     uint32_t st = 0, phase = 0;
@@ -1031,8 +1227,17 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
 #pragma unroll
             for (uint32_t k = 0; k < E; ++k) h[k] += q[k];
         }
+        float mu = 0.0f;
+        if constexpr (MEAN) {
 #pragma unroll
-        for (uint32_t k = 0; k < E; ++k) sum += h[k] * h[k];
+            for (uint32_t k = 0; k < E; ++k) mu += h[k];
+            if (lost) mu = kNan;
+            mu = row_sum(mu, T, slots[turn][2]) * p.inv_cols;
+            if (t == 0 && p.mean) p.mean[r] = mu;
+            centre(h, mu, p.cols);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < E; ++k) sum += MEAN ? (h[k] - mu) * (h[k] - mu) : h[k] * h[k];
         if (lost) sum = kNan;
         const float s = rsqrtf(row_sum(sum, T, slots[turn][0]) * p.inv_cols + p.eps);
         if (t == 0) {
@@ -1044,7 +1249,11 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
             store_elements(p.res_out + r * p.res_out_pitch, p.res_dt, p.cols, h);
         }
 #pragma unroll
-        for (uint32_t k = 0; k < E; ++k) h[k] = h[k] * s * w[k];
+        for (uint32_t k = 0; k < E; ++k) {
+            if (MEAN) h[k] -= mu;
+            h[k] = h[k] * s * w[k];
+            if (MEAN) h[k] += b[k];
+        }
         if (p.y_dt == DTT_E4M3) scale_elements(p, r, slots[turn][1], h);
         store_elements(p.y + r * p.y_pitch, p.y_dt, p.cols, h);
         if (++st == S) { st = 0; phase ^= 1; }
@@ -1054,12 +1263,12 @@ __global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_fwd_ring_elements_ker
 
 // 16384 x 4001 in f32: 179 us, 0.86 of the copy rate; 1021 x 5001 in f32 19 us, 0.63: one CTA a SM (60 KiB a
 // stage), seven rows each.
-template <uint32_t E>
-__global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+template <bool MEAN, uint32_t E>
+__global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
-    if (blockIdx.x >= p.partials) return weight_columns(p);
+    if (blockIdx.x >= p.partials) return weight_columns<MEAN>(p);
     extern __shared__ __align__(128) uint8_t stages[];
-    __shared__ float slots[2][32];
+    __shared__ float slots[2][MEAN ? 64 : 32];
     __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t gb = p.cols * (p.dy_dt == DTT_BF16 ? 2 : 4), hb = p.cols * (p.h_dt == DTT_BF16 ? 2 : 4);
@@ -1088,11 +1297,12 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
     wait_previous();
     if (t == 0)
         for (uint32_t i = 0; i + 1 < S; ++i) start();
-    float w[E], acc[E];
+    float w[E], acc[E], acc_b[MEAN ? E : 1];
 #pragma unroll
     for (uint32_t k = 0; k < E; ++k) {
         w[k] = 1.0f;
         acc[k] = 0.0f;
+        if (MEAN) acc_b[k] = 0.0f;
     }
     if (p.w) load_elements(p.w, p.w_dt, p.cols, w);
     __syncthreads();
@@ -1101,24 +1311,26 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
     uint32_t turn = 0;
     bool lost = false;
     for (uint64_t r = blockIdx.x; r < p.rows; r += p.partials, turn ^= 1) {
-        const float s = p.rstd[r];
+        const float s = p.rstd[r], mu = MEAN ? p.mean[r] : 0.0f;
         lost = lost || DTT_NORM_ROW_LATE || !bar_wait(saddr(full + st), phase);
         const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
-        float g[E], n[E], dot = 0.0f;
+        float g[E], n[E], dot = 0.0f, all = 0.0f;
         load_elements(row + skip_of(p.dy, r, p.dy_pitch), p.dy_dt, p.cols, g);
         load_elements(row + g_room + skip_of(p.h, r, p.h_pitch), p.h_dt, p.cols, n);
 #pragma unroll
         for (uint32_t k = 0; k < E; ++k) {
-            n[k] *= s;
+            n[k] = (MEAN ? n[k] - mu : n[k]) * s;
             acc[k] += g[k] * n[k];
+            if (MEAN) acc_b[k] += g[k];
             g[k] *= w[k];
             dot += g[k] * n[k];
+            if (MEAN) all += g[k];
         }
         if (lost) dot = kNan;
-        const float m = row_sum(dot, T, slots[turn]) * p.inv_cols;
+        const float2 means = row_means<MEAN>(dot, all, T, slots[turn], p.inv_cols);
         if (t == 0 && !lost) start();
 #pragma unroll
-        for (uint32_t k = 0; k < E; ++k) g[k] = s * (g[k] - n[k] * m);
+        for (uint32_t k = 0; k < E; ++k) g[k] = s * ((MEAN ? g[k] - means.y : g[k]) - n[k] * means.x);
         if (p.dres) {
             load_elements(row + g_room + h_room + skip_of(p.dres, r, p.dres_pitch), p.h_dt, p.cols, n);
 #pragma unroll
@@ -1130,13 +1342,20 @@ __global__ void __launch_bounds__(kRingThreads) rmsnorm_bwd_ring_elements_kernel
     if (lost) {                                     // acc has taken rows that had not arrived
         if (t == 0) await_copies(full, S, next, p.partials);
         make_nan(acc);
+        if (MEAN) make_nan(acc_b);
     }
     if (p.partial) store_elements(reinterpret_cast<char*>(p.partial + (uint64_t)blockIdx.x * p.cols), DTT_F32, p.cols, acc);
+    if constexpr (MEAN)
+        if (p.partial) store_elements(reinterpret_cast<char*>(p.partial_b + (uint64_t)blockIdx.x * p.cols), DTT_F32, p.cols, acc_b);
 }
 
 // dweight[c] = the partial rows' sum.  32 columns a CTA; its 32 warps take every 32nd partial row, and
 // their sums are added in warp order.  304 partial rows of 4096: about 4 us, from L2.
-__global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* partial, uint32_t partials, uint32_t cols, float* dweight) {
+// blockIdx.y 1: the bias's partial rows and gradient.
+__global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* partial_w, const float* partial_b, uint32_t partials, uint32_t cols, float* dweight, float* dbias) {
+    const float* partial = blockIdx.y ? partial_b : partial_w;
+    float* out = blockIdx.y ? dbias : dweight;
+    if (!out) return;
     __shared__ float part[32][33];
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
@@ -1151,7 +1370,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* part
     v = part[lane][warp];                            // warp w adds column w
 #pragma unroll
     for (uint32_t o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if (lane == 0 && (uint64_t)blockIdx.x * 32 + warp < cols) dweight[(uint64_t)blockIdx.x * 32 + warp] = v;
+    if (lane == 0 && (uint64_t)blockIdx.x * 32 + warp < cols) out[(uint64_t)blockIdx.x * 32 + warp] = v;
 }
 
 uint32_t short_lanes(uint32_t cols) {
@@ -1173,6 +1392,7 @@ uint32_t element_threads(uint32_t cols, uint32_t E, uint32_t threads) {
     return t <= threads ? t : 0;
 }
 
+template <bool MEAN>
 cudaError_t launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t xe = p.x_dt == DTT_BF16 ? 2 : 4, re = p.res ? (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
     const uint32_t sms = sm_count();
@@ -1180,53 +1400,54 @@ cudaError_t launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     if (vec && p.cols <= kShortCols) {
         const uint32_t lanes = short_lanes(p.cols);
         const uint64_t each = 256 / lanes;
-        return launch(rmsnorm_fwd_short_kernel, (uint32_t)((p.rows + each - 1) / each), 256, 0, 0, true, stream, p, lanes);
+        return launch(norm_fwd_short_kernel<MEAN>, (uint32_t)((p.rows + each - 1) / each), 256, 0, 0, true, stream, p, lanes);
     }
     // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
     // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
     // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
-    const ring::Plan g = ring::plan(p.cols, vec, vec ? xb + rb : xb + rb + 60, kFwdOwn, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : ring::kStages);
+    const ring::Plan g = ring::plan(p.cols, vec, vec ? xb + rb : xb + rb + 60, kFwdOwn<MEAN>, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : ring::kStages);
     // The chunk form's loads wait for one another, the ring's do not: 152 x 8064 (bf16) 6.7 us by chunks, 3.7 by
     // the ring.  The element form's go out together, and it is the faster one while there are few rows:
     // 600 x 3001 5.7 us and 6.6, 2400 x 3001 22.2 and 18.4.
     if (g.ctas && (vec || p.rows >= 8 * sms)) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
-        auto kernel = vec ? (g.nch == 1 ? rmsnorm_fwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>)
-                          : (g.nch == 1 ? rmsnorm_fwd_ring_elements_kernel<8> : rmsnorm_fwd_ring_elements_kernel<16>);
+        auto kernel = vec ? (g.nch == 1 ? norm_fwd_ring_kernel<MEAN, 1> : g.nch == 2 ? norm_fwd_ring_kernel<MEAN, 2> : norm_fwd_ring_kernel<MEAN, 4>)
+                          : (g.nch == 1 ? norm_fwd_ring_elements_kernel<MEAN, 8> : norm_fwd_ring_elements_kernel<MEAN, 16>);
         return launch(kernel, grid, g.threads, g.smem, 0, true, stream, p, g.stages);
     }
     if (!vec) {
         if (const uint32_t t = element_threads(p.cols, 8, kFwdThreads)) {
             const uint32_t each = t == 32 ? kWarpRows : 1;
-            return launch(rmsnorm_fwd_elements_kernel<8>, (uint32_t)((p.rows + each - 1) / each), dim3(t, each), 0, 0, true, stream, p);
+            return launch(norm_fwd_elements_kernel<MEAN, 8>, (uint32_t)((p.rows + each - 1) / each), dim3(t, each), 0, 0, true, stream, p);
         }
         if (const uint32_t t = element_threads(p.cols, 16, kFwdThreads))
-            return launch(rmsnorm_fwd_elements_kernel<16>, (uint32_t)p.rows, t, 0, 0, true, stream, p);
-        return launch(rmsnorm_fwd_kernel<kLong, false>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
+            return launch(norm_fwd_elements_kernel<MEAN, 16>, (uint32_t)p.rows, t, 0, 0, true, stream, p);
+        return launch(norm_fwd_kernel<MEAN, kLong, false>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
     }
-    if (p.cols <= 32 * kFwdThreads) return launch(rmsnorm_fwd_kernel<4, true>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
-    return launch(rmsnorm_fwd_kernel<kLong, true>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
+    if (p.cols <= 32 * kFwdThreads) return launch(norm_fwd_kernel<MEAN, 4, true>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
+    return launch(norm_fwd_kernel<MEAN, kLong, true>, (uint32_t)p.rows, kFwdThreads, 0, 0, true, stream, p);
 }
 
 // Sets p.partials, the CTAs that take rows, and as many partial rows of the weight's gradient.
+template <bool MEAN>
 cudaError_t launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
-    const uint32_t columns = p.dweight ? (uint32_t)std::min<uint64_t>((p.cols + 31) / 32, 4 * sm_count()) : 0;
+    const uint32_t columns = p.dweight || p.dbias ? (uint32_t)std::min<uint64_t>((p.cols + 31) / 32, 4 * sm_count()) : 0;
     const uint32_t ge = p.dy_dt == DTT_BF16 ? 2 : 4, he = p.h_dt == DTT_BF16 ? 2 : 4;
     const uint32_t sms = sm_count();
     if (vec && p.cols <= kShortCols) {
         const uint32_t lanes = short_lanes(p.cols);
         const uint64_t each = 256 / lanes;
         p.partials = (uint32_t)std::min<uint64_t>((p.rows + each - 1) / each, most_partials(p.cols));
-        return launch(rmsnorm_bwd_short_kernel, p.partials + columns, 256, 0, 0, true, stream, p, lanes);
+        return launch(norm_bwd_short_kernel<MEAN>, p.partials + columns, 256, 0, 0, true, stream, p, lanes);
     }
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
-    const ring::Plan g = ring::plan(p.cols, vec, vec ? stage : stage + 90, kBwdOwn, 2048, {1024, 512, 256}, 1, ring::kStages);
+    const ring::Plan g = ring::plan(p.cols, vec, vec ? stage : stage + 90, kBwdOwn<MEAN>, 2048, {1024, 512, 256}, 1, ring::kStages);
     // by chunks and by the ring: 200 x 4096 (bf16) 11.2 us and 7.6, 16384 x 4096 255 and 92; by elements and by
     // the ring: 152 x 1021 (f32) 5.5 and 5.6, 460 x 5001 (f32) 15.3 and 10.8
     if (g.ctas && (vec || p.rows > sms)) {
         p.partials = (uint32_t)std::min<uint64_t>({p.rows, (uint64_t)g.ctas * sms, (uint64_t)most_partials(p.cols)});
-        auto kernel = vec ? (g.nch == 1 ? rmsnorm_bwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_bwd_ring_kernel<2> : rmsnorm_bwd_ring_kernel<4>)
-                          : (g.nch == 1 ? rmsnorm_bwd_ring_elements_kernel<8> : rmsnorm_bwd_ring_elements_kernel<16>);
+        auto kernel = vec ? (g.nch == 1 ? norm_bwd_ring_kernel<MEAN, 1> : g.nch == 2 ? norm_bwd_ring_kernel<MEAN, 2> : norm_bwd_ring_kernel<MEAN, 4>)
+                          : (g.nch == 1 ? norm_bwd_ring_elements_kernel<MEAN, 8> : norm_bwd_ring_elements_kernel<MEAN, 16>);
         return launch(kernel, p.partials + columns, g.threads, g.smem, 0, true, stream, p, g.stages);
     }
     auto walk = [&](uint32_t each) {       // walkers a CTA
@@ -1238,14 +1459,14 @@ cudaError_t launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         if (const uint32_t t = element_threads(p.cols, 8, kBwdThreads)) {
             const uint32_t each = t == 32 ? kWarpRows : 1;
             walk(each);
-            return launch(rmsnorm_bwd_elements_kernel<8>, p.partials + columns, dim3(t, each), 0, 0, true, stream, p);
+            return launch(norm_bwd_elements_kernel<MEAN, 8>, p.partials + columns, dim3(t, each), 0, 0, true, stream, p);
         }
         if (const uint32_t t = element_threads(p.cols, 16, kBwdThreads))
-            return launch(rmsnorm_bwd_elements_kernel<16>, p.partials + columns, t, 0, 0, true, stream, p);
-        return launch(rmsnorm_bwd_kernel<kLong, false>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
+            return launch(norm_bwd_elements_kernel<MEAN, 16>, p.partials + columns, t, 0, 0, true, stream, p);
+        return launch(norm_bwd_kernel<MEAN, kLong, false>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
     }
-    if (p.cols <= 32 * kBwdThreads) return launch(rmsnorm_bwd_kernel<4, true>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
-    return launch(rmsnorm_bwd_kernel<kLong, true>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
+    if (p.cols <= 32 * kBwdThreads) return launch(norm_bwd_kernel<MEAN, 4, true>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
+    return launch(norm_bwd_kernel<MEAN, kLong, true>, p.partials + columns, kBwdThreads, 0, 0, true, stream, p);
 }
 
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
@@ -1289,30 +1510,40 @@ cudaError_t prepare(const void* kernel, uint32_t own = ~0u) {
 
 }  // namespace
 
-cudaError_t preload_norm_kernels() {
+namespace {
+
+template <bool MEAN>
+cudaError_t preload_norm() {
     const void* kernels[] = {
-        (const void*)rmsnorm_fwd_short_kernel, (const void*)rmsnorm_bwd_short_kernel,
-        (const void*)rmsnorm_fwd_kernel<4, true>, (const void*)rmsnorm_fwd_kernel<kLong, true>,
-        (const void*)rmsnorm_fwd_kernel<kLong, false>, (const void*)rmsnorm_fwd_elements_kernel<8>,
-        (const void*)rmsnorm_fwd_elements_kernel<16>,
-        (const void*)rmsnorm_bwd_kernel<4, true>, (const void*)rmsnorm_bwd_kernel<kLong, true>,
-        (const void*)rmsnorm_bwd_kernel<kLong, false>, (const void*)rmsnorm_bwd_elements_kernel<8>,
-        (const void*)rmsnorm_bwd_elements_kernel<16>, (const void*)rmsnorm_dweight_kernel};
+        (const void*)norm_fwd_short_kernel<MEAN>, (const void*)norm_bwd_short_kernel<MEAN>,
+        (const void*)norm_fwd_kernel<MEAN, 4, true>, (const void*)norm_fwd_kernel<MEAN, kLong, true>,
+        (const void*)norm_fwd_kernel<MEAN, kLong, false>, (const void*)norm_fwd_elements_kernel<MEAN, 8>,
+        (const void*)norm_fwd_elements_kernel<MEAN, 16>,
+        (const void*)norm_bwd_kernel<MEAN, 4, true>, (const void*)norm_bwd_kernel<MEAN, kLong, true>,
+        (const void*)norm_bwd_kernel<MEAN, kLong, false>, (const void*)norm_bwd_elements_kernel<MEAN, 8>,
+        (const void*)norm_bwd_elements_kernel<MEAN, 16>, (const void*)norm_dweight_kernel};
     for (const void* k : kernels) {
         const cudaError_t e = prepare(k);
         if (e != cudaSuccess) return e;
     }
-    const void* fwd_rings[] = {(const void*)rmsnorm_fwd_ring_kernel<1>, (const void*)rmsnorm_fwd_ring_kernel<2>, (const void*)rmsnorm_fwd_ring_kernel<4>,
-                               (const void*)rmsnorm_fwd_ring_elements_kernel<8>, (const void*)rmsnorm_fwd_ring_elements_kernel<16>};
-    const void* bwd_rings[] = {(const void*)rmsnorm_bwd_ring_kernel<1>, (const void*)rmsnorm_bwd_ring_kernel<2>, (const void*)rmsnorm_bwd_ring_kernel<4>,
-                               (const void*)rmsnorm_bwd_ring_elements_kernel<8>, (const void*)rmsnorm_bwd_ring_elements_kernel<16>};
+    const void* fwd_rings[] = {(const void*)norm_fwd_ring_kernel<MEAN, 1>, (const void*)norm_fwd_ring_kernel<MEAN, 2>, (const void*)norm_fwd_ring_kernel<MEAN, 4>,
+                               (const void*)norm_fwd_ring_elements_kernel<MEAN, 8>, (const void*)norm_fwd_ring_elements_kernel<MEAN, 16>};
+    const void* bwd_rings[] = {(const void*)norm_bwd_ring_kernel<MEAN, 1>, (const void*)norm_bwd_ring_kernel<MEAN, 2>, (const void*)norm_bwd_ring_kernel<MEAN, 4>,
+                               (const void*)norm_bwd_ring_elements_kernel<MEAN, 8>, (const void*)norm_bwd_ring_elements_kernel<MEAN, 16>};
     for (uint32_t i = 0; i < 10; ++i) {
         const void* k = i < 5 ? fwd_rings[i] : bwd_rings[i - 5];
-        cudaError_t e = prepare(k, i < 5 ? kFwdOwn : kBwdOwn);
+        cudaError_t e = prepare(k, i < 5 ? kFwdOwn<MEAN> : kBwdOwn<MEAN>);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring::kSmem);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t preload_norm_kernels() {
+    const cudaError_t e = preload_norm<false>();
+    return e == cudaSuccess ? preload_norm<true>() : e;
 }
 
 }  // namespace dtt
@@ -1327,11 +1558,21 @@ extern "C" int dtt_rmsnorm_workspace(const dtt_rmsnorm_desc* d, uint64_t* bytes)
     return DTT_OK;
 }
 
-extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, const void* x, uint64_t x_pitch,
-                                   const void* residual, uint64_t residual_pitch, const void* weight,
-                                   void* residual_out, uint64_t residual_out_pitch, void* y, uint64_t y_pitch,
-                                   float* scales, float* rstd, cudaStream_t stream) {
-    const char* who = "dtt_rmsnorm_forward";
+extern "C" int dtt_layernorm_workspace(const dtt_layernorm_desc* d, uint64_t* bytes) {
+    const int rc = check_desc("dtt_layernorm_workspace", d);
+    if (rc) return rc;
+    if (!bytes) return fail(DTT_EINVAL, "dtt_layernorm_workspace: null bytes");
+    *bytes = 2 * (uint64_t)most_partials(d->cols) * d->cols * 4;
+    return DTT_OK;
+}
+
+namespace {
+
+// bias and mean: the layer norm's.
+template <bool MEAN>
+int forward(const char* who, const dtt_rmsnorm_desc* d, uint64_t rows, const void* x, uint64_t x_pitch, const void* residual,
+            uint64_t residual_pitch, const void* weight, const void* bias, void* residual_out, uint64_t residual_out_pitch, void* y,
+            uint64_t y_pitch, float* scales, float* mean, float* rstd, cudaStream_t stream) {
     int rc = check_desc(who, d);
     if (rc) return rc;
     if (rows >= (1ull << 31)) return fail(DTT_EINVAL, "%s: 2^31 rows or more", who);
@@ -1340,9 +1581,11 @@ extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, con
     if ((rc = check_rows(who, "x", x, x_pitch, rows, d->cols, d->x_dtype, false)) ||
         (rc = check_rows(who, "residual", residual, residual_pitch, rows, d->cols, d->residual_dtype, true)) ||
         (rc = check_rows(who, "weight", weight, 0, 1, d->cols, d->weight_dtype, true)) ||
+        (rc = check_rows(who, "bias", bias, 0, 1, d->cols, d->weight_dtype, true)) ||
         (rc = check_rows(who, "residual_out", residual_out, residual_out_pitch, rows, d->cols, d->residual_dtype, true)) ||
         (rc = check_rows(who, "y", y, y_pitch, rows, d->cols, d->y_dtype, false)) ||
         (rc = check_rows(who, "scales", scales, 0, 1, 0, DTT_F32, !e4m3)) ||
+        (rc = check_rows(who, "mean", mean, 0, 1, 0, DTT_F32, true)) ||
         (rc = check_rows(who, "rstd", rstd, 0, 1, 0, DTT_F32, true)))
         return rc;
     if (scales && !e4m3) return fail(DTT_EINVAL, "%s: scales go with an e4m3 y alone", who);
@@ -1353,9 +1596,11 @@ extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, con
     p.x = static_cast<const char*>(x);
     p.res = static_cast<const char*>(residual);
     p.w = static_cast<const char*>(weight);
+    p.b = static_cast<const char*>(bias);
     p.res_out = static_cast<char*>(residual_out);
     p.y = static_cast<char*>(y);
     p.scales = scales;
+    p.mean = mean;
     p.rstd = rstd;
     p.x_pitch = x_pitch;
     p.res_pitch = residual_pitch;
@@ -1372,34 +1617,37 @@ extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, con
     p.eps = d->eps;
     p.inv_cols = 1.0f / (float)d->cols;
     const bool vec = d->cols % 8 == 0 && aligned(x, x_pitch, 16) && aligned(residual, residual ? residual_pitch : 0, 16) &&
-                     aligned(weight, 0, 16) && aligned(residual_out, residual_out ? residual_out_pitch : 0, 16) &&
+                     aligned(weight, 0, 16) && aligned(bias, 0, 16) && aligned(residual_out, residual_out ? residual_out_pitch : 0, 16) &&
                      aligned(y, y_pitch, e4m3 ? 8 : 16);
-    const cudaError_t e = launch_fwd(p, vec, stream);
+    const cudaError_t e = launch_fwd<MEAN>(p, vec, stream);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }
 
-extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, const void* dy, uint64_t dy_pitch,
-                                    const void* h, uint64_t h_pitch, const void* weight, const float* rstd,
-                                    const void* dres, uint64_t dres_pitch, void* dx, uint64_t dx_pitch,
-                                    float* dweight, void* workspace, uint64_t workspace_bytes, cudaStream_t stream) {
-    const char* who = "dtt_rmsnorm_backward";
+// mean and dbias: the layer norm's.
+template <bool MEAN>
+int backward(const char* who, const dtt_rmsnorm_desc* d, uint64_t rows, const void* dy, uint64_t dy_pitch, const void* h, uint64_t h_pitch,
+             const void* weight, const float* mean, const float* rstd, const void* dres, uint64_t dres_pitch, void* dx, uint64_t dx_pitch,
+             float* dweight, float* dbias, void* workspace, uint64_t workspace_bytes, cudaStream_t stream) {
+    const uint64_t part_bytes = d ? (uint64_t)most_partials(d->cols) * d->cols * 4 : 0;
     int rc = check_desc(who, d);
     if (rc) return rc;
     if (rows >= (1ull << 31)) return fail(DTT_EINVAL, "%s: 2^31 rows or more", who);
     if (dweight && !weight) return fail(DTT_EINVAL, "%s: a weight's gradient without a weight", who);
     if ((rc = check_rows(who, "weight", weight, 0, 1, d->cols, d->weight_dtype, true)) ||
-        (rc = check_rows(who, "dweight", dweight, 0, 1, 0, DTT_F32, true)))
+        (rc = check_rows(who, "dweight", dweight, 0, 1, 0, DTT_F32, true)) ||
+        (rc = check_rows(who, "dbias", dbias, 0, 1, 0, DTT_F32, true)))
         return rc;
-    if (dweight && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 ||
-                    workspace_bytes < (uint64_t)most_partials(d->cols) * d->cols * 4))
+    if ((dweight || dbias) && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < (MEAN ? 2 : 1) * part_bytes))
         return fail(DTT_EINVAL, "%s: the workspace is missing, misaligned or short", who);
     if (rows == 0) {
-        if (dweight) DTT_CUDA_TRY(cudaMemsetAsync(dweight, 0, d->cols * 4, stream));
+        for (float* out : {dweight, dbias})
+            if (out) DTT_CUDA_TRY(cudaMemsetAsync(out, 0, d->cols * 4, stream));
         return DTT_OK;
     }
     if ((rc = check_rows(who, "dy", dy, dy_pitch, rows, d->cols, d->x_dtype, false)) ||
         (rc = check_rows(who, "h", h, h_pitch, rows, d->cols, d->residual_dtype, false)) ||
+        (rc = check_rows(who, "mean", mean, 0, 1, 0, DTT_F32, !MEAN)) ||
         (rc = check_rows(who, "rstd", rstd, 0, 1, 0, DTT_F32, false)) ||
         (rc = check_rows(who, "dres", dres, dres_pitch, rows, d->cols, d->residual_dtype, true)) ||
         (rc = check_rows(who, "dx", dx, dx_pitch, rows, d->cols, d->residual_dtype, false)))
@@ -1411,12 +1659,15 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
     p.dy = static_cast<const char*>(dy);
     p.h = static_cast<const char*>(h);
     p.w = static_cast<const char*>(weight);
+    p.mean = mean;
     p.rstd = rstd;
     p.dres = static_cast<const char*>(dres);
     p.dx = static_cast<char*>(dx);
     const bool few = rows <= kFewRows;
-    p.partial = dweight && !few ? static_cast<float*>(workspace) : nullptr;
+    p.partial = (dweight || dbias) && !few ? static_cast<float*>(workspace) : nullptr;
+    p.partial_b = MEAN && p.partial ? p.partial + part_bytes / 4 : nullptr;
     p.dweight = few ? dweight : nullptr;
+    p.dbias = few ? dbias : nullptr;
     p.dy_pitch = dy_pitch;
     p.h_pitch = h_pitch;
     p.dres_pitch = dres_pitch;
@@ -1429,9 +1680,43 @@ extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, co
     p.inv_cols = 1.0f / (float)d->cols;
     const bool vec = d->cols % 8 == 0 && aligned(dy, dy_pitch, 16) && aligned(h, h_pitch, 16) && aligned(weight, 0, 16) &&
                      aligned(dres, dres ? dres_pitch : 0, 16) && aligned(dx, dx_pitch, 16);
-    cudaError_t e = launch_bwd(p, vec, stream);
+    cudaError_t e = launch_bwd<MEAN>(p, vec, stream);
     if (e == cudaSuccess && p.partial)
-        e = launch(rmsnorm_dweight_kernel, (p.cols + 31) / 32, 1024, 0, 0, true, stream, p.partial, p.partials, p.cols, dweight);
+        e = launch(norm_dweight_kernel, dim3((p.cols + 31) / 32, MEAN ? 2 : 1), 1024, 0, 0, true, stream, p.partial, p.partial_b, p.partials, p.cols, dweight, dbias);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
+}
+
+}  // namespace
+
+extern "C" int dtt_rmsnorm_forward(const dtt_rmsnorm_desc* d, uint64_t rows, const void* x, uint64_t x_pitch,
+                                   const void* residual, uint64_t residual_pitch, const void* weight,
+                                   void* residual_out, uint64_t residual_out_pitch, void* y, uint64_t y_pitch,
+                                   float* scales, float* rstd, cudaStream_t stream) {
+    return forward<false>("dtt_rmsnorm_forward", d, rows, x, x_pitch, residual, residual_pitch, weight, nullptr, residual_out,
+                          residual_out_pitch, y, y_pitch, scales, nullptr, rstd, stream);
+}
+
+extern "C" int dtt_layernorm_forward(const dtt_layernorm_desc* d, uint64_t rows, const void* x, uint64_t x_pitch,
+                                     const void* residual, uint64_t residual_pitch, const void* weight, const void* bias,
+                                     void* residual_out, uint64_t residual_out_pitch, void* y, uint64_t y_pitch,
+                                     float* scales, float* mean, float* rstd, cudaStream_t stream) {
+    return forward<true>("dtt_layernorm_forward", d, rows, x, x_pitch, residual, residual_pitch, weight, bias, residual_out,
+                         residual_out_pitch, y, y_pitch, scales, mean, rstd, stream);
+}
+
+extern "C" int dtt_rmsnorm_backward(const dtt_rmsnorm_desc* d, uint64_t rows, const void* dy, uint64_t dy_pitch,
+                                    const void* h, uint64_t h_pitch, const void* weight, const float* rstd,
+                                    const void* dres, uint64_t dres_pitch, void* dx, uint64_t dx_pitch,
+                                    float* dweight, void* workspace, uint64_t workspace_bytes, cudaStream_t stream) {
+    return backward<false>("dtt_rmsnorm_backward", d, rows, dy, dy_pitch, h, h_pitch, weight, nullptr, rstd, dres, dres_pitch, dx,
+                           dx_pitch, dweight, nullptr, workspace, workspace_bytes, stream);
+}
+
+extern "C" int dtt_layernorm_backward(const dtt_layernorm_desc* d, uint64_t rows, const void* dy, uint64_t dy_pitch,
+                                      const void* h, uint64_t h_pitch, const void* weight, const float* mean, const float* rstd,
+                                      const void* dres, uint64_t dres_pitch, void* dx, uint64_t dx_pitch, float* dweight,
+                                      float* dbias, void* workspace, uint64_t workspace_bytes, cudaStream_t stream) {
+    return backward<true>("dtt_layernorm_backward", d, rows, dy, dy_pitch, h, h_pitch, weight, mean, rstd, dres, dres_pitch, dx,
+                          dx_pitch, dweight, dbias, workspace, workspace_bytes, stream);
 }

@@ -1,7 +1,8 @@
-"""Operators on the block of rows that a rank owns between a reduce-scatter and an all-gather
-(C ABI in include/dtt_ops.h): the residual's addition with a root-mean-square norm, that norm's
-backward pass, and the orthogonalisation of a momentum update.  Argument checks, marshalling and
-the workspaces only; tensors are torch CUDA tensors whose rows are contiguous (any row pitch).
+"""Operators on what a rank owns between a reduce-scatter and an all-gather (C ABI in
+include/dtt_ops.h): the residual's addition with a root-mean-square norm or a layer norm and their
+backward passes, tokens' rows sorted by expert and back, the orthogonalisation of a momentum update,
+and AdamW over the tensors of the rank's share.  Argument checks, marshalling and the workspaces only;
+tensors are torch CUDA tensors whose rows are contiguous (any row pitch).
 An object lives as long as the graphs that hold its calls."""
 from __future__ import annotations
 
@@ -80,13 +81,16 @@ class RMSNorm:
     the first call with a dweight, in the order of that call's stream), so one object serves one stream at a time (or
     the caller orders the streams)."""
 
+    _who, _calls = "RMSNorm", "dtt_rmsnorm_"
+
     def __init__(self, cols: int, x: str = "bf16", residual: str = "bf16", weight: str = "bf16",
                  y: str = "bf16", group: int = 0, eps: float = 1e-6):
-        who = "RMSNorm"
+        who = self._who
         self.desc = D.dtt_rmsnorm_desc(_code(who, "x", x), _code(who, "residual", residual),
                                        _code(who, "weight", weight), _code(who, "y", y), group, eps, cols)
         need = C.c_uint64()
-        D._check(D.lib().dtt_rmsnorm_workspace(C.byref(self.desc), C.byref(need)))
+        workspace, self._forward, self._backward = (getattr(D.lib(), self._calls + k) for k in ("workspace", "forward", "backward"))
+        D._check(workspace(C.byref(self.desc), C.byref(need)))
         self.cols, self.group, self.workspace_bytes = cols, group, need.value
         types = _torch_types()
         self._x, self._res, self._w, self._y = types[x], types[residual], types[weight], types[y]
@@ -95,17 +99,16 @@ class RMSNorm:
         self.scale_cols = -(-cols // group) if group else 1
         self._workspace = None
         self._ref = C.byref(self.desc)
-        self._forward, self._backward = D.lib().dtt_rmsnorm_forward, D.lib().dtt_rmsnorm_backward
 
     def _rows(self, name: str, t, shape, dtype, size: int) -> Tuple[int, int]:
         """(address, pitch in bytes) of a [rows, cols] argument of `size`-byte elements; (0, 0) for None."""
         if t is None:
             return 0, 0
         if t.dtype != dtype or t.shape != shape:
-            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+            raise D.DttError(D.EINVAL, f"{self._who}: {name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
         row, col = t.stride()
         if not t.is_cuda or (col != 1 and self.cols > 1):
-            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be on the GPU with contiguous rows")
+            raise D.DttError(D.EINVAL, f"{self._who}: {name} must be on the GPU with contiguous rows")
         return t.data_ptr(), row * size
 
     def _flat(self, name: str, t, n: int, dtype) -> int:
@@ -113,8 +116,17 @@ class RMSNorm:
         if t is None:
             return 0
         if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be {n} contiguous {dtype} on the GPU")
+            raise D.DttError(D.EINVAL, f"{self._who}: {name} must be {n} contiguous {dtype} on the GPU")
         return t.data_ptr()
+
+    def _scratch(self, needed: bool, stream, device) -> Tuple[int, int]:
+        """(address, bytes) of the backward pass's workspace, where the call needs one."""
+        if not needed:
+            return 0, 0
+        if self._workspace is None or self._workspace.buffer.device != device:
+            self._workspace = _Workspace.on(stream, self.workspace_bytes, device)
+        self._workspace.use(stream)
+        return self._workspace.address, self.workspace_bytes
 
     def forward(self, x, weight, y, residual=None, residual_out=None, scales=None, rstd=None, stream=None) -> None:
         """y, and where given residual_out (= h; may be residual itself), scales ([rows, scale_cols]
@@ -141,17 +153,329 @@ class RMSNorm:
         hp, hs = self._rows("h", h, shape, self._res, self._rese)
         sp, ss = self._rows("dres", dres, shape, self._res, self._rese)
         xp, xs = self._rows("dx", dx, shape, self._res, self._rese)
-        ws, need = 0, 0
-        if dweight is not None:
-            if self._workspace is None or self._workspace.buffer.device != dy.device:
-                self._workspace = _Workspace.on(stream, self.workspace_bytes, dy.device)
-            self._workspace.use(stream)
-            ws, need = self._workspace.address, self.workspace_bytes
+        ws, need = self._scratch(dweight is not None, stream, dy.device)
         rc = self._backward(self._ref, rows, gp, gs, hp, hs, self._flat("weight", weight, self.cols, self._w),
                             self._flat("rstd", rstd, rows, self._f32), sp, ss, xp, xs,
                             self._flat("dweight", dweight, self.cols, self._f32), ws, need, D._stream(stream))
         if rc:
             D._check(rc)
+
+
+def _here(who: str, name: str, t) -> None:
+    """t is on the current device: the calls launch there."""
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise D.DttError(D.EINVAL, f"{who}: {name} must be on the current GPU")
+
+
+class LayerNorm(RMSNorm):
+    """h = x + residual; y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias, row by row, and its gradients
+    (dtt_layernorm_forward / dtt_layernorm_backward: see there for the definitions).
+
+    Arguments as RMSNorm's; the bias has the weight's type.  Keeps the backward pass's workspace in the same way
+    (allocated by the first call with a dweight or a dbias)."""
+
+    _who, _calls = "LayerNorm", "dtt_layernorm_"
+
+    def __init__(self, cols: int, x: str = "bf16", residual: str = "bf16", weight: str = "bf16",
+                 y: str = "bf16", group: int = 0, eps: float = 1e-5):
+        super().__init__(cols, x, residual, weight, y, group, eps)
+
+    def forward(self, x, weight, bias, y, residual=None, residual_out=None, scales=None, mean=None, rstd=None,
+                stream=None) -> None:
+        """y, and where given residual_out (= h; may be residual itself), scales ([rows, scale_cols] f32, with an
+        e4m3 y), mean and rstd ([rows] f32, which the backward pass needs).  weight, bias: or None."""
+        rows = x.shape[0]
+        shape = (rows, self.cols)
+        _here(self._who, "x", x)
+        xp, xs = self._rows("x", x, shape, self._x, self._xe)
+        rp, rs = self._rows("residual", residual, shape, self._res, self._rese)
+        op, os_ = self._rows("residual_out", residual_out, shape, self._res, self._rese)
+        yp, ys = self._rows("y", y, shape, self._y, self._ye)
+        rc = self._forward(self._ref, rows, xp, xs, rp, rs, self._flat("weight", weight, self.cols, self._w),
+                           self._flat("bias", bias, self.cols, self._w), op, os_, yp, ys,
+                           self._flat("scales", scales, rows * self.scale_cols, self._f32),
+                           self._flat("mean", mean, rows, self._f32), self._flat("rstd", rstd, rows, self._f32),
+                           D._stream(stream))
+        if rc:
+            D._check(rc)
+
+    def backward(self, dy, h, weight, mean, rstd, dx, dweight=None, dbias=None, dres=None, stream=None) -> None:
+        """dx ([rows, cols] in the residual's type: the gradient of x and of residual; may be dres itself)
+        and, where given, dweight and dbias ([cols] f32), from the forward's h, mean and rstd and the
+        gradients dy of y and dres of residual_out (None: zero)."""
+        rows = dy.shape[0]
+        shape = (rows, self.cols)
+        _here(self._who, "dy", dy)
+        gp, gs = self._rows("dy", dy, shape, self._x, self._xe)
+        hp, hs = self._rows("h", h, shape, self._res, self._rese)
+        sp, ss = self._rows("dres", dres, shape, self._res, self._rese)
+        xp, xs = self._rows("dx", dx, shape, self._res, self._rese)
+        flat = self._flat
+        args = (flat("weight", weight, self.cols, self._w), flat("mean", mean, rows, self._f32),
+                flat("rstd", rstd, rows, self._f32), sp, ss, xp, xs,
+                flat("dweight", dweight, self.cols, self._f32), flat("dbias", dbias, self.cols, self._f32))
+        ws, need = self._scratch(dweight is not None or dbias is not None, stream, dy.device)
+        rc = self._backward(self._ref, rows, gp, gs, hp, hs, *args, ws, need, D._stream(stream))
+        if rc:
+            D._check(rc)
+
+
+class ExpertRows:
+    """Tokens' rows sorted by the experts first .. first + experts - 1 that a rank holds, and back with weights,
+    and their gradients (dtt_experts_*: see there for the definitions).
+
+    top_k: choices of a token.  align: an expert's rows are filled up to a multiple of it, with zeros.  Keeps the
+    sort's workspace (allocated by the first `route`, in the order of that call's stream), so that one object
+    routes on one stream at a time (or the caller orders the streams); the other calls need none."""
+
+    _who = "ExpertRows"
+
+    def __init__(self, experts: int, top_k: int, first: int = 0, align: int = 1):
+        for name, v, most in (("experts", experts, 1024), ("top_k", top_k, 32), ("first", first, 2 ** 31 - 1), ("align", align, 65536)):
+            if not 0 <= v <= most:
+                raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be at most {most} and not negative, not {v}")
+        self.desc = D.dtt_experts_desc(experts, first, top_k, align)
+        need = C.c_uint64()
+        D._check(D.lib().dtt_experts_workspace(C.byref(self.desc), C.byref(need)))
+        self.experts, self.top_k, self.first, self.align = experts, top_k, first, align
+        self.workspace_bytes = need.value
+        self._workspace = None
+        self._ref = C.byref(self.desc)
+        import torch
+        self._i32, self._i64, self._f32 = torch.int32, torch.int64, torch.float32
+        self._row_types = {torch.bfloat16: D.BF16, torch.float32: D.F32}
+        L = D.lib()
+        self._route, self._dispatch, self._combine, self._combine_backward = (
+            L.dtt_experts_route, L.dtt_experts_dispatch, L.dtt_experts_combine, L.dtt_experts_combine_backward)
+
+    def most_rows(self, tokens: int) -> int:
+        """Rows that are always enough for so many tokens."""
+        return tokens * self.top_k + self.experts * (self.align - 1)
+
+    def _flat(self, name: str, t, shape, dtype) -> int:
+        """Address of a contiguous argument; 0 for None."""
+        if t is None:
+            return 0
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be contiguous {dtype} {list(shape)} on the GPU, "
+                                       f"not {t.dtype} {list(t.shape)}")
+        return t.data_ptr()
+
+    def _rows(self, name: str, t, rows, cols, dtypes=None) -> Tuple[int, int]:
+        """(address, pitch in bytes) of an argument of rows (None: any number) x cols; (0, 0) for None."""
+        if t is None:
+            return 0, 0
+        if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be [{'any' if rows is None else rows}, {cols}], not {list(t.shape)}")
+        if dtypes is not None and t.dtype not in dtypes:
+            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be one of {list(dtypes)}, not {t.dtype}")
+        row, col = t.stride()
+        if not t.is_cuda or (col != 1 and cols > 1):
+            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be on the GPU with contiguous rows")
+        return t.data_ptr(), row * t.element_size()
+
+    def _sorted(self, position, offsets, counts) -> Tuple[int, int, int]:
+        return (self._flat("position", position, (position.shape[0], self.top_k), self._i32),
+                self._flat("offsets", offsets, (self.experts + 1,), self._i32),
+                self._flat("counts", counts, (self.experts,), self._i32))
+
+    def route(self, ids, position, offsets, counts, max_rows: Optional[int] = None, stream=None) -> None:
+        """ids: [tokens, top_k] int32 or int64, any values (those that are not this rank's experts have no row).
+        position ([tokens, top_k] int32): each pair's row, or -1; offsets ([experts + 1] int32): where each expert's
+        rows begin; counts ([experts] int32): how many pairs it has.  max_rows: rows that there are room for
+        (None: most_rows(tokens)); pairs beyond get -1."""
+        _here(self._who, "ids", ids)
+        tokens = ids.shape[0]
+        ip = self._flat("ids", ids, (tokens, self.top_k), self._i64 if ids.dtype == self._i64 else self._i32)
+        pp = self._flat("position", position, (tokens, self.top_k), self._i32)
+        op, cp = self._flat("offsets", offsets, (self.experts + 1,), self._i32), self._flat("counts", counts, (self.experts,), self._i32)
+        if self._workspace is None or self._workspace.buffer.device != ids.device:
+            self._workspace = _Workspace.on(stream, self.workspace_bytes, ids.device)
+        self._workspace.use(stream)
+        rows = self.most_rows(tokens) if max_rows is None else max_rows
+        if not 0 <= rows < 2 ** 31:
+            raise D.DttError(D.EINVAL, f"ExpertRows: max_rows must be 0 .. 2^31 - 1, not {rows}")
+        rc = self._route(self._ref, tokens, ip, ids.element_size(), rows, pp, op, cp, self._workspace.address,
+                         self.workspace_bytes, D._stream(stream))
+        if rc:
+            D._check(rc)
+
+    def dispatch(self, x, position, offsets, counts, rows, scales=None, row_scales=None, stream=None) -> None:
+        """rows[position[t, j]] = x[t] (both of one type, any), and row_scales[position[t, j]] = scales[t] (f32, both or
+        neither); zeros in the rows that fill an expert's up; rows behind the last expert's are left as they were."""
+        _here(self._who, "x", x)
+        tokens, cols = x.shape[0], x.shape[-1]
+        xp, xs = self._rows("x", x, tokens, cols)
+        rp, rs = self._rows("rows", rows, None, cols, (x.dtype,))
+        pp, op, cp = self._sorted(position, offsets, counts)
+        if position.shape[0] != tokens:
+            raise D.DttError(D.EINVAL, f"ExpertRows: position is of {position.shape[0]} tokens, x of {tokens}")
+        sp = ss = tp = ts = n = 0
+        if scales is not None or row_scales is not None:
+            if scales is None or row_scales is None:
+                raise D.DttError(D.EINVAL, "ExpertRows: scales and row_scales go together")
+            n = scales.shape[-1]
+            sp, ss = self._rows("scales", scales, tokens, n, (self._f32,))
+            tp, ts = self._rows("row_scales", row_scales, rows.shape[0], n, (self._f32,))
+        rc = self._dispatch(self._ref, tokens, pp, op, cp, xp, xs, cols * x.element_size(), rp, rs, rows.shape[0],
+                            sp, ss, n, tp, ts, D._stream(stream))
+        if rc:
+            D._check(rc)
+
+    def combine(self, rows, position, out, weights=None, stream=None) -> None:
+        """out[t] = sum of weights[t, j] rows[position[t, j]] over the pairs with a row (rows, out: bf16 or f32; weights:
+        [tokens, top_k] f32).  weights None: 1, the gradient of `dispatch`, whose rows' gradient `rows` is then."""
+        _here(self._who, "out", out)
+        tokens, cols = out.shape[0], out.shape[-1]
+        op, os_ = self._rows("out", out, tokens, cols, self._row_types)
+        rp, rs = self._rows("rows", rows, None, cols, self._row_types)
+        pairs = (tokens, self.top_k)
+        rc = self._combine(self._ref, tokens, cols, self._flat("position", position, pairs, self._i32), rp,
+                           self._row_types[rows.dtype], rs, rows.shape[0], self._flat("weights", weights, pairs, self._f32),
+                           op, self._row_types[out.dtype], os_, D._stream(stream))
+        if rc:
+            D._check(rc)
+
+    def combine_backward(self, dout, rows, position, weights, offsets, counts, drows, dweights=None, stream=None) -> None:
+        """drows[position[t, j]] = weights[t, j] dout[t], zeros in the rows that fill an expert's up (those behind the last
+        expert's are left as they were), and where given dweights[t, j] = dout[t] . rows[position[t, j]] ([tokens, top_k]
+        f32, 0 for a pair without a row).  rows may be None without dweights; drows has its type."""
+        _here(self._who, "dout", dout)
+        tokens, cols = dout.shape[0], dout.shape[-1]
+        gp, gs = self._rows("dout", dout, tokens, cols, self._row_types)
+        dp, ds = self._rows("drows", drows, None, cols, self._row_types)
+        rp, rs = self._rows("rows", rows, drows.shape[0], cols, (drows.dtype,))
+        pp, op, cp = self._sorted(position, offsets, counts)
+        pairs = (tokens, self.top_k)
+        if position.shape != pairs:
+            raise D.DttError(D.EINVAL, f"ExpertRows: position is of {position.shape[0]} tokens, dout of {tokens}")
+        rc = self._combine_backward(self._ref, tokens, cols, pp, op, cp, gp, self._row_types[dout.dtype], gs, rp,
+                                    self._row_types[drows.dtype], rs, drows.shape[0],
+                                    self._flat("weights", weights, pairs, self._f32), dp, ds,
+                                    self._flat("dweights", dweights, pairs, self._f32), D._stream(stream))
+        if rc:
+            D._check(rc)
+
+
+class AdamW:
+    """AdamW over a list of tensors in one pass (owner of a dtt_adamw*; dtt_ops.h has the definition).
+
+    params, grads: lists of contiguous tensors, each list of one type, bf16 or f32.  m, v: the states, all f32, or all
+    torch.float8_e4m3fn with m_scales and v_scales (f32, `blocks(n)` of a tensor of n elements); zeros, scales
+    too, before the first step; v holds the root's codes then.  copies: bf16 tensors that get the new weights too
+    (with f32 weights; None in a place: none).  weight_decay: one for all or one a tensor.  seed: None, rounding
+    to nearest; 0 .. 2^32 - 1, rounding codes and bf16 weights at random.
+
+    The object keeps the tensors alive, and their addresses: a tensor must stay where it is."""
+
+    BLOCK = 128
+
+    @classmethod
+    def blocks(cls, n: int) -> int:
+        """Scales of a tensor of n elements with 8-bit states."""
+        return -(-n // cls.BLOCK)
+
+    def __init__(self, params: Sequence, grads: Sequence, m: Sequence, v: Sequence, m_scales: Optional[Sequence] = None,
+                 v_scales: Optional[Sequence] = None, copies: Optional[Sequence] = None, betas: Sequence[float] = (0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: Union[float, Sequence[float]] = 0.01, seed: Optional[int] = None):
+        import torch
+        self._h = None
+        who, count = "AdamW", len(params)
+        bf16, f32, e4m3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+        codes = {bf16: D.BF16, f32: D.F32, e4m3: D.E4M3}
+        if not count:
+            raise D.DttError(D.EINVAL, f"{who}: no tensors")
+        decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        small = m[0].dtype == e4m3 if len(m) else False
+        self._lists = {"params": list(params), "grads": list(grads), "m": list(m), "v": list(v)}
+        for name, given in (("m_scales", m_scales), ("v_scales", v_scales), ("copies", copies)):
+            self._lists[name] = [None] * count if given is None else list(given)
+        for name, ts in (*self._lists.items(), ("weight_decay", decay)):
+            if len(ts) != count:
+                raise D.DttError(D.EINVAL, f"{who}: {len(ts)} {name} for {count} params")
+        kinds = {"params": (params[0].dtype, (bf16, f32)), "grads": (grads[0].dtype, (bf16, f32)), "m": (m[0].dtype, (f32, e4m3)),
+                 "v": (m[0].dtype, (f32, e4m3)), "m_scales": (f32, (f32,)), "v_scales": (f32, (f32,)), "copies": (bf16, (bf16,))}
+        table = (D.dtt_adamw_tensor * count)()
+        for name, ts in self._lists.items():
+            dtype, allowed = kinds[name]
+            if dtype not in allowed:
+                raise D.DttError(D.EINVAL, f"{who}: {name} are {list(allowed)}, not {dtype}")
+            for i, t in enumerate(ts):
+                if t is None:
+                    if name == "copies" or (name in ("m_scales", "v_scales") and not small):
+                        continue
+                    raise D.DttError(D.EINVAL, f"{who}: {name}[{i}] is missing")
+                n = params[i].numel()
+                if t.dtype != dtype or t.numel() != (self.blocks(n) if name in ("m_scales", "v_scales") else n) or not t.is_contiguous():
+                    raise D.DttError(D.EINVAL, f"{who}: {name}[{i}] must be contiguous {dtype} of params[{i}]'s size, not "
+                                               f"{t.dtype} of {t.numel()} elements")
+                _here(who, f"{name}[{i}]", t)
+        for i, e in enumerate(table):
+            at = {name: ts[i].data_ptr() if ts[i] is not None and params[i].numel() else None for name, ts in self._lists.items()}
+            e.param, e.grad, e.m, e.v = at["params"], at["grads"], at["m"], at["v"]
+            e.m_scales, e.v_scales, e.copy = at["m_scales"], at["v_scales"], at["copies"]
+            e.n, e.weight_decay = params[i].numel(), decay[i]
+        if seed is not None and not 0 <= seed < 2 ** 32:
+            raise D.DttError(D.EINVAL, f"{who}: seed must be 0 .. 2^32 - 1, not {seed}")
+        self.desc = D.dtt_adamw_desc(codes[params[0].dtype], codes[grads[0].dtype], codes[m[0].dtype], seed is not None,
+                                     betas[0], betas[1], eps, seed or 0)
+        self.count, self._grad_type, self._device = count, grads[0].dtype, params[0].get_device()
+        self._f32, self._i32, self._current = f32, torch.int32, torch.cuda.current_device
+        out = C.c_void_p()
+        D._check(D.lib().dtt_adamw_create(C.byref(self.desc), table, count, C.byref(out)))
+        self._h = out
+        self._run = D.lib().dtt_adamw_run
+
+    def _scalar(self, name: str, t, dtype) -> int:
+        if t.dtype != dtype or t.numel() != 1 or not t.is_cuda or t.get_device() != self._device:
+            raise D.DttError(D.EINVAL, f"AdamW: {name} must be one {dtype} on the tensors' GPU")
+        return t.data_ptr()
+
+    def run(self, lr, step, grad_scale=None, grads: Optional[Sequence] = None, stream=None) -> None:
+        """One step.  lr: a number, or one f32 on the GPU.  step: its number, from 1, or one int32 on the GPU, the
+        steps made so far, which the call counts up (what a captured call needs).  grad_scale: one f32 on the GPU that
+        the gradients are multiplied by.  grads: this step's gradients where they are not the constructor's
+        (like these; the caller keeps them alive)."""
+        if self._current() != self._device:
+            raise D.DttError(D.EINVAL, "AdamW: the tensors' GPU must be the current one")
+        lr_at = step_at = 0
+        if not isinstance(lr, (int, float)):
+            lr, lr_at = 0.0, self._scalar("lr", lr, self._f32)
+        if not isinstance(step, int):
+            step, step_at = 0, self._scalar("step", step, self._i32)
+        elif not 1 <= step < 2 ** 32:
+            raise D.DttError(D.EINVAL, f"AdamW: step must be 1 .. 2^32 - 1, not {step}")
+        table = None
+        if grads is not None:
+            if len(grads) != self.count:
+                raise D.DttError(D.EINVAL, f"AdamW: {len(grads)} grads for {self.count} params")
+            for i, (g, p) in enumerate(zip(grads, self._lists["params"])):
+                if g.dtype != self._grad_type or g.numel() != p.numel() or not g.is_contiguous() or g.get_device() != self._device:
+                    raise D.DttError(D.EINVAL, f"AdamW: grads[{i}] must be like the constructor's")
+            table = D._ptr_array(grads)
+        rc = self._run(self._h, table, lr, step, lr_at, step_at,
+                       0 if grad_scale is None else self._scalar("grad_scale", grad_scale, self._f32), D._stream(stream))
+        if rc:
+            D._check(rc)
+
+    def close(self) -> None:
+        if self._h is not None and self._h.value:
+            D.lib().dtt_adamw_destroy(self._h)
+            self._h = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+        return False
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class Orthogonalizer:

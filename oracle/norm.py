@@ -1,5 +1,5 @@
-"""Residual addition with a root-mean-square norm, and its backward pass, from their definitions in
-64 bits (numpy)."""
+"""Residual addition with a root-mean-square norm or a layer norm, and their backward passes, from their
+definitions in 64 bits (numpy)."""
 import numpy as np
 
 E4M3_MAX, SCALE_MIN = 448.0, 2.0 ** -100
@@ -33,3 +33,24 @@ def backward(dy, h, weight, rstd, dres):
     g = dy if weight is None else dy * weight.astype(np.float64)
     dx = s * (g - n * (g * n).mean(axis=1, keepdims=True))
     return dx if dres is None else dx + dres.astype(np.float64), (dy * n).sum(axis=0)
+
+
+def layer_forward(x, residual, weight, bias, eps):
+    """(h, mean, rstd, y) for rows x cols arrays (residual, weight, bias: or None)."""
+    h = x.astype(np.float64) if residual is None else x.astype(np.float64) + residual.astype(np.float64)
+    mean = h.mean(axis=1)
+    d = h - mean[:, None]
+    rstd = 1.0 / np.sqrt((d * d).mean(axis=1) + eps)
+    y = d * rstd[:, None]
+    if weight is not None:
+        y = y * weight.astype(np.float64)
+    return h, mean, rstd, y if bias is None else y + bias.astype(np.float64)
+
+
+def layer_backward(dy, h, weight, mean, rstd, dres):
+    """(dx, dweight, dbias)."""
+    dy, s = dy.astype(np.float64), rstd.astype(np.float64)[:, None]
+    n = (h.astype(np.float64) - mean.astype(np.float64)[:, None]) * s
+    g = dy if weight is None else dy * weight.astype(np.float64)
+    dx = s * (g - g.mean(axis=1, keepdims=True) - n * (g * n).mean(axis=1, keepdims=True))
+    return dx if dres is None else dx + dres.astype(np.float64), (dy * n).sum(axis=0), dy.sum(axis=0)
