@@ -21,7 +21,7 @@ namespace {
 constexpr uint32_t kThreads = 256, kChunk = 8 * kThreads;      // elements of a CTA
 constexpr uint32_t kBlock = DTT_ADAMW_BLOCK;                   // elements of a scale: 16 threads' or 4 of each lane's
 constexpr float kCodeMax = 448.0f, kScaleLeast = 0x1p-100f;
-constexpr float kCodeLeast = 0x1p-9f, kCodeNormal = 0x1p-6f;   // e4m3's smallest values: of all, of the normal ones
+constexpr float kCodeLeast = 0x1p-9f;                          // e4m3's smallest value above zero
 constexpr uint64_t kMostElements = 1ull << 40;
 
 struct Tensor {
@@ -34,7 +34,8 @@ struct Tensor {
     uint16_t* copy;             // or null
     uint64_t n;
     float decay;
-    uint32_t lead;              // elements before the first, counted so that every eighth is 16-byte aligned; kElements: none is
+    uint32_t lead;              // pointers (not the scales') are moved back by so many elements, from where every eighth is 16-byte
+                                // aligned (codes: 8-byte); kElements: there is no such place for all of them
 };
 constexpr uint32_t kElements = 8;
 
@@ -68,9 +69,13 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 constexpr uint32_t kGolden = 0x9E3779B9u, kThird = 0x2E1B2139u;
 
+__device__ __forceinline__ uint32_t random_bits(uint64_t i, uint32_t seed) {
+    return mix((uint32_t)i * kGolden + seed + (uint32_t)(i >> 32) * kThird);
+}
+
 __device__ __forceinline__ float root_of(float v) {
     float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
 
@@ -91,18 +96,21 @@ __device__ __forceinline__ Rates rates_of(const Scalars& s) {
     return r;
 }
 
-// Up with the probability of what lies below: a random number in the place of the bits that are cut off.  Below
-// e4m3's normal values the spacing stays that of [2^-6, 2^-5), which is where they are moved for it.  What is
-// not finite is left as it is.
-__device__ __forceinline__ float stochastic_e4m3(float x, uint32_t noise16) {
-    const float size = fabsf(x), low = size < kCodeNormal ? kCodeNormal : 0.0f;
-    const float up = __uint_as_float((__float_as_uint(size + low) + (noise16 << 4)) & 0xFFF00000u) - low;
-    return size <= 2 * kCodeMax ? copysignf(up, x) : x;
+// Up with the probability of what lies below: a random number in the place of the bits that are cut off, the
+// noise's 16 bits (at bit 4) in that of the highest of them.  x 2^-120 has e4m3's exponents and its subnormal values
+// where f32 has its own, so that the code is bits 20 to 26 of the magnitude; it comes back in the highest byte,
+// without the sign.  A NaN becomes 448's code, as what is past it.  The sum comes before the shift: of the highest byte of
+// (x << 4) + noise, with nothing else asked for, CUDA 13.0's compiler leaves out the x.
+__device__ __forceinline__ uint32_t stochastic_code(float x, uint32_t noise) {
+    return (__float_as_uint(fminf(fabsf(x), kCodeMax) * 0x1p-120f) + noise) << 4;
 }
+__device__ __forceinline__ uint32_t noise_m(uint32_t r) { return r >> 12 & 0xFFFF0u; }      // r's high 16 bits at bit 4
+__device__ __forceinline__ uint32_t noise_v(uint32_t r) { return r << 4 & 0xFFFF0u; }       // its low ones
+
 __device__ __forceinline__ float stochastic_bf16(float x, uint32_t noise16) {
-    const float up = __uint_as_float((__float_as_uint(x) + noise16) & 0xFFFF0000u);
-    return fabsf(x) < __builtin_inff() ? up : x;
+    return isnan(x) ? x : __uint_as_float(__float_as_uint(x) + noise16);       // what is cut off is cut off when it is packed
 }
+__device__ __forceinline__ uint32_t pack_cut(float lo, float hi) { return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632); }
 
 // One element.  root: sqrt(v), where states are codes.
 template <bool S8>
@@ -124,18 +132,27 @@ __device__ __forceinline__ Scale scale_from(float top) {
     return {scale, 1.0f / scale};
 }
 
-// The code of m, and of a root, which stays above zero: the next step divides by it.
+// The codes of N elements' m and of their roots, which stay above zero: the next step divides by them.  noise: the
+// elements' random bits.  16 bits hold two codes; poisoned: 0x7F7F where the block has a NaN, else 0.
 template <bool SR>
-__device__ __forceinline__ float moment_code(float m, float inv, uint32_t noise) {
-    const float x = m * inv;
-    return SR ? stochastic_e4m3(x, noise >> 16) : x;
+__device__ __forceinline__ uint32_t moment_codes(float a, float b, float inv, uint32_t ra, uint32_t rb, uint32_t poisoned) {
+    a *= inv;
+    b *= inv;
+    if (!SR) return pack_e4m3(a, b);
+    const uint32_t codes = __byte_perm(stochastic_code(a, noise_m(ra)), stochastic_code(b, noise_m(rb)), 0x0073);
+    const uint32_t signs = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0073) & 0x8080u;
+    return (codes & 0xFFFFu) | signs | poisoned;
 }
 template <bool SR>
-__device__ __forceinline__ float root_code(float root, float inv, uint32_t noise) {
-    float x = root * inv;
-    if (SR) x = stochastic_e4m3(x, noise & 0xFFFFu);
-    return root == 0.0f ? 0.0f : max_nan(x, kCodeLeast);
+__device__ __forceinline__ uint32_t root_codes(float a, float b, float inv, uint32_t ra, uint32_t rb, uint32_t poisoned) {
+    if (!SR)
+        return pack_e4m3(a == 0.0f ? 0.0f : max_nan(a * inv, kCodeLeast), b == 0.0f ? 0.0f : max_nan(b * inv, kCodeLeast));
+    // a root is zero or normal: twice its bits are then 2^24 at least, the place of the smallest code
+    const uint32_t least_a = min(__float_as_uint(a) << 1, 1u << 24), least_b = min(__float_as_uint(b) << 1, 1u << 24);
+    const uint32_t code_a = max(stochastic_code(a * inv, noise_v(ra)), least_a), code_b = max(stochastic_code(b * inv, noise_v(rb)), least_b);
+    return (__byte_perm(code_a, code_b, 0x0073) & 0xFFFFu) | poisoned;
 }
+__device__ __forceinline__ uint32_t poisoned(float top) { return isnan(top) ? 0x7F7Fu : 0u; }
 
 __device__ __forceinline__ void unpack_e4m3(uint32_t pair, float& lo, float& hi) {
     uint32_t h;
@@ -183,13 +200,10 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
         update<S8>(p[k], g[k], m[k], v[k], root[k], keep, r, s);
         if (i0 + 32 * k >= t.n) m[k] = root[k] = 0.0f;
     }
-    uint32_t noise[8];
+    uint32_t noise[8] = {}, code_m[4], code_v[4];
     if (SR) {
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-            const uint64_t i = i0 + 32 * k;
-            noise[k] = mix((uint32_t)i * kGolden + seed + (uint32_t)(i >> 32) * kThird);
-        }
+        for (uint32_t k = 0; k < 8; ++k) noise[k] = random_bits(i0 + 32 * k, seed);
     }
     if (S8) {
 #pragma unroll
@@ -200,17 +214,18 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
                 tm = max_nan(tm, fabsf(m[k]));
                 tr = max_nan(tr, root[k]);
             }
-            const Scale sm = scale_from(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tm))));
-            const Scale sr = scale_from(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tr) & 0x7FFFFFFFu)));
+            tm = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tm)));
+            tr = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tr) & 0x7FFFFFFFu));
+            const Scale sm = scale_from(tm), sr = scale_from(tr);
             const uint64_t i = i0 + 32 * b;
             if (threadIdx.x % 32 == 0 && i < t.n) {
                 t.ms[i / kBlock] = sm.scale;
                 t.vs[i / kBlock] = sr.scale;
             }
 #pragma unroll
-            for (uint32_t k = b; k < b + 4; ++k) {
-                m[k] = moment_code<SR>(m[k], sm.inv, SR ? noise[k] : 0);
-                v[k] = root_code<SR>(root[k], sr.inv, SR ? noise[k] : 0);
+            for (uint32_t k = b; k < b + 4; k += 2) {
+                code_m[k / 2] = moment_codes<SR>(m[k], m[k + 1], sm.inv, noise[k], noise[k + 1], poisoned(tm));
+                code_v[k / 2] = root_codes<SR>(root[k], root[k + 1], sr.inv, noise[k], noise[k + 1], poisoned(tr));
             }
         }
     }
@@ -219,17 +234,146 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
         const uint64_t i = i0 + 32 * k;
         if (i >= t.n) break;
         if (S8) {
-            reinterpret_cast<uint8_t*>(t.m)[i] = (uint8_t)pack_e4m3(m[k], 0.0f);
-            reinterpret_cast<uint8_t*>(t.v)[i] = (uint8_t)pack_e4m3(v[k], 0.0f);
+            reinterpret_cast<uint8_t*>(t.m)[i] = (uint8_t)(code_m[k / 2] >> 8 * (k % 2));
+            reinterpret_cast<uint8_t*>(t.v)[i] = (uint8_t)(code_v[k / 2] >> 8 * (k % 2));
         } else {
             reinterpret_cast<float*>(t.m)[i] = m[k];
             reinterpret_cast<float*>(t.v)[i] = v[k];
         }
         if (P == DTT_BF16)
-            reinterpret_cast<uint16_t*>(t.p)[i] = (uint16_t)pack_bf16(SR ? stochastic_bf16(p[k], noise[k] * kThird >> 16) : p[k], 0.0f);
+            reinterpret_cast<uint16_t*>(t.p)[i] = SR ? (uint16_t)pack_cut(stochastic_bf16(p[k], noise[k] * kThird >> 16), 0.0f) : (uint16_t)pack_bf16(p[k], 0.0f);
         else
             reinterpret_cast<float*>(t.p)[i] = p[k];
-        if (t.copy) t.copy[i] = (uint16_t)pack_bf16(p[k], 0.0f);
+        if (P == DTT_F32 && t.copy) t.copy[i] = (uint16_t)pack_bf16(p[k], 0.0f);
+    }
+}
+
+// 8 neighbouring elements from `at`, of which [lo, hi) are the tensor's.
+template <uint32_t DT>
+__device__ __forceinline__ Raw8 raw_group(const char* base, uint64_t at) {
+    return raw8(base + at * (DT == DTT_BF16 ? 2 : 4), DT);
+}
+template <uint32_t DT>
+__device__ __forceinline__ void store_group(char* base, uint64_t at, const float (&v)[8]) {
+    store8<true>(base + at * (DT == DTT_BF16 ? 2 : 4), DT, 0, 8, v);
+}
+
+// Eight neighbouring elements a thread, a block of 128 sixteen lanes.  Pointers are those of the element `lead` places before
+// the first, so that every eighth from there is aligned; the groups at the tensor's ends that it does not fill go
+// element by element.
+template <uint32_t P, uint32_t G, bool S8, bool SR>
+__device__ __forceinline__ void chunk_by_groups(const Tensor& t, uint64_t at, uint32_t seed, const Rates& r, const Scalars& s) {
+    const uint64_t i = at + 8 * threadIdx.x, from = t.lead, to = t.lead + t.n;
+    const bool whole = i >= from && i + 8 <= to;
+    const float keep = 1.0f - r.lr * t.decay;
+    float p[8], g[8], m[8], v[8], root[8];
+    if (whole) {
+        const Raw8 gs = raw_group<G>(t.g, i), ps = raw_group<P>(t.p, i);
+        if (S8) {
+            const uint2 cm = *reinterpret_cast<const uint2*>(t.m + i), cv = *reinterpret_cast<const uint2*>(t.v + i);
+            const float sm = t.ms[i / kBlock], sv = t.vs[i / kBlock];
+            unpack8(cm, m);
+            unpack8(cv, v);
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                m[k] *= sm;
+                v[k] *= sv;
+                v[k] *= v[k];
+            }
+        } else {
+            const Raw8 a = raw_group<DTT_F32>(t.m, i), b = raw_group<DTT_F32>(t.v, i);
+            expand8(a, DTT_F32, m);
+            expand8(b, DTT_F32, v);
+        }
+        expand8(gs, G, g);
+        expand8(ps, P, p);
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            p[k] = g[k] = m[k] = v[k] = 0.0f;
+            if (i + k < from || i + k >= to) continue;
+            p[k] = element<P>(t.p, i + k);
+            g[k] = element<G>(t.g, i + k);
+            if (S8) {
+                float none;
+                unpack_e4m3(reinterpret_cast<const uint8_t*>(t.m)[i + k], m[k], none);
+                unpack_e4m3(reinterpret_cast<const uint8_t*>(t.v)[i + k], v[k], none);
+                m[k] *= t.ms[i / kBlock];
+                v[k] *= t.vs[i / kBlock];
+                v[k] *= v[k];
+            } else {
+                m[k] = element<DTT_F32>(t.m, i + k);
+                v[k] = element<DTT_F32>(t.v, i + k);
+            }
+        }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) update<S8>(p[k], g[k], m[k], v[k], root[k], keep, r, s);
+    uint32_t noise[8] = {};
+    if (SR) {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) noise[k] = random_bits(i + k - from, seed);
+    }
+    uint2 cm{}, cv{};
+    if (S8) {
+        float tm = 0.0f, tr = 0.0f;             // elements that are not the tensor's have m and root 0
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            tm = max_nan(tm, fabsf(m[k]));
+            tr = max_nan(tr, root[k]);
+        }
+#pragma unroll
+        for (uint32_t d = 1; d < kBlock / 8; d *= 2) {
+            tm = max_nan(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, d));
+            tr = max_nan(tr, __shfl_xor_sync(0xFFFFFFFFu, tr, d));
+        }
+        const Scale sm = scale_from(tm), sr = scale_from(tr);
+        if (threadIdx.x % (kBlock / 8) == 0 && i < to) {
+            t.ms[i / kBlock] = sm.scale;
+            t.vs[i / kBlock] = sr.scale;
+        }
+        uint32_t c[4], d[4];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; k += 2) {
+            c[k / 2] = moment_codes<SR>(m[k], m[k + 1], sm.inv, noise[k], noise[k + 1], poisoned(tm));
+            d[k / 2] = root_codes<SR>(root[k], root[k + 1], sr.inv, noise[k], noise[k + 1], poisoned(tr));
+        }
+        cm = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        cv = make_uint2(d[0] | d[1] << 16, d[2] | d[3] << 16);
+    }
+    float q[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) q[k] = P == DTT_BF16 && SR ? stochastic_bf16(p[k], noise[k] * kThird >> 16) : p[k];
+    if (whole) {
+        if (S8) {
+            *reinterpret_cast<uint2*>(t.m + i) = cm;
+            *reinterpret_cast<uint2*>(t.v + i) = cv;
+        } else {
+            store_group<DTT_F32>(t.m, i, m);
+            store_group<DTT_F32>(t.v, i, v);
+        }
+        if (P == DTT_BF16 && SR)
+            *reinterpret_cast<uint4*>(t.p + 2 * i) = make_uint4(pack_cut(q[0], q[1]), pack_cut(q[2], q[3]), pack_cut(q[4], q[5]), pack_cut(q[6], q[7]));
+        else
+            store_group<P>(t.p, i, p);
+        if (P == DTT_F32 && t.copy) store_group<DTT_BF16>(reinterpret_cast<char*>(t.copy), i, p);
+        return;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        if (i + k < from || i + k >= to) continue;
+        if (S8) {
+            reinterpret_cast<uint8_t*>(t.m)[i + k] = (uint8_t)((k < 4 ? cm.x : cm.y) >> 8 * (k % 4));
+            reinterpret_cast<uint8_t*>(t.v)[i + k] = (uint8_t)((k < 4 ? cv.x : cv.y) >> 8 * (k % 4));
+        } else {
+            reinterpret_cast<float*>(t.m)[i + k] = m[k];
+            reinterpret_cast<float*>(t.v)[i + k] = v[k];
+        }
+        if (P == DTT_BF16)
+            reinterpret_cast<uint16_t*>(t.p)[i + k] = SR ? (uint16_t)pack_cut(q[k], 0.0f) : (uint16_t)pack_bf16(p[k], 0.0f);
+        else
+            reinterpret_cast<float*>(t.p)[i + k] = p[k];
+        if (P == DTT_F32 && t.copy) t.copy[i + k] = (uint16_t)pack_bf16(p[k], 0.0f);
     }
 }
 
@@ -248,7 +392,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const Rates r = rates_of(b.s);
     uint32_t seed = 0;
     if (SR) seed = mix(mix(b.s.seed + r.step) + b.number + lo);
-    chunk_by_elements<P, G, S8, SR>(t, at, seed, r, b.s);
+    if (t.lead < kElements) chunk_by_groups<P, G, S8, SR>(t, at, seed, r, b.s);
+    else chunk_by_elements<P, G, S8, SR>(t, at, seed, r, b.s);
 }
 
 __global__ void adamw_advance_kernel(uint32_t* step) {
@@ -274,9 +419,29 @@ struct Kernels {
     }
 };
 
-uint32_t bytes_of(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
+uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4 : 1; }
 
 bool misaligned(const void* p, uint32_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+// By groups where all of a tensor's pointers are aligned at the same element, with 8-bit states the first, where its
+// blocks begin.
+Tensor tensor_of(const dtt_adamw_desc& d, const dtt_adamw_tensor& t, const void* grad) {
+    Tensor r{static_cast<char*>(t.param), static_cast<const char*>(grad), static_cast<char*>(t.m), static_cast<char*>(t.v), t.m_scales, t.v_scales,
+             static_cast<uint16_t*>(t.copy), t.n, t.weight_decay, kElements};
+    const uint32_t pe = elem_bytes(d.param_dtype), ge = elem_bytes(d.grad_dtype), se = elem_bytes(d.state_dtype);
+    const auto off = [](const void* p, uint32_t size, uint32_t lead) { return (reinterpret_cast<uintptr_t>(p) - lead * size) % std::min(16u, 8 * size) != 0; };
+    for (uint32_t lead = 0; lead < (d.state_dtype == DTT_E4M3 ? 1 : kElements); ++lead) {
+        if (off(r.p, pe, lead) || off(r.g, ge, lead) || off(r.m, se, lead) || off(r.v, se, lead) || (r.copy && off(r.copy, 2, lead))) continue;
+        r.lead = lead;
+        r.p -= lead * pe;
+        r.g -= lead * ge;
+        r.m -= lead * se;
+        r.v -= lead * se;
+        if (r.copy) r.copy -= lead;
+        break;
+    }
+    return r;
+}
 
 }  // namespace
 
@@ -286,7 +451,7 @@ cudaError_t preload_adamw_kernels() {
         dtt_adamw_desc d{};
         d.param_dtype = k & 1 ? DTT_BF16 : DTT_F32;
         d.grad_dtype = k & 2 ? DTT_BF16 : DTT_F32;
-        d.state_dtype = k & 4 ? DTT_E4M3 : DTT_F32;
+        d.state_dtype = k & 4 ? (uint32_t)DTT_E4M3 : (uint32_t)DTT_F32;
         d.stochastic = k >> 3;
         e = prepare_kernel(Kernels<kFew>::of(d));
         if (e == cudaSuccess) e = prepare_kernel(Kernels<kMany>::of(d));
@@ -319,11 +484,9 @@ int run_batches(const dtt_adamw& o, const void* const* grads, const Scalars& s, 
             // an empty tensor between two of a launch would shift the numbers after it
             if (o.number[i] != b.number + k) break;
             const dtt_adamw_tensor& t = o.tensors[i];
-            const uint64_t need = (t.n + kChunk - 1) / kChunk;
+            b.t[k] = tensor_of(o.d, t, grads ? grads[o.number[i]] : t.grad);
+            const uint64_t need = (t.n + b.t[k].lead % kElements + kChunk - 1) / kChunk;
             if (chunks + need > 0x7FFFFFFFull) break;
-            b.t[k] = Tensor{static_cast<char*>(t.param), static_cast<const char*>(grads ? grads[o.number[i]] : t.grad),
-                            static_cast<char*>(t.m), static_cast<char*>(t.v), t.m_scales, t.v_scales,
-                            static_cast<uint16_t*>(t.copy), t.n, t.weight_decay, kElements};
             b.first[k] = chunks;
             chunks += (uint32_t)need;
         }
@@ -351,7 +514,7 @@ extern "C" int dtt_adamw_create(const dtt_adamw_desc* d, const dtt_adamw_tensor*
     if (!(d->eps >= 0x1p-100f) || !std::isfinite(d->eps)) return fail(DTT_EINVAL, "%s: eps must be finite and 2^-100 at least", who);
     if (count && !tensors) return fail(DTT_EINVAL, "%s: null tensors", who);
     const bool s8 = d->state_dtype == DTT_E4M3;
-    const uint32_t pe = bytes_of(d->param_dtype), ge = bytes_of(d->grad_dtype), se = bytes_of(d->state_dtype);
+    const uint32_t pe = elem_bytes(d->param_dtype), ge = elem_bytes(d->grad_dtype), se = elem_bytes(d->state_dtype);
     for (uint32_t i = 0; i < count; ++i) {
         const dtt_adamw_tensor& t = tensors[i];
         if (!std::isfinite(t.weight_decay)) return fail(DTT_EINVAL, "%s: tensor %u: the decay must be finite", who, i);
@@ -395,7 +558,7 @@ extern "C" int dtt_adamw_run(dtt_adamw* o, const void* const* grads, float lr, u
     if (grads)
         for (size_t i = 0; i < o->tensors.size(); ++i) {
             const void* g = grads[o->number[i]];
-            if (!g || misaligned(g, bytes_of(o->d.grad_dtype)))
+            if (!g || misaligned(g, elem_bytes(o->d.grad_dtype)))
                 return fail(DTT_EINVAL, "%s: gradient %u is missing or not aligned to its elements", who, o->number[i]);
         }
     const dtt_adamw_desc& d = o->d;
