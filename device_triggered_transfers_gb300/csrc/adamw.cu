@@ -23,6 +23,12 @@ constexpr uint32_t kBlock = DTT_ADAMW_BLOCK;                   // elements of a 
 constexpr float kCodeMax = 448.0f, kScaleLeast = 0x1p-100f;
 constexpr float kCodeLeast = 0x1p-9f;                          // e4m3's smallest value above zero
 constexpr uint64_t kMostElements = 1ull << 40;
+// 8-bit states: where there are many elements a CTA takes several chunks, whose copies go out together and which share
+// the search for the tensor and the step's numbers.  32M weights: 88 us with one chunk a CTA, straight from global memory, 59 with
+// four.  (f32 states: 715 us with one at 151M weights; two or three by way of shared memory 766 to 789, reads that run
+// further ahead of the writes cost more than they hide.)
+constexpr uint32_t kTurns = 4;
+constexpr uint64_t kManyElements = 4ull * kTurns * kChunk * kSms;
 
 struct Tensor {
     char* p;
@@ -36,28 +42,33 @@ struct Tensor {
     float decay;
     uint32_t lead;              // pointers (not the scales') are moved back by so many elements, from where every eighth is 16-byte
                                 // aligned (codes: 8-byte); kElements: there is no such place for all of them
+    uint32_t number;            // in the caller's list
 };
 constexpr uint32_t kElements = 8;
 
 struct Scalars {
-    float beta1, beta2, one_less_beta1, one_less_beta2, eps;
+    float beta1, beta2, root_beta2;     // root_beta2: its square root, as the next's
+    float one_less_beta1, root_one_less_beta2;
+    float eps;
     float lr, lr_by_c1, root_c2;        // by the host's step: lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
     float log_beta1, log_beta2;         // for the device's step
     const float* lr_dev;                // or null
     const uint32_t* step_dev;           // or null
     const float* grad_scale;            // or null
     uint32_t step, seed;                // seed: mixed once
+    uint32_t sixteen;                   // 16 (stochastic_code)
 };
 
 template <uint32_t N>
 struct Batch {
     Tensor t[N];
-    uint32_t first[N + 1];              // chunk that tensor i begins with
-    uint32_t count, number;             // number: of t[0] in the whole list
+    uint32_t first[N + 1];              // CTA that tensor i begins with
+    uint32_t count;
+    uint32_t turns;                     // chunks that a CTA takes one after the other
     Scalars s;
 };
 // Arguments end at 32764 bytes.
-constexpr uint32_t kFew = 48, kMany = 384;
+constexpr uint32_t kFew = 44, kMany = 384;
 static_assert(sizeof(Batch<kMany>) <= 32764 && sizeof(Batch<kFew>) <= 4096, "the tables of tensors travel as arguments");
 
 // 32 bits from 32: products with odd numbers (fractional digits of pi and e) carry every bit upwards, shifts bring
@@ -73,19 +84,52 @@ __device__ __forceinline__ uint32_t random_bits(uint64_t i, uint32_t seed) {
     return mix((uint32_t)i * kGolden + seed + (uint32_t)(i >> 32) * kThird);
 }
 
+// ---- pairs: two f32 an instruction -------------------------------------------------------------
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ float2 apart(Pair a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 __device__ __forceinline__ float root_of(float v) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 
 // What a step's formula needs, by the host or by the device's own step and rate.
 struct Rates {
-    float lr, lr_by_c1, root_c2, gs;
+    float lr, lr_by_c1, root_c2;
+    float g_m, g_v;             // what the gradient enters m and, squared, v with
     uint32_t step;
 };
 __device__ __forceinline__ Rates rates_of(const Scalars& s) {
-    Rates r{s.lr, s.lr_by_c1, s.root_c2, s.grad_scale ? *s.grad_scale : 1.0f, s.step};
+    const float gs = s.grad_scale ? *s.grad_scale : 1.0f;
+    Rates r{s.lr, s.lr_by_c1, s.root_c2, s.one_less_beta1 * gs, s.root_one_less_beta2 * gs, s.step};
     if (s.lr_dev || s.step_dev) {
         if (s.lr_dev) r.lr = *s.lr_dev;
         if (s.step_dev) r.step = *s.step_dev;
@@ -96,63 +140,86 @@ __device__ __forceinline__ Rates rates_of(const Scalars& s) {
     return r;
 }
 
-// Up with the probability of what lies below: a random number in the place of the bits that are cut off, the
-// noise's 16 bits (at bit 4) in that of the highest of them.  x 2^-120 has e4m3's exponents and its subnormal values
-// where f32 has its own, so that the code is bits 20 to 26 of the magnitude; it comes back in the highest byte,
-// without the sign.  A NaN becomes 448's code, as what is past it.  The sum comes before the shift: of the highest byte of
-// (x << 4) + noise, with nothing else asked for, CUDA 13.0's compiler leaves out the x.
-__device__ __forceinline__ uint32_t stochastic_code(float x, uint32_t noise) {
-    return (__float_as_uint(fminf(fabsf(x), kCodeMax) * 0x1p-120f) + noise) << 4;
-}
-__device__ __forceinline__ uint32_t noise_m(uint32_t r) { return r >> 12 & 0xFFFF0u; }      // r's high 16 bits at bit 4
-__device__ __forceinline__ uint32_t noise_v(uint32_t r) { return r << 4 & 0xFFFF0u; }       // its low ones
-
-__device__ __forceinline__ float stochastic_bf16(float x, uint32_t noise16) {
-    return isnan(x) ? x : __uint_as_float(__float_as_uint(x) + noise16);       // what is cut off is cut off when it is packed
-}
-__device__ __forceinline__ uint32_t pack_cut(float lo, float hi) { return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632); }
-
-// One element.  root: sqrt(v), where states are codes.
+// m and v, as the old ones or as codes with what their scales make of them: m_by and v_by are beta1 and beta2, or the
+// scales times beta1 and sqrt(beta2).  root: sqrt(v).
 template <bool S8>
-__device__ __forceinline__ void update(float& p, float g, float& m, float& v, float& root, float keep, const Rates& r, const Scalars& s) {
-    g *= r.gs;
-    m = fmaf(s.beta1, m, s.one_less_beta1 * g);
-    v = fmaf(s.beta2, v, (s.one_less_beta2 * g) * g);
-    root = root_of(v);
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(root, r.root_c2, s.eps)));
-    p = fmaf(p, keep, -r.lr_by_c1 * (m * inv));
+__device__ __forceinline__ void update(Pair& p, Pair g, Pair& m, Pair& v, float2& root, float m_by, float v_by, float keep, const Rates& r, float eps) {
+    m = fma2(m, both(m_by), g * both(r.g_m));
+    const Pair gv = g * both(r.g_v);
+    if (S8) {
+        v = v * both(v_by);
+        v = fma2(v, v, gv * gv);
+    } else {
+        v = fma2(v, both(v_by), gv * gv);
+    }
+    const float2 a = apart(v);
+    root = make_float2(root_of(a.x), root_of(a.y));
+    const float2 d = apart(fma2(pair(root.x, root.y), both(r.root_c2), both(eps)));
+    p = fma2(m * pair(reciprocal(d.x), reciprocal(d.y)), both(-r.lr_by_c1), p * both(keep));
 }
 
+// ---- codes ---------------------------------------------------------------------------------------
 struct Scale {
-    float scale, inv;
+    float scale, inv;           // top inv is 448 at most
 };
 __device__ __forceinline__ Scale scale_from(float top) {
     const float scale = max_nan(top * (1.0f / kCodeMax), kScaleLeast);
-    return {scale, 1.0f / scale};
+    float inv = reciprocal(scale);
+    if (top * inv > kCodeMax) inv *= 1.0f - 0x1p-22f;
+    return {scale, inv};
 }
 
-// The codes of N elements' m and of their roots, which stay above zero: the next step divides by them.  noise: the
-// elements' random bits.  16 bits hold two codes; poisoned: 0x7F7F where the block has a NaN, else 0.
+// Up with the probability of what lies below: a random number in the place of the bits that are cut off, the
+// noise's 16 bits (at bit 8) in that of the highest of them.  x, 448 at most, times 2^-120 has e4m3's exponents and its
+// subnormal values where f32 has its own, so that the code is bits 20 to 26 of the magnitude; it comes back in the
+// highest byte, and the sign is shifted out.  The shift by 4 is a product with a number that the compiler does not know: of
+// the highest byte of (x << 4) + noise, with nothing else asked for, CUDA 13.0's leaves out the x.
+constexpr float kCodeUnit = 0x1p-120f;
+__device__ __forceinline__ uint32_t stochastic_code(float x, uint32_t noise, uint32_t sixteen) {
+    uint32_t r;
+    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(r) : "r"(__float_as_uint(x)), "r"(sixteen), "r"(noise));
+    return r;
+}
+__device__ __forceinline__ uint32_t noise_m(uint32_t r) { return __byte_perm(r, 0, 0x4324); }      // r's high 16 bits at bit 8
+__device__ __forceinline__ uint32_t noise_v(uint32_t r) { return __byte_perm(r, 0, 0x4104); }      // its low ones
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// The same of bf16; what is cut off is cut off when it is packed.
+__device__ __forceinline__ uint32_t stochastic_bf16(float x, uint32_t r) { return __float_as_uint(x) + (r * kThird >> 16); }
+__device__ __forceinline__ uint32_t pack_cut(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7632); }
+
+// Four elements' codes of m and of their roots, which stay above zero: the next step divides by them.  r: the
+// elements' random bits.
 template <bool SR>
-__device__ __forceinline__ uint32_t moment_codes(float a, float b, float inv, uint32_t ra, uint32_t rb, uint32_t poisoned) {
-    a *= inv;
-    b *= inv;
-    if (!SR) return pack_e4m3(a, b);
-    const uint32_t codes = __byte_perm(stochastic_code(a, noise_m(ra)), stochastic_code(b, noise_m(rb)), 0x0073);
-    const uint32_t signs = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0073) & 0x8080u;
-    return (codes & 0xFFFFu) | signs | poisoned;
+__device__ __forceinline__ uint32_t moment_codes(const Pair (&m)[2], float inv, const uint32_t* r, uint32_t sixteen) {
+    const Pair x[2] = {m[0] * both(inv), m[1] * both(inv)};
+    const float2 a = apart(x[0]), b = apart(x[1]);
+    if (!SR) return pack_e4m3(a.x, a.y) | pack_e4m3(b.x, b.y) << 16;
+    const float2 c = apart(x[0] * both(kCodeUnit)), d = apart(x[1] * both(kCodeUnit));
+    const uint32_t codes = top_bytes(stochastic_code(c.x, noise_m(r[0]), sixteen), stochastic_code(c.y, noise_m(r[1]), sixteen),
+                                     stochastic_code(d.x, noise_m(r[2]), sixteen), stochastic_code(d.y, noise_m(r[3]), sixteen));
+    return codes | (top_bytes(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)) & 0x80808080u);
+}
+__device__ __forceinline__ uint32_t stays_above_zero(uint32_t code, float root) {
+    asm("{\n\t.reg .pred p;\n\tsetp.gt.f32 p, %1, 0f00000000;\n\t@p max.u32 %0, %0, %2;\n\t}" : "+r"(code) : "f"(root), "r"(1u << 24));
+    return code;
 }
 template <bool SR>
-__device__ __forceinline__ uint32_t root_codes(float a, float b, float inv, uint32_t ra, uint32_t rb, uint32_t poisoned) {
-    if (!SR)
-        return pack_e4m3(a == 0.0f ? 0.0f : max_nan(a * inv, kCodeLeast), b == 0.0f ? 0.0f : max_nan(b * inv, kCodeLeast));
-    // a root is zero or normal: twice its bits are then 2^24 at least, the place of the smallest code
-    const uint32_t least_a = min(__float_as_uint(a) << 1, 1u << 24), least_b = min(__float_as_uint(b) << 1, 1u << 24);
-    const uint32_t code_a = max(stochastic_code(a * inv, noise_v(ra)), least_a), code_b = max(stochastic_code(b * inv, noise_v(rb)), least_b);
-    return (__byte_perm(code_a, code_b, 0x0073) & 0xFFFFu) | poisoned;
+__device__ __forceinline__ uint32_t root_codes(const float2 (&root)[2], float inv, const uint32_t* r, uint32_t sixteen) {
+    const Pair x[2] = {pair(root[0].x, root[0].y) * both(inv), pair(root[1].x, root[1].y) * both(inv)};
+    if (SR) {
+        const float2 c = apart(x[0] * both(kCodeUnit)), d = apart(x[1] * both(kCodeUnit));
+        return top_bytes(stays_above_zero(stochastic_code(c.x, noise_v(r[0]), sixteen), root[0].x), stays_above_zero(stochastic_code(c.y, noise_v(r[1]), sixteen), root[0].y),
+                         stays_above_zero(stochastic_code(d.x, noise_v(r[2]), sixteen), root[1].x), stays_above_zero(stochastic_code(d.y, noise_v(r[3]), sixteen), root[1].y));
+    }
+    const float2 a = apart(x[0]), b = apart(x[1]);
+    const auto least = [](float x, float root) { return root == 0.0f ? 0.0f : max_nan(x, kCodeLeast); };
+    return pack_e4m3(least(a.x, root[0].x), least(a.y, root[0].y)) | pack_e4m3(least(b.x, root[1].x), least(b.y, root[1].y)) << 16;
 }
-__device__ __forceinline__ uint32_t poisoned(float top) { return isnan(top) ? 0x7F7Fu : 0u; }
+// What becomes of four codes in a block with a NaN, whose scale is one.
+__device__ __forceinline__ uint32_t poison(float top) { return isnan(top) ? 0x7F7F7F7Fu : 0u; }
 
 __device__ __forceinline__ void unpack_e4m3(uint32_t pair, float& lo, float& hi) {
     uint32_t h;
@@ -166,55 +233,104 @@ __device__ __forceinline__ void unpack8(uint2 q, float (&v)[8]) {
     unpack_e4m3(q.y >> 16, v[6], v[7]);
 }
 
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// ---- chunks ----------------------------------------------------------------------------------------
 template <uint32_t DT>
 __device__ __forceinline__ float element(const char* base, uint64_t i) {
     return DT == DTT_BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[i] << 16) : reinterpret_cast<const float*>(base)[i];
 }
 
+template <uint32_t P, uint32_t G, bool S8, class T>
+__device__ __forceinline__ void load_element(const T& t, uint64_t i, float& p, float& g, float& m, float& v) {
+    p = element<P>(t.p, i);
+    g = element<G>(t.g, i);
+    if (S8) {
+        float none;
+        unpack_e4m3(reinterpret_cast<const uint8_t*>(t.m)[i], m, none);
+        unpack_e4m3(reinterpret_cast<const uint8_t*>(t.v)[i], v, none);
+    } else {
+        m = element<DTT_F32>(t.m, i);
+        v = element<DTT_F32>(t.v, i);
+    }
+}
+
+// p: its rounded bits in the high half, where it is bf16 and rounded at random.
+template <uint32_t P, bool S8, bool SR, class T>
+__device__ __forceinline__ void store_element(const T& t, uint64_t i, float p, uint32_t cut, float m, float v, uint32_t code_m, uint32_t code_v) {
+    if (S8) {
+        reinterpret_cast<uint8_t*>(t.m)[i] = (uint8_t)code_m;
+        reinterpret_cast<uint8_t*>(t.v)[i] = (uint8_t)code_v;
+    } else {
+        reinterpret_cast<float*>(t.m)[i] = m;
+        reinterpret_cast<float*>(t.v)[i] = v;
+    }
+    if (P == DTT_BF16)
+        reinterpret_cast<uint16_t*>(t.p)[i] = SR ? (uint16_t)(cut >> 16) : (uint16_t)pack_bf16(p, 0.0f);
+    else
+        reinterpret_cast<float*>(t.p)[i] = p;
+    if (P == DTT_F32 && t.copy) reinterpret_cast<uint16_t*>(t.copy)[i] = (uint16_t)pack_bf16(p, 0.0f);
+}
+
+// bf16 of eight weights rounded at random; NaN, which the sum would turn into something else, is left as it is.
+__device__ __forceinline__ void cut_weights(const float (&p)[8], const uint32_t (&r)[8], uint32_t (&cut)[8]) {
+    Pair none = both(0.0f);                     // NaN where one of them is infinite or NaN
+#pragma unroll
+    for (uint32_t k = 0; k < 8; k += 2) none = fma2(pair(p[k], p[k + 1]), both(0.0f), none);
+    const float2 n = apart(none);
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) cut[k] = stochastic_bf16(p[k], r[k]);
+    if (isnan(n.x + n.y)) {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+            if (isnan(p[k])) cut[k] = 0x7FFF0000u;
+    }
+}
+
 // Elements i, one by one, of a tensor of which nothing is aligned: a warp's 256 neighbours, a lane every 32nd, so
 // that accesses are contiguous over the warp and a block of 128 is four of each lane's.
 template <uint32_t P, uint32_t G, bool S8, bool SR>
-__device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, uint32_t seed, const Rates& r, const Scalars& s) {
+__device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, uint32_t seed, float keep, const Rates& r, const Scalars& s) {
     const uint64_t i0 = at + threadIdx.x / 32 * 256 + threadIdx.x % 32;
-    const float keep = 1.0f - r.lr * t.decay;
-    float p[8], g[8], m[8], v[8], root[8];
+    float p[8], g[8], m[8], v[8], ms[2], vs[2];
+    float2 root[4];
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
         const uint64_t i = min(i0 + 32 * k, t.n - 1);
-        p[k] = element<P>(t.p, i);
-        g[k] = element<G>(t.g, i);
-        if (S8) {
-            float none;
-            unpack_e4m3(reinterpret_cast<const uint8_t*>(t.m)[i], m[k], none);
-            unpack_e4m3(reinterpret_cast<const uint8_t*>(t.v)[i], v[k], none);
-            m[k] *= t.ms[i / kBlock];
-            v[k] *= t.vs[i / kBlock];
-            v[k] *= v[k];
-        } else {
-            m[k] = element<DTT_F32>(t.m, i);
-            v[k] = element<DTT_F32>(t.v, i);
+        load_element<P, G, S8>(t, i, p[k], g[k], m[k], v[k]);
+        if (S8 && k % 4 == 0) {
+            ms[k / 4] = t.ms[i / kBlock];
+            vs[k / 4] = t.vs[i / kBlock];
         }
     }
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) {
-        update<S8>(p[k], g[k], m[k], v[k], root[k], keep, r, s);
-        if (i0 + 32 * k >= t.n) m[k] = root[k] = 0.0f;
+    for (uint32_t k = 0; k < 8; k += 2) {
+        Pair pp = pair(p[k], p[k + 1]), mm = pair(m[k], m[k + 1]), vv = pair(v[k], v[k + 1]);
+        update<S8>(pp, pair(g[k], g[k + 1]), mm, vv, root[k / 2], S8 ? ms[k / 4] * s.beta1 : s.beta1, S8 ? vs[k / 4] * s.root_beta2 : s.beta2, keep, r, s.eps);
+        const float2 a = apart(pp), b = apart(mm), c = apart(vv);
+        p[k] = a.x, p[k + 1] = a.y, m[k] = b.x, m[k + 1] = b.y, v[k] = c.x, v[k + 1] = c.y;
     }
-    uint32_t noise[8] = {}, code_m[4], code_v[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+        if (S8 && i0 + 32 * k >= t.n) m[k] = (k % 2 ? root[k / 2].y : root[k / 2].x) = 0.0f;
+    uint32_t bits[8] = {}, cut[8] = {}, code_m[2] = {}, code_v[2] = {};
     if (SR) {
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) noise[k] = random_bits(i0 + 32 * k, seed);
+        for (uint32_t k = 0; k < 8; ++k) bits[k] = random_bits(i0 + 32 * k, seed);
+        if (P == DTT_BF16) cut_weights(p, bits, cut);
     }
     if (S8) {
 #pragma unroll
         for (uint32_t b = 0; b < 8; b += 4) {
-            float tm = 0.0f, tr = 0.0f;
-#pragma unroll
-            for (uint32_t k = b; k < b + 4; ++k) {
-                tm = max_nan(tm, fabsf(m[k]));
-                tr = max_nan(tr, root[k]);
-            }
-            tm = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tm)));
+            float tm = max3_nan(max_nan(fabsf(m[b]), fabsf(m[b + 1])), fabsf(m[b + 2]), fabsf(m[b + 3]));
+            float tr = max3_nan(max_nan(root[b / 2].x, root[b / 2].y), root[b / 2 + 1].x, root[b / 2 + 1].y);
+            // as bits, magnitudes order like integers, with NaN on top
+            tm = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tm) & 0x7FFFFFFFu));
             tr = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tr) & 0x7FFFFFFFu));
             const Scale sm = scale_from(tm), sr = scale_from(tr);
             const uint64_t i = i0 + 32 * b;
@@ -222,163 +338,219 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
                 t.ms[i / kBlock] = sm.scale;
                 t.vs[i / kBlock] = sr.scale;
             }
-#pragma unroll
-            for (uint32_t k = b; k < b + 4; k += 2) {
-                code_m[k / 2] = moment_codes<SR>(m[k], m[k + 1], sm.inv, noise[k], noise[k + 1], poisoned(tm));
-                code_v[k / 2] = root_codes<SR>(root[k], root[k + 1], sr.inv, noise[k], noise[k + 1], poisoned(tr));
-            }
+            const Pair ms[2] = {pair(m[b], m[b + 1]), pair(m[b + 2], m[b + 3])};
+            const float2 roots[2] = {root[b / 2], root[b / 2 + 1]};
+            code_m[b / 4] = moment_codes<SR>(ms, sm.inv, bits + b, s.sixteen) | poison(tm);
+            code_v[b / 4] = root_codes<SR>(roots, sr.inv, bits + b, s.sixteen) | poison(tr);
         }
     }
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
         const uint64_t i = i0 + 32 * k;
-        if (i >= t.n) break;
-        if (S8) {
-            reinterpret_cast<uint8_t*>(t.m)[i] = (uint8_t)(code_m[k / 2] >> 8 * (k % 2));
-            reinterpret_cast<uint8_t*>(t.v)[i] = (uint8_t)(code_v[k / 2] >> 8 * (k % 2));
-        } else {
-            reinterpret_cast<float*>(t.m)[i] = m[k];
-            reinterpret_cast<float*>(t.v)[i] = v[k];
-        }
-        if (P == DTT_BF16)
-            reinterpret_cast<uint16_t*>(t.p)[i] = SR ? (uint16_t)pack_cut(stochastic_bf16(p[k], noise[k] * kThird >> 16), 0.0f) : (uint16_t)pack_bf16(p[k], 0.0f);
-        else
-            reinterpret_cast<float*>(t.p)[i] = p[k];
-        if (P == DTT_F32 && t.copy) t.copy[i] = (uint16_t)pack_bf16(p[k], 0.0f);
+        if (i < t.n) store_element<P, S8, SR>(t, i, p[k], cut[k], m[k], v[k], code_m[k / 4] >> 8 * (k % 4), code_v[k / 4] >> 8 * (k % 4));
     }
 }
 
-// 8 neighbouring elements from `at`, of which [lo, hi) are the tensor's.
-template <uint32_t DT>
-__device__ __forceinline__ Raw8 raw_group(const char* base, uint64_t at) {
-    return raw8(base + at * (DT == DTT_BF16 ? 2 : 4), DT);
-}
-template <uint32_t DT>
-__device__ __forceinline__ void store_group(char* base, uint64_t at, const float (&v)[8]) {
-    store8<true>(base + at * (DT == DTT_BF16 ? 2 : 4), DT, 0, 8, v);
+// A CTA's part of a tensor whose groups are aligned: elements are counted from its start.
+struct Part {
+    char* p;
+    const char* g;
+    char* m;
+    char* v;
+    float* ms;
+    float* vs;
+    char* copy;
+    uint64_t first;             // the start's number in the tensor; before the tensor's first element: wrapped around
+    uint32_t head, end;         // the tensor's elements there
+};
+template <uint32_t P, uint32_t G, bool S8>
+__device__ __forceinline__ Part part_of(const Tensor& t, uint64_t start, uint32_t count) {
+    Part r;
+    r.p = t.p + start * (P == DTT_BF16 ? 2 : 4);
+    r.g = t.g + start * (G == DTT_BF16 ? 2 : 4);
+    r.m = t.m + start * (S8 ? 1 : 4);
+    r.v = t.v + start * (S8 ? 1 : 4);
+    r.ms = S8 ? t.ms + start / kBlock : nullptr;
+    r.vs = S8 ? t.vs + start / kBlock : nullptr;
+    r.copy = P == DTT_F32 && t.copy ? reinterpret_cast<char*>(t.copy + start) : nullptr;
+    r.first = start - t.lead;
+    r.head = start ? 0 : t.lead;
+    r.end = (uint32_t)min((uint64_t)count, t.lead + t.n - start);
+    return r;
 }
 
-// Eight neighbouring elements a thread, a block of 128 sixteen lanes.  Pointers are those of the element `lead` places before
-// the first, so that every eighth from there is aligned; the groups at the tensor's ends that it does not fill go
-// element by element.
-template <uint32_t P, uint32_t G, bool S8, bool SR>
-__device__ __forceinline__ void chunk_by_groups(const Tensor& t, uint64_t at, uint32_t seed, const Rates& r, const Scalars& s) {
-    const uint64_t i = at + 8 * threadIdx.x, from = t.lead, to = t.lead + t.n;
-    const bool whole = i >= from && i + 8 <= to;
-    const float keep = 1.0f - r.lr * t.decay;
-    float p[8], g[8], m[8], v[8], root[8];
-    if (whole) {
-        const Raw8 gs = raw_group<G>(t.g, i), ps = raw_group<P>(t.p, i);
-        if (S8) {
-            const uint2 cm = *reinterpret_cast<const uint2*>(t.m + i), cv = *reinterpret_cast<const uint2*>(t.v + i);
-            const float sm = t.ms[i / kBlock], sv = t.vs[i / kBlock];
-            unpack8(cm, m);
-            unpack8(cv, v);
+// 8-bit states: a thread's groups come through shared memory, each thread copying its own, all chunks' copies under way
+// at once and in nobody's registers; nobody waits but for its own.
+template <uint32_t P, uint32_t G>
+struct Stage {
+    static constexpr uint32_t ge = G == DTT_BF16 ? 16 : 32, pe = P == DTT_BF16 ? 16 : 32;      // bytes of a group
+    static constexpr uint32_t p = kThreads * ge, m = p + kThreads * pe, v = m + kThreads * 8, bytes = v + kThreads * 8;
+};
+__device__ __forceinline__ void copy16(uint32_t to, const char* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const char* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+template <uint32_t P, uint32_t G>
+__device__ __forceinline__ void start_copies(const Part& a, uint32_t o, uint32_t stage) {
+    using S = Stage<P, G>;
+    const uint32_t t = threadIdx.x;
+    if (o + 8 <= a.end) {
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
-                m[k] *= sm;
-                v[k] *= sv;
-                v[k] *= v[k];
-            }
+        for (uint32_t k = 0; k < S::ge; k += 16) copy16(stage + k * kThreads + 16 * t, a.g + o * (S::ge / 8) + k);
+#pragma unroll
+        for (uint32_t k = 0; k < S::pe; k += 16) copy16(stage + S::p + k * kThreads + 16 * t, a.p + o * (S::pe / 8) + k);
+        copy8(stage + S::m + 8 * t, a.m + o);
+        copy8(stage + S::v + 8 * t, a.v + o);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+    return q;
+}
+__device__ __forceinline__ uint2 shared8(uint32_t at) {
+    uint2 q;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "r"(at) : "memory");
+    return q;
+}
+
+template <uint32_t DT>
+__device__ __forceinline__ Raw8 group_of(const char* base, uint32_t o) {
+    return raw8(base + (uint64_t)o * (DT == DTT_BF16 ? 2 : 4), DT);
+}
+// What nobody reads before the next step leaves L2 first: 151M weights with f32 states 703 us, with plain stores 715
+// (and with loads marked so too 719).
+template <uint32_t DT>
+__device__ __forceinline__ void put_group(char* base, uint32_t o, const float (&v)[8]) {
+    char* at = base + (uint64_t)o * (DT == DTT_BF16 ? 2 : 4);
+    if (DT == DTT_BF16) {
+        __stcs(reinterpret_cast<uint4*>(at), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
+    } else {
+        __stcs(reinterpret_cast<float4*>(at), make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(reinterpret_cast<float4*>(at + 16), make_float4(v[4], v[5], v[6], v[7]));
+    }
+}
+template <uint32_t DT>
+__device__ __forceinline__ void shared_group(uint32_t at, float (&v)[8]) {
+    Raw8 q{};
+    q.a = shared16(at + 16 * threadIdx.x);
+    if (DT == DTT_F32) q.b = shared16(at + 16 * kThreads + 16 * threadIdx.x);
+    expand8(q, DT, v);
+}
+
+// Eight neighbouring elements a thread, from element o of the part, a block of 128 sixteen lanes.  Pointers are those of
+// the element `lead` places before the tensor's first, so that every eighth from there is aligned; the groups at its
+// ends that it does not fill go element by element.
+template <uint32_t P, uint32_t G, bool S8, bool SR>
+__device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage, float ms, float vs, uint32_t seed, float keep, const Rates& r, const Scalars& s) {
+    float p[8], g[8], m[8], v[8];
+    float2 root[4];
+    const bool whole = o >= a.head && o + 8 <= a.end;
+    const auto mine = [&](uint32_t k) { return o + k >= a.head && o + k < a.end; };
+    const uint64_t first = a.first + o;
+    if (whole) {
+        if (S8) {
+            using S = Stage<P, G>;
+            shared_group<G>(stage, g);
+            shared_group<P>(stage + S::p, p);
+            unpack8(shared8(stage + S::m + 8 * threadIdx.x), m);
+            unpack8(shared8(stage + S::v + 8 * threadIdx.x), v);
         } else {
-            const Raw8 a = raw_group<DTT_F32>(t.m, i), b = raw_group<DTT_F32>(t.v, i);
-            expand8(a, DTT_F32, m);
-            expand8(b, DTT_F32, v);
+            const Raw8 gs = group_of<G>(a.g, o), ps = group_of<P>(a.p, o), x = group_of<DTT_F32>(a.m, o), y = group_of<DTT_F32>(a.v, o);
+            expand8(gs, G, g);
+            expand8(ps, P, p);
+            expand8(x, DTT_F32, m);
+            expand8(y, DTT_F32, v);
         }
-        expand8(gs, G, g);
-        expand8(ps, P, p);
     } else {
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) {
             p[k] = g[k] = m[k] = v[k] = 0.0f;
-            if (i + k < from || i + k >= to) continue;
-            p[k] = element<P>(t.p, i + k);
-            g[k] = element<G>(t.g, i + k);
-            if (S8) {
-                float none;
-                unpack_e4m3(reinterpret_cast<const uint8_t*>(t.m)[i + k], m[k], none);
-                unpack_e4m3(reinterpret_cast<const uint8_t*>(t.v)[i + k], v[k], none);
-                m[k] *= t.ms[i / kBlock];
-                v[k] *= t.vs[i / kBlock];
-                v[k] *= v[k];
-            } else {
-                m[k] = element<DTT_F32>(t.m, i + k);
-                v[k] = element<DTT_F32>(t.v, i + k);
-            }
+            if (mine(k)) load_element<P, G, S8>(a, o + k, p[k], g[k], m[k], v[k]);
         }
     }
+    const float m_by = S8 ? ms * s.beta1 : s.beta1, v_by = S8 ? vs * s.root_beta2 : s.beta2;
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) update<S8>(p[k], g[k], m[k], v[k], root[k], keep, r, s);
-    uint32_t noise[8] = {};
+    for (uint32_t k = 0; k < 8; k += 2) {
+        Pair pp = pair(p[k], p[k + 1]), mm = pair(m[k], m[k + 1]), vv = pair(v[k], v[k + 1]);
+        update<S8>(pp, pair(g[k], g[k + 1]), mm, vv, root[k / 2], m_by, v_by, keep, r, s.eps);
+        const float2 a = apart(pp), b = apart(mm), c = apart(vv);
+        p[k] = a.x, p[k + 1] = a.y, m[k] = b.x, m[k + 1] = b.y, v[k] = c.x, v[k + 1] = c.y;
+    }
+    uint32_t bits[8] = {}, cut[8] = {};
     if (SR) {
+        const uint32_t key = (uint32_t)first * kGolden + seed + (uint32_t)(first >> 32) * kThird;
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) noise[k] = random_bits(i + k - from, seed);
+        for (uint32_t k = 0; k < 8; ++k) bits[k] = mix(key + k * kGolden);
+        if (!S8 && (uint32_t)first > 0xFFFFFFF8u) {      // 2^32 elements end in this group, or the tensor begins there
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) bits[k] = random_bits(first + k, seed);
+        }
+        if (P == DTT_BF16) cut_weights(p, bits, cut);
     }
     uint2 cm{}, cv{};
     if (S8) {
-        float tm = 0.0f, tr = 0.0f;             // elements that are not the tensor's have m and root 0
+        // elements that are not the tensor's have m and root 0
+        float tm = max3_nan(max3_nan(fabsf(m[0]), fabsf(m[1]), fabsf(m[2])), fabsf(m[3]), fabsf(m[4]));
+        float tr = max3_nan(max3_nan(root[0].x, root[0].y, root[1].x), root[1].y, root[2].x);
+        tm = max3_nan(max_nan(tm, fabsf(m[5])), fabsf(m[6]), fabsf(m[7]));
+        tr = max3_nan(max_nan(tr, root[2].y), root[3].x, root[3].y);
+        // both over the block's lanes: even lanes go on with m's, odd ones with the roots'
+        const bool odd = threadIdx.x % 2;
+        float top = max_nan(odd ? tr : tm, __shfl_xor_sync(0xFFFFFFFFu, odd ? tm : tr, 1));
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-            tm = max_nan(tm, fabsf(m[k]));
-            tr = max_nan(tr, root[k]);
-        }
-#pragma unroll
-        for (uint32_t d = 1; d < kBlock / 8; d *= 2) {
-            tm = max_nan(tm, __shfl_xor_sync(0xFFFFFFFFu, tm, d));
-            tr = max_nan(tr, __shfl_xor_sync(0xFFFFFFFFu, tr, d));
-        }
+        for (uint32_t d = 2; d < kBlock / 8; d *= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
+        tm = odd ? other : top;
+        tr = odd ? top : other;
         const Scale sm = scale_from(tm), sr = scale_from(tr);
-        if (threadIdx.x % (kBlock / 8) == 0 && i < to) {
-            t.ms[i / kBlock] = sm.scale;
-            t.vs[i / kBlock] = sr.scale;
+        if (threadIdx.x % (kBlock / 8) == 0 && o < a.end) {
+            a.ms[o / kBlock] = sm.scale;
+            a.vs[o / kBlock] = sr.scale;
         }
-        uint32_t c[4], d[4];
-#pragma unroll
-        for (uint32_t k = 0; k < 8; k += 2) {
-            c[k / 2] = moment_codes<SR>(m[k], m[k + 1], sm.inv, noise[k], noise[k + 1], poisoned(tm));
-            d[k / 2] = root_codes<SR>(root[k], root[k + 1], sr.inv, noise[k], noise[k + 1], poisoned(tr));
-        }
-        cm = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-        cv = make_uint2(d[0] | d[1] << 16, d[2] | d[3] << 16);
+        const Pair m0[2] = {pair(m[0], m[1]), pair(m[2], m[3])}, m1[2] = {pair(m[4], m[5]), pair(m[6], m[7])};
+        const float2 r0[2] = {root[0], root[1]}, r1[2] = {root[2], root[3]};
+        cm = make_uint2(moment_codes<SR>(m0, sm.inv, bits, s.sixteen) | poison(tm), moment_codes<SR>(m1, sm.inv, bits + 4, s.sixteen) | poison(tm));
+        cv = make_uint2(root_codes<SR>(r0, sr.inv, bits, s.sixteen) | poison(tr), root_codes<SR>(r1, sr.inv, bits + 4, s.sixteen) | poison(tr));
     }
-    float q[8];
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) q[k] = P == DTT_BF16 && SR ? stochastic_bf16(p[k], noise[k] * kThird >> 16) : p[k];
     if (whole) {
         if (S8) {
-            *reinterpret_cast<uint2*>(t.m + i) = cm;
-            *reinterpret_cast<uint2*>(t.v + i) = cv;
+            *reinterpret_cast<uint2*>(a.m + o) = cm;
+            *reinterpret_cast<uint2*>(a.v + o) = cv;
         } else {
-            store_group<DTT_F32>(t.m, i, m);
-            store_group<DTT_F32>(t.v, i, v);
+            put_group<DTT_F32>(a.m, o, m);
+            put_group<DTT_F32>(a.v, o, v);
         }
         if (P == DTT_BF16 && SR)
-            *reinterpret_cast<uint4*>(t.p + 2 * i) = make_uint4(pack_cut(q[0], q[1]), pack_cut(q[2], q[3]), pack_cut(q[4], q[5]), pack_cut(q[6], q[7]));
+            *reinterpret_cast<uint4*>(a.p + (uint64_t)o * 2) = make_uint4(pack_cut(cut[0], cut[1]), pack_cut(cut[2], cut[3]), pack_cut(cut[4], cut[5]), pack_cut(cut[6], cut[7]));
         else
-            store_group<P>(t.p, i, p);
-        if (P == DTT_F32 && t.copy) store_group<DTT_BF16>(reinterpret_cast<char*>(t.copy), i, p);
+            put_group<P>(a.p, o, p);
+        if (P == DTT_F32 && a.copy) put_group<DTT_BF16>(a.copy, o, p);
         return;
     }
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) {
-        if (i + k < from || i + k >= to) continue;
-        if (S8) {
-            reinterpret_cast<uint8_t*>(t.m)[i + k] = (uint8_t)((k < 4 ? cm.x : cm.y) >> 8 * (k % 4));
-            reinterpret_cast<uint8_t*>(t.v)[i + k] = (uint8_t)((k < 4 ? cv.x : cv.y) >> 8 * (k % 4));
-        } else {
-            reinterpret_cast<float*>(t.m)[i + k] = m[k];
-            reinterpret_cast<float*>(t.v)[i + k] = v[k];
-        }
-        if (P == DTT_BF16)
-            reinterpret_cast<uint16_t*>(t.p)[i + k] = SR ? (uint16_t)pack_cut(q[k], 0.0f) : (uint16_t)pack_bf16(p[k], 0.0f);
-        else
-            reinterpret_cast<float*>(t.p)[i + k] = p[k];
-        if (P == DTT_F32 && t.copy) t.copy[i + k] = (uint16_t)pack_bf16(p[k], 0.0f);
+    for (uint32_t k = 0; k < 8; ++k)
+        if (mine(k))
+            store_element<P, S8, SR>(a, o + k, p[k], cut[k], m[k], v[k], (k < 4 ? cm.x : cm.y) >> 8 * (k % 4), (k < 4 ? cv.x : cv.y) >> 8 * (k % 4));
+}
+
+// The chunks one after the other, once a thread's own copies for each have landed.
+template <uint32_t TURN, uint32_t P, uint32_t G, bool SR>
+__device__ __forceinline__ void take_turns(const Part& a, uint32_t stage, const float (&ms)[kTurns], const float (&vs)[kTurns], uint32_t seed, float keep,
+                                           const Rates& r, const Scalars& s) {
+    if constexpr (TURN < kTurns) {
+        if (TURN * kChunk >= a.end) return;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 1 - TURN) : "memory");
+        group<P, G, true, SR>(a, TURN * kChunk + 8 * threadIdx.x, stage + TURN * Stage<P, G>::bytes, ms[TURN], vs[TURN], seed, keep, r, s);
+        take_turns<TURN + 1, P, G, SR>(a, stage, ms, vs, seed, keep, r, s);
     }
 }
 
 template <uint32_t P, uint32_t G, bool S8, bool SR, uint32_t N>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Batch<N> b) {
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Batch<N> b) {
     launch_next();
     uint32_t lo = 0, hi = b.count;                  // first[lo] <= blockIdx.x < first[hi]
     while (hi - lo > 1) {
@@ -387,13 +559,36 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         else hi = mid;
     }
     const Tensor& t = b.t[lo];
-    const uint64_t at = (uint64_t)(blockIdx.x - b.first[lo]) * kChunk;
     wait_previous();
     const Rates r = rates_of(b.s);
+    const float keep = 1.0f - r.lr * t.decay;
     uint32_t seed = 0;
-    if (SR) seed = mix(mix(b.s.seed + r.step) + b.number + lo);
-    if (t.lead < kElements) chunk_by_groups<P, G, S8, SR>(t, at, seed, r, b.s);
-    else chunk_by_elements<P, G, S8, SR>(t, at, seed, r, b.s);
+    if (SR) seed = mix(mix(b.s.seed + r.step) + t.number);
+    const uint64_t start = (uint64_t)(blockIdx.x - b.first[lo]) * b.turns * kChunk;
+    if (t.lead < kElements) {
+        const Part a = part_of<P, G, S8>(t, start, b.turns * kChunk);
+        if (S8) {
+            extern __shared__ __align__(16) uint8_t stages[];
+            const uint32_t stage = saddr(stages);
+            float ms[kTurns], vs[kTurns];
+#pragma unroll
+            for (uint32_t turn = 0; turn < kTurns; ++turn) {        // those past the part's end copy nothing
+                const uint32_t o = turn * kChunk + 8 * threadIdx.x;
+                ms[turn] = vs[turn] = 0.0f;
+                if (o < a.end) {
+                    ms[turn] = a.ms[o / kBlock];
+                    vs[turn] = a.vs[o / kBlock];
+                }
+                start_copies<P, G>(a, o, stage + turn * Stage<P, G>::bytes);
+            }
+            take_turns<0, P, G, SR>(a, stage, ms, vs, seed, keep, r, b.s);
+        } else {
+            group<P, G, S8, SR>(a, 8 * threadIdx.x, 0, 0.0f, 0.0f, seed, keep, r, b.s);
+        }
+    } else {
+        const uint64_t end = min(start + b.turns * kChunk, t.n);
+        for (uint64_t at = start; at < end; at += kChunk) chunk_by_elements<P, G, S8, SR>(t, at, seed, keep, r, b.s);
+    }
 }
 
 __global__ void adamw_advance_kernel(uint32_t* step) {
@@ -423,11 +618,18 @@ uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : dt == DTT_F32 ? 4
 
 bool misaligned(const void* p, uint32_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
+// Shared memory of a chunk.
+uint32_t stage_bytes(const dtt_adamw_desc& d) {
+    const bool p2 = d.param_dtype == DTT_BF16, g2 = d.grad_dtype == DTT_BF16;
+    if (d.state_dtype != DTT_E4M3) return 0;
+    return p2 ? (g2 ? Stage<DTT_BF16, DTT_BF16>::bytes : Stage<DTT_BF16, DTT_F32>::bytes) : g2 ? Stage<DTT_F32, DTT_BF16>::bytes : Stage<DTT_F32, DTT_F32>::bytes;
+}
+
 // By groups where all of a tensor's pointers are aligned at the same element, with 8-bit states the first, where its
 // blocks begin.
-Tensor tensor_of(const dtt_adamw_desc& d, const dtt_adamw_tensor& t, const void* grad) {
+Tensor tensor_of(const dtt_adamw_desc& d, const dtt_adamw_tensor& t, const void* grad, uint32_t number) {
     Tensor r{static_cast<char*>(t.param), static_cast<const char*>(grad), static_cast<char*>(t.m), static_cast<char*>(t.v), t.m_scales, t.v_scales,
-             static_cast<uint16_t*>(t.copy), t.n, t.weight_decay, kElements};
+             static_cast<uint16_t*>(t.copy), t.n, t.weight_decay, kElements, number};
     const uint32_t pe = elem_bytes(d.param_dtype), ge = elem_bytes(d.grad_dtype), se = elem_bytes(d.state_dtype);
     const auto off = [](const void* p, uint32_t size, uint32_t lead) { return (reinterpret_cast<uintptr_t>(p) - lead * size) % std::min(16u, 8 * size) != 0; };
     for (uint32_t lead = 0; lead < (d.state_dtype == DTT_E4M3 ? 1 : kElements); ++lead) {
@@ -453,8 +655,11 @@ cudaError_t preload_adamw_kernels() {
         d.grad_dtype = k & 2 ? DTT_BF16 : DTT_F32;
         d.state_dtype = k & 4 ? (uint32_t)DTT_E4M3 : (uint32_t)DTT_F32;
         d.stochastic = k >> 3;
+        const int smem = (int)(kTurns * stage_bytes(d));
         e = prepare_kernel(Kernels<kFew>::of(d));
         if (e == cudaSuccess) e = prepare_kernel(Kernels<kMany>::of(d));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernels<kFew>::of(d), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernels<kMany>::of(d), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     }
     return e;
 }
@@ -467,6 +672,7 @@ struct dtt_adamw {
     dtt_adamw_desc d;
     std::vector<dtt_adamw_tensor> tensors;          // without the empty ones
     std::vector<uint32_t> number;                   // of each in the caller's list
+    uint64_t elements = 0;                          // of all
 };
 
 namespace {
@@ -475,24 +681,23 @@ template <uint32_t N>
 int run_batches(const dtt_adamw& o, const void* const* grads, const Scalars& s, cudaStream_t stream) {
     const char* who = "dtt_adamw_run";
     const auto kernel = Kernels<N>::of(o.d);
+    const uint32_t turns = o.d.state_dtype == DTT_E4M3 && o.elements >= kManyElements ? kTurns : 1;
     for (size_t i = 0; i < o.tensors.size();) {
         Batch<N> b;
-        uint32_t chunks = 0, k = 0;
+        uint32_t ctas = 0, k = 0;
         b.s = s;
-        b.number = o.number[i];
         for (; k < N && i < o.tensors.size(); ++k, ++i) {
-            // an empty tensor between two of a launch would shift the numbers after it
-            if (o.number[i] != b.number + k) break;
             const dtt_adamw_tensor& t = o.tensors[i];
-            b.t[k] = tensor_of(o.d, t, grads ? grads[o.number[i]] : t.grad);
-            const uint64_t need = (t.n + b.t[k].lead % kElements + kChunk - 1) / kChunk;
-            if (chunks + need > 0x7FFFFFFFull) break;
-            b.first[k] = chunks;
-            chunks += (uint32_t)need;
+            b.t[k] = tensor_of(o.d, t, grads ? grads[o.number[i]] : t.grad, o.number[i]);
+            const uint64_t each = (uint64_t)turns * kChunk, need = (t.n + b.t[k].lead % kElements + each - 1) / each;
+            if (ctas + need > 0x7FFFFFFFull) break;
+            b.first[k] = ctas;
+            ctas += (uint32_t)need;
         }
-        b.first[k] = chunks;
+        b.first[k] = ctas;
         b.count = k;
-        const cudaError_t e = launch(kernel, chunks, kThreads, 0, 0, true, stream, b);
+        b.turns = turns;
+        const cudaError_t e = launch(kernel, ctas, kThreads, turns * stage_bytes(o.d), 0, true, stream, b);
         if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     }
     return DTT_OK;
@@ -538,6 +743,7 @@ extern "C" int dtt_adamw_create(const dtt_adamw_desc* d, const dtt_adamw_tensor*
             if (tensors[i].n) {
                 o->tensors.push_back(tensors[i]);
                 o->number.push_back(i);
+                o->elements += tensors[i].n;
             }
     } catch (const std::bad_alloc&) {
         delete o;
@@ -565,8 +771,10 @@ extern "C" int dtt_adamw_run(dtt_adamw* o, const void* const* grads, float lr, u
     Scalars s{};
     s.beta1 = (float)d.beta1;
     s.beta2 = (float)d.beta2;
+    s.root_beta2 = (float)std::sqrt(d.beta2);
     s.one_less_beta1 = (float)(1.0 - d.beta1);
-    s.one_less_beta2 = (float)(1.0 - d.beta2);
+    s.root_one_less_beta2 = (float)std::sqrt(1.0 - d.beta2);
+    s.sixteen = 16;
     s.eps = d.eps;
     s.lr = lr;
     if (!step_dev) {

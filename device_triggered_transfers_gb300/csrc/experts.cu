@@ -19,7 +19,9 @@ constexpr uint32_t kMostExperts = 1024, kMostChoices = 32;
 constexpr uint32_t kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
 constexpr uint32_t kMostParts = 64;            // CTAs of the sort, at most
 constexpr uint32_t kPartPairs = 2048;          // pairs of a CTA, at least, while there are fewer
-constexpr uint32_t kRowThreads = 256;
+// A row's threads, at most.  131072 rows of 4096 (bf16) combined: 209 us with 256 (four CTAs an SM), 224 with 512 (two),
+// 211 with 128 (eight); backward 402, 450, 411.
+constexpr uint32_t kCopyThreads = 256, kRowThreads = 256;
 constexpr uint32_t kFillRows = 8;              // rows of one CTA where an expert's rows are filled up
 
 struct RouteParams {
@@ -175,7 +177,7 @@ __device__ __forceinline__ uint32_t row_of(const Sorted& s, uint64_t pair) { ret
 // Rows from an expert's last to where the next one's begin, zeros: CTA `cta` of fill_ctas.
 template <class W>
 __device__ __forceinline__ void zero_words(char* row, uint32_t bytes) {
-    for (uint32_t i = threadIdx.x; i < bytes / sizeof(W); i += blockDim.x) reinterpret_cast<W*>(row)[i] = W{};
+    for (uint32_t i = threadIdx.y * blockDim.x + threadIdx.x; i < bytes / sizeof(W); i += blockDim.x * blockDim.y) reinterpret_cast<W*>(row)[i] = W{};
 }
 template <class W>
 __device__ __forceinline__ void fill_rows(const Sorted& s, const Rows& rows, uint32_t cta) {
@@ -206,7 +208,7 @@ struct DispatchParams {
 
 // W: the word that rows are moved by, SW: their scales.
 template <class W, class SW>
-__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_constant__ DispatchParams p) {
+__global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const __grid_constant__ DispatchParams p) {
     launch_next();
     wait_previous();
     if (blockIdx.x < p.s.fill_ctas) {
@@ -225,76 +227,176 @@ struct CombineParams {
     const float* weights;       // or null
     char* out;
     uint64_t rows_pitch, out_pitch;
-    uint32_t cols, rows_dt, out_dt;
+    uint32_t cols;
 };
 
-template <bool VEC>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+// Eight columns of a row from c, which VEC has in one piece, as they are loaded: those from `cols` on are zeros.
+template <uint32_t DT>
+struct Columns {
+    static constexpr uint32_t size = DT == DTT_BF16 ? 2 : 4;
+    uint32_t raw[2 * size];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const char* row, uint32_t c, uint32_t cols) {
+        if constexpr (VEC) {
+            const Raw8 q = raw8(row + (uint64_t)c * size, DT);
+            raw[0] = q.a.x, raw[1] = q.a.y, raw[2] = q.a.z, raw[3] = q.a.w;
+            if constexpr (DT != DTT_BF16) raw[4] = q.b.x, raw[5] = q.b.y, raw[6] = q.b.z, raw[7] = q.b.w;
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                if constexpr (DT == DTT_BF16) {
+                    const uint32_t v = c + i < cols ? reinterpret_cast<const uint16_t*>(row)[c + i] : 0;
+                    raw[i / 2] = i % 2 ? raw[i / 2] | v << 16 : v;
+                } else {
+                    raw[i] = c + i < cols ? reinterpret_cast<const uint32_t*>(row)[c + i] : 0;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void none() {
+#pragma unroll
+        for (uint32_t i = 0; i < 2 * size; ++i) raw[i] = 0;
+    }
+    __device__ __forceinline__ void expand(float (&v)[8]) const {
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            if constexpr (DT == DTT_BF16) v[i] = i % 2 ? bf16_hi(raw[i / 2]) : bf16_lo(raw[i / 2]);
+            else v[i] = __uint_as_float(raw[i]);
+        }
+    }
+};
+
+// How many of a token's rows are on their way to a thread at once: what 64 registers hold.  (Backward with eight of bf16 it
+// takes more, and so fewer CTAs: 534 us and not 402.)
+template <uint32_t DT> constexpr uint32_t kAtOnce = DT == DTT_BF16 ? 8 : 4;
+
+// A token by blockDim.x threads, eight columns each at a time, blockDim.y tokens a CTA.  A token's rows lie anywhere, so
+// that what counts is how many loads are out: all of a batch's go before the first is looked at.
+template <bool VEC, uint32_t RDT, uint32_t ODT>
+__global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(const __grid_constant__ CombineParams p) {
     launch_next();
     wait_previous();
-    const uint64_t token = blockIdx.x;
+    constexpr uint32_t J = kAtOnce<RDT>;
+    const uint64_t token = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (token >= p.s.tokens) return;
+    const uint64_t pairs = token * p.s.k;
     for (uint32_t c = 8 * threadIdx.x; c < p.cols; c += 8 * blockDim.x) {
         float sum[8] = {};
-        for (uint32_t j = 0; j < p.s.k; ++j) {
-            const uint32_t r = row_of(p.s, token * p.s.k + j);
-            if (r >= p.s.max_rows) continue;
-            const float w = p.weights ? p.weights[token * p.s.k + j] : 1.0f;
-            float v[8];
-            load8<VEC>(p.rows + r * p.rows_pitch, p.rows_dt, c, p.cols, v);
+        for (uint32_t j0 = 0; j0 < p.s.k; j0 += J) {
+            Columns<RDT> v[J];
+            float w[J];
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+            for (uint32_t j = 0; j < J; ++j) {
+                const uint32_t r = j0 + j < p.s.k ? row_of(p.s, pairs + j0 + j) : ~0u;
+                w[j] = 0.0f;                    // without a row: zeros, with a weight of 0
+                v[j].none();
+                if (r < p.s.max_rows) {
+                    w[j] = p.weights ? p.weights[pairs + j0 + j] : 1.0f;
+                    v[j].template load<VEC>(p.rows + r * p.rows_pitch, c, p.cols);
+                }
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < J; ++j) {
+                float f[8];
+                v[j].expand(f);
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) sum[i] = fmaf(w[j], f[i], sum[i]);
+            }
         }
-        store8<VEC>(p.out + token * p.out_pitch, p.out_dt, c, p.cols, sum);
+        store8<VEC>(p.out + token * p.out_pitch, ODT, c, p.cols, sum);
     }
 }
 
 struct BackwardParams {
     Sorted s;
     const char* dout;
-    const char* rows;           // or null: no weights' gradient
+    const char* rows;
     const float* weights;
     Rows drows;
-    float* dweights;            // or null
+    float* dweights;            // or null: rows are not read
     uint64_t dout_pitch, rows_pitch;
-    uint32_t cols, dout_dt, rows_dt;
+    uint32_t cols;
 };
 
-template <bool VEC, class W>
-__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const __grid_constant__ BackwardParams p) {
+// Sums over a warp of N values a lane, N a power of two up to 32: lane l gets value l % N's.  Each exchange halves the
+// values that a lane goes on with.
+template <uint32_t N>
+__device__ __forceinline__ float sum_of_mine(float (&v)[N]) {
+#pragma unroll
+    for (uint32_t h = N / 2; h > 0; h /= 2) {
+        const bool up = threadIdx.x & h;
+#pragma unroll
+        for (uint32_t i = 0; i < h; ++i) {
+            const float keep = up ? v[i + h] : v[i], give = up ? v[i] : v[i + h];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, h);
+        }
+    }
+#pragma unroll
+    for (uint32_t d = N; d < 32; d *= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], d);
+    return v[0];
+}
+
+// Tokens as above; a token's own row is read once for a batch of its rows, whose dot products with it are summed up over
+// the token's threads at the end.
+template <bool VEC, uint32_t RDT, uint32_t GDT, class W>
+__global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(const __grid_constant__ BackwardParams p) {
     launch_next();
     wait_previous();
-    __shared__ float sums[kRowThreads / 32];
+    constexpr uint32_t J = 4;
+    __shared__ float sums[2][kRowThreads / 32][J];
     if (blockIdx.x < p.s.fill_ctas) return fill_rows<W>(p.s, p.drows, blockIdx.x);
-    const uint64_t token = blockIdx.x - p.s.fill_ctas;
-    for (uint32_t j = 0; j < p.s.k; ++j) {
-        const uint64_t pair = token * p.s.k + j;
-        const uint32_t r = row_of(p.s, pair);
-        float dot = 0.0f;
-        if (r < p.s.max_rows) {
-            const float w = p.weights[pair];
-            for (uint32_t c = 8 * threadIdx.x; c < p.cols; c += 8 * blockDim.x) {
-                float g[8], v[8];
-                load8<VEC>(p.dout + token * p.dout_pitch, p.dout_dt, c, p.cols, g);
-                if (p.dweights) {
-                    load8<VEC>(p.rows + r * p.rows_pitch, p.rows_dt, c, p.cols, v);
+    const uint64_t token = (uint64_t)(blockIdx.x - p.s.fill_ctas) * blockDim.y + threadIdx.y;
+    if (token >= p.s.tokens) return;            // a whole warp: tokens share no barrier
+    const uint64_t pairs = token * p.s.k;
+    const char* dout = p.dout + token * p.dout_pitch;
+    uint32_t turn = 0;
+    for (uint32_t j0 = 0; j0 < p.s.k; j0 += J, turn ^= 1) {
+        uint32_t r[J];
+        float w[J], dot[J];
 #pragma unroll
-                    for (uint32_t i = 0; i < 8; ++i) dot = fmaf(g[i], v[i], dot);
+        for (uint32_t j = 0; j < J; ++j) {
+            r[j] = j0 + j < p.s.k ? row_of(p.s, pairs + j0 + j) : ~0u;
+            w[j] = r[j] < p.s.max_rows ? p.weights[pairs + j0 + j] : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (uint32_t c = 8 * threadIdx.x; c < p.cols; c += 8 * blockDim.x) {
+            Columns<GDT> gs;
+            Columns<RDT> v[J];
+            gs.template load<VEC>(dout, c, p.cols);
+            if (p.dweights) {
+#pragma unroll
+                for (uint32_t j = 0; j < J; ++j) {
+                    v[j].none();
+                    if (r[j] < p.s.max_rows) v[j].template load<VEC>(p.rows + r[j] * p.rows_pitch, c, p.cols);
+                }
+            }
+            float g[8];
+            gs.expand(g);
+#pragma unroll
+            for (uint32_t j = 0; j < J; ++j) {
+                if (r[j] >= p.s.max_rows) continue;
+                float f[8];
+                if (p.dweights) {
+                    v[j].expand(f);
+#pragma unroll
+                    for (uint32_t i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
                 }
 #pragma unroll
-                for (uint32_t i = 0; i < 8; ++i) g[i] *= w;
-                store8<VEC>(p.drows.at + r * p.drows.pitch, p.rows_dt, c, p.cols, g);
+                for (uint32_t i = 0; i < 8; ++i) f[i] = g[i] * w[j];
+                store8<VEC>(p.drows.at + r[j] * p.drows.pitch, RDT, c, p.cols, f);
             }
         }
         if (!p.dweights) continue;
-#pragma unroll
-        for (uint32_t o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-        if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (uint32_t i = 1; i < kRowThreads / 32; ++i) dot += sums[i];
-            p.dweights[pair] = dot;
+        const uint32_t lane = threadIdx.x % 32;
+        float sum = sum_of_mine(dot);
+        if (blockDim.x > 32) {
+            if (lane < J) sums[turn][threadIdx.x / 32][lane] = sum;
+            __syncthreads();
+            sum = 0.0f;
+            if (threadIdx.x < J)
+                for (uint32_t i = 0; i < blockDim.x / 32; ++i) sum += sums[turn][i][threadIdx.x];
         }
-        __syncthreads();
+        if (threadIdx.x < J && j0 + threadIdx.x < p.s.k) p.dweights[pairs + j0 + threadIdx.x] = sum;
     }
 }
 
@@ -350,8 +452,31 @@ uint64_t bits_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 template <class SW>
 cudaError_t launch_dispatch(uint32_t word, uint32_t grid, cudaStream_t stream, const DispatchParams& p) {
     auto kernel = word == 16 ? dispatch_kernel<uint4, SW> : word == 4 ? dispatch_kernel<uint32_t, SW> : word == 2 ? dispatch_kernel<uint16_t, SW> : dispatch_kernel<uint8_t, SW>;
-    return launch(kernel, grid, kRowThreads, 0, 0, true, stream, p);
+    return launch(kernel, grid, kCopyThreads, 0, 0, true, stream, p);
 }
+
+// A token's threads, as many as it has eights of columns, and the tokens of a CTA: several where a token is one warp.
+dim3 token_block(uint64_t cols) {
+    const uint32_t t = (uint32_t)std::min<uint64_t>((cols + 255) / 256 * 32, kRowThreads);
+    return dim3(t, t == 32 ? 8 : 1);
+}
+uint64_t ctas_of(uint64_t tokens, dim3 block) { return (tokens + block.y - 1) / block.y; }
+
+using CombineKernel = void (*)(CombineParams);
+template <bool VEC>
+CombineKernel combine_of(uint32_t rows, uint32_t out) {
+    if (rows == DTT_BF16) return out == DTT_BF16 ? combine_kernel<VEC, DTT_BF16, DTT_BF16> : combine_kernel<VEC, DTT_BF16, DTT_F32>;
+    return out == DTT_BF16 ? combine_kernel<VEC, DTT_F32, DTT_BF16> : combine_kernel<VEC, DTT_F32, DTT_F32>;
+}
+CombineKernel combine_of(bool vec, uint32_t rows, uint32_t out) { return vec ? combine_of<true>(rows, out) : combine_of<false>(rows, out); }
+
+using BackwardKernel = void (*)(BackwardParams);
+template <bool VEC, class W>
+BackwardKernel backward_of(uint32_t rows, uint32_t dout) {
+    if (rows == DTT_BF16) return dout == DTT_BF16 ? combine_backward_kernel<VEC, DTT_BF16, DTT_BF16, W> : combine_backward_kernel<VEC, DTT_BF16, DTT_F32, W>;
+    return dout == DTT_BF16 ? combine_backward_kernel<VEC, DTT_F32, DTT_BF16, W> : combine_backward_kernel<VEC, DTT_F32, DTT_F32, W>;
+}
+BackwardKernel backward_of(bool vec, uint32_t rows, uint32_t dout) { return vec ? backward_of<true, uint4>(rows, dout) : backward_of<false, uint16_t>(rows, dout); }
 
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : 4; }
 bool aligned(const void* p, uint64_t pitch) { return bits_of(p) % 16 == 0 && pitch % 16 == 0; }
@@ -363,8 +488,11 @@ cudaError_t preload_experts_kernels() {
     auto add = [&](auto... kernels) { ((e = e == cudaSuccess ? prepare_kernel(kernels) : e), ...); };
     add(route_count_kernel, route_place_kernel, dispatch_kernel<uint4, uint4>, dispatch_kernel<uint4, uint32_t>, dispatch_kernel<uint32_t, uint4>,
         dispatch_kernel<uint32_t, uint32_t>, dispatch_kernel<uint16_t, uint4>, dispatch_kernel<uint16_t, uint32_t>, dispatch_kernel<uint8_t, uint4>,
-        dispatch_kernel<uint8_t, uint32_t>, combine_kernel<true>, combine_kernel<false>, combine_backward_kernel<true, uint4>,
-        combine_backward_kernel<false, uint16_t>);
+        dispatch_kernel<uint8_t, uint32_t>);
+    for (uint32_t i = 0; i < 8; ++i) {
+        const uint32_t a = i & 1 ? DTT_F32 : DTT_BF16, b = i & 2 ? DTT_F32 : DTT_BF16;
+        add(combine_of(i & 4, a, b), backward_of(i & 4, a, b));
+    }
     constexpr int most = (kRouteWarps + 2) * kMostExperts * 4;
     for (auto k : {route_count_kernel, route_place_kernel})
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -475,10 +603,9 @@ extern "C" int dtt_experts_combine(const dtt_experts_desc* d, uint64_t tokens, u
     p.rows_pitch = rows_pitch;
     p.out_pitch = out_pitch;
     p.cols = (uint32_t)cols;
-    p.rows_dt = rows_dtype;
-    p.out_dt = out_dtype;
     const bool vec = cols % 8 == 0 && aligned(rows, rows_pitch) && aligned(out, out_pitch);
-    const cudaError_t e = launch(vec ? combine_kernel<true> : combine_kernel<false>, (uint32_t)tokens, kRowThreads, 0, 0, true, stream, p);
+    const dim3 block = token_block(cols);
+    const cudaError_t e = launch(combine_of(vec, rows_dtype, out_dtype), (uint32_t)ctas_of(tokens, block), block, 0, 0, true, stream, p);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }
@@ -503,7 +630,8 @@ extern "C" int dtt_experts_combine_backward(const dtt_experts_desc* d, uint64_t 
         return rc;
     BackwardParams p{};
     p.s = sorted_of(d, tokens, max_rows, position, offsets, counts);
-    const uint64_t grid = tokens + p.s.fill_ctas;
+    const dim3 block = token_block(cols);
+    const uint64_t grid = ctas_of(tokens, block) + p.s.fill_ctas;
     if (grid == 0) return DTT_OK;
     if ((rc = preload_once())) return rc;
     p.dout = static_cast<const char*>(dout);
@@ -514,10 +642,8 @@ extern "C" int dtt_experts_combine_backward(const dtt_experts_desc* d, uint64_t 
     p.dout_pitch = dout_pitch;
     p.rows_pitch = rows_pitch;
     p.cols = (uint32_t)cols;
-    p.dout_dt = dout_dtype;
-    p.rows_dt = rows_dtype;
     const bool vec = cols % 8 == 0 && aligned(dout, dout_pitch) && aligned(drows, drows_pitch) && (!dweights || aligned(rows, rows_pitch));
-    const cudaError_t e = launch(vec ? combine_backward_kernel<true, uint4> : combine_backward_kernel<false, uint16_t>, (uint32_t)grid, kRowThreads, 0, 0, true, stream, p);
+    const cudaError_t e = launch(backward_of(vec, rows_dtype, dout_dtype), (uint32_t)grid, block, 0, 0, true, stream, p);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }
