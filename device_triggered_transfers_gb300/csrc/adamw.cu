@@ -84,32 +84,6 @@ __device__ __forceinline__ uint32_t random_bits(uint64_t i, uint32_t seed) {
     return mix((uint32_t)i * kGolden + seed + (uint32_t)(i >> 32) * kThird);
 }
 
-// ---- pairs: two f32 an instruction -------------------------------------------------------------
-struct Pair {
-    uint64_t v;
-};
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
-__device__ __forceinline__ float2 apart(Pair a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 __device__ __forceinline__ float root_of(float v) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -231,13 +205,6 @@ __device__ __forceinline__ void unpack8(uint2 q, float (&v)[8]) {
     unpack_e4m3(q.x >> 16, v[2], v[3]);
     unpack_e4m3(q.y & 0xFFFFu, v[4], v[5]);
     unpack_e4m3(q.y >> 16, v[6], v[7]);
-}
-
-// The largest of three, NaN if one is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // ---- chunks ----------------------------------------------------------------------------------------

@@ -44,6 +44,7 @@ constexpr uint32_t kShortCols = 256;       // columns of the short form, at most
 // back in a graph: 16 x 4096 (bf16) 4.6 us and 2.8, 64 x 8064 6.6 and 4.5, 152 x 4096 6.1 and 3.8, 152 x 1024 5.1 and
 // 5.5, 152 x 16384 13.6 and 14.5, 304 x 8064 9.9 and 11.6.
 constexpr uint32_t kFewRows = 96;
+constexpr uint32_t kWideThreads = 768;     // of an unaligned row of the layer norm's backward pass, at most
 constexpr uint32_t kWarpRows = 8;          // element form: rows of a CTA whose rows are one warp each
 constexpr uint32_t kLong = 0;              // NCH of a row that does not fit a CTA's registers
 
@@ -858,11 +859,11 @@ __device__ __forceinline__ void make_nan(float (&v)[N]) {
 // residual.  Thread 0 starts the copies of turn i + S - 1 once turn i's reduction has passed its
 // barrier: every thread is then done with that stage's last row (turn i - 1).  16384 x 4096 (bf16 to 8 bits,
 // groups of 128): 79 us, 0.88 of the copy rate, the issue slots 73 % full.
-template <bool MEAN, uint32_t NCH>
-__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) norm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+template <uint32_t NCH>
+__global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : NCH == 2 ? 2 : 1) rmsnorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
     launch_next();
     extern __shared__ __align__(128) uint8_t stages[];
-    __shared__ float slots[2][MEAN ? 3 : 2][32];
+    __shared__ float slots[2][2][32];
     __shared__ uint64_t full[ring::kStages];
     const uint32_t T = blockDim.x, t = threadIdx.x;
     const uint32_t xb = p.cols * (p.x_dt == DTT_BF16 ? 2 : 4), rb = p.res ? p.cols * (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
@@ -887,14 +888,11 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
     wait_previous();
     if (t == 0)
         for (uint32_t i = 0; i + 1 < S; ++i) start();
-    float w[NCH][8], b[MEAN ? NCH : 1][8];
+    float w[NCH][8];
 #pragma unroll
     for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-            w[i][k] = 1.0f;
-            if (MEAN) b[i][k] = 0.0f;
-        }
+        for (uint32_t k = 0; k < 8; ++k) w[i][k] = 1.0f;
     if (p.w) {
         Raw8 ws[NCH];
 #pragma unroll
@@ -904,10 +902,6 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
         }
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) expand8(ws[i], p.w_dt, w[i]);
-    }
-    if (MEAN && p.b) {
-#pragma unroll
-        for (uint32_t i = 0; i < NCH; ++i) load8<true>(p.b, p.w_dt, 8 * (i * T + t), p.cols, b[i]);
     }
     __syncthreads();
 
@@ -929,27 +923,10 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
                 for (uint32_t k = 0; k < 8; ++k) h[i][k] += q[k];
             }
         }
-        float mu = 0.0f;
-        if constexpr (MEAN) {
-#pragma unroll
-            for (uint32_t i = 0; i < NCH; ++i)
-#pragma unroll
-                for (uint32_t k = 0; k < 8; ++k) mu += h[i][k];
-            if (lost) mu = kNan;
-            mu = row_sum(mu, T, slots[turn][2]) * p.inv_cols;
-            if (t == 0 && p.mean) p.mean[r] = mu;
-        }
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
-                if (MEAN) {
-                    if (8 * (i * T + t) >= p.cols) h[i][k] = mu;
-                    sum += (h[i][k] - mu) * (h[i][k] - mu);
-                } else {
-                    sum += h[i][k] * h[i][k];
-                }
-            }
+            for (uint32_t k = 0; k < 8; ++k) sum += h[i][k] * h[i][k];
         if (lost) sum = kNan;
         const float s = rsqrtf(row_sum(sum, T, slots[turn][0]) * p.inv_cols + p.eps);
         if (t == 0) {
@@ -966,11 +943,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i)
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) {
-                if (MEAN) h[i][k] -= mu;
-                h[i][k] = h[i][k] * s * w[i][k];                                   // s w alone may overflow
-                if (MEAN) h[i][k] += b[i][k];
-            }
+            for (uint32_t k = 0; k < 8; ++k) h[i][k] = h[i][k] * s * w[i][k];      // s w alone may overflow
         if (p.y_dt == DTT_E4M3) {
             float m[NCH];
 #pragma unroll
@@ -1006,6 +979,220 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 6 : 
         }
 #pragma unroll
         for (uint32_t i = 0; i < NCH; ++i) store8<true>(p.y + r * p.y_pitch, p.y_dt, 8 * (i * T + t), p.cols, h[i]);
+        if (++st == S) { st = 0; phase ^= 1; }
+    }
+    if (lost && t == 0) await_copies(full, S, next, gridDim.x);
+}
+
+// ---- layer norm's ring -------------------------------------------------------------------------
+// Eight columns as four pairs.  B16: the type is bf16, known when compiled.
+template <bool B16>
+__device__ __forceinline__ void pairs8(const char* at, uint32_t dt, Pair (&v)[4]) {
+    const Raw8 q = raw8(at, B16 ? (uint32_t)DTT_BF16 : dt);
+    if (B16 || dt == DTT_BF16) {
+        v[0] = pair(bf16_lo(q.a.x), bf16_hi(q.a.x)), v[1] = pair(bf16_lo(q.a.y), bf16_hi(q.a.y));
+        v[2] = pair(bf16_lo(q.a.z), bf16_hi(q.a.z)), v[3] = pair(bf16_lo(q.a.w), bf16_hi(q.a.w));
+    } else {
+        v[0] = pair(__uint_as_float(q.a.x), __uint_as_float(q.a.y)), v[1] = pair(__uint_as_float(q.a.z), __uint_as_float(q.a.w));
+        v[2] = pair(__uint_as_float(q.b.x), __uint_as_float(q.b.y)), v[3] = pair(__uint_as_float(q.b.z), __uint_as_float(q.b.w));
+    }
+}
+__device__ __forceinline__ void singles8(const Pair (&v)[4], float (&f)[8]) {
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        const float2 a = apart(v[k]);
+        f[2 * k] = a.x, f[2 * k + 1] = a.y;
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (uint32_t o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// As the ring above, with the mean and the variance by one barrier: a warp takes the mean of its own columns and sums their squares
+// about that, both by shuffles; the warps' sums S_w and squares Q_w then meet in shared memory, where
+//     mean = sum S_w / cols,   sum (h - mean)^2 = sum Q_w + sum n_w (S_w / n_w - mean)^2
+// adds what the warps' means are off by (T. F. Chan, G. H. Golub, R. J. LeVeque, 1979): no large numbers cancel.
+// 16384 x 4096 (bf16 to 8 bits, groups of 128): 84 us, 0.83 of the copy rate, with three CTAs of 256 threads an SM; 86 with four, whose
+// registers spill, 97 with two, 95 with 128 threads of four chunks each.  Two reductions with a barrier each, one value
+// an instruction and types looked up at each access: 113.
+constexpr uint32_t kLayerThreads = 256;        // of a row with two chunks a thread, at most
+template <uint32_t NCH, bool B16>
+__global__ void __launch_bounds__(NCH == 1 ? 128 : NCH == 2 ? kLayerThreads : kRingThreads, NCH == 1 ? 8 : NCH == 2 ? 3 : 1) layernorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
+    launch_next();
+    extern __shared__ __align__(128) uint8_t stages[];
+    __shared__ float2 slots[2][32];
+    __shared__ float tops[2][32];
+    __shared__ uint64_t full[ring::kStages];
+    const uint32_t T = blockDim.x, t = threadIdx.x, lane = t % 32, warp = t / 32;
+    const uint32_t xe = B16 || p.x_dt == DTT_BF16 ? 2 : 4, re = B16 || p.res_dt == DTT_BF16 ? 2 : 4;
+    const uint32_t xb = p.cols * xe, rb = p.res ? p.cols * re : 0;
+    const uint32_t stage_bytes = xb + rb;
+    uint64_t next = blockIdx.x;                     // thread 0: the row to be fetched next, and its stage
+    uint32_t next_st = 0;
+    auto start = [&] {
+        if (next >= p.rows) return;
+        const uint64_t r = next;
+        const uint32_t bar = saddr(full + next_st), dst = saddr(stages) + next_st * stage_bytes;
+        next += gridDim.x;
+        if (++next_st == S) next_st = 0;
+        bar_expect_tx(bar, stage_bytes);
+        bulk_load(dst, p.x + r * p.x_pitch, xb, bar);
+        if (rb) bulk_load(dst + xb, p.res + r * p.res_pitch, rb, bar);
+    };
+    if (t == 0) {
+        for (uint32_t i = 0; i < S; ++i) bar_init(saddr(full + i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    // columns of a warp: 256 of each of its chunks, less where the row ends
+    const auto columns_of = [&](uint32_t w) {
+        uint32_t n = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) {
+            const uint32_t c = 8 * (i * T + 32 * w);
+            if (c < p.cols) n += min(p.cols - c, 256u);
+        }
+        return (float)n;
+    };
+    const float mine_inv = 1.0f / fmaxf(columns_of(warp), 1.0f);
+    const float lanes_n = lane < T / 32 ? columns_of(lane) : 0.0f, lanes_inv = 1.0f / fmaxf(lanes_n, 1.0f);   // warp `lane`'s
+    uint32_t c[NCH], scale_at[NCH];
+    bool in[NCH], scales[NCH];
+#pragma unroll
+    for (uint32_t i = 0; i < NCH; ++i) {
+        c[i] = 8 * (i * T + t);
+        in[i] = c[i] < p.cols;
+        scale_at[i] = p.group_lanes ? c[i] / 8 / p.group_lanes : 0;
+        scales[i] = p.group_lanes ? in[i] && t % p.group_lanes == 0 : t == 0 && i == 0;
+    }
+    wait_previous();
+    if (t == 0)
+        for (uint32_t i = 0; i + 1 < S; ++i) start();
+    Pair w[NCH][4], b[NCH][4];
+#pragma unroll
+    for (uint32_t i = 0; i < NCH; ++i) {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) w[i][k] = both(1.0f), b[i][k] = both(0.0f);
+        const uint32_t we = B16 || p.w_dt == DTT_BF16 ? 2 : 4;
+        if (p.w && in[i]) pairs8<B16>(p.w + c[i] * we, p.w_dt, w[i]);
+        if (p.b && in[i]) pairs8<B16>(p.b + c[i] * we, p.w_dt, b[i]);
+    }
+    __syncthreads();
+
+    uint32_t st = 0, phase = 0, turn = 0;
+    bool lost = false;
+    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x, turn ^= 1) {
+        lost = lost || DTT_NORM_ROW_LATE || !bar_wait(saddr(full + st), phase);
+        const char* row = reinterpret_cast<const char*>(stages) + st * stage_bytes;
+        Pair h[NCH][4], sum = both(0.0f);
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) {
+            // a thread past the row's end takes its first chunk, and leaves it out
+            const uint32_t from = in[i] ? c[i] : 0;
+            pairs8<B16>(row + from * xe, p.x_dt, h[i]);
+            if (rb) {
+                Pair q[4];
+                pairs8<B16>(row + xb + from * re, p.res_dt, q);
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) h[i][k] = h[i][k] + q[k];
+            }
+        }
+        if (lost) {
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) h[i][k] = both(kNan);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) {
+            if (!in[i]) continue;
+            if (p.res_out) {
+                float f[8];
+                singles8(h[i], f);
+                store8<true>(p.res_out + r * p.res_out_pitch, B16 ? (uint32_t)DTT_BF16 : p.res_dt, c[i], p.cols, f);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) sum = sum + h[i][k];
+        }
+        const float2 part = apart(sum);
+        const float own = warp_sum(part.x + part.y);
+        const Pair centre = both(-own * mine_inv);
+        Pair squares = both(0.0f);
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i) {
+            if (!in[i]) continue;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                const Pair d = h[i][k] + centre;
+                squares = fma2(d, d, squares);
+            }
+        }
+        const float2 part2 = apart(squares);
+        const float own2 = warp_sum(part2.x + part2.y);
+        if (lane == 0) slots[turn][warp] = make_float2(own, own2);
+        __syncthreads();
+        const float2 from_warp = lane < T / 32 ? slots[turn][lane] : make_float2(0.0f, 0.0f);
+        const float mu = warp_sum(from_warp.x) * p.inv_cols;
+        const float off = from_warp.x * lanes_inv - mu;
+        const float s = rsqrtf(warp_sum(fmaf(lanes_n * off, off, from_warp.y)) * p.inv_cols + p.eps);
+        if (t == 0) {
+            if (!lost) start();
+            if (p.mean) p.mean[r] = mu;
+            if (p.rstd) p.rstd[r] = s;
+        }
+        const Pair less = both(-mu), by = both(s);
+#pragma unroll
+        for (uint32_t i = 0; i < NCH; ++i)
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) h[i][k] = fma2((h[i][k] + less) * by, w[i][k], b[i][k]);
+        if (p.y_dt == DTT_E4M3) {
+            float m[NCH];
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i) {
+                float f[8];
+                singles8(h[i], f);
+                m[i] = max3_nan(max3_nan(fabsf(f[0]), fabsf(f[1]), fabsf(f[2])), fabsf(f[3]), fabsf(f[4]));
+                m[i] = max3_nan(max_nan(m[i], fabsf(f[5])), fabsf(f[6]), fabsf(f[7]));
+                if (!in[i]) m[i] = 0.0f;
+            }
+            if (p.group_lanes == 0) {
+#pragma unroll
+                for (uint32_t i = 1; i < NCH; ++i) m[0] = max_nan(m[0], m[i]);
+                m[0] = row_max(m[0], T, tops[turn]);
+#pragma unroll
+                for (uint32_t i = 1; i < NCH; ++i) m[i] = m[0];
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < NCH; ++i)
+                    for (uint32_t d = p.group_lanes >> 1; d > 0; d >>= 1) m[i] = max_nan(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], d));
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i) {
+                const float scale = scale_of(m[i]);
+                const Divisor v = divisor_of(scale);
+                if (scales[i]) p.scales[r * p.groups + scale_at[i]] = scale;
+                // quotient() of two at a time
+                const Pair inv = both(v.inv), less_d = both(-v.d);
+                float f[8];
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const Pair q = h[i][k] * inv;
+                    const float2 a = apart(fma2(fma2(less_d, q, h[i][k]), inv, q));
+                    f[2 * k] = a.x, f[2 * k + 1] = a.y;
+                }
+                if (in[i]) store8<true>(p.y + r * p.y_pitch, DTT_E4M3, c[i], p.cols, f);
+            }
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < NCH; ++i) {
+                float f[8];
+                singles8(h[i], f);
+                if (in[i]) store8<true>(p.y + r * p.y_pitch, p.y_dt, c[i], p.cols, f);
+            }
+        }
         if (++st == S) { st = 0; phase ^= 1; }
     }
     if (lost && t == 0) await_copies(full, S, next, gridDim.x);
@@ -1264,7 +1451,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) norm_fwd_ring_elements_kernel
 // 16384 x 4001 in f32: 179 us, 0.86 of the copy rate; 1021 x 5001 in f32 19 us, 0.63: one CTA a SM (60 KiB a
 // stage), seven rows each.
 template <bool MEAN, uint32_t E>
-__global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
+__global__ void __launch_bounds__(MEAN && E == 8 ? kWideThreads : kRingThreads) norm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
     if (blockIdx.x >= p.partials) return weight_columns<MEAN>(p);
     extern __shared__ __align__(128) uint8_t stages[];
@@ -1392,6 +1579,12 @@ uint32_t element_threads(uint32_t cols, uint32_t E, uint32_t threads) {
     return t <= threads ? t : 0;
 }
 
+using RingKernel = void (*)(FwdParams, uint32_t);
+RingKernel layernorm_ring(uint32_t nch, bool b16) {
+    if (b16) return nch == 1 ? layernorm_fwd_ring_kernel<1, true> : nch == 2 ? layernorm_fwd_ring_kernel<2, true> : layernorm_fwd_ring_kernel<4, true>;
+    return nch == 1 ? layernorm_fwd_ring_kernel<1, false> : nch == 2 ? layernorm_fwd_ring_kernel<2, false> : layernorm_fwd_ring_kernel<4, false>;
+}
+
 template <bool MEAN>
 cudaError_t launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     const uint32_t xe = p.x_dt == DTT_BF16 ? 2 : 4, re = p.res ? (p.res_dt == DTT_BF16 ? 2 : 4) : 0;
@@ -1405,14 +1598,19 @@ cudaError_t launch_fwd(const FwdParams& p, bool vec, cudaStream_t stream) {
     // two stages where a CTA has many rows: reads that run further ahead of the writes cost more than they
     // hide (40000 x 2048 to 8 bits: 104 us with three, 90 with two; 2048 x 4096, three rows a CTA: 14.7 and
     // 16.5; the backward pass, 30000 x 1024: 63 with eight, 76 with two)
-    const ring::Plan g = ring::plan(p.cols, vec, vec ? xb + rb : xb + rb + 60, kFwdOwn<MEAN>, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : ring::kStages);
+    const ring::Plan g = MEAN && vec ? ring::plan(p.cols, vec, xb + rb, kFwdOwn<MEAN>, 1024, {1024, 768, 512}, 2, p.rows >= 32 * sms ? 2 : ring::kStages, 16 * kLayerThreads)
+                                     : ring::plan(p.cols, vec, vec ? xb + rb : xb + rb + 60, kFwdOwn<MEAN>, vec ? 1024 : 2048, {vec ? 1536u : 1024u, 1024, 512}, 2, p.rows >= 32 * sms ? 2 : ring::kStages);
     // The chunk form's loads wait for one another, the ring's do not: 152 x 8064 (bf16) 6.7 us by chunks, 3.7 by
     // the ring.  The element form's go out together, and it is the faster one while there are few rows:
     // 600 x 3001 5.7 us and 6.6, 2400 x 3001 22.2 and 18.4.
     if (g.ctas && (vec || p.rows >= 8 * sms)) {
         const uint32_t grid = (uint32_t)std::min<uint64_t>(p.rows, g.ctas * sms);
-        auto kernel = vec ? (g.nch == 1 ? norm_fwd_ring_kernel<MEAN, 1> : g.nch == 2 ? norm_fwd_ring_kernel<MEAN, 2> : norm_fwd_ring_kernel<MEAN, 4>)
-                          : (g.nch == 1 ? norm_fwd_ring_elements_kernel<MEAN, 8> : norm_fwd_ring_elements_kernel<MEAN, 16>);
+        if (!vec) return launch(g.nch == 1 ? norm_fwd_ring_elements_kernel<MEAN, 8> : norm_fwd_ring_elements_kernel<MEAN, 16>, grid, g.threads, g.smem, 0, true, stream, p, g.stages);
+        if constexpr (MEAN) {
+            const bool b16 = p.x_dt == DTT_BF16 && (!p.res || p.res_dt == DTT_BF16) && (!p.res_out || p.res_dt == DTT_BF16) && ((!p.w && !p.b) || p.w_dt == DTT_BF16);
+            return launch(layernorm_ring(g.nch, b16), grid, g.threads, g.smem, 0, true, stream, p, g.stages);
+        }
+        auto kernel = g.nch == 1 ? rmsnorm_fwd_ring_kernel<1> : g.nch == 2 ? rmsnorm_fwd_ring_kernel<2> : rmsnorm_fwd_ring_kernel<4>;
         return launch(kernel, grid, g.threads, g.smem, 0, true, stream, p, g.stages);
     }
     if (!vec) {
@@ -1441,7 +1639,13 @@ cudaError_t launch_bwd(BwdParams& p, bool vec, cudaStream_t stream) {
         return launch(norm_bwd_short_kernel<MEAN>, p.partials + columns, 256, 0, 0, true, stream, p, lanes);
     }
     const uint64_t stage = (uint64_t)p.cols * (ge + (p.dres ? 2 : 1) * he);
-    const ring::Plan g = ring::plan(p.cols, vec, vec ? stage : stage + 90, kBwdOwn<MEAN>, 2048, {1024, 512, 256}, 1, ring::kStages);
+    ring::Plan g = ring::plan(p.cols, vec, vec ? stage : stage + 90, kBwdOwn<MEAN>, 2048, {1024, 512, 256}, 1, ring::kStages);
+    // where an SM has room for one CTA the layer norm gives it more threads: 1021 x 5001 (f32) 23 us with 16 elements a
+    // thread, 22 with 8
+    if (MEAN && !vec && g.ctas == 1 && g.nch == 2 && p.cols <= 8 * kWideThreads && p.rows > kFewRows) {
+        g.nch = 1;
+        g.threads = (p.cols + 255) / 256 * 32;
+    }
     // by chunks and by the ring: 200 x 4096 (bf16) 11.2 us and 7.6, 16384 x 4096 255 and 92; by elements and by
     // the ring: 152 x 1021 (f32) 5.5 and 5.6, 460 x 5001 (f32) 15.3 and 10.8
     if (g.ctas && (vec || p.rows > sms)) {
@@ -1526,14 +1730,19 @@ cudaError_t preload_norm() {
         const cudaError_t e = prepare(k);
         if (e != cudaSuccess) return e;
     }
-    const void* fwd_rings[] = {(const void*)norm_fwd_ring_kernel<MEAN, 1>, (const void*)norm_fwd_ring_kernel<MEAN, 2>, (const void*)norm_fwd_ring_kernel<MEAN, 4>,
-                               (const void*)norm_fwd_ring_elements_kernel<MEAN, 8>, (const void*)norm_fwd_ring_elements_kernel<MEAN, 16>};
+    const void* fwd_rings[] = {(const void*)(MEAN ? layernorm_ring(1, true) : rmsnorm_fwd_ring_kernel<1>), (const void*)(MEAN ? layernorm_ring(2, true) : rmsnorm_fwd_ring_kernel<2>),
+                               (const void*)(MEAN ? layernorm_ring(4, true) : rmsnorm_fwd_ring_kernel<4>), (const void*)norm_fwd_ring_elements_kernel<MEAN, 8>,
+                               (const void*)norm_fwd_ring_elements_kernel<MEAN, 16>, (const void*)layernorm_ring(1, false), (const void*)layernorm_ring(2, false),
+                               (const void*)layernorm_ring(4, false)};
     const void* bwd_rings[] = {(const void*)norm_bwd_ring_kernel<MEAN, 1>, (const void*)norm_bwd_ring_kernel<MEAN, 2>, (const void*)norm_bwd_ring_kernel<MEAN, 4>,
                                (const void*)norm_bwd_ring_elements_kernel<MEAN, 8>, (const void*)norm_bwd_ring_elements_kernel<MEAN, 16>};
-    for (uint32_t i = 0; i < 10; ++i) {
-        const void* k = i < 5 ? fwd_rings[i] : bwd_rings[i - 5];
-        cudaError_t e = prepare(k, i < 5 ? kFwdOwn<MEAN> : kBwdOwn<MEAN>);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring::kSmem);
+    auto ring = [](const void* k, uint32_t own) {
+        const cudaError_t e = prepare(k, own);
+        return e == cudaSuccess ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring::kSmem) : e;
+    };
+    for (uint32_t i = 0; i < (MEAN ? 8 : 5); ++i) {
+        cudaError_t e = ring(fwd_rings[i], kFwdOwn<MEAN>);
+        if (e == cudaSuccess && i < 5) e = ring(bwd_rings[i], kBwdOwn<MEAN>);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -24,8 +24,9 @@ struct Plan {
 // where an SM has four CTAs or more.  stage: bytes of one; own: of the kernel's shared memory beside the stages.
 // Measured: the forward pass of 20000 x 5001 (f32) takes 279 us with one CTA of five stages, 211 with two of two;
 // the backward pass of 4000 x 4096 (f32) 49 us with one, 53 with two.
+// two: columns of at most two chunks a thread.
 inline Plan plan(uint32_t cols, bool vec, uint64_t stage, uint32_t own, uint32_t one, const uint32_t (&threads)[3], uint32_t least,
-                 uint32_t stages) {
+                 uint32_t stages, uint32_t two = 16 * kThreads) {
     Plan g{};
     if (2 * stage > kSmem) return g;
     const uint32_t bytes = (uint32_t)stage;
@@ -33,7 +34,7 @@ inline Plan plan(uint32_t cols, bool vec, uint64_t stage, uint32_t own, uint32_t
     for (; i < (vec ? 3 : 2); ++i) {
         g.nch = 1u << i;
         g.threads = ((cols + 8 * g.nch - 1) / (8 * g.nch) + 31) / 32 * 32;
-        if (g.threads <= kThreads && (i > 0 || cols <= one)) break;
+        if (g.threads <= kThreads && cols <= (i == 0 ? one : i == 1 ? two : ~0u)) break;
     }
     if (g.threads < 64 || g.threads > kThreads) return {};
     auto fit = [&](uint32_t ctas, uint32_t n) {
