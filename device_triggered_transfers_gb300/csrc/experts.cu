@@ -42,17 +42,31 @@ __device__ __forceinline__ uint32_t expert_of(const RouteParams& p, uint64_t i) 
     return id >= 0 && e < p.experts ? (uint32_t)e : p.experts;
 }
 
-// How many of the warp's run of pairs each expert has: mine[e], zero before.  Pairs of 32 neighbours that share an
-// expert are counted by the first of them.
-__device__ __forceinline__ void count_run(const RouteParams& p, uint64_t from, uint64_t to, uint32_t* mine) {
+// The warp's run of pairs, 32 neighbours at a time in their order: each(i, e, same), e the expert of the lane's pair i
+// (`experts` from `to` on), same the lanes that share it.  Experts of kAhead times 32 pairs are loaded together.
+constexpr uint32_t kAhead = 4;
+template <class F>
+__device__ __forceinline__ void walk_run(const RouteParams& p, uint64_t from, uint64_t to, F each) {
     const uint32_t lane = threadIdx.x % 32;
-    for (uint64_t i0 = from; i0 < to; i0 += 32) {
-        const uint64_t i = i0 + lane;
-        const uint32_t e = i < to ? expert_of(p, i) : p.experts;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        if (e < p.experts && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+    for (uint64_t i0 = from; i0 < to; i0 += 32 * kAhead) {
+        uint32_t e[kAhead];
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint64_t i = i0 + 32 * k + lane;
+            e[k] = i < to ? expert_of(p, i) : p.experts;
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k) each(i0 + 32 * k + lane, e[k], __match_any_sync(0xFFFFFFFFu, e[k]));
     }
+}
+
+// How many of the run each expert has: mine[e], zero before.  Pairs of 32 neighbours that share an expert are counted by
+// the first of them.
+__device__ __forceinline__ void count_run(const RouteParams& p, uint64_t from, uint64_t to, uint32_t* mine) {
+    walk_run(p, from, to, [&](uint64_t, uint32_t e, uint32_t same) {
+        if (e < p.experts && threadIdx.x % 32 == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    });
 }
 
 __global__ void __launch_bounds__(kRouteThreads) route_count_kernel(const __grid_constant__ RouteParams p) {
@@ -114,20 +128,37 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
     const uint64_t from = min(blockIdx.x * p.each + warp * run, p.pairs), to = min(blockIdx.x * p.each + warp * run + run, p.pairs);
     count_run(p, from, to, counts + warp * p.experts);
     __syncthreads();
-    // each warp's first place among its expert's rows, and all of an expert's rows
-    for (uint32_t e = t; e < p.experts; e += kRouteThreads) {
-        uint32_t sum = 0, before = 0;
-        if (p.parts)
-            for (uint32_t b = 0; b < gridDim.x; ++b) {
-                if (b == blockIdx.x) before = sum;
-                sum += p.parts[(uint64_t)b * p.experts + e];
+    // of each expert, the pairs of the CTAs before this one and of all: kRouteThreads / experts threads (or one) add up the
+    // parts of as many ranges of CTAs
+    if (p.parts) {
+        const uint32_t groups = p.experts < kRouteThreads ? kRouteThreads / p.experts : 1, g = t / p.experts;
+        const uint32_t each = (gridDim.x + groups - 1) / groups;
+        for (uint32_t e = t; e < p.experts; e += kRouteThreads) total[e] = offset[e] = 0;
+        __syncthreads();
+        if (g < groups || groups == 1)
+            for (uint32_t e = groups == 1 ? t : t % p.experts; e < p.experts; e += kRouteThreads) {
+                uint32_t sum = 0, before = 0;
+                const uint32_t b0 = groups == 1 ? 0 : g * each, b1 = min(b0 + each, gridDim.x);
+#pragma unroll 16
+                for (uint32_t b = b0; b < b1; ++b) {
+                    const uint32_t n = p.parts[(uint64_t)b * p.experts + e];
+                    sum += n;
+                    before += b < blockIdx.x ? n : 0;
+                }
+                atomicAdd(total + e, sum);             // whole numbers: in any order
+                atomicAdd(offset + e, before);
             }
+        __syncthreads();
+    }
+    // each warp's first place among its expert's rows
+    for (uint32_t e = t; e < p.experts; e += kRouteThreads) {
+        uint32_t before = p.parts ? offset[e] : 0;
         for (uint32_t w = 0; w < kRouteWarps; ++w) {
             const uint32_t n = counts[w * p.experts + e];
             counts[w * p.experts + e] = before;
             before += n;
         }
-        total[e] = p.parts ? sum : before;
+        if (!p.parts) total[e] = before;
         offset[e] = (total[e] + p.align - 1) / p.align * p.align;
     }
     __syncthreads();
@@ -142,17 +173,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
                 p.offsets[e + 1] = (int32_t)min(offset[e] + (total[e] + p.align - 1) / p.align * p.align, p.max_rows);
         }
     uint32_t* mine = counts + warp * p.experts;
-    for (uint64_t i0 = from; i0 < to; i0 += 32) {
-        const uint64_t i = i0 + lane;
-        const uint32_t e = i < to ? expert_of(p, i) : p.experts;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    walk_run(p, from, to, [&](uint64_t i, uint32_t e, uint32_t same) {
         uint32_t at = p.max_rows;
         if (e < p.experts) at = offset[e] + mine[e] + __popc(same & ((1u << lane) - 1));
         __syncwarp();
         if (e < p.experts && lane == __ffs(same) - 1) mine[e] += __popc(same);
         __syncwarp();
         if (i < to) p.position[i] = at < p.max_rows ? (int32_t)at : -1;
-    }
+    });
 }
 
 // ---- rows --------------------------------------------------------------------------------------

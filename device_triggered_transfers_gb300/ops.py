@@ -105,10 +105,10 @@ class RMSNorm:
         if t is None:
             return 0, 0
         if t.dtype != dtype or t.shape != shape:
-            raise D.DttError(D.EINVAL, f"{self._who}: {name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
         row, col = t.stride()
         if not t.is_cuda or (col != 1 and self.cols > 1):
-            raise D.DttError(D.EINVAL, f"{self._who}: {name} must be on the GPU with contiguous rows")
+            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be on the GPU with contiguous rows")
         return t.data_ptr(), row * size
 
     def _flat(self, name: str, t, n: int, dtype) -> int:
@@ -116,7 +116,7 @@ class RMSNorm:
         if t is None:
             return 0
         if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-            raise D.DttError(D.EINVAL, f"{self._who}: {name} must be {n} contiguous {dtype} on the GPU")
+            raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be {n} contiguous {dtype} on the GPU")
         return t.data_ptr()
 
     def _scratch(self, needed: bool, stream, device) -> Tuple[int, int]:
@@ -161,11 +161,13 @@ class RMSNorm:
             D._check(rc)
 
 
-def _here(who: str, name: str, t) -> None:
-    """t is on the current device: the calls launch there."""
+def _here(who: str, name: str, t) -> int:
+    """The number of t's GPU, which is the current one: the calls launch there."""
     import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    device = t.get_device()
+    if device < 0 or device != torch.cuda.current_device():
         raise D.DttError(D.EINVAL, f"{who}: {name} must be on the current GPU")
+    return device
 
 
 class LayerNorm(RMSNorm):
@@ -181,13 +183,30 @@ class LayerNorm(RMSNorm):
                  y: str = "bf16", group: int = 0, eps: float = 1e-5):
         super().__init__(cols, x, residual, weight, y, group, eps)
 
+    def _rows(self, name: str, t, shape, dtype, size: int) -> Tuple[int, int]:
+        if t is None:
+            return 0, 0
+        if t.dtype != dtype or t.shape != shape:
+            raise D.DttError(D.EINVAL, f"LayerNorm: {name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+        row, col = t.stride()
+        if t.get_device() != self._device or (col != 1 and self.cols > 1):
+            raise D.DttError(D.EINVAL, f"LayerNorm: {name} must be on the current GPU with contiguous rows")
+        return t.data_ptr(), row * size
+
+    def _flat(self, name: str, t, n: int, dtype) -> int:
+        if t is None:
+            return 0
+        if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != self._device:
+            raise D.DttError(D.EINVAL, f"LayerNorm: {name} must be {n} contiguous {dtype} on the current GPU")
+        return t.data_ptr()
+
     def forward(self, x, weight, bias, y, residual=None, residual_out=None, scales=None, mean=None, rstd=None,
                 stream=None) -> None:
         """y, and where given residual_out (= h; may be residual itself), scales ([rows, scale_cols] f32, with an
         e4m3 y), mean and rstd ([rows] f32, which the backward pass needs).  weight, bias: or None."""
         rows = x.shape[0]
         shape = (rows, self.cols)
-        _here(self._who, "x", x)
+        self._device = _here(self._who, "x", x)
         xp, xs = self._rows("x", x, shape, self._x, self._xe)
         rp, rs = self._rows("residual", residual, shape, self._res, self._rese)
         op, os_ = self._rows("residual_out", residual_out, shape, self._res, self._rese)
@@ -206,7 +225,7 @@ class LayerNorm(RMSNorm):
         gradients dy of y and dres of residual_out (None: zero)."""
         rows = dy.shape[0]
         shape = (rows, self.cols)
-        _here(self._who, "dy", dy)
+        self._device = _here(self._who, "dy", dy)
         gp, gs = self._rows("dy", dy, shape, self._x, self._xe)
         hp, hs = self._rows("h", h, shape, self._res, self._rese)
         sp, ss = self._rows("dres", dres, shape, self._res, self._rese)
@@ -257,8 +276,8 @@ class ExpertRows:
         """Address of a contiguous argument; 0 for None."""
         if t is None:
             return 0
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be contiguous {dtype} {list(shape)} on the GPU, "
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._device:
+            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be contiguous {dtype} {list(shape)} on the current GPU, "
                                        f"not {t.dtype} {list(t.shape)}")
         return t.data_ptr()
 
@@ -266,13 +285,14 @@ class ExpertRows:
         """(address, pitch in bytes) of an argument of rows (None: any number) x cols; (0, 0) for None."""
         if t is None:
             return 0, 0
-        if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be [{'any' if rows is None else rows}, {cols}], not {list(t.shape)}")
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be [{'any' if rows is None else rows}, {cols}], not {list(shape)}")
         if dtypes is not None and t.dtype not in dtypes:
             raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be one of {list(dtypes)}, not {t.dtype}")
         row, col = t.stride()
-        if not t.is_cuda or (col != 1 and cols > 1):
-            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be on the GPU with contiguous rows")
+        if t.get_device() != self._device or (col != 1 and cols > 1):
+            raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be on the current GPU with contiguous rows")
         return t.data_ptr(), row * t.element_size()
 
     def _sorted(self, position, offsets, counts) -> Tuple[int, int, int]:
@@ -285,7 +305,7 @@ class ExpertRows:
         position ([tokens, top_k] int32): each pair's row, or -1; offsets ([experts + 1] int32): where each expert's
         rows begin; counts ([experts] int32): how many pairs it has.  max_rows: rows that there are room for
         (None: most_rows(tokens)); pairs beyond get -1."""
-        _here(self._who, "ids", ids)
+        self._device = _here(self._who, "ids", ids)
         tokens = ids.shape[0]
         ip = self._flat("ids", ids, (tokens, self.top_k), self._i64 if ids.dtype == self._i64 else self._i32)
         pp = self._flat("position", position, (tokens, self.top_k), self._i32)
@@ -304,7 +324,7 @@ class ExpertRows:
     def dispatch(self, x, position, offsets, counts, rows, scales=None, row_scales=None, stream=None) -> None:
         """rows[position[t, j]] = x[t] (both of one type, any), and row_scales[position[t, j]] = scales[t] (f32, both or
         neither); zeros in the rows that fill an expert's up; rows behind the last expert's are left as they were."""
-        _here(self._who, "x", x)
+        self._device = _here(self._who, "x", x)
         tokens, cols = x.shape[0], x.shape[-1]
         xp, xs = self._rows("x", x, tokens, cols)
         rp, rs = self._rows("rows", rows, None, cols, (x.dtype,))
@@ -326,7 +346,7 @@ class ExpertRows:
     def combine(self, rows, position, out, weights=None, stream=None) -> None:
         """out[t] = sum of weights[t, j] rows[position[t, j]] over the pairs with a row (rows, out: bf16 or f32; weights:
         [tokens, top_k] f32).  weights None: 1, the gradient of `dispatch`, whose rows' gradient `rows` is then."""
-        _here(self._who, "out", out)
+        self._device = _here(self._who, "out", out)
         tokens, cols = out.shape[0], out.shape[-1]
         op, os_ = self._rows("out", out, tokens, cols, self._row_types)
         rp, rs = self._rows("rows", rows, None, cols, self._row_types)
@@ -341,7 +361,7 @@ class ExpertRows:
         """drows[position[t, j]] = weights[t, j] dout[t], zeros in the rows that fill an expert's up (those behind the last
         expert's are left as they were), and where given dweights[t, j] = dout[t] . rows[position[t, j]] ([tokens, top_k]
         f32, 0 for a pair without a row).  rows may be None without dweights; drows has its type."""
-        _here(self._who, "dout", dout)
+        self._device = _here(self._who, "dout", dout)
         tokens, cols = dout.shape[0], dout.shape[-1]
         gp, gs = self._rows("dout", dout, tokens, cols, self._row_types)
         dp, ds = self._rows("drows", drows, None, cols, self._row_types)
