@@ -271,6 +271,33 @@ def test_a_captured_pass_replays_and_another_stream_takes_it(rows, cols):
         check_backward(dict(dy=dy, h=out["residual_out"], weight=a["weight"], mean=out["mean"], rstd=out["rstd"]), None, dx, dw, db, "f32")
 
 
+@pytest.mark.parametrize("late", ["true", "r % 5 == 3", "r % 5 == 3 && t == 37"])
+def test_rows_that_do_not_arrive_in_time_are_nan_and_so_are_the_parameters_gradients(late, tmp_path):
+    """As test_gpu_ops_edges.py has it for the other norm: every value is right or NaN, whoever gives a row up."""
+    from test_gpu_ops_edges import library_with
+    L = library_with("norm.cu", [f"-DDTT_NORM_ROW_LATE=({late})"], str(tmp_path))
+    for rows, cols, pad, kind in ((2000, 1024, 0, "bf16"), (1000, 4096, 0, "bf16"), (1000, 4096, 0, "f32"), (400, 12288, 0, "bf16"), (1300, 1001, 1, "f32"), (1300, 5001, 3, "f32")):
+        op, a, more, _ = case(rows, cols, x=kind, residual=kind, weight=kind, y=kind, pad=pad)
+        back, b, dres, _ = grad_case(rows, cols, x=kind, residual=kind, weight=kind, pad=pad)
+        got = []
+        for other in (False, True):
+            if other:
+                op._forward, back._backward = L.dtt_layernorm_forward, L.dtt_layernorm_backward
+            y, h, dx = (torch.full((rows, cols + pad), 7.0, device="cuda").to(TYPES[kind])[:, :cols] for _ in range(3))
+            mean, rstd, dw, db = (torch.full((n,), 7.0, device="cuda") for n in (rows, rows, cols, cols))
+            forward(op, a, more, dict(y=y, residual_out=h, mean=mean, rstd=rstd))
+            back.backward(**b, dx=dx, dweight=dw, dbias=db, dres=dres)
+            got.append((y, h, mean, rstd, dx, dw, db))
+        for right, seen in zip(*got):
+            assert not torch.isnan(right).any()
+            gone = torch.isnan(seen)
+            assert gone.all() if late == "true" else (gone | (seen == right)).all()
+        y, h, mean, rstd, dx, dw, db = got[1]
+        assert torch.isnan(rstd[3::5]).all() and torch.isnan(mean[3::5]).all() and torch.isnan(h[3::5]).any(-1).all() and torch.isnan(dx[3::5]).all()
+        assert torch.equal(torch.isnan(rstd), torch.isnan(y).all(-1)) and torch.equal(torch.isnan(rstd), torch.isnan(y).any(-1))
+        assert torch.equal(torch.isnan(dx).any(-1), torch.isnan(dx).all(-1)) and torch.isnan(dw).any() and torch.isnan(db).any()
+
+
 def test_rows_past_four_gigabytes():
     rows, cols = 70000, 32768                  # 4.6 GB of bf16
     x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
