@@ -12,9 +12,19 @@
 #include "internal.h"
 #include "rowio.cuh"
 
+#ifndef RING_COLS
+#define RING_COLS 1024
+#endif
+#ifndef RING_TOKENS
+#define RING_TOKENS 4
+#endif
 namespace dtt {
 namespace {
 
+// Whether a thread gives an item of the ring up: a build of its own shows that the results stay the same.
+#ifndef DTT_EXPERTS_LATE
+#define DTT_EXPERTS_LATE false
+#endif
 constexpr uint32_t kMostExperts = 1024, kMostChoices = 32;
 constexpr uint32_t kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
 constexpr uint32_t kMostParts = 64;            // CTAs of the sort, at most
@@ -202,17 +212,21 @@ struct Sorted {
 
 __device__ __forceinline__ uint32_t row_of(const Sorted& s, uint64_t pair) { return (uint32_t)s.position[pair]; }   // -1: no row
 
-// Rows from an expert's last to where the next one's begin, zeros: CTA `cta` of fill_ctas.
+// Rows from an expert's last to where the next one's begin, zeros: part `cta` of fill_ctas, by `threads` threads.
 template <class W>
-__device__ __forceinline__ void zero_words(char* row, uint32_t bytes) {
-    for (uint32_t i = threadIdx.y * blockDim.x + threadIdx.x; i < bytes / sizeof(W); i += blockDim.x * blockDim.y) reinterpret_cast<W*>(row)[i] = W{};
+__device__ __forceinline__ void zero_words(char* row, uint32_t bytes, uint32_t t, uint32_t threads) {
+    for (uint32_t i = t; i < bytes / sizeof(W); i += threads) reinterpret_cast<W*>(row)[i] = W{};
 }
 template <class W>
-__device__ __forceinline__ void fill_rows(const Sorted& s, const Rows& rows, uint32_t cta) {
+__device__ __forceinline__ void fill_rows(const Sorted& s, const Rows& rows, uint32_t cta, uint32_t t, uint32_t threads) {
     const uint32_t e = cta / s.fills;
     const uint32_t from = (uint32_t)s.offsets[e] + (uint32_t)s.counts[e] + cta % s.fills * kFillRows;
     const uint32_t to = min(min((uint32_t)s.offsets[e + 1], s.max_rows), from + kFillRows);
-    for (uint32_t r = from; r < to; ++r) zero_words<W>(rows.at + r * rows.pitch, rows.bytes);
+    for (uint32_t r = from; r < to; ++r) zero_words<W>(rows.at + r * rows.pitch, rows.bytes, t, threads);
+}
+template <class W>
+__device__ __forceinline__ void fill_rows(const Sorted& s, const Rows& rows, uint32_t cta) {
+    fill_rows<W>(s, rows, cta, threadIdx.y * blockDim.x + threadIdx.x, blockDim.x * blockDim.y);
 }
 
 template <class W>
@@ -428,6 +442,237 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(const 
     }
 }
 
+// ---- rows through shared memory -----------------------------------------------------------------
+// For many tokens of long rows: persistent CTAs, two an SM, of eight warps that add up and one that fetches.  An item is a
+// batch of a token's rows in 2048 columns (and for the gradients the token's own row); the ninth warp has bulk copies of
+// the next items under way, so that reading positions, rows and adding up overlap.  A thread whose wait for an item runs
+// out takes it, and all after it, straight from global memory: the results are the same.
+constexpr uint32_t kAdders = 256, kTile = 8 * kAdders, kItems = 3;
+constexpr uint32_t kWaitLimit = 1u << 18;      // looks at an mbarrier; one that fails takes 4 us: a second
+constexpr uint32_t kRingSmem = 108 * 1024;     // of a CTA's items, at most
+
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {      // false: the wait ran out
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ void bulk(uint32_t dst, const char* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void adders_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kAdders) : "memory"); }
+
+// What an item holds: J rows' pieces, then the token's own; and beside it the rows' places and weights.
+template <uint32_t RDT, uint32_t GDT, bool BACK>
+struct Item {
+    static constexpr uint32_t J = RDT == DTT_BF16 ? 8 : 4;
+    static constexpr uint32_t piece = kTile * (RDT == DTT_BF16 ? 2 : 4), own = BACK ? kTile * (GDT == DTT_BF16 ? 2 : 4) : 0;
+    static constexpr uint32_t bytes = J * piece + own, count = kRingSmem / bytes < kItems ? kRingSmem / bytes : kItems;
+};
+struct Known {
+    uint32_t row[8];            // ~0: none
+    float weight[8];
+};
+
+struct RingParams {
+    Sorted s;
+    const char* rows;
+    const char* own;            // backward: dout
+    const float* weights;       // or null: 1
+    char* out;                  // forward
+    Rows drows;                 // backward
+    float* dweights;            // backward, or null: rows are not read
+    uint64_t rows_pitch, own_pitch, out_pitch;
+    uint32_t cols;
+};
+
+template <uint32_t RDT, uint32_t GDT, bool BACK>
+struct Ring {
+    using I = Item<RDT, GDT, BACK>;
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == I::count) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// The pairs j0 .. j0 + J - 1 of a token as lane j of a warp has them.
+template <uint32_t J>
+__device__ __forceinline__ uint32_t lane_row(const RingParams& p, uint64_t token, uint32_t j0) {
+    const uint32_t lane = threadIdx.x % 32;
+    const uint32_t r = lane < J && j0 + lane < p.s.k ? row_of(p.s, token * p.s.k + j0 + lane) : ~0u;
+    return r < p.s.max_rows ? r : ~0u;
+}
+
+// The ninth warp.  Items in the adders' order: forward a token's columns, and its batches within them; backward its
+// batches, and the columns within.
+template <uint32_t RDT, uint32_t GDT, bool BACK>
+__device__ __forceinline__ void fetch(const RingParams& p, uint32_t items, uint32_t full, uint32_t empty, Known* known) {
+    using I = Item<RDT, GDT, BACK>;
+    constexpr uint32_t re = RDT == DTT_BF16 ? 2 : 4, ge = GDT == DTT_BF16 ? 2 : 4;
+    const uint32_t lane = threadIdx.x % 32, tiles = (p.cols + kTile - 1) / kTile, batches = (p.s.k + I::J - 1) / I::J;
+    const bool reads = !BACK || p.dweights;
+    Ring<RDT, GDT, BACK> ring;
+    uint32_t sent = 0;
+    bool late = false;
+    uint64_t token = blockIdx.x;
+    uint32_t ahead = token < p.s.tokens ? lane_row<I::J>(p, token, 0) : ~0u;      // of the next token's first batch
+    for (; token < p.s.tokens && !late; token += gridDim.x) {
+        const uint32_t first = ahead;
+        if (token + gridDim.x < p.s.tokens) ahead = lane_row<I::J>(p, token + gridDim.x, 0);
+        for (uint32_t n = 0; n < tiles * batches && !late; ++n) {
+            const uint32_t tile = BACK ? n % tiles : n / batches, batch = BACK ? n / tiles : n % batches, j0 = batch * I::J;
+            const uint32_t r = batch == 0 ? first : lane_row<I::J>(p, token, j0);
+            const bool has = r != ~0u;
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, has);
+            const float w = has && p.weights ? p.weights[token * p.s.k + j0 + lane] : 1.0f;
+            const uint32_t c = tile * kTile, columns = min(kTile, p.cols - c);
+            const uint32_t bar = full + 8 * ring.at, to = items + ring.at * I::bytes;
+            // the item's place is free once the adders are done with it and the copies into it have landed, which adders that
+            // have given up do not tell; all lanes give up if one does
+            late = __any_sync(0xFFFFFFFFu, !arrived(empty + 8 * ring.at, ring.phase ^ 1) || !arrived(bar, ring.phase ^ 1));
+            if (late) break;
+            if (lane < I::J) {
+                known[ring.at].row[lane] = r;
+                known[ring.at].weight[lane] = w;
+            }
+            __syncwarp();
+            if (lane == 0) bar_expect_tx(bar, (reads ? __popc(mask) * columns * re : 0) + (BACK && mask ? columns * ge : 0));
+            __syncwarp();
+            if (reads && has) bulk(to + lane * I::piece, p.rows + r * p.rows_pitch + (uint64_t)c * re, columns * re, bar);
+            if (BACK && mask && lane == 0) bulk(to + I::J * I::piece, p.own + token * p.own_pitch + (uint64_t)c * ge, columns * ge, bar);
+            ring.next();
+            ++sent;
+        }
+    }
+    // no copy is under way when the CTA leaves
+    for (uint32_t n = sent > I::count ? sent - I::count : 0; n < sent; ++n) (void)arrived(full + 8 * (n % I::count), n / I::count & 1);
+}
+
+// Eight columns of a row's piece, or from global memory.
+template <uint32_t DT>
+__device__ __forceinline__ void piece8(bool late, const char* item, const char* global, float (&v)[8]) {
+    if (late) expand8(raw8(global, DT), DT, v);
+    else expand8(raw8(item, DT), DT, v);
+}
+
+template <uint32_t RDT, uint32_t GDT, bool BACK>
+__global__ void __launch_bounds__(kAdders + 32, 2) rows_ring_kernel(const __grid_constant__ RingParams p) {
+    using I = Item<RDT, GDT, BACK>;
+    launch_next();
+    extern __shared__ __align__(128) uint8_t items[];
+    __shared__ uint64_t full[I::count], empty[I::count];
+    __shared__ Known known[I::count];
+    __shared__ float sums[2][kAdders / 32][I::J];
+    constexpr uint32_t re = RDT == DTT_BF16 ? 2 : 4, ge = GDT == DTT_BF16 ? 2 : 4;
+    const uint32_t t = threadIdx.x;
+    if (t == 0) {
+        for (uint32_t i = 0; i < I::count; ++i) {
+            bar_init(saddr(full + i), 1);
+            bar_init(saddr(empty + i), kAdders / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    wait_previous();
+    if (t >= kAdders) return fetch<RDT, GDT, BACK>(p, saddr(items), saddr(full), saddr(empty), known);
+
+    const uint32_t tiles = (p.cols + kTile - 1) / kTile, batches = (p.s.k + I::J - 1) / I::J, lane = t % 32;
+    Ring<RDT, GDT, BACK> ring;
+    bool late = false;
+    // item by item; what it knows of the rows, too
+    const auto wait = [&] { late = late || DTT_EXPERTS_LATE || !arrived(saddr(full + ring.at), ring.phase); };
+    const auto row_at = [&](uint64_t token, uint32_t j0, uint32_t j) {
+        if (!late) return known[ring.at].row[j];
+        const uint32_t r = j0 + j < p.s.k ? row_of(p.s, token * p.s.k + j0 + j) : ~0u;
+        return r < p.s.max_rows ? r : ~0u;
+    };
+    const auto weight_at = [&](uint64_t token, uint32_t j0, uint32_t j) {
+        return !late ? known[ring.at].weight[j] : p.weights ? p.weights[token * p.s.k + j0 + j] : 1.0f;
+    };
+    const auto done = [&] {
+        __syncwarp();
+        if (lane == 0) arrive(saddr(empty + ring.at));
+        ring.next();
+    };
+    if constexpr (BACK)
+        for (uint32_t f = blockIdx.x; f < p.s.fill_ctas; f += gridDim.x) fill_rows<uint4>(p.s, p.drows, f, t, kAdders);
+    uint32_t turn = 0;
+    for (uint64_t token = blockIdx.x; token < p.s.tokens; token += gridDim.x) {
+        if constexpr (!BACK) {
+            for (uint32_t tile = 0; tile < tiles; ++tile) {
+                const uint32_t c = tile * kTile + 8 * t;
+                float sum[8] = {};
+                for (uint32_t j0 = 0; j0 < p.s.k; j0 += I::J) {
+                    wait();
+                    const char* item = reinterpret_cast<const char*>(items) + ring.at * I::bytes;
+#pragma unroll
+                    for (uint32_t j = 0; j < I::J; ++j) {
+                        const uint32_t r = row_at(token, j0, j);
+                        if (r == ~0u || c >= p.cols) continue;
+                        const float w = weight_at(token, j0, j);
+                        float v[8];
+                        piece8<RDT>(late, item + j * I::piece + 8 * t * re, p.rows + r * p.rows_pitch + (uint64_t)c * re, v);
+#pragma unroll
+                        for (uint32_t i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+                    }
+                    done();
+                }
+                if (c < p.cols) store8<true>(p.out + token * p.out_pitch, GDT, c, p.cols, sum);
+            }
+        } else {
+            for (uint32_t j0 = 0; j0 < p.s.k; j0 += I::J, turn ^= 1) {
+                float dot[I::J] = {};
+                for (uint32_t tile = 0; tile < tiles; ++tile) {
+                    const uint32_t c = tile * kTile + 8 * t;
+                    wait();
+                    const char* item = reinterpret_cast<const char*>(items) + ring.at * I::bytes;
+                    float g[8];
+                    bool have = false;
+#pragma unroll
+                    for (uint32_t j = 0; j < I::J; ++j) {
+                        const uint32_t r = row_at(token, j0, j);
+                        if (r == ~0u || c >= p.cols) continue;
+                        if (!have) piece8<GDT>(late, item + I::J * I::piece + 8 * t * ge, p.own + token * p.own_pitch + (uint64_t)c * ge, g);
+                        have = true;
+                        const float w = weight_at(token, j0, j);
+                        float v[8];
+                        if (p.dweights) {
+                            piece8<RDT>(late, item + j * I::piece + 8 * t * re, p.rows + r * p.rows_pitch + (uint64_t)c * re, v);
+#pragma unroll
+                            for (uint32_t i = 0; i < 8; ++i) dot[j] = fmaf(g[i], v[i], dot[j]);
+                        }
+#pragma unroll
+                        for (uint32_t i = 0; i < 8; ++i) v[i] = g[i] * w;
+                        store8<true>(p.drows.at + r * p.drows.pitch, RDT, c, p.cols, v);
+                    }
+                    done();
+                }
+                if (!p.dweights) continue;
+                const float mine = sum_of_mine(dot);
+                if (lane < I::J) sums[turn][t / 32][lane] = mine;
+                adders_sync();
+                if (t < I::J && j0 + t < p.s.k) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (uint32_t i = 0; i < kAdders / 32; ++i) sum += sums[turn][i][t];
+                    p.dweights[token * p.s.k + j0 + t] = sum;
+                }
+            }
+        }
+    }
+}
+
 // ---- host --------------------------------------------------------------------------------------
 int check_desc(const char* who, const dtt_experts_desc* d) {
     if (!d) return fail(DTT_EINVAL, "%s: null desc", who);
@@ -506,6 +751,25 @@ BackwardKernel backward_of(uint32_t rows, uint32_t dout) {
 }
 BackwardKernel backward_of(bool vec, uint32_t rows, uint32_t dout) { return vec ? backward_of<true, uint4>(rows, dout) : backward_of<false, uint16_t>(rows, dout); }
 
+// The rows through shared memory: for the grid and what it takes.
+struct RingLaunch {
+    void (*kernel)(RingParams);
+    uint32_t smem;
+};
+template <bool BACK, uint32_t RDT, uint32_t GDT>
+RingLaunch ring_of() { return {rows_ring_kernel<RDT, GDT, BACK>, Item<RDT, GDT, BACK>::bytes * Item<RDT, GDT, BACK>::count}; }
+template <bool BACK>
+RingLaunch ring_of(uint32_t rows, uint32_t other) {
+    if (rows == DTT_BF16) return other == DTT_BF16 ? ring_of<BACK, DTT_BF16, DTT_BF16>() : ring_of<BACK, DTT_BF16, DTT_F32>();
+    return other == DTT_BF16 ? ring_of<BACK, DTT_F32, DTT_BF16>() : ring_of<BACK, DTT_F32, DTT_F32>();
+}
+bool through_ring(bool vec, uint64_t tokens, uint64_t cols) { return vec && cols >= RING_COLS && tokens >= RING_TOKENS * kSms; }
+cudaError_t launch_ring(const RingLaunch& r, const RingParams& p, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) sms = 1;
+    return launch(r.kernel, (uint32_t)std::min<uint64_t>(p.s.tokens, 2 * (uint64_t)sms), kAdders + 32, r.smem, 0, true, stream, p);
+}
+
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : 4; }
 bool aligned(const void* p, uint64_t pitch) { return bits_of(p) % 16 == 0 && pitch % 16 == 0; }
 
@@ -520,6 +784,9 @@ cudaError_t preload_experts_kernels() {
     for (uint32_t i = 0; i < 8; ++i) {
         const uint32_t a = i & 1 ? DTT_F32 : DTT_BF16, b = i & 2 ? DTT_F32 : DTT_BF16;
         add(combine_of(i & 4, a, b), backward_of(i & 4, a, b));
+        const RingLaunch r = i & 4 ? ring_of<true>(a, b) : ring_of<false>(a, b);
+        add(r.kernel);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(r.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.smem);
     }
     constexpr int most = (kRouteWarps + 2) * kMostExperts * 4;
     for (auto k : {route_count_kernel, route_place_kernel})
@@ -633,7 +900,15 @@ extern "C" int dtt_experts_combine(const dtt_experts_desc* d, uint64_t tokens, u
     p.cols = (uint32_t)cols;
     const bool vec = cols % 8 == 0 && aligned(rows, rows_pitch) && aligned(out, out_pitch);
     const dim3 block = token_block(cols);
-    const cudaError_t e = launch(combine_of(vec, rows_dtype, out_dtype), (uint32_t)ctas_of(tokens, block), block, 0, 0, true, stream, p);
+    RingParams q{};
+    q.s = p.s;
+    q.rows = p.rows;
+    q.weights = weights;
+    q.out = p.out;
+    q.rows_pitch = rows_pitch;
+    q.out_pitch = out_pitch;
+    q.cols = p.cols;
+    const cudaError_t e = through_ring(vec, tokens, cols) ? launch_ring(ring_of<false>(rows_dtype, out_dtype), q, stream) : launch(combine_of(vec, rows_dtype, out_dtype), (uint32_t)ctas_of(tokens, block), block, 0, 0, true, stream, p);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }
@@ -671,7 +946,17 @@ extern "C" int dtt_experts_combine_backward(const dtt_experts_desc* d, uint64_t 
     p.rows_pitch = rows_pitch;
     p.cols = (uint32_t)cols;
     const bool vec = cols % 8 == 0 && aligned(dout, dout_pitch) && aligned(drows, drows_pitch) && (!dweights || aligned(rows, rows_pitch));
-    const cudaError_t e = launch(backward_of(vec, rows_dtype, dout_dtype), (uint32_t)grid, block, 0, 0, true, stream, p);
+    RingParams q{};
+    q.s = p.s;
+    q.rows = p.rows;
+    q.own = p.dout;
+    q.weights = weights;
+    q.drows = p.drows;
+    q.dweights = dweights;
+    q.rows_pitch = rows_pitch;
+    q.own_pitch = dout_pitch;
+    q.cols = p.cols;
+    const cudaError_t e = through_ring(vec, tokens, cols) ? launch_ring(ring_of<true>(rows_dtype, dout_dtype), q, stream) : launch(backward_of(vec, rows_dtype, dout_dtype), (uint32_t)grid, block, 0, 0, true, stream, p);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }

@@ -101,6 +101,12 @@ ROWS = [(1, 1, 1, 1, 1, 0, 1, 0, 0), (1, 4096, 8, 128, 16, 0, 1, 0, 0), (37, 409
         (33, 999, 3, 9, 4, 2, 5, 1, 3), (300, 8064, 4, 64, 16, 16, 128, 0, 0), (129, 64, 6, 12, 12, 0, 128, 0, 0), (50, 20000, 2, 4, 2, 1, 1, 0, 0), (9, 30, 32, 40, 40, 0, 7, 2, 2)]
 
 
+# many tokens of long rows come through shared memory: parts of a tile, whole ones, more choices than a batch has
+RING = [(610, 1024, 2, 8, 8, 0, 1, 0, 0), (700, 1032, 9, 16, 16, 0, 8, 8, 8), (650, 8064, 4, 64, 16, 16, 16, 0, 0), (613, 4096, 8, 32, 32, 0, 128, 0, 0),
+        (609, 2056, 32, 40, 30, 5, 4, 0, 16), (1301, 2048, 1, 4, 1, 2, 1, 0, 0)]
+ROWS += RING
+
+
 def batch(tokens, cols, k, of, experts, first, align, pad_x, pad_r, dtype, spare=3):
     """A sorted batch, x, and a buffer of sevens with some rows more than are needed."""
     op = D.ExpertRows(experts, k, first=first, align=align)
@@ -330,6 +336,30 @@ def test_calls_that_read_what_the_call_before_wrote_need_no_wait_between_them():
     ids.clamp_(min=0)
     for a, b in zip(chain(True), chain(False)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("late", ["true", "t == 37", "t % 7 == 3 && ring.at == 1"])
+def test_a_wait_that_is_given_up_changes_nothing(late, tmp_path):
+    """Threads that give an item up, all of them or some, take it and the later ones from global memory: the same bits."""
+    from test_gpu_ops_edges import library_with
+    L = library_with("experts.cu", [f"-DDTT_EXPERTS_LATE=({late})"], str(tmp_path))
+    for shape in RING:
+        tokens, cols, k = shape[:3]
+        for dtype, other_dtype in ((BF16, BF16), (F32, BF16)):
+            op, plan, _, buffer = batch(*shape, dtype)
+            rows = torch.randn(buffer.shape[0], cols, generator=gen(1), device="cuda").to(dtype)
+            dout = torch.randn(tokens, cols, generator=gen(2), device="cuda").to(other_dtype)
+            weights = torch.rand(tokens, k, generator=gen(3), device="cuda")
+            got = []
+            for other in (False, True):
+                if other:
+                    op._combine, op._combine_backward = L.dtt_experts_combine, L.dtt_experts_combine_backward
+                out, drows, dweights = torch.zeros_like(dout), torch.full_like(rows, 7.0), torch.zeros_like(weights)
+                op.combine(rows, plan[0], out, weights=weights)
+                op.combine_backward(dout, rows, plan[0], weights, *plan[1:], drows, dweights)
+                got.append((out, drows, dweights))
+            for a, b in zip(*got):
+                assert torch.equal(a, b)
 
 
 def test_rows_past_four_gigabytes():
