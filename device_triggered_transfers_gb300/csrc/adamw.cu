@@ -115,9 +115,9 @@ __device__ __forceinline__ Rates rates_of(const Scalars& s) {
 }
 
 // m and v, as the old ones or as codes with what their scales make of them: m_by and v_by are beta1 and beta2, or the
-// scales times beta1 and sqrt(beta2).  root: sqrt(v).
+// scales times beta1 and sqrt(beta2).  root: sqrt(v).  decay: lr times the tensor's.
 template <bool S8>
-__device__ __forceinline__ void update(Pair& p, Pair g, Pair& m, Pair& v, float2& root, float m_by, float v_by, float keep, const Rates& r, float eps) {
+__device__ __forceinline__ void update(Pair& p, Pair g, Pair& m, Pair& v, float2& root, float m_by, float v_by, float decay, const Rates& r, float eps) {
     m = fma2(m, both(m_by), g * both(r.g_m));
     const Pair gv = g * both(r.g_v);
     if (S8) {
@@ -129,7 +129,8 @@ __device__ __forceinline__ void update(Pair& p, Pair g, Pair& m, Pair& v, float2
     const float2 a = apart(v);
     root = make_float2(root_of(a.x), root_of(a.y));
     const float2 d = apart(fma2(pair(root.x, root.y), both(r.root_c2), both(eps)));
-    p = fma2(m * pair(reciprocal(d.x), reciprocal(d.y)), both(-r.lr_by_c1), p * both(keep));
+    // p - decay p, not p (1 - decay): 1 - 1e-6 in f32 is off by up to 6 % of the 1e-6, of every weight the same way
+    p = fma2(m * pair(reciprocal(d.x), reciprocal(d.y)), both(-r.lr_by_c1), fma2(p, both(-decay), p));
 }
 
 // ---- codes ---------------------------------------------------------------------------------------
@@ -262,7 +263,7 @@ __device__ __forceinline__ void cut_weights(const float (&p)[8], const uint32_t 
 // Elements i, one by one, of a tensor of which nothing is aligned: a warp's 256 neighbours, a lane every 32nd, so
 // that accesses are contiguous over the warp and a block of 128 is four of each lane's.
 template <uint32_t P, uint32_t G, bool S8, bool SR>
-__device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, uint32_t seed, float keep, const Rates& r, const Scalars& s) {
+__device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, uint32_t seed, float decay, const Rates& r, const Scalars& s) {
     const uint64_t i0 = at + threadIdx.x / 32 * 256 + threadIdx.x % 32;
     float p[8], g[8], m[8], v[8], ms[2], vs[2];
     float2 root[4];
@@ -278,7 +279,7 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
 #pragma unroll
     for (uint32_t k = 0; k < 8; k += 2) {
         Pair pp = pair(p[k], p[k + 1]), mm = pair(m[k], m[k + 1]), vv = pair(v[k], v[k + 1]);
-        update<S8>(pp, pair(g[k], g[k + 1]), mm, vv, root[k / 2], S8 ? ms[k / 4] * s.beta1 : s.beta1, S8 ? vs[k / 4] * s.root_beta2 : s.beta2, keep, r, s.eps);
+        update<S8>(pp, pair(g[k], g[k + 1]), mm, vv, root[k / 2], S8 ? ms[k / 4] * s.beta1 : s.beta1, S8 ? vs[k / 4] * s.root_beta2 : s.beta2, decay, r, s.eps);
         const float2 a = apart(pp), b = apart(mm), c = apart(vv);
         p[k] = a.x, p[k + 1] = a.y, m[k] = b.x, m[k + 1] = b.y, v[k] = c.x, v[k + 1] = c.y;
     }
@@ -412,7 +413,7 @@ __device__ __forceinline__ void shared_group(uint32_t at, float (&v)[8]) {
 // the element `lead` places before the tensor's first, so that every eighth from there is aligned; the groups at its
 // ends that it does not fill go element by element.
 template <uint32_t P, uint32_t G, bool S8, bool SR>
-__device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage, float ms, float vs, uint32_t seed, float keep, const Rates& r, const Scalars& s) {
+__device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage, float ms, float vs, uint32_t seed, float decay, const Rates& r, const Scalars& s) {
     float p[8], g[8], m[8], v[8];
     float2 root[4];
     const bool whole = o >= a.head && o + 8 <= a.end;
@@ -443,7 +444,7 @@ __device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage,
 #pragma unroll
     for (uint32_t k = 0; k < 8; k += 2) {
         Pair pp = pair(p[k], p[k + 1]), mm = pair(m[k], m[k + 1]), vv = pair(v[k], v[k + 1]);
-        update<S8>(pp, pair(g[k], g[k + 1]), mm, vv, root[k / 2], m_by, v_by, keep, r, s.eps);
+        update<S8>(pp, pair(g[k], g[k + 1]), mm, vv, root[k / 2], m_by, v_by, decay, r, s.eps);
         const float2 a = apart(pp), b = apart(mm), c = apart(vv);
         p[k] = a.x, p[k + 1] = a.y, m[k] = b.x, m[k + 1] = b.y, v[k] = c.x, v[k + 1] = c.y;
     }
@@ -506,13 +507,13 @@ __device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage,
 
 // The chunks one after the other, once a thread's own copies for each have landed.
 template <uint32_t TURN, uint32_t P, uint32_t G, bool SR>
-__device__ __forceinline__ void take_turns(const Part& a, uint32_t stage, const float (&ms)[kTurns], const float (&vs)[kTurns], uint32_t seed, float keep,
+__device__ __forceinline__ void take_turns(const Part& a, uint32_t stage, const float (&ms)[kTurns], const float (&vs)[kTurns], uint32_t seed, float decay,
                                            const Rates& r, const Scalars& s) {
     if constexpr (TURN < kTurns) {
         if (TURN * kChunk >= a.end) return;
         asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 1 - TURN) : "memory");
-        group<P, G, true, SR>(a, TURN * kChunk + 8 * threadIdx.x, stage + TURN * Stage<P, G>::bytes, ms[TURN], vs[TURN], seed, keep, r, s);
-        take_turns<TURN + 1, P, G, SR>(a, stage, ms, vs, seed, keep, r, s);
+        group<P, G, true, SR>(a, TURN * kChunk + 8 * threadIdx.x, stage + TURN * Stage<P, G>::bytes, ms[TURN], vs[TURN], seed, decay, r, s);
+        take_turns<TURN + 1, P, G, SR>(a, stage, ms, vs, seed, decay, r, s);
     }
 }
 
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     const Tensor& t = b.t[lo];
     wait_previous();
     const Rates r = rates_of(b.s);
-    const float keep = 1.0f - r.lr * t.decay;
+    const float decay = r.lr * t.decay;
     uint32_t seed = 0;
     if (SR) seed = mix(mix(b.s.seed + r.step) + t.number);
     const uint64_t start = (uint64_t)(blockIdx.x - b.first[lo]) * b.turns * kChunk;
@@ -548,13 +549,13 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
                 }
                 start_copies<P, G>(a, o, stage + turn * Stage<P, G>::bytes);
             }
-            take_turns<0, P, G, SR>(a, stage, ms, vs, seed, keep, r, b.s);
+            take_turns<0, P, G, SR>(a, stage, ms, vs, seed, decay, r, b.s);
         } else {
-            group<P, G, S8, SR>(a, 8 * threadIdx.x, 0, 0.0f, 0.0f, seed, keep, r, b.s);
+            group<P, G, S8, SR>(a, 8 * threadIdx.x, 0, 0.0f, 0.0f, seed, decay, r, b.s);
         }
     } else {
         const uint64_t end = min(start + b.turns * kChunk, t.n);
-        for (uint64_t at = start; at < end; at += kChunk) chunk_by_elements<P, G, S8, SR>(t, at, seed, keep, r, b.s);
+        for (uint64_t at = start; at < end; at += kChunk) chunk_by_elements<P, G, S8, SR>(t, at, seed, decay, r, b.s);
     }
 }
 

@@ -21,8 +21,9 @@ namespace {
 #endif
 constexpr uint32_t kMostExperts = 1024, kMostChoices = 32;
 constexpr uint32_t kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
-constexpr uint32_t kMostParts = 64;            // CTAs of the sort, at most
-constexpr uint32_t kPartPairs = 2048;          // pairs of a CTA, at least, while there are fewer
+// 131072 pairs: 198 us with their rows' dispatch, with half as many parts 201, a quarter 206.
+constexpr uint32_t kMostParts = 128;           // CTAs of the sort, at most
+constexpr uint32_t kPartPairs = 1024;          // pairs of a CTA, at least, while there are fewer
 // A row's threads, at most.  131072 rows of 4096 (bf16) combined: 209 us with 256 (four CTAs an SM), 224 with 512 (two),
 // 211 with 128 (eight); backward 402, 450, 411.
 constexpr uint32_t kCopyThreads = 256, kRowThreads = 256;

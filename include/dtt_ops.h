@@ -256,11 +256,11 @@ int dtt_experts_combine_backward(const dtt_experts_desc* desc, uint64_t tokens, 
  *     g = grad_scale grad
  *     m <- beta1 m + (1 - beta1) g
  *     v <- beta2 v + (1 - beta2) g^2
- *     p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *     p <- p - lr weight_decay p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *     copy = p, rounded to bf16 (where there is one: the all-gather's part of the new weights)
  * States: DTT_F32, m and v as they are; or DTT_E4M3: m and sqrt(v) in codes of 8 bits, with one f32 scale for
  * each DTT_ADAMW_BLOCK elements of a tensor (the last block holds what is left),
- *     scale = max(max |x| / 448, 2^-100) over the block (to an ulp),  code = e4m3(x (1 / scale)),
+ *     scale = max(max |x| / 448, 2^-100) over the block (to an ulp),  code = e4m3(x / scale) (x / scale to a few ulp),
  * but a root above zero has the code 2^-9 at least, since the next step divides by it.  The step itself uses the
  * new m and v before they are rounded.  All states zero, their scales too, is the start.
  * stochastic = 0: codes and bf16 weights are rounded to nearest.  1: up, away from zero, with the probability of

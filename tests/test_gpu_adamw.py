@@ -307,6 +307,17 @@ def test_codes_rounded_at_random_follow_a_slow_average():
         assert abs(ratio - (1.0 if seed is None else 0.999 ** 500)) < (1e-3 if seed is None else 6 * 0.0022)
 
 
+def test_a_small_decay_is_that_of_its_size():
+    """Of 1e-6, where 1 - 1e-6 in f32 is 1.3 % off: weights without gradients shrink by 1e-6 on average, each product and sum
+    rounded by half an ulp (2^-24 of the weight) at random, of which a million's mean keeps a thousandth; six of that is allowed."""
+    n = 1 << 20
+    p = 1 + torch.rand(n, generator=gen(3), device="cuda")
+    before = p.double()
+    zeros = [torch.zeros(n, device="cuda") for _ in range(3)]
+    D.AdamW([p], zeros[:1], zeros[1:2], zeros[2:], weight_decay=0.1).run(1e-5, 1)
+    assert abs(float(((before - p.double()) / before).mean()) - 1e-6) < 6 * 2 * E / 1024
+
+
 @pytest.mark.parametrize("shift", [0, 1])
 @pytest.mark.parametrize("state,seed", [("f32", None), ("e4m3", None), ("e4m3", 3)])
 def test_nan_and_infinity_stay_in_their_element_or_block(state, seed, shift):
