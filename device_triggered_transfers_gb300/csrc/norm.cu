@@ -1015,9 +1015,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 // about that, both by shuffles; the warps' sums S_w and squares Q_w then meet in shared memory, where
 //     mean = sum S_w / cols,   sum (h - mean)^2 = sum Q_w + sum n_w (S_w / n_w - mean)^2
 // adds what the warps' means are off by (T. F. Chan, G. H. Golub, R. J. LeVeque, 1979): no large numbers cancel.
-// 16384 x 4096 (bf16 to 8 bits, groups of 128): 84 us, 0.83 of the copy rate, with three CTAs of 256 threads an SM; 86 with four, whose
-// registers spill, 97 with two, 95 with 128 threads of four chunks each.  Two reductions with a barrier each, one value
-// an instruction and types looked up at each access: 113.
+// 16384 x 4096 (bf16 to 8 bits, groups of 128): 81 us, 0.86 of the copy rate (84 where the residual's rows stay in L2 as long as
+// others).  With three CTAs of 256 threads an SM; four, whose registers spill, took 3 more, two 13, and 128 threads of four chunks
+// each 12.  Two reductions with a barrier each, one value an instruction and types looked up at each access: 113.
 constexpr uint32_t kLayerThreads = 256;        // of a row with two chunks a thread, at most
 template <uint32_t NCH, bool B16>
 __global__ void __launch_bounds__(NCH == 1 ? 128 : NCH == 2 ? kLayerThreads : kRingThreads, NCH == 1 ? 8 : NCH == 2 ? 3 : 1) layernorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
@@ -1112,7 +1112,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 128 : NCH == 2 ? kLayerThreads : kR
             if (p.res_out) {
                 float f[8];
                 singles8(h[i], f);
-                store8<true>(p.res_out + r * p.res_out_pitch, B16 ? (uint32_t)DTT_BF16 : p.res_dt, c[i], p.cols, f);
+                store8_first_out(p.res_out + r * p.res_out_pitch, B16 ? (uint32_t)DTT_BF16 : p.res_dt, c[i], f);
             }
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) sum = sum + h[i][k];
