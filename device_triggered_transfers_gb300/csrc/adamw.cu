@@ -48,7 +48,7 @@ constexpr uint32_t kElements = 8;
 
 struct Scalars {
     float beta1, beta2, root_beta2;     // root_beta2: its square root, as the next's
-    float one_less_beta1, root_one_less_beta2;
+    float one_less_beta1, one_less_beta2, root_one_less_beta2;
     float eps;
     float lr, lr_by_c1, root_c2;        // by the host's step: lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
     float log_beta1, log_beta2;         // for the device's step
@@ -245,6 +245,61 @@ __device__ __forceinline__ void store_element(const T& t, uint64_t i, float p, u
     if (P == DTT_F32 && t.copy) reinterpret_cast<uint16_t*>(t.copy)[i] = (uint16_t)pack_bf16(p, 0.0f);
 }
 
+// Where an element's noise is 0 the largest of a block, which is 448 or an ulp below it once its scale is taken off, has
+// 448's code or the one below, 7 % less; with any other noise it has 448's.  Which of them is not to depend on how products and
+// sums are put together here, so that it is worked out once more by the formula, each product and sum rounded by itself.
+// code and scale: the old m's or root's; g: the gradient.
+__device__ __forceinline__ uint32_t largest_code(float x) {
+    const float by = __fmul_rn(x, 1.0f / kCodeMax), inv = __frcp_rn(by > kScaleLeast ? by : kScaleLeast);
+    return __fmul_rn(x, inv) < kCodeMax ? 0x7Du : 0x7Eu;
+}
+__device__ __forceinline__ uint32_t largest_m(float code, float scale, float g, const Scalars& s) {
+    if (s.grad_scale) g = __fmul_rn(g, *s.grad_scale);
+    const float m = __fadd_rn(__fmul_rn(s.beta1, __fmul_rn(code, scale)), __fmul_rn(s.one_less_beta1, g));
+    return largest_code(fabsf(m)) | (__float_as_uint(m) >> 24 & 0x80u);
+}
+__device__ __forceinline__ uint32_t largest_root(float code, float scale, float g, const Scalars& s) {
+    if (s.grad_scale) g = __fmul_rn(g, *s.grad_scale);
+    const float root = __fmul_rn(code, scale);
+    return largest_code(__fsqrt_rn(__fadd_rn(__fmul_rn(s.beta2, __fmul_rn(root, root)), __fmul_rn(__fmul_rn(s.one_less_beta2, g), g))));
+}
+// Whether an element's noise may be 0, of m or of the root: a half of the difference borrows where the half is 0, or where
+// the lower one borrowed.
+template <uint32_t N>
+__device__ __forceinline__ bool any_noise_0(const uint32_t* bits) {
+    uint32_t t = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < N; ++k) t |= (bits[k] - 0x00010001u) & ~bits[k];
+    return t & 0x80008000u;
+}
+// Elements i + k step of one block, k < count, of which one's noise is 0, if they are the block's largest.  Codes are in m
+// and v already; as they were they are bytes of old_m and old_v, in the block with scales ms and vs.  first: the number
+// of element 0.  A scale that is the least one does not make a code of 448.
+struct Tops {
+    float ms, vs, m, root;
+};
+__device__ __forceinline__ float code_value(uint2 codes, uint32_t k) {
+    float v, none;
+    unpack_e4m3((k < 4 ? codes.x : codes.y) >> 8 * (k % 4) & 0xFFu, v, none);
+    return v;
+}
+template <uint32_t G>
+__device__ __forceinline__ void settle_largest(const char* gs, char* m, char* v, uint64_t i, uint64_t first, uint32_t step, uint32_t count, uint2 old_m, uint2 old_v,
+                                               Tops t, uint32_t seed, const Rates& r, const Scalars& s) {
+    const auto scaled = [](float top) { return top * (1.0f / kCodeMax) > kScaleLeast && top < INFINITY; };
+#pragma unroll 1
+    for (uint32_t k = 0; k < count; ++k, i += step) {
+        const uint32_t bits = random_bits(first + i, seed);
+        if (bits >= 1u << 16 && (bits & 0xFFFFu)) continue;
+        const float g = element<G>(gs, i), cm = code_value(old_m, k), cv = code_value(old_v, k);
+        const float gv = __fmul_rn(g, r.g_v), root = __fmul_rn(cv, __fmul_rn(t.vs, s.root_beta2));         // as update() has them
+        if (bits < 1u << 16 && scaled(t.m) && fabsf(fmaf(cm, __fmul_rn(t.ms, s.beta1), __fmul_rn(g, r.g_m))) == t.m)
+            reinterpret_cast<uint8_t*>(m)[i] = (uint8_t)largest_m(cm, t.ms, g, s);
+        if (!(bits & 0xFFFFu) && scaled(t.root) && root_of(fmaf(root, root, __fmul_rn(gv, gv))) == t.root)
+            reinterpret_cast<uint8_t*>(v)[i] = (uint8_t)largest_root(cv, t.vs, g, s);
+    }
+}
+
 // bf16 of eight weights rounded at random; NaN, which the sum would turn into something else, is left as it is.
 __device__ __forceinline__ void cut_weights(const float (&p)[8], const uint32_t (&r)[8], uint32_t (&cut)[8]) {
     Pair none = both(0.0f);                     // NaN where one of them is infinite or NaN
@@ -267,10 +322,16 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
     const uint64_t i0 = at + threadIdx.x / 32 * 256 + threadIdx.x % 32;
     float p[8], g[8], m[8], v[8], ms[2], vs[2];
     float2 root[4];
+    uint32_t old_m[2] = {}, old_v[2] = {};
+    Tops tops[2];
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
         const uint64_t i = min(i0 + 32 * k, t.n - 1);
         load_element<P, G, S8>(t, i, p[k], g[k], m[k], v[k]);
+        if (S8 && SR) {
+            old_m[k / 4] |= (uint32_t) reinterpret_cast<const uint8_t*>(t.m)[i] << 8 * (k % 4);
+            old_v[k / 4] |= (uint32_t) reinterpret_cast<const uint8_t*>(t.v)[i] << 8 * (k % 4);
+        }
         if (S8 && k % 4 == 0) {
             ms[k / 4] = t.ms[i / kBlock];
             vs[k / 4] = t.vs[i / kBlock];
@@ -306,16 +367,25 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
                 t.ms[i / kBlock] = sm.scale;
                 t.vs[i / kBlock] = sr.scale;
             }
-            const Pair ms[2] = {pair(m[b], m[b + 1]), pair(m[b + 2], m[b + 3])};
+            const Pair of_m[2] = {pair(m[b], m[b + 1]), pair(m[b + 2], m[b + 3])};
             const float2 roots[2] = {root[b / 2], root[b / 2 + 1]};
-            code_m[b / 4] = moment_codes<SR>(ms, sm.inv, bits + b, s.sixteen) | poison(tm);
+            code_m[b / 4] = moment_codes<SR>(of_m, sm.inv, bits + b, s.sixteen) | poison(tm);
             code_v[b / 4] = root_codes<SR>(roots, sr.inv, bits + b, s.sixteen) | poison(tr);
+            tops[b / 4] = {ms[b / 4], vs[b / 4], tm, tr};
         }
     }
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
         const uint64_t i = i0 + 32 * k;
         if (i < t.n) store_element<P, S8, SR>(t, i, p[k], cut[k], m[k], v[k], code_m[k / 4] >> 8 * (k % 4), code_v[k / 4] >> 8 * (k % 4));
+    }
+    if (S8 && SR) {
+#pragma unroll
+        for (uint32_t b = 0; b < 8; b += 4) {
+            const uint64_t i = i0 + 32 * b;
+            if (i < t.n && any_noise_0<4>(bits + b))
+                settle_largest<G>(t.g, t.m, t.v, i, 0, 32, (uint32_t)min((t.n - i + 31) / 32, (uint64_t)4), make_uint2(old_m[b / 4], 0), make_uint2(old_v[b / 4], 0), tops[b / 4], seed, r, s);
+        }
     }
 }
 
@@ -374,6 +444,9 @@ __device__ __forceinline__ void start_copies(const Part& a, uint32_t o, uint32_t
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void copy1(uint32_t to, const char* from) {
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(to), "r"((uint32_t)*reinterpret_cast<const uint8_t*>(from)) : "memory");
+}
 __device__ __forceinline__ uint4 shared16(uint32_t at) {
     uint4 q;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
@@ -413,7 +486,7 @@ __device__ __forceinline__ void shared_group(uint32_t at, float (&v)[8]) {
 // the element `lead` places before the tensor's first, so that every eighth from there is aligned; the groups at its
 // ends that it does not fill go element by element.
 template <uint32_t P, uint32_t G, bool S8, bool SR>
-__device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage, float ms, float vs, uint32_t seed, float decay, const Rates& r, const Scalars& s) {
+__device__ __forceinline__ bool group(const Part& a, uint32_t o, uint32_t stage, float ms, float vs, uint32_t seed, float decay, const Rates& r, const Scalars& s) {
     float p[8], g[8], m[8], v[8];
     float2 root[4];
     const bool whole = o >= a.head && o + 8 <= a.end;
@@ -438,6 +511,10 @@ __device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage,
         for (uint32_t k = 0; k < 8; ++k) {
             p[k] = g[k] = m[k] = v[k] = 0.0f;
             if (mine(k)) load_element<P, G, S8>(a, o + k, p[k], g[k], m[k], v[k]);
+            if (S8 && SR && mine(k)) {
+                copy1(stage + Stage<P, G>::m + 8 * threadIdx.x + k, a.m + o + k);
+                copy1(stage + Stage<P, G>::v + 8 * threadIdx.x + k, a.v + o + k);
+            }
         }
     }
     const float m_by = S8 ? ms * s.beta1 : s.beta1, v_by = S8 ? vs * s.root_beta2 : s.beta2;
@@ -459,6 +536,7 @@ __device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage,
         }
         if (P == DTT_BF16) cut_weights(p, bits, cut);
     }
+    bool settle = false;
     uint2 cm{}, cv{};
     if (S8) {
         // elements that are not the tensor's have m and root 0
@@ -483,6 +561,9 @@ __device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage,
         const float2 r0[2] = {root[0], root[1]}, r1[2] = {root[2], root[3]};
         cm = make_uint2(moment_codes<SR>(m0, sm.inv, bits, s.sixteen) | poison(tm), moment_codes<SR>(m1, sm.inv, bits + 4, s.sixteen) | poison(tm));
         cv = make_uint2(root_codes<SR>(r0, sr.inv, bits, s.sixteen) | poison(tr), root_codes<SR>(r1, sr.inv, bits + 4, s.sixteen) | poison(tr));
+        settle = SR && any_noise_0<8>(bits) && o < a.end;
+        if (settle)                             // in the place of g, which has been taken from there
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + 16 * threadIdx.x), "f"(ms), "f"(vs), "f"(tm), "f"(tr) : "memory");
     }
     if (whole) {
         if (S8) {
@@ -497,24 +578,27 @@ __device__ __forceinline__ void group(const Part& a, uint32_t o, uint32_t stage,
         else
             put_group<P>(a.p, o, p);
         if (P == DTT_F32 && a.copy) put_group<DTT_BF16>(a.copy, o, p);
-        return;
+        return settle;
     }
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)
         if (mine(k))
             store_element<P, S8, SR>(a, o + k, p[k], cut[k], m[k], v[k], (k < 4 ? cm.x : cm.y) >> 8 * (k % 4), (k < 4 ? cv.x : cv.y) >> 8 * (k % 4));
+    return settle;
 }
 
-// The chunks one after the other, once a thread's own copies for each have landed.
+// The chunks one after the other, once a thread's own copies for each have landed.  Bit i of what comes back: chunk i is
+// left to settle.
 template <uint32_t TURN, uint32_t P, uint32_t G, bool SR>
-__device__ __forceinline__ void take_turns(const Part& a, uint32_t stage, const float (&ms)[kTurns], const float (&vs)[kTurns], uint32_t seed, float decay,
+__device__ __forceinline__ uint32_t take_turns(const Part& a, uint32_t stage, const float (&ms)[kTurns], const float (&vs)[kTurns], uint32_t seed, float decay,
                                            const Rates& r, const Scalars& s) {
     if constexpr (TURN < kTurns) {
-        if (TURN * kChunk >= a.end) return;
+        if (TURN * kChunk >= a.end) return 0;
         asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 1 - TURN) : "memory");
-        group<P, G, true, SR>(a, TURN * kChunk + 8 * threadIdx.x, stage + TURN * Stage<P, G>::bytes, ms[TURN], vs[TURN], seed, decay, r, s);
-        take_turns<TURN + 1, P, G, SR>(a, stage, ms, vs, seed, decay, r, s);
+        const bool settle = group<P, G, true, SR>(a, TURN * kChunk + 8 * threadIdx.x, stage + TURN * Stage<P, G>::bytes, ms[TURN], vs[TURN], seed, decay, r, s);
+        return take_turns<TURN + 1, P, G, SR>(a, stage, ms, vs, seed, decay, r, s) | (settle ? 1u << TURN : 0u);
     }
+    return 0;
 }
 
 template <uint32_t P, uint32_t G, bool S8, bool SR, uint32_t N>
@@ -549,7 +633,20 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
                 }
                 start_copies<P, G>(a, o, stage + turn * Stage<P, G>::bytes);
             }
-            take_turns<0, P, G, SR>(a, stage, ms, vs, seed, decay, r, b.s);
+            const uint32_t settle = take_turns<0, P, G, SR>(a, stage, ms, vs, seed, decay, r, b.s);
+            // Only now, with nothing of the chunks in registers: one thread in 1000 has something to do here.  32M weights
+            // take 65.6 us, settled among the chunks' work 75.0, and 59.7 if nothing asked for a noise of 0.
+            if (SR && settle) {
+#pragma unroll 1
+                for (uint32_t turn = 0; turn < kTurns; ++turn) {
+                    if (!(settle >> turn & 1)) continue;
+                    using S = Stage<P, G>;
+                    const uint32_t o = turn * kChunk + 8 * threadIdx.x, at = stage + turn * S::bytes;
+                    const uint4 t = shared16(at + 16 * threadIdx.x);
+                    const Tops tops{__uint_as_float(t.x), __uint_as_float(t.y), __uint_as_float(t.z), __uint_as_float(t.w)};
+                    settle_largest<G>(a.g, a.m, a.v, o, a.first, 1, min(a.end - o, 8u), shared8(at + S::m + 8 * threadIdx.x), shared8(at + S::v + 8 * threadIdx.x), tops, seed, r, b.s);
+                }
+            }
         } else {
             group<P, G, S8, SR>(a, 8 * threadIdx.x, 0, 0.0f, 0.0f, seed, decay, r, b.s);
         }
@@ -741,6 +838,7 @@ extern "C" int dtt_adamw_run(dtt_adamw* o, const void* const* grads, float lr, u
     s.beta2 = (float)d.beta2;
     s.root_beta2 = (float)std::sqrt(d.beta2);
     s.one_less_beta1 = (float)(1.0 - d.beta1);
+    s.one_less_beta2 = (float)(1.0 - d.beta2);
     s.root_one_less_beta2 = (float)std::sqrt(1.0 - d.beta2);
     s.sixteen = 16;
     s.eps = d.eps;

@@ -307,6 +307,56 @@ def test_codes_rounded_at_random_follow_a_slow_average():
         assert abs(ratio - (1.0 if seed is None else 0.999 ** 500)) < (1e-3 if seed is None else 6 * 0.0022)
 
 
+def alike_blocks(n):
+    """(gradient, code of m, of v, scale of m, of v) that a block's elements share, of n / 128 blocks, f32."""
+    rng, blocks = np.random.default_rng(3), n // OA.BLOCK
+    f = lambda x: x.astype(np.float32)  # noqa: E731
+    codes = np.concatenate([np.arange(8, 16) * 2.0 ** e for e in range(-3, 5)])
+    return (f(1e-3 * rng.standard_normal(blocks)), f(rng.choice(codes, blocks) * rng.choice([-1, 1], blocks)), f(rng.choice(codes, blocks)),
+            f(1e-6 * (1 + rng.random(blocks))), f(1e-5 * (1 + rng.random(blocks))))
+
+
+def largest_code(x):
+    """Of a block's largest x by its scale, rounded down, each operation of f32 by itself."""
+    f = np.float32
+    return np.where(x * (f(1) / (x * f(1 / 448))) < f(448), 0x7D, 0x7E)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_a_blocks_largest_with_a_noise_of_0_has_the_formulas_code(shift):
+    """It is 448 or an ulp below, and 448's code or the one below, by the formula's roundings alone.  Elements of a block are alike,
+    so that each is its largest; one in 65536 has a noise of 0."""
+    n, seed, f = 1 << 21, 5, np.float32
+    g, m, v, ms, vs = alike_blocks(n)
+    a = Lists([n], "bf16", "f32", "e4m3", seed=seed, shift=shift)
+    for name, x in (("g", g), ("m", m), ("v", v)):
+        t = getattr(a, name)[0]
+        t.copy_(torch.from_numpy(OA.spread(x, n)).cuda().to(t.dtype))
+    a.ms[0].copy_(torch.from_numpy(ms))
+    a.vs[0].copy_(torch.from_numpy(vs))
+    a.op.run(LR, 3)
+    noise_m, noise_v, _ = OA.noise(seed, 3, 0, np.arange(n))
+    new_m = f(BETAS[0]) * (m * ms) + f(1 - BETAS[0]) * g
+    root = v * vs
+    new_root = np.sqrt(f(BETAS[1]) * (root * root) + f(1 - BETAS[1]) * g * g)
+    for got, new, noise in ((a.m[0], new_m, noise_m), (a.v[0], new_root, noise_v)):
+        code = largest_code(np.abs(new))
+        assert len(set(code)) == 2 and (noise == 0).sum() > 16
+        want = np.where(noise == 0, OA.spread(code, n), 0x7E) | np.where(OA.spread(new, n) < 0, 0x80, 0)
+        assert np.array_equal(got.view(torch.uint8).cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_blocks_of_zeros_stay_zero_with_any_noise(shift):
+    a = Lists([1 << 21], "bf16", "f32", "e4m3", seed=5, shift=shift, zero=True)
+    a.g[0].zero_()
+    a.op.run(LR, 1)
+    for t in (a.m[0], a.v[0]):
+        assert not t.view(torch.uint8).any()
+    for t in (a.ms[0], a.vs[0]):
+        assert (t == OA.SCALE_MIN).all()
+
+
 def test_a_small_decay_is_that_of_its_size():
     """Of 1e-6, where 1 - 1e-6 in f32 is 1.3 % off: weights without gradients shrink by 1e-6 on average, each product and sum
     rounded by half an ulp (2^-24 of the weight) at random, of which a million's mean keeps a thousandth; six of that is allowed."""
