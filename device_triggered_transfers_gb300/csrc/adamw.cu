@@ -768,6 +768,40 @@ int run_batches(const dtt_adamw& o, const void* const* grads, const Scalars& s, 
     return DTT_OK;
 }
 
+// Whether a buffer that is written overlaps another one; of: the tensor of the one that begins later.
+bool overlap(const dtt_adamw_desc& d, const dtt_adamw_tensor* tensors, uint32_t count, uint32_t* of) {
+    struct Span {
+        uintptr_t from, to;
+        uint32_t tensor;
+        bool written;
+    };
+    std::vector<Span> spans;
+    for (uint32_t i = 0; i < count; ++i) {
+        const dtt_adamw_tensor& t = tensors[i];
+        const uint64_t se = elem_bytes(d.state_dtype), blocks = (t.n + kBlock - 1) / kBlock;
+        const auto add = [&](const void* p, uint64_t bytes, bool written) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            if (p && bytes) spans.push_back({at, at + bytes, i, written});
+        };
+        add(t.param, t.n * elem_bytes(d.param_dtype), true);
+        add(t.m, t.n * se, true);
+        add(t.v, t.n * se, true);
+        add(t.m_scales, blocks * 4, true);
+        add(t.v_scales, blocks * 4, true);
+        add(t.copy, t.n * 2, true);
+        add(t.grad, t.n * elem_bytes(d.grad_dtype), false);
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.from < b.from; });
+    uintptr_t any = 0, written = 0;             // where those up to here end
+    for (const Span& x : spans) {
+        *of = x.tensor;
+        if (x.from < (x.written ? any : written)) return true;
+        any = std::max(any, x.to);
+        if (x.written) written = std::max(written, x.to);
+    }
+    return false;
+}
+
 }  // namespace
 
 extern "C" int dtt_adamw_create(const dtt_adamw_desc* d, const dtt_adamw_tensor* tensors, uint32_t count, dtt_adamw** out) {
@@ -797,6 +831,12 @@ extern "C" int dtt_adamw_create(const dtt_adamw_desc* d, const dtt_adamw_tensor*
         if (misaligned(t.param, pe) || misaligned(t.grad, ge) || misaligned(t.m, se) || misaligned(t.v, se) ||
             misaligned(t.m_scales, 4) || misaligned(t.v_scales, 4) || misaligned(t.copy, 2))
             return fail(DTT_EINVAL, "%s: tensor %u: a pointer is not aligned to its elements", who, i);
+    }
+    uint32_t of = 0;
+    try {
+        if (overlap(*d, tensors, count, &of)) return fail(DTT_EINVAL, "%s: tensor %u: a buffer overlaps another one", who, of);
+    } catch (const std::bad_alloc&) {
+        return fail(DTT_ENOMEM, "%s: out of host memory", who);
     }
     int rc = preload_once();
     if (rc) return rc;

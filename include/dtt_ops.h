@@ -261,7 +261,8 @@ int dtt_experts_combine_backward(const dtt_experts_desc* desc, uint64_t tokens, 
  * States: DTT_F32, m and v as they are; or DTT_E4M3: m and sqrt(v) in codes of 8 bits, with one f32 scale for
  * each DTT_ADAMW_BLOCK elements of a tensor (the last block holds what is left),
  *     scale = max(max |x| / 448, 2^-100) over the block (to an ulp),  code = e4m3(x / scale) (x / scale to a few ulp),
- * but a root above zero has the code 2^-9 at least, since the next step divides by it.  The step itself uses the
+ * but a root above zero has the code 2^-9 at least, since the next step divides by it, and a block's largest is
+ * rounded at random as the formula's products and sums, each rounded to f32 by itself, leave it.  The step itself uses the
  * new m and v before they are rounded.  All states zero, their scales too, is the start.
  * stochastic = 0: codes and bf16 weights are rounded to nearest.  1: up, away from zero, with the probability of
  * what lies below, so that small changes that nearest would lose each time add up on average; a copy stays
@@ -303,12 +304,14 @@ typedef struct dtt_adamw_tensor {
 typedef struct dtt_adamw dtt_adamw;
 
 /* A handle: the desc and the list of tensors, checked and kept on the host (it holds no device memory).  The
- * buffers stay the caller's; no two of them overlap, but for gradients, which may.
+ * buffers stay the caller's; none that is written overlaps another one, or a gradient (gradients may one another), which is
+ * refused for the list's own: a tensor comes once.
  * Errors: DTT_EINVAL, DTT_ENOMEM, DTT_ECUDA. */
 int dtt_adamw_create(const dtt_adamw_desc* desc, const dtt_adamw_tensor* tensors, uint32_t count, dtt_adamw** out);
 
 /* One step over all tensors.
- *  - grads: NULL, or this step's gradients in the list's order (those of empty tensors are not looked at).
+ *  - grads: NULL, or this step's gradients in the list's order (those of empty tensors are not looked at), which overlap
+ *    nothing that is written.
  *  - lr_dev: device f32, read when the kernels run; lr is then not used.  NULL: lr, which must be finite.
  *  - step_dev: device uint32, the steps made so far, which the call counts up first: what a graph that is
  *    replayed needs.  step is then not used.  NULL: step, 1 or more.

@@ -175,6 +175,25 @@ def test_adamw_refuses_a_bad_tensor(desc, over):
     assert b"tensor 1" in L.dtt_last_error()
 
 
+@pytest.mark.parametrize("over", [dict(param=256), dict(m=1024), dict(v=1024 + 36), dict(grad=2048 + 36), dict(v=512 + 16), dict(param=1020)])
+def test_adamw_refuses_buffers_that_overlap(over):
+    """Ten elements: the first tensor has its param (f32) at 256, grad (bf16) at 512, m and v at 1024 and 2048."""
+    out, L = C.c_void_p(), D.lib()
+    apart = dict(param=1 << 16, grad=1 << 17, m=1 << 18, v=1 << 19)
+    both = (D.dtt_adamw_tensor * 2)(adam_tensor(), adam_tensor(**{**apart, **over}))
+    assert L.dtt_adamw_create(C.byref(adam_desc()), both, 2, C.byref(out)) == D.EINVAL and not out.value
+    assert b"overlaps" in L.dtt_last_error()
+
+
+def test_adamw_takes_gradients_that_overlap_and_neighbours():
+    """As far as a GPU: the list is fine."""
+    out, L = C.c_void_p(), D.lib()
+    both = (D.dtt_adamw_tensor * 2)(adam_tensor(), adam_tensor(param=256 + 40, m=1024 + 40, v=2048 + 40))
+    rc = L.dtt_adamw_create(C.byref(adam_desc()), both, 2, C.byref(out))
+    assert rc == D.OK if out.value else b"overlaps" not in L.dtt_last_error()
+    L.dtt_adamw_destroy(out)
+
+
 def test_adamw_refuses_what_is_null():
     out, L = C.c_void_p(), D.lib()
     assert L.dtt_adamw_create(None, C.byref(adam_tensor()), 1, C.byref(out)) == D.EINVAL
