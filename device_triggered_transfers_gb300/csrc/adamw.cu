@@ -24,9 +24,9 @@ constexpr float kCodeMax = 448.0f, kScaleLeast = 0x1p-100f;
 constexpr float kCodeLeast = 0x1p-9f;                          // e4m3's smallest value above zero
 constexpr uint64_t kMostElements = 1ull << 40;
 // 8-bit states: where there are many elements a CTA takes several chunks, whose copies go out together and which share
-// the search for the tensor and the step's numbers.  32M weights: 88 us with one chunk a CTA, straight from global memory, 59 with
-// four.  (f32 states: 715 us with one at 151M weights; two or three by way of shared memory 766 to 789, reads that run
-// further ahead of the writes cost more than they hide.)
+// the search for the tensor and the step's numbers.  32M weights: 88 us with one chunk a CTA, straight from global memory, 60 with
+// four, before the largest were settled.  (f32 states: 715 us with one at 151M weights; two or three by way of shared
+// memory 766 to 789, reads that run further ahead of the writes cost more than they hide.)
 constexpr uint32_t kTurns = 4;
 constexpr uint64_t kManyElements = 4ull * kTurns * kChunk * kSms;
 
