@@ -438,14 +438,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(const 
 }
 
 // ---- rows through shared memory -----------------------------------------------------------------
-// For many tokens of long rows: persistent CTAs, two an SM, of eight warps that add up and one that fetches.  An item is a
+// For many tokens of long rows: persistent CTAs, three an SM, of eight warps that add up and one that fetches.  An item is a
 // batch of a token's rows in 2048 columns (and for the gradients the token's own row), each row's piece in a slot of its own,
 // so that items of few rows, as where most experts are other ranks', are many under way.  The ninth warp has bulk copies of the
 // next items going, so that reading positions, rows and adding up overlap.  A thread whose wait for an item runs out
 // takes it, and all after it, straight from global memory: the results are the same.
-constexpr uint32_t kAdders = 256, kTile = 8 * kAdders, kBatch = 8, kItems = 16;
+constexpr uint32_t kAdders = 256, kTile = 8 * kAdders, kBatch = 8, kItems = 12, kRingCtas = 3;
 constexpr uint32_t kWaitLimit = 1u << 18;      // looks at an mbarrier; one that fails takes 4 us: a second
-constexpr uint32_t kRingSmem = 108 * 1024;     // of a CTA's slots, at most
+constexpr uint32_t kRingSmem = 72 * 1024;      // of a CTA's slots, at most
 
 __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {      // false: the wait ran out
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
@@ -472,9 +472,9 @@ struct Slots {
     static_assert(count > kBatch, "an item with all its rows fits");
 };
 // What the adders know of an item.
-struct Known {
-    uint4 rows[kBatch];         // of those there are: number, weight, its piece's place in the slots
-    uint32_t own_at, mask, slots;
+struct __align__(16) Known {
+    uint4 rows[kBatch];         // of those there are, in order: number, weight, its piece's place in the slots
+    uint32_t own_at, mask, none[2];
 };
 
 struct RingParams {
@@ -500,7 +500,7 @@ struct Turn {
     }
 };
 
-// The pairs j0 .. j0 + kBatch - 1 of a token as lane j of a warp has them: their rows, ~0 for none, and weights.
+// The pairs j0 .. j0 + kBatch - 1 of a token as lane j of a warp has them: their rows, as they are, and weights.
 struct Pairs {
     uint32_t row = ~0u;
     float weight = 1.0f;
@@ -513,27 +513,77 @@ __device__ __forceinline__ Pairs lane_pairs(const RingParams& p, uint64_t token,
         r.row = row_of(p.s, pair);
         if (p.weights) r.weight = p.weights[pair];
     }
-    if (r.row >= p.s.max_rows) r.row = ~0u;
+    return r;
+}
+
+// What of an item does not depend on its columns, for the lane that fetches a piece: lane j row j's, lane kBatch the token's.
+struct Pieces {
+    const char* from;           // null: none
+    uint32_t row, weight;       // row: of the token's lane the mask of the rows there are
+    uint32_t rank;              // which of the rows there are
+    uint32_t place, size;       // slots before this piece's, and bytes of an element
+    bool known;                 // the adders are told
+    uint32_t slots, bytes;      // of the item, and of its columns: bytes each
+};
+template <uint32_t RDT, uint32_t GDT, bool BACK>
+__device__ __forceinline__ Pieces pieces_of(const RingParams& p, uint64_t token, const Pairs& mine) {
+    using S = Slots<RDT, GDT, BACK>;
+    const uint32_t lane = threadIdx.x % 32;
+    const bool reads = !BACK || p.dweights, has = mine.row < p.s.max_rows;
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, has), rows = reads ? __popc(mask) : 0;
+    const bool own = BACK && mask, mine_is_own = lane == kBatch;
+    Pieces r;
+    r.slots = rows + own;
+    r.bytes = rows * S::re + (own ? S::ge : 0);
+    r.from = mine_is_own ? (own ? p.own + token * p.own_pitch : nullptr) : reads && has ? p.rows + mine.row * p.rows_pitch : nullptr;
+    r.row = mine_is_own ? mask : mine.row;
+    r.weight = __float_as_uint(mine.weight);
+    r.rank = mine_is_own ? kBatch : __popc(mask & ((1u << lane) - 1));
+    r.place = mine_is_own ? rows : reads ? r.rank : 0;
+    r.size = mine_is_own ? S::ge : S::re;
+    r.known = has || mine_is_own;
     return r;
 }
 
 // The ninth warp.  Items in the adders' order: forward a token's columns, and its batches within them; backward its
-// batches, and the columns within (the first alone where a batch has no rows).
+// batches, and the columns within (the first alone where a batch has no rows).  It is one warp's instructions one after the
+// other, so that what does not depend on the columns is worked out once a batch, and lanes do the rows' and the token's
+// piece at once: 2000 tokens without a row here 4.6 us, with all of it for each item 5.8.
 template <uint32_t RDT, uint32_t GDT, bool BACK>
 __device__ __forceinline__ void fetch(const RingParams& p, uint32_t slots, uint32_t full, uint32_t empty, Known* known) {
     using S = Slots<RDT, GDT, BACK>;
     const uint32_t lane = threadIdx.x % 32, tiles = (p.cols + kTile - 1) / kTile, batches = (p.s.k + kBatch - 1) / kBatch;
-    const bool reads = !BACK || p.dweights;
     Turn turn, oldest;                          // the next item's, and of those under way the first
     uint32_t under_way = 0, free = S::count, head = 0;
+    uint32_t held = 0;                          // slots of the item whose turn is the lane's number
+    static_assert(kItems <= 32, "a lane each");
     bool late = false;
-    // the first item under way is done with: its copies have landed, which adders that have given up do not tell, and
-    // the adders have taken them; all lanes give up if one does
+    // the first item under way is done with: its copies have landed, which adders that have given up do not tell (even
+    // lanes look), and the adders have taken them (odd ones); all lanes give up if one does
+    const uint32_t done = lane % 2 ? empty : full;
     const auto retire = [&] {
-        late = late || __any_sync(0xFFFFFFFFu, !arrived(full + 8 * oldest.at, oldest.phase) || !arrived(empty + 8 * oldest.at, oldest.phase));
-        free += known[oldest.at].slots;
+        late = late || __any_sync(0xFFFFFFFFu, !arrived(done + 8 * oldest.at, oldest.phase));
+        free += __shfl_sync(0xFFFFFFFFu, held, oldest.at);
         --under_way;
         oldest.next();
+    };
+    const auto item = [&](const Pieces& x, uint32_t tile) {
+        while (!late && (under_way == kItems || free < x.slots)) retire();
+        if (late) return;
+        const uint32_t c = tile * kTile, columns = min(kTile, p.cols - c), bar = full + 8 * turn.at, at = head + x.place;
+        const uint32_t to = (at < S::count ? at : at - S::count) * S::bytes;
+        if (x.known)
+            reinterpret_cast<uint4*>(known + turn.at)[x.rank] = lane < kBatch ? make_uint4(x.row, x.weight, to, 0) : make_uint4(to, x.row, 0, 0);
+        __syncwarp();
+        if (lane == 0) bar_expect_tx(bar, columns * x.bytes);
+        __syncwarp();
+        if (x.from) bulk(slots + to, x.from + (uint64_t)c * x.size, columns * x.size, bar);
+        if (lane == turn.at) held = x.slots;
+        head += x.slots;
+        if (head >= S::count) head -= S::count;
+        free -= x.slots;
+        ++under_way;
+        turn.next();
     };
     uint64_t token = blockIdx.x;
     // the first batches of the next two tokens: their latency is not to be an item's
@@ -542,38 +592,16 @@ __device__ __forceinline__ void fetch(const RingParams& p, uint32_t slots, uint3
         const Pairs first = ahead;
         ahead = further;
         further = lane_pairs(p, token + 2 * (uint64_t)gridDim.x, 0);
-        Pairs mine = first;
-        for (uint32_t n = 0; n < tiles * batches; ++n) {
-            const uint32_t tile = BACK ? n % tiles : n / batches, batch = BACK ? n / tiles : n % batches, j0 = batch * kBatch;
-            if (batches > 1 && (!BACK || tile == 0)) mine = batch == 0 ? first : lane_pairs(p, token, j0);
-            const uint32_t r = mine.row;
-            const bool has = r != ~0u;
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, has);
-            if (BACK && mask == 0 && tile > 0) continue;
-            const float w = mine.weight;
-            const uint32_t c = tile * kTile, columns = min(kTile, p.cols - c);
-            const uint32_t copies = reads ? __popc(mask) : 0, own = BACK && mask ? 1 : 0;
-            while (!late && (under_way == kItems || free < copies + own)) retire();
-            if (late) break;
-            const uint32_t bar = full + 8 * turn.at;
-            const auto slot = [&](uint32_t i) { return (head + i < S::count ? head + i : head + i - S::count) * S::bytes; };
-            const uint32_t to = slot(__popc(mask & ((1u << lane) - 1)));
-            if (has) known[turn.at].rows[lane] = make_uint4(r, __float_as_uint(w), to, 0);
-            if (lane == 0) {
-                known[turn.at].own_at = slot(copies);
-                known[turn.at].mask = mask;
-                known[turn.at].slots = copies + own;
+        const Pieces of_first = pieces_of<RDT, GDT, BACK>(p, token, first);
+        const auto batch_of = [&](uint32_t batch) { return batch == 0 ? of_first : pieces_of<RDT, GDT, BACK>(p, token, lane_pairs(p, token, batch * kBatch)); };
+        if constexpr (BACK) {
+            for (uint32_t batch = 0; batch < batches && !late; ++batch) {
+                const Pieces x = batch_of(batch);
+                for (uint32_t tile = 0; tile < (x.slots ? tiles : 1) && !late; ++tile) item(x, tile);
             }
-            __syncwarp();
-            if (lane == 0) bar_expect_tx(bar, copies * columns * S::re + own * columns * S::ge);
-            __syncwarp();
-            if (reads && has) bulk(slots + to, p.rows + r * p.rows_pitch + (uint64_t)c * S::re, columns * S::re, bar);
-            if (own && lane == 0) bulk(slots + slot(copies), p.own + token * p.own_pitch + (uint64_t)c * S::ge, columns * S::ge, bar);
-            head += copies + own;
-            if (head >= S::count) head -= S::count;
-            free -= copies + own;
-            ++under_way;
-            turn.next();
+        } else {
+            for (uint32_t tile = 0; tile < tiles && !late; ++tile)
+                for (uint32_t batch = 0; batch < batches && !late; ++batch) item(batch_of(batch), tile);
         }
     }
     // no copy is under way when the CTA leaves
@@ -587,10 +615,12 @@ __device__ __forceinline__ void piece8(bool late, const char* item, const char* 
     else expand8(raw8(item, DT), DT, v);
 }
 
-// 131072 rows of 4096 in bf16: combined in 177 us, the copy rate (reads outnumber writes); their gradients in 366 us, 0.92 (373
-// with stores that stay in L2 as long as others, and 2000 tokens of 8064 with one row each 25 and not 22).
+// 131072 rows of 4096 in bf16: combined in 174 us, the copy rate (reads outnumber writes); their gradients in 361 us, 0.93.
+// 2000 tokens of 8064 with a row each: 17.8 us for the gradients, 0.80.  Items of few rows are bound by the adders' instructions one
+// after the other, so that three CTAs an SM with 72 KiB of slots each are ahead of two with 108 (177, 368 and 22 us), and
+// the rows that there are come one behind the other (18.2 where each of eight places is looked at).
 template <uint32_t RDT, uint32_t GDT, bool BACK>
-__global__ void __launch_bounds__(kAdders + 32, 2) rows_ring_kernel(const __grid_constant__ RingParams p) {
+__global__ void __launch_bounds__(kAdders + 32, kRingCtas) rows_ring_kernel(const __grid_constant__ RingParams p) {
     using S = Slots<RDT, GDT, BACK>;
     launch_next();
     extern __shared__ __align__(128) uint8_t slots[];
@@ -621,8 +651,9 @@ __global__ void __launch_bounds__(kAdders + 32, 2) rows_ring_kernel(const __grid
         for (uint32_t j = 0; j < kBatch && j0 + j < p.s.k; ++j) mask |= (row_of(p.s, token * p.s.k + j0 + j) < p.s.max_rows ? 1u : 0u) << j;
         return mask;
     };
-    const auto row_at = [&](uint64_t pair, uint32_t j) {
-        if (!late) return known[ring.at].rows[j];
+    const auto row_at = [&](uint64_t pairs, uint32_t mask, uint32_t i) {          // the i-th of the rows there are
+        if (!late) return known[ring.at].rows[i];
+        const uint64_t pair = pairs + __fns(mask, 0, i + 1);
         return make_uint4(row_of(p.s, pair), __float_as_uint(p.weights ? p.weights[pair] : 1.0f), 0, 0);
     };
     const char* base = reinterpret_cast<const char*>(slots);
@@ -641,11 +672,11 @@ __global__ void __launch_bounds__(kAdders + 32, 2) rows_ring_kernel(const __grid
                 float sum[8] = {};
                 for (uint32_t j0 = 0; j0 < p.s.k; j0 += kBatch) {
                     wait();
-                    const uint32_t mask = c < p.cols ? mask_of(token, j0) : 0;
+                    const uint32_t mask = c < p.cols ? mask_of(token, j0) : 0, n = __popc(mask);
 #pragma unroll
                     for (uint32_t j = 0; j < kBatch; ++j) {
-                        if (!(mask >> j & 1)) continue;
-                        const uint4 row = row_at(token * p.s.k + j0 + j, j);
+                        if (j >= n) break;
+                        const uint4 row = row_at(token * p.s.k + j0, mask, j);
                         const float w = __uint_as_float(row.y);
                         float v[8];
                         piece8<RDT>(late, base + row.z + 8 * t * S::re, p.rows + row.x * p.rows_pitch + (uint64_t)c * S::re, v);
@@ -665,12 +696,13 @@ __global__ void __launch_bounds__(kAdders + 32, 2) rows_ring_kernel(const __grid
                     wait();
                     mask = mask_of(token, j0);
                     if (mask && c < p.cols) {
+                        const uint32_t n = __popc(mask);
                         float g[8];
                         piece8<GDT>(late, base + known[ring.at].own_at + 8 * t * S::ge, p.own + token * p.own_pitch + (uint64_t)c * S::ge, g);
 #pragma unroll
                         for (uint32_t j = 0; j < kBatch; ++j) {
-                            if (!(mask >> j & 1)) continue;
-                            const uint4 row = row_at(token * p.s.k + j0 + j, j);
+                            if (j >= n) break;
+                            const uint4 row = row_at(token * p.s.k + j0, mask, j);
                             const float w = __uint_as_float(row.y);
                             float v[8];
                             if (p.dweights) {
@@ -692,9 +724,10 @@ __global__ void __launch_bounds__(kAdders + 32, 2) rows_ring_kernel(const __grid
                     const float mine = sum_of_mine(dot);
                     if (lane < kBatch) sums[turn][t / 32][lane] = mine;
                     adders_sync();
-                    if (t < kBatch) {
+                    if (t < kBatch && mask >> t & 1) {
+                        const uint32_t rank = __popc(mask & ((1u << t) - 1));
 #pragma unroll
-                        for (uint32_t i = 0; i < kAdders / 32; ++i) sum += sums[turn][i][t];
+                        for (uint32_t i = 0; i < kAdders / 32; ++i) sum += sums[turn][i][rank];
                     }
                     turn ^= 1;
                 }
@@ -794,16 +827,20 @@ RingLaunch ring_of(uint32_t rows, uint32_t other) {
     if (rows == DTT_BF16) return other == DTT_BF16 ? ring_of<BACK, DTT_BF16, DTT_BF16>() : ring_of<BACK, DTT_BF16, DTT_F32>();
     return other == DTT_BF16 ? ring_of<BACK, DTT_F32, DTT_BF16>() : ring_of<BACK, DTT_F32, DTT_F32>();
 }
-// Measured over 300 to 20000 tokens, with 8 choices of 64 experts all here, 8 of 64 with a quarter here, and 2 of 16 all
-// here (bf16; straight from global memory, and by the ring).  Forward, 2600 tokens of 2048 columns: 20 us and 20, 11 and 13.5,
-// 11 and 13; of 4096: 37 and 33, 19 and 19, 18 and 18; of 8064: 72 and 61, 34 and 30, 32 and 29.  Backward, of 1024: 21 and 22, 12
-// and 15, 9 and 15; of 2048: 38 and 32, 21 and 17, 16 and 17; of 8064: 138 and 118, 50 and 39, 44 and 38.  At 300 tokens the
-// same sides win from the same columns on.
-bool through_ring(bool vec, uint64_t tokens, uint64_t cols, bool back) { return vec && cols >= (back ? 2048 : 4096) && tokens >= kSms; }
+// Measured over 80 to 20000 tokens, with 8 choices of 64 experts all here, 8 of 64 with a quarter here, and 2 of 16 all
+// here (bf16, us straight from global memory and by the ring).  Forward, 2600 tokens of 1024 columns: 11.2 and 11.4, 6.2 and
+// 6.8, 6.0 and 6.3; of 2048: 20.1 and 17.6, 11.2 and 8.4, 10.8 and 8.1; of 8064: 71 and 58, 34 and 25, 32 and 24.  300 tokens
+// of 2048: 3.9 and 4.2, 2.4 and 2.6, 2.3 and 2.4; of 4096: 7.4 and 7.0, 3.9 and 3.4, 3.6 and 3.1; 80 of 4096: 3.3 and 3.8, 2.8
+// and 2.9, 2.6 and 2.5.  Backward, 2600 tokens of 1024: 21.0 and 17.6, 11.7 and 10.1, 8.9 and 9.6; of 2048: 38 and 33, 21 and 12, 16
+// and 12; 300 of 2048: 7.5 and 6.4, 3.8 and 3.4, 2.6 and 3.1; of 4096: 13.1 and 10.6, 6.6 and 4.6, 4.5 and 4.1.
+bool through_ring(bool vec, uint64_t tokens, uint32_t k, uint64_t cols, bool back) {
+    const uint64_t least = back ? (k >= 8 ? 1024 : 2048) : tokens >= 8 * kSms ? 2048 : 4096;
+    return vec && cols >= least && tokens >= kSms;
+}
 cudaError_t launch_ring(const RingLaunch& r, const RingParams& p, cudaStream_t stream) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) sms = 1;
-    return launch(r.kernel, (uint32_t)std::min<uint64_t>(p.s.tokens, 2 * (uint64_t)sms), kAdders + 32, r.smem, 0, true, stream, p);
+    return launch(r.kernel, (uint32_t)std::min<uint64_t>(p.s.tokens, kRingCtas * (uint64_t)sms), kAdders + 32, r.smem, 0, true, stream, p);
 }
 
 uint32_t elem_bytes(uint32_t dt) { return dt == DTT_BF16 ? 2 : 4; }
@@ -944,7 +981,7 @@ extern "C" int dtt_experts_combine(const dtt_experts_desc* d, uint64_t tokens, u
     q.rows_pitch = rows_pitch;
     q.out_pitch = out_pitch;
     q.cols = p.cols;
-    const cudaError_t e = through_ring(vec, tokens, cols, false) ? launch_ring(ring_of<false>(rows_dtype, out_dtype), q, stream) : launch(combine_of(vec, rows_dtype, out_dtype), (uint32_t)ctas_of(tokens, block), block, 0, 0, true, stream, p);
+    const cudaError_t e = through_ring(vec, tokens, d->top_k, cols, false) ? launch_ring(ring_of<false>(rows_dtype, out_dtype), q, stream) : launch(combine_of(vec, rows_dtype, out_dtype), (uint32_t)ctas_of(tokens, block), block, 0, 0, true, stream, p);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }
@@ -992,7 +1029,7 @@ extern "C" int dtt_experts_combine_backward(const dtt_experts_desc* d, uint64_t 
     q.rows_pitch = rows_pitch;
     q.own_pitch = dout_pitch;
     q.cols = p.cols;
-    const cudaError_t e = through_ring(vec, tokens, cols, true) ? launch_ring(ring_of<true>(rows_dtype, dout_dtype), q, stream) : launch(backward_of(vec, rows_dtype, dout_dtype), (uint32_t)grid, block, 0, 0, true, stream, p);
+    const cudaError_t e = through_ring(vec, tokens, d->top_k, cols, true) ? launch_ring(ring_of<true>(rows_dtype, dout_dtype), q, stream) : launch(backward_of(vec, rows_dtype, dout_dtype), (uint32_t)grid, block, 0, 0, true, stream, p);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;
 }

@@ -103,7 +103,8 @@ ROWS = [(1, 1, 1, 1, 1, 0, 1, 0, 0), (1, 4096, 8, 128, 16, 0, 1, 0, 0), (37, 409
 
 # many tokens of long rows come through shared memory: parts of a tile, whole ones, more choices than a batch has
 RING = [(610, 1024, 2, 8, 8, 0, 1, 0, 0), (700, 1032, 9, 16, 16, 0, 8, 8, 8), (650, 8064, 4, 64, 16, 16, 16, 0, 0), (613, 4096, 8, 32, 32, 0, 128, 0, 0),
-        (609, 2056, 32, 40, 30, 5, 4, 0, 16), (1301, 2048, 1, 4, 1, 2, 1, 0, 0)]
+        (609, 2056, 32, 40, 30, 5, 4, 0, 16), (1301, 2048, 1, 4, 1, 2, 1, 0, 0), (200, 4104, 20, 40, 30, 5, 4, 0, 16), (1300, 2056, 32, 40, 30, 5, 4, 8, 0),
+        (500, 6000, 8, 64, 2, 7, 1, 0, 0)]
 ROWS += RING
 
 
