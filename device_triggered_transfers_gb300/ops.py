@@ -161,11 +161,18 @@ class RMSNorm:
             D._check(rc)
 
 
+def _current_device() -> int:
+    """torch.cuda.current_device, in whose place the first call puts it: an import takes 0.1 us of each call."""
+    global _current_device
+    import torch
+    _current_device = torch.cuda.current_device
+    return _current_device()
+
+
 def _here(who: str, name: str, t) -> int:
     """The number of t's GPU, which is the current one: the calls launch there."""
-    import torch
     device = t.get_device()
-    if device < 0 or device != torch.cuda.current_device():
+    if device < 0 or device != _current_device():
         raise D.DttError(D.EINVAL, f"{who}: {name} must be on the current GPU")
     return device
 
@@ -295,8 +302,8 @@ class ExpertRows:
             raise D.DttError(D.EINVAL, f"ExpertRows: {name} must be on the current GPU with contiguous rows")
         return t.data_ptr(), row * t.element_size()
 
-    def _sorted(self, position, offsets, counts) -> Tuple[int, int, int]:
-        return (self._flat("position", position, (position.shape[0], self.top_k), self._i32),
+    def _sorted(self, tokens: int, position, offsets, counts) -> Tuple[int, int, int]:
+        return (self._flat("position", position, (tokens, self.top_k), self._i32),
                 self._flat("offsets", offsets, (self.experts + 1,), self._i32),
                 self._flat("counts", counts, (self.experts,), self._i32))
 
@@ -325,12 +332,11 @@ class ExpertRows:
         """rows[position[t, j]] = x[t] (both of one type, any), and row_scales[position[t, j]] = scales[t] (f32, both or
         neither); zeros in the rows that fill an expert's up; rows behind the last expert's are left as they were."""
         self._device = _here(self._who, "x", x)
-        tokens, cols = x.shape[0], x.shape[-1]
+        shape = x.shape
+        tokens, cols = shape[0], shape[-1]
         xp, xs = self._rows("x", x, tokens, cols)
         rp, rs = self._rows("rows", rows, None, cols, (x.dtype,))
-        pp, op, cp = self._sorted(position, offsets, counts)
-        if position.shape[0] != tokens:
-            raise D.DttError(D.EINVAL, f"ExpertRows: position is of {position.shape[0]} tokens, x of {tokens}")
+        pp, op, cp = self._sorted(tokens, position, offsets, counts)
         sp = ss = tp = ts = n = 0
         if scales is not None or row_scales is not None:
             if scales is None or row_scales is None:
@@ -366,10 +372,8 @@ class ExpertRows:
         gp, gs = self._rows("dout", dout, tokens, cols, self._row_types)
         dp, ds = self._rows("drows", drows, None, cols, self._row_types)
         rp, rs = self._rows("rows", rows, drows.shape[0], cols, (drows.dtype,))
-        pp, op, cp = self._sorted(position, offsets, counts)
+        pp, op, cp = self._sorted(tokens, position, offsets, counts)
         pairs = (tokens, self.top_k)
-        if position.shape != pairs:
-            raise D.DttError(D.EINVAL, f"ExpertRows: position is of {position.shape[0]} tokens, dout of {tokens}")
         rc = self._combine_backward(self._ref, tokens, cols, pp, op, cp, gp, self._row_types[dout.dtype], gs, rp,
                                     self._row_types[drows.dtype], rs, drows.shape[0],
                                     self._flat("weights", weights, pairs, self._f32), dp, ds,
