@@ -52,11 +52,9 @@ struct FwdParams {
     const char* x;
     const char* res;            // or null
     const char* w;              // or null
-    const char* b;              // layer norm: or null
     char* res_out;              // or null
     char* y;
     float* scales;
-    float* mean;                // layer norm: or null
     float* rstd;                // or null
     uint64_t x_pitch, res_pitch, res_out_pitch, y_pitch;
     uint64_t rows;
@@ -64,25 +62,29 @@ struct FwdParams {
     uint32_t x_dt, res_dt, w_dt, y_dt;
     uint32_t group_lanes;       // lanes that share a scale: 4, 8, 16; 0: one scale per row
     float eps, inv_cols;
+    // layer norm:
+    const char* b;              // or null
+    float* mean;                // or null
 };
 
 struct BwdParams {
     const char* dy;
     const char* h;
     const char* w;              // or null
-    const float* mean;          // layer norm
     const float* rstd;
     const char* dres;           // or null
     char* dx;
     float* partial;             // [partials][cols], or null: no weight gradient, or few rows
-    float* partial_b;           // layer norm: the same of the bias's gradient, or null
     float* dweight;             // few rows: the CTAs after the first `partials` work it out; else null
-    float* dbias;               // the same
     uint64_t dy_pitch, h_pitch, dres_pitch, dx_pitch;
     uint64_t rows;
     uint32_t cols, partials, walkers;   // walker i takes rows i, i + walkers, ...
     uint32_t dy_dt, h_dt, w_dt;
     float inv_cols;
+    // layer norm:
+    const float* mean;
+    float* partial_b;           // as partial and dweight, of the bias's gradient
+    float* dbias;
 };
 
 // The scale of a group whose largest magnitude is m.

@@ -119,15 +119,6 @@ class RMSNorm:
             raise D.DttError(D.EINVAL, f"RMSNorm: {name} must be {n} contiguous {dtype} on the GPU")
         return t.data_ptr()
 
-    def _scratch(self, needed: bool, stream, device) -> Tuple[int, int]:
-        """(address, bytes) of the backward pass's workspace, where the call needs one."""
-        if not needed:
-            return 0, 0
-        if self._workspace is None or self._workspace.buffer.device != device:
-            self._workspace = _Workspace.on(stream, self.workspace_bytes, device)
-        self._workspace.use(stream)
-        return self._workspace.address, self.workspace_bytes
-
     def forward(self, x, weight, y, residual=None, residual_out=None, scales=None, rstd=None, stream=None) -> None:
         """y, and where given residual_out (= h; may be residual itself), scales ([rows, scale_cols]
         f32, with an e4m3 y) and rstd ([rows] f32, which the backward pass needs)."""
@@ -153,7 +144,12 @@ class RMSNorm:
         hp, hs = self._rows("h", h, shape, self._res, self._rese)
         sp, ss = self._rows("dres", dres, shape, self._res, self._rese)
         xp, xs = self._rows("dx", dx, shape, self._res, self._rese)
-        ws, need = self._scratch(dweight is not None, stream, dy.device)
+        ws, need = 0, 0
+        if dweight is not None:
+            if self._workspace is None or self._workspace.buffer.device != dy.device:
+                self._workspace = _Workspace.on(stream, self.workspace_bytes, dy.device)
+            self._workspace.use(stream)
+            ws, need = self._workspace.address, self.workspace_bytes
         rc = self._backward(self._ref, rows, gp, gs, hp, hs, self._flat("weight", weight, self.cols, self._w),
                             self._flat("rstd", rstd, rows, self._f32), sp, ss, xp, xs,
                             self._flat("dweight", dweight, self.cols, self._f32), ws, need, D._stream(stream))
@@ -241,7 +237,12 @@ class LayerNorm(RMSNorm):
         args = (flat("weight", weight, self.cols, self._w), flat("mean", mean, rows, self._f32),
                 flat("rstd", rstd, rows, self._f32), sp, ss, xp, xs,
                 flat("dweight", dweight, self.cols, self._f32), flat("dbias", dbias, self.cols, self._f32))
-        ws, need = self._scratch(dweight is not None or dbias is not None, stream, dy.device)
+        ws, need = 0, 0
+        if dweight is not None or dbias is not None:
+            if self._workspace is None or self._workspace.buffer.device != dy.device:
+                self._workspace = _Workspace.on(stream, self.workspace_bytes, dy.device)
+            self._workspace.use(stream)
+            ws, need = self._workspace.address, self.workspace_bytes
         rc = self._backward(self._ref, rows, gp, gs, hp, hs, *args, ws, need, D._stream(stream))
         if rc:
             D._check(rc)
