@@ -271,8 +271,9 @@ int dtt_experts_combine_backward(const dtt_experts_desc* desc, uint64_t tokens, 
  * x ^= x >> 16 } on 32 bits and r = mix(i 0x9E3779B9 + (i >> 32) 0x2E1B2139 + mix(mix(mix(seed) + t) + tensor)),
  * m is rounded by r's high 16 bits, sqrt(v) by its low 16, p by the high 16 of r 0x2E1B2139.  They take the
  * place of the highest 16 of the bits that are cut off.
- * The same call on the same values gives the same bits.  v and its root are f32: gradients below 1e-22 add nothing to
- * v, above 1e19 make it infinite and the step zero.  NaN in a gradient makes its element's p, m and v NaN, with
+ * The same call on the same values gives the same bits.  v and its root are f32, a subnormal v (gradients below 1e-18 or
+ * so) with the digits that are left there, and with 8-bit states all of them down to 2^-150: (1 - beta2) g^2 below 2^-150
+ * adds nothing to v; gradients above 1e19 make it infinite and the step zero.  NaN in a gradient makes its element's p, m and v NaN, with
  * 8-bit states its block's from the next step on; so does an infinity there. */
 #define DTT_ADAMW_BLOCK 128
 

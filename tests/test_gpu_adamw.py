@@ -6,6 +6,8 @@ of the terms' magnitudes.  The root is half of v's error and an ulp, the quotien
 change of p is off by 20 e of its own size and by m's error over the denominator; p itself takes 3 e.  A code is the
 value by the block's scale, to the nearest within half a spacing (e4m3: 4 significant bits, smallest normal 2^-6), or what
 stochastic rounding makes of some value within that error."""
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -407,6 +409,79 @@ def test_tiny_and_huge_gradients():
         # 1e-26 / 1e-8 of the rate
         assert (a.p[0][:128] - before[:128]).abs().max() < 1e-6 and torch.equal(a.p[0][128:], before[128:])
 
+
+def between(got, lo, hi):
+    assert ((lo <= got) & (got <= hi)).all()
+
+
+def tiny(n, grad):
+    """Gradients from 1e-21 to 1e-17, some zero, both signs."""
+    g = 10 ** (-21 + 4 * torch.rand(n, generator=gen(n), device="cuda")) * torch.randn(n, generator=gen(n + 1), device="cuda").sign()
+    return (g * (torch.rand(n, generator=gen(n + 2), device="cuda") > 0.1)).to(TYPES[grad])
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_a_subnormal_v_has_its_root(grad, shift, monkeypatch):
+    """Gradients that leave v = (1 - beta2) g^2 below 2^-126, with an eps that does not hide its root.  v's square and sum are each rounded
+    to a multiple of 2^-149, half of that off at most, beside the 9 e of normal values; the step lies between those of the least and
+    the largest such v."""
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 1e-25)
+    a = Lists([5000, 129, 3], "f32", grad, "f32", shift=shift, zero=True, decay=0.0)
+    for t in (1, 2, 1000):
+        for i, n in enumerate(a.sizes):
+            a.g[i].copy_(tiny(n + t, grad)[:n])
+        before = a.state()
+        a.op.run(LR, t)
+        a.check_gaps()
+        for i, b in enumerate(before):
+            p, g, m, v = (f64(b[k]) for k in "pgmv")
+            _, want_m, want_v = OA.step(p, g, m, v, t, LR, BETAS, EPS, 0.0)
+            off_m = 5 * E * (BETAS[0] * np.abs(m) + (1 - BETAS[0]) * np.abs(g))
+            assert (np.abs(f64(a.m[i]) - want_m) <= off_m).all()
+            off = 9 * E * want_v + 2 * 2.0 ** -150
+            between(f64(a.v[i]), want_v - off, want_v + off)
+            assert t > 1 or i > 0 or ((want_v > 0) & (want_v < 2.0 ** -126)).sum() > 0.5 * len(p)
+            most, least = (LR / (1 - BETAS[0] ** t) / (np.sqrt(np.maximum(want_v + k * off, 0)) / np.sqrt(1 - BETAS[1] ** t) + EPS) for k in (-1, 1))
+            lo, hi = least * np.abs(want_m), most * np.abs(want_m)
+            change = (p - f64(a.p[i])) * np.where(want_m < 0, -1, 1)
+            few = np.where(want_v > 0, 3 * E * np.abs(p) + 20 * E * hi + most * off_m, 0)
+            between(change, lo - few, hi + few)
+
+
+@pytest.mark.parametrize("param,grad,seed", [("f32", "f32", None), ("bf16", "bf16", 3), ("f32", "bf16", 5)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_roots_of_subnormal_squares_keep_their_codes(param, grad, seed, shift, monkeypatch):
+    """8-bit states: the root's block has its scale, a root above zero a code above zero, and the step is the formula's."""
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 1e-25)
+    a = Lists([5000, 129, 3], param, grad, "e4m3", seed=seed, shift=shift, zero=True, decay=0.0)
+    for t in (1, 2, 1000):
+        for i, n in enumerate(a.sizes):
+            a.g[i].copy_(tiny(n + t, grad)[:n])
+        before = a.state()
+        a.op.run(LR, t)
+        a.check(before, t)
+        assert max(float(s.max()) for s in a.vs) < 1e-18
+
+
+@pytest.mark.parametrize("param,grad,seed", [("f32", "f32", None), ("bf16", "bf16", 3), ("f32", "bf16", 5)])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("n", [5000, 5100000])
+def test_large_and_tiny_gradients_side_by_side(param, grad, seed, shift, n, monkeypatch):
+    """8-bit states: up to 1e18, so that v passes 2^104, beside 1e-20 in one block, one group and one chunk; large ones come and go."""
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 1e-25)
+    a = Lists([n, 333], param, grad, "e4m3", seed=seed, shift=shift, zero=True, decay=0.0)
+    for t in (1, 2, 3):
+        for i, size in enumerate(a.sizes):
+            g = tiny(size + t, "f32")[:size].clone()
+            block = torch.arange(size, device="cuda") // 128
+            some = (block % 5 == t % 3) & (torch.rand(size, generator=gen(t), device="cuda") < 0.1)
+            g[some] = (10 ** (12 + 6 * torch.rand(size, generator=gen(t + 9), device="cuda")))[some]
+            a.g[i].copy_(g.to(TYPES[grad]))
+        before = a.state()
+        a.op.run(LR, t)
+        a.check(before, t)
+        assert max(float(s.max()) for s in a.vs) * 448 > 2.0 ** 52
 
 @pytest.mark.parametrize("shift", [0, 1])
 def test_a_tensor_past_32_bits(shift):
