@@ -442,9 +442,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(const 
 // batch of a token's rows in 2048 columns (and for the gradients the token's own row), each row's piece in a slot of its own,
 // so that items of few rows, as where most experts are other ranks', are many under way.  The ninth warp has bulk copies of the
 // next items going, so that reading positions, rows and adding up overlap.  A thread whose wait for an item runs out
-// takes it, and all after it, straight from global memory: the results are the same.
+// takes it, and all after it, straight from global memory: the results are the same.  A warp of which nobody waits any more is
+// not counted among those that are done with an item: it may be items ahead, and would be counted again in a slower one's place,
+// whose slots were then filled while it reads them.  The fetching warp's wait runs out instead, and then the others'.
 constexpr uint32_t kAdders = 256, kTile = 8 * kAdders, kBatch = 8, kItems = 12, kRingCtas = 3;
-constexpr uint32_t kWaitLimit = 1u << 18;      // looks at an mbarrier; one that fails takes 4 us: a second
+#ifndef DTT_EXPERTS_WAIT_LIMIT
+#define DTT_EXPERTS_WAIT_LIMIT (1u << 18)      // looks at an mbarrier; one that fails takes 4 us: a second
+#endif
+constexpr uint32_t kWaitLimit = DTT_EXPERTS_WAIT_LIMIT;
 constexpr uint32_t kRingSmem = 72 * 1024;      // of a CTA's slots, at most
 
 __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {      // false: the wait ran out
@@ -658,8 +663,7 @@ __global__ void __launch_bounds__(kAdders + 32, kRingCtas) rows_ring_kernel(cons
     };
     const char* base = reinterpret_cast<const char*>(slots);
     const auto done = [&] {
-        __syncwarp();
-        if (lane == 0) arrive(saddr(empty + ring.at));
+        if (__any_sync(0xFFFFFFFFu, !late) && lane == 0) arrive(saddr(empty + ring.at));
         ring.next();
     };
     if constexpr (BACK)

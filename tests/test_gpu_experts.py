@@ -363,6 +363,33 @@ def test_a_wait_that_is_given_up_changes_nothing(late, tmp_path):
                 assert torch.equal(a, b)
 
 
+
+@pytest.mark.parametrize("late", ["t / 32 == 3", "t / 32 != 5", "t / 32 == 3 && ring.at == 2", "t / 64 == blockIdx.x % 4 && ring.at == 7"])
+def test_warps_that_give_up_run_ahead_of_the_others(late, tmp_path):
+    """All lanes of a warp give an item up, and from there on wait for nothing while other warps still read from the slots: no slot is
+    filled again under them, and the results keep their bits.  Waits that nothing ends are cut short."""
+    from test_gpu_ops_edges import library_with
+    L = library_with("experts.cu", [f"-DDTT_EXPERTS_LATE=({late})", "-DDTT_EXPERTS_WAIT_LIMIT=4096u"], str(tmp_path))
+    for shape in [(9000, 4096, 8, 32, 32, 0, 1, 0, 0), *RING]:
+        tokens, cols, k = shape[:3]
+        for dtype, other_dtype in ((BF16, BF16), (F32, BF16)):
+            op, plan, _, buffer = batch(*shape, dtype)
+            rows = torch.randn(buffer.shape[0], cols, generator=gen(1), device="cuda").to(dtype)
+            dout = torch.randn(tokens, cols, generator=gen(2), device="cuda").to(other_dtype)
+            weights = torch.rand(tokens, k, generator=gen(3), device="cuda")
+            got = []
+            for other in (False, True):
+                if other:
+                    op._combine, op._combine_backward = L.dtt_experts_combine, L.dtt_experts_combine_backward
+                out, drows, dweights, alone = torch.zeros_like(dout), torch.full_like(rows, 7.0), torch.zeros_like(weights), torch.full_like(rows, 7.0)
+                op.combine(rows, plan[0], out, weights=weights)
+                op.combine_backward(dout, rows, plan[0], weights, *plan[1:], drows, dweights)
+                op.combine_backward(dout, None, plan[0], weights, *plan[1:], alone)          # no barrier among the warps
+                got.append((out, drows, dweights, alone))
+            for a, b in zip(*got):
+                assert torch.equal(a, b)
+
+
 def test_rows_past_four_gigabytes():
     tokens, cols, k = 20011, 32768, 4              # 80044 rows of 64 KiB: 5.2 GB
     op = D.ExpertRows(8, k)
