@@ -19,6 +19,10 @@ namespace {
 #ifndef DTT_EXPERTS_LATE
 #define DTT_EXPERTS_LATE false
 #endif
+// And whether the fetching warp gives up its wait for the oldest item.
+#ifndef DTT_EXPERTS_FETCH_LATE
+#define DTT_EXPERTS_FETCH_LATE false
+#endif
 constexpr uint32_t kMostExperts = 1024, kMostChoices = 32;
 constexpr uint32_t kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
 // 131072 pairs: 198 us with their rows' dispatch, with half as many parts 201, a quarter 206.
@@ -567,7 +571,8 @@ __device__ __forceinline__ void fetch(const RingParams& p, uint32_t slots, uint3
     // lanes look), and the adders have taken them (odd ones); all lanes give up if one does
     const uint32_t done = lane % 2 ? empty : full;
     const auto retire = [&] {
-        late = late || __any_sync(0xFFFFFFFFu, !arrived(done + 8 * oldest.at, oldest.phase));
+        late = late || __any_sync(0xFFFFFFFFu, DTT_EXPERTS_FETCH_LATE || !arrived(done + 8 * oldest.at, oldest.phase));
+        if (late) return;                       // it is still under way: its copies may be
         free += __shfl_sync(0xFFFFFFFFu, held, oldest.at);
         --under_way;
         oldest.next();

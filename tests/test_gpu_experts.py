@@ -390,6 +390,30 @@ def test_warps_that_give_up_run_ahead_of_the_others(late, tmp_path):
                 assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("late", ["true", "oldest.at == 3", "lane == 0 && oldest.at == 9", "lane % 2 && blockIdx.x % 3 == 1"])
+def test_a_fetching_warp_that_gives_up_leaves_no_copy_behind(late, tmp_path):
+    """It starts no more items, waits for those under way, the one it gave up among them, and the other warps take what is left from
+    global memory: the same bits, launch after launch."""
+    from test_gpu_ops_edges import library_with
+    L = library_with("experts.cu", [f"-DDTT_EXPERTS_FETCH_LATE=({late})", "-DDTT_EXPERTS_WAIT_LIMIT=4096u"], str(tmp_path))
+    for shape in [(9000, 4096, 8, 32, 32, 0, 1, 0, 0), *RING]:
+        tokens, cols, k = shape[:3]
+        op, plan, _, buffer = batch(*shape, BF16)
+        rows = torch.randn(buffer.shape[0], cols, generator=gen(1), device="cuda").to(BF16)
+        dout = torch.randn(tokens, cols, generator=gen(2), device="cuda").to(BF16)
+        weights = torch.rand(tokens, k, generator=gen(3), device="cuda")
+        got = []
+        for other in (False, True, True):
+            if other:
+                op._combine, op._combine_backward = L.dtt_experts_combine, L.dtt_experts_combine_backward
+            out, drows, dweights = torch.zeros_like(dout), torch.full_like(rows, 7.0), torch.zeros_like(weights)
+            op.combine(rows, plan[0], out, weights=weights)
+            op.combine_backward(dout, rows, plan[0], weights, *plan[1:], drows, dweights)
+            got.append((out, drows, dweights))
+        for a, *others in zip(*got):
+            assert all(torch.equal(a, b) for b in others)
+
+
 def test_rows_past_four_gigabytes():
     tokens, cols, k = 20011, 32768, 4              # 80044 rows of 64 KiB: 5.2 GB
     op = D.ExpertRows(8, k)
