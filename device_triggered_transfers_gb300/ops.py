@@ -72,6 +72,19 @@ class _Workspace:
         return w
 
 
+def _workspace_on(op, device, stream) -> int:
+    """Address of `op`'s workspace on a GPU, for a call on `stream`.  Once allocated a GPU's stays as long as `op`, whatever
+    other GPUs it is used on: graphs hold its address."""
+    w = op._workspace                                  # the last call's
+    if w is None or w.buffer.device != device:
+        w = op._workspaces.get(device)
+        if w is None:
+            w = op._workspaces[device] = _Workspace.on(stream, op.workspace_bytes, device)
+        op._workspace = w
+    w.use(stream)
+    return w.address
+
+
 class RMSNorm:
     """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, row by row, and its gradients
     (dtt_rmsnorm_forward / dtt_rmsnorm_backward: see there for the definitions).
@@ -97,7 +110,7 @@ class RMSNorm:
         self._f32 = types["f32"]
         self._xe, self._rese, self._ye = (_SIZES[k] for k in (x, residual, y))
         self.scale_cols = -(-cols // group) if group else 1
-        self._workspace = None
+        self._workspace, self._workspaces = None, {}
         self._ref = C.byref(self.desc)
 
     def _rows(self, name: str, t, shape, dtype, size: int) -> Tuple[int, int]:
@@ -146,10 +159,7 @@ class RMSNorm:
         xp, xs = self._rows("dx", dx, shape, self._res, self._rese)
         ws, need = 0, 0
         if dweight is not None:
-            if self._workspace is None or self._workspace.buffer.device != dy.device:
-                self._workspace = _Workspace.on(stream, self.workspace_bytes, dy.device)
-            self._workspace.use(stream)
-            ws, need = self._workspace.address, self.workspace_bytes
+            ws, need = _workspace_on(self, dy.device, stream), self.workspace_bytes
         rc = self._backward(self._ref, rows, gp, gs, hp, hs, self._flat("weight", weight, self.cols, self._w),
                             self._flat("rstd", rstd, rows, self._f32), sp, ss, xp, xs,
                             self._flat("dweight", dweight, self.cols, self._f32), ws, need, D._stream(stream))
@@ -239,10 +249,7 @@ class LayerNorm(RMSNorm):
                 flat("dweight", dweight, self.cols, self._f32), flat("dbias", dbias, self.cols, self._f32))
         ws, need = 0, 0
         if dweight is not None or dbias is not None:
-            if self._workspace is None or self._workspace.buffer.device != dy.device:
-                self._workspace = _Workspace.on(stream, self.workspace_bytes, dy.device)
-            self._workspace.use(stream)
-            ws, need = self._workspace.address, self.workspace_bytes
+            ws, need = _workspace_on(self, dy.device, stream), self.workspace_bytes
         rc = self._backward(self._ref, rows, gp, gs, hp, hs, *args, ws, need, D._stream(stream))
         if rc:
             D._check(rc)
@@ -267,7 +274,7 @@ class ExpertRows:
         D._check(D.lib().dtt_experts_workspace(C.byref(self.desc), C.byref(need)))
         self.experts, self.top_k, self.first, self.align = experts, top_k, first, align
         self.workspace_bytes = need.value
-        self._workspace = None
+        self._workspace, self._workspaces = None, {}
         self._ref = C.byref(self.desc)
         import torch
         self._i32, self._i64, self._f32 = torch.int32, torch.int64, torch.float32
@@ -318,14 +325,12 @@ class ExpertRows:
         ip = self._flat("ids", ids, (tokens, self.top_k), self._i64 if ids.dtype == self._i64 else self._i32)
         pp = self._flat("position", position, (tokens, self.top_k), self._i32)
         op, cp = self._flat("offsets", offsets, (self.experts + 1,), self._i32), self._flat("counts", counts, (self.experts,), self._i32)
-        if self._workspace is None or self._workspace.buffer.device != ids.device:
-            self._workspace = _Workspace.on(stream, self.workspace_bytes, ids.device)
-        self._workspace.use(stream)
+        ws = _workspace_on(self, ids.device, stream)
         rows = self.most_rows(tokens) if max_rows is None else max_rows
         if not 0 <= rows < 2 ** 31:
             raise D.DttError(D.EINVAL, f"ExpertRows: max_rows must be 0 .. 2^31 - 1, not {rows}")
-        rc = self._route(self._ref, tokens, ip, ids.element_size(), rows, pp, op, cp, self._workspace.address,
-                         self.workspace_bytes, D._stream(stream))
+        rc = self._route(self._ref, tokens, ip, ids.element_size(), rows, pp, op, cp, ws, self.workspace_bytes,
+                         D._stream(stream))
         if rc:
             D._check(rc)
 
