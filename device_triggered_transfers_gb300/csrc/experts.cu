@@ -242,9 +242,9 @@ __device__ __forceinline__ void copy_row(const Sorted& s, const char* from, cons
 struct DispatchParams {
     Sorted s;
     const char* x;
-    const char* scales;         // or null
+    const char* scales;         // of no tokens: null
     uint64_t x_pitch, scales_pitch;
-    Rows rows, row_scales;
+    Rows rows, row_scales;      // row_scales' may be null: no scales
 };
 
 // W: the word that rows are moved by, SW: their scales.
@@ -254,12 +254,12 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_kernel(const __grid_con
     wait_previous();
     if (blockIdx.x < p.s.fill_ctas) {
         fill_rows<W>(p.s, p.rows, blockIdx.x);
-        if (p.scales) fill_rows<SW>(p.s, p.row_scales, blockIdx.x);
+        if (p.row_scales.at) fill_rows<SW>(p.s, p.row_scales, blockIdx.x);
         return;
     }
     const uint64_t token = blockIdx.x - p.s.fill_ctas;
     copy_row<W>(p.s, p.x + token * p.x_pitch, p.rows, token);
-    if (p.scales) copy_row<SW>(p.s, p.scales + token * p.scales_pitch, p.row_scales, token);
+    if (p.row_scales.at) copy_row<SW>(p.s, p.scales + token * p.scales_pitch, p.row_scales, token);
 }
 
 struct CombineParams {
@@ -932,7 +932,8 @@ extern "C" int dtt_experts_dispatch(const dtt_experts_desc* d, uint64_t tokens, 
     int rc = check_sizes(who, d, tokens, max_rows);
     if (rc) return rc;
     if (row_bytes < 1 || row_bytes > 1ull << 26 || scale_count > 1ull << 24) return fail(DTT_EINVAL, "%s: a row has 1 .. 2^26 bytes and up to 2^24 scales", who);
-    if ((scales != nullptr) != (row_scales != nullptr) || (scales && !scale_count))
+    const bool missing = scales ? !row_scales && max_rows : row_scales && tokens;          // scales of no tokens, or of no rows, may be null
+    if (missing || ((scales || row_scales) && !scale_count))
         return fail(DTT_EINVAL, "%s: scales and row_scales go together, with one scale a row at least", who);
     if ((rc = check_ptr(who, "position", position, 4, tokens == 0)) || (rc = check_ptr(who, "offsets", offsets, 4)) || (rc = check_ptr(who, "counts", counts, 4)) ||
         (rc = check_rows(who, "x", x, x_pitch, tokens, row_bytes, 1, tokens == 0)) || (rc = check_rows(who, "rows", rows, rows_pitch, max_rows, row_bytes, 1, max_rows == 0)) ||
@@ -951,7 +952,7 @@ extern "C" int dtt_experts_dispatch(const dtt_experts_desc* d, uint64_t tokens, 
     p.scales_pitch = scales_pitch;
     p.row_scales = Rows{reinterpret_cast<char*>(row_scales), row_scales_pitch, (uint32_t)scale_count * 4};
     const uint32_t word = word_of({bits_of(x), x_pitch, row_bytes, bits_of(rows), rows_pitch});
-    const bool wide = !scales || word_of({bits_of(scales), scales_pitch, scale_count * 4, bits_of(row_scales), row_scales_pitch}) == 16;
+    const bool wide = !row_scales || word_of({bits_of(scales), scales_pitch, scale_count * 4, bits_of(row_scales), row_scales_pitch}) == 16;
     const cudaError_t e = wide ? launch_dispatch<uint4>(word, (uint32_t)grid, stream, p) : launch_dispatch<uint32_t>(word, (uint32_t)grid, stream, p);
     if (e != cudaSuccess) return fail(DTT_ECUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     return DTT_OK;

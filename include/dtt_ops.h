@@ -221,7 +221,8 @@ int dtt_experts_workspace(const dtt_experts_desc* desc, uint64_t* bytes);
 
 /* rows[position[t][j]] = x[t], and zeros in the rows that fill an expert's up (so that products over them add nothing);
  * rows from offsets[experts] on are left as they were.  Rows are moved as they are, row_bytes (1 .. 2^26) of any
- * type; with scales, scale_count f32 a row, row_scales[position[t][j]] = scales[t] the same way (NULL both: none).
+ * type; with scales, scale_count f32 a row, row_scales[position[t][j]] = scales[t] the same way (NULL both: none;
+ * those of 0 tokens or of 0 rows may be NULL by themselves, as x and rows then may).
  * position, offsets, counts: dtt_experts_route's for the same desc; a position is looked at before it is used (one
  * that is not below max_rows has no row), two equal ones leave either row.  No output overlaps an input. */
 int dtt_experts_dispatch(const dtt_experts_desc* desc, uint64_t tokens, const int32_t* position, const int32_t* offsets,

@@ -275,6 +275,24 @@ def test_tokens_of_no_batch():
     assert (rows == 7).all()
 
 
+
+def test_no_tokens_and_no_rows_with_scales():
+    """Rows that fill an expert up are zeros, their scales too; nothing else is written."""
+    op = D.ExpertRows(2, 2, align=4)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    x, scales = torch.zeros(0, 64, device="cuda").to(E4M3), torch.zeros(0, 3, device="cuda")
+    rows, row_scales = torch.full((10, 64), 7.0, device="cuda").to(E4M3), torch.full((10, 3), 7.0, device="cuda")
+    op.dispatch(x, torch.zeros(0, 2, dtype=torch.int32, device="cuda"), ints(0, 4, 8), ints(1, 4), rows, scales=scales, row_scales=row_scales)
+    for t in (rows.float(), row_scales):
+        assert not t[1:4].any() and (t[0] == 7).all() and (t[4:] == 7).all()
+    plan = routed(op, choices(6, 2, 2), max_rows=0)
+    op.dispatch(torch.zeros(6, 64, device="cuda").to(E4M3), *plan, rows[:0], scales=torch.zeros(6, 3, device="cuda"), row_scales=row_scales[:0])
+    torch.cuda.synchronize()
+    assert (row_scales[0] == 7).all()
+    with pytest.raises(D.DttError):
+        op.dispatch(x, plan[0][:0], *plan[1:], rows, scales=scales)
+
+
 def test_a_captured_pass_replays_with_other_choices():
     """The whole way there and back in a graph whose first call allocates the workspace; then other ids in place."""
     tokens, cols, k = 300, 512, 4

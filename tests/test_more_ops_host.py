@@ -126,6 +126,17 @@ def test_expert_rows_of_nothing_are_no_work():
     assert L.dtt_experts_combine(C.byref(d), 0, 64, 0, 0, D.BF16, 0, 0, 0, 0, D.BF16, 0, 0) == D.OK
 
 
+def test_dispatch_takes_no_tokens_and_no_rows_with_scales():
+    """An empty tensor has no address; the other one of the two does."""
+    d, L = experts_desc(align=1), D.lib()
+    nothing = dict(tokens=0, x=0, x_pitch=0, position=0, scales=0, scales_pitch=0)
+    for over in (dict(SCALED, **nothing), dict(SCALED, rows=0, rows_pitch=0, max_rows=0, row_scales=0, row_scales_pitch=0),
+                 dict(SCALED, **nothing, rows=0, rows_pitch=0, max_rows=0, row_scales=0, row_scales_pitch=0)):
+        assert L.dtt_experts_dispatch(C.byref(d), *dict(DISPATCH, **{**SCALED, **over}).values(), 0) == D.OK, over
+    for over in (dict(SCALED, scales=0), dict(SCALED, row_scales=0), dict(SCALED, **nothing, scale_count=0)):
+        assert L.dtt_experts_dispatch(C.byref(d), *dict(DISPATCH, **{**SCALED, **over}).values(), 0) == D.EINVAL, over
+
+
 def test_the_sort_s_workspace_follows_the_experts():
     n = C.c_uint64()
     D._check(D.lib().dtt_experts_workspace(C.byref(experts_desc()), C.byref(n)))
