@@ -483,6 +483,47 @@ def test_large_and_tiny_gradients_side_by_side(param, grad, seed, shift, n, monk
         a.check(before, t)
         assert max(float(s.max()) for s in a.vs) * 448 > 2.0 ** 52
 
+
+@pytest.mark.parametrize("param,grad,state,seed", [k for k in KINDS if k[2] == "e4m3"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_several_chunks_a_cta(param, grad, state, seed, shift):
+    """From some five million elements on, 8-bit states: tensors that end in a CTA's first, second, third and last chunk, at its end and
+    just past it, with neighbours on both sides."""
+    a = Lists([129, 5000001, 6145, 2049, 4097, 8191, 8192, 8193, 1], param, grad, state, copy=param == "f32", seed=seed, shift=shift)
+    before = a.state()
+    a.op.run(LR, 3)
+    copies, a.copies = a.copies, None
+    a.check(before, 3)
+    for copy, p in zip(copies or [], a.p):                   # NaN, of a random code of m past 448, is not equal to itself
+        assert torch.equal(torch.nan_to_num(copy), torch.nan_to_num(p.to(BF16))) and torch.equal(torch.isnan(copy), torch.isnan(p))
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+def test_a_blocks_largest_in_every_chunk_of_a_cta(grad):
+    """With a noise of 0 it has the formula's code there too."""
+    n, seed, f = 6 << 20, 5, np.float32
+    g, m, v, ms, vs = alike_blocks(n)
+    a = Lists([n], "bf16", grad, "e4m3", seed=seed)
+    for name, x in (("g", g), ("m", m), ("v", v)):
+        t = getattr(a, name)[0]
+        t.copy_(torch.from_numpy(OA.spread(x, n)).cuda().to(t.dtype))
+    g = a.g[0][::128].float().cpu().numpy()                  # as rounded to its type
+    a.ms[0].copy_(torch.from_numpy(ms))
+    a.vs[0].copy_(torch.from_numpy(vs))
+    a.op.run(LR, 3)
+    noise_m, noise_v, _ = OA.noise(seed, 3, 0, np.arange(n))
+    new_m = f(BETAS[0]) * (m * ms) + f(1 - BETAS[0]) * g
+    root = v * vs
+    new_root = np.sqrt(f(BETAS[1]) * (root * root) + f(1 - BETAS[1]) * g * g)
+    chunk = np.arange(n) // 2048 % 4
+    for got, new, noise in ((a.m[0], new_m, noise_m), (a.v[0], new_root, noise_v)):
+        code = largest_code(np.abs(new))
+        for k in range(4):
+            assert (noise[chunk == k] == 0).sum() > 8 and len(set(OA.spread(code, n)[(chunk == k) & (noise == 0)])) == 2
+        want = np.where(noise == 0, OA.spread(code, n), 0x7E) | np.where(OA.spread(new, n) < 0, 0x80, 0)
+        assert np.array_equal(got.view(torch.uint8).cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("shift", [0, 1])
 def test_a_tensor_past_32_bits(shift):
     """2^32 + 5 elements of 8-bit states: byte offsets, element numbers and the random bits beyond 32 bits."""
