@@ -99,7 +99,8 @@ int dtt_rmsnorm_workspace(const dtt_rmsnorm_desc* desc, uint64_t* bytes);
 /* For each row, all as above but
  *     mean = mean_c h_c,   s = 1 / sqrt(mean_c (h_c - mean)^2 + eps)     (f32, over the unrounded h, the mean first)
  *     y_c  = (h_c - mean) s weight_c + bias_c                            (weight NULL: 1, bias NULL: 0)
- * weight_dtype is the bias's too.  A row whose squares overflow f32 has rstd 0. */
+ * weight_dtype is the bias's too.  A row whose squares about the mean overflow f32 has rstd 0; one whose sum does has an
+ * infinite mean and NaN in y. */
 typedef dtt_rmsnorm_desc dtt_layernorm_desc;
 
 /* As dtt_rmsnorm_forward, with the bias, and the mean ([rows] f32, or NULL) beside rstd. */

@@ -131,6 +131,23 @@ def test_constant_rows_give_the_bias_and_nan_and_infinity_stay_in_their_row(rows
           {k: None if v is None else v[keep] for k, v in out.items()}, "f32", 0)
 
 
+
+@pytest.mark.parametrize("rows,cols,pad", [(9, 128, 0), (700, 1024, 0), (700, 8192, 0), (9, 16384, 0), (9, 40000, 0), (9, 1001, 1), (1300, 1001, 1), (2, 40003, 1)])
+def test_rows_whose_squares_or_sum_leave_f32(rows, cols, pad):
+    """Squares about a mean of 0 that overflow: rstd 0, and so the bias; a sum that does: an infinite mean, and NaN."""
+    op, a, more, out = case(rows, cols, x="f32", residual="f32", weight="f32", y="f32", pad=pad)
+    more["residual"][:2] = 0
+    a["x"][0] = 1e30 * (1 - 2 * (torch.arange(cols, device="cuda") % 2))
+    a["x"][1] = 3e38
+    forward(op, a, more, out)
+    assert out["rstd"][0] == 0 and torch.equal(out["y"][0], a["bias"]) and out["mean"][0].abs() <= 1e30 / cols * 1.001
+    assert torch.isinf(out["mean"][1]) and torch.isnan(out["y"][1]).all()
+    keep = slice(2, None)
+    if rows > 2:
+        check({"x": a["x"][keep], "weight": a["weight"], "bias": a["bias"]}, {"residual": more["residual"][keep]},
+              {k: None if v is None else v[keep] for k, v in out.items()}, "f32", 0)
+
+
 @pytest.mark.parametrize("rows,cols", [(5, 128), (5, 4096), (700, 4096), (5, 40000), (3, 1001), (1300, 1001)])
 def test_in_place_and_without_the_optional_outputs(rows, cols):
     op, a, more, out = case(rows, cols, y="e4m3")
