@@ -47,8 +47,9 @@ struct Tensor {
 constexpr uint32_t kElements = 8;
 
 // 8-bit states: v is taken times kUnit^2, its root times kUnit, so that where f32's v would be subnormal it is not, and the
-// root's instruction, which takes subnormal numbers for 0, needs no step of its own (three more an element: 32M weights 67.7 us
-// and not 65; a look for such a v among eight elements 67.1).
+// root's instruction, which takes subnormal numbers for 0, needs no step of its own.  Past 2^104 v leaves f32 then, which eight elements' largest
+// root tells, and the few of which it does are worked out again.  32M weights (bf16, at random; to nearest; f32, to nearest) 64.5, 50.4 and 110 us;
+// with three instructions more at each root 66, 51 and 116; with those few worked out after all others 64, 54 and 117.
 constexpr float kUnit = 0x1p12f;
 
 struct Scalars {
@@ -125,48 +126,68 @@ __device__ __forceinline__ Rates rates_of(const Scalars& s) {
     return r;
 }
 
-// m and v, as the old ones or as codes with what their scales make of them: m_by and v_by are beta1 and beta2, or the
-// scales times beta1 and sqrt(beta2).  root: sqrt(v), with 8-bit states times kUnit; infinite then where v is above
-// 2^104, unless LARGE.  decay: lr times the tensor's.
-template <bool S8, bool LARGE>
-__device__ __forceinline__ void update(Pair& p, Pair g, Pair& m, Pair& v, float2& root, float m_by, float v_by, float decay, const Rates& r, float eps) {
-    m = fma2(m, both(m_by), g * both(r.g_m));
-    const Pair gv = g * both(r.g_v);
-    if (S8) {
-        const Pair old = v * both(v_by);
-        v = fma2(old, old, gv * gv);
-        const float2 a = apart(v);
-        root = make_float2(root_of_normal(a.x), root_of_normal(a.y));
-        if (LARGE) {
-            const Pair o = old * both(1.0f / kUnit), n = gv * both(1.0f / kUnit);
-            const float2 w = apart(fma2(o, o, n * n));
-            if (isinf(a.x)) root.x = root_of(w.x) * kUnit;
-            if (isinf(a.y)) root.y = root_of(w.y) * kUnit;
-        }
-    } else {
-        v = fma2(v, both(v_by), gv * gv);
-        const float2 a = apart(v);
-        root = make_float2(root_of(a.x), root_of(a.y));
-    }
-    const float2 d = apart(fma2(pair(root.x, root.y), both(r.root_c2), both(eps)));
-    // p - decay p, not p (1 - decay): what rounding 1 - 1e-6 to f32 is off by, up to 2^-25, is 3 % of the 1e-6, of every weight the same
-    // way
-    p = fma2(m * pair(reciprocal(d.x), reciprocal(d.y)), both(-r.lr_by_c1), fma2(p, both(-decay), p));
+// 8-bit states: the root times kUnit of one element, whose code and gradient are these, where v is above 2^104; and of any.
+__device__ __forceinline__ float large_root_from(float code, float v_by, float g, const Rates& r) {
+    const float o = __fmul_rn(code, v_by) * (1.0f / kUnit), n = __fmul_rn(g, r.g_v) * (1.0f / kUnit);
+    return root_of_normal(fmaf(o, o, __fmul_rn(n, n))) * kUnit;
+}
+__device__ __forceinline__ float root_from(float code, float v_by, float g, const Rates& r) {
+    const float old = __fmul_rn(code, v_by), gv = __fmul_rn(g, r.g_v), v = fmaf(old, old, __fmul_rn(gv, gv));
+    return isinf(v) ? large_root_from(code, v_by, g, r) : root_of_normal(v);
 }
 
-// Eight elements, each four with scales of their own.  top: their roots' largest, NaN if one is.
-template <bool S8, bool LARGE>
-__device__ __forceinline__ void update_eight(float (&p)[8], const float (&g)[8], float (&m)[8], float (&v)[8], float2 (&root)[4], float& top, float2 m_by, float2 v_by,
-                                             float decay, const Rates& r, float eps) {
+// Eight elements.  m and v: as the old ones or as codes with what their scales make of them: m_by and v_by, one for each four, are beta1
+// and beta2, or the scales times beta1 and sqrt(beta2).  root: sqrt(v), with 8-bit states times kUnit; top: their largest, NaN if one
+// is.  decay: lr times the tensor's.  again(k): large_root_from for element k, asked for where v, times kUnit's square, has left f32 (past 2^104).
+template <bool S8, class Again>
+__device__ __forceinline__ void update(float (&p)[8], const float (&g)[8], float (&m)[8], float (&v)[8], float2 (&root)[4], float& top, float2 m_by, float2 v_by,
+                                       float decay, const Rates& r, float eps, Again again) {
 #pragma unroll
     for (uint32_t k = 0; k < 8; k += 2) {
-        Pair pp = pair(p[k], p[k + 1]), mm = pair(m[k], m[k + 1]), vv = pair(v[k], v[k + 1]);
-        update<S8, LARGE>(pp, pair(g[k], g[k + 1]), mm, vv, root[k / 2], k < 4 ? m_by.x : m_by.y, k < 4 ? v_by.x : v_by.y, decay, r, eps);
-        const float2 a = apart(pp), b = apart(mm), c = apart(vv);
-        p[k] = a.x, p[k + 1] = a.y, m[k] = b.x, m[k + 1] = b.y, v[k] = c.x, v[k + 1] = c.y;
+        const Pair gg = pair(g[k], g[k + 1]), gv = gg * both(r.g_v);
+        const Pair mm = fma2(pair(m[k], m[k + 1]), both(k < 4 ? m_by.x : m_by.y), gg * both(r.g_m));
+        Pair vv = pair(v[k], v[k + 1]);
+        const Pair by = both(k < 4 ? v_by.x : v_by.y);
+        if (S8) {
+            vv = vv * by;
+            vv = fma2(vv, vv, gv * gv);
+        } else {
+            vv = fma2(vv, by, gv * gv);
+        }
+        const float2 b = apart(mm), c = apart(vv);
+        m[k] = b.x, m[k + 1] = b.y, v[k] = c.x, v[k + 1] = c.y;
+        root[k / 2] = S8 ? make_float2(root_of_normal(c.x), root_of_normal(c.y)) : make_float2(root_of(c.x), root_of(c.y));
     }
-    top = max3_nan(max3_nan(root[0].x, root[0].y, root[1].x), root[1].y, root[2].x);
-    top = max3_nan(max_nan(top, root[2].y), root[3].x, root[3].y);
+    const auto largest = [&] {
+        const float a = max3_nan(max3_nan(root[0].x, root[0].y, root[1].x), root[1].y, root[2].x);
+        return max3_nan(max_nan(a, root[2].y), root[3].x, root[3].y);
+    };
+    if (S8) {
+        top = largest();
+        if (!(top < INFINITY)) {
+            uint32_t left = 0;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) left |= (isinf(k % 2 ? root[k / 2].y : root[k / 2].x) ? 1u : 0u) << k;
+#pragma unroll 1
+            for (; left; left &= left - 1) {
+                const uint32_t at = __ffs(left) - 1;
+                const float x = again(at);
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    if (k == at) (k % 2 ? root[k / 2].y : root[k / 2].x) = x;
+            }
+            top = largest();
+        }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; k += 2) {
+        const float2 d = apart(fma2(pair(root[k / 2].x, root[k / 2].y), both(r.root_c2), both(eps)));
+        const Pair pp = pair(p[k], p[k + 1]);
+        // p - decay p, not p (1 - decay): what rounding 1 - 1e-6 to f32 is off by, up to 2^-25, is 3 % of the 1e-6, of every weight the same
+        // way
+        const float2 a = apart(fma2(pair(m[k], m[k + 1]) * pair(reciprocal(d.x), reciprocal(d.y)), both(-r.lr_by_c1), fma2(pp, both(-decay), pp)));
+        p[k] = a.x, p[k + 1] = a.y;
+    }
 }
 
 // ---- codes ---------------------------------------------------------------------------------------
@@ -251,14 +272,19 @@ __device__ __forceinline__ float element(const char* base, uint64_t i) {
     return DT == DTT_BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[i] << 16) : reinterpret_cast<const float*>(base)[i];
 }
 
+__device__ __forceinline__ float code_of(const char* codes, uint64_t i) {
+    float v, none;
+    unpack_e4m3(reinterpret_cast<const uint8_t*>(codes)[i], v, none);
+    return v;
+}
+
 template <uint32_t P, uint32_t G, bool S8, class T>
 __device__ __forceinline__ void load_element(const T& t, uint64_t i, float& p, float& g, float& m, float& v) {
     p = element<P>(t.p, i);
     g = element<G>(t.g, i);
     if (S8) {
-        float none;
-        unpack_e4m3(reinterpret_cast<const uint8_t*>(t.m)[i], m, none);
-        unpack_e4m3(reinterpret_cast<const uint8_t*>(t.v)[i], v, none);
+        m = code_of(t.m, i);
+        v = code_of(t.v, i);
     } else {
         m = element<DTT_F32>(t.m, i);
         v = element<DTT_F32>(t.v, i);
@@ -330,13 +356,10 @@ __device__ __forceinline__ void settle_largest(const char* gs, char* m, char* v,
     for (uint32_t k = 0; k < count; ++k, i += step) {
         const uint32_t bits = random_bits(first + i, seed);
         if (bits >= 1u << 16 && (bits & 0xFFFFu)) continue;
-        const float g = element<G>(gs, i), cm = code_value(old_m, k), cv = code_value(old_v, k);
-        Pair none = both(0.0f), other = none, square = pair(cv, 0.0f);
-        float2 root;                                                                                   // as update() has it
-        update<true, true>(none, pair(g, 0.0f), other, square, root, 0.0f, __fmul_rn(t.vs, s.root_beta2), 0.0f, r, s.eps);
+        const float g = element<G>(gs, i), cm = code_value(old_m, k), cv = code_value(old_v, k);           // m and root: as update() has them
         if (bits < 1u << 16 && scaled(t.m) && fabsf(fmaf(cm, __fmul_rn(t.ms, s.beta1), __fmul_rn(g, r.g_m))) == t.m)
             reinterpret_cast<uint8_t*>(m)[i] = (uint8_t)largest_m(cm, t.ms, g, s);
-        if (!(bits & 0xFFFFu) && scaled(t.root * (1.0f / kUnit)) && root.x == t.root)
+        if (!(bits & 0xFFFFu) && scaled(t.root * (1.0f / kUnit)) && root_from(cv, __fmul_rn(t.vs, s.root_beta2), g, r) == t.root)
             reinterpret_cast<uint8_t*>(v)[i] = (uint8_t)largest_root(cv, t.vs, g, s);
     }
 }
@@ -385,7 +408,10 @@ __device__ __forceinline__ void chunk_by_elements(const Tensor& t, uint64_t at, 
     const float2 m_by = S8 ? make_float2(ms[0] * s.beta1, ms[1] * s.beta1) : make_float2(s.beta1, s.beta1);
     const float2 v_by = S8 ? make_float2(vs[0] * s.root_beta2, vs[1] * s.root_beta2) : make_float2(s.beta2, s.beta2);
     float top;
-    update_eight<S8, true>(p, g, m, v, root, top, m_by, v_by, decay, r, s.eps);
+    update<S8>(p, g, m, v, root, top, m_by, v_by, decay, r, s.eps, [&](uint32_t k) {
+        const uint64_t i = min(i0 + 32 * k, t.n - 1);
+        return large_root_from(code_of(t.v, i), k < 4 ? v_by.x : v_by.y, element<G>(t.g, i), r);
+    });
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)
         if (S8 && i0 + 32 * k >= t.n) m[k] = (k % 2 ? root[k / 2].y : root[k / 2].x) = 0.0f;
@@ -526,11 +552,9 @@ __device__ __forceinline__ void shared_group(uint32_t at, float (&v)[8]) {
 
 // Eight neighbouring elements a thread, from element o of the part, a block of 128 sixteen lanes.  Pointers are those of
 // the element `lead` places before the tensor's first, so that every eighth from there is aligned; the groups at its
-// ends that it does not fill go element by element.  With 8-bit states and LARGE not set, nothing is written of a warp's groups where
-// a root is infinite or NaN: they are to be taken again.
-enum : uint32_t { kSettle = 1, kAgain = 1 << kTurns };      // what is left to do of a group (of chunk i: times 2^i)
-template <uint32_t P, uint32_t G, bool S8, bool SR, bool LARGE>
-__device__ __forceinline__ uint32_t group(const Part& a, uint32_t o, uint32_t stage, float ms, float vs, uint32_t seed, float decay, const Rates& r, const Scalars& s) {
+// ends that it does not fill go element by element.
+template <uint32_t P, uint32_t G, bool S8, bool SR>
+__device__ __forceinline__ bool group(const Part& a, uint32_t o, uint32_t stage, float ms, float vs, uint32_t seed, float decay, const Rates& r, const Scalars& s) {
     float p[8], g[8], m[8], v[8];
     float2 root[4];
     const bool whole = o >= a.head && o + 8 <= a.end;
@@ -563,8 +587,8 @@ __device__ __forceinline__ uint32_t group(const Part& a, uint32_t o, uint32_t st
     }
     const float m_by = S8 ? ms * s.beta1 : s.beta1, v_by = S8 ? vs * s.root_beta2 : s.beta2;
     float tr;
-    update_eight<S8, LARGE>(p, g, m, v, root, tr, make_float2(m_by, m_by), make_float2(v_by, v_by), decay, r, s.eps);
-    if (S8 && !LARGE && __any_sync(0xFFFFFFFFu, !(tr < INFINITY))) return kAgain;
+    update<S8>(p, g, m, v, root, tr, make_float2(m_by, m_by), make_float2(v_by, v_by), decay, r, s.eps,
+               [&](uint32_t k) { return large_root_from(code_of(a.v, o + k), v_by, element<G>(a.g, o + k), r); });
     uint32_t bits[8] = {}, cut[8] = {};
     if (SR) {
         const uint32_t key = (uint32_t)first * kGolden + seed + (uint32_t)(first >> 32) * kThird;
@@ -616,24 +640,25 @@ __device__ __forceinline__ uint32_t group(const Part& a, uint32_t o, uint32_t st
         else
             put_group<P>(a.p, o, p);
         if (P == DTT_F32 && a.copy) put_group<DTT_BF16>(a.copy, o, p);
-        return settle ? kSettle : 0;
+        return settle;
     }
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)
         if (mine(k))
             store_element<P, S8, SR>(a, o + k, p[k], cut[k], m[k], v[k], (k < 4 ? cm.x : cm.y) >> 8 * (k % 4), (k < 4 ? cv.x : cv.y) >> 8 * (k % 4));
-    return settle ? kSettle : 0;
+    return settle;
 }
 
-// The chunks one after the other, once a thread's own copies for each have landed.  What comes back: what is left to do of each.
+// The chunks one after the other, once a thread's own copies for each have landed.  Bit i of what comes back: chunk i is
+// left to settle.
 template <uint32_t TURN, uint32_t P, uint32_t G, bool SR>
 __device__ __forceinline__ uint32_t take_turns(const Part& a, uint32_t stage, const float (&ms)[kTurns], const float (&vs)[kTurns], uint32_t seed, float decay,
                                            const Rates& r, const Scalars& s) {
     if constexpr (TURN < kTurns) {
         if (TURN * kChunk >= a.end) return 0;
         asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 1 - TURN) : "memory");
-        const uint32_t left = group<P, G, true, SR, false>(a, TURN * kChunk + 8 * threadIdx.x, stage + TURN * Stage<P, G>::bytes, ms[TURN], vs[TURN], seed, decay, r, s);
-        return take_turns<TURN + 1, P, G, SR>(a, stage, ms, vs, seed, decay, r, s) | left << TURN;
+        const bool settle = group<P, G, true, SR>(a, TURN * kChunk + 8 * threadIdx.x, stage + TURN * Stage<P, G>::bytes, ms[TURN], vs[TURN], seed, decay, r, s);
+        return take_turns<TURN + 1, P, G, SR>(a, stage, ms, vs, seed, decay, r, s) | (settle ? 1u << TURN : 0u);
     }
     return 0;
 }
@@ -670,23 +695,13 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
                 }
                 start_copies<P, G>(a, o, stage + turn * Stage<P, G>::bytes);
             }
-            uint32_t left = take_turns<0, P, G, SR>(a, stage, ms, vs, seed, decay, r, b.s);
-            if (left >= kAgain) {                               // for all of the warp, or for none.  Here for the same reason: 70.3 us where update() does it
-#pragma unroll 1
-                for (uint32_t turn = 0; turn < kTurns; ++turn) {
-                    if (!(left & kAgain << turn)) continue;
-                    const uint32_t o = turn * kChunk + 8 * threadIdx.x;
-                    const bool any = o < a.end;
-                    left |= group<P, G, true, SR, true>(a, o, stage + turn * Stage<P, G>::bytes, any ? a.ms[o / kBlock] : 0.0f, any ? a.vs[o / kBlock] : 0.0f, seed, decay, r,
-                                                        b.s) << turn;
-                }
-            }
+            const uint32_t settle = take_turns<0, P, G, SR>(a, stage, ms, vs, seed, decay, r, b.s);
             // Only now, with nothing of the chunks in registers: one thread in 1000 has something to do here.  32M weights
-            // take 65.2 us, settled among the chunks' work 10 more, and 5 less if nothing asked for a noise of 0.
-            if (SR && left & (kAgain - kSettle)) {
+            // take 65.5 us, settled among the chunks' work 10 more, and 5 less if nothing asked for a noise of 0.
+            if (SR && settle) {
 #pragma unroll 1
                 for (uint32_t turn = 0; turn < kTurns; ++turn) {
-                    if (!(left & kSettle << turn)) continue;
+                    if (!(settle >> turn & 1)) continue;
                     using S = Stage<P, G>;
                     const uint32_t o = turn * kChunk + 8 * threadIdx.x, at = stage + turn * S::bytes;
                     const uint4 t = shared16(at + 16 * threadIdx.x);
@@ -695,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
                 }
             }
         } else {
-            group<P, G, S8, SR, false>(a, 8 * threadIdx.x, 0, 0.0f, 0.0f, seed, decay, r, b.s);
+            group<P, G, S8, SR>(a, 8 * threadIdx.x, 0, 0.0f, 0.0f, seed, decay, r, b.s);
         }
     } else {
         const uint64_t end = min(start + b.turns * kChunk, t.n);
