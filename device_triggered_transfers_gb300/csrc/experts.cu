@@ -626,9 +626,9 @@ __device__ __forceinline__ void piece8(bool late, const char* item, const char* 
 }
 
 // 131072 rows of 4096 in bf16: combined in 174 us, the copy rate (reads outnumber writes); their gradients in 361 us, 0.93.
-// 2000 tokens of 8064 with a row each: 17.8 us for the gradients, 0.80.  Items of few rows are bound by the adders' instructions one
-// after the other, so that three CTAs an SM with 72 KiB of slots each are ahead of two with 108 (177, 368 and 22 us), and
-// the rows that there are come one behind the other (18.2 where each of eight places is looked at).
+// 2000 tokens of 8064 with a row each: 18 to 23 us for the gradients, by how evenly the router's choices fall.  Items of few rows are bound by the adders' instructions one
+// after the other, so that three CTAs an SM with 72 KiB of slots each are ahead of two with 108 (177, 368 and 22 us
+// where these take 174, 361 and 18), and the rows that there are come one behind the other (18.2 where each of eight places is looked at).
 template <uint32_t RDT, uint32_t GDT, bool BACK>
 __global__ void __launch_bounds__(kAdders + 32, kRingCtas) rows_ring_kernel(const __grid_constant__ RingParams p) {
     using S = Slots<RDT, GDT, BACK>;

@@ -173,7 +173,8 @@ __device__ __forceinline__ float row_max(float v, uint32_t tpr, float* slot) {
 }
 
 // One row a CTA.  NCH chunks a thread stay in registers; kLong reads the row again for each pass over it.
-// 2000 x 32768 in bf16: 141 us, 0.55 of the copy rate; loads that wait for one another bound it.
+// 2000 x 32768 in bf16: 141 us, 0.55 of the copy rate; loads that wait for one another bound it.  The layer norm, which reduces the row
+// twice: 188 us, 0.41; 1000 x 70000, read once more for the mean, 235 us, 0.35.
 template <bool MEAN, uint32_t NCH, bool VEC>
 __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(const __grid_constant__ FwdParams p) {
     launch_next();
@@ -349,7 +350,8 @@ __device__ __forceinline__ void weight_columns(const BwdParams& p) {
 // A row by `lanes` neighbouring lanes of a warp (a power of two), a chunk each; a CTA has 256 / lanes rows.  A
 // thread's loads all go out before the first value is used, and many CTAs hide them: with two or four rows a
 // thread under way the forward pass of 300000 x 128 (bf16 to 8 bits) took 58 and 82 us where one took 57.
-// Behind another call it takes 59 (bf16 52), 0.67 (0.88) of the copy rate; the exact quotients are 2 us of it.
+// Behind another call it takes 59 (bf16 52), 0.67 (0.88) of the copy rate; the exact quotients are 2 us of it.  The layer norm
+// (bf16): 67, 0.67.
 template <bool MEAN>
 __global__ void __launch_bounds__(256) norm_fwd_short_kernel(const __grid_constant__ FwdParams p, uint32_t lanes) {
     launch_next();
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(256) norm_fwd_short_kernel(const __grid_consta
 
 // The same split; a CTA walks over rows, each thread at the same columns, whose part of the weight's gradient
 // adds up in its registers; at the end the CTA's rows' sums, in their order, become its partial row.
-// 300000 x 128 in bf16: 62 us, 0.73 of the copy rate.
+// 300000 x 128 in bf16: 62 us, 0.73 of the copy rate; the layer norm 65, 0.70.
 template <bool MEAN>
 __global__ void __launch_bounds__(256, 4) norm_bwd_short_kernel(const __grid_constant__ BwdParams p, uint32_t lanes) {
     launch_next();
@@ -483,7 +485,8 @@ __global__ void __launch_bounds__(256, 4) norm_bwd_short_kernel(const __grid_con
 
 // A CTA walks over rows: each thread keeps the same columns for all of them, so the weight's gradient adds up
 // in its registers and is written once, as the CTA's partial row (kLong: in the partial row itself).
-// 2000 x 16384 in f32: 173 us, 0.45 of the copy rate, bound as the forward pass.
+// 2000 x 16384 in f32: 173 us, 0.45 of the copy rate, bound as the forward pass; the layer norm 243, 0.32.  kLong adds up in the partial rows
+// in memory: the layer norm's 1000 x 70000 (bf16) 1040 us, 0.08.
 template <bool MEAN, uint32_t NCH, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const __grid_constant__ BwdParams p) {
     launch_next();
@@ -1020,6 +1023,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 // 16384 x 4096 (bf16 to 8 bits, groups of 128): 81 us, 0.86 of the copy rate (84 where the residual's rows stay in L2 as long as
 // others).  With three CTAs of 256 threads an SM; four, whose registers spill, took 3 more, two 13, and 128 threads of four chunks
 // each 12.  Two reductions with a barrier each, one value an instruction and types looked up at each access: 113.
+// To bf16 95 us, 0.83; f32 throughout 185, 0.86.  Rows of 8064 columns (four chunks a thread) to bf16 175, 0.89, to 8 bits 179, 0.76;
+// 30000 x 1024 51 and 53, 0.71 and 0.60.
 constexpr uint32_t kLayerThreads = 256;        // of a row with two chunks a thread, at most
 template <uint32_t NCH, bool B16>
 __global__ void __launch_bounds__(NCH == 1 ? 128 : NCH == 2 ? kLayerThreads : kRingThreads, NCH == 1 ? 8 : NCH == 2 ? 3 : 1) layernorm_fwd_ring_kernel(const __grid_constant__ FwdParams p, uint32_t S) {
@@ -1441,7 +1446,8 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : kRingThreads, NCH == 1 ? 4 : 
 // The ring for rows at any alignment, an element a thread.  A bulk copy moves whole 16-byte
 // words: from the one that holds the row's first byte to the one that holds its last.  The few bytes
 // beside the row in these two are copied with it and not looked at (an allocation never ends within
-// such a word).  4093 x 5001 (bf16 with an f32 residual): 41.6 us, 0.87 of the copy rate.
+// such a word).  4093 x 5001 (bf16 with an f32 residual): 41.6 us, 0.87 of the copy rate; the layer norm, with its second reduction, 51,
+// 0.71.
 struct Words {
     uint64_t from;              // address of the first
     uint32_t bytes;             // of all
@@ -1550,8 +1556,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) norm_fwd_ring_elements_kernel
     if (lost && t == 0) await_copies(full, S, next, gridDim.x);
 }
 
-// 16384 x 4001 in f32: 179 us, 0.86 of the copy rate; 1021 x 5001 in f32 19 us, 0.63: one CTA a SM (60 KiB a
-// stage), seven rows each.
+// 16384 x 4001 in f32: 179 us, 0.86 of the copy rate (layer norm 171, 0.90); 1021 x 5001 in f32 19 us, 0.63 (layer norm 22, 0.54): one CTA a SM
+// (60 KiB a stage), seven rows each.
 template <bool MEAN, uint32_t E>
 __global__ void __launch_bounds__(MEAN && E == 8 ? kWideThreads : kRingThreads) norm_bwd_ring_elements_kernel(const __grid_constant__ BwdParams p, uint32_t S) {
     launch_next();
